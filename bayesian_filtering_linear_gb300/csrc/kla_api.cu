@@ -258,6 +258,85 @@ kla_status check_conv_shape(int B, int H, int T, int D, int W) {
   return KLA_OK;
 }
 
+// Shape checks of the delta rule's entry points.
+kla_status check_delta_shape(int B, int Hk, int H, int T, int dk, int dv) {
+  const kla_status st = check_shape(B, H, T, dk, dv);
+  if (st != KLA_OK) return st;
+  if (Hk < 0 || (H > 0 && (Hk == 0 || H % Hk != 0))) return KLA_ERR_INVALID_ARG;
+  return KLA_OK;
+}
+
+// The gates [B,H,T] are read and written an element at a time: a token's slice of them may start anywhere.
+bool gates_aligned(int io, const void* a, const void* b, const void* c = nullptr, const void* d = nullptr) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                        reinterpret_cast<uintptr_t>(c) | reinterpret_cast<uintptr_t>(d);
+  return (all & (io_size(io) - 1)) == 0;
+}
+
+// An output range meets an input range or another output's, other than the
+// pair (same_out, same_in) where both are the same array.
+struct Range {
+  const void* p;
+  size_t n;
+};
+bool ranges_clash(const Range* outs, int no, const Range* ins, int ni, int same_out = -1, int same_in = -1) {
+  for (int o = 0; o < no; ++o) {
+    for (int i = 0; i < ni; ++i) {
+      if (o == same_out && i == same_in && outs[o].p == ins[i].p) continue;
+      if (ranges_overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n)) return true;
+    }
+    for (int p = o + 1; p < no; ++p)
+      if (ranges_overlap(outs[o].p, outs[o].n, outs[p].p, outs[p].n)) return true;
+  }
+  return false;
+}
+
+// Shapes, options and strides of the norm with rotation. `span`: elements from
+// the first to the last that the strides reach.
+kla_status check_norm_rope(int B, int Hq, int Hk, int T, int D, kla_dtype io, const kla_norm_rope_options* opt,
+                           const long long* strides[2], long long st[2][3], size_t span[2]) {
+  if (B < 0 || Hq < 0 || Hk < 0 || T < 0 || !opt) return KLA_ERR_INVALID_ARG;
+  if (!valid_d(D)) return KLA_ERR_UNSUPPORTED_SHAPE;
+  if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
+  if (opt->norm < KLA_NORM_NONE || opt->norm > KLA_NORM_L2 || opt->layout < KLA_ROPE_HALF ||
+      opt->layout > KLA_ROPE_INTERLEAVED || opt->rot_dim < 0 || opt->rot_dim > D || opt->rot_dim % 2 != 0 ||
+      !(opt->eps >= 0.f))
+    return KLA_ERR_INVALID_ARG;
+  const int heads[2] = {Hq, Hk};
+  if ((long long)Hq + Hk > INT_MAX) return KLA_ERR_UNSUPPORTED_SHAPE;
+  const long long rows = (long long)B * ((long long)Hq + Hk);
+  if (rows > INT_MAX || (rows > 0 && (long long)T > (1LL << 46) / (rows * D))) return KLA_ERR_UNSUPPORTED_SHAPE;
+  const long long unit = 16 / (long long)io_size(io);
+  for (int i = 0; i < 2; ++i) {
+    const long long dense[3] = {(long long)heads[i] * T * D, (long long)T * D, D};
+    const long long most[3] = {B, heads[i], T};
+    span[i] = 0;
+    bool empty = false;
+    size_t last = D;
+    for (int j = 0; j < 3; ++j) {
+      st[i][j] = strides[i] ? strides[i][j] : dense[j];
+      if (most[j] == 0) empty = true;
+    }
+    for (int j = 0; j < 3 && !empty; ++j) {
+      if (most[j] <= 1) continue;
+      if (st[i][j] < 0 || st[i][j] > (1LL << 46) / (most[j] - 1)) return KLA_ERR_INVALID_ARG;
+      if (st[i][j] % unit != 0) return KLA_ERR_MISALIGNED;
+      last += (size_t)(most[j] - 1) * (size_t)st[i][j];
+    }
+    if (!empty) span[i] = last;
+  }
+  return KLA_OK;
+}
+
+kla::NormRopeArgs norm_rope_args(const float* inv_freq, const long long* positions, int B, int T, int D, kla_dtype io,
+                                 const kla_norm_rope_options* opt) {
+  kla::NormRopeArgs a{};
+  a.inv_freq = inv_freq; a.positions = positions; a.offset = opt->offset;
+  a.B = B; a.T = T; a.D = D; a.rot = opt->rot_dim; a.norm = opt->norm; a.layout = opt->layout; a.io = (int)io;
+  a.eps = opt->eps; a.rot_scale = opt->rot_scale;
+  return a;
+}
+
 void fill_info(const Plan& p, kla_plan_info* out) {
   out->strategy = p.strategy;
   out->chunk_len = p.chunk_len;
@@ -672,6 +751,190 @@ kla_status kla_conv_backward(const void* x, const float* weight, const float* bi
   a.B = B; a.H = H; a.T = T; a.D = D; a.W = W; a.io = (int)io; a.act = activation;
   return kla::launch_conv_backward(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK
                                                                                                   : KLA_ERR_CUDA;
+}
+
+kla_status kla_delta_forward(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const float* state0, void* o, float* stateT, int B, int Hk, int H, int T, int dk,
+                             int dv, kla_dtype io, float scale, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  const kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
+  if (st != KLA_OK) return st;
+  if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
+  const long long bh = (long long)B * H, tokens = bh * T;
+  if (tokens > 0 && (!q || !k || !v || !g || !beta || !o)) return KLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, state0, o, stateT};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  if (!gates_aligned(io, g, beta)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), keys = (size_t)B * Hk * T * dk * z, gates = (size_t)tokens * z;
+  const size_t vals = (size_t)tokens * dv * z, states = (size_t)bh * dk * dv * sizeof(float);
+  const Range ins[] = {{q, keys}, {k, keys}, {v, vals}, {g, gates}, {beta, gates}, {state0, states}};
+  const Range outs[] = {{stateT, states}, {o, vals}};
+  if (ranges_clash(outs, 2, ins, 6, 0, 5)) return KLA_ERR_INVALID_ARG;
+  if (bh == 0 || (T == 0 && !stateT)) return KLA_OK;
+  kla::DeltaArgs a{q, k, v, g, beta, state0, o, stateT, B, Hk, H, T, dk, dv, (int)io, scale};
+  return kla::launch_delta_recurrent(a, nullptr, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK
+                                                                                                        : KLA_ERR_CUDA;
+}
+
+kla_status kla_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                          float* state, void* o, int B, int Hk, int H, int dk, int dv, kla_dtype io, float scale,
+                          void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  const kla_status st = check_delta_shape(B, Hk, H, 1, dk, dv);
+  if (st != KLA_OK) return st;
+  if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
+  const long long bh = (long long)B * H;
+  if (bh > 0 && (!q || !k || !v || !g || !beta || !state || !o)) return KLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, state, o};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  if (!gates_aligned(io, g, beta)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), keys = (size_t)B * Hk * dk * z, gates = (size_t)bh * z, vals = (size_t)bh * dv * z;
+  const Range ins[] = {{q, keys}, {k, keys}, {v, vals}, {g, gates}, {beta, gates}};
+  const Range outs[] = {{o, vals}, {state, (size_t)bh * dk * dv * sizeof(float)}};
+  if (ranges_clash(outs, 2, ins, 5)) return KLA_ERR_INVALID_ARG;
+  if (bh == 0) return KLA_OK;
+  kla::DeltaArgs a{q, k, v, g, beta, state, o, state, B, Hk, H, 1, dk, dv, (int)io, scale};
+  return kla::launch_delta_step(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+size_t kla_delta_backward_workspace_size(int B, int Hk, int H, int T, int dk, int dv) {
+  if (check_delta_shape(B, Hk, H, T, dk, dv) != KLA_OK) return (size_t)-1;
+  if ((long long)B * H * T == 0) return 0;
+  return kla::delta_backward_bytes(B, Hk, H, T, dk, dv);
+}
+
+kla_status kla_delta_backward(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                              const float* state0, const void* go, const float* gstateT, void* gq, void* gk,
+                              void* gv, void* gg, void* gbeta, float* gstate0, int B, int Hk, int H, int T, int dk,
+                              int dv, kla_dtype io, float scale, void* workspace, size_t ws_bytes, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  const kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
+  if (st != KLA_OK) return st;
+  if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
+  const long long bh = (long long)B * H, tokens = bh * T;
+  if (tokens > 0 && (!q || !k || !v || !g || !beta || !gq || !gk || !gv || !gg || !gbeta)) return KLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, state0, go, gstateT, gq, gk, gv, gstate0, workspace};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  if (!gates_aligned(io, g, beta, gg, gbeta)) return KLA_ERR_MISALIGNED;
+  const size_t need = tokens > 0 ? kla::delta_backward_bytes(B, Hk, H, T, dk, dv) : 0;
+  const size_t z = io_size(io), keys = (size_t)B * Hk * T * dk * z, gates = (size_t)tokens * z;
+  const size_t vals = (size_t)tokens * dv * z, states = (size_t)bh * dk * dv * sizeof(float);
+  const Range ins[] = {{q, keys}, {k, keys}, {v, vals}, {g, gates}, {beta, gates}, {state0, states}, {go, vals},
+                       {gstateT, states}};
+  const Range outs[] = {{gq, keys}, {gk, keys}, {gv, vals}, {gg, gates}, {gbeta, gates}, {gstate0, states},
+                        {workspace, need}};
+  if (ranges_clash(outs, 7, ins, 8)) return KLA_ERR_INVALID_ARG;
+  if (bh == 0) return KLA_OK;
+  if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {  // the state's gradient passes through
+    if (!gstate0) return KLA_OK;
+    const cudaError_t e = gstateT ? cudaMemcpyAsync(gstate0, gstateT, states, cudaMemcpyDeviceToDevice, s)
+                                  : cudaMemsetAsync(gstate0, 0, states, s);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  }
+  kla::DeltaArgs a{q, k, v, g, beta, state0, nullptr, nullptr, B, Hk, H, T, dk, dv, (int)io, scale};
+  kla::DeltaGradArgs d{go, gstateT, gq, gk, gv, gg, gbeta, gstate0};
+  return kla::launch_delta_backward(a, d, workspace, s) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+kla_status kla_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                         const float* inv_freq, const long long* positions, void* yq, void* yk, int B, int Hq,
+                         int Hk, int T, int D, const long long* q_strides, const long long* k_strides,
+                         kla_dtype io, const kla_norm_rope_options* opt, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  const long long* strides[2] = {q_strides, k_strides};
+  long long s3[2][3];
+  size_t span[2];
+  kla_status st = check_norm_rope(B, Hq, Hk, T, D, io, opt, strides, s3, span);
+  if (st != KLA_OK) return st;
+  const long long tokens = (long long)B * T;
+  if (tokens > 0 && ((Hq > 0 && (!q || !yq)) || (Hk > 0 && (!k || !yk)))) return KLA_ERR_INVALID_ARG;
+  if (tokens > 0 && opt->rot_dim > 0 && !inv_freq) return KLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, q_weight, k_weight, inv_freq, positions, yq, yk};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), wb = D * sizeof(float);
+  const Range ins[] = {{q, span[0] * z}, {k, span[1] * z}, {q_weight, wb}, {k_weight, wb},
+                       {inv_freq, opt->rot_dim / 2 * sizeof(float)}, {positions, (size_t)tokens * sizeof(long long)}};
+  const Range outs[] = {{yq, (size_t)tokens * Hq * D * z}, {yk, (size_t)tokens * Hk * D * z}};
+  if (ranges_clash(outs, 2, ins, 6)) return KLA_ERR_INVALID_ARG;
+  if (tokens == 0 || Hq + Hk == 0) return KLA_OK;
+  int sms = 0;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
+  kla::NormRopeArgs a = norm_rope_args(inv_freq, positions, B, T, D, io, opt);
+  a.q = {q, s3[0][0], s3[0][1], s3[0][2], q_weight, yq, nullptr, nullptr, 0, 0, 0, Hq};
+  a.k = {k, s3[1][0], s3[1][1], s3[1][2], k_weight, yk, nullptr, nullptr, 0, 0, 0, Hk};
+  return kla::launch_norm_rope(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+size_t kla_norm_rope_backward_workspace_size(int B, int Hq, int Hk, int T, int D) {
+  const kla_norm_rope_options opt{KLA_NORM_RMS, KLA_ROPE_HALF, 0, 0.f, 1.f, 0};
+  const long long* strides[2] = {nullptr, nullptr};
+  long long s3[2][3];
+  size_t span[2];
+  if (check_norm_rope(B, Hq, Hk, T, D, KLA_F32, &opt, strides, s3, span) != KLA_OK) return (size_t)-1;
+  int sms = 0;
+  if (device_sms(&sms) != KLA_OK) return (size_t)-1;
+  return kla::norm_rope_partial_bytes(B, Hq, Hk, T, D, sms);
+}
+
+kla_status kla_norm_rope_backward(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                  const float* inv_freq, const long long* positions, const void* gyq,
+                                  const void* gyk, void* gq, void* gk, float* gq_weight, float* gk_weight, int B,
+                                  int Hq, int Hk, int T, int D, const long long* q_strides,
+                                  const long long* k_strides, const long long* gq_strides,
+                                  const long long* gk_strides, kla_dtype io, const kla_norm_rope_options* opt,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  const long long *strides[2] = {q_strides, k_strides}, *gstrides[2] = {gq_strides, gk_strides};
+  long long s3[2][3], g3[2][3];
+  size_t span[2], gspan[2];
+  kla_status st = check_norm_rope(B, Hq, Hk, T, D, io, opt, strides, s3, span);
+  if (st != KLA_OK) return st;
+  if ((st = check_norm_rope(B, Hq, Hk, T, D, io, opt, gstrides, g3, gspan)) != KLA_OK) return st;
+  const long long tokens = (long long)B * T;
+  if (tokens > 0 && ((Hq > 0 && (!q || !gq)) || (Hk > 0 && (!k || !gk)))) return KLA_ERR_INVALID_ARG;
+  if (tokens > 0 && opt->rot_dim > 0 && !inv_freq) return KLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, q_weight, k_weight, inv_freq, positions, gyq, gyk, gq, gk, gq_weight, gk_weight, workspace};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), wb = D * sizeof(float);
+  const Range ins[] = {{q, span[0] * z}, {k, span[1] * z}, {q_weight, wb}, {k_weight, wb},
+                       {inv_freq, opt->rot_dim / 2 * sizeof(float)}, {positions, (size_t)tokens * sizeof(long long)},
+                       {gyq, (size_t)tokens * Hq * D * z}, {gyk, (size_t)tokens * Hk * D * z}};
+  const Range outs[] = {{gq, gspan[0] * z}, {gk, gspan[1] * z}, {gq_weight, wb}, {gk_weight, wb}};
+  for (int o = 0; o < 4; ++o) {
+    if (ranges_clash(outs + o, 1, ins, 8)) return KLA_ERR_INVALID_ARG;
+    // gq and gk may lie between each other's rows, as parts of one projection's gradient
+    for (int p = std::max(o + 1, 2); p < 4; ++p)
+      if (ranges_overlap(outs[o].p, outs[o].n, outs[p].p, outs[p].n)) return KLA_ERR_INVALID_ARG;
+  }
+  const bool sums = gq_weight || gk_weight;
+  int sms = 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (tokens == 0 || Hq + Hk == 0) {
+    if (gq_weight && cudaMemsetAsync(gq_weight, 0, wb, s) != cudaSuccess) return KLA_ERR_CUDA;
+    if (gk_weight && cudaMemsetAsync(gk_weight, 0, wb, s) != cudaSuccess) return KLA_ERR_CUDA;
+    return KLA_OK;
+  }
+  if (sums && !workspace) return KLA_ERR_WORKSPACE;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
+  const size_t need = kla::norm_rope_partial_bytes(B, Hq, Hk, T, D, sms);
+  if (sums && ws_bytes < need) return KLA_ERR_WORKSPACE;
+  if (sums) {
+    const Range ws[] = {{workspace, need}};
+    if (ranges_clash(ws, 1, ins, 8) || ranges_clash(ws, 1, outs, 4)) return KLA_ERR_INVALID_ARG;
+  }
+  kla::NormRopeArgs a = norm_rope_args(inv_freq, positions, B, T, D, io, opt);
+  a.q = {q, s3[0][0], s3[0][1], s3[0][2], q_weight, nullptr, gyq, gq, g3[0][0], g3[0][1], g3[0][2], Hq};
+  a.k = {k, s3[1][0], s3[1][1], s3[1][2], k_weight, nullptr, gyk, gk, g3[1][0], g3[1][1], g3[1][2], Hk};
+  a.part = sums ? reinterpret_cast<float*>(workspace) : nullptr;
+  a.gwq = gq_weight; a.gwk = gk_weight;
+  return kla::launch_norm_rope_backward(a, sms, s) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 }  // extern "C"

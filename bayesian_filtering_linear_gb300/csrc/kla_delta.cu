@@ -1,0 +1,151 @@
+// The gated delta rule over a sequence, token by token (sm_103a):
+//
+//   u_t = β_t (v_t − a_t S_{t−1}ᵀ k_t),   S_t = a_t S_{t−1} + k_t u_tᵀ,   o_t = scale · S_tᵀ q_t
+//
+// The columns of a state are independent recurrences that share k, q, a, β.
+// A lane keeps RL rows of one column in registers, as fp32 pairs for the
+// packed arithmetic, and G = DK / RL neighbouring lanes hold a column; the
+// two dot products end in log2(G) lane exchanges. Tokens come through shared
+// memory sixteen at a time (a tile of k and q rows serves every column of
+// the block). Per state element a token costs four multiply-adds (k·S, k u,
+// a S + k u, q·S); the chain from one token to the next is a dot product, its
+// exchanges and the update, which is what bounds a call with few heads.
+#include "kla_device.cuh"
+#include "kla_launch.h"
+
+namespace kla {
+
+namespace {
+
+constexpr int kTile = kDeltaCkpt;  // tokens staged at a time
+
+template <typename IO, int DK, bool CKPT>
+__global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArgs a, float* ckpt) {
+  constexpr int RL = DK >= 64 ? 16 : DK / 4, G = DK / RL, NC = 128 / G, Q4 = RL / 4;
+  __shared__ __align__(16) float ks[kTile][DK], qs[kTile][DK], vs[kTile][NC], os[kTile][NC];
+  __shared__ float as[kTile], bs[kTile];
+  const int tid = threadIdx.x, r = tid % G, c = tid / G;
+  const int col_blocks = (a.dv + NC - 1) / NC;
+  const long long bh = blockIdx.x / col_blocks;
+  const int c0 = (int)(blockIdx.x % col_blocks) * NC, j = c0 + c;
+  const bool mine = j < a.dv;  // heads narrower than a block leave lanes idle
+  const int h = (int)(bh % a.H);
+  const long long key = (bh / a.H) * a.Hk + h / (a.H / a.Hk);
+  const int T = a.T;
+  const IO* q = reinterpret_cast<const IO*>(a.q) + key * T * DK;
+  const IO* k = reinterpret_cast<const IO*>(a.k) + key * T * DK;
+  const IO* v = reinterpret_cast<const IO*>(a.v) + bh * T * a.dv;
+  const IO* g = reinterpret_cast<const IO*>(a.g) + bh * T;
+  const IO* beta = reinterpret_cast<const IO*>(a.beta) + bh * T;
+  IO* o = reinterpret_cast<IO*>(a.o) + bh * T * a.dv;
+
+  // rows of the lane: float4 groups r, r + G, ... so that G lanes read one
+  // stretch of k and q
+  f2 S[2 * Q4];
+#pragma unroll
+  for (int i = 0; i < Q4; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = 0.f, y = 0.f;
+      if (a.state0 && mine) {
+        const float* p = a.state0 + ((size_t)bh * DK + (i * G + r) * 4 + 2 * e) * a.dv + j;
+        x = p[0];
+        y = p[a.dv];
+      }
+      S[2 * i + e] = f2_make(x, y);
+    }
+  const int chunks = (T + kTile - 1) / kTile;
+  for (int n = 0; n < chunks; ++n) {
+    const int t0 = n * kTile, len = min(kTile, T - t0);
+    if (CKPT && mine) {
+#pragma unroll
+      for (int i = 0; i < 2 * Q4; ++i) {
+        float* p = ckpt + (((size_t)bh * chunks + n) * DK + ((i >> 1) * G + r) * 4 + 2 * (i & 1)) * a.dv + j;
+        p[0] = f2_lo(S[i]);
+        p[a.dv] = f2_hi(S[i]);
+      }
+    }
+    for (int i = tid; i < len * DK; i += 128) {
+      ks[i / DK][i % DK] = to_f32<IO>(k[(size_t)t0 * DK + i]);
+      qs[i / DK][i % DK] = a.scale * to_f32<IO>(q[(size_t)t0 * DK + i]);
+    }
+    for (int i = tid; i < len * NC; i += 128)
+      if (c0 + i % NC < a.dv) vs[i / NC][i % NC] = to_f32<IO>(v[(size_t)(t0 + i / NC) * a.dv + c0 + i % NC]);
+    if (tid < len) {
+      as[tid] = expf(to_f32<IO>(g[t0 + tid]));
+      bs[tid] = to_f32<IO>(beta[t0 + tid]);
+    }
+    __syncthreads();
+    for (int t = 0; t < len; ++t) {
+      f2 kk[2 * Q4], p0 = 0, p1 = 0;
+#pragma unroll
+      for (int i = 0; i < Q4; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&ks[t][(i * G + r) * 4]);
+        kk[2 * i] = x.x;
+        kk[2 * i + 1] = x.y;
+        p0 = f2_fma(x.x, S[2 * i], p0);
+        p1 = f2_fma(x.y, S[2 * i + 1], p1);
+      }
+      p0 = f2_add(p0, p1);
+      float p = f2_lo(p0) + f2_hi(p0);
+#pragma unroll
+      for (int m = 1; m < G; m <<= 1) p += __shfl_xor_sync(~0u, p, m);
+      const float decay = as[t], u = bs[t] * (vs[t][c] - decay * p);
+      const f2 u2 = f2_make(u, u), a2 = f2_make(decay, decay);
+      f2 o0 = 0, o1 = 0;
+#pragma unroll
+      for (int i = 0; i < Q4; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&qs[t][(i * G + r) * 4]);
+        S[2 * i] = f2_fma(a2, S[2 * i], f2_mul(kk[2 * i], u2));
+        S[2 * i + 1] = f2_fma(a2, S[2 * i + 1], f2_mul(kk[2 * i + 1], u2));
+        o0 = f2_fma(x.x, S[2 * i], o0);
+        o1 = f2_fma(x.y, S[2 * i + 1], o1);
+      }
+      o0 = f2_add(o0, o1);
+      float y = f2_lo(o0) + f2_hi(o0);
+#pragma unroll
+      for (int m = 1; m < G; m <<= 1) y += __shfl_xor_sync(~0u, y, m);
+      if (r == 0) os[t][c] = y;
+    }
+    __syncthreads();
+    if (a.o)
+      for (int i = tid; i < len * NC; i += 128)
+        if (c0 + i % NC < a.dv) o[(size_t)(t0 + i / NC) * a.dv + c0 + i % NC] = from_f32<IO>(os[i / NC][i % NC]);
+  }
+  if (a.stateT && mine) {
+#pragma unroll
+    for (int i = 0; i < 2 * Q4; ++i) {
+      float* p = a.stateT + ((size_t)bh * DK + ((i >> 1) * G + r) * 4 + 2 * (i & 1)) * a.dv + j;
+      p[0] = f2_lo(S[i]);
+      p[a.dv] = f2_hi(S[i]);
+    }
+  }
+}
+
+template <typename IO, int DK>
+void launch_dk(const DeltaArgs& a, float* ckpt, cudaStream_t s) {
+  constexpr int NC = 128 / (DK >= 64 ? DK / 16 : 4);
+  const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.dv + NC - 1) / NC));
+  if (ckpt) kla_delta_recurrent_kernel<IO, DK, true><<<blocks, 128, 0, s>>>(a, ckpt);
+  else kla_delta_recurrent_kernel<IO, DK, false><<<blocks, 128, 0, s>>>(a, nullptr);
+}
+
+template <typename IO>
+void launch_io(const DeltaArgs& a, float* ckpt, cudaStream_t s) {
+  switch (a.dk) {
+    case 16: launch_dk<IO, 16>(a, ckpt, s); break;
+    case 32: launch_dk<IO, 32>(a, ckpt, s); break;
+    case 64: launch_dk<IO, 64>(a, ckpt, s); break;
+    default: launch_dk<IO, 128>(a, ckpt, s); break;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_delta_recurrent(const DeltaArgs& a, float* ckpt, cudaStream_t s) {
+  if (a.io == IO_BF16) launch_io<__nv_bfloat16>(a, ckpt, s);
+  else launch_io<float>(a, ckpt, s);
+  return cudaGetLastError();
+}
+
+}  // namespace kla

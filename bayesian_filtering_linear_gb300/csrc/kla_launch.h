@@ -129,4 +129,56 @@ size_t conv_partial_bytes(int B, int H, int T, int D, int W, int num_sms);
 cudaError_t launch_conv(const ConvArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_conv_backward(const ConvArgs& a, int num_sms, cudaStream_t s);
 
+// Gated delta rule (kla_delta*.cu). q, k [B,Hk,T,dk], v, o [B,H,T,dv], g, beta
+// [B,H,T] in io; states [B,H,dk,dv] fp32. Value head h reads key head
+// h / (H / Hk). Null state pointers: zeros / not wanted.
+struct DeltaArgs {
+  const void *q, *k, *v, *g, *beta;
+  const float* state0;
+  void* o;
+  float* stateT;
+  int B, Hk, H, T, dk, dv;
+  int io;
+  float scale;
+};
+struct DeltaGradArgs {
+  const void* go;         // dL/do, or null (zero)
+  const float* gstateT;   // dL/dS_T, or null (zero)
+  void *gq, *gk, *gv, *gg, *gbeta;
+  float* gstate0;         // dL/dS_0, or null
+};
+cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t s);
+// Token by token with the state in registers. `ckpt`: also store the state
+// before every kDeltaCkpt-th token, [B·H][ceil(T / kDeltaCkpt)][dk][dv] fp32.
+constexpr int kDeltaCkpt = 16;
+cudaError_t launch_delta_recurrent(const DeltaArgs& a, float* ckpt, cudaStream_t s);
+size_t delta_backward_bytes(int B, int Hk, int H, int T, int dk, int dv);
+cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, void* workspace, cudaStream_t s);
+
+// Norm of queries and keys with the position rotation (kla_norm_rope.cu).
+// Strides in elements, last dimension contiguous.
+struct NormRopeTensor {
+  const void* x;       // [B,H,T,D] by strides
+  long long sb, sh, st;
+  const float* w;      // [D] or null (ones)
+  void* y;             // forward: contiguous [B,H,T,D]
+  const void* gy;      // backward: contiguous [B,H,T,D], or null (zero)
+  void* gx;            // backward: by strides of its own
+  long long gsb, gsh, gst;
+  int H;
+};
+struct NormRopeArgs {
+  NormRopeTensor q, k;
+  const float* inv_freq;        // [rot/2]
+  const long long* positions;   // [B,T], or null: offset + t
+  long long offset;
+  int B, T, D, rot, norm, layout, io;
+  float eps, rot_scale;
+  float* part;                  // backward: per-block weight-gradient partials [blocks][2][D], or null
+  float *gwq, *gwk;             // backward: [D] fp32, or null
+};
+size_t norm_rope_partial_bytes(int B, int Hq, int Hk, int T, int D, int num_sms);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_rope_backward(const NormRopeArgs& a, int num_sms, cudaStream_t s);
+
 }  // namespace kla

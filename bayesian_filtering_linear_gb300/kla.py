@@ -9,6 +9,7 @@ implementation here. If the library is missing this module fails to import.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -26,7 +27,9 @@ EXPORTS = ("kla_plan", "kla_plan_for_sms", "kla_forward_workspace_size", "kla_fo
            "kla_status_string", "kla_version", "kla_forward_chunked_noalloc", "kla_backward_workspace_size",
            "kla_backward", "kla_forward_uncertainty", "kla_step_gated", "kla_backward_plan_for_sms",
            "kla_shard_map", "kla_shard_start", "kla_conv", "kla_conv_backward_workspace_size",
-           "kla_conv_backward")
+           "kla_conv_backward", "kla_delta_forward", "kla_delta_step", "kla_delta_backward_workspace_size",
+           "kla_delta_backward", "kla_norm_rope", "kla_norm_rope_backward_workspace_size",
+           "kla_norm_rope_backward")
 
 
 class Options(ctypes.Structure):
@@ -37,6 +40,11 @@ class Options(ctypes.Structure):
 class BackwardPlanInfo(ctypes.Structure):
     _fields_ = [("cols_per_block", ctypes.c_int), ("cols_per_lane", ctypes.c_int), ("threads", ctypes.c_int),
                 ("column_blocks", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class NormRopeOptions(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("eps", ctypes.c_float),
+                ("rot_scale", ctypes.c_float), ("offset", ctypes.c_longlong)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -88,6 +96,21 @@ def load_library(path: str = LIB_PATH):
     lib.kla_conv_backward_workspace_size.argtypes = [i] * 5
     lib.kla_conv_backward.restype = i
     lib.kla_conv_backward.argtypes = [vp] * 10 + [i] * 7 + [vp, sz, vp]
+    f, strides, nr = ctypes.c_float, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(NormRopeOptions)
+    lib.kla_delta_forward.restype = i
+    lib.kla_delta_forward.argtypes = [vp] * 8 + [i] * 7 + [f, vp]
+    lib.kla_delta_step.restype = i
+    lib.kla_delta_step.argtypes = [vp] * 7 + [i] * 6 + [f, vp]
+    lib.kla_delta_backward_workspace_size.restype = sz
+    lib.kla_delta_backward_workspace_size.argtypes = [i] * 6
+    lib.kla_delta_backward.restype = i
+    lib.kla_delta_backward.argtypes = [vp] * 14 + [i] * 7 + [f, vp, sz, vp]
+    lib.kla_norm_rope.restype = i
+    lib.kla_norm_rope.argtypes = [vp] * 8 + [i] * 5 + [strides, strides, i, nr, vp]
+    lib.kla_norm_rope_backward_workspace_size.restype = sz
+    lib.kla_norm_rope_backward_workspace_size.argtypes = [i] * 5
+    lib.kla_norm_rope_backward.restype = i
+    lib.kla_norm_rope_backward.argtypes = [vp] * 12 + [i] * 5 + [strides] * 4 + [i, nr, vp, sz, vp]
     return lib
 
 
@@ -478,6 +501,241 @@ def conv_backward(x, weight, bias=None, window=None, *, gy=None, gwindow_out=Non
     return out
 
 
+# ---- the gated delta rule ------------------------------------------------------
+
+def _delta_shapes(q, k, v, g, beta, tokens=True):
+    B, Hk, T, dk = q.shape if tokens else (*q.shape[:2], 1, q.shape[2])
+    H, dv = v.shape[1], v.shape[-1]
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if dt not in _IO:
+        raise TypeError(f"unsupported I/O dtype {dt}")
+    t = (T,) if tokens else ()
+    for name, x, shape in (("q", q, (B, Hk, *t, dk)), ("k", k, (B, Hk, *t, dk)), ("v", v, (B, H, *t, dv)),
+                           ("g", g, (B, H, *t)), ("beta", beta, (B, H, *t))):
+        _need(x, name, dt, shape, dev)
+    return B, Hk, H, T, dk, dv, dev, dt
+
+
+def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, o=None, stateT=None,
+                  final_state: bool = True, stream=None):
+    """The gated delta rule over whole sequences (kla_delta_forward): with
+    a = e^g, per token ``u = β (v − a Sᵀk)``, ``S ← a S + k uᵀ``, ``o = scale · Sᵀq``.
+    q, k ``[B,Hk,T,dk]``, v ``[B,H,T,dv]`` (H a multiple of Hk), g, beta
+    ``[B,H,T]``; ``state0`` fp32 ``[B,H,dk,dv]`` (None: zeros). ``scale``:
+    dk^-0.5 when None. Returns ``(o, stateT)`` (stateT None when
+    ``final_state`` is False and none was given)."""
+    B, Hk, H, T, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta)
+    for name, t in (("state0", state0), ("stateT", stateT)):
+        if t is not None:
+            _need(t, name, torch.float32, (B, H, dk, dv), dev)
+    if o is None:
+        o = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+    else:
+        _need(o, "o", dt, (B, H, T, dv), dev)
+    if final_state and stateT is None:
+        stateT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = LIB.kla_delta_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state0), _ptr(o),
+                                   _ptr(stateT), B, Hk, H, T, dk, dv, _IO[dt],
+                                   dk ** -0.5 if scale is None else scale, _stream(stream))
+    _check(st, "kla_delta_forward")
+    return o, stateT
+
+
+def delta_step(q, k, v, g, beta, state, *, scale: float | None = None, o=None, stream=None):
+    """One decode token of the gated delta rule (kla_delta_step): q, k
+    ``[B,Hk,dk]``, v ``[B,H,dv]``, g, beta ``[B,H]``; the fp32 state
+    ``[B,H,dk,dv]`` is updated in place; returns o."""
+    B, Hk, H, _, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta, tokens=False)
+    _need(state, "state", torch.float32, (B, H, dk, dv), dev)
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=dt, device=dev)
+    else:
+        _need(o, "o", dt, (B, H, dv), dev)
+    with torch.cuda.device(dev):
+        st = LIB.kla_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(o), B, Hk, H, dk,
+                                dv, _IO[dt], dk ** -0.5 if scale is None else scale, _stream(stream))
+    _check(st, "kla_delta_step")
+    return o
+
+
+def delta_backward(q, k, v, g, beta, state0=None, *, go=None, gstateT=None, scale: float | None = None,
+                   state_grad: bool = True, workspace=None, stream=None):
+    """Gradients of a scalar loss through :func:`delta_forward` given ``go`` =
+    dL/do and optionally ``gstateT`` = dL/dS_T (kla_delta_backward). Returns a
+    dict with ``gq, gk, gv, gg, gbeta`` (I/O dtype) and, with ``state_grad``,
+    ``gstate0`` (fp32)."""
+    B, Hk, H, T, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta)
+    for name, t in (("state0", state0), ("gstateT", gstateT)):
+        if t is not None:
+            _need(t, name, torch.float32, (B, H, dk, dv), dev)
+    if go is not None:
+        _need(go, "go", dt, (B, H, T, dv), dev)
+    out = {"gq": torch.empty_like(q), "gk": torch.empty_like(k), "gv": torch.empty_like(v),
+           "gg": torch.empty_like(g), "gbeta": torch.empty_like(beta)}
+    if state_grad:
+        out["gstate0"] = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = LIB.kla_delta_backward_workspace_size(B, Hk, H, T, dk, dv)
+            if nbytes == ctypes.c_size_t(-1).value:
+                raise KlaError(ERR_INVALID_ARG, "kla_delta_backward_workspace_size")
+            workspace = torch.empty(int(nbytes), dtype=torch.uint8, device=dev) if nbytes else None
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = LIB.kla_delta_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state0), _ptr(go),
+                                    _ptr(gstateT), _ptr(out["gq"]), _ptr(out["gk"]), _ptr(out["gv"]),
+                                    _ptr(out["gg"]), _ptr(out["gbeta"]), _ptr(out.get("gstate0")), B, Hk, H, T, dk,
+                                    dv, _IO[dt], dk ** -0.5 if scale is None else scale, _ptr(workspace), ws_bytes,
+                                    _stream(stream))
+    _check(st, "kla_delta_backward")
+    return out
+
+
+# ---- norm of queries and keys with the position rotation ------------------------
+
+_NORMS = {"none": 0, "rms": 1, "l2": 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Rotation frequencies ``[rot_dim/2]`` (fp32) and the factor for the
+    rotated entries (``rot_scale``), optionally scaled for contexts ``factor``
+    times as long as the ``original_length`` that a model was trained on:
+    "linear" divides every frequency by the factor; "ntk" raises the base so
+    that the lowest frequency is divided by it and the highest kept; "bands"
+    keeps frequencies that turn at least ``beta_fast`` times over the original
+    length, divides those that turn at most ``beta_slow`` times, blends linearly
+    (over the pair's index) between, and scales the rotated entries by
+    0.1 ln(factor) + 1."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if scaling not in ("none", "linear", "ntk", "bands"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling != "none" and factor < 1.0:
+        raise ValueError("factor must be at least 1")
+    half, rot_scale = rot_dim // 2, 1.0
+    i = torch.arange(half, dtype=torch.float64)
+    if scaling == "ntk" and half > 1:
+        base = base * factor ** (half / (half - 1))
+    freq = base ** (-i / max(half, 1))
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "bands":
+        if original_length < 1:
+            raise ValueError("scaling by bands needs original_length")
+
+        def index(turns):  # the pair that turns so often over the original length
+            return half * math.log(original_length / (2 * math.pi * turns)) / math.log(base)
+
+        lo, hi = max(0.0, math.floor(index(beta_fast))), min(half - 1.0, math.ceil(index(beta_slow)))
+        slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - slow) + freq / factor * slow
+        rot_scale = 0.1 * math.log(factor) + 1.0
+    return freq.float().to(device or "cpu"), rot_scale
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale):
+    B, Hq, T, D = q.shape
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if dt not in _IO:
+        raise TypeError(f"unsupported I/O dtype {dt}")
+    if norm not in _NORMS or layout not in _LAYOUTS:
+        raise ValueError(f"unknown norm {norm!r} or layout {layout!r}")
+    Hk = 0 if k is None else k.shape[1]
+    for name, x, h in (("q", q, Hq), ("k", k, Hk)):
+        if x is None:
+            continue
+        if x.device != dev or x.dtype != dt or tuple(x.shape) != (B, h, T, D):
+            raise ValueError(f"{name} must be {(B, h, T, D)} of {dt} on {dev}")
+        if x.numel() and x.stride(-1) != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, name, torch.float32, (D,), dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
+    if positions is not None:
+        _need(positions, "positions", torch.int64, (B, T), dev)
+    opt = NormRopeOptions(_NORMS[norm], _LAYOUTS[layout], rot, eps, rot_scale, int(offset))
+    strides = [None if x is None else (ctypes.c_longlong * 3)(*x.stride()[:3]) for x in (q, k)]
+    return B, Hq, Hk, T, D, dev, dt, opt, strides
+
+
+def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, norm: str = "rms",
+              layout: str = "half", eps: float = 1e-6, rot_scale: float = 1.0, offset: int = 0, yq=None, yk=None,
+              stream=None):
+    """Per-head norm ("rms", "l2" or "none") of queries and keys with weights
+    ``[D]`` (fp32, None: ones) and the rotation of their first
+    ``2·len(inv_freq)`` entries by position (kla_norm_rope). q ``[B,Hq,T,D]``
+    and k ``[B,Hk,T,D]`` (or None) may be strided views, e.g. a projection's
+    ``[B,T,H,D]`` transposed; ``positions`` int64 ``[B,T]`` (None: ``offset`` +
+    t). Returns contiguous ``(yq, yk)``."""
+    B, Hq, Hk, T, D, dev, dt, opt, strides = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset,
+                                                             norm, layout, eps, rot_scale)
+    if yq is None:
+        yq = torch.empty((B, Hq, T, D), dtype=dt, device=dev)
+    else:
+        _need(yq, "yq", dt, (B, Hq, T, D), dev)
+    if k is not None:
+        if yk is None:
+            yk = torch.empty((B, Hk, T, D), dtype=dt, device=dev)
+        else:
+            _need(yk, "yk", dt, (B, Hk, T, D), dev)
+    with torch.cuda.device(dev):
+        st = LIB.kla_norm_rope(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions),
+                               _ptr(yq), _ptr(yk), B, Hq, Hk, T, D, strides[0], strides[1], _IO[dt],
+                               ctypes.byref(opt), _stream(stream))
+    _check(st, "kla_norm_rope")
+    return yq, yk
+
+
+def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, gyq=None, gyk=None,
+                       norm: str = "rms", layout: str = "half", eps: float = 1e-6, rot_scale: float = 1.0,
+                       offset: int = 0, workspace=None, stream=None):
+    """Gradients through :func:`norm_rope` given ``gyq``, ``gyk`` (None: zero;
+    kla_norm_rope_backward). Returns a dict with ``gq, gk`` (in the memory
+    order of q and k) and, for given weights, ``gq_weight, gk_weight``."""
+    B, Hq, Hk, T, D, dev, dt, opt, strides = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset,
+                                                             norm, layout, eps, rot_scale)
+    for name, t, h in (("gyq", gyq, Hq), ("gyk", gyk, Hk)):
+        if t is not None:
+            _need(t, name, dt, (B, h, T, D), dev)
+    # gradients in the inputs' own order, dense whatever lies between a view's rows
+    out, gstrides = {}, [None, None]
+    for n, (name, x) in enumerate((("gq", q), ("gk", k))):
+        if x is None:
+            continue
+        order = sorted(range(3), key=lambda d: x.stride(d), reverse=True)
+        back = [order.index(d) for d in range(3)]
+        out[name] = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=dev).permute(*back, 3)
+        gstrides[n] = (ctypes.c_longlong * 3)(*out[name].stride()[:3])
+    for name, w in (("gq_weight", q_weight), ("gk_weight", k_weight)):
+        if w is not None:
+            out[name] = torch.empty((D,), dtype=torch.float32, device=dev)
+    sums = "gq_weight" in out or "gk_weight" in out
+    with torch.cuda.device(dev):
+        if workspace is None and sums:
+            nbytes = LIB.kla_norm_rope_backward_workspace_size(B, Hq, Hk, T, D)
+            if nbytes == ctypes.c_size_t(-1).value:
+                raise KlaError(ERR_CUDA, "kla_norm_rope_backward_workspace_size")
+            workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = LIB.kla_norm_rope_backward(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                                        _ptr(positions), _ptr(gyq), _ptr(gyk), _ptr(out["gq"]), _ptr(out.get("gk")),
+                                        _ptr(out.get("gq_weight")), _ptr(out.get("gk_weight")), B, Hq, Hk, T, D,
+                                        *strides, *gstrides, _IO[dt], ctypes.byref(opt), _ptr(workspace),
+                                        ws_bytes, _stream(stream))
+    _check(st, "kla_norm_rope_backward")
+    return out
+
+
 # ---- autograd: the entry points as differentiable torch operations ------------
 
 class _ScanFunction(torch.autograd.Function):
@@ -532,3 +790,55 @@ def causal_conv(x, weight, bias=None, window=None, *, activation: int = ACT_SILU
     ``(y, window_out)`` like :func:`conv`; gradients come from
     kla_conv_backward."""
     return _ConvFunction.apply(x, weight, bias, window, int(activation))
+
+
+class _DeltaFunction(torch.autograd.Function):
+    """kla_delta_forward with kla_delta_backward as its derivative."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, state0, scale):
+        o, stateT = delta_forward(q, k, v, g, beta, state0, scale=scale)
+        ctx.save_for_backward(q, k, v, g, beta, state0)
+        ctx.scale = scale
+        return o, stateT
+
+    @staticmethod
+    def backward(ctx, go, gstateT):
+        q, k, v, g, beta, state0 = ctx.saved_tensors
+        d = delta_backward(q, k, v, g, beta, state0, go=None if go is None else go.to(q.dtype).contiguous(),
+                           gstateT=None if gstateT is None else gstateT.contiguous(), scale=ctx.scale,
+                           state_grad=state0 is not None)
+        return d["gq"], d["gk"], d["gv"], d["gg"], d["gbeta"], d.get("gstate0"), None
+
+
+def delta_rule(q, k, v, g, beta, state0=None, *, scale: float | None = None):
+    """Differentiable gated delta rule (autograd): returns ``(o, stateT)`` like
+    :func:`delta_forward`; gradients come from kla_delta_backward."""
+    return _DeltaFunction.apply(q, k, v, g, beta, state0, scale)
+
+
+class _NormRopeFunction(torch.autograd.Function):
+    """kla_norm_rope with kla_norm_rope_backward as its derivative."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, how):
+        ctx.save_for_backward(q, k, q_weight, k_weight, inv_freq, positions)
+        ctx.how = how
+        return norm_rope(q, k, q_weight, k_weight, inv_freq, positions, **how)
+
+    @staticmethod
+    def backward(ctx, gyq, gyk):
+        q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
+        d = norm_rope_backward(q, k, q_weight, k_weight, inv_freq, positions,
+                               gyq=None if gyq is None else gyq.to(q.dtype).contiguous(),
+                               gyk=None if gyk is None else gyk.to(q.dtype).contiguous(), **ctx.how)
+        return d["gq"], d.get("gk"), d.get("gq_weight"), d.get("gk_weight"), None, None, None
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, norm: str = "rms",
+                 layout: str = "half", eps: float = 1e-6, rot_scale: float = 1.0, offset: int = 0):
+    """Differentiable norm and rotation of queries and keys (autograd): returns
+    ``(yq, yk)`` like :func:`norm_rope`; gradients come from
+    kla_norm_rope_backward."""
+    how = {"norm": norm, "layout": layout, "eps": eps, "rot_scale": rot_scale, "offset": offset}
+    return _NormRopeFunction.apply(q, k, q_weight, k_weight, inv_freq, positions, how)

@@ -364,6 +364,103 @@ kla_status kla_conv_backward(const void* x, const float* weight, const float* bi
                              void* gwindow, int B, int H, int T, int D, int W, kla_dtype io, int activation,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- the gated delta rule ------------------------------------------------
+ * A sequence mixer beside the Kalman scan, over the same head layout: each
+ * value head carries a matrix state S [d_k, d_v] whose update erases what the
+ * state holds under the key before it writes (the Kalman update with a
+ * diagonal covariance replaced by a step of strength β along k). Per token,
+ * with decay a = e^g:
+ *     u = β (v − a Sᵀk),   S ← a S + k uᵀ,   o = scale · Sᵀq
+ * q, k [B,Hk,T,dk]; v, o [B,H,T,dv]; g, beta [B,H,T]: all in `io`. H is a
+ * multiple of Hk; value head h reads key head h / (H / Hk). States [B,H,dk,dv]
+ * are fp32. d_k, d_v, alignment, streams and errors as in the conventions
+ * above, but the gates g, beta and their gradients need only the alignment of
+ * their elements (a token's slice may start anywhere); B, Hk, H, T ≥ 0, and H
+ * not a multiple of Hk (or Hk = 0 < H) is INVALID_ARG. Domain: g ≤ 0 (−∞
+ * resets the state), any β; the recurrence is a contraction for ‖k‖ ≤ 1 and
+ * 0 ≤ β ≤ 2 (kla_norm_rope normalises keys). Nothing traps outside it. */
+
+/* Whole sequences.
+ *   state0: the state before the first token, or NULL for zeros.
+ *   o (required unless B·H·T = 0) must not overlap any input.
+ *   stateT: the state after the last token, or NULL. It may be state0 itself
+ *     (an in-place update) but must not overlap it otherwise. T = 0 copies
+ *     the state. */
+kla_status kla_delta_forward(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const float* state0, void* o, float* stateT, int B, int Hk, int H, int T, int dk,
+                             int dv, kla_dtype io, float scale, void* stream);
+
+/* One decode token: q, k [B,Hk,dk]; v, o [B,H,dv]; g, beta [B,H]; the state
+ * [B,H,dk,dv] is read and overwritten. */
+kla_status kla_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                          float* state, void* o, int B, int Hk, int H, int dk, int dv, kla_dtype io, float scale,
+                          void* stream);
+
+/* Gradients of a loss L through kla_delta_forward.
+ *   go = dL/do [B,H,T,dv] in `io`, gstateT = dL/dS_T fp32 (each NULL: zero).
+ *   Outputs, written and not accumulated, in `io`: gq, gk [B,Hk,T,dk] (summed
+ *     over the value heads of a key head in a fixed order), gv [B,H,T,dv], gg,
+ *     gbeta [B,H,T]; required unless B·H·T = 0. gstate0 fp32 [B,H,dk,dv] or
+ *     NULL: dL/dS_0 (with state0 NULL: at zero).
+ *   workspace / ws_bytes: device scratch of at least
+ *     kla_delta_backward_workspace_size() bytes (else WORKSPACE).
+ *   Outputs and the workspace must not overlap inputs or each other. Repeated
+ *   calls give identical bits. */
+size_t kla_delta_backward_workspace_size(int B, int Hk, int H, int T, int dk, int dv);
+kla_status kla_delta_backward(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                              const float* state0, const void* go, const float* gstateT, void* gq, void* gk,
+                              void* gv, void* gg, void* gbeta, float* gstate0, int B, int Hk, int H, int T, int dk,
+                              int dv, kla_dtype io, float scale, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- norm of queries and keys with the position rotation -----------------
+ * What a mixer's queries and keys go through after their projection, in one
+ * pass: every row x of D entries becomes
+ *     n = x · r · w,  r = 1/sqrt(mean(x²) + eps) (RMS), 1/sqrt(Σx² + eps) (L2) or 1 (NONE)
+ *     y = n with its first rot_dim entries turned: pair i by the angle
+ *         position · inv_freq[i], times rot_scale
+ * where pair i is (i, i + rot_dim/2) (HALF) or (2i, 2i + 1) (INTERLEAVED). */
+typedef enum kla_norm { KLA_NORM_NONE = 0, KLA_NORM_RMS = 1, KLA_NORM_L2 = 2 } kla_norm;
+typedef enum kla_rope_layout { KLA_ROPE_HALF = 0, KLA_ROPE_INTERLEAVED = 1 } kla_rope_layout;
+
+typedef struct kla_norm_rope_options {
+  int norm;         /* kla_norm */
+  int layout;       /* kla_rope_layout */
+  int rot_dim;      /* even, 0 ≤ rot_dim ≤ D; 0: no rotation */
+  float eps;        /* ≥ 0 */
+  float rot_scale;  /* multiplies the rotated entries (1 unless a long-context scaling asks for more) */
+  long long offset; /* position of token 0 where `positions` is NULL */
+} kla_norm_rope_options;
+
+/*   q [B,Hq,T,D], k [B,Hk,T,D] in `io`, by strides in elements
+ *     {batch, head, token} (NULL: contiguous); the last dimension is
+ *     contiguous and every stride a multiple of 16 bytes (else MISALIGNED).
+ *     A projection's [B,T,H,D] is thus read in place. Hk = 0 leaves k out.
+ *   q_weight, k_weight [D] fp32, or NULL for ones.
+ *   inv_freq [rot_dim/2] fp32 (required when rot_dim > 0).
+ *   positions [B,T] 64-bit, |position| < 2^44, or NULL: offset + t.
+ *   yq, yk: contiguous [B,H,T,D] in `io`; must not overlap any input.
+ *   D one of 16, 32, 64, 128 (else UNSUPPORTED_SHAPE). */
+kla_status kla_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                         const float* inv_freq, const long long* positions, void* yq, void* yk, int B, int Hq,
+                         int Hk, int T, int D, const long long* q_strides, const long long* k_strides,
+                         kla_dtype io, const kla_norm_rope_options* opt, void* stream);
+
+/* Gradients through kla_norm_rope: gyq, gyk contiguous [B,H,T,D] in `io`
+ * (NULL: zero). gq, gk in `io`, by strides of their own (as q's and k's;
+ * NULL: contiguous; required unless empty); their rows must not share memory.
+ * gq_weight, gk_weight [D] fp32 or NULL to skip, summed over B, heads and T in
+ * a fixed order.
+ *   workspace / ws_bytes: kla_norm_rope_backward_workspace_size() bytes when
+ *   a weight gradient is wanted (else WORKSPACE); may be NULL otherwise. */
+size_t kla_norm_rope_backward_workspace_size(int B, int Hq, int Hk, int T, int D);
+kla_status kla_norm_rope_backward(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                  const float* inv_freq, const long long* positions, const void* gyq,
+                                  const void* gyk, void* gq, void* gk, float* gq_weight, float* gk_weight, int B,
+                                  int Hq, int Hk, int T, int D, const long long* q_strides,
+                                  const long long* k_strides, const long long* gq_strides,
+                                  const long long* gk_strides, kla_dtype io, const kla_norm_rope_options* opt,
+                                  void* workspace, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* kla_status_string(kla_status s);
 
