@@ -16,9 +16,9 @@
 // of a row, are computed once for all heads of the group. Input strides are
 // free: a projection's [B,T,H,D] is read in place and leaves as [B,H,T,D].
 //
-// Angles: pos·f / 2π is formed as an unevaluated sum of two floats from f/2π
-// split the same way, its whole turns taken off exactly, and the rest given to
-// sincospif, so that a position of millions is as exact as the first.
+// Angles: pos·f / 2π is formed from f/2π as an unevaluated sum of floats, each
+// term's whole turns taken off exactly, and the rest given to sincospif, so
+// that a position of billions is as exact as the first.
 #include <algorithm>
 
 #include "kla_device.cuh"
@@ -68,23 +68,26 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// The part of a turn that pos·f leaves: in [-0.5, 0.5] turns.
+__device__ __forceinline__ float fraction(float x) { return x - rintf(x); }
+
+// The part of a turn that pos·f leaves: in [-0.5, 0.5] turns, for |pos| < 2^44.
 __device__ __forceinline__ float turn_of(long long pos, float f) {
-  constexpr float kHi = 0.15915494309189535f;               // 1/2π in two floats
-  constexpr float kLo = (float)(0.15915494309189535 - (double)kHi);
-  const float h = f * kHi, l = fmaf(f, kHi, -h) + f * kLo;  // f/2π = h + l
-  // pos = p1·2^20 + p0, both exact in fp32 for |pos| < 2^44
-  const float p0 = (float)(pos & 0xfffff), p1 = (float)(pos >> 20) * 1048576.f;
+  // 1/2π = k0 + k1 + k2 (to 2^-78), and f/2π = h + l + m
+  constexpr float k0 = 0x1.45f306p-3f, k1 = 0x1.b9391p-28f, k2 = 0x1.529fc2p-54f;
+  const float h = f * k0, e = fmaf(f, k0, -h);
+  const float h1 = f * k1, e1 = fmaf(f, k1, -h1);
+  const float l = e + h1, m = ((e - (l - h1)) + (h1 - (l - (l - h1)))) + e1 + f * k2;
+  // pos = p1·2^20 + p0, both exact in fp32
+  const float part[2] = {(float)(pos & 0xfffff), (float)(pos >> 20) * 1048576.f};
   float turn = 0.f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float p = i ? p1 : p0;
-    const float x = p * h, e = fmaf(p, h, -x);  // p·h = x + e exactly
-    float low = fmaf(p, l, e);
-    low -= rintf(low);
-    turn += (x - rintf(x)) + low;
+    const float p = part[i];
+    const float x = p * h, xe = fmaf(p, h, -x);  // p·h = x + xe exactly, and the same for l
+    const float y = p * l, ye = fmaf(p, l, -y);
+    turn += (fraction(x) + fraction(xe)) + (fraction(y) + fmaf(p, m, ye));
   }
-  return turn - rintf(turn);
+  return fraction(turn);
 }
 
 // The angles of a lane's elements, as y = x·c + other·s with the sign of the
