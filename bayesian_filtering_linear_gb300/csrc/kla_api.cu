@@ -753,27 +753,35 @@ kla_status kla_conv_backward(const void* x, const float* weight, const float* bi
                                                                                                   : KLA_ERR_CUDA;
 }
 
+size_t kla_delta_forward_workspace_size(int B, int Hk, int H, int T, int dk, int dv) {
+  if (check_delta_shape(B, Hk, H, T, dk, dv) != KLA_OK) return (size_t)-1;
+  if ((long long)B * H * T == 0) return 0;
+  return kla::delta_forward_bytes(B, Hk, H, T, dk, dv);
+}
+
 kla_status kla_delta_forward(const void* q, const void* k, const void* v, const void* g, const void* beta,
                              const float* state0, void* o, float* stateT, int B, int Hk, int H, int T, int dk,
-                             int dv, kla_dtype io, float scale, void* stream) {
+                             int dv, kla_dtype io, float scale, void* workspace, size_t ws_bytes, void* stream) {
   // ---- validation: no CUDA call before it passes ---------------------------
   const kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
   if (st != KLA_OK) return st;
   if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
   const long long bh = (long long)B * H, tokens = bh * T;
   if (tokens > 0 && (!q || !k || !v || !g || !beta || !o)) return KLA_ERR_INVALID_ARG;
-  const void* ptrs[] = {q, k, v, state0, o, stateT};
+  const void* ptrs[] = {q, k, v, state0, o, stateT, workspace};
   for (const void* ptr : ptrs)
     if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
   if (!gates_aligned(io, g, beta)) return KLA_ERR_MISALIGNED;
   const size_t z = io_size(io), keys = (size_t)B * Hk * T * dk * z, gates = (size_t)tokens * z;
   const size_t vals = (size_t)tokens * dv * z, states = (size_t)bh * dk * dv * sizeof(float);
   const Range ins[] = {{q, keys}, {k, keys}, {v, vals}, {g, gates}, {beta, gates}, {state0, states}};
-  const Range outs[] = {{stateT, states}, {o, vals}};
-  if (ranges_clash(outs, 2, ins, 6, 0, 5)) return KLA_ERR_INVALID_ARG;
+  const size_t need = tokens > 0 ? kla::delta_forward_bytes(B, Hk, H, T, dk, dv) : 0;
+  const Range outs[] = {{stateT, states}, {o, vals}, {workspace, need}};
+  if (ranges_clash(outs, 3, ins, 6, 0, 5)) return KLA_ERR_INVALID_ARG;
   if (bh == 0 || (T == 0 && !stateT)) return KLA_OK;
+  if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
   kla::DeltaArgs a{q, k, v, g, beta, state0, o, stateT, B, Hk, H, T, dk, dv, (int)io, scale};
-  return kla::launch_delta_recurrent(a, nullptr, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK
+  return kla::launch_delta_forward(a, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK
                                                                                                         : KLA_ERR_CUDA;
 }
 

@@ -1,0 +1,133 @@
+// Shared pieces of the chunked gated delta rule (kla_delta_chunk.cu,
+// kla_delta_backward.cu): the workspace, tile loads and per-chunk gates.
+#pragma once
+
+#include "kla_launch.h"
+#include "kla_umma.cuh"
+
+namespace kla {
+namespace delta {
+
+using namespace umma;
+
+constexpr int C = 64;             // tokens of a chunk
+constexpr int kThreads = 256;     // of the kernels that take a chunk each
+constexpr int kGates = 5 * C;     // floats: cumulative g in two floats, decay from the start, to the end, β
+constexpr float kMinLog = -104.f; // e^-104 is 0 in fp32: smaller logs change nothing but the sums' exactness
+
+template <typename IO>
+constexpr int kParts = sizeof(IO) == 2 ? 1 : 3;  // bf16 parts that hold an input exactly (fp32: to 24 bits)
+
+__host__ __device__ constexpr int pad64(int d) { return d <= 64 ? 64 : 128; }
+
+// Per chunk of every value head, padded to whole chunks and to widths of 64.
+struct Workspace {
+  float* M;      // [chunks][64][64]: (I + A)^-1
+  float* gates;  // [chunks][5][64]
+  float* S;      // [chunks][DK][DV]: the state before each chunk
+  float* U;      // [chunks][64][DV]
+  float* Z;      // [chunks][DK][DV]: first Qᵀ(G O'), then the gradient of the state after each chunk
+  float* R;      // [chunks][64][DV]: first Pᵀ O', then dR
+  float* part;   // [B·H][T][2][dk]: gradients of q and k by value head (shared key heads)
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <typename IO>
+__device__ __forceinline__ float2 load_two(const IO* p);
+template <>
+__device__ __forceinline__ float2 load_two<float>(const float* p) { return *reinterpret_cast<const float2*>(p); }
+template <>
+__device__ __forceinline__ float2 load_two<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ void store_two(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store_two(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = bf16_pair(x, y);
+}
+template <typename IO>
+__device__ __forceinline__ void load_eight(const IO* p, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = load_two(p + 2 * i);
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+  }
+}
+
+// Rows [0, len) of 64 (the rest zero) of an io array [.][d], columns c0 to
+// c0 + W (those from d on zero), into tiles of kParts<IO> parts.
+template <typename IO, int W>
+__device__ __forceinline__ void load_tile(char* tile, const IO* src, int len, int d, int c0, int tid, int threads) {
+  constexpr int PARTS = kParts<IO>, PART = W / 64 * kTileBytes;
+  for (int i = tid; i < C * W / 8; i += threads) {
+    const int r = i / (W / 8), c = i % (W / 8) * 8;
+    char* t = tile + (c >> 6) * kTileBytes;
+    const bool in = r < len && c0 + c < d;
+    if (PARTS == 1) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (in) v = *reinterpret_cast<const uint4*>(src + (size_t)r * d + c0 + c);
+      *reinterpret_cast<uint4*>(t + r * 128 + ((((c >> 3) ^ r) & 7) << 4)) = v;
+    } else {
+      float x[8] = {};
+      if (in) {
+        const float4 lo = *reinterpret_cast<const float4*>(src + (size_t)r * d + c0 + c);
+        const float4 hi = *reinterpret_cast<const float4*>(src + (size_t)r * d + c0 + c + 4);
+        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+      }
+      store_eight<PARTS>(t, PART, r, c & 63, x);
+    }
+  }
+}
+
+// A workspace array's rows, 64 columns of row length ld, into one column of tiles.
+template <int PARTS, int ROWS>
+__device__ __forceinline__ void load_parts(char* tile, const float* src, int ld, int tid, int threads) {
+  for (int i = tid; i < ROWS * 8; i += threads) {
+    const int r = i >> 3, c = (i & 7) * 8;
+    const float4 lo = *reinterpret_cast<const float4*>(src + (size_t)r * ld + c);
+    const float4 hi = *reinterpret_cast<const float4*>(src + (size_t)r * ld + c + 4);
+    float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    store_eight<PARTS>(tile, ROWS * 128, r, c, x);
+  }
+}
+
+// Decay from token s to token t ≥ s of a chunk.
+__device__ __forceinline__ float decay(const float* hi, const float* lo, int t, int s) {
+  return expf((hi[t] - hi[s]) + (lo[t] - lo[s]));
+}
+
+// Everything of a block that starts a chunk: which one, and its rows.
+struct Where {
+  long long bh, key;
+  int n, t0, len;
+  size_t chunk;
+};
+__device__ __forceinline__ Where where(const DeltaArgs& a, long long chunk) {
+  const int N = (a.T + C - 1) / C;
+  Where w;
+  w.chunk = (size_t)chunk;
+  w.bh = chunk / N;
+  w.n = (int)(chunk % N);
+  w.key = (w.bh / a.H) * a.Hk + (w.bh % a.H) / (a.H / a.Hk);
+  w.t0 = w.n * C;
+  w.len = min(C, a.T - w.t0);
+  return w;
+}
+
+__device__ __forceinline__ char* align1024(char* p) {
+  return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 1023) / 1024 * 1024);
+}
+
+Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, bool backward, size_t* bytes);
+// M, gates and, with d, Pᵀ O' and Qᵀ(G O') (in R and Z).
+cudaError_t launch_prepare(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, cudaStream_t s);
+// The states before the chunks and U (rev: the gradients of the states after them and dR), one block per head
+// and 64 columns.
+cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, cudaStream_t s);
+
+}  // namespace delta
+}  // namespace kla

@@ -1,0 +1,166 @@
+// Matrix products of fp32 accuracy on the tensor cores (sm_103a), for 64-token
+// chunks: operands are tiles of 64 columns in shared memory, each kept as one
+// to three bf16 parts (x = hi + mid + lo holds 24 bits), products of parts go
+// through tcgen05.mma with fp32 accumulators in TMEM, and results come back to
+// registers in the 16x256b form: lane l of a warp has rows l/4 and l/4 + 8 of
+// its 16, columns 2(l%4) and 2(l%4) + 1 of every eight.
+//
+// A tile is rows of 128 bytes (64 bf16) with the 128-byte swizzle: 16-byte
+// unit u of row r is at r·128 + (u ^ (r & 7))·16 from a 1024-byte boundary. The
+// same tile serves as a K-major operand (rows are M or N, columns are K) or as
+// an MN-major one (rows are K, columns are M or N), so nothing is transposed.
+#pragma once
+
+#include "kla_device.cuh"
+
+namespace kla {
+namespace umma {
+
+constexpr int kTileBytes = 64 * 128;  // 64 rows
+
+// ---- barriers ---------------------------------------------------------------
+__device__ __forceinline__ void mbar_init(uint64_t* bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(done) : "r"(addr), "r"(parity) : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ uint64_t nanoseconds() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase of the given parity, for two seconds at most; then it
+// gives up: `ok` turns false, and later waits return at once.
+__device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, bool& ok) {
+  const uint32_t addr = smem_addr(bar);
+  if (!ok || mbar_try(addr, parity)) return;
+  const uint64_t start = nanoseconds();
+  while (!mbar_try(addr, parity))
+    if (nanoseconds() - start > 2000000000ull) {
+      ok = false;
+      return;
+    }
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// ---- TMEM ---------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, int cols) {  // one warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, int cols) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+// 16 lanes × 32 columns from `addr` (lane in the upper half)
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---- products -------------------------------------------------------------------
+// A tile operand of PARTS parts, `part` bytes apart, K-major (rows are M or N)
+// or MN-major (rows are K). `block`: bytes between its 64-column tiles.
+template <int PARTS, bool MN>
+struct Operand {
+  uint32_t addr;  // shared-memory address of part 0
+  int part, block;
+};
+// D[M×N] (+)= A·B over K of depth, issued by one thread. Sixteen of K are 32
+// bytes along a K-major row (the next tile after 64) or 16 rows of an MN-major
+// tile. Products of parts that weigh less than the last kept part are left out
+// (i + j ≥ the larger number of parts). The small products go first: the
+// accumulator is cut to 24 bits after every instruction, which costs nothing
+// while it is small (64³ with 3 × 3 parts: 1.2e-6 of the largest value with the
+// large products first).
+template <int M, int N, int K, int PA, bool AMN, int PB, bool BMN>
+__device__ __forceinline__ void mma(uint32_t d, const Operand<PA, AMN>& a, const Operand<PB, BMN>& b,
+                                    bool accumulate = false) {
+  constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)AMN << 15) | ((uint32_t)BMN << 16) |
+                             ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+  // descriptor: address, distance of 64-column blocks (MN-major), of eight rows, version 1, 128-byte swizzle
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  constexpr int most = PA > PB ? PA : PB;
+  const uint32_t la = ((a.addr & 0x3ffff) >> 4) | ((uint32_t)(AMN ? a.block >> 4 : 1) << 16);
+  const uint32_t lb = ((b.addr & 0x3ffff) >> 4) | ((uint32_t)(BMN ? b.block >> 4 : 1) << 16);
+  uint32_t acc = accumulate ? 1u : 0u;
+#pragma unroll
+  for (int w = most - 1; w >= 0; --w)
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int j = w - i;
+      if (j < 0 || j >= PB) continue;
+#pragma unroll
+      for (int k = 0; k < K / 16; ++k) {
+        const uint32_t oa = i * a.part + (AMN ? k * 2048 : (k >> 2) * a.block + (k & 3) * 32);
+        const uint32_t ob = j * b.part + (BMN ? k * 2048 : (k >> 2) * b.block + (k & 3) * 32);
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(la + (oa >> 4)),
+            "r"(lb + (ob >> 4)), "r"(hi), "r"(idesc), "r"(acc)
+            : "memory");
+        acc = 1u;
+      }
+    }
+}
+// `bar` gets one arrival when every product issued so far is done.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+// ---- parts ------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two neighbouring columns of row r as PARTS bf16 pairs into the tile.
+template <int PARTS>
+__device__ __forceinline__ void store_pair(char* tile, int part_bytes, int r, int c, float x, float y) {
+  char* p = tile + r * 128 + ((((c >> 3) ^ r) & 7) << 4) + (c & 7) * 2;
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    const uint32_t u = bf16_pair(x, y);
+    *reinterpret_cast<uint32_t*>(p + i * part_bytes) = u;
+    if (i + 1 < PARTS) {
+      x -= __uint_as_float(u << 16);
+      y -= __uint_as_float(u & 0xffff0000u);
+    }
+  }
+}
+// Eight neighbouring columns.
+template <int PARTS>
+__device__ __forceinline__ void store_eight(char* tile, int part_bytes, int r, int c, float (&x)[8]) {
+  char* p = tile + r * 128 + ((((c >> 3) ^ r) & 7) << 4);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j] = bf16_pair(x[2 * j], x[2 * j + 1]);
+      x[2 * j] -= __uint_as_float(u[j] << 16);
+      x[2 * j + 1] -= __uint_as_float(u[j] & 0xffff0000u);
+    }
+    *reinterpret_cast<uint4*>(p + i * part_bytes) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+}  // namespace umma
+}  // namespace kla

@@ -27,7 +27,7 @@ EXPORTS = ("kla_plan", "kla_plan_for_sms", "kla_forward_workspace_size", "kla_fo
            "kla_status_string", "kla_version", "kla_forward_chunked_noalloc", "kla_backward_workspace_size",
            "kla_backward", "kla_forward_uncertainty", "kla_step_gated", "kla_backward_plan_for_sms",
            "kla_shard_map", "kla_shard_start", "kla_conv", "kla_conv_backward_workspace_size",
-           "kla_conv_backward", "kla_delta_forward", "kla_delta_step", "kla_delta_backward_workspace_size",
+           "kla_conv_backward", "kla_delta_forward_workspace_size", "kla_delta_forward", "kla_delta_step", "kla_delta_backward_workspace_size",
            "kla_delta_backward", "kla_norm_rope", "kla_norm_rope_backward_workspace_size",
            "kla_norm_rope_backward")
 
@@ -98,7 +98,9 @@ def load_library(path: str = LIB_PATH):
     lib.kla_conv_backward.argtypes = [vp] * 10 + [i] * 7 + [vp, sz, vp]
     f, strides, nr = ctypes.c_float, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(NormRopeOptions)
     lib.kla_delta_forward.restype = i
-    lib.kla_delta_forward.argtypes = [vp] * 8 + [i] * 7 + [f, vp]
+    lib.kla_delta_forward.argtypes = [vp] * 8 + [i] * 7 + [f, vp, sz, vp]
+    lib.kla_delta_forward_workspace_size.restype = sz
+    lib.kla_delta_forward_workspace_size.argtypes = [i] * 6
     lib.kla_delta_step.restype = i
     lib.kla_delta_step.argtypes = [vp] * 7 + [i] * 6 + [f, vp]
     lib.kla_delta_backward_workspace_size.restype = sz
@@ -519,7 +521,7 @@ def _delta_shapes(q, k, v, g, beta, tokens=True):
 
 
 def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, o=None, stateT=None,
-                  final_state: bool = True, stream=None):
+                  final_state: bool = True, workspace=None, stream=None):
     """The gated delta rule over whole sequences (kla_delta_forward): with
     a = e^g, per token ``u = β (v − a Sᵀk)``, ``S ← a S + k uᵀ``, ``o = scale · Sᵀq``.
     q, k ``[B,Hk,T,dk]``, v ``[B,H,T,dv]`` (H a multiple of Hk), g, beta
@@ -537,9 +539,16 @@ def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, 
     if final_state and stateT is None:
         stateT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = LIB.kla_delta_forward_workspace_size(B, Hk, H, T, dk, dv)
+            if nbytes == ctypes.c_size_t(-1).value:
+                raise KlaError(ERR_INVALID_ARG, "kla_delta_forward_workspace_size")
+            workspace = torch.empty(int(nbytes), dtype=torch.uint8, device=dev) if nbytes else None
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = LIB.kla_delta_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state0), _ptr(o),
                                    _ptr(stateT), B, Hk, H, T, dk, dv, _IO[dt],
-                                   dk ** -0.5 if scale is None else scale, _stream(stream))
+                                   dk ** -0.5 if scale is None else scale, _ptr(workspace), ws_bytes,
+                                   _stream(stream))
     _check(st, "kla_delta_forward")
     return o, stateT
 

@@ -385,10 +385,16 @@ kla_status kla_conv_backward(const void* x, const float* weight, const float* bi
  *   o (required unless B·H·T = 0) must not overlap any input.
  *   stateT: the state after the last token, or NULL. It may be state0 itself
  *     (an in-place update) but must not overlap it otherwise. T = 0 copies
- *     the state. */
+ *     the state.
+ *   workspace / ws_bytes: device scratch of at least
+ *     kla_delta_forward_workspace_size() bytes (else WORKSPACE; may be NULL
+ *     when that is 0): longer sequences run in chunks of 64 tokens.
+ *   A value that is not finite reaches every output of its 64-token chunk that
+ *   it is coupled to (for v: its column), and what follows. */
+size_t kla_delta_forward_workspace_size(int B, int Hk, int H, int T, int dk, int dv);
 kla_status kla_delta_forward(const void* q, const void* k, const void* v, const void* g, const void* beta,
                              const float* state0, void* o, float* stateT, int B, int Hk, int H, int T, int dk,
-                             int dv, kla_dtype io, float scale, void* stream);
+                             int dv, kla_dtype io, float scale, void* workspace, size_t ws_bytes, void* stream);
 
 /* One decode token: q, k [B,Hk,dk]; v, o [B,H,dv]; g, beta [B,H]; the state
  * [B,H,dk,dv] is read and overwritten. */

@@ -19,8 +19,9 @@ def pointers(names, **kw):
     return [ctypes.c_void_p(kw[n]) if n in kw else ctypes.c_void_p(A + SPACE * i) for i, n in enumerate(names)]
 
 
-def forward(B=1, Hk=1, H=2, T=8, dk=16, dv=16, io=kla.F32, **kw):
-    return L.kla_delta_forward(*pointers(NAMES, **kw), B, Hk, H, T, dk, dv, io, 1.0, None)
+def forward(B=1, Hk=1, H=2, T=8, dk=16, dv=16, io=kla.F32, ws=A + 99 * SPACE, ws_bytes=1 << 30, **kw):
+    return L.kla_delta_forward(*pointers(NAMES, **kw), B, Hk, H, T, dk, dv, io, 1.0, ctypes.c_void_p(ws), ws_bytes,
+                               None)
 
 
 def backward(B=1, Hk=1, H=2, T=8, dk=16, dv=16, io=kla.F32, ws=A + 99 * SPACE, ws_bytes=1 << 30, **kw):
@@ -55,6 +56,14 @@ def test_delta_pointers(call, names, free):
         assert call(**{n: A + SPACE * names.index("k") + 16}) == kla.ERR_INVALID_ARG, n
     with_state = {"stateT": A + SPACE * NAMES.index("state0") + 16} if call is forward else {}
     assert not with_state or call(**with_state) == kla.ERR_INVALID_ARG  # a shifted in-place update
+
+
+def test_delta_forward_workspace():
+    need = L.kla_delta_forward_workspace_size(1, 1, 2, 500, 16, 16)
+    assert need > 0 and forward(T=500, ws=None, ws_bytes=0) == kla.ERR_WORKSPACE
+    assert forward(T=500, ws_bytes=need - 1) == kla.ERR_WORKSPACE
+    assert forward(T=500, ws=A + 16) == kla.ERR_INVALID_ARG  # on q
+    assert L.kla_delta_forward_workspace_size(1, 2, 3, 500, 16, 16) == ctypes.c_size_t(-1).value
 
 
 def test_delta_backward_workspace():
