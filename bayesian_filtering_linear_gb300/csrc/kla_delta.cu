@@ -17,10 +17,10 @@ namespace kla {
 
 namespace {
 
-constexpr int kTile = kDeltaCkpt;  // tokens staged at a time
+constexpr int kTile = 16;  // tokens staged at a time
 
-template <typename IO, int DK, bool CKPT>
-__global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArgs a, float* ckpt) {
+template <typename IO, int DK>
+__global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArgs a) {
   constexpr int RL = DK >= 64 ? 16 : DK / 4, G = DK / RL, NC = 128 / G, Q4 = RL / 4;
   __shared__ __align__(16) float ks[kTile][DK], qs[kTile][DK], vs[kTile][NC], os[kTile][NC];
   __shared__ float as[kTile], bs[kTile];
@@ -57,14 +57,6 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
   const int chunks = (T + kTile - 1) / kTile;
   for (int n = 0; n < chunks; ++n) {
     const int t0 = n * kTile, len = min(kTile, T - t0);
-    if (CKPT && mine) {
-#pragma unroll
-      for (int i = 0; i < 2 * Q4; ++i) {
-        float* p = ckpt + (((size_t)bh * chunks + n) * DK + ((i >> 1) * G + r) * 4 + 2 * (i & 1)) * a.dv + j;
-        p[0] = f2_lo(S[i]);
-        p[a.dv] = f2_hi(S[i]);
-      }
-    }
     for (int i = tid; i < len * DK; i += 128) {
       ks[i / DK][i % DK] = to_f32<IO>(k[(size_t)t0 * DK + i]);
       qs[i / DK][i % DK] = a.scale * to_f32<IO>(q[(size_t)t0 * DK + i]);
@@ -123,28 +115,27 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
 }
 
 template <typename IO, int DK>
-void launch_dk(const DeltaArgs& a, float* ckpt, cudaStream_t s) {
+void launch_dk(const DeltaArgs& a, cudaStream_t s) {
   constexpr int NC = 128 / (DK >= 64 ? DK / 16 : 4);
   const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.dv + NC - 1) / NC));
-  if (ckpt) kla_delta_recurrent_kernel<IO, DK, true><<<blocks, 128, 0, s>>>(a, ckpt);
-  else kla_delta_recurrent_kernel<IO, DK, false><<<blocks, 128, 0, s>>>(a, nullptr);
+  kla_delta_recurrent_kernel<IO, DK><<<blocks, 128, 0, s>>>(a);
 }
 
 template <typename IO>
-void launch_io(const DeltaArgs& a, float* ckpt, cudaStream_t s) {
+void launch_io(const DeltaArgs& a, cudaStream_t s) {
   switch (a.dk) {
-    case 16: launch_dk<IO, 16>(a, ckpt, s); break;
-    case 32: launch_dk<IO, 32>(a, ckpt, s); break;
-    case 64: launch_dk<IO, 64>(a, ckpt, s); break;
-    default: launch_dk<IO, 128>(a, ckpt, s); break;
+    case 16: launch_dk<IO, 16>(a, s); break;
+    case 32: launch_dk<IO, 32>(a, s); break;
+    case 64: launch_dk<IO, 64>(a, s); break;
+    default: launch_dk<IO, 128>(a, s); break;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_delta_recurrent(const DeltaArgs& a, float* ckpt, cudaStream_t s) {
-  if (a.io == IO_BF16) launch_io<__nv_bfloat16>(a, ckpt, s);
-  else launch_io<float>(a, ckpt, s);
+cudaError_t launch_delta_recurrent(const DeltaArgs& a, cudaStream_t s) {
+  if (a.io == IO_BF16) launch_io<__nv_bfloat16>(a, s);
+  else launch_io<float>(a, s);
   return cudaGetLastError();
 }
 

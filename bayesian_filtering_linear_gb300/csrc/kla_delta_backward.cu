@@ -1,11 +1,6 @@
-// Gradients of the gated delta rule (sm_103a), chunk by chunk from the end.
-//
-// With D_ts the decay from token s to token t of a chunk, G_t the decay from
-// its start and E_t the decay to its end, the chunk's states follow from the
-// state S before it by
-//   A = tril(β_t D_ts k_t·k_s, −1),  M = (I + A)^-1,  U = M β(V − G K S),
-//   P = tril(D_ts q_t·k_s),          O = scale (G Q S + P U),  S' = G_end S + Kᵀ(E U),
-// and with O' = scale dL/dO, Z = dL/dS' their gradients by
+// Gradients of the gated delta rule (sm_103a), in chunks of 64 tokens on the
+// tensor cores. With the notation of kla_delta_chunk.cu, P = tril(D_ts q_t·k_s),
+// O' = scale dL/dO and Z = dL/dS' for the state after the chunk:
 //   dU = Pᵀ O' + E K Z,  dR = Mᵀ dU,  dA = −tril(dR Uᵀ, −1),  dP = tril(O' Uᵀ)
 //   dV = β dR,  dS = G_end Z + Qᵀ(G O') − Kᵀ(β G dR)
 //   dQ = G O' Sᵀ + (dP D) K
@@ -19,226 +14,291 @@
 // behind a strong decay those cancel to nothing and leave their roundings,
 // while every product above carries the decay it is the gradient of.
 //
-// One block walks a head's chunks of 16 tokens; the states before them come
-// from a forward pass. Gradients of q and k that several value heads share
-// are summed from per-head fp32 parts in a fixed order.
-#include "kla_device.cuh"
-#include "kla_launch.h"
+// Four steps: `prepare` makes M and, ahead of the chain, Pᵀ O' and Qᵀ(G O');
+// the chain runs forward for S and U, and from the end for Z and dR; then a
+// block per chunk and head makes everything else here. Gradients of q and k
+// that several value heads share are summed from per-head fp32 parts in a
+// fixed order.
+#include "kla_delta_chunk.cuh"
 
 namespace kla {
+namespace delta {
 
 namespace {
 
-constexpr int C = kDeltaCkpt, kThreads = 256;
+template <typename IO, int DK>
+struct GradSmem {
+  static constexpr int PN = sizeof(IO) == 2 ? 2 : 3;  // parts of what is not an input
+  static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, ROWS = PN * kTileBytes;
+  static constexpr int K = 0, Q = IN, O = 2 * IN, U = O + kParts<IO> * kTileBytes, R = U + ROWS, S = R + ROWS,
+                       kStage = S + PN * DK * 128;
+  // once the products with S and Z are done: (dP P + dA A), then the masked dP, dA and β dA
+  static constexpr int W = O, dP = O, dA = dP + ROWS, bA = dA + ROWS, kEnd = bA + ROWS;
+  static constexpr int kBytes = (kStage > kEnd ? kStage : kEnd) + 1024;
+  static_assert(W + 64 * 65 * 4 <= kBytes - 1024, "");
+};
 
-// out[m][n] = Σ_k a(m,k) b(k,n) by all threads, one element each at a time
-template <typename FA, typename FB, typename FO>
-__device__ __forceinline__ void matmul(int M, int N, int K, FA a, FB b, FO out) {
-  for (int i = threadIdx.x; i < M * N; i += kThreads) {
-    const int m = i / N, n = i % N;
-    float s = 0.f;
-    for (int k = 0; k < K; ++k) s = fmaf(a(m, k), b(k, n), s);
-    out(m, n, s);
-  }
+// Per row of a fragment: the sum over its four lanes; lane 0 of the four keeps it.
+__device__ __forceinline__ float row4(float x) {
+  x += __shfl_xor_sync(~0u, x, 1);
+  return x + __shfl_xor_sync(~0u, x, 2);
 }
 
-template <typename IO>
-__global__ void __launch_bounds__(kThreads) kla_delta_backward_kernel(const DeltaArgs a, const DeltaGradArgs d,
-                                                                     const float* ckpt, float* part) {
-  extern __shared__ __align__(16) float sm[];
-  const int dk = a.dk, dv = a.dv, T = a.T, tid = threadIdx.x;
-  const long long bh = blockIdx.x;
-  const int h = (int)(bh % a.H);
-  const long long key = (bh / a.H) * a.Hk + h / (a.H / a.Hk);
-  const int chunks = (T + C - 1) / C;
-  float* S = sm;                // [dk][dv]
-  float* Z = S + dk * dv;       // [dk][dv]
-  float* K = Z + dk * dv;       // [C][dk]
-  float* Q = K + C * dk;
-  float* V = Q + C * dk;        // [C][dv]
-  float* O = V + C * dv;
-  float* U = O + C * dv;
-  float* R = U + C * dv;
-  float* X = R + C * dv;        // [C][dk]
-  float* Y = X + C * dk;
-  float* M = Y + C * dk;        // [C][C]
-  float* P = M + C * C;
-  float* A = P + C * C;
-  float* dP = A + C * C;
-  float* D = dP + C * C;
-  float* W = D + C * C;         // (dP P + dA A), then its sums along s
-  __shared__ float gc[C], be[C], red[kThreads / 32], line[C];
-  __shared__ double cum[C];
-  const size_t sz = (size_t)dk * dv;
-  for (int i = tid; i < dk * dv; i += kThreads) Z[i] = d.gstateT ? d.gstateT[bh * sz + i] : 0.f;
-  for (int n = chunks - 1; n >= 0; --n) {
-    const int t0 = n * C, len = min(C, T - t0);
-    for (int i = tid; i < dk * dv; i += kThreads) S[i] = ckpt[((size_t)bh * chunks + n) * sz + i];
-    for (int i = tid; i < C * dk; i += kThreads) {
-      const bool in = i < len * dk;
-      const size_t at = ((size_t)key * T + t0) * dk + i;
-      K[i] = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.k)[at]) : 0.f;
-      Q[i] = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.q)[at]) : 0.f;
-    }
-    for (int i = tid; i < C * dv; i += kThreads) {
-      const bool in = i < len * dv;
-      const size_t at = ((size_t)bh * T + t0) * dv + i;
-      V[i] = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.v)[at]) : 0.f;
-      O[i] = in && d.go ? a.scale * to_f32<IO>(reinterpret_cast<const IO*>(d.go)[at]) : 0.f;
-    }
-    if (tid < C) {
-      const bool in = tid < len;
-      const float x = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.g)[(size_t)bh * T + t0 + tid]) : 0.f;
-      gc[tid] = x < -104.f ? -104.f : x;  // e^-104 is 0 in fp32, and sums stay finite
-      be[tid] = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.beta)[(size_t)bh * T + t0 + tid]) : 0.f;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      double x = 0;
-      for (int t = 0; t < C; ++t) cum[t] = x += gc[t];
-    }
-    __syncthreads();
-    if (tid < C * C) D[tid] = tid % C <= tid / C ? expf((float)(cum[tid / C] - cum[tid % C])) : 0.f;
-    __syncthreads();
-    matmul(C, C, dk, [&](int t, int i) { return K[t * dk + i]; }, [&](int i, int s) { return K[s * dk + i]; },
-           [&](int t, int s, float x) { A[t * C + s] = s < t ? be[t] * D[t * C + s] * x : 0.f; });
-    matmul(C, C, dk, [&](int t, int i) { return Q[t * dk + i]; }, [&](int i, int s) { return K[s * dk + i]; },
-           [&](int t, int s, float x) { P[t * C + s] = D[t * C + s] * x; });
-    matmul(C, dv, dk, [&](int t, int i) { return K[t * dk + i]; }, [&](int i, int j) { return S[i * dv + j]; },
-           [&](int t, int j, float x) { R[t * dv + j] = be[t] * (V[t * dv + j] - expf((float)cum[t]) * x); });
-    __syncthreads();
-    if (tid < C) {  // column tid of M by forward substitution
-      for (int t = 0; t < C; ++t) {
-        float x = t == tid ? 1.f : 0.f;
-        for (int s = tid; s < t; ++s) x = fmaf(-A[t * C + s], M[s * C + tid], x);
-        M[t * C + tid] = x;
-      }
-    }
-    __syncthreads();
-    auto G = [&](int t) { return expf((float)cum[t]); };
-    auto E = [&](int t) { return expf((float)(cum[C - 1] - cum[t])); };
-    matmul(C, dv, C, [&](int t, int s) { return M[t * C + s]; }, [&](int s, int j) { return R[s * dv + j]; },
-           [&](int t, int j, float x) { U[t * dv + j] = x; });
-    __syncthreads();
-    matmul(C, dv, C + dk, [&](int s, int i) { return i < C ? P[i * C + s] : E(s) * K[s * dk + i - C]; },
-           [&](int i, int j) { return i < C ? O[i * dv + j] : Z[(i - C) * dv + j]; },
-           [&](int s, int j, float x) { R[s * dv + j] = x; });
-    __syncthreads();
-    // dR = Mᵀ dU, column by column in registers
-    for (int j = tid; j < dv; j += kThreads) {
-      float x[C];
-      for (int s = 0; s < C; ++s) {
-        x[s] = 0.f;
-        for (int t = s; t < C; ++t) x[s] = fmaf(M[t * C + s], R[t * dv + j], x[s]);
-      }
-      for (int s = 0; s < C; ++s) R[s * dv + j] = x[s];
-    }
-    __syncthreads();
-    matmul(C, C, dv, [&](int t, int j) { return R[t * dv + j]; }, [&](int j, int s) { return U[s * dv + j]; },
-           [&](int t, int s, float x) {
-             W[t * C + s] = s < t ? -x * A[t * C + s] : 0.f;
-             A[t * C + s] = s < t ? -D[t * C + s] * x : 0.f;
-           });
-    __syncthreads();
-    matmul(C, C, dv, [&](int t, int j) { return O[t * dv + j]; }, [&](int j, int s) { return U[s * dv + j]; },
-           [&](int t, int s, float x) {
-             if (s < t) W[t * C + s] = fmaf(x, P[t * C + s], W[t * C + s]);
-             dP[t * C + s] = D[t * C + s] * x;
-           });
-    float zs = 0.f;
-    for (int i = tid; i < dk * dv; i += kThreads) zs = fmaf(Z[i], S[i], zs);
-    zs *= G(C - 1);
-    __syncthreads();
-    float* uz = M;  // [C]: (E U Zᵀ)_t · k_t
-    matmul(C, dk, dv, [&](int t, int j) { return U[t * dv + j]; }, [&](int j, int i) { return Z[i * dv + j]; },
-           [&](int t, int i, float x) { Y[t * dk + i] = E(t) * x; });
-    __syncthreads();
-    if (tid < C) {
-      float x = 0.f;
-      for (int i = 0; i < dk; ++i) x = fmaf(Y[tid * dk + i], K[tid * dk + i], x);
-      uz[tid] = x;
-    }
-    __syncthreads();
-    matmul(C, dk, dv, [&](int t, int j) { return R[t * dv + j]; }, [&](int j, int i) { return S[i * dv + j]; },
-           [&](int t, int i, float x) { X[t * dk + i] = -G(t) * x; });
-    __syncthreads();
-    if (tid < C) {
-      float x = 0.f;
-      for (int i = 0; i < dk; ++i) x = fmaf(X[tid * dk + i], K[tid * dk + i], x);
-      line[tid] = be[tid] * x;
-      float sum = 0.f;  // W's row tid: W[tid][t] becomes the sum over s < t
-      for (int t = 0; t < C; ++t) {
-        const float w = W[tid * C + t];
-        W[tid * C + t] = sum;
-        sum += w;
-      }
-    }
-    __syncthreads();
-    matmul(C, dk, C, [&](int t, int s) { return A[t * C + s]; }, [&](int s, int i) { return K[s * dk + i]; },
-           [&](int t, int i, float x) { X[t * dk + i] += x; });
-    matmul(C, dk, 2 * C, [&](int s, int t) { return t < C ? dP[t * C + s] : be[t - C] * A[(t - C) * C + s]; },
-           [&](int t, int i) { return t < C ? Q[t * dk + i] : K[(t - C) * dk + i]; },
-           [&](int s, int i, float x) { Y[s * dk + i] += x; });
-    for (int m = 16; m; m >>= 1) zs += __shfl_xor_sync(~0u, zs, m);
-    if ((tid & 31) == 0) red[tid >> 5] = zs;
-    __syncthreads();
-    const bool shared_keys = a.Hk != a.H;
-    const int w = tid >> 5, l = tid & 31;
-    for (int t = w; t < C; t += kThreads / 32) {
-      float acc = 0.f, kx = 0.f;
-      for (int i = l; i < dk; i += 32) {
-        float dq = 0.f;
-        for (int j = 0; j < dv; ++j) dq = fmaf(O[t * dv + j], S[i * dv + j], dq);
-        dq *= G(t);
-        acc = fmaf(Q[t * dk + i], dq, acc);
-        for (int s = 0; s <= t; ++s) dq = fmaf(dP[t * C + s], K[s * dk + i], dq);
-        const float x = X[t * dk + i], y = Y[t * dk + i];
-        kx = fmaf(K[t * dk + i], x, kx);
-        if (t < len) {
-          const float gk = fmaf(be[t], x, y);
-          if (shared_keys) {
-            float* p = part + ((size_t)bh * T + t0 + t) * 2 * dk;
-            p[i] = dq;
-            p[dk + i] = gk;
-          } else {
-            const size_t at = ((size_t)key * T + t0 + t) * dk + i;
-            reinterpret_cast<IO*>(d.gq)[at] = from_f32<IO>(dq);
-            reinterpret_cast<IO*>(d.gk)[at] = from_f32<IO>(gk);
-          }
-        }
-      }
-      float rv = 0.f;
-      for (int j = l; j < dv; j += 32) {
-        rv = fmaf(R[t * dv + j], V[t * dv + j], rv);
-        if (t < len) reinterpret_cast<IO*>(d.gv)[((size_t)bh * T + t0 + t) * dv + j] = from_f32<IO>(be[t] * R[t * dv + j]);
-      }
-      for (int m = 16; m; m >>= 1) {
-        acc += __shfl_xor_sync(~0u, acc, m);
-        kx += __shfl_xor_sync(~0u, kx, m);
-        rv += __shfl_xor_sync(~0u, rv, m);
-      }
-      if (l == 0) {
-        line[t] += acc;
-        if (t < len) reinterpret_cast<IO*>(d.gbeta)[(size_t)bh * T + t0 + t] = from_f32<IO>(rv + kx);
-      }
-    }
-    __syncthreads();
-    if (tid < len) {
-      float y = 0.f;
-      for (int i = 0; i < kThreads / 32; ++i) y += red[i];
-      for (int s = C - 1; s >= tid; --s) y += line[s] + W[s * C + tid];
-      for (int s = 0; s < tid; ++s) y += uz[s];
-      reinterpret_cast<IO*>(d.gg)[(size_t)bh * T + t0 + tid] = from_f32<IO>(y);
-    }
-    __syncthreads();
-    const float ge = G(C - 1);
-    matmul(dk, dv, 2 * C, [&](int i, int t) { return t < C ? G(t) * Q[t * dk + i] : -be[t - C] * G(t - C) * K[(t - C) * dk + i]; },
-           [&](int t, int j) { return t < C ? O[t * dv + j] : R[(t - C) * dv + j]; },
-           [&](int i, int j, float x) { Z[i * dv + j] = fmaf(ge, Z[i * dv + j], x); });
-    __syncthreads();
+template <typename IO, int DK>
+__global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs d,
+                                                                 const Workspace w) {
+  using L = GradSmem<IO, DK>;
+  constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
+  constexpr int COLS = DK == 64 ? 256 : 512, SH = 3 * DK;      // TMEM: dQ, X, Y of DK columns, then 64 shared
+  extern __shared__ char raw[];
+  char* sm = align1024(raw);
+  __shared__ float hi[C], lo[C], G[C], E[C], be[C], rv[C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int DV = pad64(a.dv), slices = DV / 64;
+  const Where at = where(a, blockIdx.x);
+  const size_t krow = (size_t)at.key * a.T + at.t0, vrow = (size_t)at.bh * a.T + at.t0;
+  const IO* k = reinterpret_cast<const IO*>(a.k) + krow * a.dk;
+  const IO* q = reinterpret_cast<const IO*>(a.q) + krow * a.dk;
+  const IO* v_in = reinterpret_cast<const IO*>(a.v) + vrow * a.dv;
+  const IO* go = d.go ? reinterpret_cast<const IO*>(d.go) + vrow * a.dv : nullptr;
+  const float* Sw = w.S + at.chunk * DK * DV;
+  const float* Zw = w.Z + at.chunk * DK * DV;
+  const float* Uw = w.U + at.chunk * C * DV;
+  const float* Rw = w.R + at.chunk * C * DV;
+  if (warp == 0) tmem_alloc(&slot, COLS);
+  if (tid == 32) mbar_init(&bar, 1);
+  if (tid < C) {
+    const float* g = w.gates + at.chunk * kGates + tid;
+    hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C], E[tid] = g[3 * C], be[tid] = g[4 * C];
+    rv[tid] = 0.f;
   }
-  if (d.gstate0)
-    for (int i = tid; i < dk * dv; i += kThreads) d.gstate0[bh * sz + i] = Z[i];
+  load_tile<IO, DK>(sm + L::K, k, at.len, a.dk, 0, tid, kThreads);
+  load_tile<IO, DK>(sm + L::Q, q, at.len, a.dk, 0, tid, kThreads);
+  fence_async();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = slot, base = smem_addr(sm);
+  const Operand<PARTS, false> Kr{base + L::K, NB * kTileBytes, kTileBytes}, Qr{base + L::Q, NB * kTileBytes, kTileBytes};
+  const Operand<PARTS, true> Kt{base + L::K, NB * kTileBytes, kTileBytes}, Qt{base + L::Q, NB * kTileBytes, kTileBytes};
+  const Operand<PARTS, false> Or{base + L::O, kTileBytes, kTileBytes};
+  const Operand<PN, false> Ur{base + L::U, kTileBytes, kTileBytes}, Rr{base + L::R, kTileBytes, kTileBytes};
+  const Operand<PN, false> Sr{base + L::S, DK * 128, DK * 128};
+  bool ok = true;
+  uint32_t phase = 0;
+  auto finish = [&] {  // the products issued so far
+    mbar_wait(&bar, phase, ok);
+    phase ^= 1;
+    fence_after();
+  };
+  auto publish = [&] {  // this block's shared-memory writes and TMEM reads, before the next products
+    fence_async();
+    fence_before();
+    __syncthreads();
+    fence_after();
+  };
+  const int quad = warp & 3, half = warp >> 2, r0 = 16 * quad + (lane >> 2), c0 = 32 * half + 2 * (lane & 3);
+  const uint32_t rows = (uint32_t)(32 * quad) << 16;
+  // entries (t, s), (t, s + 1) of a 64 × 64 fragment at index e of 16
+  auto row_of = [&](int e) { return r0 + (e & 2) * 4; };
+  auto col_of = [&](int e) { return c0 + (e >> 2) * 8; };
+
+  if (tid == 0) {  // A and P before their decays, where dQ and X come later
+    mma<64, 64, DK>(tm, Kr, Kr);
+    mma<64, 64, DK>(tm + 64, Qr, Kr);
+    commit(&bar);
+  }
+  float kk[16], qk[16], v[16];
+  finish();
+  tmem_load(tm + rows + 32 * half, kk);
+  tmem_load(tm + 64 + rows + 32 * half, qk);
+  // products with U, S: dP, dA before masks, dQ = O' Sᵀ, X = dR Sᵀ (dP and dA wait in the shared columns and in Y's)
+  for (int sl = 0; sl < slices; ++sl) {
+    if (sl) finish();
+    if (go) load_tile<IO, 64>(sm + L::O, go, at.len, a.dv, sl * 64, tid, kThreads);
+    else load_tile<IO, 64>(sm + L::O, v_in, 0, a.dv, sl * 64, tid, kThreads);
+    load_parts<PN, C>(sm + L::U, Uw + sl * 64, DV, tid, kThreads);
+    load_parts<PN, DK>(sm + L::S, Sw + sl * 64, DV, tid, kThreads);
+    for (int i = tid; i < C * 8; i += kThreads) {  // dR, and what comes of it alone
+      const int r = i >> 3, c = (i & 7) * 8, j = sl * 64 + c;
+      const float4 x0 = *reinterpret_cast<const float4*>(Rw + r * DV + j), x1 = *reinterpret_cast<const float4*>(Rw + r * DV + j + 4);
+      float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, y[8] = {}, dot = 0.f;
+      if (r < at.len && j < a.dv) {
+        load_eight<IO>(v_in + (size_t)r * a.dv + j, y);
+        IO* gv = reinterpret_cast<IO*>(d.gv) + (vrow + r) * a.dv + j;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) store_two(gv + e, be[r] * x[e], be[r] * x[e + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot = fmaf(x[e], y[e], dot);
+      dot = row4(dot);
+      dot += __shfl_xor_sync(~0u, dot, 4);
+      if ((lane & 7) == 0) rv[r] += dot;
+      store_eight<PN>(sm + L::R, kTileBytes, r, c, x);
+    }
+    publish();
+    if (tid == 0) {
+      mma<64, 64, 64>(tm + SH, Or, Ur, sl > 0);
+      mma<64, 64, 64>(tm + 2 * DK, Rr, Ur, sl > 0);
+      mma<64, DK, 64>(tm, Or, Sr, sl > 0);
+      mma<64, DK, 64>(tm + DK, Rr, Sr, sl > 0);
+      commit(&bar);
+    }
+  }
+  float gp[16], ga[16];
+  finish();
+  tmem_load(tm + SH + rows + 32 * half, gp);
+  tmem_load(tm + 2 * DK + rows + 32 * half, ga);
+  fence_before();
+  // Y = U Zᵀ, and <Z, S>
+  float z = 0.f;
+  for (int sl = 0; sl < slices; ++sl) {
+    if (sl) finish();
+    if (slices > 1) load_parts<PN, C>(sm + L::U, Uw + sl * 64, DV, tid, kThreads);
+    load_parts<PN, DK>(sm + L::S, Zw + sl * 64, DV, tid, kThreads);
+    for (int i = tid; i < DK * 16; i += kThreads) {
+      const size_t e = (size_t)(i >> 4) * DV + sl * 64 + (i & 15) * 4;
+      const float4 x = *reinterpret_cast<const float4*>(Sw + e), y = *reinterpret_cast<const float4*>(Zw + e);
+      z += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+    }
+    publish();
+    if (tid == 0) {
+      mma<64, DK, 64>(tm + 2 * DK, Ur, Sr, sl > 0);
+      commit(&bar);
+    }
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) z += __shfl_xor_sync(~0u, z, m);
+  if (lane == 0) zs[warp] = z;
+  // masks and decays while that runs; (dP P + dA A) goes through registers until the tiles are free
+  float ww[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int t = row_of(e), s = col_of(e) + (e & 1);
+    const float D = s <= t ? decay(hi, lo, t, s) : 0.f, strict = s < t ? D : 0.f;
+    const float p = s <= t ? a.scale * D * gp[e] : 0.f, x = s < t ? -strict * ga[e] : 0.f;
+    ww[e] = s < t ? fmaf(p, qk[e], be[t] * x * kk[e]) : 0.f;
+    gp[e] = p, ga[e] = x;
+  }
+  finish();
+  // dQ, X, Y so far into registers, with their decays and their products with q and k
+  float acc[3][NB][16], aq[2] = {}, ax[2] = {}, ay[2] = {};
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int cb = NB * 32 * half + 32 * nb;
+#pragma unroll
+    for (int m = 0; m < 3; ++m) tmem_load(tm + m * DK + rows + cb, acc[m][nb]);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const int t = row_of(e), o = (e & 2) >> 1, c = cb + 2 * (lane & 3) + (e >> 2) * 8;
+      float2 kv = make_float2(0.f, 0.f), qv = kv;
+      if (t < at.len && c < a.dk) kv = load_two(k + (size_t)t * a.dk + c), qv = load_two(q + (size_t)t * a.dk + c);
+      const float f[3] = {a.scale * G[t], -G[t], E[t]};
+#pragma unroll
+      for (int m = 0; m < 3; ++m) acc[m][nb][e] *= f[m], acc[m][nb][e + 1] *= f[m];
+      aq[o] += acc[0][nb][e] * qv.x + acc[0][nb][e + 1] * qv.y;
+      ax[o] += acc[1][nb][e] * kv.x + acc[1][nb][e + 1] * kv.y;
+      ay[o] += acc[2][nb][e] * kv.x + acc[2][nb][e + 1] * kv.y;
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int t = r0 + 8 * o;
+    const float f = row4(fmaf(be[t], ax[o], aq[o])), x = row4(ay[o]);
+    if ((lane & 3) == 0) from[half][t] = f, to[half][t] = x;
+  }
+  float* W = reinterpret_cast<float*>(sm + L::W);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) W[row_of(e) * 65 + col_of(e) + (e & 1)] = ww[e];
+  fence_before();
+  __syncthreads();
+  {  // W[t][s] becomes the sum of its row before s, four lanes a row; then before[s] the sum of column s from row s on
+    const int r = tid >> 2, s0 = (tid & 3) * 16;
+    float sum = 0.f;
+    for (int s = s0; s < s0 + 16; ++s) sum += W[r * 65 + s];
+    float x = __shfl_up_sync(~0u, sum, 1), y = __shfl_up_sync(~0u, sum, 2), u = __shfl_up_sync(~0u, sum, 3);
+    const int seg = tid & 3;
+    float run = (seg > 0 ? x : 0.f) + (seg > 1 ? y : 0.f) + (seg > 2 ? u : 0.f);
+    for (int s = s0; s < s0 + 16; ++s) {
+      const float e = W[r * 65 + s];
+      W[r * 65 + s] = run;
+      run += e;
+    }
+    __syncthreads();
+    sum = 0.f;
+    for (int t = s0; t < s0 + 16; ++t)
+      if (t >= r) sum += W[t * 65 + r];
+    sum = row4(sum);
+    if (seg == 0) before[r] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const int t = row_of(e), s = col_of(e);
+    store_pair<PN>(sm + L::dP, kTileBytes, t, s, gp[e], gp[e + 1]);
+    store_pair<PN>(sm + L::dA, kTileBytes, t, s, ga[e], ga[e + 1]);
+    store_pair<PN>(sm + L::bA, kTileBytes, t, s, be[t] * ga[e], be[t] * ga[e + 1]);
+  }
+  publish();
+  if (tid == 0) {
+    const Operand<PN, false> P{base + L::dP, kTileBytes, kTileBytes}, A{base + L::dA, kTileBytes, kTileBytes};
+    const Operand<PN, true> Pt{base + L::dP, kTileBytes, kTileBytes}, At{base + L::bA, kTileBytes, kTileBytes};
+    mma<64, DK, 64>(tm, P, Kt);
+    mma<64, DK, 64>(tm + DK, A, Kt);
+    mma<64, DK, 64>(tm + 2 * DK, Pt, Qt);
+    mma<64, DK, 64>(tm + 2 * DK, At, Kt, true);
+    commit(&bar);
+  }
+  if (tid < at.len) {  // the decay's gradient needs nothing more
+    float x = 0.f;
+    for (int i = 0; i < 8; ++i) x += zs[i];
+    x = fmaf(G[C - 1], x, before[tid]);
+    for (int s = C - 1; s >= tid; --s) x += from[0][s] + from[1][s];
+    for (int s = 0; s < tid; ++s) x += to[0][s] + to[1][s];
+    reinterpret_cast<IO*>(d.gg)[vrow + tid] = from_f32<IO>(x);
+  }
+  finish();
+  const float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
+  ax[0] = ax[1] = 0.f;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int cb = NB * 32 * half + 32 * nb;
+#pragma unroll
+    for (int m = 0; m < 3; ++m) {
+      tmem_load(tm + m * DK + rows + cb, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[m][nb][e] += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const int t = row_of(e), o = (e & 2) >> 1, c = cb + 2 * (lane & 3) + (e >> 2) * 8;
+      if (t >= at.len || c >= a.dk) continue;
+      const float2 kv = load_two(k + (size_t)t * a.dk + c);
+      const float x = acc[1][nb][e], y = acc[1][nb][e + 1];
+      ax[o] += x * kv.x + y * kv.y;
+      const float dq[2] = {acc[0][nb][e] + bad, acc[0][nb][e + 1] + bad};
+      const float dk[2] = {fmaf(be[t], x, acc[2][nb][e]) + bad, fmaf(be[t], y, acc[2][nb][e + 1]) + bad};
+      if (w.part) {
+        float* p = w.part + (vrow + t) * 2 * a.dk + c;
+        store_two(p, dq[0], dq[1]);
+        store_two(p + a.dk, dk[0], dk[1]);
+      } else {
+        store_two(reinterpret_cast<IO*>(d.gq) + (krow + t) * a.dk + c, dq[0], dq[1]);
+        store_two(reinterpret_cast<IO*>(d.gk) + (krow + t) * a.dk + c, dk[0], dk[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const float x = row4(ax[o]);
+    if ((lane & 3) == 0) kx[half][r0 + 8 * o] = x;
+  }
+  fence_before();
+  __syncthreads();
+  if (tid < at.len) reinterpret_cast<IO*>(d.gbeta)[vrow + tid] = from_f32<IO>(rv[tid] + kx[0][tid] + kx[1][tid] + bad);
+  if (warp == 0) tmem_free(tm, COLS);
 }
 
 // gq, gk of a key head: the sum over its value heads, in order.
@@ -257,39 +317,42 @@ __global__ void __launch_bounds__(256) kla_delta_share_kernel(const DeltaArgs a,
   }
 }
 
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+template <typename IO, int DK>
+cudaError_t grad_dk(const DeltaArgs& a, const DeltaGradArgs& g, const Workspace& w, cudaStream_t s) {
+  const int smem = GradSmem<IO, DK>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(kla_delta_grad_kernel<IO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.T + C - 1) / C));
+  kla_delta_grad_kernel<IO, DK><<<blocks, kThreads, smem, s>>>(a, g, w);
+  return cudaGetLastError();
+}
 
 }  // namespace
+}  // namespace delta
 
 size_t delta_backward_bytes(int B, int Hk, int H, int T, int dk, int dv) {
-  const size_t bh = (size_t)B * H, chunks = ((size_t)T + C - 1) / C;
-  return align256(bh * chunks * dk * dv * sizeof(float)) + (Hk != H ? bh * T * 2 * dk * sizeof(float) : 0);
+  size_t n = 0;
+  delta::workspace(nullptr, B, Hk, H, T, dk, dv, true, &n);
+  return n;
 }
 
 cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, void* workspace, cudaStream_t s) {
-  float* ckpt = reinterpret_cast<float*>(workspace);
-  const size_t chunks = ((size_t)a.T + C - 1) / C;
-  float* part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
-                                         align256((size_t)a.B * a.H * chunks * a.dk * a.dv * sizeof(float)));
-  DeltaArgs f = a;
-  f.o = nullptr;
-  f.stateT = nullptr;
-  cudaError_t e = launch_delta_recurrent(f, ckpt, s);
+  size_t n = 0;
+  const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, true, &n);
+  cudaError_t e = delta::launch_prepare(a, &g, w, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, false, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, true, s);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)(2 * a.dk * a.dv + C * (4 * a.dk + 4 * a.dv) + 6 * C * C) * sizeof(float);
-  auto run = [&](auto kernel) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return;
-    kernel<<<(unsigned)((long long)a.B * a.H), kThreads, smem, s>>>(a, g, ckpt, part);
-    e = cudaGetLastError();
-  };
-  if (a.io == IO_BF16) run(kla_delta_backward_kernel<__nv_bfloat16>);
-  else run(kla_delta_backward_kernel<float>);
+  const bool wide = delta::pad64(a.dk) == 128;
+  if (a.io == IO_BF16)
+    e = wide ? delta::grad_dk<__nv_bfloat16, 128>(a, g, w, s) : delta::grad_dk<__nv_bfloat16, 64>(a, g, w, s);
+  else
+    e = wide ? delta::grad_dk<float, 128>(a, g, w, s) : delta::grad_dk<float, 64>(a, g, w, s);
   if (e != cudaSuccess || a.Hk == a.H) return e;
   const long long blocks = ((long long)a.B * a.Hk * a.T * 2 * a.dk + 255) / 256;
   const unsigned grid = (unsigned)(blocks < (1LL << 30) ? blocks : 1LL << 30);
-  if (a.io == IO_BF16) kla_delta_share_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, g, part);
-  else kla_delta_share_kernel<float><<<grid, 256, 0, s>>>(a, g, part);
+  if (a.io == IO_BF16) delta::kla_delta_share_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, g, w.part);
+  else delta::kla_delta_share_kernel<float><<<grid, 256, 0, s>>>(a, g, w.part);
   return cudaGetLastError();
 }
 

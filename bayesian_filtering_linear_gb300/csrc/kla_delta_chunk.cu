@@ -588,7 +588,7 @@ size_t delta_forward_bytes(int B, int Hk, int H, int T, int dk, int dv) {
 }
 
 cudaError_t launch_delta_forward(const DeltaArgs& a, void* workspace, cudaStream_t s) {
-  if (!delta_chunked(a.T)) return launch_delta_recurrent(a, nullptr, s);
+  if (!delta_chunked(a.T)) return launch_delta_recurrent(a, s);
   size_t n = 0;
   const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, false, &n);
   cudaError_t e = delta::launch_prepare(a, nullptr, w, s);

@@ -148,10 +148,8 @@ struct DeltaGradArgs {
   float* gstate0;         // dL/dS_0, or null
 };
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t s);
-// Token by token with the state in registers. `ckpt`: also store the state
-// before every kDeltaCkpt-th token, [B·H][ceil(T / kDeltaCkpt)][dk][dv] fp32.
-constexpr int kDeltaCkpt = 16;
-cudaError_t launch_delta_recurrent(const DeltaArgs& a, float* ckpt, cudaStream_t s);
+// Token by token with the state in registers.
+cudaError_t launch_delta_recurrent(const DeltaArgs& a, cudaStream_t s);
 // Whole sequences: token by token, or in chunks with `workspace`.
 size_t delta_forward_bytes(int B, int Hk, int H, int T, int dk, int dv);
 cudaError_t launch_delta_forward(const DeltaArgs& a, void* workspace, cudaStream_t s);
