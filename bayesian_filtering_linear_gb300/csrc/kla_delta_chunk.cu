@@ -43,8 +43,8 @@ __device__ __forceinline__ void small_matmul(float* dst, const float* a, const f
 }
 
 // M = (I + A)^-1 for A strictly lower, 64 × 64 with row length 68: substitution in the 16 × 16 blocks on the diagonal,
-// then [[X, 0], [L, Y]]^-1 = [[X', 0], [−Y' L X', Y']] for 32 and 64. W: scratch of 64 × 68.
-__device__ void invert(const float* A, float* M, float* W, int tid) {
+// then [[X, 0], [L, Y]]^-1 = [[X', 0], [−Y' L X', Y']] for 32 and 64. L X' goes where A's upper blocks would be.
+__device__ void invert(float* A, float* M, int tid) {
   if (tid < 64) {
     const int b = tid & 48, c = tid & 15;
     float x[16];
@@ -64,9 +64,9 @@ __device__ void invert(const float* A, float* M, float* W, int tid) {
   for (int n = 16; n <= 32; n *= 2) {
     const int tasks = n * n / 4, p = tid / tasks, o = p * 2 * n * 68 + p * 2 * n;  // pair p of blocks
     const bool mine = p < 32 / n;
-    if (mine) small_matmul(W + o, A + o + n * 68, M + o, n, false, tid % tasks);
+    if (mine) small_matmul(A + o + n, A + o + n * 68, M + o, n, false, tid % tasks);
     __syncthreads();
-    if (mine) small_matmul(M + o + n * 68, M + o + n * 68 + n, W + o, n, true, tid % tasks);
+    if (mine) small_matmul(M + o + n * 68, M + o + n * 68 + n, A + o + n, n, true, tid % tasks);
     __syncthreads();
   }
 }
@@ -75,8 +75,9 @@ template <typename IO, int DK, bool BWD>
 struct PrepareSmem {
   static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes;
   static constexpr int K = 0, Q = IN, P = Q + (BWD ? IN : 0), O = P + (BWD ? 3 * kTileBytes : 0),
-                       GO = O + (BWD ? PARTS * kTileBytes : 0), A = GO + (BWD ? 3 * kTileBytes : 0),
-                       W = A + 64 * 68 * 4, M = W + 64 * 68 * 4, kBytes = M + 64 * 68 * 4 + 1024;
+                       GO = O + PARTS * kTileBytes, A = O, M = A + 64 * 68 * 4;  // A and M are done with before O and GO
+  static constexpr int kEnd = BWD && GO + 3 * kTileBytes > M + 64 * 68 * 4 ? GO + 3 * kTileBytes : M + 64 * 68 * 4;
+  static constexpr int kBytes = kEnd + 1024;
 };
 
 template <typename IO, int DK, bool BWD>
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
     }
   }
   __syncthreads();
-  invert(A, M, reinterpret_cast<float*>(sm + L::W), tid);
+  invert(A, M, tid);
   float* out = w.M + at.chunk * C * C;
   for (int i = tid; i < C * C / 4; i += kThreads) {
     float4 x = *reinterpret_cast<const float4*>(M + (i >> 4) * 68 + (i & 15) * 4);
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
   }
   if (BWD) {
     const int DV = pad64(a.dv);
+    __syncthreads();
     for (int sl = 0; sl < DV / 64; ++sl) {
       const IO* go = reinterpret_cast<const IO*>(d.go);
       const IO* src = go ? go + ((size_t)at.bh * a.T + at.t0) * a.dv : nullptr;
@@ -302,8 +304,32 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
         if (first && r < a.dk && c < a.dv) x = load_two(first + ((size_t)bh * a.dk + r) * a.dv + c);
         X[rb][i] = x.x, X[rb][i + 1] = x.y;
       }
+    // this chunk's rows of V (rev: Pᵀ O') and gates, loaded a chunk ahead
+    float ga[2], gb[2], gend = 0.f, B[16];
+    float2 raw_b[8];
+    float raw_g[2][3];
+    auto fetch = [&](int i) {
+      const int n = REV ? N - 1 - i : i, len = min(C, a.T - n * C);
+      const size_t chunk = (size_t)bh * N + n;
+      const float* gates = w.gates + chunk * kGates;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = r0 + 8 * e;
+#pragma unroll
+        for (int m = 0; m < 3; ++m) raw_g[e][m] = gates[(2 + m) * C + t];
+        const IO* v = reinterpret_cast<const IO*>(a.v) + ((size_t)bh * a.T + n * C + t) * a.dv + col + c0;
+        const float* p = w.R + (chunk * C + t) * DV + col + c0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (REV) raw_b[2 * j + e] = load_two(p + 8 * j);
+          else raw_b[2 * j + e] = t < len && col + c0 + 8 * j < a.dv ? load_two(v + 8 * j) : make_float2(0.f, 0.f);
+        }
+      }
+      return gates[2 * C + C - 1];
+    };
+    float next_end = fetch(0);
     for (int i = 0; i < N; ++i) {
-      const int n = REV ? N - 1 - i : i, b = i & 1, len = min(C, a.T - n * C);
+      const int n = REV ? N - 1 - i : i, b = i & 1;
       const uint32_t parity = i & 1;
       const size_t chunk = (size_t)bh * N + n;
 #pragma unroll
@@ -324,45 +350,34 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
         mma<64, 64, DK>(tm, Kr, Xs);
         commit(&done[0]);
       }
-      // while that runs: the state goes out, this chunk's rows come in
-      const float* gates = w.gates + chunk * kGates;
-      float ga[2], gb[2], B[16], F[RB][16];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = r0 + 8 * e;
-        const float G = gates[2 * C + t], E = gates[3 * C + t], be = gates[4 * C + t];
-        ga[e] = REV ? E : -be * G;   // Y's factor in W
-        gb[e] = REV ? -be * G : E;   // U's (dR's) on its way into X
-        if (!REV) {
-          const IO* v = reinterpret_cast<const IO*>(a.v) + ((size_t)bh * a.T + n * C + t) * a.dv + col + c0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 x = make_float2(0.f, 0.f);
-            if (t < len && col + c0 + 8 * j < a.dv) x = load_two(v + 8 * j);
-            B[4 * j + 2 * e] = be * x.x, B[4 * j + 2 * e + 1] = be * x.y;
-          }
-        } else {
-          const float* p = w.R + (chunk * C + t) * DV + col + c0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x = load_two(p + 8 * j);
-            B[4 * j + 2 * e] = x.x, B[4 * j + 2 * e + 1] = x.y;
-          }
-        }
-      }
-      const float gend = gates[2 * C + C - 1];
+      // while that runs: the state goes out; in reverse its slot first gives up Qᵀ(G O')
+      float F[REV ? RB : 1][16];
       float* Xout = (REV ? w.Z : w.S) + chunk * DK * DV + col + c0;
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           float* p = Xout + (xr[rb] + (e & 2) * 4) * DV + (e >> 2) * 8;
-          if (REV) {  // the slot holds Qᵀ(G O') until now
+          if (REV) {
             const float2 x = load_two(p);
             F[rb][e] = x.x, F[rb][e + 1] = x.y;
+          } else {
+            store_two(p, X[rb][e], X[rb][e + 1]);
           }
-          store_two(p, X[rb][e], X[rb][e + 1]);
         }
+      gend = next_end;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float G = raw_g[e][0], E = raw_g[e][1], be = raw_g[e][2];
+        ga[e] = REV ? E : -be * G;  // Y's factor in W
+        gb[e] = REV ? -be * G : E;  // U's (dR's) on its way into X
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = raw_b[2 * j + e];
+          B[4 * j + 2 * e] = REV ? x.x : be * x.x, B[4 * j + 2 * e + 1] = REV ? x.y : be * x.y;
+        }
+      }
+      if (i + 1 < N) next_end = fetch(i + 1);
       float v[16];
       mbar_wait(&done[0], parity, ok);
       fence_after();
@@ -401,13 +416,20 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       float* Uout = (REV ? w.R : w.U) + (chunk * C + r0) * DV + col + c0;
 #pragma unroll
       for (int e = 0; e < 16; e += 2) store_two(Uout + (e & 2) * 4 * DV + (e >> 2) * 8, v[e], v[e + 1]);
+      if (REV) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            store_two(Xout + (xr[rb] + (e & 2) * 4) * DV + (e >> 2) * 8, X[rb][e], X[rb][e + 1]);
+      }
       mbar_wait(&done[2], parity, ok);
       fence_after();
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         tmem_load(tm + 128 + rows + ((uint32_t)(16 * rb) << 16) + 32 * half, v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) X[rb][e] = fmaf(gend, X[rb][e], REV ? v[e] + F[rb][e] : v[e]);
+        for (int e = 0; e < 16; ++e) X[rb][e] = fmaf(gend, X[rb][e], REV ? v[e] + F[REV ? rb : 0][e] : v[e]);
       }
     }
     float* last = REV ? d.gstate0 : a.stateT;
