@@ -74,8 +74,13 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
     hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C], E[tid] = g[3 * C], be[tid] = g[4 * C];
     rv[tid] = 0.f;
   }
-  load_tile<IO, DK>(sm + L::K, k, at.len, a.dk, 0, tid, kThreads);
-  load_tile<IO, DK>(sm + L::Q, q, at.len, a.dk, 0, tid, kThreads);
+  {
+    TileLoad<IO, DK, kThreads> kl, ql;
+    kl.fetch(k, at.len, a.dk, 0, tid);
+    ql.fetch(q, at.len, a.dk, 0, tid);
+    kl.put(sm + L::K, tid);
+    ql.put(sm + L::Q, tid);
+  }
   fence_async();
   fence_before();
   __syncthreads();
@@ -116,17 +121,22 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
   tmem_load(tm + 64 + rows + 32 * half, qk);
   // products with U, S: dP, dA before masks, dQ = O' Sᵀ, X = dR Sᵀ (dP and dA wait in the shared columns and in Y's)
   for (int sl = 0; sl < slices; ++sl) {
+    TileLoad<IO, 64, kThreads> ol, vl;
+    PartsLoad<PN, C, kThreads> ul, rl;
+    PartsLoad<PN, DK, kThreads> xl;
+    rl.fetch(Rw + sl * 64, DV, tid);
+    vl.fetch(v_in, at.len, a.dv, sl * 64, tid);
+    ol.fetch(go ? go : v_in, go ? at.len : 0, a.dv, sl * 64, tid);
+    ul.fetch(Uw + sl * 64, DV, tid);
+    xl.fetch(Sw + sl * 64, DV, tid);
     if (sl) finish();
-    if (go) load_tile<IO, 64>(sm + L::O, go, at.len, a.dv, sl * 64, tid, kThreads);
-    else load_tile<IO, 64>(sm + L::O, v_in, 0, a.dv, sl * 64, tid, kThreads);
-    load_parts<PN, C>(sm + L::U, Uw + sl * 64, DV, tid, kThreads);
-    load_parts<PN, DK>(sm + L::S, Sw + sl * 64, DV, tid, kThreads);
-    for (int i = tid; i < C * 8; i += kThreads) {  // dR, and what comes of it alone
-      const int r = i >> 3, c = (i & 7) * 8, j = sl * 64 + c;
-      const float4 x0 = *reinterpret_cast<const float4*>(Rw + r * DV + j), x1 = *reinterpret_cast<const float4*>(Rw + r * DV + j + 4);
-      float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, y[8] = {}, dot = 0.f;
+#pragma unroll
+    for (int n = 0; n < rl.N; ++n) {  // dR, and what comes of it alone
+      const int i = tid + n * kThreads, r = i >> 3, c = (i & 7) * 8, j = sl * 64 + c;
+      float x[8], y[8], dot = 0.f;
+      rl.eight(n, x);
+      vl.eight(n, y);
       if (r < at.len && j < a.dv) {
-        load_eight<IO>(v_in + (size_t)r * a.dv + j, y);
         IO* gv = reinterpret_cast<IO*>(d.gv) + (vrow + r) * a.dv + j;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) store_two(gv + e, be[r] * x[e], be[r] * x[e + 1]);
@@ -138,6 +148,9 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
       if ((lane & 7) == 0) rv[r] += dot;
       store_eight<PN>(sm + L::R, kTileBytes, r, c, x);
     }
+    ol.put(sm + L::O, tid);
+    ul.put(sm + L::U, tid);
+    xl.put(sm + L::S, tid);
     publish();
     if (tid == 0) {
       mma<64, 64, 64>(tm + SH, Or, Ur, sl > 0);
@@ -155,12 +168,17 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
   // Y = U Zᵀ, and <Z, S>
   float z = 0.f;
   for (int sl = 0; sl < slices; ++sl) {
+    PartsLoad<PN, C, kThreads> ul;
+    PartsLoad<PN, DK, kThreads> xl, zl;
+    if (slices > 1) ul.fetch(Uw + sl * 64, DV, tid);
+    zl.fetch(Zw + sl * 64, DV, tid);
+    xl.fetch(Sw + sl * 64, DV, tid);
     if (sl) finish();
-    if (slices > 1) load_parts<PN, C>(sm + L::U, Uw + sl * 64, DV, tid, kThreads);
-    load_parts<PN, DK>(sm + L::S, Zw + sl * 64, DV, tid, kThreads);
-    for (int i = tid; i < DK * 16; i += kThreads) {
-      const size_t e = (size_t)(i >> 4) * DV + sl * 64 + (i & 15) * 4;
-      const float4 x = *reinterpret_cast<const float4*>(Sw + e), y = *reinterpret_cast<const float4*>(Zw + e);
+    if (slices > 1) ul.put(sm + L::U, tid);
+    zl.put(sm + L::S, tid);
+#pragma unroll
+    for (int j = 0; j < 2 * xl.N; ++j) {
+      const float4 x = xl.v[j], y = zl.v[j];
       z += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
     }
     publish();

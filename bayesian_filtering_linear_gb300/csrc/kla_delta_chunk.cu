@@ -93,10 +93,9 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Where at = where(a, blockIdx.x);
   const IO* k = reinterpret_cast<const IO*>(a.k) + ((size_t)at.key * a.T + at.t0) * a.dk;
-  load_tile<IO, DK>(sm + L::K, k, at.len, a.dk, 0, tid, kThreads);
-  if (BWD)
-    load_tile<IO, DK>(sm + L::Q, reinterpret_cast<const IO*>(a.q) + ((size_t)at.key * a.T + at.t0) * a.dk, at.len, a.dk,
-                      0, tid, kThreads);
+  TileLoad<IO, DK, kThreads> kl, ql;
+  kl.fetch(k, at.len, a.dk, 0, tid);
+  if (BWD) ql.fetch(reinterpret_cast<const IO*>(a.q) + ((size_t)at.key * a.T + at.t0) * a.dk, at.len, a.dk, 0, tid);
   if (warp == 0) tmem_alloc(&slot, COLS);
   if (tid == 32) mbar_init(&bar, 1);
   if (warp == 2) {  // the gates: two tokens a lane
@@ -129,6 +128,8 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
       out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = expf((float)(total - c)), out[4 * C + t] = b[i];
     }
   }
+  kl.put(sm + L::K, tid);
+  if (BWD) ql.put(sm + L::Q, tid);
   fence_async();
   fence_before();
   __syncthreads();
@@ -177,15 +178,17 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
     __syncthreads();
     for (int sl = 0; sl < DV / 64; ++sl) {
       const IO* go = reinterpret_cast<const IO*>(d.go);
-      const IO* src = go ? go + ((size_t)at.bh * a.T + at.t0) * a.dv : nullptr;
-      load_tile<IO, 64>(sm + L::O, src, src ? at.len : 0, a.dv, sl * 64, tid, kThreads);
-      for (int i = tid; i < C * 8; i += kThreads) {
-        const int r = i >> 3, c = (i & 7) * 8;
-        float x[8] = {};
-        if (src && r < at.len && sl * 64 + c < a.dv) load_eight<IO>(src + (size_t)r * a.dv + sl * 64 + c, x);
+      TileLoad<IO, 64, kThreads> ol;
+      ol.fetch(go + (go ? ((size_t)at.bh * a.T + at.t0) * a.dv : 0), go ? at.len : 0, a.dv, sl * 64, tid);
+      ol.put(sm + L::O, tid);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= a.scale * G[r];
-        store_eight<3>(sm + L::GO, kTileBytes, r, c, x);
+      for (int j = 0; j < ol.N; ++j) {
+        const int i = tid + j * kThreads, r = i >> 3;
+        float x[8];
+        ol.eight(j, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= a.scale * G[r];
+        store_eight<3>(sm + L::GO, kTileBytes, r, (i & 7) * 8, x);
       }
       fence_async();
       fence_before();
@@ -264,6 +267,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   bool ok = true;
   if (tid >= kChainThreads) {
     const int ft = tid - kChainThreads;
+    const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
     for (int i = 0; i < N; ++i) {
       const int n = REV ? N - 1 - i : i, b = i & 1;
       const float4* src = reinterpret_cast<const float4*>(w.M + ((size_t)bh * N + n) * C * C);
@@ -273,9 +277,11 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
         m[2 * j] = src[(ft + j * kFeedThreads) * 2];
         m[2 * j + 1] = src[(ft + j * kFeedThreads) * 2 + 1];
       }
+      TileLoad<IO, DK, kFeedThreads> kl;
+      if (PARTS == 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
       if (i >= 2) mbar_wait(&empty[b], ((i >> 1) - 1) & 1, ok);
-      load_tile<IO, DK>(sm + L::K + b * L::KB, reinterpret_cast<const IO*>(a.k) + ((size_t)key * a.T + n * C) * a.dk,
-                        min(C, a.T - n * C), a.dk, 0, ft, kFeedThreads);
+      if (PARTS > 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);  // too many to hold while waiting
+      kl.put(sm + L::K + b * L::KB, ft);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = ft + j * kFeedThreads;
@@ -474,14 +480,21 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   if (warp == 0) tmem_alloc(&slot, 128);
   if (tid == 32) mbar_init(&bar, 1);
   const size_t row = (size_t)at.key * a.T + at.t0;
-  load_tile<IO, DK>(sm + L::K, reinterpret_cast<const IO*>(a.k) + row * a.dk, at.len, a.dk, 0, tid, kThreads);
-  load_tile<IO, DK>(sm + L::Q, reinterpret_cast<const IO*>(a.q) + row * a.dk, at.len, a.dk, 0, tid, kThreads);
-  load_parts<PN, DK>(sm + L::S, w.S + at.chunk * DK * DV + col, DV, tid, kThreads);
-  load_parts<PN, C>(sm + L::U, w.U + at.chunk * C * DV + col, DV, tid, kThreads);
+  TileLoad<IO, DK, kThreads> kl, ql;
+  PartsLoad<PN, DK, kThreads> xl;
+  PartsLoad<PN, C, kThreads> ul;
+  kl.fetch(reinterpret_cast<const IO*>(a.k) + row * a.dk, at.len, a.dk, 0, tid);
+  ql.fetch(reinterpret_cast<const IO*>(a.q) + row * a.dk, at.len, a.dk, 0, tid);
+  xl.fetch(w.S + at.chunk * DK * DV + col, DV, tid);
+  ul.fetch(w.U + at.chunk * C * DV + col, DV, tid);
   if (tid < C) {
     const float* g = w.gates + at.chunk * kGates + tid;
     hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C];
   }
+  kl.put(sm + L::K, tid);
+  ql.put(sm + L::Q, tid);
+  xl.put(sm + L::S, tid);
+  ul.put(sm + L::U, tid);
   fence_async();
   fence_before();
   __syncthreads();

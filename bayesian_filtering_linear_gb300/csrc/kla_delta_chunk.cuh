@@ -48,52 +48,86 @@ __device__ __forceinline__ void store_two(float* p, float x, float y) { *reinter
 __device__ __forceinline__ void store_two(__nv_bfloat16* p, float x, float y) {
   *reinterpret_cast<uint32_t*>(p) = bf16_pair(x, y);
 }
-template <typename IO>
-__device__ __forceinline__ void load_eight(const IO* p, float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = load_two(p + 2 * i);
-    x[2 * i] = v.x;
-    x[2 * i + 1] = v.y;
-  }
-}
-
 // Rows [0, len) of 64 (the rest zero) of an io array [.][d], columns c0 to
-// c0 + W (those from d on zero), into tiles of kParts<IO> parts.
-template <typename IO, int W>
-__device__ __forceinline__ void load_tile(char* tile, const IO* src, int len, int d, int c0, int tid, int threads) {
-  constexpr int PARTS = kParts<IO>, PART = W / 64 * kTileBytes;
-  for (int i = tid; i < C * W / 8; i += threads) {
-    const int r = i / (W / 8), c = i % (W / 8) * 8;
-    char* t = tile + (c >> 6) * kTileBytes;
-    const bool in = r < len && c0 + c < d;
-    if (PARTS == 1) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (in) v = *reinterpret_cast<const uint4*>(src + (size_t)r * d + c0 + c);
-      *reinterpret_cast<uint4*>(t + r * 128 + ((((c >> 3) ^ r) & 7) << 4)) = v;
-    } else {
-      float x[8] = {};
-      if (in) {
-        const float4 lo = *reinterpret_cast<const float4*>(src + (size_t)r * d + c0 + c);
-        const float4 hi = *reinterpret_cast<const float4*>(src + (size_t)r * d + c0 + c + 4);
-        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-      }
-      store_eight<PARTS>(t, PART, r, c & 63, x);
+// c0 + W (those from d on zero), as tiles of kParts<IO> parts, by THREADS
+// threads: fetch() brings a thread's share into registers, all loads in flight
+// together, and put() writes the parts.
+template <typename IO, int W, int THREADS>
+struct TileLoad {
+  static constexpr int N = C * W / 8 / THREADS, PARTS = kParts<IO>, PART = W / 64 * kTileBytes;
+  uint4 v[N * sizeof(IO) / 2];
+  __device__ __forceinline__ void fetch(const IO* src, int len, int d, int c0, int tid) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = tid + j * THREADS, r = i / (W / 8), c = i % (W / 8) * 8;
+      const bool in = r < len && c0 + c < d;
+      const uint4* p = reinterpret_cast<const uint4*>(src + (size_t)r * d + c0 + c);
+#pragma unroll
+      for (int e = 0; e < (int)sizeof(IO) / 2; ++e)
+        v[j * sizeof(IO) / 2 + e] = in ? p[e] : make_uint4(0, 0, 0, 0);
     }
   }
-}
-
-// A workspace array's rows, 64 columns of row length ld, into one column of tiles.
-template <int PARTS, int ROWS>
-__device__ __forceinline__ void load_parts(char* tile, const float* src, int ld, int tid, int threads) {
-  for (int i = tid; i < ROWS * 8; i += threads) {
-    const int r = i >> 3, c = (i & 7) * 8;
-    const float4 lo = *reinterpret_cast<const float4*>(src + (size_t)r * ld + c);
-    const float4 hi = *reinterpret_cast<const float4*>(src + (size_t)r * ld + c + 4);
-    float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    store_eight<PARTS>(tile, ROWS * 128, r, c, x);
+  __device__ __forceinline__ void put(char* tile, int tid) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = tid + j * THREADS, r = i / (W / 8), c = i % (W / 8) * 8;
+      char* t = tile + (c >> 6) * kTileBytes;
+      if (PARTS == 1) {
+        *reinterpret_cast<uint4*>(t + r * 128 + ((((c >> 3) ^ r) & 7) << 4)) = v[j];
+      } else {
+        float x[8];
+        eight(j, x);
+        store_eight<PARTS>(t, PART, r, c & 63, x);
+      }
+    }
   }
-}
+  // the thread's j-th eight values
+  __device__ __forceinline__ void eight(int j, float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(IO) / 2; ++e) {
+      const uint4 y = v[j * sizeof(IO) / 2 + e];
+      const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (PARTS == 1) {
+          x[2 * m] = __uint_as_float(u[m] << 16);
+          x[2 * m + 1] = __uint_as_float(u[m] & 0xffff0000u);
+        } else {
+          x[4 * e + m] = __uint_as_float(u[m]);
+        }
+      }
+    }
+  }
+};
+
+// A workspace array's rows, 64 columns of row length ld, as one column of tiles.
+template <int PARTS, int ROWS, int THREADS>
+struct PartsLoad {
+  static constexpr int N = ROWS * 8 / THREADS;
+  float4 v[2 * N];
+  __device__ __forceinline__ void fetch(const float* src, int ld, int tid) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = tid + j * THREADS;
+      const float4* p = reinterpret_cast<const float4*>(src + (size_t)(i >> 3) * ld + (i & 7) * 8);
+      v[2 * j] = p[0];
+      v[2 * j + 1] = p[1];
+    }
+  }
+  __device__ __forceinline__ void eight(int j, float (&x)[8]) const {
+    const float4 a = v[2 * j], b = v[2 * j + 1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ void put(char* tile, int tid) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = tid + j * THREADS;
+      float x[8];
+      eight(j, x);
+      store_eight<PARTS>(tile, ROWS * 128, i >> 3, (i & 7) * 8, x);
+    }
+  }
+};
 
 // Decay from token s to token t ≥ s of a chunk.
 __device__ __forceinline__ float decay(const float* hi, const float* lo, int t, int s) {
