@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
   __shared__ float hi[C], lo[C], G[C], E[C], be[C], rv[C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int DV = pad64(a.dv), slices = DV / 64;
   const Where at = where(a, blockIdx.x);
   const size_t krow = (size_t)at.key * a.T + at.t0, vrow = (size_t)at.bh * a.T + at.t0;
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = slot, base = smem_addr(sm);
+  const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   const Operand<PARTS, false> Kr{base + L::K, NB * kTileBytes, kTileBytes}, Qr{base + L::Q, NB * kTileBytes, kTileBytes};
   const Operand<PARTS, true> Kt{base + L::K, NB * kTileBytes, kTileBytes}, Qt{base + L::Q, NB * kTileBytes, kTileBytes};
   const Operand<PARTS, false> Or{base + L::O, kTileBytes, kTileBytes};
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
     ul.put(sm + L::U, tid);
     xl.put(sm + L::S, tid);
     publish();
-    if (tid == 0) {
+    if (warp == 0 && elect()) {
       mma<64, 64, 64>(tm + SH, Or, Ur, sl > 0);
       mma<64, 64, 64>(tm + 2 * DK, Rr, Ur, sl > 0);
       mma<64, DK, 64>(tm, Or, Sr, sl > 0);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
       z += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
     }
     publish();
-    if (tid == 0) {
+    if (warp == 0 && elect()) {
       mma<64, DK, 64>(tm + 2 * DK, Ur, Sr, sl > 0);
       commit(&bar);
     }
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArg
     store_pair<PN>(sm + L::bA, kTileBytes, t, s, be[t] * ga[e], be[t] * ga[e + 1]);
   }
   publish();
-  if (tid == 0) {
+  if (warp == 0 && elect()) {
     const Operand<PN, false> P{base + L::dP, kTileBytes, kTileBytes}, A{base + L::dA, kTileBytes, kTileBytes};
     const Operand<PN, true> Pt{base + L::dP, kTileBytes, kTileBytes}, At{base + L::bA, kTileBytes, kTileBytes};
     mma<64, DK, 64>(tm, P, Kt);

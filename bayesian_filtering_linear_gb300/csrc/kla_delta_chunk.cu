@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
   __shared__ float hi[C], lo[C], G[C], be[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Where at = where(a, blockIdx.x);
   const IO* k = reinterpret_cast<const IO*>(a.k) + ((size_t)at.key * a.T + at.t0) * a.dk;
   TileLoad<IO, DK, kThreads> kl, ql;
@@ -134,10 +134,10 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = slot, base = smem_addr(sm);
+  const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   const Operand<PARTS, false> Kr{base + L::K, DK / 64 * kTileBytes, kTileBytes}, Qr{base + L::Q, DK / 64 * kTileBytes, kTileBytes};
   bool ok = true;
-  if (tid == 0) {
+  if (warp == 0 && elect()) {
     mma<64, 64, DK>(tm, Kr, Kr);
     if (BWD) mma<64, 64, DK>(tm + 64, Qr, Kr);
     commit(&bar);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
       fence_before();
       __syncthreads();
       fence_after();
-      if (tid == 0) {
+      if (warp == 0 && elect()) {
         const Operand<3, true> Pt{base + L::P, kTileBytes, kTileBytes}, GO{base + L::GO, kTileBytes, kTileBytes};
         const Operand<PARTS, true> O{base + L::O, kTileBytes, kTileBytes}, Qt{base + L::Q, DK / 64 * kTileBytes, kTileBytes};
         mma<64, 64, 64>(tm + 128, Pt, O);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   char* sm = align1024(raw);
   __shared__ uint64_t full[2], empty[2], done[3];
   __shared__ uint32_t slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int DV = pad64(a.dv), N = (a.T + C - 1) / C;
   const long long bh = blockIdx.x / (DV / 64);
   const int col = (int)(blockIdx.x % (DV / 64)) * 64;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = slot, base = smem_addr(sm);
+  const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
   if (tid >= kChainThreads) {
     const int ft = tid - kChainThreads;
@@ -350,11 +350,13 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       const Operand<PARTS, true> Kt{base + L::K + b * L::KB, RB * kTileBytes, kTileBytes};
       const Operand<3, REV> Mx{base + L::M + b * L::MB, kTileBytes, kTileBytes};
       const Operand<3, true> Xs{base + L::X, DK * 128, DK * 128}, Ws{base + L::W, kTileBytes, kTileBytes};
-      if (tid == 0) {
+      if (warp == 0) {
         mbar_wait(&full[b], (i >> 1) & 1, ok);
         fence_after();
-        mma<64, 64, DK>(tm, Kr, Xs);
-        commit(&done[0]);
+        if (elect()) {
+          mma<64, 64, DK>(tm, Kr, Xs);
+          commit(&done[0]);
+        }
       }
       // while that runs: the state goes out; in reverse its slot first gives up Qᵀ(G O')
       float F[REV ? RB : 1][16];
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       fence_async();
       fence_before();
       bar_sync(1, kChainThreads);
-      if (tid == 0) {
+      if (warp == 0 && elect()) {
         fence_after();
         mma<64, 64, 64>(tm + 64, Mx, Ws);
         commit(&done[1]);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       fence_async();
       fence_before();
       bar_sync(1, kChainThreads);
-      if (tid == 0) {
+      if (warp == 0 && elect()) {
         fence_after();
         mma<DK, 64, 64>(tm + 128, Kt, Ws);
         commit(&done[2]);
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   __shared__ float hi[C], lo[C], G[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int DV = pad64(a.dv);
   const Where at = where(a, blockIdx.x / (DV / 64));
   const int col = (int)(blockIdx.x % (DV / 64)) * 64;
@@ -499,9 +501,9 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = slot, base = smem_addr(sm);
+  const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
-  if (tid == 0) {
+  if (warp == 0 && elect()) {
     const Operand<PARTS, false> Kr{base + L::K, DK / 64 * kTileBytes, kTileBytes}, Qr{base + L::Q, DK / 64 * kTileBytes, kTileBytes};
     mma<64, 64, DK>(tm, Qr, Kr);
     mma<64, 64, DK>(tm + 64, Qr, Operand<PN, true>{base + L::S, DK * 128, DK * 128});
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   fence_before();
   __syncthreads();
   fence_after();
-  if (tid == 0) {
+  if (warp == 0 && elect()) {
     mma<64, 64, 64>(tm, Operand<PN, false>{base + L::P, kTileBytes, kTileBytes},
                     Operand<PN, true>{base + L::U, kTileBytes, kTileBytes});
     commit(&bar);

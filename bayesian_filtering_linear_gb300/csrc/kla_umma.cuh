@@ -73,6 +73,17 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// One lane of a converged warp. Products are issued by a warp that takes the
+// branch as a whole, with values the compiler knows to be the same in all its
+// lanes: descriptors then stay in uniform registers (inside a branch of one
+// thread each product cost 60 to 100 cycles to issue).
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
+
 // ---- products -------------------------------------------------------------------
 // A tile operand of PARTS parts, `part` bytes apart, K-major (rows are M or N)
 // or MN-major (rows are K). `block`: bytes between its 64-column tiles.
