@@ -14,7 +14,7 @@
 // behind a strong decay those cancel to nothing and leave their roundings,
 // while every product above carries the decay it is the gradient of.
 //
-// Four steps: `prepare` makes M and, ahead of the chain, Pᵀ O' and Qᵀ(G O');
+// Four steps: `prepare` makes, ahead of the chain, Mᵀ (E K), Mᵀ Pᵀ O' and Qᵀ(G O');
 // the chain runs forward for S and U, and from the end for Z and dR; then a
 // block per chunk and head makes everything else here. Gradients of q and k
 // that several value heads share are summed from per-head fp32 parts in a
@@ -35,7 +35,7 @@ struct GradSmem {
   // once the products with S and Z are done: (dP P + dA A), then the masked dP, dA and β dA
   static constexpr int W = O, dP = O, dA = dP + ROWS, bA = dA + ROWS, kEnd = bA + ROWS;
   static constexpr int kBytes = (kStage > kEnd ? kStage : kEnd) + 1024;
-  static_assert(W + 64 * 65 * 4 <= kBytes - 1024, "");
+  static_assert(W + 64 * 65 * 4 <= kBytes - 1024 && kBytes <= kMaxBytes, "");
 };
 
 // Per row of a fragment: the sum over its four lanes; lane 0 of the four keeps it.

@@ -6,12 +6,13 @@
 //   U = M β(V − G K S),   S' = G_end S + Kᵀ(E U)
 //   O = scale (G Q S + tril(D_ts q_t·k_s) U)
 //
-// Three kernels. `prepare` (a block per chunk and head) makes M. `chain` (a
-// block per head and 64 columns, in order over the chunks) carries S in
-// registers: three products and three round trips between TMEM, registers and
-// shared memory per chunk, whose latency bounds it. `output` (a block per
-// chunk, head and 64 columns) makes O. The backward pass runs the same chain
-// from the end with Mᵀ (see kla_delta_backward.cu).
+// Three kernels. `prepare` (a block per chunk and head) makes M and with it
+// W = −M (β G K) and M (β V). `chain` (a block per head and 64 columns, in
+// order over the chunks) carries S in registers: U = M (β V) + W S and the
+// update, two products and two round trips between TMEM, registers and shared
+// memory per chunk, whose latency bounds it. `output` (a block per chunk, head
+// and 64 columns) makes O. The backward pass runs the same chain from the end
+// with Mᵀ (see kla_delta_backward.cu).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
 // and everything that flows into them are kept in three, so that a state is as
@@ -73,29 +74,53 @@ __device__ void invert(float* A, float* M, int tid) {
 
 template <typename IO, int DK, bool BWD>
 struct PrepareSmem {
-  static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes;
-  static constexpr int K = 0, Q = IN, P = Q + (BWD ? IN : 0), O = P + (BWD ? 3 * kTileBytes : 0),
-                       GO = O + PARTS * kTileBytes, A = O, M = A + 64 * 68 * 4;  // A and M are done with before O and GO
-  static constexpr int kEnd = BWD && GO + 3 * kTileBytes > M + 64 * 68 * 4 ? GO + 3 * kTileBytes : M + 64 * 68 * 4;
+  static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes, M3 = 3 * kTileBytes, T = DK / 64 * M3;
+  static constexpr int kSquare = 64 * 68 * 4;
+  // K is last used before O comes in its place; A and M in fp32 are done with before the tiles T1 and T2
+  // (β G K and E K for DK = 128 fill both, one after the other)
+  static constexpr int K = 0, Q = IN, MP = Q + (BWD ? IN : 0), P = MP + M3, T1 = P + (BWD ? M3 : 0), T2 = T1 + M3,
+                       A = T1, M = A + kSquare;
+  static constexpr int kTiles = BWD ? T2 + M3 : T1 + T, kEnd = kTiles > M + kSquare ? kTiles : M + kSquare;
   static constexpr int kBytes = kEnd + 1024;
+  static_assert(kBytes <= kMaxBytes, "");
 };
+
+// 16 × 32 fragments of a product of W columns from TMEM to rows of fp32
+template <int W, int ROWS>
+__device__ __forceinline__ void drain(uint32_t tm, float* out, int ld, int quad, int half, int lane, float bad) {
+  float v[16];
+#pragma unroll
+  for (int rb = 0; rb < ROWS / 64; ++rb)
+#pragma unroll
+    for (int cb = 0; cb < W / 64; ++cb) {
+      tmem_load(tm + ((uint32_t)(32 * quad + 16 * rb) << 16) + 64 * cb + 32 * half, v);
+      const int r = (ROWS == 64 ? 16 * quad : 32 * quad + 16 * rb) + (lane >> 2), c = 64 * cb + 32 * half + 2 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) store_two(out + (r + (i & 2) * 4) * ld + c + (i >> 2) * 8, v[i] + bad, v[i + 1] + bad);
+    }
+}
 
 template <typename IO, int DK, bool BWD>
 __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                     const Workspace w) {
   using L = PrepareSmem<IO, DK, BWD>;
-  constexpr int PARTS = L::PARTS, COLS = BWD ? 256 : 64;
+  constexpr int PARTS = L::PARTS, COLS = BWD || DK == 128 ? 256 : 128, NB = DK / 64;
   extern __shared__ char raw[];
   char* sm = align1024(raw);
-  __shared__ float hi[C], lo[C], G[C], be[C];
+  __shared__ float hi[C], lo[C], G[C], E[C], be[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Where at = where(a, blockIdx.x);
-  const IO* k = reinterpret_cast<const IO*>(a.k) + ((size_t)at.key * a.T + at.t0) * a.dk;
-  TileLoad<IO, DK, kThreads> kl, ql;
-  kl.fetch(k, at.len, a.dk, 0, tid);
-  if (BWD) ql.fetch(reinterpret_cast<const IO*>(a.q) + ((size_t)at.key * a.T + at.t0) * a.dk, at.len, a.dk, 0, tid);
+  const int DV = pad64(a.dv);
+  const size_t krow = ((size_t)at.key * a.T + at.t0) * a.dk, vrow = ((size_t)at.bh * a.T + at.t0) * a.dv;
+  TileLoad<IO, DK, kThreads> kl;
+  kl.fetch(reinterpret_cast<const IO*>(a.k) + krow, at.len, a.dk, 0, tid);
+  if (BWD) {
+    TileLoad<IO, DK, kThreads> ql;
+    ql.fetch(reinterpret_cast<const IO*>(a.q) + krow, at.len, a.dk, 0, tid);
+    ql.put(sm + L::Q, tid);
+  }
   if (warp == 0) tmem_alloc(&slot, COLS);
   if (tid == 32) mbar_init(&bar, 1);
   if (warp == 2) {  // the gates: two tokens a lane
@@ -123,20 +148,33 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const double c = lane ? before + x[i] : x[i];
-      const float h = (float)c, l = (float)(c - h), g = expf(h) * (1.f + l);
-      hi[t] = h, lo[t] = l, G[t] = g, be[t] = b[i];
-      out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = expf((float)(total - c)), out[4 * C + t] = b[i];
+      const float h = (float)c, l = (float)(c - h), g = expf(h) * (1.f + l), e = expf((float)(total - c));
+      hi[t] = h, lo[t] = l, G[t] = g, E[t] = e, be[t] = b[i];
+      out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = e, out[4 * C + t] = b[i];
     }
   }
   kl.put(sm + L::K, tid);
-  if (BWD) ql.put(sm + L::Q, tid);
-  fence_async();
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
-  const Operand<PARTS, false> Kr{base + L::K, DK / 64 * kTileBytes, kTileBytes}, Qr{base + L::Q, DK / 64 * kTileBytes, kTileBytes};
   bool ok = true;
+  uint32_t phase = 0;
+  auto finish = [&] {  // the products issued so far
+    mbar_wait(&bar, phase, ok);
+    phase ^= 1;
+    fence_after();
+  };
+  auto publish = [&] {  // this block's shared-memory writes and TMEM reads, before the next products
+    fence_async();
+    fence_before();
+    __syncthreads();
+    fence_after();
+  };
+  publish();
+  const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
+  const Operand<PARTS, false> Kr{base + L::K, NB * kTileBytes, kTileBytes}, Qr{base + L::Q, NB * kTileBytes, kTileBytes};
+  const Operand<PARTS, true> Qt{base + L::Q, NB * kTileBytes, kTileBytes};
+  const Operand<3, false> Mr{base + L::MP, kTileBytes, kTileBytes};
+  const Operand<3, true> Mt{base + L::MP, kTileBytes, kTileBytes}, Pt{base + L::P, kTileBytes, kTileBytes};
+  const Operand<3, true> Kb{base + L::T1, NB * kTileBytes, kTileBytes};
+  const Operand<3, true> V1{base + L::T1, kTileBytes, kTileBytes}, V2{base + L::T2, kTileBytes, kTileBytes};
   if (warp == 0 && elect()) {
     mma<64, 64, DK>(tm, Kr, Kr);
     if (BWD) mma<64, 64, DK>(tm + 64, Qr, Kr);
@@ -146,8 +184,9 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
   float* M = reinterpret_cast<float*>(sm + L::M);
   const int quad = warp & 3, half = warp >> 2, r0 = 16 * quad + (lane >> 2), c0 = 32 * half + 2 * (lane & 3);
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
-  mbar_wait(&bar, 0, ok);
-  fence_after();
+  TileLoad<IO, 64, kThreads> vl;
+  vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, 0, tid);
+  finish();
   float v[16];
   tmem_load(tm + rows + 32 * half, v);
 #pragma unroll
@@ -167,57 +206,86 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
   }
   __syncthreads();
   invert(A, M, tid);
-  float* out = w.M + at.chunk * C * C;
-  for (int i = tid; i < C * C / 4; i += kThreads) {
-    float4 x = *reinterpret_cast<const float4*>(M + (i >> 4) * 68 + (i & 15) * 4);
-    if (!ok) x.x = x.y = x.z = x.w = __int_as_float(0x7fc00000);  // a wait ran out
-    reinterpret_cast<float4*>(out)[i] = x;
+  for (int i = tid; i < C * 8; i += kThreads) {
+    const float4* p = reinterpret_cast<const float4*>(M + (i >> 3) * 68 + (i & 7) * 8);
+    float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
+    store_eight<3>(sm + L::MP, kTileBytes, i >> 3, (i & 7) * 8, x);
   }
-  if (BWD) {
-    const int DV = pad64(a.dv);
-    __syncthreads();
-    for (int sl = 0; sl < DV / 64; ++sl) {
-      const IO* go = reinterpret_cast<const IO*>(d.go);
-      TileLoad<IO, 64, kThreads> ol;
-      ol.fetch(go + (go ? ((size_t)at.bh * a.T + at.t0) * a.dv : 0), go ? at.len : 0, a.dv, sl * 64, tid);
-      ol.put(sm + L::O, tid);
+  __syncthreads();
+  // rows of an input times a factor, as three parts
+  auto scaled = [&](auto& tile, int W, char* to, int part, auto factor) {
 #pragma unroll
-      for (int j = 0; j < ol.N; ++j) {
-        const int i = tid + j * kThreads, r = i >> 3;
-        float x[8];
-        ol.eight(j, x);
+    for (int j = 0; j < tile.N; ++j) {
+      const int i = tid + j * kThreads, r = i / (W / 8), c = i % (W / 8) * 8;
+      float x[8];
+      tile.eight(j, x);
+      const float f = factor(r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= a.scale * G[r];
-        store_eight<3>(sm + L::GO, kTileBytes, r, (i & 7) * 8, x);
-      }
-      fence_async();
-      fence_before();
-      __syncthreads();
-      fence_after();
+      for (int e = 0; e < 8; ++e) x[e] *= f;
+      store_eight<3>(to + (c >> 6) * kTileBytes, part, r, c & 63, x);
+    }
+  };
+  scaled(kl, DK, sm + L::T1, NB * kTileBytes, [&](int r) { return -be[r] * G[r]; });
+  if (BWD && DK == 64) scaled(kl, DK, sm + L::T2, kTileBytes, [&](int r) { return E[r]; });
+  publish();
+  if (warp == 0 && elect()) {
+    mma<64, DK, 64>(tm, Mr, Kb);
+    if (BWD && DK == 64) mma<64, 64, 64>(tm + 64, Mt, V2);
+    commit(&bar);
+  }
+  finish();
+  if (BWD && DK == 128) {
+    scaled(kl, DK, sm + L::T1, NB * kTileBytes, [&](int r) { return E[r]; });
+    publish();
+    if (warp == 0 && elect()) {
+      mma<64, DK, 64>(tm + DK, Mt, Kb);
+      commit(&bar);
+    }
+    finish();
+  }
+  float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
+  drain<DK, 64>(tm, w.W + at.chunk * C * DK, DK, quad, half, lane, bad);
+  if (BWD) drain<DK, 64>(tm + DK, w.Wr + at.chunk * C * DK, DK, quad, half, lane, bad);
+  for (int sl = 0; sl < DV / 64; ++sl) {
+    if (sl) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, sl * 64, tid);
+    if (!BWD) {
+      scaled(vl, 64, sm + L::T1, kTileBytes, [&](int r) { return be[r]; });
+      publish();
       if (warp == 0 && elect()) {
-        const Operand<3, true> Pt{base + L::P, kTileBytes, kTileBytes}, GO{base + L::GO, kTileBytes, kTileBytes};
-        const Operand<PARTS, true> O{base + L::O, kTileBytes, kTileBytes}, Qt{base + L::Q, DK / 64 * kTileBytes, kTileBytes};
-        mma<64, 64, 64>(tm + 128, Pt, O);
-        mma<DK, 64, 64>(tm + 192, Qt, GO);
+        mma<64, 64, 64>(tm, Mr, V1);
         commit(&bar);
       }
-      mbar_wait(&bar, (sl + 1) & 1, ok);
-      fence_after();
-      const float bad = ok ? 0.f : __int_as_float(0x7fc00000);
-      tmem_load(tm + 128 + rows + 32 * half, v);
-      float* R = w.R + at.chunk * C * DV + sl * 64;
-#pragma unroll
-      for (int i = 0; i < 16; i += 2)
-        store_two(R + (r0 + (i & 2) * 4) * DV + c0 + (i >> 2) * 8, v[i] + bad, v[i + 1] + bad);
-      float* Z = w.Z + at.chunk * DK * DV + sl * 64;
-#pragma unroll
-      for (int rb = 0; rb < DK / 64; ++rb) {
-        tmem_load(tm + 192 + rows + ((uint32_t)(16 * rb) << 16) + 32 * half, v);
-        const int r = (DK == 64 ? 16 * quad : 32 * quad + 16 * rb) + (lane >> 2);
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) store_two(Z + (r + (i & 2) * 4) * DV + c0 + (i >> 2) * 8, v[i], v[i + 1]);
+      finish();
+      drain<64, 64>(tm, w.U + at.chunk * C * DV + sl * 64, DV, quad, half, lane, 0.f);
+    } else {
+      const IO* go = reinterpret_cast<const IO*>(d.go);
+      TileLoad<IO, 64, kThreads> ol;
+      ol.fetch(go + (go ? vrow : 0), go ? at.len : 0, a.dv, sl * 64, tid);
+      scaled(vl, 64, sm + L::T2, kTileBytes, [&](int r) { return be[r]; });
+      ol.put(sm + L::K, tid);
+      scaled(ol, 64, sm + L::T1, kTileBytes, [&](int r) { return a.scale * G[r]; });
+      publish();
+      if (warp == 0 && elect()) {
+        mma<64, 64, 64>(tm + 64, Pt, Operand<PARTS, true>{base + L::K, kTileBytes, kTileBytes});
+        mma<64, 64, 64>(tm, Mr, V2);
+        mma<DK, 64, 64>(tm + 128, Qt, V1);
+        commit(&bar);
       }
-      fence_before();
+      finish();
+      tmem_load(tm + 64 + rows + 32 * half, v);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2)  // Pᵀ O' goes on to Mᵀ Pᵀ O'
+        store_pair<3>(sm + L::T1, kTileBytes, r0 + (i & 2) * 4, c0 + (i >> 2) * 8, v[i], v[i + 1]);
+      publish();
+      if (warp == 0 && elect()) {
+        mma<64, 64, 64>(tm + 192, Mt, V1);
+        commit(&bar);
+      }
+      drain<64, 64>(tm, w.U + at.chunk * C * DV + sl * 64, DV, quad, half, lane, 0.f);
+      drain<64, DK>(tm + 128, w.Z + at.chunk * DK * DV + sl * 64, DV, quad, half, lane, 0.f);
+      finish();
+      bad = ok ? 0.f : __int_as_float(0x7fc00000);
+      drain<64, 64>(tm + 192, w.R + at.chunk * C * DV + sl * 64, DV, quad, half, lane, bad);
     }
   }
   fence_before();
@@ -226,17 +294,20 @@ __global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const Delta
 }
 
 // ---- the chain ----------------------------------------------------------------------
-// X: the state (rev: its gradient). Per chunk, with Y = K X:
-//   forward:  W = β(V − G Y),       U = M W,   X = G_end X + Kᵀ(E U)
-//   reverse:  W = Pᵀ O' + E Y,     dR = Mᵀ W,  X = G_end X + Qᵀ(G O') − Kᵀ(β G dR)
-// Eight warps walk the chunks; four more bring K and M of the next chunk as
-// parts, two chunks deep.
+// X: the state (rev: its gradient), W: −M (β G K) (rev: Mᵀ (E K)). Per chunk:
+//   forward:  U = M (β V) + W X,       X = G_end X + Kᵀ(E U)
+//   reverse:  dR = Mᵀ Pᵀ O' + W X,     X = G_end X + Qᵀ(G O') − Kᵀ(β G dR)
+// Eight warps walk the chunks; four more bring K and W of the next chunk as
+// parts, two chunks deep where shared memory holds them.
 constexpr int kChainThreads = 256, kFeedThreads = 128;
 
 template <typename IO, int DK>
 struct ChainSmem {
-  static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, MB = 3 * kTileBytes;
-  static constexpr int K = 0, M = 2 * KB, X = M + 2 * MB, W = X + 3 * DK * 128, kBytes = W + MB + 1024;
+  static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, WB = 3 * DK / 64 * kTileBytes;
+  static constexpr int STAGES = sizeof(IO) == 4 && DK == 128 ? 1 : 2;
+  static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + 3 * DK * 128,
+                       kBytes = U + 3 * kTileBytes + 1024;
+  static_assert(kBytes <= kMaxBytes, "");
 };
 
 template <typename IO, int DK, bool REV>
@@ -244,10 +315,10 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
                                                                                       const DeltaGradArgs d,
                                                                                       const Workspace w) {
   using L = ChainSmem<IO, DK>;
-  constexpr int PARTS = kParts<IO>, RB = DK / 64;
+  constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES;
   extern __shared__ char raw[];
   char* sm = align1024(raw);
-  __shared__ uint64_t full[2], empty[2], done[3];
+  __shared__ uint64_t full[STAGES], empty[STAGES], done[2];
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int DV = pad64(a.dv), N = (a.T + C - 1) / C;
@@ -255,40 +326,34 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   const int col = (int)(blockIdx.x % (DV / 64)) * 64;
   const long long key = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(&full[i], kFeedThreads), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 3; ++i) mbar_init(&done[i], 1);
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], kFeedThreads), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
   }
-  if (warp == 0) tmem_alloc(&slot, 256);
+  if (warp == 0) tmem_alloc(&slot, 128);
   fence_async();
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
-  if (tid >= kChainThreads) {
+  if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
     const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
+    const float* W = (REV ? w.Wr : w.W) + (size_t)bh * N * C * DK;
     for (int i = 0; i < N; ++i) {
-      const int n = REV ? N - 1 - i : i, b = i & 1;
-      const float4* src = reinterpret_cast<const float4*>(w.M + ((size_t)bh * N + n) * C * C);
-      float4 m[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[2 * j] = src[(ft + j * kFeedThreads) * 2];
-        m[2 * j + 1] = src[(ft + j * kFeedThreads) * 2 + 1];
-      }
+      const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
+      const uint32_t before = STAGES == 2 ? ((i >> 1) - 1) & 1 : (i - 1) & 1;
       TileLoad<IO, DK, kFeedThreads> kl;
+      PartsLoad<3, C, kFeedThreads> wl[RB];
+      // what registers hold comes in ahead of the wait for its place
+      wl[0].fetch(W + (size_t)n * C * DK, DK, ft);
       if (PARTS == 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
-      if (i >= 2) mbar_wait(&empty[b], ((i >> 1) - 1) & 1, ok);
-      if (PARTS > 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);  // too many to hold while waiting
-      kl.put(sm + L::K + b * L::KB, ft);
+      if (RB > 1) wl[RB - 1].fetch(W + (size_t)n * C * DK + 64, DK, ft);
+      if (i >= STAGES) mbar_wait(&empty[b], before, ok);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = ft + j * kFeedThreads;
-        float x[8] = {m[2 * j].x, m[2 * j].y, m[2 * j].z, m[2 * j].w,
-                      m[2 * j + 1].x, m[2 * j + 1].y, m[2 * j + 1].z, m[2 * j + 1].w};
-        store_eight<3>(sm + L::M + b * L::MB, kTileBytes, e >> 3, (e & 7) * 8, x);
-      }
+      for (int rb = 0; rb < RB; ++rb) wl[rb].put(sm + L::W + b * L::WB + rb * kTileBytes, ft, RB * kTileBytes);
+      if (PARTS > 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
+      kl.put(sm + L::K + b * L::KB, ft);
       fence_async();
       mbar_arrive(&full[b]);
     }
@@ -310,34 +375,28 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
         if (first && r < a.dk && c < a.dv) x = load_two(first + ((size_t)bh * a.dk + r) * a.dv + c);
         X[rb][i] = x.x, X[rb][i + 1] = x.y;
       }
-    // this chunk's rows of V (rev: Pᵀ O') and gates, loaded a chunk ahead
-    float ga[2], gb[2], gend = 0.f, B[16];
-    float2 raw_b[8];
-    float raw_g[2][3];
-    auto fetch = [&](int i) {
-      const int n = REV ? N - 1 - i : i, len = min(C, a.T - n * C);
-      const size_t chunk = (size_t)bh * N + n;
-      const float* gates = w.gates + chunk * kGates;
+    float* const rows_u = (REV ? w.R : w.U) + ((size_t)bh * N * C + r0) * DV + col + c0;
+    float* const rows_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col + c0;
+    const float* const gates = w.gates + (size_t)bh * N * kGates + r0;
+    // a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates, loaded a chunk ahead
+    float2 B[8];
+    float g[2][3], end;
+    auto fetch = [&](int n) {
+      const float* p = rows_u + (size_t)n * C * DV;
+      const float* q = gates + (size_t)n * kGates;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int t = r0 + 8 * e;
 #pragma unroll
-        for (int m = 0; m < 3; ++m) raw_g[e][m] = gates[(2 + m) * C + t];
-        const IO* v = reinterpret_cast<const IO*>(a.v) + ((size_t)bh * a.T + n * C + t) * a.dv + col + c0;
-        const float* p = w.R + (chunk * C + t) * DV + col + c0;
+        for (int j = 0; j < 4; ++j) B[2 * j + e] = load_two(p + 8 * e * DV + 8 * j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (REV) raw_b[2 * j + e] = load_two(p + 8 * j);
-          else raw_b[2 * j + e] = t < len && col + c0 + 8 * j < a.dv ? load_two(v + 8 * j) : make_float2(0.f, 0.f);
-        }
+        for (int m = 0; m < 3; ++m) g[e][m] = q[(2 + m) * C + 8 * e];
       }
-      return gates[2 * C + C - 1];
+      end = q[3 * C - 1 - r0];
     };
-    float next_end = fetch(0);
+    fetch(REV ? N - 1 : 0);
     for (int i = 0; i < N; ++i) {
-      const int n = REV ? N - 1 - i : i, b = i & 1;
+      const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
       const uint32_t parity = i & 1;
-      const size_t chunk = (size_t)bh * N + n;
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -346,21 +405,20 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       fence_async();
       fence_before();
       bar_sync(1, kChainThreads);
-      const Operand<PARTS, false> Kr{base + L::K + b * L::KB, RB * kTileBytes, kTileBytes};
+      const Operand<3, false> Wr{base + L::W + b * L::WB, RB * kTileBytes, kTileBytes};
       const Operand<PARTS, true> Kt{base + L::K + b * L::KB, RB * kTileBytes, kTileBytes};
-      const Operand<3, REV> Mx{base + L::M + b * L::MB, kTileBytes, kTileBytes};
-      const Operand<3, true> Xs{base + L::X, DK * 128, DK * 128}, Ws{base + L::W, kTileBytes, kTileBytes};
+      const Operand<3, true> Xs{base + L::X, DK * 128, DK * 128}, Us{base + L::U, kTileBytes, kTileBytes};
       if (warp == 0) {
-        mbar_wait(&full[b], (i >> 1) & 1, ok);
+        mbar_wait(&full[b], STAGES == 2 ? (i >> 1) & 1 : i & 1, ok);
         fence_after();
         if (elect()) {
-          mma<64, 64, DK>(tm, Kr, Xs);
+          mma<64, 64, DK>(tm, Wr, Xs);
           commit(&done[0]);
         }
       }
       // while that runs: the state goes out; in reverse its slot first gives up Qᵀ(G O')
       float F[REV ? RB : 1][16];
-      float* Xout = (REV ? w.Z : w.S) + chunk * DK * DV + col + c0;
+      float* Xout = rows_x + (size_t)n * DK * DV;
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -373,57 +431,33 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
             store_two(p, X[rb][e], X[rb][e + 1]);
           }
         }
-      gend = next_end;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float G = raw_g[e][0], E = raw_g[e][1], be = raw_g[e][2];
-        ga[e] = REV ? E : -be * G;  // Y's factor in W
-        gb[e] = REV ? -be * G : E;  // U's (dR's) on its way into X
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = raw_b[2 * j + e];
-          B[4 * j + 2 * e] = REV ? x.x : be * x.x, B[4 * j + 2 * e + 1] = REV ? x.y : be * x.y;
-        }
-      }
-      if (i + 1 < N) next_end = fetch(i + 1);
       float v[16];
       mbar_wait(&done[0], parity, ok);
       fence_after();
       tmem_load(tm + rows + 32 * half, v);
+      const float gend = end;
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
-        const int o = (e & 2) >> 1;
-        store_pair<3>(sm + L::W, kTileBytes, r0 + 8 * o, c0 + (e >> 2) * 8, fmaf(ga[o], v[e], B[e]),
-                      fmaf(ga[o], v[e + 1], B[e + 1]));
+        const int o = (e & 2) >> 1, j = e >> 2;
+        const float f = REV ? -g[o][2] * g[o][0] : g[o][1];  // −β G, or E
+        v[e] += B[2 * j + o].x, v[e + 1] += B[2 * j + o].y;
+        store_pair<3>(sm + L::U, kTileBytes, r0 + 8 * o, c0 + j * 8, f * v[e], f * v[e + 1]);
       }
       fence_async();
       fence_before();
       bar_sync(1, kChainThreads);
-      if (warp == 0 && elect()) {
+      if (warp == 0) {
         fence_after();
-        mma<64, 64, 64>(tm + 64, Mx, Ws);
-        commit(&done[1]);
+        if (elect()) {
+          mma<DK, 64, 64>(tm + 64, Kt, Us);
+          commit(&done[1]);
+          commit(&empty[b]);
+        }
       }
-      mbar_wait(&done[1], parity, ok);
-      fence_after();
-      tmem_load(tm + 64 + rows + 32 * half, v);
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const int o = (e & 2) >> 1;
-        store_pair<3>(sm + L::W, kTileBytes, r0 + 8 * o, c0 + (e >> 2) * 8, gb[o] * v[e], gb[o] * v[e + 1]);
-      }
-      fence_async();
-      fence_before();
-      bar_sync(1, kChainThreads);
-      if (warp == 0 && elect()) {
-        fence_after();
-        mma<DK, 64, 64>(tm + 128, Kt, Ws);
-        commit(&done[2]);
-        commit(&empty[b]);
-      }
-      float* Uout = (REV ? w.R : w.U) + (chunk * C + r0) * DV + col + c0;
+      float* Uout = rows_u + (size_t)n * C * DV;
 #pragma unroll
       for (int e = 0; e < 16; e += 2) store_two(Uout + (e & 2) * 4 * DV + (e >> 2) * 8, v[e], v[e + 1]);
+      if (i + 1 < N) fetch(REV ? n - 1 : n + 1);
       if (REV) {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
@@ -431,11 +465,11 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
           for (int e = 0; e < 16; e += 2)
             store_two(Xout + (xr[rb] + (e & 2) * 4) * DV + (e >> 2) * 8, X[rb][e], X[rb][e + 1]);
       }
-      mbar_wait(&done[2], parity, ok);
+      mbar_wait(&done[1], parity, ok);
       fence_after();
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        tmem_load(tm + 128 + rows + ((uint32_t)(16 * rb) << 16) + 32 * half, v);
+        tmem_load(tm + 64 + rows + ((uint32_t)(16 * rb) << 16) + 32 * half, v);
 #pragma unroll
         for (int e = 0; e < 16; ++e) X[rb][e] = fmaf(gend, X[rb][e], REV ? v[e] + F[REV ? rb : 0][e] : v[e]);
       }
@@ -455,7 +489,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   }
   fence_before();
   __syncthreads();
-  if (warp == 0) tmem_free(tm, 256);
+  if (warp == 0) tmem_free(tm, 128);
 }
 
 // ---- the output ----------------------------------------------------------------------
@@ -464,6 +498,7 @@ struct OutputSmem {
   static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, PN = sizeof(IO) == 2 ? 2 : 3;
   static constexpr int K = 0, Q = IN, S = 2 * IN, U = S + PN * DK * 128, P = U + PN * kTileBytes,
                        kBytes = P + PN * kTileBytes + 1024;
+  static_assert(kBytes <= kMaxBytes, "");
 };
 
 template <typename IO, int DK>
@@ -587,11 +622,12 @@ Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, boo
     return p;
   };
   Workspace w{};
-  w.M = take(n * C * C);
   w.gates = take(n * kGates);
+  w.W = take(n * C * DK);
   w.S = take(n * DK * DV);
   w.U = take(n * C * DV);
   if (backward) {
+    w.Wr = take(n * C * DK);
     w.Z = take(n * DK * DV);
     w.R = take(n * C * DV);
     if (Hk != H) w.part = take((size_t)B * H * T * 2 * dk);

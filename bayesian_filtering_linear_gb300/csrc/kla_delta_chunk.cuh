@@ -13,6 +13,7 @@ using namespace umma;
 constexpr int C = 64;             // tokens of a chunk
 constexpr int kThreads = 256;     // of the kernels that take a chunk each
 constexpr int kGates = 5 * C;     // floats: cumulative g in two floats, decay from the start, to the end, β
+constexpr int kMaxBytes = 227 * 1024 - 4096;  // shared memory of a block, less its static part
 constexpr float kMinLog = -104.f; // e^-104 is 0 in fp32: smaller logs change nothing but the sums' exactness
 
 template <typename IO>
@@ -22,12 +23,13 @@ __host__ __device__ constexpr int pad64(int d) { return d <= 64 ? 64 : 128; }
 
 // Per chunk of every value head, padded to whole chunks and to widths of 64.
 struct Workspace {
-  float* M;      // [chunks][64][64]: (I + A)^-1
   float* gates;  // [chunks][5][64]
+  float* W;      // [chunks][64][DK]: −M (β G K)
   float* S;      // [chunks][DK][DV]: the state before each chunk
-  float* U;      // [chunks][64][DV]
+  float* U;      // [chunks][64][DV]: first M (β V), then U
+  float* Wr;     // [chunks][64][DK]: Mᵀ (E K)
   float* Z;      // [chunks][DK][DV]: first Qᵀ(G O'), then the gradient of the state after each chunk
-  float* R;      // [chunks][64][DV]: first Pᵀ O', then dR
+  float* R;      // [chunks][64][DV]: first Mᵀ Pᵀ O', then dR
   float* part;   // [B·H][T][2][dk]: gradients of q and k by value head (shared key heads)
 };
 
@@ -118,13 +120,13 @@ struct PartsLoad {
     const float4 a = v[2 * j], b = v[2 * j + 1];
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
-  __device__ __forceinline__ void put(char* tile, int tid) const {
+  __device__ __forceinline__ void put(char* tile, int tid, int part = ROWS * 128) const {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int i = tid + j * THREADS;
       float x[8];
       eight(j, x);
-      store_eight<PARTS>(tile, ROWS * 128, i >> 3, (i & 7) * 8, x);
+      store_eight<PARTS>(tile, part, i >> 3, (i & 7) * 8, x);
     }
   }
 };
@@ -157,7 +159,7 @@ __device__ __forceinline__ char* align1024(char* p) {
 }
 
 Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, bool backward, size_t* bytes);
-// M, gates and, with d, Pᵀ O' and Qᵀ(G O') (in R and Z).
+// The gates, W and M (β V); with d also Wr, Mᵀ Pᵀ O' and Qᵀ(G O').
 cudaError_t launch_prepare(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, cudaStream_t s);
 // The states before the chunks and U (rev: the gradients of the states after them and dR), one block per head
 // and 64 columns.
