@@ -34,8 +34,9 @@ struct GradSmem {
                        kStage = S + PN * DK * 128;
   // once the products with S and Z are done: (dP P + dA A), then the masked dP, dA and β dA
   static constexpr int W = O, dP = O, dA = dP + ROWS, bA = dA + ROWS, kEnd = bA + ROWS;
-  static constexpr int kBytes = (kStage > kEnd ? kStage : kEnd) + 1024;
-  static_assert(W + 64 * 65 * 4 <= kBytes - 1024 && kBytes <= kMaxBytes, "");
+  static constexpr int kBytes = kStage > kEnd ? kStage : kEnd;
+  static constexpr int kBlocks = DK == 64 && kBytes <= 108 * 1024 ? 2 : 1;  // of an SM
+  static_assert(W + 64 * 65 * 4 <= kBytes && kBytes <= kMaxBytes, "");
 };
 
 // Per row of a fragment: the sum over its four lanes; lane 0 of the four keeps it.
@@ -45,13 +46,12 @@ __device__ __forceinline__ float row4(float x) {
 }
 
 template <typename IO, int DK>
-__global__ void __launch_bounds__(kThreads) kla_delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs d,
+__global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                  const Workspace w) {
   using L = GradSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
   constexpr int COLS = DK == 64 ? 256 : 512, SH = 3 * DK;      // TMEM: dQ, X, Y of DK columns, then 64 shared
-  extern __shared__ char raw[];
-  char* sm = align1024(raw);
+  extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ float hi[C], lo[C], G[C], E[C], be[C], rv[C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
@@ -337,12 +337,8 @@ __global__ void __launch_bounds__(256) kla_delta_share_kernel(const DeltaArgs a,
 
 template <typename IO, int DK>
 cudaError_t grad_dk(const DeltaArgs& a, const DeltaGradArgs& g, const Workspace& w, cudaStream_t s) {
-  const int smem = GradSmem<IO, DK>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(kla_delta_grad_kernel<IO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.T + C - 1) / C));
-  kla_delta_grad_kernel<IO, DK><<<blocks, kThreads, smem, s>>>(a, g, w);
-  return cudaGetLastError();
+  return run(kla_delta_grad_kernel<IO, DK>, GradSmem<IO, DK>::kBytes, blocks, kThreads, s, a, g, w);
 }
 
 }  // namespace

@@ -81,8 +81,9 @@ struct PrepareSmem {
   static constexpr int K = 0, Q = IN, MP = Q + (BWD ? IN : 0), P = MP + M3, T1 = P + (BWD ? M3 : 0), T2 = T1 + M3,
                        A = T1, M = A + kSquare;
   static constexpr int kTiles = BWD ? T2 + M3 : T1 + T, kEnd = kTiles > M + kSquare ? kTiles : M + kSquare;
-  static constexpr int kBytes = kEnd + 1024;
+  static constexpr int kBytes = kEnd;
   static_assert(kBytes <= kMaxBytes, "");
+  static constexpr int kBlocks = kBytes <= 74 * 1024 ? 3 : kBytes <= 112 * 1024 ? 2 : 1;  // of an SM
 };
 
 // 16 × 32 fragments of a product of W columns from TMEM to rows of fp32
@@ -101,15 +102,16 @@ __device__ __forceinline__ void drain(uint32_t tm, float* out, int ld, int quad,
 }
 
 template <typename IO, int DK, bool BWD>
-__global__ void __launch_bounds__(kThreads) kla_delta_prepare_kernel(const DeltaArgs a, const DeltaGradArgs d,
+__global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) kla_delta_prepare_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                     const Workspace w) {
   using L = PrepareSmem<IO, DK, BWD>;
   constexpr int PARTS = L::PARTS, COLS = BWD || DK == 128 ? 256 : 128, NB = DK / 64;
-  extern __shared__ char raw[];
-  char* sm = align1024(raw);
-  __shared__ float hi[C], lo[C], G[C], E[C], be[C];
+  extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
+  __shared__ float G[C], E[C], be[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
+  float* hi = reinterpret_cast<float*>(sm + L::MP);  // until M comes
+  float* lo = hi + C;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Where at = where(a, blockIdx.x);
   const int DV = pad64(a.dv);
@@ -306,7 +308,7 @@ struct ChainSmem {
   static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, WB = 3 * DK / 64 * kTileBytes;
   static constexpr int STAGES = sizeof(IO) == 4 && DK == 128 ? 1 : 2;
   static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + 3 * DK * 128,
-                       kBytes = U + 3 * kTileBytes + 1024;
+                       kBytes = U + 3 * kTileBytes;
   static_assert(kBytes <= kMaxBytes, "");
 };
 
@@ -316,8 +318,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
                                                                                       const Workspace w) {
   using L = ChainSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES;
-  extern __shared__ char raw[];
-  char* sm = align1024(raw);
+  extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ uint64_t full[STAGES], empty[STAGES], done[2];
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -497,7 +498,7 @@ template <typename IO, int DK>
 struct OutputSmem {
   static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, PN = sizeof(IO) == 2 ? 2 : 3;
   static constexpr int K = 0, Q = IN, S = 2 * IN, U = S + PN * DK * 128, P = U + PN * kTileBytes,
-                       kBytes = P + PN * kTileBytes + 1024;
+                       kBytes = P + PN * kTileBytes;
   static_assert(kBytes <= kMaxBytes, "");
 };
 
@@ -505,8 +506,7 @@ template <typename IO, int DK>
 __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaArgs a, const Workspace w) {
   using L = OutputSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN;
-  extern __shared__ char raw[];
-  char* sm = align1024(raw);
+  extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ float hi[C], lo[C], G[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
@@ -580,14 +580,6 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   fence_before();
   __syncthreads();
   if (warp == 0) tmem_free(tm, 128);
-}
-
-template <typename F, typename... Args>
-cudaError_t run(F kernel, int smem, unsigned blocks, int threads, cudaStream_t s, const Args&... args) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kernel<<<blocks, threads, smem, s>>>(args...);
-  return cudaGetLastError();
 }
 
 unsigned chunks(const DeltaArgs& a) { return (unsigned)((long long)a.B * a.H * ((a.T + C - 1) / C)); }

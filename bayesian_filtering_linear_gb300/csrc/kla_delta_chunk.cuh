@@ -154,8 +154,16 @@ __device__ __forceinline__ Where where(const DeltaArgs& a, long long chunk) {
   return w;
 }
 
-__device__ __forceinline__ char* align1024(char* p) {
-  return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 1023) / 1024 * 1024);
+// Launches with dynamic shared memory; all of an SM's L1 is asked for as shared memory, so that as many blocks fit as
+// their sizes allow.
+template <typename F, typename... Args>
+cudaError_t run(F kernel, int smem, unsigned blocks, int threads, cudaStream_t s, const Args&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  kernel<<<blocks, threads, smem, s>>>(args...);
+  return cudaGetLastError();
 }
 
 Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, bool backward, size_t* bytes);
