@@ -26,65 +26,85 @@ namespace delta {
 
 namespace {
 
-// dst[n×n] = ± a·b for n = 16 or 32, all with row length 68; four columns a task.
-__device__ __forceinline__ void small_matmul(float* dst, const float* a, const float* b, int n, bool neg, int task) {
-  const int i = task / (n / 4), j = task % (n / 4) * 4;
+// Four columns j of row i of ± a·b, over k in [k0, k1): matrices of row length 68, k0 and k1 multiples of four.
+__device__ __forceinline__ void four_columns(float* dst, const float* a, const float* b, int i, int j, int k0, int k1,
+                                             float sign) {
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) {
-    const float x = a[i * 68 + k];
-    const float4 y = *reinterpret_cast<const float4*>(b + k * 68 + j);
-    s.x = fmaf(x, y.x, s.x);
-    s.y = fmaf(x, y.y, s.y);
-    s.z = fmaf(x, y.z, s.z);
-    s.w = fmaf(x, y.w, s.w);
+#pragma unroll 4
+  for (int k = k0; k < k1; k += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(a + i * 68 + k);
+    const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 y = *reinterpret_cast<const float4*>(b + (k + e) * 68 + j);
+      s.x = fmaf(f[e], y.x, s.x);
+      s.y = fmaf(f[e], y.y, s.y);
+      s.z = fmaf(f[e], y.z, s.z);
+      s.w = fmaf(f[e], y.w, s.w);
+    }
   }
-  if (neg) s = make_float4(-s.x, -s.y, -s.z, -s.w);
-  *reinterpret_cast<float4*>(dst + i * 68 + j) = s;
+  *reinterpret_cast<float4*>(dst + i * 68 + j) = make_float4(sign * s.x, sign * s.y, sign * s.z, sign * s.w);
 }
 
 // M = (I + A)^-1 for A strictly lower, 64 × 64 with row length 68: substitution in the 16 × 16 blocks on the diagonal,
-// then [[X, 0], [L, Y]]^-1 = [[X', 0], [−Y' L X', Y']] for 32 and 64. L X' goes where A's upper blocks would be.
-__device__ void invert(float* A, float* M, int tid) {
-  if (tid < 64) {
-    const int b = tid & 48, c = tid & 15;
+// then [[X, 0], [L, Y]]^-1 = [[X', 0], [−Y' L X', Y']] for 32 and 64 (X', Y' lower triangular, so the sums start at the
+// column or end at the row). L X' goes where A's upper blocks would be. Powers of A are not used: they grow like
+// binomials where keys repeat.
+__device__ void invert(float* A, float* M, int warp, int lane) {
+  if (warp < 2) {
+    const int b = warp * 32 + (lane & 16), c = lane & 15;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       x[i] = i == c ? 1.f : 0.f;
 #pragma unroll
-      for (int s = 0; s < i; ++s) x[i] = fmaf(-A[(b + i) * 68 + b + s], x[s], x[i]);
+      for (int s = 0; s < i; s += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(A + (b + i) * 68 + b + s);  // zero from column i on
+        x[i] = fmaf(-y.x, x[s], x[i]);
+        if (s + 1 < i) x[i] = fmaf(-y.y, x[s + 1], x[i]);
+        if (s + 2 < i) x[i] = fmaf(-y.z, x[s + 2], x[i]);
+        if (s + 3 < i) x[i] = fmaf(-y.w, x[s + 3], x[i]);
+      }
       M[(b + i) * 68 + b + c] = x[i];
     }
   } else {
-    for (int i = tid - 64; i < 64 * 64; i += kThreads - 64)
-      if ((i >> 10) != ((i & 63) >> 4)) M[(i >> 6) * 68 + (i & 63)] = 0.f;
+    for (int i = (warp - 2) * 32 + lane; i < 64 * 16; i += kThreads - 64) {
+      const int r = i >> 4, c = (i & 15) * 4;
+      if ((r >> 4) != (c >> 4)) *reinterpret_cast<float4*>(M + r * 68 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
   __syncthreads();
-#pragma unroll
-  for (int n = 16; n <= 32; n *= 2) {
-    const int tasks = n * n / 4, p = tid / tasks, o = p * 2 * n * 68 + p * 2 * n;  // pair p of blocks
-    const bool mine = p < 32 / n;
-    if (mine) small_matmul(A + o + n, A + o + n * 68, M + o, n, false, tid % tasks);
-    __syncthreads();
-    if (mine) small_matmul(M + o + n * 68, M + o + n * 68 + n, A + o + n, n, true, tid % tasks);
-    __syncthreads();
-  }
+  const int o = (warp >> 1) * (32 * 68 + 32), i16 = lane & 15, j16 = ((warp & 1) * 2 + (lane >> 4)) * 4;  // two pairs of 16
+  if (warp < 4) four_columns(A + o + 16, A + o + 16 * 68, M + o, i16, j16, j16, 16, 1.f);
+  __syncthreads();
+  if (warp < 4) four_columns(M + o + 16 * 68, M + o + 16 * 68 + 16, A + o + 16, i16, j16, 0, 16, -1.f);
+  __syncthreads();
+  four_columns(A + 32, A + 32 * 68, M, lane, warp * 4, warp * 4, 32, 1.f);
+  __syncthreads();
+  four_columns(M + 32 * 68, M + 32 * 68 + 32, A + 32, warp * 4 + (lane >> 3), (lane & 7) * 4, 0, warp * 4 + 4, -1.f);
+  __syncthreads();
 }
 
 template <typename IO, int DK, bool BWD>
 struct PrepareSmem {
   static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes, M3 = 3 * kTileBytes, T = DK / 64 * M3;
-  static constexpr int kSquare = 64 * 68 * 4;
-  // K is last used before O comes in its place; A and M in fp32 are done with before the tiles T1 and T2
-  // (β G K and E K for DK = 128 fill both, one after the other)
-  static constexpr int K = 0, Q = IN, MP = Q + (BWD ? IN : 0), P = MP + M3, T1 = P + (BWD ? M3 : 0), T2 = T1 + M3,
-                       A = T1, M = A + kSquare;
-  static constexpr int kTiles = BWD ? T2 + M3 : T1 + T, kEnd = kTiles > M + kSquare ? kTiles : M + kSquare;
-  static constexpr int kBytes = kEnd;
+  static_assert(64 * 68 * 4 <= M3, "");
+  // T1 and T2: tiles on their way into products with M; T1 first holds M in fp32 (and forward K, for one product), MP
+  // first A. β G K and E K for DK = 128 fill both, one after the other. In the backward pass O takes K's place.
+  static constexpr int Q = 0, K = BWD ? IN : 0, P = 2 * IN, T1 = BWD ? P + M3 : 0, T2 = T1 + M3,
+                       MP = BWD ? T2 + M3 : T1 + (T > IN ? T : IN), M = T1, A = MP;
+  static constexpr int kBytes = MP + M3;
   static_assert(kBytes <= kMaxBytes, "");
-  static constexpr int kBlocks = kBytes <= 74 * 1024 ? 3 : kBytes <= 112 * 1024 ? 2 : 1;  // of an SM
+  static constexpr int kBlocks = kBytes <= 53 * 1024 ? 4 : kBytes <= 72 * 1024 ? 3 : kBytes <= 112 * 1024 ? 2 : 1;  // of an SM
 };
+
+// (h + l) += (yh + yl), the sum again as two floats
+__device__ __forceinline__ void add_two(float& h, float& l, float yh, float yl) {
+  const float s = h + yh, t = s - h;
+  const float e = ((h - (s - t)) + (yh - t)) + (l + yl);
+  h = s + e;
+  l = e - (h - s);
+}
 
 // 16 × 32 fragments of a product of W columns from TMEM to rows of fp32
 template <int W, int ROWS>
@@ -110,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   __shared__ float G[C], E[C], be[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
-  float* hi = reinterpret_cast<float*>(sm + L::MP);  // until M comes
+  float* hi = reinterpret_cast<float*>(sm + L::A + 64 * 68 * 4);  // behind A, until MP comes
   float* lo = hi + C;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Where at = where(a, blockIdx.x);
@@ -125,32 +145,34 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   }
   if (warp == 0) tmem_alloc(&slot, COLS);
   if (tid == 32) mbar_init(&bar, 1);
-  if (warp == 2) {  // the gates: two tokens a lane
-    double x[2];
-    float b[2];
+  if (warp == 2) {  // the gates: two tokens a lane, cumulative logs as sums of two floats
+    float gh[2], gl[2] = {}, b[2];
     const size_t row = (size_t)at.bh * a.T + at.t0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const bool in = t < at.len;
       const float g = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.g)[row + t]) : 0.f;
-      x[i] = g < kMinLog ? kMinLog : g;
+      gh[i] = g < kMinLog ? kMinLog : g;
       b[i] = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.beta)[row + t]) : 0.f;
     }
-    x[1] += x[0];
-    double sum = x[1];
+    add_two(gh[1], gl[1], gh[0], gl[0]);
+    float sh = gh[1], sl = gl[1];  // sums over the lanes up to this one
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const double y = __shfl_up_sync(~0u, sum, m);
-      if (lane >= m) sum += y;
+      const float yh = __shfl_up_sync(~0u, sh, m), yl = __shfl_up_sync(~0u, sl, m);
+      if (lane >= m) add_two(sh, sl, yh, yl);
     }
-    const double before = __shfl_up_sync(~0u, sum, 1), total = __shfl_sync(~0u, sum, 31);
+    const float th = __shfl_sync(~0u, sh, 31), tl = __shfl_sync(~0u, sl, 31);
+    float ph = __shfl_up_sync(~0u, sh, 1), pl = __shfl_up_sync(~0u, sl, 1);
+    if (lane == 0) ph = pl = 0.f;
     float* out = w.gates + at.chunk * kGates;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
-      const double c = lane ? before + x[i] : x[i];
-      const float h = (float)c, l = (float)(c - h), g = expf(h) * (1.f + l), e = expf((float)(total - c));
+      float h = ph, l = pl;
+      add_two(h, l, gh[i], gl[i]);
+      const float g = expf(h) * (1.f + l), e = expf((th - h) + (tl - l));
       hi[t] = h, lo[t] = l, G[t] = g, E[t] = e, be[t] = b[i];
       out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = e, out[4 * C + t] = b[i];
     }
@@ -191,29 +213,33 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   finish();
   float v[16];
   tmem_load(tm + rows + 32 * half, v);
+  const bool below = 32 * half <= 16 * quad + 15;  // some of the warp's fragment is on or under the diagonal
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8 + (i & 1);
-    A[t * 68 + s] = s < t ? be[t] * decay(hi, lo, t, s) * v[i] : 0.f;
+  for (int i = 0; i < 16; i += 2) {
+    const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
+    float2 D = make_float2(0.f, 0.f);
+    if (below) D = make_float2(decay(hi, lo, t, s), decay(hi, lo, t, s + 1));
+    store_two(A + t * 68 + s, s < t ? be[t] * D.x * v[i] : 0.f, s + 1 < t ? be[t] * D.y * v[i + 1] : 0.f);
+    if (BWD) v[i] = D.x, v[i + 1] = D.y;
   }
   if (BWD) {  // P, scaled
-    tmem_load(tm + 64 + rows + 32 * half, v);
+    float y[16];
+    tmem_load(tm + 64 + rows + 32 * half, y);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
-      const float x = s <= t ? a.scale * decay(hi, lo, t, s) * v[i] : 0.f;
-      const float y = s + 1 <= t ? a.scale * decay(hi, lo, t, s + 1) * v[i + 1] : 0.f;
-      store_pair<3>(sm + L::P, kTileBytes, t, s, x, y);
+      store_pair<3>(sm + L::P, kTileBytes, t, s, s <= t ? a.scale * v[i] * y[i] : 0.f,
+                    s + 1 <= t ? a.scale * v[i + 1] * y[i + 1] : 0.f);
     }
   }
   __syncthreads();
-  invert(A, M, tid);
+  invert(A, M, warp, lane);
   for (int i = tid; i < C * 8; i += kThreads) {
     const float4* p = reinterpret_cast<const float4*>(M + (i >> 3) * 68 + (i & 7) * 8);
     float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
     store_eight<3>(sm + L::MP, kTileBytes, i >> 3, (i & 7) * 8, x);
   }
-  __syncthreads();
+  __syncthreads();  // M's place is free
   // rows of an input times a factor, as three parts
   auto scaled = [&](auto& tile, int W, char* to, int part, auto factor) {
 #pragma unroll

@@ -131,9 +131,10 @@ struct PartsLoad {
   }
 };
 
-// Decay from token s to token t ≥ s of a chunk.
+// Decay from token s to token t ≥ s of a chunk (for s > t some number, without overflow).
 __device__ __forceinline__ float decay(const float* hi, const float* lo, int t, int s) {
-  return expf((hi[t] - hi[s]) + (lo[t] - lo[s]));
+  const float x = (hi[t] - hi[s]) + (lo[t] - lo[s]);
+  return expf(s > t ? 0.f : x);
 }
 
 // Everything of a block that starts a chunk: which one, and its rows.
