@@ -45,6 +45,20 @@ __device__ __forceinline__ float row4(float x) {
   return x + __shfl_xor_sync(~0u, x, 2);
 }
 
+// Columns c and c + 1 of row r of a tile of parts.
+template <int PARTS>
+__device__ __forceinline__ float2 tile_two(const char* tile, int part, int r, int c) {
+  const char* p = tile + (c >> 6) * kTileBytes + r * 128 + ((((c >> 3) ^ r) & 7) << 4) + (c & 7) * 2;
+  float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = PARTS - 1; i >= 0; --i) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p + i * part);
+    x.x += __uint_as_float(u << 16);
+    x.y += __uint_as_float(u & 0xffff0000u);
+  }
+  return x;
+}
+
 template <typename IO, int DK>
 __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                  const Workspace w) {
@@ -52,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
   constexpr int COLS = DK == 64 ? 256 : 512, SH = 3 * DK;      // TMEM: dQ, X, Y of DK columns, then 64 shared
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
-  __shared__ float hi[C], lo[C], G[C], E[C], be[C], rv[C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
+  __shared__ float hi[C], lo[C], G[C], E[C], be[C], rv[2][C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -72,7 +86,6 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   if (tid < C) {
     const float* g = w.gates + at.chunk * kGates + tid;
     hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C], E[tid] = g[3 * C], be[tid] = g[4 * C];
-    rv[tid] = 0.f;
   }
   {
     TileLoad<IO, DK, kThreads> kl, ql;
@@ -104,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     __syncthreads();
     fence_after();
   };
-  const int quad = warp & 3, half = warp >> 2, r0 = 16 * quad + (lane >> 2), c0 = 32 * half + 2 * (lane & 3);
+  const Lanes l(tid);
+  const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
   // entries (t, s), (t, s + 1) of a 64 × 64 fragment at index e of 16
   auto row_of = [&](int e) { return r0 + (e & 2) * 4; };
@@ -115,42 +129,26 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     mma<64, 64, DK>(tm + 64, Qr, Kr);
     commit(&bar);
   }
-  float kk[16], qk[16], v[16];
+  float kk[16], qk[16], v[16], rdot[2] = {};
   finish();
   tmem_load(tm + rows + 32 * half, kk);
   tmem_load(tm + 64 + rows + 32 * half, qk);
   // products with U, S: dP, dA before masks, dQ = O' Sᵀ, X = dR Sᵀ (dP and dA wait in the shared columns and in Y's)
   for (int sl = 0; sl < slices; ++sl) {
-    TileLoad<IO, 64, kThreads> ol, vl;
-    PartsLoad<PN, C, kThreads> ul, rl;
-    PartsLoad<PN, DK, kThreads> xl;
-    rl.fetch(Rw + sl * 64, DV, tid);
-    vl.fetch(v_in, at.len, a.dv, sl * 64, tid);
+    TileLoad<IO, 64, kThreads> ol;
+    Fragment ul, rl, xl[NB], vl;
+    rl.load(Rw + sl * kBlock, tid);
     ol.fetch(go ? go : v_in, go ? at.len : 0, a.dv, sl * 64, tid);
-    ul.fetch(Uw + sl * 64, DV, tid);
-    xl.fetch(Sw + sl * 64, DV, tid);
+    ul.load(Uw + sl * kBlock, tid);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) xl[nb].load(Sw + (sl * NB + nb) * kBlock, tid);
+    load_rows(v_in, l, sl * 64, at.len, a.dv, vl.v);
     if (sl) finish();
-#pragma unroll
-    for (int n = 0; n < rl.N; ++n) {  // dR, and what comes of it alone
-      const int i = tid + n * kThreads, r = i >> 3, c = (i & 7) * 8, j = sl * 64 + c;
-      float x[8], y[8], dot = 0.f;
-      rl.eight(n, x);
-      vl.eight(n, y);
-      if (r < at.len && j < a.dv) {
-        IO* gv = reinterpret_cast<IO*>(d.gv) + (vrow + r) * a.dv + j;
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) store_two(gv + e, be[r] * x[e], be[r] * x[e + 1]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dot = fmaf(x[e], y[e], dot);
-      dot = row4(dot);
-      dot += __shfl_xor_sync(~0u, dot, 4);
-      if ((lane & 7) == 0) rv[r] += dot;
-      store_eight<PN>(sm + L::R, kTileBytes, r, c, x);
-    }
     ol.put(sm + L::O, tid);
-    ul.put(sm + L::U, tid);
-    xl.put(sm + L::S, tid);
+    ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
+    rl.put<PN>(sm + L::R, kTileBytes, l.r, l.c);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) xl[nb].put<PN>(sm + L::S, DK * 128, block_row<DK>(l, nb), l.c);
     publish();
     if (warp == 0 && elect()) {
       mma<64, 64, 64>(tm + SH, Or, Ur, sl > 0);
@@ -159,6 +157,14 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
       mma<64, DK, 64>(tm + DK, Rr, Sr, sl > 0);
       commit(&bar);
     }
+    // while that runs, what comes of dR alone
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int o = (e & 2) >> 1;
+      rdot[o] = fmaf(rl.v[e], vl.v[e], rdot[o]);
+      rl.v[e] *= be[r0 + 8 * o];
+    }
+    store_rows(reinterpret_cast<IO*>(d.gv) + vrow * a.dv, l, sl * 64, at.len, a.dv, rl.v);
   }
   float gp[16], ga[16];
   finish();
@@ -168,18 +174,18 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   // Y = U Zᵀ, and <Z, S>
   float z = 0.f;
   for (int sl = 0; sl < slices; ++sl) {
-    PartsLoad<PN, C, kThreads> ul;
-    PartsLoad<PN, DK, kThreads> xl, zl;
-    if (slices > 1) ul.fetch(Uw + sl * 64, DV, tid);
-    zl.fetch(Zw + sl * 64, DV, tid);
-    xl.fetch(Sw + sl * 64, DV, tid);
-    if (sl) finish();
-    if (slices > 1) ul.put(sm + L::U, tid);
-    zl.put(sm + L::S, tid);
+    Fragment ul, zl[NB], xl;
+    if (slices > 1) ul.load(Uw + sl * kBlock, tid);
 #pragma unroll
-    for (int j = 0; j < 2 * xl.N; ++j) {
-      const float4 x = xl.v[j], y = zl.v[j];
-      z += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+    for (int nb = 0; nb < NB; ++nb) zl[nb].load(Zw + (sl * NB + nb) * kBlock, tid);
+    if (sl) finish();
+    if (slices > 1) ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      xl.load(Sw + (sl * NB + nb) * kBlock, tid);
+      zl[nb].put<PN>(sm + L::S, DK * 128, block_row<DK>(l, nb), l.c);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z = fmaf(xl.v[e], zl[nb].v[e], z);
     }
     publish();
     if (warp == 0 && elect()) {
@@ -211,8 +217,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
       const int t = row_of(e), o = (e & 2) >> 1, c = cb + 2 * (lane & 3) + (e >> 2) * 8;
-      float2 kv = make_float2(0.f, 0.f), qv = kv;
-      if (t < at.len && c < a.dk) kv = load_two(k + (size_t)t * a.dk + c), qv = load_two(q + (size_t)t * a.dk + c);
+      const float2 kv = tile_two<PARTS>(sm + L::K, NB * kTileBytes, t, c), qv = tile_two<PARTS>(sm + L::Q, NB * kTileBytes, t, c);
       const float f[3] = {a.scale * G[t], -G[t], E[t]};
 #pragma unroll
       for (int m = 0; m < 3; ++m) acc[m][nb][e] *= f[m], acc[m][nb][e + 1] *= f[m];
@@ -225,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   for (int o = 0; o < 2; ++o) {
     const int t = r0 + 8 * o;
     const float f = row4(fmaf(be[t], ax[o], aq[o])), x = row4(ay[o]);
-    if ((lane & 3) == 0) from[half][t] = f, to[half][t] = x;
+    const float y = row4(rdot[o]);
+    if ((lane & 3) == 0) from[half][t] = f, to[half][t] = x, rv[half][t] = y;
   }
   float* W = reinterpret_cast<float*>(sm + L::W);
 #pragma unroll
@@ -292,20 +298,27 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
       const int t = row_of(e), o = (e & 2) >> 1, c = cb + 2 * (lane & 3) + (e >> 2) * 8;
-      if (t >= at.len || c >= a.dk) continue;
-      const float2 kv = load_two(k + (size_t)t * a.dk + c);
-      const float x = acc[1][nb][e], y = acc[1][nb][e + 1];
-      ax[o] += x * kv.x + y * kv.y;
-      const float dq[2] = {acc[0][nb][e] + bad, acc[0][nb][e + 1] + bad};
-      const float dk[2] = {fmaf(be[t], x, acc[2][nb][e]) + bad, fmaf(be[t], y, acc[2][nb][e + 1]) + bad};
-      if (w.part) {
-        float* p = w.part + (vrow + t) * 2 * a.dk + c;
-        store_two(p, dq[0], dq[1]);
-        store_two(p + a.dk, dk[0], dk[1]);
-      } else {
-        store_two(reinterpret_cast<IO*>(d.gq) + (krow + t) * a.dk + c, dq[0], dq[1]);
-        store_two(reinterpret_cast<IO*>(d.gk) + (krow + t) * a.dk + c, dk[0], dk[1]);
+      const float2 kv = tile_two<PARTS>(sm + L::K, NB * kTileBytes, t, c);
+      float *x = acc[1][nb] + e, *y = acc[2][nb] + e;
+      ax[o] += x[0] * kv.x + x[1] * kv.y;
+      y[0] = fmaf(be[t], x[0], y[0]) + bad;
+      y[1] = fmaf(be[t], x[1], y[1]) + bad;
+      acc[0][nb][e] += bad;
+      acc[0][nb][e + 1] += bad;
+    }
+    const int cs = cb - 32 * half;  // store_rows counts the half's 32 columns itself
+    if (w.part) {
+      float* p = w.part + vrow * 2 * a.dk;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const int t = row_of(e), c = cb + 2 * (lane & 3) + (e >> 2) * 8;
+        if (t >= at.len || c >= a.dk) continue;
+        store_two(p + (size_t)t * 2 * a.dk + c, acc[0][nb][e], acc[0][nb][e + 1]);
+        store_two(p + (size_t)t * 2 * a.dk + a.dk + c, acc[2][nb][e], acc[2][nb][e + 1]);
       }
+    } else {
+      store_rows(reinterpret_cast<IO*>(d.gq) + krow * a.dk, l, cs, at.len, a.dk, acc[0][nb]);
+      store_rows(reinterpret_cast<IO*>(d.gk) + krow * a.dk, l, cs, at.len, a.dk, acc[2][nb]);
     }
   }
 #pragma unroll
@@ -315,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   }
   fence_before();
   __syncthreads();
-  if (tid < at.len) reinterpret_cast<IO*>(d.gbeta)[vrow + tid] = from_f32<IO>(rv[tid] + kx[0][tid] + kx[1][tid] + bad);
+  if (tid < at.len) reinterpret_cast<IO*>(d.gbeta)[vrow + tid] = from_f32<IO>(rv[0][tid] + rv[1][tid] + kx[0][tid] + kx[1][tid] + bad);
   if (warp == 0) tmem_free(tm, COLS);
 }
 

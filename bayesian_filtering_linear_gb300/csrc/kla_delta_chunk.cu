@@ -106,19 +106,17 @@ __device__ __forceinline__ void add_two(float& h, float& l, float yh, float yl) 
   l = e - (h - s);
 }
 
-// 16 × 32 fragments of a product of W columns from TMEM to rows of fp32
-template <int W, int ROWS>
-__device__ __forceinline__ void drain(uint32_t tm, float* out, int ld, int quad, int half, int lane, float bad) {
-  float v[16];
+// Blocks of a product from TMEM: `BLOCKS` of them across columns (ROWS = 64) or down 128 rows
+template <int ROWS, int BLOCKS>
+__device__ __forceinline__ void drain(uint32_t tm, float* out, const Lanes& l, int tid, float bad) {
 #pragma unroll
-  for (int rb = 0; rb < ROWS / 64; ++rb)
+  for (int b = 0; b < BLOCKS; ++b) {
+    Fragment f;
+    tmem_load(tm + ((uint32_t)(32 * l.quad + (ROWS == 64 ? 0 : 16 * b)) << 16) + (ROWS == 64 ? 64 * b : 0) + 32 * l.half, f.v);
 #pragma unroll
-    for (int cb = 0; cb < W / 64; ++cb) {
-      tmem_load(tm + ((uint32_t)(32 * quad + 16 * rb) << 16) + 64 * cb + 32 * half, v);
-      const int r = (ROWS == 64 ? 16 * quad : 32 * quad + 16 * rb) + (lane >> 2), c = 64 * cb + 32 * half + 2 * (lane & 3);
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) store_two(out + (r + (i & 2) * 4) * ld + c + (i >> 2) * 8, v[i] + bad, v[i + 1] + bad);
-    }
+    for (int i = 0; i < 16; ++i) f.v[i] += bad;
+    f.store(out + b * kBlock, tid);
+  }
 }
 
 template <typename IO, int DK, bool BWD>
@@ -206,7 +204,8 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   }
   float* A = reinterpret_cast<float*>(sm + L::A);
   float* M = reinterpret_cast<float*>(sm + L::M);
-  const int quad = warp & 3, half = warp >> 2, r0 = 16 * quad + (lane >> 2), c0 = 32 * half + 2 * (lane & 3);
+  const Lanes l(tid);
+  const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
   TileLoad<IO, 64, kThreads> vl;
   vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, 0, tid);
@@ -272,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
     finish();
   }
   float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
-  drain<DK, 64>(tm, w.W + at.chunk * C * DK, DK, quad, half, lane, bad);
-  if (BWD) drain<DK, 64>(tm + DK, w.Wr + at.chunk * C * DK, DK, quad, half, lane, bad);
+  drain<64, NB>(tm, w.W + at.chunk * C * DK, l, tid, bad);
+  if (BWD) drain<64, NB>(tm + DK, w.Wr + at.chunk * C * DK, l, tid, bad);
   for (int sl = 0; sl < DV / 64; ++sl) {
     if (sl) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, sl * 64, tid);
     if (!BWD) {
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
         commit(&bar);
       }
       finish();
-      drain<64, 64>(tm, w.U + at.chunk * C * DV + sl * 64, DV, quad, half, lane, 0.f);
+      drain<64, 1>(tm, w.U + at.chunk * C * DV + sl * kBlock, l, tid, 0.f);
     } else {
       const IO* go = reinterpret_cast<const IO*>(d.go);
       TileLoad<IO, 64, kThreads> ol;
@@ -309,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
         mma<64, 64, 64>(tm + 192, Mt, V1);
         commit(&bar);
       }
-      drain<64, 64>(tm, w.U + at.chunk * C * DV + sl * 64, DV, quad, half, lane, 0.f);
-      drain<64, DK>(tm + 128, w.Z + at.chunk * DK * DV + sl * 64, DV, quad, half, lane, 0.f);
+      drain<64, 1>(tm, w.U + at.chunk * C * DV + sl * kBlock, l, tid, 0.f);
+      drain<DK, NB>(tm + 128, w.Z + at.chunk * DK * DV + sl * NB * kBlock, l, tid, 0.f);
       finish();
       bad = ok ? 0.f : __int_as_float(0x7fc00000);
-      drain<64, 64>(tm + 192, w.R + at.chunk * C * DV + sl * 64, DV, quad, half, lane, bad);
+      drain<64, 1>(tm + 192, w.R + at.chunk * C * DV + sl * kBlock, l, tid, bad);
     }
   }
   fence_before();
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ uint64_t full[STAGES], empty[STAGES], done[2];
   __shared__ uint32_t slot;
-  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5);
   const int DV = pad64(a.dv), N = (a.T + C - 1) / C;
   const long long bh = blockIdx.x / (DV / 64);
   const int col = (int)(blockIdx.x % (DV / 64)) * 64;
@@ -371,64 +370,61 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
       const uint32_t before = STAGES == 2 ? ((i >> 1) - 1) & 1 : (i - 1) & 1;
       TileLoad<IO, DK, kFeedThreads> kl;
-      PartsLoad<3, C, kFeedThreads> wl[RB];
+      Fragment f[RB][2];  // what the threads of the two halves of columns hold
       // what registers hold comes in ahead of the wait for its place
-      wl[0].fetch(W + (size_t)n * C * DK, DK, ft);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f[rb][h].load(W + (size_t)n * C * DK + rb * kBlock, ft + h * kFeedThreads);
       if (PARTS == 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
-      if (RB > 1) wl[RB - 1].fetch(W + (size_t)n * C * DK + 64, DK, ft);
       if (i >= STAGES) mbar_wait(&empty[b], before, ok);
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) wl[rb].put(sm + L::W + b * L::WB + rb * kTileBytes, ft, RB * kTileBytes);
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const Lanes l(ft + h * kFeedThreads);
+          f[rb][h].put<3>(sm + L::W + b * L::WB + rb * kTileBytes, RB * kTileBytes, l.r, l.c);
+        }
       if (PARTS > 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
       kl.put(sm + L::K + b * L::KB, ft);
       fence_async();
       mbar_arrive(&full[b]);
     }
   } else {
-    const int quad = warp & 3, half = warp >> 2;
-    const int r0 = 16 * quad + (lane >> 2), c0 = 32 * half + 2 * (lane & 3);
-    const uint32_t rows = (uint32_t)(32 * quad) << 16;
-    int xr[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) xr[rb] = (DK == 64 ? 16 * quad : 32 * quad + 16 * rb) + (lane >> 2);
-    float X[RB][16];
+    const Lanes l(tid);
+    const uint32_t rows = ((uint32_t)(32 * l.quad) << 16) + 32 * l.half;
+    Fragment X[RB];
     const float* first = REV ? d.gstateT : a.state0;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const int r = xr[rb] + (i & 2) * 4, c = col + c0 + (i >> 2) * 8;
+      for (int e = 0; e < 16; e += 2) {
+        const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = col + l.c + (e >> 2) * 8;
         float2 x = make_float2(0.f, 0.f);
         if (first && r < a.dk && c < a.dv) x = load_two(first + ((size_t)bh * a.dk + r) * a.dv + c);
-        X[rb][i] = x.x, X[rb][i + 1] = x.y;
+        X[rb].v[e] = x.x, X[rb].v[e + 1] = x.y;
       }
-    float* const rows_u = (REV ? w.R : w.U) + ((size_t)bh * N * C + r0) * DV + col + c0;
-    float* const rows_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col + c0;
-    const float* const gates = w.gates + (size_t)bh * N * kGates + r0;
+    float* const blocks_u = (REV ? w.R : w.U) + (size_t)bh * N * C * DV + col * 64;
+    float* const blocks_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col * DK;
+    const float* const gates = w.gates + (size_t)bh * N * kGates;
     // a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates, loaded a chunk ahead
-    float2 B[8];
+    Fragment B;
     float g[2][3], end;
     auto fetch = [&](int n) {
-      const float* p = rows_u + (size_t)n * C * DV;
       const float* q = gates + (size_t)n * kGates;
+      B.load(blocks_u + (size_t)n * C * DV, tid);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) B[2 * j + e] = load_two(p + 8 * e * DV + 8 * j);
-#pragma unroll
-        for (int m = 0; m < 3; ++m) g[e][m] = q[(2 + m) * C + 8 * e];
-      }
-      end = q[3 * C - 1 - r0];
+        for (int m = 0; m < 3; ++m) g[o][m] = q[(2 + m) * C + l.r + 8 * o];
+      end = q[3 * C - 1];
     };
     fetch(REV ? N - 1 : 0);
     for (int i = 0; i < N; ++i) {
       const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
       const uint32_t parity = i & 1;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          store_pair<3>(sm + L::X, DK * 128, xr[rb] + (e & 2) * 4, c0 + (e >> 2) * 8, X[rb][e], X[rb][e + 1]);
+      for (int rb = 0; rb < RB; ++rb) X[rb].put<3>(sm + L::X, DK * 128, block_row<DK>(l, rb), l.c);
       fence_async();
       fence_before();
       bar_sync(1, kChainThreads);
@@ -444,32 +440,25 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
         }
       }
       // while that runs: the state goes out; in reverse its slot first gives up Qᵀ(G O')
-      float F[REV ? RB : 1][16];
-      float* Xout = rows_x + (size_t)n * DK * DV;
+      Fragment F[REV ? RB : 1];
+      float* Xout = blocks_x + (size_t)n * DK * DV;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float* p = Xout + (xr[rb] + (e & 2) * 4) * DV + (e >> 2) * 8;
-          if (REV) {
-            const float2 x = load_two(p);
-            F[rb][e] = x.x, F[rb][e + 1] = x.y;
-          } else {
-            store_two(p, X[rb][e], X[rb][e + 1]);
-          }
-        }
-      float v[16];
+      for (int rb = 0; rb < RB; ++rb) {
+        if (REV) F[rb].load(Xout + rb * kBlock, tid);
+        else X[rb].store(Xout + rb * kBlock, tid);
+      }
+      Fragment u, s;
       mbar_wait(&done[0], parity, ok);
       fence_after();
-      tmem_load(tm + rows + 32 * half, v);
+      tmem_load(tm + rows, u.v);
       const float gend = end;
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const int o = (e & 2) >> 1, j = e >> 2;
-        const float f = REV ? -g[o][2] * g[o][0] : g[o][1];  // −β G, or E
-        v[e] += B[2 * j + o].x, v[e + 1] += B[2 * j + o].y;
-        store_pair<3>(sm + L::U, kTileBytes, r0 + 8 * o, c0 + j * 8, f * v[e], f * v[e + 1]);
+      for (int e = 0; e < 16; ++e) {
+        const int o = (e & 2) >> 1;
+        u.v[e] += B.v[e];
+        s.v[e] = (REV ? -g[o][2] * g[o][0] : g[o][1]) * u.v[e];  // −β G, or E
       }
+      s.put<3>(sm + L::U, kTileBytes, l.r, l.c);
       fence_async();
       fence_before();
       bar_sync(1, kChainThreads);
@@ -481,24 +470,19 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
           commit(&empty[b]);
         }
       }
-      float* Uout = rows_u + (size_t)n * C * DV;
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) store_two(Uout + (e & 2) * 4 * DV + (e >> 2) * 8, v[e], v[e + 1]);
+      u.store(blocks_u + (size_t)n * C * DV, tid);
       if (i + 1 < N) fetch(REV ? n - 1 : n + 1);
       if (REV) {
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            store_two(Xout + (xr[rb] + (e & 2) * 4) * DV + (e >> 2) * 8, X[rb][e], X[rb][e + 1]);
+        for (int rb = 0; rb < RB; ++rb) X[rb].store(Xout + rb * kBlock, tid);
       }
       mbar_wait(&done[1], parity, ok);
       fence_after();
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        tmem_load(tm + 64 + rows + ((uint32_t)(16 * rb) << 16) + 32 * half, v);
+        tmem_load(tm + 64 + rows + ((uint32_t)(16 * rb) << 16), s.v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) X[rb][e] = fmaf(gend, X[rb][e], REV ? v[e] + F[REV ? rb : 0][e] : v[e]);
+        for (int e = 0; e < 16; ++e) X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? s.v[e] + F[REV ? rb : 0].v[e] : s.v[e]);
       }
     }
     float* last = REV ? d.gstate0 : a.stateT;
@@ -507,10 +491,10 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const int r = xr[rb] + (i & 2) * 4, c = col + c0 + (i >> 2) * 8;
+        for (int e = 0; e < 16; e += 2) {
+          const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = col + l.c + (e >> 2) * 8;
           if (r < a.dk && c < a.dv)
-            store_two(last + ((size_t)bh * a.dk + r) * a.dv + c, X[rb][i] + bad, X[rb][i + 1] + bad);
+            store_two(last + ((size_t)bh * a.dk + r) * a.dv + c, X[rb].v[e] + bad, X[rb].v[e + 1] + bad);
         }
     }
   }
@@ -536,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   __shared__ float hi[C], lo[C], G[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
-  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5);
   const int DV = pad64(a.dv);
   const Where at = where(a, blockIdx.x / (DV / 64));
   const int col = (int)(blockIdx.x % (DV / 64)) * 64;
@@ -544,20 +528,22 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   if (tid == 32) mbar_init(&bar, 1);
   const size_t row = (size_t)at.key * a.T + at.t0;
   TileLoad<IO, DK, kThreads> kl, ql;
-  PartsLoad<PN, DK, kThreads> xl;
-  PartsLoad<PN, C, kThreads> ul;
+  const Lanes l(tid);
+  Fragment xl[DK / 64], ul;
   kl.fetch(reinterpret_cast<const IO*>(a.k) + row * a.dk, at.len, a.dk, 0, tid);
   ql.fetch(reinterpret_cast<const IO*>(a.q) + row * a.dk, at.len, a.dk, 0, tid);
-  xl.fetch(w.S + at.chunk * DK * DV + col, DV, tid);
-  ul.fetch(w.U + at.chunk * C * DV + col, DV, tid);
+#pragma unroll
+  for (int rb = 0; rb < DK / 64; ++rb) xl[rb].load(w.S + at.chunk * DK * DV + col * DK + rb * kBlock, tid);
+  ul.load(w.U + at.chunk * C * DV + col * 64, tid);
   if (tid < C) {
     const float* g = w.gates + at.chunk * kGates + tid;
     hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C];
   }
   kl.put(sm + L::K, tid);
   ql.put(sm + L::Q, tid);
-  xl.put(sm + L::S, tid);
-  ul.put(sm + L::U, tid);
+#pragma unroll
+  for (int rb = 0; rb < DK / 64; ++rb) xl[rb].put<PN>(sm + L::S, DK * 128, block_row<DK>(l, rb), l.c);
+  ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
   fence_async();
   fence_before();
   __syncthreads();
@@ -570,7 +556,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
     mma<64, 64, DK>(tm + 64, Qr, Operand<PN, true>{base + L::S, DK * 128, DK * 128});
     commit(&bar);
   }
-  const int quad = warp & 3, half = warp >> 2, r0 = 16 * quad + (lane >> 2), c0 = 32 * half + 2 * (lane & 3);
+  const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
   mbar_wait(&bar, 0, ok);
   fence_after();
@@ -595,14 +581,10 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   mbar_wait(&bar, 1, ok);
   fence_after();
   tmem_load(tm + rows + 32 * half, v);
-  IO* o = reinterpret_cast<IO*>(a.o) + ((size_t)at.bh * a.T + at.t0) * a.dv + col;
   const float scale = ok ? a.scale : __int_as_float(0x7fc00000);  // a wait ran out
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const int t = r0 + (i & 2) * 4, c = c0 + (i >> 2) * 8;
-    if (t < at.len && col + c < a.dv)
-      store_two(o + (size_t)t * a.dv + c, scale * fmaf(G[t], y[i], v[i]), scale * fmaf(G[t], y[i + 1], v[i + 1]));
-  }
+  for (int i = 0; i < 16; ++i) v[i] = scale * fmaf(G[l.r + (i & 2) * 4], y[i], v[i]);
+  store_rows(reinterpret_cast<IO*>(a.o) + ((size_t)at.bh * a.T + at.t0) * a.dv, l, col, at.len, a.dv, v);
   fence_before();
   __syncthreads();
   if (warp == 0) tmem_free(tm, 128);

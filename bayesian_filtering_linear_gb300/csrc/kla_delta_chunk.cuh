@@ -21,7 +21,10 @@ constexpr int kParts = sizeof(IO) == 2 ? 1 : 3;  // bf16 parts that hold an inpu
 
 __host__ __device__ constexpr int pad64(int d) { return d <= 64 ? 64 : 128; }
 
-// Per chunk of every value head, padded to whole chunks and to widths of 64.
+// Per chunk of every value head, padded to whole chunks and to widths of 64:
+// blocks of 64 × 64 (a column of blocks per 64 columns, one or two rows of
+// them) in the order of the fragments that 256 threads hold of them, so that
+// a warp's stores and loads are whole lines (see Fragment).
 struct Workspace {
   float* gates;  // [chunks][5][64]
   float* W;      // [chunks][64][DK]: −M (β G K)
@@ -102,34 +105,98 @@ struct TileLoad {
   }
 };
 
-// A workspace array's rows, 64 columns of row length ld, as one column of tiles.
-template <int PARTS, int ROWS, int THREADS>
-struct PartsLoad {
-  static constexpr int N = ROWS * 8 / THREADS;
-  float4 v[2 * N];
-  __device__ __forceinline__ void fetch(const float* src, int ld, int tid) {
+// A thread's sixteen values of a 64 × 64 block as they come from TMEM: rows
+// r and r + 8, columns c + 8 j and the next, j < 4 (value 4 j + 2 o + e is row
+// r + 8 o, column c + 8 j + e).
+constexpr int kBlock = 64 * 64;
+struct Lanes {
+  int quad, half, lane, r, c;
+  __device__ __forceinline__ Lanes(int tid)
+      : quad((tid >> 5) & 3), half(tid >> 7), lane(tid & 31), r(16 * quad + (lane >> 2)), c(32 * half + 2 * (lane & 3)) {}
+};
+// rows of block rb of an array of DK rows (TMEM spreads 64 rows over 16 lanes of each quadrant, 128 over all)
+template <int DK>
+__device__ __forceinline__ int block_row(const Lanes& l, int rb) {
+  return (DK == 64 ? 16 * l.quad : 32 * l.quad + 16 * rb) + (l.lane >> 2);
+}
+struct Fragment {
+  float v[16];
+  __device__ __forceinline__ void load(const float* block, int tid) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int i = tid + j * THREADS;
-      const float4* p = reinterpret_cast<const float4*>(src + (size_t)(i >> 3) * ld + (i & 7) * 8);
-      v[2 * j] = p[0];
-      v[2 * j + 1] = p[1];
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(block)[j * 256 + tid];
+      v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
     }
   }
-  __device__ __forceinline__ void eight(int j, float (&x)[8]) const {
-    const float4 a = v[2 * j], b = v[2 * j + 1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  __device__ __forceinline__ void put(char* tile, int tid, int part = ROWS * 128) const {
+  __device__ __forceinline__ void store(float* block, int tid) const {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int i = tid + j * THREADS;
-      float x[8];
-      eight(j, x);
-      store_eight<PARTS>(tile, part, i >> 3, (i & 7) * 8, x);
-    }
+    for (int j = 0; j < 4; ++j)
+      reinterpret_cast<float4*>(block)[j * 256 + tid] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  }
+  // into a column of tiles as parts, from row r and column c
+  template <int PARTS>
+  __device__ __forceinline__ void put(char* tile, int part, int r, int c) const {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) store_pair<PARTS>(tile, part, r + (e & 2) * 4, c + (e >> 2) * 8, v[e], v[e + 1]);
   }
 };
+
+// Four lanes that hold columns 2 q and 2 q + 1 of four eights turn them so that lane q holds all of eight q (and back).
+__device__ __forceinline__ void turn_four(uint32_t (&u)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  uint32_t a = __shfl_xor_sync(~0u, odd ? u[0] : u[1], 1), b = __shfl_xor_sync(~0u, odd ? u[2] : u[3], 1);
+  if (odd) u[0] = a, u[2] = b;
+  else u[1] = a, u[3] = b;
+  a = __shfl_xor_sync(~0u, high ? u[0] : u[2], 2), b = __shfl_xor_sync(~0u, high ? u[1] : u[3], 2);
+  if (high) u[0] = a, u[1] = b;
+  else u[2] = a, u[3] = b;
+}
+// A fragment to and from rows of an io array of width d: columns from c0 on, rows below len (all lanes of a warp call).
+template <typename IO>
+__device__ __forceinline__ void store_rows(IO* out, const Lanes& l, int c0, int len, int d, const float (&v)[16]) {
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int r = l.r + 8 * o;
+    if (sizeof(IO) == 2) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = bf16_pair(v[4 * j + 2 * o], v[4 * j + 2 * o + 1]);
+      turn_four(u, l.lane);
+      const int c = c0 + 32 * l.half + 8 * (l.lane & 3);
+      if (r < len && c < d) *reinterpret_cast<uint4*>(out + (size_t)r * d + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r < len && c0 + l.c + 8 * j < d) store_two(out + (size_t)r * d + c0 + l.c + 8 * j, v[4 * j + 2 * o], v[4 * j + 2 * o + 1]);
+    }
+  }
+}
+template <typename IO>
+__device__ __forceinline__ void load_rows(const IO* in, const Lanes& l, int c0, int len, int d, float (&v)[16]) {
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int r = l.r + 8 * o;
+    if (sizeof(IO) == 2) {
+      const int c = c0 + 32 * l.half + 8 * (l.lane & 3);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < len && c < d) x = *reinterpret_cast<const uint4*>(in + (size_t)r * d + c);
+      uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      turn_four(u, l.lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[4 * j + 2 * o] = __uint_as_float(u[j] << 16);
+        v[4 * j + 2 * o + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 x = make_float2(0.f, 0.f);
+        if (r < len && c0 + l.c + 8 * j < d) x = load_two(in + (size_t)r * d + c0 + l.c + 8 * j);
+        v[4 * j + 2 * o] = x.x, v[4 * j + 2 * o + 1] = x.y;
+      }
+    }
+  }
+}
 
 // Decay from token s to token t ≥ s of a chunk (for s > t some number, without overflow).
 __device__ __forceinline__ float decay(const float* hi, const float* lo, int t, int s) {
