@@ -10,11 +10,13 @@
 //
 // Every element is read once and written once, so HBM bounds it. A row of a
 // head is held by a group of lanes, 16 bytes a lane; the sum of squares is a
-// few lane exchanges, and the other member of a pair is in the lane itself
-// (neighbouring pairs) or one exchange away (halves). A group keeps one token
-// and goes through heads, so that the angles, which cost more than the rest
-// of a row, are computed once for all heads of the group. Input strides are
-// free: a projection's [B,T,H,D] is read in place and leaves as [B,H,T,D].
+// few lane exchanges, and the other members of a lane's pairs are in the lane
+// itself (neighbouring pairs) or in one other lane (halves), fetched as they
+// were read. A group keeps one token and goes through heads, four rows (two
+// backward) in flight at a time, so that the angles, which cost as much as
+// several rows, are computed once, and with the weights folded in a rotated
+// entry is r (x wc + x' ws). Input strides are free: a projection's [B,T,H,D]
+// is read in place and leaves as [B,H,T,D].
 //
 // Angles: pos·f / 2π is formed from f/2π as an unevaluated sum of floats, each
 // term's whole turns taken off exactly, and the rest given to sincospif, so
@@ -31,40 +33,38 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kNormNone = 0, kNormRms = 1;  // else L2
 
-// 16 bytes of a row as fp32
+// 16 bytes of a row
 template <typename IO>
-struct Vec;
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const float* p, float* x) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+struct Row {
+  static constexpr int N = 16 / sizeof(IO);
+  uint4 v;
+  __device__ __forceinline__ void load(const void* p, long long i) {
+    v = *reinterpret_cast<const uint4*>(reinterpret_cast<const IO*>(p) + i);
   }
-  static __device__ __forceinline__ void store(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  __device__ __forceinline__ void values(float (&x)[N]) const {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      if (N == 4) {
+        x[i] = __uint_as_float(u[i]);
+      } else {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
+  static __device__ __forceinline__ void store(void* p, long long i, const float (&x)[N]) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    for (int j = 0; j < 4; ++j) {
+      if (N == 4) {
+        u[j] = __float_as_uint(x[j]);
+      } else {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+        u[j] = *reinterpret_cast<const uint32_t*>(&y);
+      }
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<uint4*>(reinterpret_cast<IO*>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 };
 
@@ -90,50 +90,62 @@ __device__ __forceinline__ float turn_of(long long pos, float f) {
   return fraction(turn);
 }
 
+// The other member of element e's pair (e itself where it is not rotated).
+__device__ __forceinline__ int other(const NormRopeArgs& a, int e) {
+  if (e >= a.rot) return e;
+  if (a.layout) return e ^ 1;
+  return e < a.rot / 2 ? e + a.rot / 2 : e - a.rot / 2;
+}
+
 // The angles of a lane's elements, as y = x·c + other·s with the sign of the
 // element's place in its pair in s.
 template <int VE>
-__device__ __forceinline__ void angles(const NormRopeArgs& a, long long pos, int e0, float* c, float* s) {
+__device__ __forceinline__ void angles(const NormRopeArgs& a, long long pos, int e0, float (&c)[VE], float (&s)[VE]) {
   const int R = a.rot / 2;
 #pragma unroll
   for (int j = 0; j < VE; ++j) {
     const int e = e0 + j;
+    if (a.layout && (j & 1)) {  // a pair's second
+      c[j] = c[j - 1];
+      s[j] = -s[j - 1];
+      continue;
+    }
     c[j] = 1.f;
     s[j] = 0.f;
     if (e < a.rot) {
       const int i = a.layout ? e / 2 : (e < R ? e : e - R);
-      const bool first = a.layout ? !(e & 1) : e < R;
       float sn, cs;
       sincospif(2.f * turn_of(pos, a.inv_freq[i]), &sn, &cs);
       c[j] = cs * a.rot_scale;
-      s[j] = (first ? -sn : sn) * a.rot_scale;
+      s[j] = (a.layout || e < R ? -sn : sn) * a.rot_scale;
     }
   }
 }
 
-// The other members of a lane's pairs. `aligned`: R is a multiple of the lane's elements (halves).
-template <int VE>
-__device__ __forceinline__ void others(const NormRopeArgs& a, int lane_in_row, bool aligned, float* row, const float* x,
-                                       float* o) {
-  const int R = a.rot / 2, e0 = lane_in_row * VE;
+// The other members of a lane's pairs, zero where nothing is rotated. `aligned`: halves that are whole lanes.
+template <typename IO>
+__device__ __forceinline__ void others(const NormRopeArgs& a, int e0, bool aligned, float* row, const Row<IO>& v,
+                                       const float (&x)[Row<IO>::N], float (&o)[Row<IO>::N]) {
+  constexpr int VE = Row<IO>::N;
   if (a.layout) {
 #pragma unroll
-    for (int j = 0; j < VE; ++j) o[j] = x[j ^ 1];
+    for (int j = 0; j < VE; ++j) o[j] = e0 + j < a.rot ? x[j ^ 1] : 0.f;
   } else if (aligned) {
-    const int d = R / VE;
-    const int lane = threadIdx.x & 31;
+    const int R = a.rot / 2, d = R / VE, lane = threadIdx.x & 31;
     const int from = e0 < R ? lane + d : (e0 < a.rot ? lane - d : lane);
-#pragma unroll
-    for (int j = 0; j < VE; ++j) o[j] = __shfl_sync(~0u, x[j], from);
+    Row<IO> w;
+    w.v.x = __shfl_sync(~0u, v.v.x, from);
+    w.v.y = __shfl_sync(~0u, v.v.y, from);
+    w.v.z = __shfl_sync(~0u, v.v.z, from);
+    w.v.w = __shfl_sync(~0u, v.v.w, from);
+    if (e0 >= a.rot) w.v = make_uint4(0, 0, 0, 0);
+    w.values(o);
   } else {  // through the group's row in shared memory
 #pragma unroll
     for (int j = 0; j < VE; ++j) row[e0 + j] = x[j];
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      const int e = e0 + j;
-      o[j] = e < R ? row[e + R] : (e < a.rot ? row[e - R] : 0.f);
-    }
+    for (int j = 0; j < VE; ++j) o[j] = e0 + j < a.rot ? row[other(a, e0 + j)] : 0.f;
     __syncwarp();
   }
 }
@@ -147,89 +159,99 @@ __device__ __forceinline__ float row_sum(float x) {
 
 __device__ __forceinline__ float inv_size(const NormRopeArgs& a, float sum) {
   if (a.norm == kNormNone) return 1.f;
-  return 1.0f / sqrtf((a.norm == kNormRms ? sum / (float)a.D : sum) + a.eps);
+  return rsqrtf(fmaf(sum, a.norm == kNormRms ? 1.f / (float)a.D : 1.f, a.eps));
 }
 
-// A group of LPR lanes: one token, a range of the heads of q followed by those
-// of k. BWD also sums the weight gradients of the block.
+// A block takes GROUPS tokens and one of `splits` ranges of the heads of q
+// followed by those of k; BWD also sums its weight gradients. Lanes without a
+// token go along, so that every lane of a warp takes part in its exchanges.
 template <typename IO, int D, bool BWD>
 __global__ void __launch_bounds__(kThreads) kla_norm_rope_kernel(const NormRopeArgs a, int splits) {
-  constexpr int VE = Vec<IO>::N, LPR = D / VE, GROUPS = kThreads / LPR;
+  constexpr int VE = Row<IO>::N, LPR = D / VE, GROUPS = kThreads / LPR, U = BWD ? 2 : 4;
   __shared__ float rows[GROUPS][D];
   const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR, e0 = l * VE;
   const bool aligned = (a.rot / 2) % VE == 0;
   const int heads = a.q.H + a.k.H, per = (heads + splits - 1) / splits;
-  const long long tokens = (long long)a.B * a.T;
-  float accq[BWD ? VE : 1] = {}, acck[BWD ? VE : 1] = {};
-  // whole blocks step together, so that every lane of a warp takes part in its exchanges
-  const long long total = tokens * splits, stride = (long long)gridDim.x * GROUPS;
-  for (long long base = (long long)blockIdx.x * GROUPS; base < total; base += stride) {
-    const long long job = base + grp;
-    const bool live = job < total;
-    const long long tok = live ? job % tokens : 0;
-    const int h0 = live ? (int)(job / tokens) * per : 0, h1 = live ? min(heads, h0 + per) : 0;
-    const int b = (int)(tok / a.T);
-    const long long t = tok % a.T;
+  const long long tokens = (long long)a.B * a.T, groups = (tokens + GROUPS - 1) / GROUPS;
+  float acc[2][BWD ? VE : 1] = {};
+  for (long long job = blockIdx.x; job < groups * splits; job += gridDim.x) {
+    const int h0 = (int)(job / groups) * per, h1 = min(heads, h0 + per);
+    const long long tok = job % groups * GROUPS + grp;
+    const bool live = tok < tokens;
+    const long long at = live ? tok : 0;
+    const int b = (int)(at / a.T);
+    const long long t = at % a.T;
     float c[VE], s[VE];
-    if (a.rot) angles<VE>(a, a.positions ? a.positions[tok] : a.offset + t, e0, c, s);
-    for (int i = 0; i < per; ++i) {
-      const int hh = h0 + i;
-      const bool on = hh < h1;
-      const bool isq = hh < a.q.H;
-      const NormRopeTensor& p = isq ? a.q : a.k;
-      const int h = isq ? hh : hh - a.q.H;
-      const long long xi = b * p.sb + h * p.sh + t * p.st + e0;
-      const long long yi = (((long long)b * p.H + h) * a.T + t) * D + e0;
-      float x[VE], w[VE], y[VE], o[VE];
 #pragma unroll
-      for (int j = 0; j < VE; ++j) x[j] = 0.f, w[j] = 1.f;
-      if (on) {
-        Vec<IO>::load(reinterpret_cast<const IO*>(p.x) + xi, x);
-        if (p.w)
+    for (int j = 0; j < VE; ++j) c[j] = 1.f, s[j] = 0.f;
+    if (a.rot) angles<VE>(a, a.positions ? a.positions[at] : a.offset + t, e0, c, s);
 #pragma unroll
-          for (int j = 0; j < VE; ++j) w[j] = p.w[e0 + j];
+    for (int m = 0; m < 2; ++m) {
+      const NormRopeTensor& p = m ? a.k : a.q;
+      const int lo = m ? max(h0 - a.q.H, 0) : h0, hi = m ? h1 - a.q.H : min(h1, a.q.H);
+      if (lo >= hi) continue;
+      float w[VE], wc[VE], ws[VE];  // forward: the weights are part of the rotation
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        w[j] = p.w ? p.w[e0 + j] : 1.f;
+        wc[j] = w[j] * c[j];
+        ws[j] = (p.w ? p.w[other(a, e0 + j)] : 1.f) * s[j];
       }
-      float sum = 0.f;
+      const long long x0 = b * p.sb + t * p.st + e0, y0 = ((long long)b * p.H * a.T + t) * D + e0;
+      for (int h = lo; h < hi; h += U) {
+        Row<IO> xv[U], gv[U];
 #pragma unroll
-      for (int j = 0; j < VE; ++j) sum = fmaf(x[j], x[j], sum);
-      const float total_sq = row_sum<LPR>(sum);
-      const float r = on ? inv_size(a, total_sq) : 0.f;  // idle lanes add nothing, whatever ε is
-      if (!BWD) {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) y[j] = x[j] * r * w[j];
-        if (a.rot) {
-          others<VE>(a, l, aligned, rows[grp], y, o);
-#pragma unroll
-          for (int j = 0; j < VE; ++j)
-            if (e0 + j < a.rot) y[j] = fmaf(y[j], c[j], o[j] * s[j]);
+        for (int u = 0; u < U; ++u) {
+          xv[u].v = gv[u].v = make_uint4(0, 0, 0, 0);
+          if (live && h + u < hi) {
+            xv[u].load(p.x, x0 + (h + u) * p.sh);
+            if (BWD && p.gy) gv[u].load(p.gy, y0 + (long long)(h + u) * a.T * D);
+          }
         }
-        if (on) Vec<IO>::store(reinterpret_cast<IO*>(p.y) + yi, y);
-      } else {
-        float g[VE];
 #pragma unroll
-        for (int j = 0; j < VE; ++j) g[j] = 0.f;
-        if (on && p.gy) Vec<IO>::load(reinterpret_cast<const IO*>(p.gy) + yi, g);
-        if (a.rot) {  // the transpose: the same cosines, the sines' sign turned
-          others<VE>(a, l, aligned, rows[grp], g, o);
+        for (int u = 0; u < U; ++u) {
+          const bool on = live && h + u < hi;
+          float x[VE], o[VE], y[VE];
+          xv[u].values(x);
+          float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < VE; ++j)
-            if (e0 + j < a.rot) g[j] = fmaf(g[j], c[j], -o[j] * s[j]);
+          for (int j = 0; j < VE; ++j) sum = fmaf(x[j], x[j], sum);
+          sum = row_sum<LPR>(sum);
+          const float r = on ? inv_size(a, sum) : 0.f;  // idle lanes add nothing, whatever ε is
+          if (!BWD) {
+            if (a.rot) {
+              others<IO>(a, e0, aligned, rows[grp], xv[u], x, o);
+#pragma unroll
+              for (int j = 0; j < VE; ++j) y[j] = r * fmaf(x[j], wc[j], o[j] * ws[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < VE; ++j) y[j] = r * (x[j] * w[j]);
+            }
+            if (on) Row<IO>::store(p.y, y0 + (long long)(h + u) * a.T * D, y);
+          } else {
+            float g[VE];
+            gv[u].values(g);
+            if (a.rot) {  // the transpose: the same cosines, the sines' sign turned
+              others<IO>(a, e0, aligned, rows[grp], gv[u], g, o);
+#pragma unroll
+              for (int j = 0; j < VE; ++j) g[j] = fmaf(g[j], c[j], -o[j] * s[j]);
+            }
+            float dot = 0.f;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              x[j] *= r;
+              acc[m][j] = fmaf(g[j], x[j], acc[m][j]);
+              g[j] *= w[j];
+              dot = fmaf(g[j], x[j], dot);
+            }
+            dot = row_sum<LPR>(dot);
+            if (a.norm == kNormNone) dot = 0.f;
+            else if (a.norm == kNormRms) dot *= 1.f / (float)D;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) y[j] = r * fmaf(-x[j], dot, g[j]);
+            if (on) Row<IO>::store(p.gx, b * p.gsb + (h + u) * p.gsh + t * p.gst + e0, y);
+          }
         }
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const float xr = x[j] * r;
-          if (isq) accq[j] = fmaf(g[j], xr, accq[j]);
-          else acck[j] = fmaf(g[j], xr, acck[j]);
-          g[j] *= w[j];
-          dot = fmaf(g[j], xr, dot);
-        }
-        dot = row_sum<LPR>(dot);
-        if (a.norm == kNormNone) dot = 0.f;
-        else if (a.norm == kNormRms) dot /= (float)D;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) y[j] = r * (g[j] - x[j] * r * dot);
-        if (on) Vec<IO>::store(reinterpret_cast<IO*>(p.gx) + b * p.gsb + h * p.gsh + t * p.gst + e0, y);
       }
     }
   }
@@ -238,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) kla_norm_rope_kernel(const NormRopeA
     for (int m = 0; m < 2; ++m) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < VE; ++j) rows[grp][e0 + j] = m ? acck[j] : accq[j];
+      for (int j = 0; j < VE; ++j) rows[grp][e0 + j] = acc[m][j];
       __syncthreads();
       for (int i = threadIdx.x; i < D; i += kThreads) {
         float x = 0.f;
@@ -260,19 +282,19 @@ __global__ void __launch_bounds__(32) kla_norm_rope_sum_kernel(const NormRopeArg
   if (threadIdx.x == 0) out[i] = x;
 }
 
-// How many groups share a token's heads, and the blocks. A token's angles cost
-// about as much as several rows, so a group takes all heads unless that leaves
-// the device short of warps (about 32 an SM).
+// How many blocks share a token's heads, and the blocks. A token's angles cost
+// about as much as several rows, so a block takes all heads unless that leaves
+// the device short of blocks (four an SM; backward, where every block leaves
+// partial sums, no more than that).
 void geometry(int B, int heads, int T, int D, int io, int num_sms, bool bwd, int* splits, unsigned* blocks) {
-  const long long gpb = kThreads * (io == IO_BF16 ? 8 : 4) / D, tokens = (long long)B * T;
-  const long long want = (long long)num_sms * 4 * gpb;
-  long long s = tokens > 0 ? (want + tokens - 1) / tokens : 1;
+  const long long gpb = kThreads * (io == IO_BF16 ? 8 : 4) / D, groups = ((long long)B * T + gpb - 1) / gpb;
+  const long long want = (long long)num_sms * 4;
+  long long s = groups > 0 ? (want + groups - 1) / groups : 1;
   s = std::min<long long>(std::max<long long>(s, 1), std::max(heads, 1));
   const long long per = (heads + s - 1) / s;
   s = per > 0 ? (heads + per - 1) / per : 1;
   *splits = (int)s;
-  long long n = (tokens * s + gpb - 1) / gpb;
-  n = std::min<long long>(n, bwd ? num_sms * 8LL : 1LL << 30);
+  const long long n = std::min<long long>(groups * s, bwd ? want : 1LL << 30);
   *blocks = (unsigned)std::max<long long>(n, 1);
 }
 

@@ -22,6 +22,7 @@ F32, BF16 = 0, 1
 AUTO, SEQUENTIAL, CHUNKED = 0, 1, 2
 _STRATEGIES = {"auto": AUTO, "sequential": SEQUENTIAL, "chunked": CHUNKED}
 _IO = {torch.float32: F32, torch.bfloat16: BF16}
+_NO_SIZE = ctypes.c_size_t(-1).value  # a workspace size for bad arguments
 # Every function the header declares, for the export check.
 EXPORTS = ("kla_plan", "kla_plan_for_sms", "kla_forward_workspace_size", "kla_forward", "kla_step",
            "kla_status_string", "kla_version", "kla_forward_chunked_noalloc", "kla_backward_workspace_size",
@@ -505,6 +506,27 @@ def conv_backward(x, weight, bias=None, window=None, *, gy=None, gwindow_out=Non
 
 # ---- the gated delta rule ------------------------------------------------------
 
+# A decode token's kernels take a few microseconds, so the calls below keep the
+# host's share of a call small: one comparison per tensor on the way that is
+# taken when all is well (what is wrong is found out afterwards), addresses as
+# plain integers, and the device's context only entered when it is another.
+
+def _fits(x, dtype, shape, device):
+    return x.dtype == dtype and x.shape == shape and x.device == device and x.is_contiguous()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(device, stream, call):
+    """``call(stream)`` on ``device``, with the given or its current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+
+
 def _delta_shapes(q, k, v, g, beta, tokens=True):
     B, Hk, T, dk = q.shape if tokens else (*q.shape[:2], 1, q.shape[2])
     H, dv = v.shape[1], v.shape[-1]
@@ -513,10 +535,12 @@ def _delta_shapes(q, k, v, g, beta, tokens=True):
         raise ValueError("inputs must be CUDA tensors")
     if dt not in _IO:
         raise TypeError(f"unsupported I/O dtype {dt}")
-    t = (T,) if tokens else ()
-    for name, x, shape in (("q", q, (B, Hk, *t, dk)), ("k", k, (B, Hk, *t, dk)), ("v", v, (B, H, *t, dv)),
-                           ("g", g, (B, H, *t)), ("beta", beta, (B, H, *t))):
-        _need(x, name, dt, shape, dev)
+    keys, gates = q.shape, (B, H, T) if tokens else (B, H)
+    values = (*gates, dv)
+    if not (_fits(q, dt, keys, dev) and _fits(k, dt, keys, dev) and _fits(v, dt, values, dev)
+            and _fits(g, dt, gates, dev) and _fits(beta, dt, gates, dev)):
+        for name, x, shape in (("q", q, keys), ("k", k, keys), ("v", v, values), ("g", g, gates), ("beta", beta, gates)):
+            _need(x, name, dt, shape, dev)
     return B, Hk, H, T, dk, dv, dev, dt
 
 
@@ -538,17 +562,16 @@ def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, 
         _need(o, "o", dt, (B, H, T, dv), dev)
     if final_state and stateT is None:
         stateT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            nbytes = LIB.kla_delta_forward_workspace_size(B, Hk, H, T, dk, dv)
-            if nbytes == ctypes.c_size_t(-1).value:
-                raise KlaError(ERR_INVALID_ARG, "kla_delta_forward_workspace_size")
-            workspace = torch.empty(int(nbytes), dtype=torch.uint8, device=dev) if nbytes else None
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = LIB.kla_delta_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state0), _ptr(o),
-                                   _ptr(stateT), B, Hk, H, T, dk, dv, _IO[dt],
-                                   dk ** -0.5 if scale is None else scale, _ptr(workspace), ws_bytes,
-                                   _stream(stream))
+    if workspace is None:
+        nbytes = LIB.kla_delta_forward_workspace_size(B, Hk, H, T, dk, dv)
+        if nbytes == _NO_SIZE:
+            raise KlaError(ERR_INVALID_ARG, "kla_delta_forward_workspace_size")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _on_device(dev, stream, lambda s: LIB.kla_delta_forward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), o.data_ptr(),
+        _addr(stateT), B, Hk, H, T, dk, dv, _IO[dt], dk ** -0.5 if scale is None else scale, _addr(workspace), ws_bytes,
+        s))
     _check(st, "kla_delta_forward")
     return o, stateT
 
@@ -558,14 +581,15 @@ def delta_step(q, k, v, g, beta, state, *, scale: float | None = None, o=None, s
     ``[B,Hk,dk]``, v ``[B,H,dv]``, g, beta ``[B,H]``; the fp32 state
     ``[B,H,dk,dv]`` is updated in place; returns o."""
     B, Hk, H, _, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta, tokens=False)
-    _need(state, "state", torch.float32, (B, H, dk, dv), dev)
+    if not _fits(state, torch.float32, (B, H, dk, dv), dev):
+        _need(state, "state", torch.float32, (B, H, dk, dv), dev)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=dt, device=dev)
+        o = torch.empty_like(v)
     else:
         _need(o, "o", dt, (B, H, dv), dev)
-    with torch.cuda.device(dev):
-        st = LIB.kla_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(o), B, Hk, H, dk,
-                                dv, _IO[dt], dk ** -0.5 if scale is None else scale, _stream(stream))
+    st = _on_device(dev, stream, lambda s: LIB.kla_delta_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), o.data_ptr(), B, Hk,
+        H, dk, dv, _IO[dt], dk ** -0.5 if scale is None else scale, s))
     _check(st, "kla_delta_step")
     return o
 
@@ -586,18 +610,17 @@ def delta_backward(q, k, v, g, beta, state0=None, *, go=None, gstateT=None, scal
            "gg": torch.empty_like(g), "gbeta": torch.empty_like(beta)}
     if state_grad:
         out["gstate0"] = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            nbytes = LIB.kla_delta_backward_workspace_size(B, Hk, H, T, dk, dv)
-            if nbytes == ctypes.c_size_t(-1).value:
-                raise KlaError(ERR_INVALID_ARG, "kla_delta_backward_workspace_size")
-            workspace = torch.empty(int(nbytes), dtype=torch.uint8, device=dev) if nbytes else None
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = LIB.kla_delta_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state0), _ptr(go),
-                                    _ptr(gstateT), _ptr(out["gq"]), _ptr(out["gk"]), _ptr(out["gv"]),
-                                    _ptr(out["gg"]), _ptr(out["gbeta"]), _ptr(out.get("gstate0")), B, Hk, H, T, dk,
-                                    dv, _IO[dt], dk ** -0.5 if scale is None else scale, _ptr(workspace), ws_bytes,
-                                    _stream(stream))
+    if workspace is None:
+        nbytes = LIB.kla_delta_backward_workspace_size(B, Hk, H, T, dk, dv)
+        if nbytes == _NO_SIZE:
+            raise KlaError(ERR_INVALID_ARG, "kla_delta_backward_workspace_size")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _on_device(dev, stream, lambda s: LIB.kla_delta_backward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), _addr(go),
+        _addr(gstateT), out["gq"].data_ptr(), out["gk"].data_ptr(), out["gv"].data_ptr(), out["gg"].data_ptr(),
+        out["gbeta"].data_ptr(), _addr(out.get("gstate0")), B, Hk, H, T, dk, dv, _IO[dt],
+        dk ** -0.5 if scale is None else scale, _addr(workspace), ws_bytes, s))
     _check(st, "kla_delta_backward")
     return out
 
@@ -606,6 +629,7 @@ def delta_backward(q, k, v, g, beta, state0=None, *, go=None, gstateT=None, scal
 
 _NORMS = {"none": 0, "rms": 1, "l2": 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
+_Strides = ctypes.c_longlong * 3
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -659,21 +683,22 @@ def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset, norm,
     for name, x, h in (("q", q, Hq), ("k", k, Hk)):
         if x is None:
             continue
-        if x.device != dev or x.dtype != dt or tuple(x.shape) != (B, h, T, D):
+        if x.device != dev or x.dtype != dt or x.shape != (B, h, T, D):
             raise ValueError(f"{name} must be {(B, h, T, D)} of {dt} on {dev}")
-        if x.numel() and x.stride(-1) != 1:
+        if x.stride(3) != 1 and x.numel():
             raise ValueError(f"{name}'s last dimension must be contiguous")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
+        if w is not None and not _fits(w, torch.float32, (D,), dev):
             _need(w, name, torch.float32, (D,), dev)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _need(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
-    if positions is not None:
+        if not _fits(inv_freq, torch.float32, (rot // 2,), dev):
+            _need(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
+    if positions is not None and not _fits(positions, torch.int64, (B, T), dev):
         _need(positions, "positions", torch.int64, (B, T), dev)
-    opt = NormRopeOptions(_NORMS[norm], _LAYOUTS[layout], rot, eps, rot_scale, int(offset))
-    strides = [None if x is None else (ctypes.c_longlong * 3)(*x.stride()[:3]) for x in (q, k)]
+    opt = NormRopeOptions(_NORMS[norm], _LAYOUTS[layout], rot, eps, rot_scale, offset)
+    strides = [None if x is None else _Strides(*x.stride()[:3]) for x in (q, k)]
     return B, Hq, Hk, T, D, dev, dt, opt, strides
 
 
@@ -697,10 +722,9 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=
             yk = torch.empty((B, Hk, T, D), dtype=dt, device=dev)
         else:
             _need(yk, "yk", dt, (B, Hk, T, D), dev)
-    with torch.cuda.device(dev):
-        st = LIB.kla_norm_rope(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions),
-                               _ptr(yq), _ptr(yk), B, Hq, Hk, T, D, strides[0], strides[1], _IO[dt],
-                               ctypes.byref(opt), _stream(stream))
+    st = _on_device(dev, stream, lambda s: LIB.kla_norm_rope(
+        q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), yq.data_ptr(),
+        _addr(yk), B, Hq, Hk, T, D, strides[0], strides[1], _IO[dt], ctypes.byref(opt), s))
     _check(st, "kla_norm_rope")
     return yq, yk
 
@@ -724,23 +748,26 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
         order = sorted(range(3), key=lambda d: x.stride(d), reverse=True)
         back = [order.index(d) for d in range(3)]
         out[name] = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=dev).permute(*back, 3)
-        gstrides[n] = (ctypes.c_longlong * 3)(*out[name].stride()[:3])
+        gstrides[n] = _Strides(*out[name].stride()[:3])
     for name, w in (("gq_weight", q_weight), ("gk_weight", k_weight)):
         if w is not None:
             out[name] = torch.empty((D,), dtype=torch.float32, device=dev)
     sums = "gq_weight" in out or "gk_weight" in out
-    with torch.cuda.device(dev):
-        if workspace is None and sums:
+    def call(s):
+        scratch = workspace
+        if scratch is None and sums:
             nbytes = LIB.kla_norm_rope_backward_workspace_size(B, Hq, Hk, T, D)
-            if nbytes == ctypes.c_size_t(-1).value:
+            if nbytes == _NO_SIZE:
                 raise KlaError(ERR_CUDA, "kla_norm_rope_backward_workspace_size")
-            workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = LIB.kla_norm_rope_backward(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-                                        _ptr(positions), _ptr(gyq), _ptr(gyk), _ptr(out["gq"]), _ptr(out.get("gk")),
-                                        _ptr(out.get("gq_weight")), _ptr(out.get("gk_weight")), B, Hq, Hk, T, D,
-                                        *strides, *gstrides, _IO[dt], ctypes.byref(opt), _ptr(workspace),
-                                        ws_bytes, _stream(stream))
+            scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if scratch is None else scratch.numel() * scratch.element_size()
+        return LIB.kla_norm_rope_backward(
+            q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), _addr(gyq),
+            _addr(gyk), out["gq"].data_ptr(), _addr(out.get("gk")), _addr(out.get("gq_weight")),
+            _addr(out.get("gk_weight")), B, Hq, Hk, T, D, *strides, *gstrides, _IO[dt], ctypes.byref(opt),
+            _addr(scratch), ws_bytes, s)
+
+    st = _on_device(dev, stream, call)
     _check(st, "kla_norm_rope_backward")
     return out
 
