@@ -511,37 +511,48 @@ def conv_backward(x, weight, bias=None, window=None, *, gy=None, gwindow_out=Non
 # taken when all is well (what is wrong is found out afterwards), addresses as
 # plain integers, and the device's context only entered when it is another.
 
-def _fits(x, dtype, shape, device):
-    return x.dtype == dtype and x.shape == shape and x.device == device and x.is_contiguous()
+def _fits(x, dtype, shape, index):
+    """A contiguous tensor of this dtype and shape on CUDA device ``index``."""
+    try:
+        return x.dtype is dtype and x.shape == shape and x.get_device() == index and x.is_contiguous()
+    except AttributeError:
+        return False
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_device(device, stream, call):
-    """``call(stream)`` on ``device``, with the given or its current stream."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
-    return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+# the current stream's handle without making a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(index, stream, fn, args):
+    """``fn(*args, stream)`` on device ``index``, with the given or its current stream."""
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        return fn(*args, handle)
+    with torch.cuda.device(index):
+        return fn(*args, handle)
 
 
 def _delta_shapes(q, k, v, g, beta, tokens=True):
     B, Hk, T, dk = q.shape if tokens else (*q.shape[:2], 1, q.shape[2])
     H, dv = v.shape[1], v.shape[-1]
-    dev, dt = q.device, q.dtype
-    if dev.type != "cuda":
+    dt, index = q.dtype, q.get_device()
+    if index < 0:
         raise ValueError("inputs must be CUDA tensors")
-    if dt not in _IO:
+    io = _IO.get(dt)
+    if io is None:
         raise TypeError(f"unsupported I/O dtype {dt}")
     keys, gates = q.shape, (B, H, T) if tokens else (B, H)
     values = (*gates, dv)
-    if not (_fits(q, dt, keys, dev) and _fits(k, dt, keys, dev) and _fits(v, dt, values, dev)
-            and _fits(g, dt, gates, dev) and _fits(beta, dt, gates, dev)):
+    if not (q.is_contiguous() and _fits(k, dt, keys, index) and _fits(v, dt, values, index)
+            and _fits(g, dt, gates, index) and _fits(beta, dt, gates, index)):
         for name, x, shape in (("q", q, keys), ("k", k, keys), ("v", v, values), ("g", g, gates), ("beta", beta, gates)):
-            _need(x, name, dt, shape, dev)
-    return B, Hk, H, T, dk, dv, dev, dt
+            _need(x, name, dt, shape, q.device)
+    return B, Hk, H, T, dk, dv, index, dt, io
 
 
 def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, o=None, stateT=None,
@@ -552,26 +563,27 @@ def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, 
     ``[B,H,T]``; ``state0`` fp32 ``[B,H,dk,dv]`` (None: zeros). ``scale``:
     dk^-0.5 when None. Returns ``(o, stateT)`` (stateT None when
     ``final_state`` is False and none was given)."""
-    B, Hk, H, T, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta)
+    B, Hk, H, T, dk, dv, index, dt, io = _delta_shapes(q, k, v, g, beta)
+    states = (B, H, dk, dv)
     for name, t in (("state0", state0), ("stateT", stateT)):
-        if t is not None:
-            _need(t, name, torch.float32, (B, H, dk, dv), dev)
+        if t is not None and not _fits(t, torch.float32, states, index):
+            _need(t, name, torch.float32, states, q.device)
     if o is None:
-        o = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-    else:
-        _need(o, "o", dt, (B, H, T, dv), dev)
+        o = torch.empty_like(v)
+    elif not _fits(o, dt, v.shape, index):
+        _need(o, "o", dt, v.shape, q.device)
     if final_state and stateT is None:
-        stateT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        stateT = torch.empty(states, dtype=torch.float32, device=q.device)
     if workspace is None:
         nbytes = LIB.kla_delta_forward_workspace_size(B, Hk, H, T, dk, dv)
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_INVALID_ARG, "kla_delta_forward_workspace_size")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _on_device(dev, stream, lambda s: LIB.kla_delta_forward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), o.data_ptr(),
-        _addr(stateT), B, Hk, H, T, dk, dv, _IO[dt], dk ** -0.5 if scale is None else scale, _addr(workspace), ws_bytes,
-        s))
+    st = _run(index, stream, LIB.kla_delta_forward,
+              (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), o.data_ptr(),
+               _addr(stateT), B, Hk, H, T, dk, dv, io, dk ** -0.5 if scale is None else scale, _addr(workspace),
+               ws_bytes))
     _check(st, "kla_delta_forward")
     return o, stateT
 
@@ -580,16 +592,16 @@ def delta_step(q, k, v, g, beta, state, *, scale: float | None = None, o=None, s
     """One decode token of the gated delta rule (kla_delta_step): q, k
     ``[B,Hk,dk]``, v ``[B,H,dv]``, g, beta ``[B,H]``; the fp32 state
     ``[B,H,dk,dv]`` is updated in place; returns o."""
-    B, Hk, H, _, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta, tokens=False)
-    if not _fits(state, torch.float32, (B, H, dk, dv), dev):
-        _need(state, "state", torch.float32, (B, H, dk, dv), dev)
+    B, Hk, H, _, dk, dv, index, dt, io = _delta_shapes(q, k, v, g, beta, tokens=False)
+    if not _fits(state, torch.float32, (B, H, dk, dv), index):
+        _need(state, "state", torch.float32, (B, H, dk, dv), q.device)
     if o is None:
         o = torch.empty_like(v)
-    else:
-        _need(o, "o", dt, (B, H, dv), dev)
-    st = _on_device(dev, stream, lambda s: LIB.kla_delta_step(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), o.data_ptr(), B, Hk,
-        H, dk, dv, _IO[dt], dk ** -0.5 if scale is None else scale, s))
+    elif not _fits(o, dt, v.shape, index):
+        _need(o, "o", dt, v.shape, q.device)
+    st = _run(index, stream, LIB.kla_delta_step,
+              (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), o.data_ptr(),
+               B, Hk, H, dk, dv, io, dk ** -0.5 if scale is None else scale))
     _check(st, "kla_delta_step")
     return o
 
@@ -600,27 +612,28 @@ def delta_backward(q, k, v, g, beta, state0=None, *, go=None, gstateT=None, scal
     dL/do and optionally ``gstateT`` = dL/dS_T (kla_delta_backward). Returns a
     dict with ``gq, gk, gv, gg, gbeta`` (I/O dtype) and, with ``state_grad``,
     ``gstate0`` (fp32)."""
-    B, Hk, H, T, dk, dv, dev, dt = _delta_shapes(q, k, v, g, beta)
+    B, Hk, H, T, dk, dv, index, dt, io = _delta_shapes(q, k, v, g, beta)
+    states = (B, H, dk, dv)
     for name, t in (("state0", state0), ("gstateT", gstateT)):
-        if t is not None:
-            _need(t, name, torch.float32, (B, H, dk, dv), dev)
-    if go is not None:
-        _need(go, "go", dt, (B, H, T, dv), dev)
-    out = {"gq": torch.empty_like(q), "gk": torch.empty_like(k), "gv": torch.empty_like(v),
-           "gg": torch.empty_like(g), "gbeta": torch.empty_like(beta)}
+        if t is not None and not _fits(t, torch.float32, states, index):
+            _need(t, name, torch.float32, states, q.device)
+    if go is not None and not _fits(go, dt, v.shape, index):
+        _need(go, "go", dt, v.shape, q.device)
+    gq, gk, gv, gg, gbeta = (torch.empty_like(x) for x in (q, k, v, g, beta))
+    out = {"gq": gq, "gk": gk, "gv": gv, "gg": gg, "gbeta": gbeta}
     if state_grad:
-        out["gstate0"] = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        out["gstate0"] = torch.empty(states, dtype=torch.float32, device=q.device)
     if workspace is None:
         nbytes = LIB.kla_delta_backward_workspace_size(B, Hk, H, T, dk, dv)
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_INVALID_ARG, "kla_delta_backward_workspace_size")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _on_device(dev, stream, lambda s: LIB.kla_delta_backward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), _addr(go),
-        _addr(gstateT), out["gq"].data_ptr(), out["gk"].data_ptr(), out["gv"].data_ptr(), out["gg"].data_ptr(),
-        out["gbeta"].data_ptr(), _addr(out.get("gstate0")), B, Hk, H, T, dk, dv, _IO[dt],
-        dk ** -0.5 if scale is None else scale, _addr(workspace), ws_bytes, s))
+    st = _run(index, stream, LIB.kla_delta_backward,
+              (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), _addr(go),
+               _addr(gstateT), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gg.data_ptr(), gbeta.data_ptr(),
+               _addr(out.get("gstate0")), B, Hk, H, T, dk, dv, io, dk ** -0.5 if scale is None else scale,
+               _addr(workspace), ws_bytes))
     _check(st, "kla_delta_backward")
     return out
 
@@ -672,34 +685,37 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
 
 def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale):
     B, Hq, T, D = q.shape
-    dev, dt = q.device, q.dtype
-    if dev.type != "cuda":
+    dt, index = q.dtype, q.get_device()
+    if index < 0:
         raise ValueError("inputs must be CUDA tensors")
     if dt not in _IO:
         raise TypeError(f"unsupported I/O dtype {dt}")
     if norm not in _NORMS or layout not in _LAYOUTS:
         raise ValueError(f"unknown norm {norm!r} or layout {layout!r}")
-    Hk = 0 if k is None else k.shape[1]
-    for name, x, h in (("q", q, Hq), ("k", k, Hk)):
-        if x is None:
-            continue
-        if x.device != dev or x.dtype != dt or x.shape != (B, h, T, D):
-            raise ValueError(f"{name} must be {(B, h, T, D)} of {dt} on {dev}")
-        if x.stride(3) != 1 and x.numel():
-            raise ValueError(f"{name}'s last dimension must be contiguous")
+    Hk, k_strides = 0, None
+    q_strides = q.stride()
+    if q_strides[3] != 1 and q.numel():
+        raise ValueError("q's last dimension must be contiguous")
+    if k is not None:
+        Hk, k_strides = k.shape[1], k.stride()
+        if k.get_device() != index or k.dtype is not dt or k.shape != (B, Hk, T, D):
+            raise ValueError(f"k must be {(B, Hk, T, D)} of {dt} on {q.device}")
+        if k_strides[3] != 1 and k.numel():
+            raise ValueError("k's last dimension must be contiguous")
+        k_strides = _Strides(*k_strides[:3])
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and not _fits(w, torch.float32, (D,), dev):
-            _need(w, name, torch.float32, (D,), dev)
+        if w is not None and not _fits(w, torch.float32, (D,), index):
+            _need(w, name, torch.float32, (D,), q.device)
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        if not _fits(inv_freq, torch.float32, (rot // 2,), dev):
-            _need(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
-    if positions is not None and not _fits(positions, torch.int64, (B, T), dev):
-        _need(positions, "positions", torch.int64, (B, T), dev)
+        half = inv_freq.numel()
+        rot = 2 * half
+        if not _fits(inv_freq, torch.float32, (half,), index):
+            _need(inv_freq, "inv_freq", torch.float32, (half,), q.device)
+    if positions is not None and not _fits(positions, torch.int64, (B, T), index):
+        _need(positions, "positions", torch.int64, (B, T), q.device)
     opt = NormRopeOptions(_NORMS[norm], _LAYOUTS[layout], rot, eps, rot_scale, offset)
-    strides = [None if x is None else _Strides(*x.stride()[:3]) for x in (q, k)]
-    return B, Hq, Hk, T, D, dev, dt, opt, strides
+    return B, Hq, Hk, T, D, index, dt, opt, _Strides(*q_strides[:3]), k_strides
 
 
 def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, norm: str = "rms",
@@ -711,20 +727,20 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     and k ``[B,Hk,T,D]`` (or None) may be strided views, e.g. a projection's
     ``[B,T,H,D]`` transposed; ``positions`` int64 ``[B,T]`` (None: ``offset`` +
     t). Returns contiguous ``(yq, yk)``."""
-    B, Hq, Hk, T, D, dev, dt, opt, strides = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset,
-                                                             norm, layout, eps, rot_scale)
+    B, Hq, Hk, T, D, index, dt, opt, q_strides, k_strides = _norm_rope_args(
+        q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale)
     if yq is None:
-        yq = torch.empty((B, Hq, T, D), dtype=dt, device=dev)
-    else:
-        _need(yq, "yq", dt, (B, Hq, T, D), dev)
+        yq = torch.empty((B, Hq, T, D), dtype=dt, device=q.device)
+    elif not _fits(yq, dt, (B, Hq, T, D), index):
+        _need(yq, "yq", dt, (B, Hq, T, D), q.device)
     if k is not None:
         if yk is None:
-            yk = torch.empty((B, Hk, T, D), dtype=dt, device=dev)
-        else:
-            _need(yk, "yk", dt, (B, Hk, T, D), dev)
-    st = _on_device(dev, stream, lambda s: LIB.kla_norm_rope(
-        q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), yq.data_ptr(),
-        _addr(yk), B, Hq, Hk, T, D, strides[0], strides[1], _IO[dt], ctypes.byref(opt), s))
+            yk = torch.empty((B, Hk, T, D), dtype=dt, device=q.device)
+        elif not _fits(yk, dt, (B, Hk, T, D), index):
+            _need(yk, "yk", dt, (B, Hk, T, D), q.device)
+    st = _run(index, stream, LIB.kla_norm_rope,
+              (q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions),
+               yq.data_ptr(), _addr(yk), B, Hq, Hk, T, D, q_strides, k_strides, _IO[dt], ctypes.byref(opt)))
     _check(st, "kla_norm_rope")
     return yq, yk
 
@@ -735,39 +751,39 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
     """Gradients through :func:`norm_rope` given ``gyq``, ``gyk`` (None: zero;
     kla_norm_rope_backward). Returns a dict with ``gq, gk`` (in the memory
     order of q and k) and, for given weights, ``gq_weight, gk_weight``."""
-    B, Hq, Hk, T, D, dev, dt, opt, strides = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset,
-                                                             norm, layout, eps, rot_scale)
+    B, Hq, Hk, T, D, index, dt, opt, q_strides, k_strides = _norm_rope_args(
+        q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale)
     for name, t, h in (("gyq", gyq, Hq), ("gyk", gyk, Hk)):
-        if t is not None:
-            _need(t, name, dt, (B, h, T, D), dev)
+        if t is not None and not _fits(t, dt, (B, h, T, D), index):
+            _need(t, name, dt, (B, h, T, D), q.device)
     # gradients in the inputs' own order, dense whatever lies between a view's rows
     out, gstrides = {}, [None, None]
     for n, (name, x) in enumerate((("gq", q), ("gk", k))):
         if x is None:
             continue
-        order = sorted(range(3), key=lambda d: x.stride(d), reverse=True)
-        back = [order.index(d) for d in range(3)]
-        out[name] = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=dev).permute(*back, 3)
-        gstrides[n] = _Strides(*out[name].stride()[:3])
+        if x.is_contiguous():
+            out[name] = torch.empty_like(x)
+        else:
+            order = sorted(range(3), key=x.stride().__getitem__, reverse=True)
+            back = [order.index(d) for d in range(3)]
+            out[name] = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=q.device).permute(*back, 3)
+            gstrides[n] = _Strides(*out[name].stride()[:3])
     for name, w in (("gq_weight", q_weight), ("gk_weight", k_weight)):
         if w is not None:
-            out[name] = torch.empty((D,), dtype=torch.float32, device=dev)
-    sums = "gq_weight" in out or "gk_weight" in out
-    def call(s):
-        scratch = workspace
-        if scratch is None and sums:
+            out[name] = torch.empty_like(w)
+    sums = q_weight is not None or k_weight is not None
+    if workspace is None and sums:
+        with torch.cuda.device(index):
             nbytes = LIB.kla_norm_rope_backward_workspace_size(B, Hq, Hk, T, D)
-            if nbytes == _NO_SIZE:
-                raise KlaError(ERR_CUDA, "kla_norm_rope_backward_workspace_size")
-            scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if scratch is None else scratch.numel() * scratch.element_size()
-        return LIB.kla_norm_rope_backward(
-            q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), _addr(gyq),
-            _addr(gyk), out["gq"].data_ptr(), _addr(out.get("gk")), _addr(out.get("gq_weight")),
-            _addr(out.get("gk_weight")), B, Hq, Hk, T, D, *strides, *gstrides, _IO[dt], ctypes.byref(opt),
-            _addr(scratch), ws_bytes, s)
-
-    st = _on_device(dev, stream, call)
+        if nbytes == _NO_SIZE:
+            raise KlaError(ERR_CUDA, "kla_norm_rope_backward_workspace_size")
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _run(index, stream, LIB.kla_norm_rope_backward,
+              (q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), _addr(gyq),
+               _addr(gyk), out["gq"].data_ptr(), _addr(out.get("gk")), _addr(out.get("gq_weight")),
+               _addr(out.get("gk_weight")), B, Hq, Hk, T, D, q_strides, k_strides, *gstrides, _IO[dt],
+               ctypes.byref(opt), _addr(workspace), ws_bytes))
     _check(st, "kla_norm_rope_backward")
     return out
 
