@@ -763,7 +763,7 @@ kla_status kla_delta_forward(const void* q, const void* k, const void* v, const 
                              const float* state0, void* o, float* stateT, int B, int Hk, int H, int T, int dk,
                              int dv, kla_dtype io, float scale, void* workspace, size_t ws_bytes, void* stream) {
   // ---- validation: no CUDA call before it passes ---------------------------
-  const kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
+  kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
   if (st != KLA_OK) return st;
   if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
   const long long bh = (long long)B * H, tokens = bh * T;
@@ -780,8 +780,10 @@ kla_status kla_delta_forward(const void* q, const void* k, const void* v, const 
   if (ranges_clash(outs, 3, ins, 6, 0, 5)) return KLA_ERR_INVALID_ARG;
   if (bh == 0 || (T == 0 && !stateT)) return KLA_OK;
   if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
   kla::DeltaArgs a{q, k, v, g, beta, state0, o, stateT, B, Hk, H, T, dk, dv, (int)io, scale};
-  return kla::launch_delta_forward(a, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK
+  return kla::launch_delta_forward(a, sms, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK
                                                                                                         : KLA_ERR_CUDA;
 }
 
@@ -818,7 +820,7 @@ kla_status kla_delta_backward(const void* q, const void* k, const void* v, const
                               void* gv, void* gg, void* gbeta, float* gstate0, int B, int Hk, int H, int T, int dk,
                               int dv, kla_dtype io, float scale, void* workspace, size_t ws_bytes, void* stream) {
   // ---- validation: no CUDA call before it passes ---------------------------
-  const kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
+  kla_status st = check_delta_shape(B, Hk, H, T, dk, dv);
   if (st != KLA_OK) return st;
   if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
   const long long bh = (long long)B * H, tokens = bh * T;
@@ -844,9 +846,11 @@ kla_status kla_delta_backward(const void* q, const void* k, const void* v, const
                                   : cudaMemsetAsync(gstate0, 0, states, s);
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
   }
+  int sms = 0;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
   kla::DeltaArgs a{q, k, v, g, beta, state0, nullptr, nullptr, B, Hk, H, T, dk, dv, (int)io, scale};
   kla::DeltaGradArgs d{go, gstateT, gq, gk, gv, gg, gbeta, gstate0};
-  return kla::launch_delta_backward(a, d, workspace, s) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  return kla::launch_delta_backward(a, d, sms, workspace, s) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 kla_status kla_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,

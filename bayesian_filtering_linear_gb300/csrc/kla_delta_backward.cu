@@ -363,12 +363,13 @@ size_t delta_backward_bytes(int B, int Hk, int H, int T, int dk, int dv) {
   return n;
 }
 
-cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, void* workspace, cudaStream_t s) {
+cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, int num_sms, void* workspace,
+                                  cudaStream_t s) {
   size_t n = 0;
   const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, true, &n);
   cudaError_t e = delta::launch_prepare(a, &g, w, s);
-  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, false, s);
-  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, true, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, false, num_sms, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, true, num_sms, s);
   if (e != cudaSuccess) return e;
   const bool wide = delta::pad64(a.dk) == 128;
   if (a.io == IO_BF16)

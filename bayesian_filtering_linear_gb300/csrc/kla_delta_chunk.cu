@@ -324,9 +324,10 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
 // X: the state (rev: its gradient), W: −M (β G K) (rev: Mᵀ (E K)). Per chunk:
 //   forward:  U = M (β V) + W X,       X = G_end X + Kᵀ(E U)
 //   reverse:  dR = Mᵀ Pᵀ O' + W X,     X = G_end X + Qᵀ(G O') − Kᵀ(β G dR)
-// Eight warps walk the chunks; four more bring K and W of the next chunk as
-// parts, two chunks deep where shared memory holds them.
-constexpr int kChainThreads = 256, kFeedThreads = 128;
+// Eight warps walk the chunks, each with a quarter of the rows and half of the
+// columns; four more bring K and W of the next chunk as parts, two chunks deep
+// where shared memory holds them; one issues the products.
+constexpr int kChainThreads = 256, kFeedThreads = 128, kChainBlock = kChainThreads + kFeedThreads + 32;
 
 template <typename IO, int DK>
 struct ChainSmem {
@@ -337,19 +338,19 @@ struct ChainSmem {
   static_assert(kBytes <= kMaxBytes, "");
 };
 
-template <typename IO, int DK, bool REV>
-__global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_kernel(const DeltaArgs a,
-                                                                                      const DeltaGradArgs d,
-                                                                                      const Workspace w) {
+// NV: columns of a block, 64 or 32.
+template <typename IO, int DK, bool REV, int NV>
+__global__ void __launch_bounds__(kChainBlock)
+    kla_delta_chain_kernel(const DeltaArgs a, const DeltaGradArgs d, const Workspace w) {
   using L = ChainSmem<IO, DK>;
-  constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES;
+  constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES, J = NV / 16;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ uint64_t full[STAGES], empty[STAGES], done[2];
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5);
   const int DV = pad64(a.dv), N = (a.T + C - 1) / C;
-  const long long bh = blockIdx.x / (DV / 64);
-  const int col = (int)(blockIdx.x % (DV / 64)) * 64;
+  const long long bh = blockIdx.x / (DV / NV);
+  const int part = (int)(blockIdx.x % (DV / NV)), col = part * NV / 64 * 64;  // the 64 columns it is in
   const long long key = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], kFeedThreads), mbar_init(&empty[i], 1);
@@ -362,7 +363,30 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
   fence_after();
   const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
-  if (warp >= kChainThreads / 32) {
+  if (warp == kChainBlock / 32 - 1) {  // the products
+    for (int i = 0; i < N; ++i) {
+      const int b = STAGES == 2 ? i & 1 : 0;
+      const Operand<3, false> Wr{base + L::W + b * L::WB, RB * kTileBytes, kTileBytes};
+      const Operand<PARTS, true> Kt{base + L::K + b * L::KB, RB * kTileBytes, kTileBytes};
+      const Operand<3, true> Xs{base + L::X, DK * 128, DK * 128}, Us{base + L::U, kTileBytes, kTileBytes};
+      mbar_wait(&full[b], STAGES == 2 ? (i >> 1) & 1 : i & 1, ok);
+      bar_sync(1, kChainThreads + 32);
+      fence_after();
+      if (elect()) {
+        mma<64, NV, DK>(tm, Wr, Xs);
+        commit(&done[0]);
+      }
+      __syncwarp();
+      bar_sync(2, kChainThreads + 32);
+      fence_after();
+      if (elect()) {
+        mma<DK, NV, 64>(tm + 64, Kt, Us);
+        commit(&done[1]);
+        commit(&empty[b]);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
     const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
     const float* W = (REV ? w.Wr : w.W) + (size_t)bh * N * C * DK;
@@ -370,12 +394,11 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
       const uint32_t before = STAGES == 2 ? ((i >> 1) - 1) & 1 : (i - 1) & 1;
       TileLoad<IO, DK, kFeedThreads> kl;
-      Fragment f[RB][2];  // what the threads of the two halves of columns hold
+      Fragment f[2];  // what the threads of the two halves of columns hold
       // what registers hold comes in ahead of the wait for its place
+      const float* src = W + (size_t)n * C * DK;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) f[rb][h].load(W + (size_t)n * C * DK + rb * kBlock, ft + h * kFeedThreads);
+      for (int h = 0; h < 2; ++h) f[h].load(src, ft + h * kFeedThreads);
       if (PARTS == 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
       if (i >= STAGES) mbar_wait(&empty[b], before, ok);
 #pragma unroll
@@ -383,7 +406,8 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const Lanes l(ft + h * kFeedThreads);
-          f[rb][h].put<3>(sm + L::W + b * L::WB + rb * kTileBytes, RB * kTileBytes, l.r, l.c);
+          f[h].template put<3>(sm + L::W + b * L::WB + rb * kTileBytes, RB * kTileBytes, l.r, l.c);
+          if (rb + 1 < RB) f[h].load(src + kBlock, ft + h * kFeedThreads);
         }
       if (PARTS > 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
       kl.put(sm + L::K + b * L::KB, ft);
@@ -391,15 +415,19 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       mbar_arrive(&full[b]);
     }
   } else {
-    const Lanes l(tid);
-    const uint32_t rows = ((uint32_t)(32 * l.quad) << 16) + 32 * l.half;
-    Fragment X[RB];
+    // the warp's eights of columns: of the 64, the 32 of `half` from the j0-th on; in the block's tiles, from column lc on
+    const int sub = warp >> 2, half = NV == 64 ? sub : part & 1, j0 = NV == 64 ? 0 : 2 * sub;
+    const int vt = half * 128 + (tid & 127);  // the thread of 256 whose fragments these are
+    const Lanes l(vt);
+    const int lc = NV / 2 * sub + 2 * (l.lane & 3), gc = col + 32 * half + 8 * j0 + 2 * (l.lane & 3);
+    const uint32_t rows = ((uint32_t)(32 * l.quad) << 16) + NV / 2 * sub;
+    Columns<J> X[RB];
     const float* first = REV ? d.gstateT : a.state0;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = col + l.c + (e >> 2) * 8;
+      for (int e = 0; e < 4 * J; e += 2) {
+        const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = gc + (e >> 2) * 8;
         float2 x = make_float2(0.f, 0.f);
         if (first && r < a.dk && c < a.dv) x = load_two(first + ((size_t)bh * a.dk + r) * a.dv + c);
         X[rb].v[e] = x.x, X[rb].v[e + 1] = x.y;
@@ -408,11 +436,11 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
     float* const blocks_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col * DK;
     const float* const gates = w.gates + (size_t)bh * N * kGates;
     // a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates, loaded a chunk ahead
-    Fragment B;
+    Columns<J> B;
     float g[2][3], end;
     auto fetch = [&](int n) {
       const float* q = gates + (size_t)n * kGates;
-      B.load(blocks_u + (size_t)n * C * DV, tid);
+      B.load(blocks_u + (size_t)n * C * DV, vt, j0);
 #pragma unroll
       for (int o = 0; o < 2; ++o)
 #pragma unroll
@@ -421,60 +449,41 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
     };
     fetch(REV ? N - 1 : 0);
     for (int i = 0; i < N; ++i) {
-      const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
+      const int n = REV ? N - 1 - i : i;
       const uint32_t parity = i & 1;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) X[rb].put<3>(sm + L::X, DK * 128, block_row<DK>(l, rb), l.c);
+      for (int rb = 0; rb < RB; ++rb) X[rb].template put<3>(sm + L::X, DK * 128, block_row<DK>(l, rb), lc);
       fence_async();
       fence_before();
-      bar_sync(1, kChainThreads);
-      const Operand<3, false> Wr{base + L::W + b * L::WB, RB * kTileBytes, kTileBytes};
-      const Operand<PARTS, true> Kt{base + L::K + b * L::KB, RB * kTileBytes, kTileBytes};
-      const Operand<3, true> Xs{base + L::X, DK * 128, DK * 128}, Us{base + L::U, kTileBytes, kTileBytes};
-      if (warp == 0) {
-        mbar_wait(&full[b], STAGES == 2 ? (i >> 1) & 1 : i & 1, ok);
-        fence_after();
-        if (elect()) {
-          mma<64, 64, DK>(tm, Wr, Xs);
-          commit(&done[0]);
-        }
-      }
-      // while that runs: the state goes out; in reverse its slot first gives up Qᵀ(G O')
-      Fragment F[REV ? RB : 1];
+      bar_arrive(1, kChainThreads + 32);
+      // while the product runs: the state goes out; in reverse its slot first gives up Qᵀ(G O')
+      Columns<J> F[REV ? RB : 1];
       float* Xout = blocks_x + (size_t)n * DK * DV;
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        if (REV) F[rb].load(Xout + rb * kBlock, tid);
-        else X[rb].store(Xout + rb * kBlock, tid);
+        if (REV) F[rb].load(Xout + rb * kBlock, vt, j0);
+        else X[rb].store(Xout + rb * kBlock, vt, j0);
       }
-      Fragment u, s;
+      Columns<J> u, s;
       mbar_wait(&done[0], parity, ok);
       fence_after();
       tmem_load(tm + rows, u.v);
       const float gend = end;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 4 * J; ++e) {
         const int o = (e & 2) >> 1;
         u.v[e] += B.v[e];
         s.v[e] = (REV ? -g[o][2] * g[o][0] : g[o][1]) * u.v[e];  // −β G, or E
       }
-      s.put<3>(sm + L::U, kTileBytes, l.r, l.c);
+      s.template put<3>(sm + L::U, kTileBytes, l.r, lc);
       fence_async();
       fence_before();
-      bar_sync(1, kChainThreads);
-      if (warp == 0) {
-        fence_after();
-        if (elect()) {
-          mma<DK, 64, 64>(tm + 64, Kt, Us);
-          commit(&done[1]);
-          commit(&empty[b]);
-        }
-      }
-      u.store(blocks_u + (size_t)n * C * DV, tid);
+      bar_arrive(2, kChainThreads + 32);
+      u.store(blocks_u + (size_t)n * C * DV, vt, j0);
       if (i + 1 < N) fetch(REV ? n - 1 : n + 1);
       if (REV) {
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) X[rb].store(Xout + rb * kBlock, tid);
+        for (int rb = 0; rb < RB; ++rb) X[rb].store(Xout + rb * kBlock, vt, j0);
       }
       mbar_wait(&done[1], parity, ok);
       fence_after();
@@ -482,7 +491,8 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
       for (int rb = 0; rb < RB; ++rb) {
         tmem_load(tm + 64 + rows + ((uint32_t)(16 * rb) << 16), s.v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? s.v[e] + F[REV ? rb : 0].v[e] : s.v[e]);
+        for (int e = 0; e < 4 * J; ++e)
+          X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? s.v[e] + F[REV ? rb : 0].v[e] : s.v[e]);
       }
     }
     float* last = REV ? d.gstate0 : a.stateT;
@@ -491,8 +501,8 @@ __global__ void __launch_bounds__(kChainThreads + kFeedThreads) kla_delta_chain_
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = col + l.c + (e >> 2) * 8;
+        for (int e = 0; e < 4 * J; e += 2) {
+          const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = gc + (e >> 2) * 8;
           if (r < a.dk && c < a.dv)
             store_two(last + ((size_t)bh * a.dk + r) * a.dv + c, X[rb].v[e] + bad, X[rb].v[e + 1] + bad);
         }
@@ -599,12 +609,21 @@ cudaError_t prepare_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspa
   return run(kla_delta_prepare_kernel<IO, DK, false>, PrepareSmem<IO, DK, false>::kBytes, chunks(a), kThreads, s, a,
              DeltaGradArgs{}, w);
 }
+template <typename IO, int DK, int NV>
+cudaError_t chain_nv(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, cudaStream_t s) {
+  const unsigned blocks = (unsigned)((long long)a.B * a.H * (pad64(a.dv) / NV));
+  const int smem = ChainSmem<IO, DK>::kBytes;
+  if (rev) return run(kla_delta_chain_kernel<IO, DK, true, NV>, smem, blocks, kChainBlock, s, a, *d, w);
+  return run(kla_delta_chain_kernel<IO, DK, false, NV>, smem, blocks, kChainBlock, s, a, DeltaGradArgs{}, w);
+}
 template <typename IO, int DK>
-cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, cudaStream_t s) {
-  const unsigned blocks = (unsigned)((long long)a.B * a.H * (pad64(a.dv) / 64));
-  const int threads = kChainThreads + kFeedThreads, smem = ChainSmem<IO, DK>::kBytes;
-  if (rev) return run(kla_delta_chain_kernel<IO, DK, true>, smem, blocks, threads, s, a, *d, w);
-  return run(kla_delta_chain_kernel<IO, DK, false>, smem, blocks, threads, s, a, DeltaGradArgs{}, w);
+cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, int num_sms,
+                     cudaStream_t s) {
+  // A chunk's latency bounds the chain, and blocks of 32 columns take less of it (64 tokens, d 128: 2.4 us against
+  // 3.0), as long as every block has an SM; with more heads than that W and K would be brought in twice (128 heads,
+  // d 64: 160 us against 156).
+  if ((long long)a.B * a.H * (pad64(a.dv) / 32) <= num_sms) return chain_nv<IO, DK, 32>(a, d, w, rev, s);
+  return chain_nv<IO, DK, 64>(a, d, w, rev, s);
 }
 template <typename IO, int DK>
 cudaError_t output_dk(const DeltaArgs& a, const Workspace& w, cudaStream_t s) {
@@ -642,11 +661,12 @@ cudaError_t launch_prepare(const DeltaArgs& a, const DeltaGradArgs* d, const Wor
   return wide ? prepare_dk<float, 128>(a, d, w, s) : prepare_dk<float, 64>(a, d, w, s);
 }
 
-cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, cudaStream_t s) {
+cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, int num_sms,
+                         cudaStream_t s) {
   const bool wide = pad64(a.dk) == 128;
   if (a.io == IO_BF16)
-    return wide ? chain_dk<__nv_bfloat16, 128>(a, d, w, rev, s) : chain_dk<__nv_bfloat16, 64>(a, d, w, rev, s);
-  return wide ? chain_dk<float, 128>(a, d, w, rev, s) : chain_dk<float, 64>(a, d, w, rev, s);
+    return wide ? chain_dk<__nv_bfloat16, 128>(a, d, w, rev, num_sms, s) : chain_dk<__nv_bfloat16, 64>(a, d, w, rev, num_sms, s);
+  return wide ? chain_dk<float, 128>(a, d, w, rev, num_sms, s) : chain_dk<float, 64>(a, d, w, rev, num_sms, s);
 }
 
 }  // namespace delta
@@ -660,12 +680,12 @@ size_t delta_forward_bytes(int B, int Hk, int H, int T, int dk, int dv) {
   return n;
 }
 
-cudaError_t launch_delta_forward(const DeltaArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_delta_forward(const DeltaArgs& a, int num_sms, void* workspace, cudaStream_t s) {
   if (!delta_chunked(a.T)) return launch_delta_recurrent(a, s);
   size_t n = 0;
   const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, false, &n);
   cudaError_t e = delta::launch_prepare(a, nullptr, w, s);
-  if (e == cudaSuccess) e = delta::launch_chain(a, nullptr, w, false, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, nullptr, w, false, num_sms, s);
   if (e != cudaSuccess) return e;
   const bool wide = delta::pad64(a.dk) == 128;
   if (a.io == IO_BF16)

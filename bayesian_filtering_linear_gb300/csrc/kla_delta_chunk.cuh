@@ -36,6 +36,9 @@ struct Workspace {
   float* part;   // [B·H][T][2][dk]: gradients of q and k by value head (shared key heads)
 };
 
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -119,27 +122,30 @@ template <int DK>
 __device__ __forceinline__ int block_row(const Lanes& l, int rb) {
   return (DK == 64 ? 16 * l.quad : 32 * l.quad + 16 * rb) + (l.lane >> 2);
 }
-struct Fragment {
-  float v[16];
-  __device__ __forceinline__ void load(const float* block, int tid) {
+template <int J>
+struct Columns {  // J of the four eights of columns, from the j0-th
+  float v[4 * J];
+  __device__ __forceinline__ void load(const float* block, int tid, int j0 = 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 x = reinterpret_cast<const float4*>(block)[j * 256 + tid];
+    for (int j = 0; j < J; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(block)[(j0 + j) * 256 + tid];
       v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
     }
   }
-  __device__ __forceinline__ void store(float* block, int tid) const {
+  __device__ __forceinline__ void store(float* block, int tid, int j0 = 0) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      reinterpret_cast<float4*>(block)[j * 256 + tid] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    for (int j = 0; j < J; ++j)
+      reinterpret_cast<float4*>(block)[(j0 + j) * 256 + tid] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   }
   // into a column of tiles as parts, from row r and column c
   template <int PARTS>
   __device__ __forceinline__ void put(char* tile, int part, int r, int c) const {
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) store_pair<PARTS>(tile, part, r + (e & 2) * 4, c + (e >> 2) * 8, v[e], v[e + 1]);
+    for (int e = 0; e < 4 * J; e += 2) store_pair<PARTS>(tile, part, r + (e & 2) * 4, c + (e >> 2) * 8, v[e], v[e + 1]);
   }
 };
+
+using Fragment = Columns<4>;
 
 // Four lanes that hold columns 2 q and 2 q + 1 of four eights turn them so that lane q holds all of eight q (and back).
 __device__ __forceinline__ void turn_four(uint32_t (&u)[4], int lane) {
@@ -238,8 +244,9 @@ Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, boo
 // The gates, W and M (β V); with d also Wr, Mᵀ Pᵀ O' and Qᵀ(G O').
 cudaError_t launch_prepare(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, cudaStream_t s);
 // The states before the chunks and U (rev: the gradients of the states after them and dR), one block per head
-// and 64 columns.
-cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, cudaStream_t s);
+// and 64 or 32 columns.
+cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, int num_sms,
+                         cudaStream_t s);
 
 }  // namespace delta
 }  // namespace kla

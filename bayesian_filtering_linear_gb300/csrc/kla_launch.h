@@ -152,9 +152,10 @@ cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t s);
 cudaError_t launch_delta_recurrent(const DeltaArgs& a, cudaStream_t s);
 // Whole sequences: token by token, or in chunks with `workspace`.
 size_t delta_forward_bytes(int B, int Hk, int H, int T, int dk, int dv);
-cudaError_t launch_delta_forward(const DeltaArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_delta_forward(const DeltaArgs& a, int num_sms, void* workspace, cudaStream_t s);
 size_t delta_backward_bytes(int B, int Hk, int H, int T, int dk, int dv);
-cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, void* workspace, cudaStream_t s);
+cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, int num_sms, void* workspace,
+                                  cudaStream_t s);
 
 // Norm of queries and keys with the position rotation (kla_norm_rope.cu).
 // Strides in elements, last dimension contiguous.

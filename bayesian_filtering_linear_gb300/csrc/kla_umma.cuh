@@ -84,6 +84,16 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[8]) {  // 16 lanes × 16 columns
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // ---- products -------------------------------------------------------------------
 // A tile operand of PARTS parts, `part` bytes apart, K-major (rows are M or N)
 // or MN-major (rows are K). `block`: bytes between its 64-column tiles.
