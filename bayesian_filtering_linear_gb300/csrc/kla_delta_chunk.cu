@@ -17,8 +17,9 @@
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
 // and everything that flows into them are kept in three, so that a state is as
 // exact as in fp32; the outputs of bf16 calls are made from two parts (2^-16,
-// against the 2^-8 of their rounding). Log decays are summed in 64 bits and
-// kept as two floats, so that D of late tokens is exact behind a strong decay.
+// against the 2^-8 of their rounding). Cumulative log decays are kept as sums
+// of two floats, in powers of two, so that D of late tokens is exact behind a
+// strong decay.
 #include "kla_delta_chunk.cuh"
 
 namespace kla {
@@ -46,26 +47,30 @@ __device__ __forceinline__ void four_columns(float* dst, const float* a, const f
   *reinterpret_cast<float4*>(dst + i * 68 + j) = make_float4(sign * s.x, sign * s.y, sign * s.z, sign * s.w);
 }
 
-// M = (I + A)^-1 for A strictly lower, 64 × 64 with row length 68: substitution in the 16 × 16 blocks on the diagonal,
-// then [[X, 0], [L, Y]]^-1 = [[X', 0], [−Y' L X', Y']] for 32 and 64 (X', Y' lower triangular, so the sums start at the
-// column or end at the row). L X' goes where A's upper blocks would be. Powers of A are not used: they grow like
-// binomials where keys repeat.
-__device__ void invert(float* A, float* M, int warp, int lane) {
+// M = (I + A)^-1 for A strictly lower, 64 × 64 with row length 68: substitution in the 16 × 16 blocks on the diagonal (a
+// lane per column; each entry as it is found goes into all later ones, from D, the blocks' columns), then
+// [[X, 0], [L, Y]]^-1 = [[X', 0], [−Y' L X', Y']] for 32 and 64 (X', Y' lower triangular, so the sums start at the column
+// or end at the row). L X' goes where A's upper blocks would be. Powers of A are not used: they grow like binomials where
+// keys repeat.
+constexpr int kDiagRow = 20, kDiagFloats = 4 * 16 * kDiagRow;
+__device__ void invert(float* A, float* M, const float* D, int warp, int lane) {
   if (warp < 2) {
     const int b = warp * 32 + (lane & 16), c = lane & 15;
+    const float* col = D + (b >> 4) * 16 * kDiagRow;
     float x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      x[i] = i == c ? 1.f : 0.f;
+    for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
 #pragma unroll
-      for (int s = 0; s < i; s += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(A + (b + i) * 68 + b + s);  // zero from column i on
-        x[i] = fmaf(-y.x, x[s], x[i]);
-        if (s + 1 < i) x[i] = fmaf(-y.y, x[s + 1], x[i]);
-        if (s + 2 < i) x[i] = fmaf(-y.z, x[s + 2], x[i]);
-        if (s + 3 < i) x[i] = fmaf(-y.w, x[s + 3], x[i]);
+    for (int s = 0; s < 16; ++s) {
+      M[(b + s) * 68 + b + c] = x[s];
+#pragma unroll
+      for (int i = (s + 1) & ~3; i < 16; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(col + s * kDiagRow + i);
+        if (i > s) x[i] = fmaf(-f.x, x[s], x[i]);
+        if (i + 1 > s) x[i + 1] = fmaf(-f.y, x[s], x[i + 1]);
+        if (i + 2 > s) x[i + 2] = fmaf(-f.z, x[s], x[i + 2]);
+        x[i + 3] = fmaf(-f.w, x[s], x[i + 3]);
       }
-      M[(b + i) * 68 + b + c] = x[i];
     }
   } else {
     for (int i = (warp - 2) * 32 + lane; i < 64 * 16; i += kThreads - 64) {
@@ -75,7 +80,7 @@ __device__ void invert(float* A, float* M, int warp, int lane) {
   }
   __syncthreads();
   const int o = (warp >> 1) * (32 * 68 + 32), i16 = lane & 15, j16 = ((warp & 1) * 2 + (lane >> 4)) * 4;  // two pairs of 16
-  if (warp < 4) four_columns(A + o + 16, A + o + 16 * 68, M + o, i16, j16, j16, 16, 1.f);
+  if (warp < 4) four_columns(A + o + 16, A + o + 16 * 68, M + o, i16, j16, 0, 16, 1.f);
   __syncthreads();
   if (warp < 4) four_columns(M + o + 16 * 68, M + o + 16 * 68 + 16, A + o + 16, i16, j16, 0, 16, -1.f);
   __syncthreads();
@@ -88,7 +93,7 @@ __device__ void invert(float* A, float* M, int warp, int lane) {
 template <typename IO, int DK, bool BWD>
 struct PrepareSmem {
   static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes, M3 = 3 * kTileBytes, T = DK / 64 * M3;
-  static_assert(64 * 68 * 4 <= M3, "");
+  static_assert((64 * 68 + 2 * C + kDiagFloats) * 4 <= M3, "");
   // T1 and T2: tiles on their way into products with M; T1 first holds M in fp32 (and forward K, for one product), MP
   // first A. β G K and E K for DK = 128 fill both, one after the other. In the backward pass O takes K's place.
   static constexpr int Q = 0, K = BWD ? IN : 0, P = 2 * IN, T1 = BWD ? P + M3 : 0, T2 = T1 + M3,
@@ -144,14 +149,16 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   if (warp == 0) tmem_alloc(&slot, COLS);
   if (tid == 32) mbar_init(&bar, 1);
   if (warp == 2) {  // the gates: two tokens a lane, cumulative logs as sums of two floats
-    float gh[2], gl[2] = {}, b[2];
+    float gh[2], gl[2], b[2];
     const size_t row = (size_t)at.bh * a.T + at.t0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const bool in = t < at.len;
       const float g = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.g)[row + t]) : 0.f;
-      gh[i] = g < kMinLog ? kMinLog : g;
+      const float c = g < kMinLog ? kMinLog : g;
+      gh[i] = c * kLog2e;  // in powers of two from here on
+      gl[i] = fmaf(c, kLog2e, -gh[i]) + c * kLog2eLow;
       b[i] = in ? to_f32<IO>(reinterpret_cast<const IO*>(a.beta)[row + t]) : 0.f;
     }
     add_two(gh[1], gl[1], gh[0], gl[0]);
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
       const int t = 2 * lane + i;
       float h = ph, l = pl;
       add_two(h, l, gh[i], gl[i]);
-      const float g = expf(h) * (1.f + l), e = expf((th - h) + (tl - l));
+      const float g = exp2_of(h + l), e = exp2_of((th - h) + (tl - l));
       hi[t] = h, lo[t] = l, G[t] = g, E[t] = e, be[t] = b[i];
       out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = e, out[4 * C + t] = b[i];
     }
@@ -204,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   }
   float* A = reinterpret_cast<float*>(sm + L::A);
   float* M = reinterpret_cast<float*>(sm + L::M);
+  float* diag = lo + C;
   const Lanes l(tid);
   const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
@@ -218,7 +226,13 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
     const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
     float2 D = make_float2(0.f, 0.f);
     if (below) D = make_float2(decay(hi, lo, t, s), decay(hi, lo, t, s + 1));
-    store_two(A + t * 68 + s, s < t ? be[t] * D.x * v[i] : 0.f, s + 1 < t ? be[t] * D.y * v[i + 1] : 0.f);
+    const float x = s < t ? be[t] * D.x * v[i] : 0.f, y = s + 1 < t ? be[t] * D.y * v[i + 1] : 0.f;
+    store_two(A + t * 68 + s, x, y);
+    if (half == quad >> 1 && i >> 3 == (quad & 1)) {  // of the 16 × 16 blocks on the diagonal, the columns too
+      float* p = diag + (quad * 16 + (s & 15)) * kDiagRow + (t & 15);
+      p[0] = x;
+      p[kDiagRow] = y;
+    }
     if (BWD) v[i] = D.x, v[i + 1] = D.y;
   }
   if (BWD) {  // P, scaled
@@ -232,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
     }
   }
   __syncthreads();
-  invert(A, M, warp, lane);
+  invert(A, M, diag, warp, lane);
   for (int i = tid; i < C * 8; i += kThreads) {
     const float4* p = reinterpret_cast<const float4*>(M + (i >> 3) * 68 + (i & 7) * 8);
     float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
@@ -573,11 +587,13 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   float v[16], y[16];
   tmem_load(tm + rows + 32 * half, v);
   tmem_load(tm + 64 + rows + 32 * half, y);
+  const bool below = 32 * half <= 16 * quad + 15;  // some of the warp's fragment is on or under the diagonal
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
-    store_pair<PN>(sm + L::P, kTileBytes, t, s, s <= t ? decay(hi, lo, t, s) * v[i] : 0.f,
-                   s + 1 <= t ? decay(hi, lo, t, s + 1) * v[i + 1] : 0.f);
+    float2 D = make_float2(0.f, 0.f);
+    if (below) D = make_float2(decay(hi, lo, t, s), decay(hi, lo, t, s + 1));
+    store_pair<PN>(sm + L::P, kTileBytes, t, s, s <= t ? D.x * v[i] : 0.f, s + 1 <= t ? D.y * v[i + 1] : 0.f);
   }
   fence_async();
   fence_before();

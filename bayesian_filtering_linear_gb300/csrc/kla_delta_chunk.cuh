@@ -12,7 +12,7 @@ using namespace umma;
 
 constexpr int C = 64;             // tokens of a chunk
 constexpr int kThreads = 256;     // of the kernels that take a chunk each
-constexpr int kGates = 5 * C;     // floats: cumulative g in two floats, decay from the start, to the end, β
+constexpr int kGates = 5 * C;     // floats: cumulative log2 of the decay in two, decay from the start, to the end, β
 constexpr int kMaxBytes = 227 * 1024 - 4096;  // shared memory of a block, less its static part
 constexpr float kMinLog = -104.f; // e^-104 is 0 in fp32: smaller logs change nothing but the sums' exactness
 
@@ -204,10 +204,17 @@ __device__ __forceinline__ void load_rows(const IO* in, const Lanes& l, int c0, 
   }
 }
 
-// Decay from token s to token t ≥ s of a chunk (for s > t some number, without overflow).
+constexpr float kLog2e = 1.44269504f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
+// 2^x by the hardware's instruction (2 ulp)
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Decay from token s to token t ≥ s of a chunk, from the cumulative logs (for s > t some number, without overflow).
 __device__ __forceinline__ float decay(const float* hi, const float* lo, int t, int s) {
   const float x = (hi[t] - hi[s]) + (lo[t] - lo[s]);
-  return expf(s > t ? 0.f : x);
+  return exp2_of(s > t ? 0.f : x);
 }
 
 // Everything of a block that starts a chunk: which one, and its rows.

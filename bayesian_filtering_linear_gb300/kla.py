@@ -773,8 +773,11 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
             out[name] = torch.empty_like(w)
     sums = q_weight is not None or k_weight is not None
     if workspace is None and sums:
-        with torch.cuda.device(index):
+        if index == torch.cuda.current_device():  # the size goes by the device's SMs
             nbytes = LIB.kla_norm_rope_backward_workspace_size(B, Hq, Hk, T, D)
+        else:
+            with torch.cuda.device(index):
+                nbytes = LIB.kla_norm_rope_backward_workspace_size(B, Hq, Hk, T, D)
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_CUDA, "kla_norm_rope_backward_workspace_size")
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
