@@ -92,15 +92,15 @@ __device__ void invert(float* A, float* M, const float* D, int warp, int lane) {
 
 template <typename IO, int DK, bool BWD>
 struct PrepareSmem {
-  static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes, M3 = 3 * kTileBytes, T = DK / 64 * M3;
+  static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes, ROWS = PARTS * kTileBytes;
+  static constexpr int M3 = 3 * kTileBytes;
+  // T1 first holds A (with the cumulative logs and the diagonal blocks' columns behind it), T2 the inverse in fp32
+  static constexpr int K = 0, Q = IN, V = Q + (BWD ? IN : 0), P = V + ROWS, T1 = P + (BWD ? M3 : 0), T2 = T1 + M3,
+                       A = T1, M = T2;
   static_assert((64 * 68 + 2 * C + kDiagFloats) * 4 <= M3, "");
-  // T1 and T2: tiles on their way into products with M; T1 first holds M in fp32 (and forward K, for one product), MP
-  // first A. β G K and E K for DK = 128 fill both, one after the other. In the backward pass O takes K's place.
-  static constexpr int Q = 0, K = BWD ? IN : 0, P = 2 * IN, T1 = BWD ? P + M3 : 0, T2 = T1 + M3,
-                       MP = BWD ? T2 + M3 : T1 + (T > IN ? T : IN), M = T1, A = MP;
-  static constexpr int kBytes = MP + M3;
+  static constexpr int kBytes = T2 + M3;
   static_assert(kBytes <= kMaxBytes, "");
-  static constexpr int kBlocks = kBytes <= 53 * 1024 ? 4 : kBytes <= 72 * 1024 ? 3 : kBytes <= 112 * 1024 ? 2 : 1;  // of an SM
+  static constexpr int kBlocks = kBytes <= 72 * 1024 ? 3 : kBytes <= 110 * 1024 ? 2 : 1;  // of an SM
 };
 
 // (h + l) += (yh + yl), the sum again as two floats
@@ -128,7 +128,7 @@ template <typename IO, int DK, bool BWD>
 __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) kla_delta_prepare_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                     const Workspace w) {
   using L = PrepareSmem<IO, DK, BWD>;
-  constexpr int PARTS = L::PARTS, COLS = BWD || DK == 128 ? 256 : 128, NB = DK / 64;
+  constexpr int PARTS = L::PARTS, COLS = DK == 128 ? 256 : 128, NB = DK / 64;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ float G[C], E[C], be[C];
   __shared__ uint64_t bar;
@@ -199,11 +199,11 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   publish();
   const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   const Operand<PARTS, false> Kr{base + L::K, NB * kTileBytes, kTileBytes}, Qr{base + L::Q, NB * kTileBytes, kTileBytes};
-  const Operand<PARTS, true> Qt{base + L::Q, NB * kTileBytes, kTileBytes};
-  const Operand<3, false> Mr{base + L::MP, kTileBytes, kTileBytes};
-  const Operand<3, true> Mt{base + L::MP, kTileBytes, kTileBytes}, Pt{base + L::P, kTileBytes, kTileBytes};
-  const Operand<3, true> Kb{base + L::T1, NB * kTileBytes, kTileBytes};
-  const Operand<3, true> V1{base + L::T1, kTileBytes, kTileBytes}, V2{base + L::T2, kTileBytes, kTileBytes};
+  const Operand<PARTS, true> Kt{base + L::K, NB * kTileBytes, kTileBytes}, Qt{base + L::Q, NB * kTileBytes, kTileBytes};
+  const Operand<PARTS, true> Vt{base + L::V, kTileBytes, kTileBytes};
+  const Operand<3, false> T1r{base + L::T1, kTileBytes, kTileBytes}, T2r{base + L::T2, kTileBytes, kTileBytes};
+  const Operand<3, false> Pr{base + L::P, kTileBytes, kTileBytes};
+  const Operand<3, true> T1t{base + L::T1, kTileBytes, kTileBytes}, T2t{base + L::T2, kTileBytes, kTileBytes};
   if (warp == 0 && elect()) {
     mma<64, 64, DK>(tm, Kr, Kr);
     if (BWD) mma<64, 64, DK>(tm + 64, Qr, Kr);
@@ -247,86 +247,89 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   }
   __syncthreads();
   invert(A, M, diag, warp, lane);
-  for (int i = tid; i < C * 8; i += kThreads) {
+  float m[2][8];  // two eights of M a thread
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = tid + j * kThreads;
     const float4* p = reinterpret_cast<const float4*>(M + (i >> 3) * 68 + (i & 7) * 8);
-    float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
-    store_eight<3>(sm + L::MP, kTileBytes, i >> 3, (i & 7) * 8, x);
+    const float4 x = p[0], y = p[1];
+    m[j][0] = x.x, m[j][1] = x.y, m[j][2] = x.z, m[j][3] = x.w, m[j][4] = y.x, m[j][5] = y.y, m[j][6] = y.z, m[j][7] = y.w;
   }
-  __syncthreads();  // M's place is free
-  // rows of an input times a factor, as three parts
-  auto scaled = [&](auto& tile, int W, char* to, int part, auto factor) {
+  __syncthreads();
+  // M times factors of its rows or columns, as parts: inputs are then operands as they are, exact in one part
+  auto put_m = [&](int to, auto factor) {
 #pragma unroll
-    for (int j = 0; j < tile.N; ++j) {
-      const int i = tid + j * kThreads, r = i / (W / 8), c = i % (W / 8) * 8;
+    for (int j = 0; j < 2; ++j) {
+      const int i = tid + j * kThreads, r = i >> 3, c = (i & 7) * 8;
       float x[8];
-      tile.eight(j, x);
-      const float f = factor(r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= f;
-      store_eight<3>(to + (c >> 6) * kTileBytes, part, r, c & 63, x);
+      for (int e = 0; e < 8; ++e) x[e] = m[j][e] * factor(r, c + e);
+      store_eight<3>(sm + to, kTileBytes, r, c, x);
     }
   };
-  scaled(kl, DK, sm + L::T1, NB * kTileBytes, [&](int r) { return -be[r] * G[r]; });
-  if (BWD && DK == 64) scaled(kl, DK, sm + L::T2, kTileBytes, [&](int r) { return E[r]; });
+  put_m(L::T1, [&](int, int c) { return -be[c] * G[c]; });
+  put_m(L::T2, [&](int, int c) { return be[c]; });
+  vl.put(sm + L::V, tid);
   publish();
   if (warp == 0 && elect()) {
-    mma<64, DK, 64>(tm, Mr, Kb);
-    if (BWD && DK == 64) mma<64, 64, 64>(tm + 64, Mt, V2);
+    mma<64, DK, 64>(tm, T1r, Kt);
+    mma<64, 64, 64>(tm + DK, T2r, Vt);
     commit(&bar);
   }
+  const int slices = DV / 64;
+  if (slices > 1) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, 64, tid);
   finish();
-  if (BWD && DK == 128) {
-    scaled(kl, DK, sm + L::T1, NB * kTileBytes, [&](int r) { return E[r]; });
+  float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
+  drain<64, NB>(tm, w.W + at.chunk * C * DK, l, tid, bad);
+  drain<64, 1>(tm + DK, w.U + at.chunk * C * DV, l, tid, bad);
+  if (slices > 1) {
+    vl.put(sm + L::V, tid);
     publish();
     if (warp == 0 && elect()) {
-      mma<64, DK, 64>(tm + DK, Mt, Kb);
+      mma<64, 64, 64>(tm + DK, T2r, Vt);
       commit(&bar);
     }
     finish();
+    drain<64, 1>(tm + DK, w.U + at.chunk * C * DV + kBlock, l, tid, bad);
   }
-  float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
-  drain<64, NB>(tm, w.W + at.chunk * C * DK, l, tid, bad);
-  if (BWD) drain<64, NB>(tm + DK, w.Wr + at.chunk * C * DK, l, tid, bad);
-  for (int sl = 0; sl < DV / 64; ++sl) {
-    if (sl) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, sl * 64, tid);
-    if (!BWD) {
-      scaled(vl, 64, sm + L::T1, kTileBytes, [&](int r) { return be[r]; });
-      publish();
-      if (warp == 0 && elect()) {
-        mma<64, 64, 64>(tm, Mr, V1);
-        commit(&bar);
-      }
-      finish();
-      drain<64, 1>(tm, w.U + at.chunk * C * DV + sl * kBlock, l, tid, 0.f);
-    } else {
-      const IO* go = reinterpret_cast<const IO*>(d.go);
-      TileLoad<IO, 64, kThreads> ol;
-      ol.fetch(go + (go ? vrow : 0), go ? at.len : 0, a.dv, sl * 64, tid);
-      scaled(vl, 64, sm + L::T2, kTileBytes, [&](int r) { return be[r]; });
-      ol.put(sm + L::K, tid);
-      scaled(ol, 64, sm + L::T1, kTileBytes, [&](int r) { return a.scale * G[r]; });
-      publish();
-      if (warp == 0 && elect()) {
-        mma<64, 64, 64>(tm + 64, Pt, Operand<PARTS, true>{base + L::K, kTileBytes, kTileBytes});
-        mma<64, 64, 64>(tm, Mr, V2);
-        mma<DK, 64, 64>(tm + 128, Qt, V1);
-        commit(&bar);
-      }
-      finish();
-      tmem_load(tm + 64 + rows + 32 * half, v);
+  if (BWD) {  // Mᵀ (E K) = (E M)ᵀ K, and Mᵀ Pᵀ O' = (P M)ᵀ O'
+    const IO* go = reinterpret_cast<const IO*>(d.go);
+    vl.fetch(go + (go ? vrow : 0), go ? at.len : 0, a.dv, 0, tid);
+    put_m(L::T1, [&](int r, int) { return E[r]; });
+    put_m(L::T2, [&](int, int) { return 1.f; });
+    publish();
+    if (warp == 0 && elect()) {
+      mma<64, DK, 64>(tm, T1t, Kt);
+      mma<64, 64, 64>(tm + DK, Pr, T2t);
+      commit(&bar);
+    }
+    finish();
+    drain<64, NB>(tm, w.Wr + at.chunk * C * DK, l, tid, bad);
+    Fragment pm;
+    tmem_load(tm + DK + rows + 32 * half, pm.v);
+    pm.put<3>(sm + L::T1, kTileBytes, r0, c0);
+    for (int sl = 0; sl < slices; ++sl) {
+      if (sl) vl.fetch(go + (go ? vrow : 0), go ? at.len : 0, a.dv, sl * 64, tid);
+      vl.put(sm + L::V, tid);
 #pragma unroll
-      for (int i = 0; i < 16; i += 2)  // Pᵀ O' goes on to Mᵀ Pᵀ O'
-        store_pair<3>(sm + L::T1, kTileBytes, r0 + (i & 2) * 4, c0 + (i >> 2) * 8, v[i], v[i + 1]);
+      for (int j = 0; j < vl.N; ++j) {  // G O'
+        const int i = tid + j * kThreads, r = i >> 3;
+        float x[8];
+        vl.eight(j, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= a.scale * G[r];
+        store_eight<3>(sm + L::T2, kTileBytes, r, (i & 7) * 8, x);
+      }
       publish();
       if (warp == 0 && elect()) {
-        mma<64, 64, 64>(tm + 192, Mt, V1);
+        mma<64, 64, 64>(tm, T1t, Vt);
+        mma<DK, 64, 64>(tm + 64, Qt, T2t);
         commit(&bar);
       }
-      drain<64, 1>(tm, w.U + at.chunk * C * DV + sl * kBlock, l, tid, 0.f);
-      drain<DK, NB>(tm + 128, w.Z + at.chunk * DK * DV + sl * NB * kBlock, l, tid, 0.f);
       finish();
       bad = ok ? 0.f : __int_as_float(0x7fc00000);
-      drain<64, 1>(tm + 192, w.R + at.chunk * C * DV + sl * kBlock, l, tid, bad);
+      drain<64, 1>(tm, w.R + at.chunk * C * DV + sl * kBlock, l, tid, bad);
+      drain<DK, NB>(tm + 64, w.Z + at.chunk * DK * DV + sl * NB * kBlock, l, tid, bad);
     }
   }
   fence_before();
