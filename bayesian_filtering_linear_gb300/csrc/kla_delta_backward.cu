@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
   constexpr int COLS = DK == 64 ? 256 : 512, SH = 3 * DK;      // TMEM: dQ, X, Y of DK columns, then 64 shared
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
-  __shared__ float hi[C], lo[C], G[C], E[C], be[C], rv[2][C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
+  __shared__ __align__(16) float2 logs[C];
+  __shared__ float G[C], E[C], be[C], rv[2][C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   if (tid == 32) mbar_init(&bar, 1);
   if (tid < C) {
     const float* g = w.gates + at.chunk * kGates + tid;
-    hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C], E[tid] = g[3 * C], be[tid] = g[4 * C];
+    logs[tid] = make_float2(g[0], g[C]), G[tid] = g[2 * C], E[tid] = g[3 * C], be[tid] = g[4 * C];
   }
   {
     TileLoad<IO, DK, kThreads> kl, ql;
@@ -198,11 +199,11 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   if (lane == 0) zs[warp] = z;
   // masks and decays while that runs; (dP P + dA A) goes through registers until the tiles are free
   float ww[16];
+  decays(logs, l, ww);
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int t = row_of(e), s = col_of(e) + (e & 1);
-    const float D = s <= t ? decay(hi, lo, t, s) : 0.f, strict = s < t ? D : 0.f;
-    const float p = s <= t ? a.scale * D * gp[e] : 0.f, x = s < t ? -strict * ga[e] : 0.f;
+    const float p = a.scale * ww[e] * gp[e], x = s < t ? -ww[e] * ga[e] : 0.f;
     ww[e] = s < t ? fmaf(p, qk[e], be[t] * x * kk[e]) : 0.f;
     gp[e] = p, ga[e] = x;
   }

@@ -130,11 +130,10 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   using L = PrepareSmem<IO, DK, BWD>;
   constexpr int PARTS = L::PARTS, COLS = DK == 128 ? 256 : 128, NB = DK / 64;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
-  __shared__ float G[C], E[C], be[C];
+  __shared__ __align__(16) float G[C], E[C], be[C], nbG[C];  // decays from the start and to the end, β, −β G
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
-  float* hi = reinterpret_cast<float*>(sm + L::A + 64 * 68 * 4);  // behind A, until MP comes
-  float* lo = hi + C;
+  float2* logs = reinterpret_cast<float2*>(sm + L::A + 64 * 68 * 4);  // behind A, until T1 comes
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Where at = where(a, blockIdx.x);
   const int DV = pad64(a.dv);
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
       float h = ph, l = pl;
       add_two(h, l, gh[i], gl[i]);
       const float g = exp2_of(h + l), e = exp2_of((th - h) + (tl - l));
-      hi[t] = h, lo[t] = l, G[t] = g, E[t] = e, be[t] = b[i];
+      logs[t] = make_float2(h, l), G[t] = g, E[t] = e, be[t] = b[i], nbG[t] = -b[i] * g;
       out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = e, out[4 * C + t] = b[i];
     }
   }
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   }
   float* A = reinterpret_cast<float*>(sm + L::A);
   float* M = reinterpret_cast<float*>(sm + L::M);
-  float* diag = lo + C;
+  float* diag = reinterpret_cast<float*>(logs + C);
   const Lanes l(tid);
   const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
@@ -220,30 +219,25 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   finish();
   float v[16];
   tmem_load(tm + rows + 32 * half, v);
-  const bool below = 32 * half <= 16 * quad + 15;  // some of the warp's fragment is on or under the diagonal
+  float D[16];
+  decays(logs, l, D);
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
-    float2 D = make_float2(0.f, 0.f);
-    if (below) D = make_float2(decay(hi, lo, t, s), decay(hi, lo, t, s + 1));
-    const float x = s < t ? be[t] * D.x * v[i] : 0.f, y = s + 1 < t ? be[t] * D.y * v[i + 1] : 0.f;
+    const float x = s < t ? be[t] * D[i] * v[i] : 0.f, y = s + 1 < t ? be[t] * D[i + 1] * v[i + 1] : 0.f;
     store_two(A + t * 68 + s, x, y);
     if (half == quad >> 1 && i >> 3 == (quad & 1)) {  // of the 16 × 16 blocks on the diagonal, the columns too
       float* p = diag + (quad * 16 + (s & 15)) * kDiagRow + (t & 15);
       p[0] = x;
       p[kDiagRow] = y;
     }
-    if (BWD) v[i] = D.x, v[i + 1] = D.y;
   }
   if (BWD) {  // P, scaled
-    float y[16];
-    tmem_load(tm + 64 + rows + 32 * half, y);
+    Fragment p;
+    tmem_load(tm + 64 + rows + 32 * half, p.v);
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
-      store_pair<3>(sm + L::P, kTileBytes, t, s, s <= t ? a.scale * v[i] * y[i] : 0.f,
-                    s + 1 <= t ? a.scale * v[i + 1] * y[i + 1] : 0.f);
-    }
+    for (int i = 0; i < 16; ++i) p.v[i] *= a.scale * D[i];
+    p.put<3>(sm + L::P, kTileBytes, r0, c0);
   }
   __syncthreads();
   invert(A, M, diag, warp, lane);
@@ -257,18 +251,27 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   }
   __syncthreads();
   // M times factors of its rows or columns, as parts: inputs are then operands as they are, exact in one part
-  auto put_m = [&](int to, auto factor) {
+  auto put_m = [&](int to, const float* by_column, const float* by_row) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int i = tid + j * kThreads, r = i >> 3, c = (i & 7) * 8;
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = m[j][e] * factor(r, c + e);
+      for (int e = 0; e < 8; ++e) x[e] = m[j][e];
+      if (by_column) {
+        const float4 f = *reinterpret_cast<const float4*>(by_column + c), g = *reinterpret_cast<const float4*>(by_column + c + 4);
+        x[0] *= f.x, x[1] *= f.y, x[2] *= f.z, x[3] *= f.w, x[4] *= g.x, x[5] *= g.y, x[6] *= g.z, x[7] *= g.w;
+      }
+      if (by_row) {
+        const float f = by_row[r];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= f;
+      }
       store_eight<3>(sm + to, kTileBytes, r, c, x);
     }
   };
-  put_m(L::T1, [&](int, int c) { return -be[c] * G[c]; });
-  put_m(L::T2, [&](int, int c) { return be[c]; });
+  put_m(L::T1, nbG, nullptr);
+  put_m(L::T2, be, nullptr);
   vl.put(sm + L::V, tid);
   publish();
   if (warp == 0 && elect()) {
@@ -295,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   if (BWD) {  // Mᵀ (E K) = (E M)ᵀ K, and Mᵀ Pᵀ O' = (P M)ᵀ O'
     const IO* go = reinterpret_cast<const IO*>(d.go);
     vl.fetch(go + (go ? vrow : 0), go ? at.len : 0, a.dv, 0, tid);
-    put_m(L::T1, [&](int r, int) { return E[r]; });
-    put_m(L::T2, [&](int, int) { return 1.f; });
+    put_m(L::T1, nullptr, E);
+    put_m(L::T2, nullptr, nullptr);
     publish();
     if (warp == 0 && elect()) {
       mma<64, DK, 64>(tm, T1t, Kt);
@@ -544,7 +547,8 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   using L = OutputSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
-  __shared__ float hi[C], lo[C], G[C];
+  __shared__ __align__(16) float2 logs[C];
+  __shared__ float G[C];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5);
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   ul.load(w.U + at.chunk * C * DV + col * 64, tid);
   if (tid < C) {
     const float* g = w.gates + at.chunk * kGates + tid;
-    hi[tid] = g[0], lo[tid] = g[C], G[tid] = g[2 * C];
+    logs[tid] = make_float2(g[0], g[C]), G[tid] = g[2 * C];
   }
   kl.put(sm + L::K, tid);
   ql.put(sm + L::Q, tid);
@@ -583,20 +587,19 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
     mma<64, 64, DK>(tm + 64, Qr, Operand<PN, true>{base + L::S, DK * 128, DK * 128});
     commit(&bar);
   }
-  const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
-  const uint32_t rows = (uint32_t)(32 * quad) << 16;
+  const int half = l.half;
+  const uint32_t rows = (uint32_t)(32 * l.quad) << 16;
   mbar_wait(&bar, 0, ok);
   fence_after();
   float v[16], y[16];
   tmem_load(tm + rows + 32 * half, v);
   tmem_load(tm + 64 + rows + 32 * half, y);
-  const bool below = 32 * half <= 16 * quad + 15;  // some of the warp's fragment is on or under the diagonal
+  {
+    Fragment p;
+    decays(logs, l, p.v);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const int t = r0 + (i & 2) * 4, s = c0 + (i >> 2) * 8;
-    float2 D = make_float2(0.f, 0.f);
-    if (below) D = make_float2(decay(hi, lo, t, s), decay(hi, lo, t, s + 1));
-    store_pair<PN>(sm + L::P, kTileBytes, t, s, s <= t ? D.x * v[i] : 0.f, s + 1 <= t ? D.y * v[i + 1] : 0.f);
+    for (int i = 0; i < 16; ++i) p.v[i] *= v[i];
+    p.put<PN>(sm + L::P, kTileBytes, l.r, l.c);
   }
   fence_async();
   fence_before();

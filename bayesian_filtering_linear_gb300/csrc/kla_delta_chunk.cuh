@@ -211,10 +211,25 @@ __device__ __forceinline__ float exp2_of(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Decay from token s to token t ≥ s of a chunk, from the cumulative logs (for s > t some number, without overflow).
-__device__ __forceinline__ float decay(const float* hi, const float* lo, int t, int s) {
-  const float x = (hi[t] - hi[s]) + (lo[t] - lo[s]);
-  return exp2_of(s > t ? 0.f : x);
+// The decays D_ts of a thread's fragment from the cumulative logs (zero above the diagonal).
+__device__ __forceinline__ void decays(const float2* logs, const Lanes& l, float (&D)[16]) {
+  if (32 * l.half > 16 * l.quad + 15) {  // all of the warp's fragment is above it
+#pragma unroll
+    for (int e = 0; e < 16; ++e) D[e] = 0.f;
+    return;
+  }
+  const float2 t[2] = {logs[l.r], logs[l.r + 8]};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int s = l.c + 8 * j;
+    const float4 y = *reinterpret_cast<const float4*>(logs + s);  // of tokens s and s + 1
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const float d0 = (t[o].x - y.x) + (t[o].y - y.y), d1 = (t[o].x - y.z) + (t[o].y - y.w);
+      D[4 * j + 2 * o] = s <= l.r + 8 * o ? exp2_of(d0) : 0.f;
+      D[4 * j + 2 * o + 1] = s + 1 <= l.r + 8 * o ? exp2_of(d1) : 0.f;
+    }
+  }
 }
 
 // Everything of a block that starts a chunk: which one, and its rows.
