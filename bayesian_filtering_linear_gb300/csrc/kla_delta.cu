@@ -6,8 +6,8 @@
 // A lane keeps RL rows of one column in registers, as fp32 pairs for the
 // packed arithmetic, and G = DK / RL neighbouring lanes hold a column; the
 // two dot products end in log2(G) lane exchanges. Tokens come through shared
-// memory sixteen at a time (a tile of k and q rows serves every column of
-// the block). Per state element a token costs four multiply-adds (k·S, k u,
+// memory sixteen at a time, the next sixteen on their way in registers
+// meanwhile. Per state element a token costs four multiply-adds (k·S, k u,
 // a S + k u, q·S); the chain from one token to the next is a dot product, its
 // exchanges and the update, which is what bounds a call with few heads.
 #include "kla_device.cuh"
@@ -17,13 +17,26 @@ namespace kla {
 
 namespace {
 
-constexpr int kTile = 16;  // tokens staged at a time
+constexpr int kTile = 16, kThreads = 128;  // tokens staged at a time
+
+template <typename IO>
+__device__ __forceinline__ float4 load_four(const IO* p);
+template <>
+__device__ __forceinline__ float4 load_four<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load_four<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
 
 template <typename IO, int DK>
-__global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArgs a) {
-  constexpr int RL = DK >= 64 ? 16 : DK / 4, G = DK / RL, NC = 128 / G, Q4 = RL / 4;
-  __shared__ __align__(16) float ks[kTile][DK], qs[kTile][DK], vs[kTile][NC], os[kTile][NC];
-  __shared__ float as[kTile], bs[kTile];
+__global__ void __launch_bounds__(kThreads) kla_delta_recurrent_kernel(const DeltaArgs a) {
+  constexpr int RL = DK >= 64 ? 16 : DK / 4, G = DK / RL, NC = kThreads / G, Q4 = RL / 4;
+  constexpr int NK = (kTile * DK / 4 + kThreads - 1) / kThreads;  // fours of k and of q a thread brings
+  static_assert(kTile * NC / 4 <= kThreads, "");
+  __shared__ __align__(16) float ks[2][kTile][DK], qs[2][kTile][DK], vs[2][kTile][NC], os[2][kTile][NC];
+  __shared__ float2 gates[2][kTile];  // decay, β
   const int tid = threadIdx.x, r = tid % G, c = tid / G;
   const int col_blocks = (a.dv + NC - 1) / NC;
   const long long bh = blockIdx.x / col_blocks;
@@ -34,10 +47,12 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
   const int T = a.T;
   const IO* q = reinterpret_cast<const IO*>(a.q) + key * T * DK;
   const IO* k = reinterpret_cast<const IO*>(a.k) + key * T * DK;
-  const IO* v = reinterpret_cast<const IO*>(a.v) + bh * T * a.dv;
+  const IO* v = reinterpret_cast<const IO*>(a.v) + bh * T * a.dv + c0;
   const IO* g = reinterpret_cast<const IO*>(a.g) + bh * T;
   const IO* beta = reinterpret_cast<const IO*>(a.beta) + bh * T;
-  IO* o = reinterpret_cast<IO*>(a.o) + bh * T * a.dv;
+  IO* o = reinterpret_cast<IO*>(a.o) + bh * T * a.dv + c0;
+  const int vt = tid / (NC / 4), vc = tid % (NC / 4) * 4;  // the thread's four of a tile of v and o
+  const bool vin = tid < kTile * NC / 4 && c0 + vc < a.dv;
 
   // rows of the lane: float4 groups r, r + G, ... so that G lanes read one
   // stretch of k and q
@@ -54,25 +69,51 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
       }
       S[2 * i + e] = f2_make(x, y);
     }
-  const int chunks = (T + kTile - 1) / kTile;
-  for (int n = 0; n < chunks; ++n) {
-    const int t0 = n * kTile, len = min(kTile, T - t0);
-    for (int i = tid; i < len * DK; i += 128) {
-      ks[i / DK][i % DK] = to_f32<IO>(k[(size_t)t0 * DK + i]);
-      qs[i / DK][i % DK] = a.scale * to_f32<IO>(q[(size_t)t0 * DK + i]);
+
+  float4 kx[NK], qx[NK], vx;
+  float gx = 0.f, bx = 0.f;
+  auto fetch = [&](int t0) {  // a tile's inputs into registers (zeros past the end)
+    const int len = T - t0;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int e = (tid + i * kThreads) * 4;
+      kx[i] = qx[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < kTile * DK && e / DK < len) {
+        kx[i] = load_four<IO>(k + (size_t)t0 * DK + e);
+        qx[i] = load_four<IO>(q + (size_t)t0 * DK + e);
+      }
     }
-    for (int i = tid; i < len * NC; i += 128)
-      if (c0 + i % NC < a.dv) vs[i / NC][i % NC] = to_f32<IO>(v[(size_t)(t0 + i / NC) * a.dv + c0 + i % NC]);
-    if (tid < len) {
-      as[tid] = expf(to_f32<IO>(g[t0 + tid]));
-      bs[tid] = to_f32<IO>(beta[t0 + tid]);
+    vx = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (vin && vt < len) vx = load_four<IO>(v + (size_t)(t0 + vt) * a.dv + vc);
+    if (tid < kTile) {
+      gx = tid < len ? to_f32<IO>(g[t0 + tid]) : 0.f;
+      bx = tid < len ? to_f32<IO>(beta[t0 + tid]) : 0.f;
     }
-    __syncthreads();
-    for (int t = 0; t < len; ++t) {
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int e = (tid + i * kThreads) * 4;
+      if (e < kTile * DK) {
+        *reinterpret_cast<float4*>(&ks[b][0][0] + e) = kx[i];
+        *reinterpret_cast<float4*>(&qs[b][0][0] + e) = qx[i];
+      }
+    }
+    if (tid < kTile * NC / 4) *reinterpret_cast<float4*>(&vs[b][vt][vc]) = vx;
+    if (tid < kTile) gates[b][tid] = make_float2(expf(gx), bx);
+  };
+  if (T > 0) fetch(0);
+  const int tiles = (T + kTile - 1) / kTile;
+  for (int n = 0; n < tiles; ++n) {
+    const int t0 = n * kTile, len = min(kTile, T - t0), b = n & 1;
+    put(b);
+    __syncthreads();  // (and the tile before the last is read)
+    if (n + 1 < tiles) fetch(t0 + kTile);
+    auto token = [&](int t) {
       f2 kk[2 * Q4], p0 = 0, p1 = 0;
 #pragma unroll
       for (int i = 0; i < Q4; ++i) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&ks[t][(i * G + r) * 4]);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&ks[b][t][(i * G + r) * 4]);
         kk[2 * i] = x.x;
         kk[2 * i + 1] = x.y;
         p0 = f2_fma(x.x, S[2 * i], p0);
@@ -82,12 +123,13 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
       float p = f2_lo(p0) + f2_hi(p0);
 #pragma unroll
       for (int m = 1; m < G; m <<= 1) p += __shfl_xor_sync(~0u, p, m);
-      const float decay = as[t], u = bs[t] * (vs[t][c] - decay * p);
-      const f2 u2 = f2_make(u, u), a2 = f2_make(decay, decay);
+      const float2 ab = gates[b][t];
+      const float u = ab.y * (vs[b][t][c] - ab.x * p);
+      const f2 u2 = f2_make(u, u), a2 = f2_make(ab.x, ab.x);
       f2 o0 = 0, o1 = 0;
 #pragma unroll
       for (int i = 0; i < Q4; ++i) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&qs[t][(i * G + r) * 4]);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&qs[b][t][(i * G + r) * 4]);
         S[2 * i] = f2_fma(a2, S[2 * i], f2_mul(kk[2 * i], u2));
         S[2 * i + 1] = f2_fma(a2, S[2 * i + 1], f2_mul(kk[2 * i + 1], u2));
         o0 = f2_fma(x.x, S[2 * i], o0);
@@ -97,12 +139,21 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
       float y = f2_lo(o0) + f2_hi(o0);
 #pragma unroll
       for (int m = 1; m < G; m <<= 1) y += __shfl_xor_sync(~0u, y, m);
-      if (r == 0) os[t][c] = y;
+      if (r == 0) os[b][t][c] = y;
+    };
+    if (len == kTile) {  // unrolled, so that one token's output overlaps the next one's chain
+#pragma unroll 8
+      for (int t = 0; t < kTile; ++t) token(t);
+    } else {
+      for (int t = 0; t < len; ++t) token(t);
     }
     __syncthreads();
-    if (a.o)
-      for (int i = tid; i < len * NC; i += 128)
-        if (c0 + i % NC < a.dv) o[(size_t)(t0 + i / NC) * a.dv + c0 + i % NC] = from_f32<IO>(os[i / NC][i % NC]);
+    if (vin && vt < len) {
+      const float4 y = *reinterpret_cast<const float4*>(&os[b][vt][vc]);
+      IO* p = o + (size_t)(t0 + vt) * a.dv + vc;
+      p[0] = from_f32<IO>(a.scale * y.x), p[1] = from_f32<IO>(a.scale * y.y);
+      p[2] = from_f32<IO>(a.scale * y.z), p[3] = from_f32<IO>(a.scale * y.w);
+    }
   }
   if (a.stateT && mine) {
 #pragma unroll
@@ -116,9 +167,9 @@ __global__ void __launch_bounds__(128) kla_delta_recurrent_kernel(const DeltaArg
 
 template <typename IO, int DK>
 void launch_dk(const DeltaArgs& a, cudaStream_t s) {
-  constexpr int NC = 128 / (DK >= 64 ? DK / 16 : 4);
+  constexpr int NC = kThreads / (DK >= 64 ? DK / 16 : 4);
   const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.dv + NC - 1) / NC));
-  kla_delta_recurrent_kernel<IO, DK><<<blocks, 128, 0, s>>>(a);
+  kla_delta_recurrent_kernel<IO, DK><<<blocks, kThreads, 0, s>>>(a);
 }
 
 template <typename IO>

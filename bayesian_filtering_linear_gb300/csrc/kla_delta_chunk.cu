@@ -20,6 +20,8 @@
 // against the 2^-8 of their rounding). Cumulative log decays are kept as sums
 // of two floats, in powers of two, so that D of late tokens is exact behind a
 // strong decay.
+#include <algorithm>
+
 #include "kla_delta_chunk.cuh"
 
 namespace kla {
@@ -693,17 +695,33 @@ cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Works
 
 }  // namespace delta
 
-// Few tokens are faster one by one (see kla_delta.cu); the choice depends on the length alone.
-bool delta_chunked(int T) { return T > 64; }
+// Chunks, or token by token (kla_delta.cu)? The estimated times of both, in
+// microseconds, from bf16 calls on a GB300. Token by token: 0.2 us a token, or
+// 3.1e6 elements a microsecond where heads are many (heads of few rows count as
+// 40 rows). Chunks: 20 us of launches and first waits and, by latency, 1.2 us
+// a chunk (2.3 for d_k = 128), or by work, 0.052 us a chunk and head (0.116).
+// Measured, one by one / chunks: 8 heads of 64 × 64, 64 tokens 16 / 21 us, 128
+// tokens 29 / 21; 1024 heads of 64 × 64, 64 tokens 87 / 82; 1024 heads of
+// 16 × 16, 512 tokens 129 / 435; 128 heads of 128 × 128, 64 tokens 53 / 35. Past
+// 512 tokens always chunks: one by one, a rounding per token adds up (1e-6 of
+// the state after a thousand).
+bool delta_chunked(int B, int H, int T, int dk, int dv) {
+  if (T > 512) return true;
+  const double heads = (double)B * H, chunks = (T + delta::C - 1) / delta::C;
+  const bool wide = delta::pad64(dk) == 128;
+  const double tokens = std::max(2.0 + 0.2 * T, heads * T * dv * std::max(dk, 40) / 3.1e6);
+  const double work = (wide ? 0.116 : 0.052) * heads * chunks * (delta::pad64(dv) / (wide ? 128.0 : 64.0));
+  return std::max(20.0 + (wide ? 2.3 : 1.2) * chunks, 15.0 + work) < tokens;
+}
 
 size_t delta_forward_bytes(int B, int Hk, int H, int T, int dk, int dv) {
   size_t n = 0;
-  if (delta_chunked(T)) delta::workspace(nullptr, B, Hk, H, T, dk, dv, false, &n);
+  if (delta_chunked(B, H, T, dk, dv)) delta::workspace(nullptr, B, Hk, H, T, dk, dv, false, &n);
   return n;
 }
 
 cudaError_t launch_delta_forward(const DeltaArgs& a, int num_sms, void* workspace, cudaStream_t s) {
-  if (!delta_chunked(a.T)) return launch_delta_recurrent(a, s);
+  if (!delta_chunked(a.B, a.H, a.T, a.dk, a.dv)) return launch_delta_recurrent(a, s);
   size_t n = 0;
   const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, false, &n);
   cudaError_t e = delta::launch_prepare(a, nullptr, w, s);

@@ -59,11 +59,11 @@ def test_delta_pointers(call, names, free):
 
 
 def test_delta_forward_workspace():
-    need = L.kla_delta_forward_workspace_size(1, 1, 2, 500, 16, 16)
-    assert need > 0 and forward(T=500, ws=None, ws_bytes=0) == kla.ERR_WORKSPACE
-    assert forward(T=500, ws_bytes=need - 1) == kla.ERR_WORKSPACE
-    assert forward(T=500, ws=A + 16) == kla.ERR_INVALID_ARG  # on q
-    assert L.kla_delta_forward_workspace_size(1, 2, 3, 500, 16, 16) == ctypes.c_size_t(-1).value
+    need = L.kla_delta_forward_workspace_size(1, 1, 2, 600, 16, 16)
+    assert need > 0 and forward(T=600, ws=None, ws_bytes=0) == kla.ERR_WORKSPACE
+    assert forward(T=600, ws_bytes=need - 1) == kla.ERR_WORKSPACE
+    assert forward(T=600, ws=A + 16) == kla.ERR_INVALID_ARG  # on q
+    assert L.kla_delta_forward_workspace_size(1, 2, 3, 600, 16, 16) == ctypes.c_size_t(-1).value
 
 
 def test_delta_backward_workspace():
