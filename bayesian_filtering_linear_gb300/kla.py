@@ -761,13 +761,12 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
     for n, (name, x) in enumerate((("gq", q), ("gk", k))):
         if x is None:
             continue
-        if x.is_contiguous():
-            out[name] = torch.empty_like(x)
-        else:
+        g = torch.empty_like(x)  # a dense view's own strides; of a view with gaps, contiguous
+        if g.stride() != x.stride() and x.numel():
             order = sorted(range(3), key=x.stride().__getitem__, reverse=True)
             back = [order.index(d) for d in range(3)]
-            out[name] = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=q.device).permute(*back, 3)
-            gstrides[n] = _Strides(*out[name].stride()[:3])
+            g = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=q.device).permute(*back, 3)
+        out[name], gstrides[n] = g, _Strides(*g.stride()[:3])
     for name, w in (("gq_weight", q_weight), ("gk_weight", k_weight)):
         if w is not None:
             out[name] = torch.empty_like(w)
