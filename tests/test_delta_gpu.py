@@ -114,6 +114,20 @@ def test_backward_long(io):
     check_backward(problem(1, 1, 2, 700, 64, 64, io, seed=4, decay=0.05), io)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 2, 513, 128, 128), (1, 2, 2, 640, 128, 64), (2, 1, 1, 705, 128, 16)])
+def test_wide_keys_over_many_chunks(shape, io):
+    """Few heads of d_k = 128 and more than eight chunks, forward and from the end."""
+    p = problem(*shape, io, seed=sum(shape), decay=0.05)
+    p["g"][:, :, 100:102] = -float("inf")
+    p["g"][:, :, 448] = -60.0
+    check_forward(p, io)
+    check_backward(p, io)
+    p["state0"] = None
+    check_forward(p, io)
+    check_backward(p, io, gs=False)
+
+
 def hard(name, p):
     if name == "resets":            # decays of exactly zero, alone and side by side, at chunk borders too
         for t in (0, 5, 15, 16, 63, 64, 65, 99):
