@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   auto row_of = [&](int e) { return r0 + (e & 2) * 4; };
   auto col_of = [&](int e) { return c0 + (e >> 2) * 8; };
 
-  if (tid == 0) {  // A and P before their decays, where dQ and X come later
+  if (warp == 0 && elect()) {  // A and P before their decays, where dQ and X come later
     mma<64, 64, DK>(tm, Kr, Kr);
     mma<64, 64, DK>(tm + 64, Qr, Kr);
     commit(&bar);
@@ -369,8 +369,7 @@ cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, in
   size_t n = 0;
   const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, true, &n);
   cudaError_t e = delta::launch_prepare(a, &g, w, s);
-  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, false, num_sms, s);
-  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, true, num_sms, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, &g, w, num_sms, s);
   if (e != cudaSuccess) return e;
   const bool wide = delta::pad64(a.dk) == 128;
   if (a.io == IO_BF16)

@@ -349,25 +349,25 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
 // Eight warps walk the chunks, each with a quarter of the rows and half of the
 // columns; four more bring K and W of the next chunk as parts, two chunks deep
 // where shared memory holds them; one issues the products.
-constexpr int kChainThreads = 256, kFeedThreads = 128, kChainBlock = kChainThreads + kFeedThreads + 32;
+constexpr int kChainThreads = 256, kFeedThreads = 256, kChainBlock = kChainThreads + kFeedThreads + 32;
 
-template <typename IO, int DK>
+template <typename IO, int DK, int NV>
 struct ChainSmem {
   static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, WB = 3 * DK / 64 * kTileBytes;
   static constexpr int STAGES = sizeof(IO) == 4 && DK == 128 ? 1 : 2;
-  static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + 3 * DK * 128,
-                       kBytes = U + 3 * kTileBytes;
+  static constexpr int kIn = NV * C * 4, kGate = 3 * C * 4;  // a chunk's M (β V), gates
+  static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + 3 * DK * 128, B = U + 3 * kTileBytes,
+                       G = B + kIn, kBytes = G + kGate;
   static_assert(kBytes <= kMaxBytes, "");
 };
 
 // NV: columns of a block, 64 or 32.
 template <typename IO, int DK, bool REV, int NV>
-__global__ void __launch_bounds__(kChainBlock)
-    kla_delta_chain_kernel(const DeltaArgs a, const DeltaGradArgs d, const Workspace w) {
-  using L = ChainSmem<IO, DK>;
+__device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d, const Workspace& w) {
+  using L = ChainSmem<IO, DK, NV>;
   constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES, J = NV / 16;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
-  __shared__ uint64_t full[STAGES], empty[STAGES], done[2];
+  __shared__ uint64_t full[STAGES], empty[STAGES], done[2], loaded;
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5);
   const int DV = pad64(a.dv), N = (a.T + C - 1) / C;
@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(kChainBlock)
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], kFeedThreads), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
+    mbar_init(&loaded, 1);
   }
   if (warp == 0) tmem_alloc(&slot, 128);
   fence_async();
@@ -385,7 +386,20 @@ __global__ void __launch_bounds__(kChainBlock)
   fence_after();
   const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
-  if (warp == kChainBlock / 32 - 1) {  // the products
+  float* const blocks_u = (REV ? w.R : w.U) + (size_t)bh * N * C * DV + col * 64;
+  if (warp == kChainBlock / 32 - 1) {  // the products, and a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates a chunk ahead
+    auto bring = [&](int n) {
+      const float *u = blocks_u + (size_t)n * C * DV, *g = w.gates + ((size_t)bh * N + n) * kGates + 2 * C;
+      mbar_expect(&loaded, L::kIn + L::kGate);
+      bulk_copy(base + L::G, g, L::kGate, &loaded);
+      if (NV == 64) {
+        bulk_copy(base + L::B, u, L::kIn, &loaded);
+      } else {  // the half's threads of each eight of columns
+        for (int j = 0; j < 4; ++j) bulk_copy(base + L::B + j * 2048, u + j * 1024 + (part & 1) * 512, 2048, &loaded);
+      }
+    };
+    if (elect()) bring(REV ? N - 1 : 0);
+    __syncwarp();
     for (int i = 0; i < N; ++i) {
       const int b = STAGES == 2 ? i & 1 : 0;
       const Operand<3, false> Wr{base + L::W + b * L::WB, RB * kTileBytes, kTileBytes};
@@ -405,9 +419,12 @@ __global__ void __launch_bounds__(kChainBlock)
         mma<DK, NV, 64>(tm + 64, Kt, Us);
         commit(&done[1]);
         commit(&empty[b]);
+        if (i + 1 < N) bring(REV ? N - 2 - i : i + 1);
       }
       __syncwarp();
     }
+    bool in = true;
+    mbar_wait(&loaded, (N - 1) & 1, in);  // no copy is in flight when the block ends, also where a wait ran out
   } else if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
     const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
@@ -416,22 +433,16 @@ __global__ void __launch_bounds__(kChainBlock)
       const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
       const uint32_t before = STAGES == 2 ? ((i >> 1) - 1) & 1 : (i - 1) & 1;
       TileLoad<IO, DK, kFeedThreads> kl;
-      Fragment f[2];  // what the threads of the two halves of columns hold
+      Fragment f[RB];
       // what registers hold comes in ahead of the wait for its place
-      const float* src = W + (size_t)n * C * DK;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) f[h].load(src, ft + h * kFeedThreads);
-      if (PARTS == 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
+      for (int rb = 0; rb < RB; ++rb) f[rb].load(W + (size_t)n * C * DK + rb * kBlock, ft);
+      kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
       if (i >= STAGES) mbar_wait(&empty[b], before, ok);
+      const Lanes l(ft);
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const Lanes l(ft + h * kFeedThreads);
-          f[h].template put<3>(sm + L::W + b * L::WB + rb * kTileBytes, RB * kTileBytes, l.r, l.c);
-          if (rb + 1 < RB) f[h].load(src + kBlock, ft + h * kFeedThreads);
-        }
-      if (PARTS > 1) kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
+        f[rb].template put<3>(sm + L::W + b * L::WB + rb * kTileBytes, RB * kTileBytes, l.r, l.c);
       kl.put(sm + L::K + b * L::KB, ft);
       fence_async();
       mbar_arrive(&full[b]);
@@ -454,22 +465,9 @@ __global__ void __launch_bounds__(kChainBlock)
         if (first && r < a.dk && c < a.dv) x = load_two(first + ((size_t)bh * a.dk + r) * a.dv + c);
         X[rb].v[e] = x.x, X[rb].v[e + 1] = x.y;
       }
-    float* const blocks_u = (REV ? w.R : w.U) + (size_t)bh * N * C * DV + col * 64;
     float* const blocks_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col * DK;
-    const float* const gates = w.gates + (size_t)bh * N * kGates;
-    // a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates, loaded a chunk ahead
-    Columns<J> B;
-    float g[2][3], end;
-    auto fetch = [&](int n) {
-      const float* q = gates + (size_t)n * kGates;
-      B.load(blocks_u + (size_t)n * C * DV, vt, j0);
-#pragma unroll
-      for (int o = 0; o < 2; ++o)
-#pragma unroll
-        for (int m = 0; m < 3; ++m) g[o][m] = q[(2 + m) * C + l.r + 8 * o];
-      end = q[3 * C - 1];
-    };
-    fetch(REV ? N - 1 : 0);
+    const float* const gates = reinterpret_cast<const float*>(sm + L::G);
+    const float4* const in = reinterpret_cast<const float4*>(sm + L::B) + (NV == 64 ? vt : vt & 127);
     for (int i = 0; i < N; ++i) {
       const int n = REV ? N - 1 - i : i;
       const uint32_t parity = i & 1;
@@ -490,19 +488,26 @@ __global__ void __launch_bounds__(kChainBlock)
       mbar_wait(&done[0], parity, ok);
       fence_after();
       tmem_load(tm + rows, u.v);
-      const float gend = end;
+      mbar_wait(&loaded, parity, ok);
+      const float gend = gates[C - 1];
+      float g[2];  // −β G, or E
 #pragma unroll
-      for (int e = 0; e < 4 * J; ++e) {
-        const int o = (e & 2) >> 1;
-        u.v[e] += B.v[e];
-        s.v[e] = (REV ? -g[o][2] * g[o][0] : g[o][1]) * u.v[e];  // −β G, or E
+      for (int o = 0; o < 2; ++o) {
+        const float* q = gates + l.r + 8 * o;
+        g[o] = REV ? -q[2 * C] * q[0] : q[C];
       }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float4 x = in[(j0 + j) * (NV * 4)];
+        u.v[4 * j] += x.x, u.v[4 * j + 1] += x.y, u.v[4 * j + 2] += x.z, u.v[4 * j + 3] += x.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4 * J; ++e) s.v[e] = g[(e & 2) >> 1] * u.v[e];
       s.template put<3>(sm + L::U, kTileBytes, l.r, lc);
       fence_async();
       fence_before();
       bar_arrive(2, kChainThreads + 32);
       u.store(blocks_u + (size_t)n * C * DV, vt, j0);
-      if (i + 1 < N) fetch(REV ? n - 1 : n + 1);
       if (REV) {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) X[rb].store(Xout + rb * kBlock, vt, j0);
@@ -533,6 +538,14 @@ __global__ void __launch_bounds__(kChainBlock)
   fence_before();
   __syncthreads();
   if (warp == 0) tmem_free(tm, 128);
+}
+
+// BOTH: a second row of blocks walks the reverse chain, which needs nothing of the forward one.
+template <typename IO, int DK, bool BOTH, int NV>
+__global__ void __launch_bounds__(kChainBlock)
+    kla_delta_chain_kernel(const DeltaArgs a, const DeltaGradArgs d, const Workspace w) {
+  if (BOTH && blockIdx.y == 1) chain<IO, DK, true, NV>(a, d, w);
+  else chain<IO, DK, false, NV>(a, d, w);
 }
 
 // ---- the output ----------------------------------------------------------------------
@@ -634,20 +647,19 @@ cudaError_t prepare_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspa
              DeltaGradArgs{}, w);
 }
 template <typename IO, int DK, int NV>
-cudaError_t chain_nv(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, cudaStream_t s) {
+cudaError_t chain_nv(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, cudaStream_t s) {
   const unsigned blocks = (unsigned)((long long)a.B * a.H * (pad64(a.dv) / NV));
-  const int smem = ChainSmem<IO, DK>::kBytes;
-  if (rev) return run(kla_delta_chain_kernel<IO, DK, true, NV>, smem, blocks, kChainBlock, s, a, *d, w);
+  const int smem = ChainSmem<IO, DK, NV>::kBytes;
+  if (d) return run(kla_delta_chain_kernel<IO, DK, true, NV>, smem, dim3(blocks, 2), kChainBlock, s, a, *d, w);
   return run(kla_delta_chain_kernel<IO, DK, false, NV>, smem, blocks, kChainBlock, s, a, DeltaGradArgs{}, w);
 }
 template <typename IO, int DK>
-cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, int num_sms,
-                     cudaStream_t s) {
+cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, int num_sms, cudaStream_t s) {
   // A chunk's latency bounds the chain, and blocks of 32 columns take less of it (64 tokens, d 128: 2.4 us against
   // 3.0), as long as every block has an SM; with more heads than that W and K would be brought in twice (128 heads,
   // d 64: 160 us against 156).
-  if ((long long)a.B * a.H * (pad64(a.dv) / 32) <= num_sms) return chain_nv<IO, DK, 32>(a, d, w, rev, s);
-  return chain_nv<IO, DK, 64>(a, d, w, rev, s);
+  if ((long long)a.B * a.H * (pad64(a.dv) / 32) * (d ? 2 : 1) <= num_sms) return chain_nv<IO, DK, 32>(a, d, w, s);
+  return chain_nv<IO, DK, 64>(a, d, w, s);
 }
 template <typename IO, int DK>
 cudaError_t output_dk(const DeltaArgs& a, const Workspace& w, cudaStream_t s) {
@@ -685,12 +697,11 @@ cudaError_t launch_prepare(const DeltaArgs& a, const DeltaGradArgs* d, const Wor
   return wide ? prepare_dk<float, 128>(a, d, w, s) : prepare_dk<float, 64>(a, d, w, s);
 }
 
-cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, int num_sms,
-                         cudaStream_t s) {
+cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, int num_sms, cudaStream_t s) {
   const bool wide = pad64(a.dk) == 128;
   if (a.io == IO_BF16)
-    return wide ? chain_dk<__nv_bfloat16, 128>(a, d, w, rev, num_sms, s) : chain_dk<__nv_bfloat16, 64>(a, d, w, rev, num_sms, s);
-  return wide ? chain_dk<float, 128>(a, d, w, rev, num_sms, s) : chain_dk<float, 64>(a, d, w, rev, num_sms, s);
+    return wide ? chain_dk<__nv_bfloat16, 128>(a, d, w, num_sms, s) : chain_dk<__nv_bfloat16, 64>(a, d, w, num_sms, s);
+  return wide ? chain_dk<float, 128>(a, d, w, num_sms, s) : chain_dk<float, 64>(a, d, w, num_sms, s);
 }
 
 }  // namespace delta
@@ -725,7 +736,7 @@ cudaError_t launch_delta_forward(const DeltaArgs& a, int num_sms, void* workspac
   size_t n = 0;
   const delta::Workspace w = delta::workspace(workspace, a.B, a.Hk, a.H, a.T, a.dk, a.dv, false, &n);
   cudaError_t e = delta::launch_prepare(a, nullptr, w, s);
-  if (e == cudaSuccess) e = delta::launch_chain(a, nullptr, w, false, num_sms, s);
+  if (e == cudaSuccess) e = delta::launch_chain(a, nullptr, w, num_sms, s);
   if (e != cudaSuccess) return e;
   const bool wide = delta::pad64(a.dk) == 128;
   if (a.io == IO_BF16)

@@ -253,7 +253,7 @@ __device__ __forceinline__ Where where(const DeltaArgs& a, long long chunk) {
 // Launches with dynamic shared memory; all of an SM's L1 is asked for as shared memory, so that as many blocks fit as
 // their sizes allow.
 template <typename F, typename... Args>
-cudaError_t run(F kernel, int smem, unsigned blocks, int threads, cudaStream_t s, const Args&... args) {
+cudaError_t run(F kernel, int smem, dim3 blocks, int threads, cudaStream_t s, const Args&... args) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
@@ -265,10 +265,9 @@ cudaError_t run(F kernel, int smem, unsigned blocks, int threads, cudaStream_t s
 Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, bool backward, size_t* bytes);
 // The gates, W and M (β V); with d also Wr, Mᵀ Pᵀ O' and Qᵀ(G O').
 cudaError_t launch_prepare(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, cudaStream_t s);
-// The states before the chunks and U (rev: the gradients of the states after them and dR), one block per head
-// and 64 or 32 columns.
-cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, bool rev, int num_sms,
-                         cudaStream_t s);
+// The states before the chunks and U, with d also the gradients of the states after them and dR: one block per head
+// and 64 or 32 columns, and direction.
+cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, int num_sms, cudaStream_t s);
 
 }  // namespace delta
 }  // namespace kla
