@@ -355,9 +355,9 @@ template <typename IO, int DK, int NV>
 struct ChainSmem {
   static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, WB = 3 * DK / 64 * kTileBytes;
   static constexpr int STAGES = sizeof(IO) == 4 && DK == 128 ? 1 : 2;
-  static constexpr int kIn = NV * C * 4, kGate = 3 * C * 4;  // a chunk's M (β V), gates
+  static constexpr int IN = NV * C * 4, GATES = 3 * C * 4;  // a chunk's M (β V), gates
   static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + 3 * DK * 128, B = U + 3 * kTileBytes,
-                       G = B + kIn, kBytes = G + kGate;
+                       AHEAD = B + 2 * (IN + GATES) <= kMaxBytes ? 2 : 1, kBytes = B + AHEAD * (IN + GATES);
   static_assert(kBytes <= kMaxBytes, "");
 };
 
@@ -367,7 +367,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
   using L = ChainSmem<IO, DK, NV>;
   constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES, J = NV / 16;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
-  __shared__ uint64_t full[STAGES], empty[STAGES], done[2], loaded;
+  __shared__ uint64_t full[STAGES], empty[STAGES], done[2], loaded[L::AHEAD];
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5);
   const int DV = pad64(a.dv), N = (a.T + C - 1) / C;
@@ -377,7 +377,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], kFeedThreads), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
-    mbar_init(&loaded, 1);
+    for (int i = 0; i < L::AHEAD; ++i) mbar_init(&loaded[i], 1);
   }
   if (warp == 0) tmem_alloc(&slot, 128);
   fence_async();
@@ -387,18 +387,22 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
   const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
   float* const blocks_u = (REV ? w.R : w.U) + (size_t)bh * N * C * DV + col * 64;
-  if (warp == kChainBlock / 32 - 1) {  // the products, and a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates a chunk ahead
-    auto bring = [&](int n) {
+  if (warp == kChainBlock / 32 - 1) {  // the products, and a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates one or two chunks ahead
+    auto bring = [&](int i) {
+      if (i >= N) return;
+      const int n = REV ? N - 1 - i : i, b = i % L::AHEAD;
       const float *u = blocks_u + (size_t)n * C * DV, *g = w.gates + ((size_t)bh * N + n) * kGates + 2 * C;
-      mbar_expect(&loaded, L::kIn + L::kGate);
-      bulk_copy(base + L::G, g, L::kGate, &loaded);
+      const uint32_t to = base + L::B + b * (L::IN + L::GATES);
+      mbar_expect(&loaded[b], L::IN + L::GATES);
+      bulk_copy(to + L::IN, g, L::GATES, &loaded[b]);
       if (NV == 64) {
-        bulk_copy(base + L::B, u, L::kIn, &loaded);
+        bulk_copy(to, u, L::IN, &loaded[b]);
       } else {  // the half's threads of each eight of columns
-        for (int j = 0; j < 4; ++j) bulk_copy(base + L::B + j * 2048, u + j * 1024 + (part & 1) * 512, 2048, &loaded);
+        for (int j = 0; j < 4; ++j) bulk_copy(to + j * 2048, u + j * 1024 + (part & 1) * 512, 2048, &loaded[b]);
       }
     };
-    if (elect()) bring(REV ? N - 1 : 0);
+    if (elect())
+      for (int i = 0; i < L::AHEAD; ++i) bring(i);
     __syncwarp();
     for (int i = 0; i < N; ++i) {
       const int b = STAGES == 2 ? i & 1 : 0;
@@ -419,12 +423,12 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         mma<DK, NV, 64>(tm + 64, Kt, Us);
         commit(&done[1]);
         commit(&empty[b]);
-        if (i + 1 < N) bring(REV ? N - 2 - i : i + 1);
+        bring(i + L::AHEAD);
       }
       __syncwarp();
     }
-    bool in = true;
-    mbar_wait(&loaded, (N - 1) & 1, in);  // no copy is in flight when the block ends, also where a wait ran out
+    bool in = true;  // no copy is in flight when the block ends, also where a wait ran out
+    for (int i = max(N - L::AHEAD, 0); i < N; ++i) mbar_wait(&loaded[i % L::AHEAD], i / L::AHEAD & 1, in);
   } else if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
     const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
@@ -466,8 +470,6 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         X[rb].v[e] = x.x, X[rb].v[e + 1] = x.y;
       }
     float* const blocks_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col * DK;
-    const float* const gates = reinterpret_cast<const float*>(sm + L::G);
-    const float4* const in = reinterpret_cast<const float4*>(sm + L::B) + (NV == 64 ? vt : vt & 127);
     for (int i = 0; i < N; ++i) {
       const int n = REV ? N - 1 - i : i;
       const uint32_t parity = i & 1;
@@ -488,7 +490,10 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       mbar_wait(&done[0], parity, ok);
       fence_after();
       tmem_load(tm + rows, u.v);
-      mbar_wait(&loaded, parity, ok);
+      const char* const brought = sm + L::B + i % L::AHEAD * (L::IN + L::GATES);
+      const float4* const in = reinterpret_cast<const float4*>(brought) + (NV == 64 ? vt : vt & 127);
+      const float* const gates = reinterpret_cast<const float*>(brought + L::IN);
+      mbar_wait(&loaded[i % L::AHEAD], i / L::AHEAD & 1, ok);
       const float gend = gates[C - 1];
       float g[2];  // −β G, or E
 #pragma unroll
