@@ -126,6 +126,36 @@ __device__ __forceinline__ void drain(uint32_t tm, float* out, const Lanes& l, i
   }
 }
 
+// 64 × 64 BLOCKS of a product as tiles of three parts, [part][block]. A lane's four words of a row turn into one eight.
+template <int BLOCKS>
+__device__ __forceinline__ void drain_parts(uint32_t tm, char* out, const Lanes& l, float bad) {
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b) {
+    Fragment f;
+    tmem_load(tm + ((uint32_t)(32 * l.quad) << 16) + 64 * b + 32 * l.half, f.v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f.v[i] += bad;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const int r = l.r + 8 * o, c = 4 * l.half + (l.lane & 3);
+      char* to = out + b * kTileBytes + r * 128 + (((c ^ r) & 7) << 4);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float &x = f.v[4 * j + 2 * o], &y = f.v[4 * j + 2 * o + 1];
+          u[j] = bf16_pair(x, y);
+          x -= __uint_as_float(u[j] << 16);
+          y -= __uint_as_float(u[j] & 0xffff0000u);
+        }
+        turn_four(u, l.lane);
+        *reinterpret_cast<uint4*>(to + p * BLOCKS * kTileBytes) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  }
+}
+
 template <typename IO, int DK, bool BWD>
 __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) kla_delta_prepare_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                     const Workspace w) {
@@ -285,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   if (slices > 1) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, 64, tid);
   finish();
   float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
-  drain<64, NB>(tm, w.W + at.chunk * C * DK, l, tid, bad);
+  drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l, bad);
   drain<64, 1>(tm + DK, w.U + at.chunk * C * DV, l, tid, bad);
   if (slices > 1) {
     vl.put(sm + L::V, tid);
@@ -309,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
       commit(&bar);
     }
     finish();
-    drain<64, NB>(tm, w.Wr + at.chunk * C * DK, l, tid, bad);
+    drain_parts<NB>(tm, w.Wr + at.chunk * 3 * NB * kTileBytes, l, bad);
     Fragment pm;
     tmem_load(tm + DK + rows + 32 * half, pm.v);
     pm.put<3>(sm + L::T1, kTileBytes, r0, c0);
@@ -347,9 +377,13 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
 //   forward:  U = M (β V) + W X,       X = G_end X + Kᵀ(E U)
 //   reverse:  dR = Mᵀ Pᵀ O' + W X,     X = G_end X + Qᵀ(G O') − Kᵀ(β G dR)
 // Eight warps walk the chunks, each with a quarter of the rows and half of the
-// columns; four more bring K and W of the next chunk as parts, two chunks deep
-// where shared memory holds them; one issues the products.
-constexpr int kChainThreads = 256, kFeedThreads = 256, kChainBlock = kChainThreads + kFeedThreads + 32;
+// columns; others bring K (fp32: as parts, twice the warps) and W of the next
+// chunk, two chunks deep where shared memory holds them; one issues the products.
+constexpr int kChainThreads = 256;
+template <typename IO>
+constexpr int kFeedThreads = 128 * (sizeof(IO) / 2);
+template <typename IO>
+constexpr int kChainBlock = kChainThreads + kFeedThreads<IO> + 32;
 
 template <typename IO, int DK, int NV>
 struct ChainSmem {
@@ -365,7 +399,7 @@ struct ChainSmem {
 template <typename IO, int DK, bool REV, int NV>
 __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d, const Workspace& w) {
   using L = ChainSmem<IO, DK, NV>;
-  constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES, J = NV / 16;
+  constexpr int PARTS = kParts<IO>, RB = DK / 64, STAGES = L::STAGES, FEED = kFeedThreads<IO>, J = NV / 16;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ uint64_t full[STAGES], empty[STAGES], done[2], loaded[L::AHEAD];
   __shared__ uint32_t slot;
@@ -375,7 +409,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
   const int part = (int)(blockIdx.x % (DV / NV)), col = part * NV / 64 * 64;  // the 64 columns it is in
   const long long key = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], kFeedThreads), mbar_init(&empty[i], 1);
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], FEED + 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
     for (int i = 0; i < L::AHEAD; ++i) mbar_init(&loaded[i], 1);
   }
@@ -387,7 +421,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
   const uint32_t tm = uniform(slot), base = uniform(smem_addr(sm));
   bool ok = true;
   float* const blocks_u = (REV ? w.R : w.U) + (size_t)bh * N * C * DV + col * 64;
-  if (warp == kChainBlock / 32 - 1) {  // the products, and a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates one or two chunks ahead
+  if (warp == kChainBlock<IO> / 32 - 1) {  // the products, and a chunk's M (β V) (rev: Mᵀ Pᵀ O') and gates one or two chunks ahead
     auto bring = [&](int i) {
       if (i >= N) return;
       const int n = REV ? N - 1 - i : i, b = i % L::AHEAD;
@@ -428,25 +462,22 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       __syncwarp();
     }
     bool in = true;  // no copy is in flight when the block ends, also where a wait ran out
+    for (int i = max(N - STAGES, 0); i < N; ++i) mbar_wait(&full[i % STAGES], i / STAGES & 1, in);
     for (int i = max(N - L::AHEAD, 0); i < N; ++i) mbar_wait(&loaded[i % L::AHEAD], i / L::AHEAD & 1, in);
   } else if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
     const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
-    const float* W = (REV ? w.Wr : w.W) + (size_t)bh * N * C * DK;
+    const char* W = (REV ? w.Wr : w.W) + (size_t)bh * N * L::WB;
     for (int i = 0; i < N; ++i) {
       const int n = REV ? N - 1 - i : i, b = STAGES == 2 ? i & 1 : 0;
       const uint32_t before = STAGES == 2 ? ((i >> 1) - 1) & 1 : (i - 1) & 1;
-      TileLoad<IO, DK, kFeedThreads> kl;
-      Fragment f[RB];
-      // what registers hold comes in ahead of the wait for its place
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) f[rb].load(W + (size_t)n * C * DK + rb * kBlock, ft);
+      TileLoad<IO, DK, FEED> kl;  // comes in ahead of the wait for its place
       kl.fetch(k + (size_t)n * C * a.dk, min(C, a.T - n * C), a.dk, 0, ft);
       if (i >= STAGES) mbar_wait(&empty[b], before, ok);
-      const Lanes l(ft);
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-        f[rb].template put<3>(sm + L::W + b * L::WB + rb * kTileBytes, RB * kTileBytes, l.r, l.c);
+      if (ft == 0) {
+        mbar_expect(&full[b], L::WB);
+        bulk_copy(base + L::W + b * L::WB, W + (size_t)n * L::WB, L::WB, &full[b]);
+      }
       kl.put(sm + L::K + b * L::KB, ft);
       fence_async();
       mbar_arrive(&full[b]);
@@ -547,7 +578,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
 
 // BOTH: a second row of blocks walks the reverse chain, which needs nothing of the forward one.
 template <typename IO, int DK, bool BOTH, int NV>
-__global__ void __launch_bounds__(kChainBlock)
+__global__ void __launch_bounds__(kChainBlock<IO>)
     kla_delta_chain_kernel(const DeltaArgs a, const DeltaGradArgs d, const Workspace w) {
   if (BOTH && blockIdx.y == 1) chain<IO, DK, true, NV>(a, d, w);
   else chain<IO, DK, false, NV>(a, d, w);
@@ -655,8 +686,8 @@ template <typename IO, int DK, int NV>
 cudaError_t chain_nv(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, cudaStream_t s) {
   const unsigned blocks = (unsigned)((long long)a.B * a.H * (pad64(a.dv) / NV));
   const int smem = ChainSmem<IO, DK, NV>::kBytes;
-  if (d) return run(kla_delta_chain_kernel<IO, DK, true, NV>, smem, dim3(blocks, 2), kChainBlock, s, a, *d, w);
-  return run(kla_delta_chain_kernel<IO, DK, false, NV>, smem, blocks, kChainBlock, s, a, DeltaGradArgs{}, w);
+  if (d) return run(kla_delta_chain_kernel<IO, DK, true, NV>, smem, dim3(blocks, 2), kChainBlock<IO>, s, a, *d, w);
+  return run(kla_delta_chain_kernel<IO, DK, false, NV>, smem, blocks, kChainBlock<IO>, s, a, DeltaGradArgs{}, w);
 }
 template <typename IO, int DK>
 cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, int num_sms, cudaStream_t s) {
@@ -683,11 +714,12 @@ Workspace workspace(void* base, int B, int Hk, int H, int T, int dk, int dv, boo
   };
   Workspace w{};
   w.gates = take(n * kGates);
-  w.W = take(n * C * DK);
+  const size_t tiles = n * C * DK * 3 / 2;  // floats of three parts
+  w.W = reinterpret_cast<char*>(take(tiles));
   w.S = take(n * DK * DV);
   w.U = take(n * C * DV);
   if (backward) {
-    w.Wr = take(n * C * DK);
+    w.Wr = reinterpret_cast<char*>(take(tiles));
     w.Z = take(n * DK * DV);
     w.R = take(n * C * DV);
     if (Hk != H) w.part = take((size_t)B * H * T * 2 * dk);
