@@ -126,7 +126,7 @@ __device__ __forceinline__ void drain(uint32_t tm, float* out, const Lanes& l, i
   }
 }
 
-// 64 × 64 BLOCKS of a product as tiles of three parts, [part][block]. A lane's four words of a row turn into one eight.
+// 64 × 64 BLOCKS of a product as the chain's operand (see Workspace). A lane's four words of a row turn into one eight.
 template <int BLOCKS>
 __device__ __forceinline__ void drain_parts(uint32_t tm, char* out, const Lanes& l, float bad) {
 #pragma unroll
@@ -138,7 +138,7 @@ __device__ __forceinline__ void drain_parts(uint32_t tm, char* out, const Lanes&
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       const int r = l.r + 8 * o, c = 4 * l.half + (l.lane & 3);
-      char* to = out + b * kTileBytes + r * 128 + (((c ^ r) & 7) << 4);
+      char* to = out + (((c ^ r) & 7) << 4);
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
         uint32_t u[4];
@@ -150,7 +150,8 @@ __device__ __forceinline__ void drain_parts(uint32_t tm, char* out, const Lanes&
           y -= __uint_as_float(u[j] & 0xffff0000u);
         }
         turn_four(u, l.lane);
-        *reinterpret_cast<uint4*>(to + p * BLOCKS * kTileBytes) = make_uint4(u[0], u[1], u[2], u[3]);
+        const int row = p < 2 ? b * 128 + r + 16 * (l.quad + p) : BLOCKS * 128 + b * 64 + r;
+        *reinterpret_cast<uint4*>(to + row * 128) = make_uint4(u[0], u[1], u[2], u[3]);
       }
     }
   }
@@ -390,7 +391,8 @@ struct ChainSmem {
   static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, WB = 3 * DK / 64 * kTileBytes;
   static constexpr int STAGES = sizeof(IO) == 4 && DK == 128 ? 1 : 2;
   static constexpr int IN = NV * C * 4, GATES = 3 * C * 4;  // a chunk's M (β V), gates
-  static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + 3 * DK * 128, B = U + 3 * kTileBytes,
+  static constexpr int TILES = (3 * NV + 63) / 64;  // of X's and U's parts side by side
+  static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + TILES * DK * 128, B = U + TILES * kTileBytes,
                        AHEAD = B + 2 * (IN + GATES) <= kMaxBytes ? 2 : 1, kBytes = B + AHEAD * (IN + GATES);
   static_assert(kBytes <= kMaxBytes, "");
 };
@@ -413,7 +415,8 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
     for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
     for (int i = 0; i < L::AHEAD; ++i) mbar_init(&loaded[i], 1);
   }
-  if (warp == 0) tmem_alloc(&slot, 128);
+  constexpr int COLS = 128;  // NV, or three times 32: X's product, then U's
+  if (warp == 0) tmem_alloc(&slot, COLS);
   fence_async();
   fence_before();
   __syncthreads();
@@ -440,21 +443,40 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
     __syncwarp();
     for (int i = 0; i < N; ++i) {
       const int b = STAGES == 2 ? i & 1 : 0;
-      const Operand<3, false> Wr{base + L::W + b * L::WB, RB * kTileBytes, kTileBytes};
+      const uint32_t Wb = base + L::W + b * L::WB;
+      const Operand<1, false> Whm{Wb, 0, 2 * kTileBytes}, Wl{Wb + RB * 2 * kTileBytes, 0, kTileBytes};
       const Operand<PARTS, true> Kt{base + L::K + b * L::KB, RB * kTileBytes, kTileBytes};
-      const Operand<3, true> Xs{base + L::X, DK * 128, DK * 128}, Us{base + L::U, kTileBytes, kTileBytes};
+      auto Xp = [&](int p) { return Operand<1, true>{base + L::X + p * DK * 128, 0, DK * 128}; };
       mbar_wait(&full[b], STAGES == 2 ? (i >> 1) & 1 : i & 1, ok);
       bar_sync(1, kChainThreads + 32);
       fence_after();
       if (elect()) {
-        mma<64, NV, DK>(tm, Wr, Xs);
+        if (NV == 32) {
+          mma<128, 3 * NV, DK>(tm, Whm, Xp(0));
+          mma<64, NV, DK>(tm + 2 * NV, Wl, Xp(0), true);
+        } else {
+          mma<128, NV, DK>(tm, Whm, Xp(2));
+          mma<64, NV, DK>(tm, Wl, Xp(0), true);
+          mma<128, NV, DK>(tm, Whm, Xp(1), true);
+          mma<128, NV, DK>(tm, Whm, Xp(0), true);
+        }
         commit(&done[0]);
       }
       __syncwarp();
       bar_sync(2, kChainThreads + 32);
       fence_after();
       if (elect()) {
-        mma<DK, NV, 64>(tm + 64, Kt, Us);
+        if (NV == 32) {
+          const Operand<1, true> Us{base + L::U, 0, kTileBytes};
+          auto Kp = [&](int p) { return Operand<1, true>{Kt.addr + p * Kt.part, 0, Kt.block}; };
+          if (PARTS == 3) {
+            mma<DK, 3 * NV, 64>(tm, Kp(1), Us);
+            mma<DK, NV, 64>(tm, Kp(2), Us, true);
+          }
+          mma<DK, 3 * NV, 64>(tm, Kp(0), Us, PARTS == 3);
+        } else {
+          mma<DK, NV, 64>(tm, Kt, Operand<3, true>{base + L::U, kTileBytes, kTileBytes});
+        }
         commit(&done[1]);
         commit(&empty[b]);
         bring(i + L::AHEAD);
@@ -501,11 +523,32 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         X[rb].v[e] = x.x, X[rb].v[e + 1] = x.y;
       }
     float* const blocks_x = (REV ? w.Z : w.S) + (size_t)bh * N * DK * DV + col * DK;
+    auto load_product = [&](uint32_t from, float (&v)[4 * J]) {
+      if constexpr (NV == 32) tmem_load_sum(from, NV, v);
+      else tmem_load(from, v);
+    };
+    // three parts, NV columns each
+    auto put = [&](const Columns<J>& f, int to, int tile, int r0) {
+#pragma unroll
+      for (int e = 0; e < 4 * J; e += 2) {
+        const int r = r0 + (e & 2) * 4, c = lc + (e >> 2) * 8;
+        char* p = sm + to + r * 128 + ((((c >> 3) ^ r) & 7) << 4) + (c & 7) * 2;
+        float x = f.v[e], y = f.v[e + 1];
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+          const uint32_t v = bf16_pair(x, y);
+          if (NV == 64) *reinterpret_cast<uint32_t*>(p + m * tile) = v;
+          else *reinterpret_cast<uint32_t*>(m == 1 ? reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(p) ^ 64) : p + (m >> 1) * tile) = v;
+          x -= __uint_as_float(v << 16);
+          y -= __uint_as_float(v & 0xffff0000u);
+        }
+      }
+    };
     for (int i = 0; i < N; ++i) {
       const int n = REV ? N - 1 - i : i;
       const uint32_t parity = i & 1;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) X[rb].template put<3>(sm + L::X, DK * 128, block_row<DK>(l, rb), lc);
+      for (int rb = 0; rb < RB; ++rb) put(X[rb], L::X, DK * 128, block_row<DK>(l, rb));
       fence_async();
       fence_before();
       bar_arrive(1, kChainThreads + 32);
@@ -520,7 +563,8 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       Columns<J> u, s;
       mbar_wait(&done[0], parity, ok);
       fence_after();
-      tmem_load(tm + rows, u.v);
+      load_product(tm + rows + (16u << 16), s.v);
+      load_product(tm + rows, u.v);
       const char* const brought = sm + L::B + i % L::AHEAD * (L::IN + L::GATES);
       const float4* const in = reinterpret_cast<const float4*>(brought) + (NV == 64 ? vt : vt & 127);
       const float* const gates = reinterpret_cast<const float*>(brought + L::IN);
@@ -535,11 +579,12 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const float4 x = in[(j0 + j) * (NV * 4)];
-        u.v[4 * j] += x.x, u.v[4 * j + 1] += x.y, u.v[4 * j + 2] += x.z, u.v[4 * j + 3] += x.w;
+        u.v[4 * j] += s.v[4 * j] + x.x, u.v[4 * j + 1] += s.v[4 * j + 1] + x.y;
+        u.v[4 * j + 2] += s.v[4 * j + 2] + x.z, u.v[4 * j + 3] += s.v[4 * j + 3] + x.w;
       }
 #pragma unroll
       for (int e = 0; e < 4 * J; ++e) s.v[e] = g[(e & 2) >> 1] * u.v[e];
-      s.template put<3>(sm + L::U, kTileBytes, l.r, lc);
+      put(s, L::U, kTileBytes, l.r);
       fence_async();
       fence_before();
       bar_arrive(2, kChainThreads + 32);
@@ -552,7 +597,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       fence_after();
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        tmem_load(tm + 64 + rows + ((uint32_t)(16 * rb) << 16), s.v);
+        load_product(tm + rows + ((uint32_t)(16 * rb) << 16), s.v);
 #pragma unroll
         for (int e = 0; e < 4 * J; ++e)
           X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? s.v[e] + F[REV ? rb : 0].v[e] : s.v[e]);
@@ -573,7 +618,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
   }
   fence_before();
   __syncthreads();
-  if (warp == 0) tmem_free(tm, 128);
+  if (warp == 0) tmem_free(tm, COLS);
 }
 
 // BOTH: a second row of blocks walks the reverse chain, which needs nothing of the forward one.

@@ -25,13 +25,15 @@ __host__ __device__ constexpr int pad64(int d) { return d <= 64 ? 64 : 128; }
 // blocks of 64 × 64 (a column of blocks per 64 columns, one or two rows of
 // them) in the order of the fragments that 256 threads hold of them, so that
 // a warp's stores and loads are whole lines (see Fragment). W and Wr only the
-// chain reads: they are the three parts' tiles as its products take them.
+// chain reads: they are its operand's tiles, DK / 64 of 128 rows (in turns 16
+// rows of the largest part and 16 of the middle one), then as many of the
+// smallest part's 64 rows.
 struct Workspace {
   float* gates;  // [chunks][5][64]
-  char* W;       // [chunks][3][DK / 64] tiles: −M (β G K)
+  char* W;       // [chunks] tiles: −M (β G K)
   float* S;      // [chunks][DK][DV]: the state before each chunk
   float* U;      // [chunks][64][DV]: first M (β V), then U
-  char* Wr;      // [chunks][3][DK / 64] tiles: Mᵀ (E K)
+  char* Wr;      // [chunks] tiles: Mᵀ (E K)
   float* Z;      // [chunks][DK][DV]: first Qᵀ(G O'), then the gradient of the state after each chunk
   float* R;      // [chunks][64][DV]: first Mᵀ Pᵀ O', then dR
   float* part;   // [B·H][T][2][dk]: gradients of q and k by value head (shared key heads)

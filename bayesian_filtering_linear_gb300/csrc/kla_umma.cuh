@@ -103,6 +103,24 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[8]) {  // 16
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// The sum of three such blocks, `apart` columns from one another, the last ones first.
+__device__ __forceinline__ void tmem_load_sum(uint32_t addr, int apart, float (&v)[8]) {
+  uint32_t r[24];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+        "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23])
+      : "r"(addr), "r"(addr + apart), "r"(addr + 2 * apart)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = (__uint_as_float(r[16 + i]) + __uint_as_float(r[8 + i])) + __uint_as_float(r[i]);
+}
+
 // ---- products -------------------------------------------------------------------
 // A tile operand of PARTS parts, `part` bytes apart, K-major (rows are M or N)
 // or MN-major (rows are K). `block`: bytes between its 64-column tiles.
