@@ -125,6 +125,22 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   auto row_of = [&](int e) { return r0 + (e & 2) * 4; };
   auto col_of = [&](int e) { return c0 + (e >> 2) * 8; };
 
+  // a slice's inputs, whose loads run ahead of the waits for the products before them
+  TileLoad<IO, 64, kThreads> ol;
+  Fragment ul, rl, xl[NB], zl[NB], vl;
+  auto bring = [&](int sl) {
+    rl.load(Rw + sl * kBlock, tid);
+    ol.fetch(go ? go : v_in, go ? at.len : 0, a.dv, sl * 64, tid);
+    ul.load(Uw + sl * kBlock, tid);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) xl[nb].load(Sw + (sl * NB + nb) * kBlock, tid);
+    load_rows(v_in, l, sl * 64, at.len, a.dv, vl.v);
+  };
+  auto bring_z = [&](int sl) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) zl[nb].load(Zw + (sl * NB + nb) * kBlock, tid);
+  };
+  bring(0);
   if (warp == 0 && elect()) {  // A and P before their decays, where dQ and X come later
     mma<64, 64, DK>(tm, Kr, Kr);
     mma<64, 64, DK>(tm + 64, Qr, Kr);
@@ -136,14 +152,6 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   tmem_load(tm + 64 + rows + 32 * half, qk);
   // products with U, S: dP, dA before masks, dQ = O' Sᵀ, X = dR Sᵀ (dP and dA wait in the shared columns and in Y's)
   for (int sl = 0; sl < slices; ++sl) {
-    TileLoad<IO, 64, kThreads> ol;
-    Fragment ul, rl, xl[NB], vl;
-    rl.load(Rw + sl * kBlock, tid);
-    ol.fetch(go ? go : v_in, go ? at.len : 0, a.dv, sl * 64, tid);
-    ul.load(Uw + sl * kBlock, tid);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) xl[nb].load(Sw + (sl * NB + nb) * kBlock, tid);
-    load_rows(v_in, l, sl * 64, at.len, a.dv, vl.v);
     if (sl) finish();
     ol.put(sm + L::O, tid);
     ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
@@ -166,32 +174,37 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
       rl.v[e] *= be[r0 + 8 * o];
     }
     store_rows(reinterpret_cast<IO*>(d.gv) + vrow * a.dv, l, sl * 64, at.len, a.dv, rl.v);
+    if (sl + 1 < slices) bring(sl + 1);
+    else bring_z(sl);
   }
   float gp[16], ga[16];
   finish();
   tmem_load(tm + SH + rows + 32 * half, gp);
   tmem_load(tm + 2 * DK + rows + 32 * half, ga);
   fence_before();
-  // Y = U Zᵀ, and <Z, S>
+  // Y = U Zᵀ, and <Z, S>, from the last slice on, whose U and S are at hand
   float z = 0.f;
-  for (int sl = 0; sl < slices; ++sl) {
-    Fragment ul, zl[NB], xl;
-    if (slices > 1) ul.load(Uw + sl * kBlock, tid);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) zl[nb].load(Zw + (sl * NB + nb) * kBlock, tid);
-    if (sl) finish();
-    if (slices > 1) ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
+  for (int sl = slices - 1; sl >= 0; --sl) {
+    if (sl + 1 < slices) {
+      finish();
+      ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      xl.load(Sw + (sl * NB + nb) * kBlock, tid);
       zl[nb].put<PN>(sm + L::S, DK * 128, block_row<DK>(l, nb), l.c);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) z = fmaf(xl.v[e], zl[nb].v[e], z);
+      for (int e = 0; e < 16; ++e) z = fmaf(xl[nb].v[e], zl[nb].v[e], z);
     }
     publish();
     if (warp == 0 && elect()) {
-      mma<64, DK, 64>(tm + 2 * DK, Ur, Sr, sl > 0);
+      mma<64, DK, 64>(tm + 2 * DK, Ur, Sr, sl + 1 < slices);
       commit(&bar);
+    }
+    if (sl) {
+      ul.load(Uw + (sl - 1) * kBlock, tid);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) xl[nb].load(Sw + ((sl - 1) * NB + nb) * kBlock, tid);
+      bring_z(sl - 1);
     }
   }
 #pragma unroll
@@ -240,19 +253,27 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   fence_before();
   __syncthreads();
   {  // W[t][s] becomes the sum of its row before s, four lanes a row; then before[s] the sum of column s from row s on
-    const int r = tid >> 2, s0 = (tid & 3) * 16;
-    float sum = 0.f;
-    for (int s = s0; s < s0 + 16; ++s) sum += W[r * 65 + s];
-    float x = __shfl_up_sync(~0u, sum, 1), y = __shfl_up_sync(~0u, sum, 2), u = __shfl_up_sync(~0u, sum, 3);
-    const int seg = tid & 3;
-    float run = (seg > 0 ? x : 0.f) + (seg > 1 ? y : 0.f) + (seg > 2 ? u : 0.f);
-    for (int s = s0; s < s0 + 16; ++s) {
-      const float e = W[r * 65 + s];
-      W[r * 65 + s] = run;
-      run += e;
+    const int r = tid >> 2, seg = tid & 3, s0 = seg * 16;
+    float x[16], sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      x[s] = W[r * 65 + s0 + s];
+      sum += x[s];
+    }
+    float run = 0.f;
+#pragma unroll
+    for (int m = 1; m < 4; ++m) {
+      const float y = __shfl_up_sync(~0u, sum, m);
+      if (seg >= m) run += y;
+    }
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      W[r * 65 + s0 + s] = run;
+      run += x[s];
     }
     __syncthreads();
     sum = 0.f;
+#pragma unroll
     for (int t = s0; t < s0 + 16; ++t)
       if (t >= r) sum += W[t * 65 + r];
     sum = row4(sum);
@@ -276,13 +297,25 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     mma<64, DK, 64>(tm + 2 * DK, At, Kt, true);
     commit(&bar);
   }
-  if (tid < at.len) {  // the decay's gradient needs nothing more
+  if (warp == 1) {  // the decay's gradient needs nothing more: sums of `from` from a token on, of `to` before it; two a lane
     float x = 0.f;
     for (int i = 0; i < 8; ++i) x += zs[i];
-    x = fmaf(G[C - 1], x, before[tid]);
-    for (int s = C - 1; s >= tid; --s) x += from[0][s] + from[1][s];
-    for (int s = 0; s < tid; ++s) x += to[0][s] + to[1][s];
-    reinterpret_cast<IO*>(d.gg)[vrow + tid] = from_f32<IO>(x);
+    x *= G[C - 1];
+    const int t = 2 * lane;
+    const float f0 = from[0][t] + from[1][t], f1 = from[0][t + 1] + from[1][t + 1];
+    const float t0 = to[0][t] + to[1][t], t1 = to[0][t + 1] + to[1][t + 1];
+    float after = f0 + f1, ahead = t0 + t1;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const float f = __shfl_down_sync(~0u, after, m), y = __shfl_up_sync(~0u, ahead, m);
+      if (lane + m < 32) after += f;
+      if (lane >= m) ahead += y;
+    }
+    const float f2 = __shfl_down_sync(~0u, after, 1), y = __shfl_up_sync(~0u, ahead, 1);
+    const float from1 = f1 + (lane < 31 ? f2 : 0.f), to0 = lane ? y : 0.f;
+    IO* gg = reinterpret_cast<IO*>(d.gg) + vrow + t;
+    if (t < at.len) gg[0] = from_f32<IO>((x + before[t]) + (f0 + from1) + to0);
+    if (t + 1 < at.len) gg[1] = from_f32<IO>((x + before[t + 1]) + from1 + (to0 + t0));
   }
   finish();
   const float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
