@@ -88,10 +88,27 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     const float* g = w.gates + at.chunk * kGates + tid;
     logs[tid] = make_float2(g[0], g[C]), G[tid] = g[2 * C], E[tid] = g[3 * C], be[tid] = g[4 * C];
   }
+  const Lanes l(tid);
+  // a slice's inputs, whose loads run ahead of the waits for the products before them
+  TileLoad<IO, 64, kThreads> ol;
+  Fragment ul, rl, xl[NB], zl[NB], vl;
+  auto bring = [&](int sl) {
+    rl.load(Rw + sl * kBlock, tid);
+    ol.fetch(go ? go : v_in, go ? at.len : 0, a.dv, sl * 64, tid);
+    ul.load(Uw + sl * kBlock, tid);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) xl[nb].load(Sw + (sl * NB + nb) * kBlock, tid);
+    load_rows(v_in, l, sl * 64, at.len, a.dv, vl.v);
+  };
+  auto bring_z = [&](int sl) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) zl[nb].load(Zw + (sl * NB + nb) * kBlock, tid);
+  };
   {
     TileLoad<IO, DK, kThreads> kl, ql;
     kl.fetch(k, at.len, a.dk, 0, tid);
     ql.fetch(q, at.len, a.dk, 0, tid);
+    bring(0);
     kl.put(sm + L::K, tid);
     ql.put(sm + L::Q, tid);
   }
@@ -118,29 +135,12 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     __syncthreads();
     fence_after();
   };
-  const Lanes l(tid);
   const int quad = warp & 3, half = warp >> 2, r0 = l.r, c0 = l.c;
   const uint32_t rows = (uint32_t)(32 * quad) << 16;
   // entries (t, s), (t, s + 1) of a 64 × 64 fragment at index e of 16
   auto row_of = [&](int e) { return r0 + (e & 2) * 4; };
   auto col_of = [&](int e) { return c0 + (e >> 2) * 8; };
 
-  // a slice's inputs, whose loads run ahead of the waits for the products before them
-  TileLoad<IO, 64, kThreads> ol;
-  Fragment ul, rl, xl[NB], zl[NB], vl;
-  auto bring = [&](int sl) {
-    rl.load(Rw + sl * kBlock, tid);
-    ol.fetch(go ? go : v_in, go ? at.len : 0, a.dv, sl * 64, tid);
-    ul.load(Uw + sl * kBlock, tid);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) xl[nb].load(Sw + (sl * NB + nb) * kBlock, tid);
-    load_rows(v_in, l, sl * 64, at.len, a.dv, vl.v);
-  };
-  auto bring_z = [&](int sl) {
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) zl[nb].load(Zw + (sl * NB + nb) * kBlock, tid);
-  };
-  bring(0);
   if (warp == 0 && elect()) {  // A and P before their decays, where dQ and X come later
     mma<64, 64, DK>(tm, Kr, Kr);
     mma<64, 64, DK>(tm + 64, Qr, Kr);
