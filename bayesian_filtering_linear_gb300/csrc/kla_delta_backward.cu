@@ -61,7 +61,7 @@ __device__ __forceinline__ float2 tile_two(const char* tile, int part, int r, in
 
 template <typename IO, int DK>
 __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs d,
-                                                                 const Workspace w) {
+                                                                 const Workspace w, unsigned ahead) {
   using L = GradSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
   constexpr int COLS = DK == 64 ? 256 : 512, SH = 3 * DK;      // TMEM: dQ, X, Y of DK columns, then 64 shared
@@ -109,6 +109,18 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     kl.fetch(k, at.len, a.dk, 0, tid);
     ql.fetch(q, at.len, a.dk, 0, tid);
     bring(0);
+    if (tid == 128 && blockIdx.x + ahead < gridDim.x) {  // for the block that follows on this SM (431 -> 357)
+      const Where next = where(a, blockIdx.x + ahead);
+      const int in = C * DV * 4, state = DK * DV * 4;
+      prefetch_rows<IO>(a.k, next.key, next, a.T, a.dk);
+      prefetch_rows<IO>(a.q, next.key, next, a.T, a.dk);
+      prefetch_rows<IO>(a.v, next.bh, next, a.T, a.dv);
+      if (d.go) prefetch_rows<IO>(d.go, next.bh, next, a.T, a.dv);
+      prefetch(w.U + next.chunk * C * DV, in);
+      prefetch(w.R + next.chunk * C * DV, in);
+      prefetch(w.S + next.chunk * DK * DV, state);
+      prefetch(w.Z + next.chunk * DK * DV, state);
+    }
     kl.put(sm + L::K, tid);
     ql.put(sm + L::Q, tid);
   }
@@ -383,9 +395,10 @@ __global__ void __launch_bounds__(256) kla_delta_share_kernel(const DeltaArgs a,
 }
 
 template <typename IO, int DK>
-cudaError_t grad_dk(const DeltaArgs& a, const DeltaGradArgs& g, const Workspace& w, cudaStream_t s) {
+cudaError_t grad_dk(const DeltaArgs& a, const DeltaGradArgs& g, const Workspace& w, int num_sms, cudaStream_t s) {
   const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.T + C - 1) / C));
-  return run(kla_delta_grad_kernel<IO, DK>, GradSmem<IO, DK>::kBytes, blocks, kThreads, s, a, g, w);
+  using L = GradSmem<IO, DK>;
+  return run(kla_delta_grad_kernel<IO, DK>, L::kBytes, blocks, kThreads, s, a, g, w, (unsigned)(num_sms * L::kBlocks));
 }
 
 }  // namespace
@@ -406,9 +419,9 @@ cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, in
   if (e != cudaSuccess) return e;
   const bool wide = delta::pad64(a.dk) == 128;
   if (a.io == IO_BF16)
-    e = wide ? delta::grad_dk<__nv_bfloat16, 128>(a, g, w, s) : delta::grad_dk<__nv_bfloat16, 64>(a, g, w, s);
+    e = wide ? delta::grad_dk<__nv_bfloat16, 128>(a, g, w, num_sms, s) : delta::grad_dk<__nv_bfloat16, 64>(a, g, w, num_sms, s);
   else
-    e = wide ? delta::grad_dk<float, 128>(a, g, w, s) : delta::grad_dk<float, 64>(a, g, w, s);
+    e = wide ? delta::grad_dk<float, 128>(a, g, w, num_sms, s) : delta::grad_dk<float, 64>(a, g, w, num_sms, s);
   if (e != cudaSuccess || a.Hk == a.H) return e;
   const long long blocks = ((long long)a.B * a.Hk * a.T * 2 * a.dk + 255) / 256;
   const unsigned grid = (unsigned)(blocks < (1LL << 30) ? blocks : 1LL << 30);

@@ -253,6 +253,12 @@ __device__ __forceinline__ Where where(const DeltaArgs& a, long long chunk) {
   return w;
 }
 
+// A chunk's rows of an io array on their way into L2.
+template <typename IO>
+__device__ __forceinline__ void prefetch_rows(const void* p, long long head, const Where& at, int T, int d) {
+  prefetch(reinterpret_cast<const IO*>(p) + ((size_t)head * T + at.t0) * d, at.len * d * (int)sizeof(IO));
+}
+
 // Launches with dynamic shared memory; all of an SM's L1 is asked for as shared memory, so that as many blocks fit as
 // their sizes allow.
 template <typename F, typename... Args>

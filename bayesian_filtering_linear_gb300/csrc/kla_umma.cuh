@@ -34,6 +34,10 @@ __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, int byt
                "r"(bytes), "r"(smem_addr(bar))
                : "memory");
 }
+// Global memory on its way into L2, 16-byte aligned.
+__device__ __forceinline__ void prefetch(const void* from, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
   uint32_t done;
   asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
