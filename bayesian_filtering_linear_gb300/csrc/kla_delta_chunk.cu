@@ -171,13 +171,9 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   const Where at = where(a, blockIdx.x);
   const int DV = pad64(a.dv);
   const size_t krow = ((size_t)at.key * a.T + at.t0) * a.dk, vrow = ((size_t)at.bh * a.T + at.t0) * a.dv;
-  TileLoad<IO, DK, kThreads> kl;
+  TileLoad<IO, DK, kThreads> kl, ql;
   kl.fetch(reinterpret_cast<const IO*>(a.k) + krow, at.len, a.dk, 0, tid);
-  if (BWD) {
-    TileLoad<IO, DK, kThreads> ql;
-    ql.fetch(reinterpret_cast<const IO*>(a.q) + krow, at.len, a.dk, 0, tid);
-    ql.put(sm + L::Q, tid);
-  }
+  if (BWD) ql.fetch(reinterpret_cast<const IO*>(a.q) + krow, at.len, a.dk, 0, tid);
   if (warp == 0) tmem_alloc(&slot, COLS);
   if (tid == 32) mbar_init(&bar, 1);
   if (warp == 2) {  // the gates: two tokens a lane, cumulative logs as sums of two floats
@@ -215,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
     }
   }
   kl.put(sm + L::K, tid);
+  if (BWD) ql.put(sm + L::Q, tid);
   bool ok = true;
   uint32_t phase = 0;
   auto finish = [&] {  // the products issued so far
