@@ -241,13 +241,14 @@ struct Where {
   int n, t0, len;
   size_t chunk;
 };
-__device__ __forceinline__ Where where(const DeltaArgs& a, long long chunk) {
-  const int N = (a.T + C - 1) / C;
+// (in 32 bits, as a grid counts its blocks)
+__device__ __forceinline__ Where where(const DeltaArgs& a, unsigned chunk) {
+  const unsigned N = ((unsigned)a.T + C - 1) / C, bh = chunk / N, b = bh / a.H;
   Where w;
-  w.chunk = (size_t)chunk;
-  w.bh = chunk / N;
-  w.n = (int)(chunk % N);
-  w.key = (w.bh / a.H) * a.Hk + (w.bh % a.H) / (a.H / a.Hk);
+  w.chunk = chunk;
+  w.bh = bh;
+  w.n = (int)(chunk - bh * N);
+  w.key = (long long)b * a.Hk + (bh - b * a.H) / ((unsigned)a.H / a.Hk);
   w.t0 = w.n * C;
   w.len = min(C, a.T - w.t0);
   return w;
