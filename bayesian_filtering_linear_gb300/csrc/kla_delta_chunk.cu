@@ -630,14 +630,15 @@ __global__ void __launch_bounds__(kChainBlock<IO>)
 template <typename IO, int DK>
 struct OutputSmem {
   static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, PN = sizeof(IO) == 2 ? 2 : 3;
-  static constexpr int K = 0, Q = IN, S = 2 * IN, U = S + PN * DK * 128, P = U + PN * kTileBytes,
-                       kBytes = P + PN * kTileBytes,
-                       kBlocks = 228 * 1024 / (kBytes + 2048);  // of an SM
-  static_assert(kBytes <= kMaxBytes, "");
+  // U and P come when the products with K, Q and S are done, in their places
+  static constexpr int K = 0, Q = IN, S = 2 * IN, U = K, P = S, kBytes = S + PN * DK * 128,
+                       kFit = 228 * 1024 / (kBytes + 2048), kBlocks = kFit < 4 ? kFit : 4;  // of an SM
+  static_assert(kBytes <= kMaxBytes && PN * kTileBytes <= 2 * IN, "");
 };
 
 template <typename IO, int DK>
-__global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaArgs a, const Workspace w, unsigned ahead) {
+__global__ void __launch_bounds__(kThreads, OutputSmem<IO, DK>::kBlocks)
+    kla_delta_output_kernel(const DeltaArgs a, const Workspace w, unsigned ahead) {
   using L = OutputSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
@@ -678,7 +679,6 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   ql.put(sm + L::Q, tid);
 #pragma unroll
   for (int rb = 0; rb < DK / 64; ++rb) xl[rb].put<PN>(sm + L::S, DK * 128, block_row<DK>(l, rb), l.c);
-  ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
   fence_async();
   fence_before();
   __syncthreads();
@@ -695,9 +695,9 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
   const uint32_t rows = (uint32_t)(32 * l.quad) << 16;
   mbar_wait(&bar, 0, ok);
   fence_after();
+  ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
   float v[16], y[16];
   tmem_load(tm + rows + 32 * half, v);
-  tmem_load(tm + 64 + rows + 32 * half, y);
   {
     Fragment p;
     decays(logs, l, p.v);
@@ -705,6 +705,7 @@ __global__ void __launch_bounds__(kThreads) kla_delta_output_kernel(const DeltaA
     for (int i = 0; i < 16; ++i) p.v[i] *= v[i];
     p.put<PN>(sm + L::P, kTileBytes, l.r, l.c);
   }
+  tmem_load(tm + 64 + rows + 32 * half, y);
   fence_async();
   fence_before();
   __syncthreads();
