@@ -661,10 +661,10 @@ __global__ void __launch_bounds__(kThreads, OutputSmem<IO, DK>::kBlocks)
 #pragma unroll
   for (int rb = 0; rb < DK / 64; ++rb) xl[rb].load(w.S + at.chunk * DK * DV + col * DK + rb * kBlock, tid);
   ul.load(w.U + at.chunk * C * DV + col * 64, tid);
-  // For the block that follows on this SM, where two at most cover for each other (d_k 128: 698 -> 583 us; with three,
-  // d_k 64, 116 -> 120).
+  // For the block that follows on this SM, into L2, where fewer than four blocks cover for each other (65536 tokens,
+  // 16 heads of 128: 562 -> 527 us; d_k 64 in bf16, whose inputs are half as many bytes: 116 -> 120).
   const unsigned after = blockIdx.x + ahead;
-  if (L::kBlocks < 3 && tid == 128 && col == 0 && after < gridDim.x) {
+  if (L::kBlocks < 4 && tid == 128 && col == 0 && after < gridDim.x) {
     const Where next = where(a, after / (DV / 64));
     prefetch_rows<IO>(a.k, next.key, next, a.T, a.dk);
     prefetch_rows<IO>(a.q, next.key, next, a.T, a.dk);
