@@ -15,10 +15,14 @@
 // while every product above carries the decay it is the gradient of.
 //
 // Four steps: `prepare` makes, ahead of the chain, Mᵀ (E K), Mᵀ Pᵀ O' and Qᵀ(G O');
-// the chain runs forward for S and U, and from the end for Z and dR; then a
-// block per chunk and head makes everything else here. Gradients of q and k
-// that several value heads share are summed from per-head fp32 parts in a
-// fixed order.
+// the chain runs forward for S and U, and beside it from the end for Z and dR;
+// then a block per chunk and head makes everything else here. Gradients of q and
+// k that several value heads share are summed from per-head fp32 parts in a
+// fixed order. At 8 × 16 heads of 64 × 64 and 4096 tokens in bf16: prepare 357 us,
+// the chains 236 (1.4 GB, 6 TB/s), gradients 358: two blocks an SM, bound by
+// their steps' latencies, so that a block's loads start together at its start, and
+// the inputs of the block that follows on the SM are sent into L2 (425 -> 358).
+// Sixteen warps instead of eight leave 64 registers a thread: 473 us.
 #include "kla_delta_chunk.cuh"
 
 namespace kla {
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     kl.fetch(k, at.len, a.dk, 0, tid);
     ql.fetch(q, at.len, a.dk, 0, tid);
     bring(0);
-    if (tid == 128 && blockIdx.x + ahead < gridDim.x) {  // for the block that follows on this SM (431 -> 357)
+    if (tid == 128 && blockIdx.x + ahead < gridDim.x) {  // for the block that follows on this SM, into L2 (383 -> 358 us)
       const Where next = where(a, blockIdx.x + ahead);
       const int in = C * DV * 4, state = DK * DV * 4;
       prefetch_rows<IO>(a.k, next.key, next, a.T, a.dk);

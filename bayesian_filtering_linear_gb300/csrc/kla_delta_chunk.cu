@@ -7,12 +7,15 @@
 //   O = scale (G Q S + tril(D_ts q_t·k_s) U)
 //
 // Three kernels. `prepare` (a block per chunk and head) makes M and with it
-// W = −M (β G K) and M (β V). `chain` (a block per head and 64 columns, in
+// W = −M (β G K) and M (β V). `chain` (a block per head and 64 or 32 columns, in
 // order over the chunks) carries S in registers: U = M (β V) + W S and the
 // update, two products and two round trips between TMEM, registers and shared
-// memory per chunk, whose latency bounds it. `output` (a block per chunk, head
-// and 64 columns) makes O. The backward pass runs the same chain from the end
-// with Mᵀ (see kla_delta_backward.cu).
+// memory per chunk; its latency (1.3 to 1.7 us a chunk) or, with a block on most
+// SMs, DRAM bounds it. `output` (a block per chunk, head and 64 columns) makes
+// O. The backward pass runs the same chain from the end with Mᵀ, beside the
+// other (see kla_delta_backward.cu). At 8 × 16 heads of 64 × 64 and 4096 tokens in
+// bf16: prepare 191 us (shared memory busy 75% of the time), chain 111 (655 MB,
+// 5.9 TB/s), output 97 (460 MB, 4.7 TB/s).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
 // and everything that flows into them are kept in three, so that a state is as
@@ -21,6 +24,7 @@
 // of two floats, in powers of two, so that D of late tokens is exact behind a
 // strong decay.
 #include <algorithm>
+#include <cmath>
 
 #include "kla_delta_chunk.cuh"
 
@@ -375,8 +379,15 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
 //   forward:  U = M (β V) + W X,       X = G_end X + Kᵀ(E U)
 //   reverse:  dR = Mᵀ Pᵀ O' + W X,     X = G_end X + Qᵀ(G O') − Kᵀ(β G dR)
 // Eight warps walk the chunks, each with a quarter of the rows and half of the
-// columns; others bring K (fp32: as parts, twice the warps) and W of the next
-// chunk, two chunks deep where shared memory holds them; one issues the products.
+// columns; others bring K (fp32: as parts, twice the warps) of the next chunk and
+// start the copy of W, two chunks deep where shared memory holds them; one issues
+// the products and the copies of M (β V) and the gates. The eight warps read no
+// global memory on the way forward: loads ahead in registers cost them a stall
+// of 700 of 5000 cycles a chunk, and W as fp32 to be made into parts here another
+// 800 (d_k 128). Instructions are bound by their reads of shared memory (64 × 16
+// by 16 × 32 takes 26 to 30 cycles): W's largest and middle parts are one operand
+// of 128 rows, and with 32 columns X's and U's three parts lie side by side (65536 tokens, 16 heads of 128: 1900 -> 1730 us; with 64
+// columns side by side took more, 125 us against 111 of the headline shape).
 constexpr int kChainThreads = 256;
 template <typename IO>
 constexpr int kFeedThreads = 128 * (sizeof(IO) / 2);
@@ -745,9 +756,9 @@ cudaError_t chain_nv(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace
 }
 template <typename IO, int DK>
 cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, int num_sms, cudaStream_t s) {
-  // A chunk's latency bounds the chain, and blocks of 32 columns take less of it (64 tokens, d 128: 2.4 us against
-  // 3.0), as long as every block has an SM; with more heads than that W and K would be brought in twice (128 heads,
-  // d 64: 160 us against 156).
+  // A chunk's latency bounds the chain, and blocks of 32 columns take less of it (64 tokens, d 128: 1.7 us against
+  // 2.5; d 64: 1.3 against 1.7), as long as every block has an SM; with more heads than that W and K would be brought
+  // in twice (128 heads, d 64, 4096 tokens: 165 us against 115; 64 heads, d 128: 216 against 166).
   if ((long long)a.B * a.H * (pad64(a.dv) / 32) * (d ? 2 : 1) <= num_sms) return chain_nv<IO, DK, 32>(a, d, w, s);
   return chain_nv<IO, DK, 64>(a, d, w, s);
 }
@@ -801,22 +812,23 @@ cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Works
 }  // namespace delta
 
 // Chunks, or token by token (kla_delta.cu)? The estimated times of both, in
-// microseconds, from bf16 calls on a GB300. Token by token: 0.2 us a token, or
-// 3.1e6 elements a microsecond where heads are many (heads of few rows count as
-// 40 rows). Chunks: 20 us of launches and first waits and, by latency, 1.2 us
-// a chunk (2.3 for d_k = 128), or by work, 0.052 us a chunk and head (0.116).
-// Measured, one by one / chunks: 8 heads of 64 × 64, 64 tokens 16 / 21 us, 128
-// tokens 29 / 21; 1024 heads of 64 × 64, 64 tokens 87 / 82; 1024 heads of
-// 16 × 16, 512 tokens 129 / 435; 128 heads of 128 × 128, 64 tokens 53 / 35. Past
-// 512 tokens always chunks: one by one, a rounding per token adds up (1e-6 of
-// the state after a thousand).
+// microseconds, fitted to bf16 calls on a GB300. Token by token: 0.19 us a token
+// (d_k 64; 0.16 and 0.23 for 16 and 128), or 3.3e6 elements a microsecond where
+// heads are many (heads of few rows count as 40 rows). Chunks: 20 us of launches
+// and first waits and, by latency, 1.7 us a chunk (23 and 2.1 for d_k 128), or by
+// work, 0.052 us a chunk and head (0.116). Measured, one by one / chunks: 8 heads
+// of 64 × 64, 64 tokens 17 / 23 us, 128 tokens 29 / 24; 128 heads of 64 × 64, 64
+// tokens 20 / 24, 128 tokens 35 / 30; 1024 heads of 64 × 64, 32 tokens 49 / 77, 64
+// tokens 88 / 79; 1024 heads of 16 × 16, 512 tokens 130 / 397; 128 heads of
+// 128 × 128, 64 tokens 55 / 32. Past 512 tokens always chunks: one by one, a
+// rounding per token adds up (1e-6 of the state after a thousand).
 bool delta_chunked(int B, int H, int T, int dk, int dv) {
   if (T > 512) return true;
   const double heads = (double)B * H, chunks = (T + delta::C - 1) / delta::C;
   const bool wide = delta::pad64(dk) == 128;
-  const double tokens = std::max(2.0 + 0.2 * T, heads * T * dv * std::max(dk, 40) / 3.1e6);
+  const double tokens = 4.5 + T * std::hypot(0.145 + 0.0007 * dk, heads * dv * std::max(dk, 40) / 3.3e6);
   const double work = (wide ? 0.116 : 0.052) * heads * chunks * (delta::pad64(dv) / (wide ? 128.0 : 64.0));
-  return std::max(20.0 + (wide ? 2.3 : 1.2) * chunks, 15.0 + work) < tokens;
+  return std::max((wide ? 23.0 : 20.0) + (wide ? 2.1 : 1.7) * chunks, 15.0 + work) < tokens;
 }
 
 size_t delta_forward_bytes(int B, int Hk, int H, int T, int dk, int dv) {
