@@ -382,19 +382,25 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   if (warp == 0) tmem_free(tm, COLS);
 }
 
-// gq, gk of a key head: the sum over its value heads, in order.
+// gq, gk of a key head: the sum over its value heads, in order; four elements a thread.
 template <typename IO>
 __global__ void __launch_bounds__(256) kla_delta_share_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                              const float* part) {
-  const long long n = (long long)a.B * a.Hk * a.T * 2 * a.dk;
-  const int rep = a.H / a.Hk, w = 2 * a.dk;
+  const int rep = a.H / a.Hk, w = a.dk / 2;  // fours in a row of both
+  const long long row = (long long)a.T * w, n = (long long)a.B * a.Hk * row;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const int e = (int)(i % w);
-    const long long t = i / w % a.T, key = i / w / a.T;
-    float x = 0.f;
-    for (int r = 0; r < rep; ++r) x += part[((key * rep + r) * a.T + t) * w + e];
-    IO* out = reinterpret_cast<IO*>(e < a.dk ? d.gq : d.gk);
-    out[(key * a.T + t) * a.dk + e % a.dk] = from_f32<IO>(x);
+    const long long key = i / row, in = i - key * row, t = in / w;
+    const int e = (int)(in - t * w) * 4;
+    const float4* p = reinterpret_cast<const float4*>(part) + key * rep * row + in;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < rep; ++r) {
+      const float4 y = p[r * row];
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    IO* out = reinterpret_cast<IO*>(e < a.dk ? d.gq : d.gk) + (key * a.T + t) * a.dk + (e < a.dk ? e : e - a.dk);
+    store_two(out, x.x, x.y);
+    store_two(out + 2, x.z, x.w);
   }
 }
 
@@ -427,7 +433,7 @@ cudaError_t launch_delta_backward(const DeltaArgs& a, const DeltaGradArgs& g, in
   else
     e = wide ? delta::grad_dk<float, 128>(a, g, w, num_sms, s) : delta::grad_dk<float, 64>(a, g, w, num_sms, s);
   if (e != cudaSuccess || a.Hk == a.H) return e;
-  const long long blocks = ((long long)a.B * a.Hk * a.T * 2 * a.dk + 255) / 256;
+  const long long blocks = ((long long)a.B * a.Hk * a.T * (a.dk / 2) + 255) / 256;
   const unsigned grid = (unsigned)(blocks < (1LL << 30) ? blocks : 1LL << 30);
   if (a.io == IO_BF16) delta::kla_delta_share_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, g, w.part);
   else delta::kla_delta_share_kernel<float><<<grid, 256, 0, s>>>(a, g, w.part);
