@@ -535,6 +535,10 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       if constexpr (NV == 32) tmem_load_sum(from, NV, v);
       else tmem_load(from, v);
     };
+    auto load_both = [&](uint32_t from, float (&x)[4 * J], float (&y)[4 * J]) {
+      if constexpr (NV == 32) tmem_load_both_sum(from, NV, x, y);
+      else tmem_load_both(from, x, y);
+    };
     // three parts, NV columns each
     auto put = [&](const Columns<J>& f, int to, int tile, int r0) {
 #pragma unroll
@@ -568,15 +572,15 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         if (REV) F[rb].load(Xout + rb * kBlock, vt, j0);
         else X[rb].store(Xout + rb * kBlock, vt, j0);
       }
-      Columns<J> u, s;
-      mbar_wait(&done[0], parity, ok);
-      fence_after();
-      load_product(tm + rows + (16u << 16), s.v);
-      load_product(tm + rows, u.v);
       const char* const brought = sm + L::B + i % L::AHEAD * (L::IN + L::GATES);
-      const float4* const in = reinterpret_cast<const float4*>(brought) + (NV == 64 ? vt : vt & 127);
       const float* const gates = reinterpret_cast<const float*>(brought + L::IN);
+      Columns<J> B, u, s;
       mbar_wait(&loaded[i % L::AHEAD], i / L::AHEAD & 1, ok);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float4 x = reinterpret_cast<const float4*>(brought)[(j0 + j) * (NV * 4) + (NV == 64 ? vt : vt & 127)];
+        B.v[4 * j] = x.x, B.v[4 * j + 1] = x.y, B.v[4 * j + 2] = x.z, B.v[4 * j + 3] = x.w;
+      }
       const float gend = gates[C - 1];
       float g[2];  // −β G, or E
 #pragma unroll
@@ -584,12 +588,11 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         const float* q = gates + l.r + 8 * o;
         g[o] = REV ? -q[2 * C] * q[0] : q[C];
       }
+      mbar_wait(&done[0], parity, ok);
+      fence_after();
+      load_both(tm + rows, u.v, s.v);
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const float4 x = in[(j0 + j) * (NV * 4)];
-        u.v[4 * j] += s.v[4 * j] + x.x, u.v[4 * j + 1] += s.v[4 * j + 1] + x.y;
-        u.v[4 * j + 2] += s.v[4 * j + 2] + x.z, u.v[4 * j + 3] += s.v[4 * j + 3] + x.w;
-      }
+      for (int e = 0; e < 4 * J; ++e) u.v[e] += s.v[e] + B.v[e];
 #pragma unroll
       for (int e = 0; e < 4 * J; ++e) s.v[e] = g[(e & 2) >> 1] * u.v[e];
       put(s, L::U, kTileBytes, l.r);
@@ -603,13 +606,14 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       }
       mbar_wait(&done[1], parity, ok);
       fence_after();
+      Columns<J> more[RB];
+      if constexpr (RB == 2) load_both(tm + rows, more[0].v, more[1].v);
+      else load_product(tm + rows, more[0].v);
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        load_product(tm + rows + ((uint32_t)(16 * rb) << 16), s.v);
+      for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int e = 0; e < 4 * J; ++e)
-          X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? s.v[e] + F[REV ? rb : 0].v[e] : s.v[e]);
-      }
+          X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? more[rb].v[e] + F[REV ? rb : 0].v[e] : more[rb].v[e]);
     }
     float* last = REV ? d.gstate0 : a.stateT;
     if (last) {

@@ -97,17 +97,7 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 
-__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[8]) {  // 16 lanes × 16 columns
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// The sum of three such blocks, `apart` columns from one another, the last ones first.
+// 16 lanes × 16 columns, the sum of three blocks `apart` columns from one another, the last one first.
 __device__ __forceinline__ void tmem_load_sum(uint32_t addr, int apart, float (&v)[8]) {
   uint32_t r[24];
   asm volatile(
@@ -123,6 +113,50 @@ __device__ __forceinline__ void tmem_load_sum(uint32_t addr, int apart, float (&
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     v[i] = (__uint_as_float(r[16 + i]) + __uint_as_float(r[8 + i])) + __uint_as_float(r[i]);
+}
+// Both sixteen lanes of a quadrant with one wait: x from addr on, y from 16 lanes further.
+__device__ __forceinline__ void tmem_load_both(uint32_t addr, float (&x)[16], float (&y)[16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+        "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]),
+        "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31])
+      : "r"(addr), "r"(addr + (16u << 16))
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] = __uint_as_float(r[i]);
+    y[i] = __uint_as_float(r[16 + i]);
+  }
+}
+// The same, each the sum of three blocks of columns
+__device__ __forceinline__ void tmem_load_both_sum(uint32_t addr, int apart, float (&x)[8], float (&y)[8]) {
+  uint32_t r[48];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%49];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%50];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%51];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%32,%33,%34,%35,%36,%37,%38,%39}, [%52];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%40,%41,%42,%43,%44,%45,%46,%47}, [%53];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+        "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]),
+        "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31]),
+        "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]),
+        "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47])
+      : "r"(addr), "r"(addr + apart), "r"(addr + 2 * apart), "r"(addr + (16u << 16)), "r"(addr + apart + (16u << 16)), "r"(addr + 2 * apart + (16u << 16))
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = (__uint_as_float(r[16 + i]) + __uint_as_float(r[8 + i])) + __uint_as_float(r[i]);
+    y[i] = (__uint_as_float(r[40 + i]) + __uint_as_float(r[32 + i])) + __uint_as_float(r[24 + i]);
+  }
 }
 
 // ---- products -------------------------------------------------------------------
