@@ -14,8 +14,8 @@
 // SMs, DRAM bounds it. `output` (a block per chunk, head and 64 columns) makes
 // O. The backward pass runs the same chain from the end with Mᵀ, beside the
 // other (see kla_delta_backward.cu). At 8 × 16 heads of 64 × 64 and 4096 tokens in
-// bf16: prepare 191 us (shared memory busy 75% of the time), chain 111 (655 MB,
-// 5.9 TB/s), output 97 (460 MB, 4.7 TB/s).
+// bf16: prepare 191 us (shared memory busy 75% of the time), chain 109 (655 MB,
+// 6.0 TB/s), output 97 (460 MB, 4.7 TB/s).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
 // and everything that flows into them are kept in three, so that a state is as
@@ -760,9 +760,9 @@ cudaError_t chain_nv(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace
 }
 template <typename IO, int DK>
 cudaError_t chain_dk(const DeltaArgs& a, const DeltaGradArgs* d, const Workspace& w, int num_sms, cudaStream_t s) {
-  // A chunk's latency bounds the chain, and blocks of 32 columns take less of it (64 tokens, d 128: 1.7 us against
+  // A chunk's latency bounds the chain, and blocks of 32 columns take less of it (64 tokens, d 128: 1.5 us against
   // 2.5; d 64: 1.3 against 1.7), as long as every block has an SM; with more heads than that W and K would be brought
-  // in twice (128 heads, d 64, 4096 tokens: 165 us against 115; 64 heads, d 128: 216 against 166).
+  // in twice (128 heads, d 64, 4096 tokens: 162 us against 114; 64 heads, d 128: 196 against 167).
   if ((long long)a.B * a.H * (pad64(a.dv) / 32) * (d ? 2 : 1) <= num_sms) return chain_nv<IO, DK, 32>(a, d, w, s);
   return chain_nv<IO, DK, 64>(a, d, w, s);
 }
