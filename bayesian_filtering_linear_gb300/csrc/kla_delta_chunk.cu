@@ -14,7 +14,8 @@
 // SMs, DRAM bounds it. `output` (a block per chunk, head and 64 columns) makes
 // O. The backward pass runs the same chain from the end with Mᵀ, beside the
 // other (see kla_delta_backward.cu). At 8 × 16 heads of 64 × 64 and 4096 tokens in
-// bf16: prepare 191 us (shared memory busy 75% of the time), chain 109 (655 MB,
+// bf16: prepare 180 us (shared memory, and the latency of a
+// dozen steps with four blocks an SM), chain 109 (655 MB,
 // 6.0 TB/s), output 97 (460 MB, 4.7 TB/s).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
@@ -100,13 +101,18 @@ template <typename IO, int DK, bool BWD>
 struct PrepareSmem {
   static constexpr int PARTS = kParts<IO>, IN = PARTS * DK / 64 * kTileBytes, ROWS = PARTS * kTileBytes;
   static constexpr int M3 = 3 * kTileBytes;
-  // T1 first holds A (with the cumulative logs and the diagonal blocks' columns behind it), T2 the inverse in fp32
-  static constexpr int K = 0, Q = IN, V = Q + (BWD ? IN : 0), P = V + ROWS, T1 = P + (BWD ? M3 : 0), T2 = T1 + M3,
-                       A = T1, M = T2;
+  // T1 first holds A (with the cumulative logs and the diagonal blocks' columns behind it), T2 the inverse in fp32.
+  // Forward, the two products of M follow one another with T1 as their operand, and V lies where the inverse was:
+  // four blocks fit on an SM (8 × 16 heads of 64, 4096 tokens: 191 -> 180 us; 16 heads of 128, 65536 tokens, three
+  // blocks that two places in TMEM held back before: 505 -> 485).
+  static constexpr int MB = 64 * 68 * 4 > ROWS ? 64 * 68 * 4 : ROWS;
+  static constexpr int K = 0, Q = IN, V0 = Q + (BWD ? IN : 0), P = V0 + (BWD ? ROWS : 0), T1 = P + (BWD ? M3 : 0),
+                       M = T1 + M3, A = T1, T2 = BWD ? M : T1, V = BWD ? V0 : M;
   static_assert((64 * 68 + 2 * C + kDiagFloats) * 4 <= M3, "");
-  static constexpr int kBytes = T2 + M3;
-  static_assert(kBytes <= kMaxBytes, "");
-  static constexpr int kBlocks = kBytes <= 72 * 1024 ? 3 : kBytes <= 110 * 1024 ? 2 : 1;  // of an SM
+  static constexpr int kBytes = M + (BWD ? M3 : MB);
+  static_assert(kBytes <= kMaxBytes && V % 1024 == 0, "");
+  static constexpr int kFit = 228 * 1024 / (kBytes + 2048);
+  static constexpr int kBlocks = BWD ? (kBytes <= 110 * 1024 ? 2 : 1) : kFit < 4 ? kFit : 4;  // of an SM
 };
 
 // (h + l) += (yh + yl), the sum again as two floats
@@ -165,7 +171,9 @@ template <typename IO, int DK, bool BWD>
 __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) kla_delta_prepare_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                     const Workspace w) {
   using L = PrepareSmem<IO, DK, BWD>;
-  constexpr int PARTS = L::PARTS, COLS = DK == 128 ? 256 : 128, NB = DK / 64;
+  // TMEM holds two blocks of 256 columns: forward, U's product takes W's place where both would need more than 128
+  constexpr bool AFTER = !BWD && DK == 128;
+  constexpr int PARTS = L::PARTS, COLS = BWD && DK == 128 ? 256 : 128, NB = DK / 64, UC = AFTER ? 0 : DK;
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ __align__(16) float G[C], E[C], be[C], nbG[C];  // decays from the start and to the end, β, −β G
   __shared__ uint64_t bar;
@@ -305,29 +313,42 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
     }
   };
   put_m(L::T1, nbG, nullptr);
-  put_m(L::T2, be, nullptr);
+  if (BWD) put_m(L::T2, be, nullptr);
   vl.put(sm + L::V, tid);
   publish();
   if (warp == 0 && elect()) {
     mma<64, DK, 64>(tm, T1r, Kt);
-    mma<64, 64, 64>(tm + DK, T2r, Vt);
+    if (BWD) mma<64, 64, 64>(tm + DK, T2r, Vt);
     commit(&bar);
   }
   const int slices = DV / 64;
   if (slices > 1) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, 64, tid);
   finish();
   float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
-  drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l, bad);
-  drain<64, 1>(tm + DK, w.U + at.chunk * C * DV, l, tid, bad);
+  if (!BWD) {
+    put_m(L::T2, be, nullptr);
+    if (AFTER) drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l, bad);
+    publish();
+    if (warp == 0 && elect()) {
+      mma<64, 64, 64>(tm + UC, T2r, Vt);
+      commit(&bar);
+    }
+  }
+  if (!AFTER) drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l, bad);
+  if (!BWD) {
+    finish();
+    bad = ok ? 0.f : __int_as_float(0x7fc00000);
+  }
+  drain<64, 1>(tm + UC, w.U + at.chunk * C * DV, l, tid, bad);
   if (slices > 1) {
     vl.put(sm + L::V, tid);
     publish();
     if (warp == 0 && elect()) {
-      mma<64, 64, 64>(tm + DK, T2r, Vt);
+      mma<64, 64, 64>(tm + UC, T2r, Vt);
       commit(&bar);
     }
     finish();
-    drain<64, 1>(tm + DK, w.U + at.chunk * C * DV + kBlock, l, tid, bad);
+    drain<64, 1>(tm + UC, w.U + at.chunk * C * DV + kBlock, l, tid, bad);
   }
   if (BWD) {  // Mᵀ (E K) = (E M)ᵀ K, and Mᵀ Pᵀ O' = (P M)ᵀ O'
     const IO* go = reinterpret_cast<const IO*>(d.go);
