@@ -10,13 +10,12 @@
 // W = −M (β G K) and M (β V). `chain` (a block per head and 64 or 32 columns, in
 // order over the chunks) carries S in registers: U = M (β V) + W S and the
 // update, two products and two round trips between TMEM, registers and shared
-// memory per chunk; its latency (1.3 to 1.7 us a chunk) or, with a block on most
+// memory per chunk; its latency (1.3 to 1.5 us a chunk) or, with a block on most
 // SMs, DRAM bounds it. `output` (a block per chunk, head and 64 columns) makes
 // O. The backward pass runs the same chain from the end with Mᵀ, beside the
 // other (see kla_delta_backward.cu). At 8 × 16 heads of 64 × 64 and 4096 tokens in
-// bf16: prepare 180 us (shared memory, and the latency of a
-// dozen steps with four blocks an SM), chain 109 (655 MB,
-// 6.0 TB/s), output 97 (460 MB, 4.7 TB/s).
+// bf16: prepare 180 us (shared memory, and the latency of a dozen steps with four
+// blocks an SM), chain 109 (655 MB, 6.0 TB/s), output 97 (460 MB, 4.7 TB/s).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
 // and everything that flows into them are kept in three, so that a state is as
