@@ -511,8 +511,11 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       }
       __syncwarp();
     }
-    bool in = true;  // no copy is in flight when the block ends, also where a wait ran out
-    for (int i = max(N - STAGES, 0); i < N; ++i) mbar_wait(&full[i % STAGES], i / STAGES & 1, in);
+    bool in = true;  // no copy and no product's arrival is under way when the block ends, also where a wait ran out
+    for (int i = max(N - STAGES, 0); i < N; ++i) {
+      mbar_wait(&full[i % STAGES], i / STAGES & 1, in);
+      mbar_wait(&empty[i % STAGES], i / STAGES & 1, in);
+    }
     for (int i = max(N - L::AHEAD, 0); i < N; ++i) mbar_wait(&loaded[i % L::AHEAD], i / L::AHEAD & 1, in);
   } else if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
