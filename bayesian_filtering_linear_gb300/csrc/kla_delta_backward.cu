@@ -19,10 +19,11 @@
 // then a block per chunk and head makes everything else here. Gradients of q and
 // k that several value heads share are summed from per-head fp32 parts in a
 // fixed order. At 8 × 16 heads of 64 × 64 and 4096 tokens in bf16: prepare 357 us,
-// the chains 232 (1.4 GB, 6 TB/s), gradients 358: two blocks an SM, bound by
+// the chains 232 (1.4 GB, 6 TB/s), gradients 405: two blocks an SM, bound by
 // their steps' latencies, so that a block's loads start together at its start, and
-// the inputs of the block that follows on the SM are sent into L2 (425 -> 358).
-// Sixteen warps instead of eight leave 64 registers a thread: 473 us.
+// the inputs of the block that follows on the SM are sent into L2 (425 -> 358 with
+// operands of two parts). Sixteen warps instead of eight leave 64 registers a
+// thread: 473 us.
 #include "kla_delta_chunk.cuh"
 
 namespace kla {
@@ -32,7 +33,7 @@ namespace {
 
 template <typename IO, int DK>
 struct GradSmem {
-  static constexpr int PN = sizeof(IO) == 2 ? 2 : 3;  // parts of what is not an input
+  static constexpr int PN = 3;  // parts of what is not an input
   static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, ROWS = PN * kTileBytes;
   static constexpr int K = 0, Q = IN, O = 2 * IN, U = O + kParts<IO> * kTileBytes, R = U + ROWS, S = R + ROWS,
                        kStage = S + PN * DK * 128;

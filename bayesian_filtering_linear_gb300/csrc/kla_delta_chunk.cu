@@ -15,12 +15,13 @@
 // O. The backward pass runs the same chain from the end with Mᵀ, beside the
 // other (see kla_delta_backward.cu). At 8 × 16 heads of 64 × 64 and 4096 tokens in
 // bf16: prepare 180 us (shared memory, and the latency of a dozen steps with four
-// blocks an SM), chain 109 (655 MB, 6.0 TB/s), output 97 (460 MB, 4.7 TB/s).
+// blocks an SM), chain 109 (655 MB, 6.0 TB/s), output 106 (460 MB, 4.3 TB/s).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
-// and everything that flows into them are kept in three, so that a state is as
-// exact as in fp32; the outputs of bf16 calls are made from two parts (2^-16,
-// against the 2^-8 of their rounding). Cumulative log decays are kept as sums
+// and everything else that is made of them are kept in three, so that states and
+// outputs are as exact as in fp32 and a bf16 output is rounded once (two parts,
+// 2^-16, would turn some 1 in 2000 outputs to the next step and save 2 to 5% of
+// a call: output 97 for 106 us, gradients 358 for 405). Cumulative log decays are kept as sums
 // of two floats, in powers of two, so that D of late tokens is exact behind a
 // strong decay.
 #include <algorithm>
@@ -667,11 +668,11 @@ __global__ void __launch_bounds__(kChainBlock<IO>)
 // ---- the output ----------------------------------------------------------------------
 template <typename IO, int DK>
 struct OutputSmem {
-  static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, PN = sizeof(IO) == 2 ? 2 : 3;
+  static constexpr int IN = kParts<IO> * DK / 64 * kTileBytes, PN = 3;  // parts of what is not an input
   // U and P come when the products with K, Q and S are done, in their places
-  static constexpr int K = 0, Q = IN, S = 2 * IN, U = K, P = S, kBytes = S + PN * DK * 128,
-                       kFit = 228 * 1024 / (kBytes + 2048), kBlocks = kFit < 4 ? kFit : 4;  // of an SM
-  static_assert(kBytes <= kMaxBytes && PN * kTileBytes <= 2 * IN, "");
+  static constexpr int K = 0, Q = IN, S = 2 * IN > PN * kTileBytes ? 2 * IN : PN * kTileBytes, U = K, P = S,
+                       kBytes = S + PN * DK * 128, kFit = 228 * 1024 / (kBytes + 2048), kBlocks = kFit < 4 ? kFit : 4;  // of an SM
+  static_assert(kBytes <= kMaxBytes, "");
 };
 
 template <typename IO, int DK>
@@ -700,7 +701,8 @@ __global__ void __launch_bounds__(kThreads, OutputSmem<IO, DK>::kBlocks)
   for (int rb = 0; rb < DK / 64; ++rb) xl[rb].load(w.S + at.chunk * DK * DV + col * DK + rb * kBlock, tid);
   ul.load(w.U + at.chunk * C * DV + col * 64, tid);
   // For the block that follows on this SM, into L2, where fewer than four blocks cover for each other (65536 tokens,
-  // 16 heads of 128: 562 -> 527 us; d_k 64 in bf16, whose inputs are half as many bytes: 116 -> 120).
+  // 16 heads of 128, with three blocks an SM: 562 -> 527 us, with the two of now 636; d_k 64 in bf16, whose inputs are
+  // half as many bytes: 116 -> 120).
   const unsigned after = blockIdx.x + ahead;
   if (L::kBlocks < 4 && tid == 128 && col == 0 && after < gridDim.x) {
     const Where next = where(a, after / (DV / 64));
