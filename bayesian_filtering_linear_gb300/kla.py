@@ -9,6 +9,7 @@ implementation here. If the library is missing this module fails to import.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -189,6 +190,34 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# the current stream's handle without making a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_stream(fn):
+    """A call with ``stream=`` runs as it would under ``torch.cuda.stream(stream)``:
+    what it allocates, its workspace above all, belongs to that stream, so that
+    memory which torch takes back is given out again only behind the kernels.
+    What it returns may also be used on the caller's stream, once that waits for
+    ``stream``. As ever, ``stream`` has to wait for inputs made elsewhere, and
+    they have to live until it has read them."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if stream.cuda_stream == _raw_stream(stream.device.index):
+            return fn(*args, stream=stream, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = fn(*args, stream=stream, **kw)
+        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(caller)
+        return out
+    return call
+
+
 def _need(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -202,6 +231,7 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+@_on_stream
 def forward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, y=None, lamT=None, etaT=None,
             strategy: str | int = "auto", chunk_len: int = 0, workspace=None, stream=None,
             final_state: bool = True, rows_per_lane: int = 0, uncertainty: bool = False, y_var=None,
@@ -262,6 +292,7 @@ def forward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, y=None, lamT=None,
     return y, lamT, etaT
 
 
+@_on_stream
 def step(q, k, v, lam_v, a, pbar, lam, eta, *, y=None, stream=None, gates: int = 0):
     """One decode step: q, k, a, pbar ``[B,H,dk]``, v, lam_v ``[B,H,dv]``;
     updates the fp32 state (lam, eta) ``[B,H,dk,dv]`` in place; returns y."""
@@ -290,6 +321,7 @@ def step(q, k, v, lam_v, a, pbar, lam, eta, *, y=None, stream=None, gates: int =
     return y
 
 
+@_on_stream
 def backward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, gy=None, glamT=None, getaT=None,
              state_grads: bool = True, workspace=None, stream=None, gates: int = 0):
     """Gradients of a scalar loss through :func:`forward`, given ``gy`` = dL/dy
@@ -336,6 +368,7 @@ def backward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, gy=None, glamT=No
 
 # ---- context-parallel sharding over T -----------------------------------------
 
+@_on_stream
 def shard_map(q, k, v, lam_v, a, pbar, *, gates: int = 0, out=None, stream=None):
     """The composed map of a shard (all of its tokens), ``[7, B, H, dk, dv]``
     fp32 (kla_shard_map): (A, B, C, D, E, F, G) take the state (P, μ) before
@@ -359,6 +392,7 @@ def shard_map(q, k, v, lam_v, a, pbar, *, gates: int = 0, out=None, stream=None)
     return out
 
 
+@_on_stream
 def shard_start(maps, lam0=None, eta0=None, *, lam_out=None, eta_out=None, stream=None):
     """Start state (λ, η) of the shard after those whose maps are stacked in
     ``maps`` ``[n, 7, B, H, dk, dv]`` (in sequence order), from (λ0, η0) (None:
@@ -395,6 +429,7 @@ def exchange_maps(local_map, group=None):
     return out if out.device == local_map.device else out.to(local_map.device)
 
 
+@_on_stream
 def forward_context_parallel(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, group=None, gates: int = 0,
                              stream=None, **forward_kw):
     """KLA forward over a sequence cut along T across the ranks of ``group``
@@ -425,6 +460,7 @@ def _conv_shapes(x, weight, window, W):
     return B, H, T, D
 
 
+@_on_stream
 def conv(x, weight, bias=None, window=None, *, activation: int = ACT_SILU, y=None, window_out=None,
          update_window: bool = False, stream=None):
     """Causal depthwise convolution of ``x`` ``[B,H,T,D]`` with taps ``weight``
@@ -463,6 +499,7 @@ def conv(x, weight, bias=None, window=None, *, activation: int = ACT_SILU, y=Non
     return y, window_out
 
 
+@_on_stream
 def conv_backward(x, weight, bias=None, window=None, *, gy=None, gwindow_out=None, activation: int = ACT_SILU,
                   param_grads: bool = True, window_grad: bool = True, workspace=None, stream=None):
     """Gradients through :func:`conv` (kla_conv_backward) given ``gy`` = dL/dy
@@ -523,10 +560,6 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-# the current stream's handle without making a Stream object, where torch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
 
 def _run(index, stream, fn, args):
     """``fn(*args, stream)`` on device ``index``, with the given or its current stream."""
@@ -555,6 +588,7 @@ def _delta_shapes(q, k, v, g, beta, tokens=True):
     return B, Hk, H, T, dk, dv, index, dt, io
 
 
+@_on_stream
 def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, o=None, stateT=None,
                   final_state: bool = True, workspace=None, stream=None):
     """The gated delta rule over whole sequences (kla_delta_forward): with
@@ -588,6 +622,7 @@ def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, 
     return o, stateT
 
 
+@_on_stream
 def delta_step(q, k, v, g, beta, state, *, scale: float | None = None, o=None, stream=None):
     """One decode token of the gated delta rule (kla_delta_step): q, k
     ``[B,Hk,dk]``, v ``[B,H,dv]``, g, beta ``[B,H]``; the fp32 state
@@ -606,6 +641,7 @@ def delta_step(q, k, v, g, beta, state, *, scale: float | None = None, o=None, s
     return o
 
 
+@_on_stream
 def delta_backward(q, k, v, g, beta, state0=None, *, go=None, gstateT=None, scale: float | None = None,
                    state_grad: bool = True, workspace=None, stream=None):
     """Gradients of a scalar loss through :func:`delta_forward` given ``go`` =
@@ -718,6 +754,7 @@ def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset, norm,
     return B, Hq, Hk, T, D, index, dt, opt, _Strides(*q_strides[:3]), k_strides
 
 
+@_on_stream
 def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, norm: str = "rms",
               layout: str = "half", eps: float = 1e-6, rot_scale: float = 1.0, offset: int = 0, yq=None, yk=None,
               stream=None):
@@ -745,6 +782,7 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     return yq, yk
 
 
+@_on_stream
 def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, gyq=None, gyk=None,
                        norm: str = "rms", layout: str = "half", eps: float = 1e-6, rot_scale: float = 1.0,
                        offset: int = 0, workspace=None, stream=None):
