@@ -314,7 +314,14 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     mma<64, DK, 64>(tm + 2 * DK, At, Kt, true);
     commit(&bar);
   }
-  if (warp == 1) {  // the decay's gradient needs nothing more: sums of `from` from a token on, of `to` before it; two a lane
+  finish();
+  if (!ok) {  // the last of an even number of products may still run
+    bool in = true;
+    mbar_wait(&bar, 1, in);
+  }
+  // a wait of any thread ran out: everything from here on is no number (gv comes of no product)
+  const float bad = __syncthreads_or(!ok) ? __int_as_float(0x7fc00000) : 0.f;
+  if (warp == 1) {  // the decay's gradient: sums of `from` from a token on, of `to` before it; two a lane
     float x = 0.f;
     for (int i = 0; i < 8; ++i) x += zs[i];
     x *= G[C - 1];
@@ -331,11 +338,9 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     const float f2 = __shfl_down_sync(~0u, after, 1), y = __shfl_up_sync(~0u, ahead, 1);
     const float from1 = f1 + (lane < 31 ? f2 : 0.f), to0 = lane ? y : 0.f;
     IO* gg = reinterpret_cast<IO*>(d.gg) + vrow + t;
-    if (t < at.len) gg[0] = from_f32<IO>((x + before[t]) + (f0 + from1) + to0);
-    if (t + 1 < at.len) gg[1] = from_f32<IO>((x + before[t + 1]) + from1 + (to0 + t0));
+    if (t < at.len) gg[0] = from_f32<IO>((x + before[t]) + (f0 + from1) + to0 + bad);
+    if (t + 1 < at.len) gg[1] = from_f32<IO>((x + before[t + 1]) + from1 + (to0 + t0) + bad);
   }
-  finish();
-  const float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
   ax[0] = ax[1] = 0.f;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {

@@ -125,26 +125,22 @@ __device__ __forceinline__ void add_two(float& h, float& l, float yh, float yl) 
 
 // Blocks of a product from TMEM: `BLOCKS` of them across columns (ROWS = 64) or down 128 rows
 template <int ROWS, int BLOCKS>
-__device__ __forceinline__ void drain(uint32_t tm, float* out, const Lanes& l, int tid, float bad) {
+__device__ __forceinline__ void drain(uint32_t tm, float* out, const Lanes& l, int tid) {
 #pragma unroll
   for (int b = 0; b < BLOCKS; ++b) {
     Fragment f;
     tmem_load(tm + ((uint32_t)(32 * l.quad + (ROWS == 64 ? 0 : 16 * b)) << 16) + (ROWS == 64 ? 64 * b : 0) + 32 * l.half, f.v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f.v[i] += bad;
     f.store(out + b * kBlock, tid);
   }
 }
 
 // 64 × 64 BLOCKS of a product as the chain's operand (see Workspace). A lane's four words of a row turn into one eight.
 template <int BLOCKS>
-__device__ __forceinline__ void drain_parts(uint32_t tm, char* out, const Lanes& l, float bad) {
+__device__ __forceinline__ void drain_parts(uint32_t tm, char* out, const Lanes& l) {
 #pragma unroll
   for (int b = 0; b < BLOCKS; ++b) {
     Fragment f;
     tmem_load(tm + ((uint32_t)(32 * l.quad) << 16) + 64 * b + 32 * l.half, f.v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f.v[i] += bad;
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       const int r = l.r + 8 * o, c = 4 * l.half + (l.lane & 3);
@@ -324,22 +320,18 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
   const int slices = DV / 64;
   if (slices > 1) vl.fetch(reinterpret_cast<const IO*>(a.v) + vrow, at.len, a.dv, 64, tid);
   finish();
-  float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
   if (!BWD) {
     put_m(L::T2, be, nullptr);
-    if (AFTER) drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l, bad);
+    if (AFTER) drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l);
     publish();
     if (warp == 0 && elect()) {
       mma<64, 64, 64>(tm + UC, T2r, Vt);
       commit(&bar);
     }
   }
-  if (!AFTER) drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l, bad);
-  if (!BWD) {
-    finish();
-    bad = ok ? 0.f : __int_as_float(0x7fc00000);
-  }
-  drain<64, 1>(tm + UC, w.U + at.chunk * C * DV, l, tid, bad);
+  if (!AFTER) drain_parts<NB>(tm, w.W + at.chunk * 3 * NB * kTileBytes, l);
+  if (!BWD) finish();
+  drain<64, 1>(tm + UC, w.U + at.chunk * C * DV, l, tid);
   if (slices > 1) {
     vl.put(sm + L::V, tid);
     publish();
@@ -348,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
       commit(&bar);
     }
     finish();
-    drain<64, 1>(tm + UC, w.U + at.chunk * C * DV + kBlock, l, tid, bad);
+    drain<64, 1>(tm + UC, w.U + at.chunk * C * DV + kBlock, l, tid);
   }
   if (BWD) {  // Mᵀ (E K) = (E M)ᵀ K, and Mᵀ Pᵀ O' = (P M)ᵀ O'
     const IO* go = reinterpret_cast<const IO*>(d.go);
@@ -362,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
       commit(&bar);
     }
     finish();
-    drain_parts<NB>(tm, w.Wr + at.chunk * 3 * NB * kTileBytes, l, bad);
+    drain_parts<NB>(tm, w.Wr + at.chunk * 3 * NB * kTileBytes, l);
     Fragment pm;
     tmem_load(tm + DK + rows + 32 * half, pm.v);
     pm.put<3>(sm + L::T1, kTileBytes, r0, c0);
@@ -385,13 +377,19 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
         commit(&bar);
       }
       finish();
-      bad = ok ? 0.f : __int_as_float(0x7fc00000);
-      drain<64, 1>(tm, w.R + at.chunk * C * DV + sl * kBlock, l, tid, bad);
-      drain<DK, NB>(tm + 64, w.Z + at.chunk * DK * DV + sl * NB * kBlock, l, tid, bad);
+      drain<64, 1>(tm, w.R + at.chunk * C * DV + sl * kBlock, l, tid);
+      drain<DK, NB>(tm + 64, w.Z + at.chunk * DK * DV + sl * NB * kBlock, l, tid);
     }
   }
   fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {  // a wait ran out: M (β V) and Mᵀ Pᵀ O' carry it into everything that comes of the chunk
+    bool in = true;
+    mbar_wait(&bar, phase ^ 1, in);
+    const int dv = pad64(a.dv);
+    const size_t block = (size_t)block_again() * C * dv;
+    fill_nan(w.U + block, C, dv, dv, thread_again(), kThreads);
+    if (BWD) fill_nan(w.R + block, C, dv, dv, thread_again(), kThreads);
+  }
   if (warp == 0) tmem_free(tm, COLS);
 }
 
@@ -425,6 +423,19 @@ struct ChainSmem {
                        AHEAD = B + 2 * (IN + GATES) <= kMaxBytes ? 2 : 1, kBytes = B + AHEAD * (IN + GATES);
   static_assert(kBytes <= kMaxBytes, "");
 };
+
+// A wait of any warp ran out: U (rev: dR) of the block's columns and its last state say so. (Within the kernel it cost the
+// long case 2%.)
+template <typename IO, bool REV, int NV>
+__device__ __noinline__ void mark_chain(const DeltaArgs& a, const DeltaGradArgs& d, const Workspace& w) {
+  const int dv = pad64(a.dv), n = (a.T + C - 1) / C, c0 = (int)(block_again() % (dv / NV)) * NV;
+  const size_t head = block_again() / (dv / NV);
+  float* u = (REV ? w.R : w.U) + head * n * C * dv + c0 / 64 * kBlock + c0 % 64 * 16;  // (a half: threads 128 to 255 of 256)
+  for (int i = 0; i < n; ++i, u += C * dv) fill_nan(u, 4, NV * 16, 1024, thread_again(), kChainBlock<IO>);
+  float* const last = REV ? d.gstate0 : a.stateT;
+  if (last && c0 < a.dv)
+    fill_nan(last + head * a.dk * a.dv + c0, a.dk, min(NV, a.dv - c0), a.dv, thread_again(), kChainBlock<IO>);
+}
 
 // NV: columns of a block, 64 or 32.
 template <typename IO, int DK, bool REV, int NV>
@@ -518,6 +529,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       mbar_wait(&empty[i % STAGES], i / STAGES & 1, in);
     }
     for (int i = max(N - L::AHEAD, 0); i < N; ++i) mbar_wait(&loaded[i % L::AHEAD], i / L::AHEAD & 1, in);
+    ok &= in;
   } else if (warp >= kChainThreads / 32) {
     const int ft = tid - kChainThreads;
     const IO* k = reinterpret_cast<const IO*>(a.k) + (size_t)key * a.T * a.dk;
@@ -639,21 +651,20 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         for (int e = 0; e < 4 * J; ++e)
           X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? more[rb].v[e] + F[REV ? rb : 0].v[e] : more[rb].v[e]);
     }
-    float* last = REV ? d.gstate0 : a.stateT;
+    float* const last = REV ? d.gstate0 : a.stateT;
     if (last) {
-      const float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait ran out
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int e = 0; e < 4 * J; e += 2) {
           const int r = block_row<DK>(l, rb) + (e & 2) * 4, c = gc + (e >> 2) * 8;
           if (r < a.dk && c < a.dv)
-            store_two(last + ((size_t)bh * a.dk + r) * a.dv + c, X[rb].v[e] + bad, X[rb].v[e + 1] + bad);
+            store_two(last + ((size_t)bh * a.dk + r) * a.dv + c, X[rb].v[e], X[rb].v[e + 1]);
         }
     }
   }
   fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) mark_chain<IO, REV, NV>(a, d, w);
   if (warp == 0) tmem_free(tm, COLS);
 }
 
@@ -758,12 +769,18 @@ __global__ void __launch_bounds__(kThreads, OutputSmem<IO, DK>::kBlocks)
   mbar_wait(&bar, 1, ok);
   fence_after();
   tmem_load(tm + rows + 32 * half, v);
-  const float scale = ok ? a.scale : __int_as_float(0x7fc00000);  // a wait ran out
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = scale * fmaf(G[l.r + (i & 2) * 4], y[i], v[i]);
+  for (int i = 0; i < 16; ++i) v[i] = a.scale * fmaf(G[l.r + (i & 2) * 4], y[i], v[i]);
   store_rows(reinterpret_cast<IO*>(a.o) + ((size_t)at.bh * a.T + at.t0) * a.dv, l, col, at.len, a.dv, v);
   fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {  // a wait ran out
+    bool in = true;
+    mbar_wait(&bar, 1, in);
+    const int slices = pad64(a.dv) / 64, c0 = (int)(block_again() % slices) * 64;
+    const Where rows = where(a, block_again() / slices);
+    fill_nan(reinterpret_cast<IO*>(a.o) + ((size_t)rows.bh * a.T + rows.t0) * a.dv + c0, rows.len, min(64, a.dv - c0), a.dv,
+             thread_again(), kThreads);
+  }
   if (warp == 0) tmem_free(tm, 128);
 }
 

@@ -50,16 +50,39 @@ __device__ __forceinline__ uint64_t nanoseconds() {
   return t;
 }
 // Waits for the phase of the given parity, for two seconds at most; then it
-// gives up: `ok` turns false, and later waits return at once.
+// gives up: `ok` turns false, and later waits return at once. A block that has
+// such a thread overwrites its outputs at its end (fill_nan).
 __device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, bool& ok) {
+#ifdef KLA_RAN_OUT  // a test's build: every wait is waited for, and counts as run out for the threads that this names
+  bool real = true;
+  if (KLA_RAN_OUT) ok = false;
+#else
+  bool& real = ok;
+#endif
   const uint32_t addr = smem_addr(bar);
-  if (!ok || mbar_try(addr, parity)) return;
+  if (!real || mbar_try(addr, parity)) return;
   const uint64_t start = nanoseconds();
   while (!mbar_try(addr, parity))
     if (nanoseconds() - start > 2000000000ull) {
-      ok = false;
+      real = ok = false;
       return;
     }
+}
+// Thread and block read anew: what follows a wait that ran out keeps no registers of the way before it.
+__device__ __forceinline__ unsigned thread_again() {
+  unsigned x;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
+  return x;
+}
+__device__ __forceinline__ unsigned block_again() {
+  unsigned x;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(x));
+  return x;
+}
+// Rows of an output that came of a wait that ran out: no numbers.
+template <typename T>
+__device__ __forceinline__ void fill_nan(T* out, int rows, int cols, size_t stride, int tid, int threads) {
+  for (int i = tid; i < rows * cols; i += threads) out[i / cols * stride + i % cols] = from_f32<T>(__int_as_float(0x7fc00000));
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
