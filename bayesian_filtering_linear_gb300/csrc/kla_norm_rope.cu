@@ -142,8 +142,10 @@ __device__ __forceinline__ float row_sum(float x) {
 // The y index of a block says whether it works on q or on k. It takes GROUPS
 // tokens and `per` of the heads at a time; BWD also sums its weight gradients.
 // Lanes without a token go along, so that every lane of a warp takes part in
-// its exchanges.
-template <typename IO, int D, bool BWD, int MODE>
+// its exchanges. NORMED false: the gradients without a norm, which know nothing
+// of x, whatever x holds (a kernel of its own: a branch or a mask in the other
+// took 3% of the headline's gradients).
+template <typename IO, int D, bool BWD, int MODE, bool NORMED>
 __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) kla_norm_rope_kernel(const NormRopeArgs a, int per) {
   constexpr int VE = Row<IO>::N, P = VE / 2, LPR = D / VE, GROUPS = kThreads / LPR, U = 2;
   __shared__ __align__(16) float rows[GROUPS][D];  // halves that cut lanes; the block's weight gradients
@@ -256,10 +258,14 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) kla_norm_rope_kernel(co
             g[j] = f2_mul(g[j], w[j]);
             dot2 = f2_fma(g[j], v[j], dot2);
           }
-          const float dot = -f * row_sum<LPR>(f2_lo(dot2) + f2_hi(dot2));
-          const f2 d2 = f2_make(dot, dot);
+          if (NORMED) {
+            const float dot = -f * row_sum<LPR>(f2_lo(dot2) + f2_hi(dot2));
+            const f2 d2 = f2_make(dot, dot);
 #pragma unroll
-          for (int j = 0; j < P; ++j) y[j] = f2_mul(r2, f2_fma(v[j], d2, g[j]));
+            for (int j = 0; j < P; ++j) g[j] = f2_mul(r2, f2_fma(v[j], d2, g[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < P; ++j) y[j] = g[j];
         }
         if (on) Row<IO>::store(out, y);
         out += ostep;
@@ -304,11 +310,17 @@ void geometry(int B, int Hq, int Hk, int T, int D, int io, int num_sms, bool bwd
   *blocks = (unsigned)std::max(std::min(n, bwd ? want : 1LL << 30), 1LL);
 }
 
+template <typename IO, int D, bool BWD, bool NORMED>
+void launch_rows(const NormRopeArgs& a, dim3 grid, int per, cudaStream_t s) {
+  if (a.layout || a.rot == 0) kla_norm_rope_kernel<IO, D, BWD, kInLane, NORMED><<<grid, kThreads, 0, s>>>(a, per);
+  else if (a.rot / 2 % Row<IO>::N == 0) kla_norm_rope_kernel<IO, D, BWD, kOtherLane, NORMED><<<grid, kThreads, 0, s>>>(a, per);
+  else kla_norm_rope_kernel<IO, D, BWD, kAnywhere, NORMED><<<grid, kThreads, 0, s>>>(a, per);
+}
+
 template <typename IO, int D, bool BWD>
 void launch_mode(const NormRopeArgs& a, dim3 grid, int per, cudaStream_t s) {
-  if (a.layout || a.rot == 0) kla_norm_rope_kernel<IO, D, BWD, kInLane><<<grid, kThreads, 0, s>>>(a, per);
-  else if (a.rot / 2 % Row<IO>::N == 0) kla_norm_rope_kernel<IO, D, BWD, kOtherLane><<<grid, kThreads, 0, s>>>(a, per);
-  else kla_norm_rope_kernel<IO, D, BWD, kAnywhere><<<grid, kThreads, 0, s>>>(a, per);
+  if (BWD && a.norm == kNormNone) launch_rows<IO, D, BWD, !BWD>(a, grid, per, s);
+  else launch_rows<IO, D, BWD, true>(a, grid, per, s);
 }
 
 template <typename IO, bool BWD>
