@@ -712,7 +712,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
         def index(turns):  # the pair that turns so often over the original length
             return half * math.log(original_length / (2 * math.pi * turns)) / math.log(base)
 
-        lo, hi = max(0.0, math.floor(index(beta_fast))), min(half - 1.0, math.ceil(index(beta_slow)))
+        # the blend's ends stay where they are, also before the first pair and past the last
+        lo, hi = math.floor(index(beta_fast)), math.ceil(index(beta_slow))
         slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         freq = freq * (1 - slow) + freq / factor * slow
         rot_scale = 0.1 * math.log(factor) + 1.0
