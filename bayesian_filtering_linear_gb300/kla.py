@@ -749,10 +749,13 @@ def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset, norm,
         rot = 2 * half
         if not _fits(inv_freq, torch.float32, (half,), index):
             _need(inv_freq, "inv_freq", torch.float32, (half,), q.device)
-    if positions is not None and not _fits(positions, torch.int64, (B, T), index):
-        _need(positions, "positions", torch.int64, (B, T), q.device)
+    if positions is not None:
+        if not _fits(positions, torch.int64, (B, T), index):
+            _need(positions, "positions", torch.int64, (B, T), q.device)
+        if positions.data_ptr() % 16:  # a token's slice may start anywhere
+            positions = positions.clone()
     opt = NormRopeOptions(_NORMS[norm], _LAYOUTS[layout], rot, eps, rot_scale, offset)
-    return B, Hq, Hk, T, D, index, dt, opt, _Strides(*q_strides[:3]), k_strides
+    return B, Hq, Hk, T, D, index, dt, opt, _Strides(*q_strides[:3]), k_strides, positions
 
 
 @_on_stream
@@ -765,7 +768,7 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     and k ``[B,Hk,T,D]`` (or None) may be strided views, e.g. a projection's
     ``[B,T,H,D]`` transposed; ``positions`` int64 ``[B,T]`` (None: ``offset`` +
     t). Returns contiguous ``(yq, yk)``."""
-    B, Hq, Hk, T, D, index, dt, opt, q_strides, k_strides = _norm_rope_args(
+    B, Hq, Hk, T, D, index, dt, opt, q_strides, k_strides, positions = _norm_rope_args(
         q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale)
     if yq is None:
         yq = torch.empty((B, Hq, T, D), dtype=dt, device=q.device)
@@ -790,7 +793,7 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
     """Gradients through :func:`norm_rope` given ``gyq``, ``gyk`` (None: zero;
     kla_norm_rope_backward). Returns a dict with ``gq, gk`` (in the memory
     order of q and k) and, for given weights, ``gq_weight, gk_weight``."""
-    B, Hq, Hk, T, D, index, dt, opt, q_strides, k_strides = _norm_rope_args(
+    B, Hq, Hk, T, D, index, dt, opt, q_strides, k_strides, positions = _norm_rope_args(
         q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale)
     for name, t, h in (("gyq", gyq, Hq), ("gyk", gyk, Hk)):
         if t is not None and not _fits(t, dt, (B, h, T, D), index):

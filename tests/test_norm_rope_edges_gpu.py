@@ -27,3 +27,22 @@ def test_without_a_norm_the_gradient_does_not_depend_on_the_row(io, layout, rot,
     bad[1, 0, 7] = 3e38
     bad[1, 1, 8, 4:9] = INF
     assert torch.equal(kla.norm_rope_backward(bad, None, w, None, f, gyq=gy, **how)["gq"], want)
+
+
+@pytest.mark.parametrize("B,T", [(1, 1), (1, 4), (2, 3)])
+def test_positions_may_start_at_any_element(B, T):
+    """A decode loop's positions[:, t:t + 1]: eight bytes further for each token."""
+    q = torch.randn(B, 2, T, 32, device=DEV)
+    w = 1 + 0.1 * torch.randn(32, device=DEV)
+    f = kla.rope_frequencies(32, device=DEV)[0]
+    many = torch.arange(7 * B * T + 1, device=DEV) * 1001
+    for start in (1, 2, 3, 7):
+        pos = many[start:start + B * T].view(B, T)
+        want = kla.norm_rope(q, q, w, w, f, pos.clone())
+        assert pos.data_ptr() % 16 == 8 * (start & 1)
+        assert all(torch.equal(a, b) for a, b in zip(kla.norm_rope(q, q, w, w, f, pos), want))
+        a, b = (kla.norm_rope_backward(q, q, w, w, f, p, gyq=q, gyk=q) for p in (pos, pos.clone()))
+        assert all(torch.equal(a[n], b[n]) for n in a)
+    x = q.requires_grad_()
+    kla.qk_norm_rope(x, None, None, None, f, many[1:1 + B * T].view(B, T))[0].sum().backward()
+    assert bool(x.grad.isfinite().all())
