@@ -834,6 +834,32 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
 
 # ---- autograd: the entry points as differentiable torch operations ------------
 
+class _OnceFunction(torch.autograd.Function):
+    """Gradients as they are, tied to what they were made of, whose own derivative raises."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("second derivatives of this operation are not built")
+
+
+def _once(backward):
+    """A backward whose gradients would count as constants under ``create_graph=True``: deriving them raises."""
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        given = [t for t in out if t is not None]
+        tied = iter(_OnceFunction.apply(len(given), *given, *ctx.saved_tensors, *grads))
+        return tuple(None if t is None else next(tied) for t in out)
+    return call
+
+
 class _ScanFunction(torch.autograd.Function):
     """kla_forward with kla_backward as its derivative."""
 
@@ -845,6 +871,7 @@ class _ScanFunction(torch.autograd.Function):
         return y, lamT, etaT
 
     @staticmethod
+    @_once
     def backward(ctx, gy, glamT, getaT):
         q, k, v, lam_v, a, pbar, lam0, eta0 = ctx.saved_tensors
         g = backward(q, k, v, lam_v, a, pbar, lam0, eta0,
@@ -872,6 +899,7 @@ class _ConvFunction(torch.autograd.Function):
         return y, wout
 
     @staticmethod
+    @_once
     def backward(ctx, gy, gwindow_out):
         x, weight, bias, window = ctx.saved_tensors
         g = conv_backward(x, weight, bias, window,
@@ -899,6 +927,7 @@ class _DeltaFunction(torch.autograd.Function):
         return o, stateT
 
     @staticmethod
+    @_once
     def backward(ctx, go, gstateT):
         q, k, v, g, beta, state0 = ctx.saved_tensors
         d = delta_backward(q, k, v, g, beta, state0, go=None if go is None else go.to(q.dtype).contiguous(),
@@ -923,6 +952,7 @@ class _NormRopeFunction(torch.autograd.Function):
         return norm_rope(q, k, q_weight, k_weight, inv_freq, positions, **how)
 
     @staticmethod
+    @_once
     def backward(ctx, gyq, gyk):
         q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
         d = norm_rope_backward(q, k, q_weight, k_weight, inv_freq, positions,
