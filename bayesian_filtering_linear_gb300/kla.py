@@ -127,9 +127,14 @@ class KlaError(RuntimeError):
         super().__init__(f"{where}: {LIB.kla_status_string(status).decode()} (status {status})")
 
 
-def _check(status: int, where: str):
+def _check(status: int, where: str, *written):
+    """Raises for a status other than OK. ``written``: tensors that the call has
+    written to, which autograd is told of: a state saved for a backward pass
+    that changes meanwhile makes that pass raise."""
     if status != OK:
         raise KlaError(status, where)
+    if written:
+        torch.autograd.graph.increment_version([t for t in written if t is not None])
 
 
 def status_string(status: int) -> str:
@@ -283,12 +288,12 @@ def forward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, y=None, lamT=None,
                                              _ptr(eta0), _ptr(y), _ptr(y_var), _ptr(lamT), _ptr(etaT), B, H, T, dk,
                                              dv, _IO[dt], _ptr(workspace), ws_bytes, ctypes.byref(opt),
                                              _stream(stream))
-            _check(st, "kla_forward_uncertainty")
+            _check(st, "kla_forward_uncertainty", y, lamT, etaT, y_var)
             return y, lamT, etaT, y_var
         st = LIB.kla_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(lam_v), _ptr(a), _ptr(pbar), _ptr(lam0), _ptr(eta0),
                              _ptr(y), _ptr(lamT), _ptr(etaT), B, H, T, dk, dv, _IO[dt],
                              _ptr(workspace), ws_bytes, ctypes.byref(opt), _stream(stream))
-    _check(st, "kla_forward")
+    _check(st, "kla_forward", y, lamT, etaT)
     return y, lamT, etaT
 
 
@@ -317,7 +322,7 @@ def step(q, k, v, lam_v, a, pbar, lam, eta, *, y=None, stream=None, gates: int =
         else:
             st = LIB.kla_step(_ptr(q), _ptr(k), _ptr(v), _ptr(lam_v), _ptr(a), _ptr(pbar), _ptr(lam), _ptr(eta),
                               _ptr(y), B, H, dk, dv, _IO[dt], _stream(stream))
-    _check(st, "kla_step")
+    _check(st, "kla_step", y, lam, eta)
     return y
 
 
@@ -388,7 +393,7 @@ def shard_map(q, k, v, lam_v, a, pbar, *, gates: int = 0, out=None, stream=None)
     with torch.cuda.device(dev):
         st = LIB.kla_shard_map(_ptr(q), _ptr(k), _ptr(v), _ptr(lam_v), _ptr(a), _ptr(pbar), _ptr(out),
                                B, H, T, dk, dv, _IO[dt], int(gates), _stream(stream))
-    _check(st, "kla_shard_map")
+    _check(st, "kla_shard_map", out)
     return out
 
 
@@ -411,7 +416,7 @@ def shard_start(maps, lam0=None, eta0=None, *, lam_out=None, eta_out=None, strea
     with torch.cuda.device(dev):
         st = LIB.kla_shard_start(_ptr(maps) if n else None, n, _ptr(lam0), _ptr(eta0), _ptr(lam_out),
                                  _ptr(eta_out), B, H, dk, dv, _stream(stream))
-    _check(st, "kla_shard_start")
+    _check(st, "kla_shard_start", lam_out, eta_out)
     return lam_out, eta_out
 
 
@@ -495,7 +500,7 @@ def conv(x, weight, bias=None, window=None, *, activation: int = ACT_SILU, y=Non
     with torch.cuda.device(dev):
         st = LIB.kla_conv(_ptr(x), _ptr(weight), _ptr(bias), _ptr(window), _ptr(y), _ptr(window_out),
                           B, H, T, D, W, _IO[dt], int(activation), _stream(stream))
-    _check(st, "kla_conv")
+    _check(st, "kla_conv", y, window_out)
     return y, window_out
 
 
@@ -618,7 +623,7 @@ def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, 
               (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), o.data_ptr(),
                _addr(stateT), B, Hk, H, T, dk, dv, io, dk ** -0.5 if scale is None else scale, _addr(workspace),
                ws_bytes))
-    _check(st, "kla_delta_forward")
+    _check(st, "kla_delta_forward", o, stateT)
     return o, stateT
 
 
@@ -637,7 +642,7 @@ def delta_step(q, k, v, g, beta, state, *, scale: float | None = None, o=None, s
     st = _run(index, stream, LIB.kla_delta_step,
               (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), o.data_ptr(),
                B, Hk, H, dk, dv, io, dk ** -0.5 if scale is None else scale))
-    _check(st, "kla_delta_step")
+    _check(st, "kla_delta_step", o, state)
     return o
 
 
@@ -782,7 +787,7 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     st = _run(index, stream, LIB.kla_norm_rope,
               (q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions),
                yq.data_ptr(), _addr(yk), B, Hq, Hk, T, D, q_strides, k_strides, _IO[dt], ctypes.byref(opt)))
-    _check(st, "kla_norm_rope")
+    _check(st, "kla_norm_rope", yq, yk)
     return yq, yk
 
 
