@@ -837,9 +837,14 @@ kla_status kla_delta_backward(const void* q, const void* k, const void* v, const
   const Range outs[] = {{gq, keys}, {gk, keys}, {gv, vals}, {gg, gates}, {gbeta, gates}, {gstate0, states},
                         {workspace, need}};
   if (ranges_clash(outs, 7, ins, 8)) return KLA_ERR_INVALID_ARG;
-  if (bh == 0) return KLA_OK;
-  if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (bh == 0) {  // key heads that no value head reads have a gradient all the same
+    if (keys > 0 && ((gq && cudaMemsetAsync(gq, 0, keys, s) != cudaSuccess) ||
+                     (gk && cudaMemsetAsync(gk, 0, keys, s) != cudaSuccess)))
+      return KLA_ERR_CUDA;
+    return KLA_OK;
+  }
+  if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
   if (T == 0) {  // the state's gradient passes through
     if (!gstate0) return KLA_OK;
     const cudaError_t e = gstateT ? cudaMemcpyAsync(gstate0, gstateT, states, cudaMemcpyDeviceToDevice, s)

@@ -406,7 +406,8 @@ kla_status kla_delta_step(const void* q, const void* k, const void* v, const voi
  *   go = dL/do [B,H,T,dv] in `io`, gstateT = dL/dS_T fp32 (each NULL: zero).
  *   Outputs, written and not accumulated, in `io`: gq, gk [B,Hk,T,dk] (summed
  *     over the value heads of a key head in a fixed order), gv [B,H,T,dv], gg,
- *     gbeta [B,H,T]; required unless B·H·T = 0. gstate0 fp32 [B,H,dk,dv] or
+ *     gbeta [B,H,T]; required unless B·H·T = 0 (with H = 0 < Hk, gq and gk are
+ *     set to zero where given). gstate0 fp32 [B,H,dk,dv] or
  *     NULL: dL/dS_0 (with state0 NULL: at zero).
  *   workspace / ws_bytes: device scratch of at least
  *     kla_delta_backward_workspace_size() bytes (else WORKSPACE).
