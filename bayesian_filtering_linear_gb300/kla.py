@@ -236,6 +236,19 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _space(workspace, index):
+    """The bytes of a workspace, which the kernels write to as they find it: contiguous, on the inputs' device."""
+    if workspace is None:
+        return 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{index}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 @_on_stream
 def forward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, y=None, lamT=None, etaT=None,
             strategy: str | int = "auto", chunk_len: int = 0, workspace=None, stream=None,
@@ -278,7 +291,7 @@ def forward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, y=None, lamT=None,
             _check(LIB.kla_plan(B, H, T, dk, dv, _IO[dt], ctypes.byref(opt), ctypes.byref(info)), "kla_plan")
             nbytes = int(info.workspace_bytes)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = _space(workspace, q.get_device())
         if want_var:
             if y_var is None:
                 y_var = torch.empty((B, H, T, dv), dtype=dt, device=dev)
@@ -361,7 +374,7 @@ def backward(q, k, v, lam_v, a, pbar, lam0=None, eta0=None, *, gy=None, glamT=No
             if nbytes == ctypes.c_size_t(-1).value:
                 raise KlaError(ERR_CUDA, "kla_backward_workspace_size")
             workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_bytes = _space(workspace, q.get_device())
         st = LIB.kla_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(lam_v), _ptr(a), _ptr(pbar), _ptr(lam0), _ptr(eta0),
                               _ptr(gy), _ptr(glamT), _ptr(getaT), _ptr(out["gq"]), _ptr(out["gk"]), _ptr(out["gv"]),
                               _ptr(out["glam_v"]), _ptr(out["ga"]), _ptr(out["gpbar"]), _ptr(out.get("glam0")),
@@ -537,7 +550,7 @@ def conv_backward(x, weight, bias=None, window=None, *, gy=None, gwindow_out=Non
             if nbytes == ctypes.c_size_t(-1).value:
                 raise KlaError(ERR_CUDA, "kla_conv_backward_workspace_size")
             workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = _space(workspace, x.get_device())
         st = LIB.kla_conv_backward(_ptr(x), _ptr(weight), _ptr(bias), _ptr(window), _ptr(gy), _ptr(gwindow_out),
                                    _ptr(out["gx"]), _ptr(out.get("gweight")), _ptr(out.get("gbias")),
                                    _ptr(out.get("gwindow")), B, H, T, D, W, _IO[dt], int(activation),
@@ -618,7 +631,7 @@ def delta_forward(q, k, v, g, beta, state0=None, *, scale: float | None = None, 
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_INVALID_ARG, "kla_delta_forward_workspace_size")
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _space(workspace, q.get_device())
     st = _run(index, stream, LIB.kla_delta_forward,
               (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), o.data_ptr(),
                _addr(stateT), B, Hk, H, T, dk, dv, io, dk ** -0.5 if scale is None else scale, _addr(workspace),
@@ -669,7 +682,7 @@ def delta_backward(q, k, v, g, beta, state0=None, *, go=None, gstateT=None, scal
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_INVALID_ARG, "kla_delta_backward_workspace_size")
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _space(workspace, q.get_device())
     st = _run(index, stream, LIB.kla_delta_backward,
               (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(state0), _addr(go),
                _addr(gstateT), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gg.data_ptr(), gbeta.data_ptr(),
@@ -827,7 +840,7 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_CUDA, "kla_norm_rope_backward_workspace_size")
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _space(workspace, q.get_device())
     st = _run(index, stream, LIB.kla_norm_rope_backward,
               (q.data_ptr(), _addr(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), _addr(gyq),
                _addr(gyk), out["gq"].data_ptr(), _addr(out.get("gk")), _addr(out.get("gq_weight")),
