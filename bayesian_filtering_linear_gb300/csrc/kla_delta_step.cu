@@ -7,7 +7,9 @@
 // whole sectors). A lane loads its rows once and keeps them in registers from
 // the dot product with k to the store, so the state crosses HBM once each
 // way, 8 bytes per element, which bounds the step; the sums over rows are
-// three lane exchanges, and no warp waits for another.
+// three lane exchanges, and no warp waits for another. The state decays by a in
+// two floats (decay_of), so that thousands of weak decays do not add up their
+// roundings.
 #include "kla_device.cuh"
 #include "kla_launch.h"
 
@@ -39,7 +41,8 @@ __global__ void __launch_bounds__(256) kla_delta_step_kernel(const DeltaArgs a) 
     k[r] = to_f32<IO>(kv[r0 + 8 * r]);
     q[r] = to_f32<IO>(qv[r0 + 8 * r]);
   }
-  const float decay = expf(to_f32<IO>(reinterpret_cast<const IO*>(a.g)[bh]));
+  float low;
+  const float decay = decay_of(to_f32<IO>(reinterpret_cast<const IO*>(a.g)[bh]), low);
   const float beta = to_f32<IO>(reinterpret_cast<const IO*>(a.beta)[bh]);
 
   float p[4] = {0.f, 0.f, 0.f, 0.f};
@@ -59,10 +62,10 @@ __global__ void __launch_bounds__(256) kla_delta_step_kernel(const DeltaArgs a) 
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    S[r].x = fmaf(k[r], u[0], decay * S[r].x);
-    S[r].y = fmaf(k[r], u[1], decay * S[r].y);
-    S[r].z = fmaf(k[r], u[2], decay * S[r].z);
-    S[r].w = fmaf(k[r], u[3], decay * S[r].w);
+    S[r].x = fmaf(decay, S[r].x, fmaf(k[r], u[0], low * S[r].x));
+    S[r].y = fmaf(decay, S[r].y, fmaf(k[r], u[1], low * S[r].y));
+    S[r].z = fmaf(decay, S[r].z, fmaf(k[r], u[2], low * S[r].z));
+    S[r].w = fmaf(decay, S[r].w, fmaf(k[r], u[3], low * S[r].w));
     o[0] = fmaf(q[r], S[r].x, o[0]);
     o[1] = fmaf(q[r], S[r].y, o[1]);
     o[2] = fmaf(q[r], S[r].z, o[2]);

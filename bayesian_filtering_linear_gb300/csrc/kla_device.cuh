@@ -146,4 +146,14 @@ __device__ __forceinline__ float gate_chain_lamv(float gL, float xL, int gates) 
   return (gates & kGateLamV) ? gL * sigmoid_f(xL) : gL;
 }
 
+// e^g as the sum of two floats, the second one for decays near 1, which would
+// be off by up to 2^-25 in one, always the same way where g is the same.
+__device__ __forceinline__ float decay_of(float g, float& low) {
+  low = 0.f;
+  if (!(g > -0.5f && g < 0.5f)) return expf(g);
+  const float e = expm1f(g), a = 1.f + e;
+  low = e - (a - 1.f);
+  return a;
+}
+
 }  // namespace kla

@@ -67,3 +67,52 @@ def test_bf16_is_fp32_rounded_once(shape):
         assert far <= (2.0 ** -20 * 2.0 ** -7) ** 0.5, (n, far)
     for x, y in ((last, last32), (a["gstate0"], b["gstate0"])):
         assert float((x - y).norm() / y.norm()) <= 2.0 ** -20
+
+
+def by_tokens(q, k, v, g, beta, S, scale):
+    """The definition in 64 bits, token by token, on the GPU."""
+    q, k, v, g, beta, S = (x.double() for x in (q, k, v, g, beta, S))
+    a, o = g.exp(), torch.empty_like(v)
+    for t in range(q.shape[2]):
+        S = S * a[:, :, t, None, None]
+        missed = v[:, :, t] - (k[:, :, t].unsqueeze(-2) @ S).squeeze(-2)
+        S = S + k[:, :, t].unsqueeze(-1) * (beta[:, :, t, None] * missed).unsqueeze(-2)
+        o[:, :, t] = (q[:, :, t].unsqueeze(-2) @ S).squeeze(-2) * scale
+    return o, S
+
+
+def weak(B, H, T, dk, dv, g, beta):
+    """Decays and writes so weak that the first tokens still matter at the end."""
+    r = torch.Generator(device=DEV).manual_seed(7)
+    randn = lambda *s: torch.randn(*s, generator=r, device=DEV)
+    unit = lambda x: torch.nn.functional.normalize(x, dim=-1)
+    return (unit(randn(B, H, T, dk)), unit(randn(B, H, T, dk)), randn(B, H, T, dv),
+            torch.full((B, H, T), g, device=DEV), torch.full((B, H, T), beta, device=DEV), randn(B, H, dk, dv))
+
+
+def rel(x, y):
+    return float((x.double() - y).norm() / y.norm())
+
+
+@pytest.mark.parametrize("B,H,T,dk,g", [(8, 128, 512, 16, -1e-5), (8, 128, 512, 16, -2e-6), (8, 128, 256, 32, -1e-5),
+                                        (8, 128, 256, 32, -0.003), (1, 8, 40, 64, -1e-5), (8, 128, 200, 16, -0.4)])
+def test_weak_decays_one_token_at_a_time(B, H, T, dk, g):
+    """The same weak decay for every token. Each token rounds the state once, by
+    2^-25 at most in the mean square, and T of them add in quadrature: √512 · 2^-25
+    < 2^-20, the bound. The factors' own roundings would add up as they are, to
+    2.4e-5."""
+    args = weak(B, H, T, dk, dk, g, 0.002)
+    assert kla.LIB.kla_delta_forward_workspace_size(B, H, H, T, dk, dk) == 0  # token by token
+    o, S = kla.delta_forward(*args, scale=1.0)
+    wo, wS = by_tokens(*args, 1.0)
+    assert rel(o, wo) <= 2.0 ** -20 and rel(S, wS) <= 2.0 ** -20, (rel(o, wo), rel(S, wS))
+
+
+def test_weak_decays_in_decode_tokens():
+    """512 single tokens, held to the same bound."""
+    args = weak(1, 8, 512, 64, 64, -1e-5, 0.002)
+    wo, wS = by_tokens(*args, 1.0)
+    S, o = args[-1].clone(), []
+    for t in range(512):
+        o.append(kla.delta_step(*(x[:, :, t].contiguous() for x in args[:5]), S, scale=1.0))
+    assert rel(S, wS) <= 2.0 ** -20 and rel(torch.stack(o, 2), wo) <= 2.0 ** -20
