@@ -208,12 +208,15 @@ __global__ void __launch_bounds__(kThreads, PrepareSmem<IO, DK, BWD>::kBlocks) k
     float ph = __shfl_up_sync(~0u, sh, 1), pl = __shfl_up_sync(~0u, sl, 1);
     if (lane == 0) ph = pl = 0.f;
     float* out = w.gates + at.chunk * kGates;
+    float low;
+    const float whole = whole_decay(th, tl, low);
+    if (lane == 31) out[5 * C] = low;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       float h = ph, l = pl;
       add_two(h, l, gh[i], gl[i]);
-      const float g = exp2_of(h + l), e = exp2_of((th - h) + (tl - l));
+      const float g = t == C - 1 ? whole : exp2_of(h + l), e = exp2_of((th - h) + (tl - l));
       logs[t] = make_float2(h, l), G[t] = g, E[t] = e, be[t] = b[i], nbG[t] = -b[i] * g;
       out[t] = h, out[C + t] = l, out[2 * C + t] = g, out[3 * C + t] = e, out[4 * C + t] = b[i];
     }
@@ -417,7 +420,7 @@ template <typename IO, int DK, int NV>
 struct ChainSmem {
   static constexpr int KB = kParts<IO> * DK / 64 * kTileBytes, WB = 3 * DK / 64 * kTileBytes;
   static constexpr int STAGES = sizeof(IO) == 4 && DK == 128 ? 1 : 2;
-  static constexpr int IN = NV * C * 4, GATES = 3 * C * 4;  // a chunk's M (β V), gates
+  static constexpr int IN = NV * C * 4, GATES = (kGates - 2 * C) * 4;  // a chunk's M (β V), gates
   static constexpr int TILES = (3 * NV + 63) / 64;  // of X's and U's parts side by side
   static constexpr int K = 0, W = STAGES * KB, X = W + STAGES * WB, U = X + TILES * DK * 128, B = U + TILES * kTileBytes,
                        AHEAD = B + 2 * (IN + GATES) <= kMaxBytes ? 2 : 1, kBytes = B + AHEAD * (IN + GATES);
@@ -617,7 +620,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
         const float4 x = reinterpret_cast<const float4*>(brought)[(j0 + j) * (NV * 4) + (NV == 64 ? vt : vt & 127)];
         B.v[4 * j] = x.x, B.v[4 * j + 1] = x.y, B.v[4 * j + 2] = x.z, B.v[4 * j + 3] = x.w;
       }
-      const float gend = gates[C - 1];
+      const float gend = gates[C - 1], glow = gates[3 * C];
       float g[2];  // −β G, or E
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
@@ -649,7 +652,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaGradArgs& d
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int e = 0; e < 4 * J; ++e)
-          X[rb].v[e] = fmaf(gend, X[rb].v[e], REV ? more[rb].v[e] + F[REV ? rb : 0].v[e] : more[rb].v[e]);
+          X[rb].v[e] = fmaf(gend, X[rb].v[e], fmaf(glow, X[rb].v[e], REV ? more[rb].v[e] + F[REV ? rb : 0].v[e] : more[rb].v[e]));
     }
     float* const last = REV ? d.gstate0 : a.stateT;
     if (last) {

@@ -12,7 +12,9 @@ using namespace umma;
 
 constexpr int C = 64;             // tokens of a chunk
 constexpr int kThreads = 256;     // of the kernels that take a chunk each
-constexpr int kGates = 5 * C;     // floats: cumulative log2 of the decay in two, decay from the start, to the end, β
+// Floats of a chunk's gates: cumulative log2 of the decay in two, decay from the start, to the end, β; then what the
+// chunk's whole decay is more than the float that has it (and three that fill 16 bytes).
+constexpr int kGates = 5 * C + 4;
 constexpr int kMaxBytes = 227 * 1024 - 4096;  // shared memory of a block, less its static part
 constexpr float kMinLog = -104.f; // e^-104 is 0 in fp32: smaller logs change nothing but the sums' exactness
 
@@ -29,7 +31,7 @@ __host__ __device__ constexpr int pad64(int d) { return d <= 64 ? 64 : 128; }
 // rows of the largest part and 16 of the middle one), then as many of the
 // smallest part's 64 rows.
 struct Workspace {
-  float* gates;  // [chunks][5][64]
+  float* gates;  // [chunks][kGates]
   char* W;       // [chunks] tiles: −M (β G K)
   float* S;      // [chunks][DK][DV]: the state before each chunk
   float* U;      // [chunks][64][DV]: first M (β V), then U
@@ -212,6 +214,23 @@ constexpr float kLog2e = 1.44269504f, kLog2eLow = (float)(1.4426950408889634 - (
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^(h + l), the decay of a whole chunk, as the sum of two floats where it is next to 1: one float is off by up to 2^-25
+// there, and over thousands of chunks with the same decay all of it would add up. e^x = 1 + x + x²/2 + … + x^8/8!.
+__device__ __forceinline__ float whole_decay(float h, float l, float& low) {
+  constexpr float kLn2 = 0.693147182f, kLn2Low = (float)(0.69314718055994531 - (double)kLn2);
+  low = 0.f;
+  if (!(h > -0.5f && h < 0.5f)) return exp2_of(h + l);
+  const float x = h * kLn2, xl = fmaf(h, kLn2, -x) + fmaf(h, kLn2Low, l * kLn2);
+  float p = fmaf(x, 1.f / 40320.f, 1.f / 5040.f);
+  p = fmaf(x, p, 1.f / 720.f);
+  p = fmaf(x, p, 1.f / 120.f);
+  p = fmaf(x, p, 1.f / 24.f);
+  p = fmaf(x, p, 1.f / 6.f);
+  p = x * x * fmaf(x, p, 0.5f);
+  const float s = x + p, y = 1.f + s;
+  low = (s - (y - 1.f)) + ((p - (s - x)) + xl);
   return y;
 }
 // The decays D_ts of a thread's fragment from the cumulative logs (zero above the diagonal).

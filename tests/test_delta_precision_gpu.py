@@ -116,3 +116,25 @@ def test_weak_decays_in_decode_tokens():
     for t in range(512):
         o.append(kla.delta_step(*(x[:, :, t].contiguous() for x in args[:5]), S, scale=1.0))
     assert rel(S, wS) <= 2.0 ** -20 and rel(torch.stack(o, 2), wo) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("T,dk,g,beta", [(4096, 64, -1e-5, 0.01), (16384, 128, -2e-6, 0.001), (16384, 64, -1e-5, 0.002),
+                                         (16384, 64, 0.0, 0.002), (8192, 64, -0.0001234, 0.02)])
+def test_weak_decays_over_many_chunks(T, dk, g, beta):
+    """The same weak decay for every token, over up to 256 chunks, forward and
+    for the gradient of the first state. A chunk rounds the state a few times
+    (the update's product and sum, four 2^-25 in the mean square): √256 · 2 ·
+    2^-25 < 2^-20, the bound."""
+    args = weak(1, 2, T, dk, 64, g, beta)
+    o, S = kla.delta_forward(*args, scale=1.0)
+    wo, wS = by_tokens(*args, 1.0)
+    assert rel(o, wo) <= 2.0 ** -20 and rel(S, wS) <= 2.0 ** -20, (rel(o, wo), rel(S, wS))
+    # the first state's gradient: Z ← a (Z − k β (kᵀZ)) from the end
+    q, k, v, a, b = (x.double() for x in args[:5])
+    Z = torch.randn(S.shape, generator=torch.Generator(device=DEV).manual_seed(8), device=DEV)
+    got = kla.delta_backward(*args, gstateT=Z, scale=1.0)["gstate0"]
+    Z, a = Z.double(), a.exp()
+    for t in reversed(range(T)):
+        u = b[:, :, t, None, None] * (k[:, :, t].unsqueeze(-2) @ Z)
+        Z = a[:, :, t, None, None] * (Z - k[:, :, t].unsqueeze(-1) * u)
+    assert rel(got, Z) <= 2.0 ** -20, rel(got, Z)
