@@ -41,6 +41,9 @@ struct GradSmem {
   static constexpr int W = O, dP = O, dA = dP + ROWS, bA = dA + ROWS, kEnd = bA + ROWS;
   static constexpr int kBytes = kStage > kEnd ? kStage : kEnd;
   static constexpr int kBlocks = DK == 64 && kBytes <= 108 * 1024 ? 2 : 1;  // of an SM
+  // Two slices of 64 columns of V add to the same sums. Where TMEM has room each has accumulators of its own, added in
+  // registers: what a slice's small products add to the other's whole sums is cut off too often (24 times).
+  static constexpr int kSet = kBlocks == 1 && DK == 64 ? 256 : 0;
   static_assert(W + 64 * 65 * 4 <= kBytes && kBytes <= kMaxBytes, "");
 };
 
@@ -69,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
                                                                  const Workspace w, unsigned ahead) {
   using L = GradSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
-  constexpr int COLS = DK == 64 ? 256 : 512, SH = 3 * DK;      // TMEM: dQ, X, Y of DK columns, then 64 shared
+  constexpr int SET = L::kSet, COLS = DK == 64 && !SET ? 256 : 512, SH = 3 * DK;  // TMEM: dQ, X, Y of DK columns, then 64 shared
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ __align__(16) float2 logs[C];
   __shared__ float G[C], E[C], be[C], rv[2][C], before[C], from[2][C], to[2][C], kx[2][C], zs[8];
@@ -177,10 +180,12 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     for (int nb = 0; nb < NB; ++nb) xl[nb].put<PN>(sm + L::S, DK * 128, block_row<DK>(l, nb), l.c);
     publish();
     if (warp == 0 && elect()) {
-      mma<64, 64, 64>(tm + SH, Or, Ur, sl > 0);
-      mma<64, 64, 64>(tm + 2 * DK, Rr, Ur, sl > 0);
-      mma<64, DK, 64>(tm, Or, Sr, sl > 0);
-      mma<64, DK, 64>(tm + DK, Rr, Sr, sl > 0);
+      const uint32_t to = tm + sl * SET;
+      const bool more = !SET && sl > 0;
+      mma<64, 64, 64>(to + SH, Or, Ur, more);
+      mma<64, 64, 64>(to + 2 * DK, Rr, Ur, more);
+      mma<64, DK, 64>(to, Or, Sr, more);
+      mma<64, DK, 64>(to + DK, Rr, Sr, more);
       commit(&bar);
     }
     // while that runs, what comes of dR alone
@@ -194,10 +199,19 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     if (sl + 1 < slices) bring(sl + 1);
     else bring_z(sl);
   }
+  auto load_sum = [&](uint32_t from, float (&x)[16]) {  // of both slices
+    tmem_load(from, x);
+    if (SET && slices > 1) {
+      float y[16];
+      tmem_load(from + SET, y);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] += y[e];
+    }
+  };
   float gp[16], ga[16];
   finish();
-  tmem_load(tm + SH + rows + 32 * half, gp);
-  tmem_load(tm + 2 * DK + rows + 32 * half, ga);
+  load_sum(tm + SH + rows + 32 * half, gp);
+  load_sum(tm + 2 * DK + rows + 32 * half, ga);
   fence_before();
   // Y = U Zᵀ, and <Z, S>, from the last slice on, whose U and S are at hand
   float z = 0.f;
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     }
     publish();
     if (warp == 0 && elect()) {
-      mma<64, DK, 64>(tm + 2 * DK, Ur, Sr, sl + 1 < slices);
+      mma<64, DK, 64>(tm + sl * SET + 2 * DK, Ur, Sr, !SET && sl + 1 < slices);
       commit(&bar);
     }
     if (sl) {
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   for (int nb = 0; nb < NB; ++nb) {
     const int cb = NB * 32 * half + 32 * nb;
 #pragma unroll
-    for (int m = 0; m < 3; ++m) tmem_load(tm + m * DK + rows + cb, acc[m][nb]);
+    for (int m = 0; m < 3; ++m) load_sum(tm + m * DK + rows + cb, acc[m][nb]);
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
       const int t = row_of(e), o = (e & 2) >> 1, c = cb + 2 * (lane & 3) + (e >> 2) * 8;
@@ -310,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     const Operand<PN, true> Pt{base + L::dP, kTileBytes, kTileBytes}, At{base + L::bA, kTileBytes, kTileBytes};
     mma<64, DK, 64>(tm, P, Kt);
     mma<64, DK, 64>(tm + DK, A, Kt);
-    mma<64, DK, 64>(tm + 2 * DK, Pt, Qt);
-    mma<64, DK, 64>(tm + 2 * DK, At, Kt, true);
+    mma_sum<64, DK, 64>(tm + 2 * DK, Pt, Qt, At, Kt);
     commit(&bar);
   }
   finish();

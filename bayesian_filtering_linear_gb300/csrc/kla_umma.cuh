@@ -198,35 +198,49 @@ struct Operand {
 // while it is small (64³ with 3 × 3 parts: 1.2e-6 of the largest value with the
 // large products first).
 template <int M, int N, int K, int PA, bool AMN, int PB, bool BMN>
-__device__ __forceinline__ void mma(uint32_t d, const Operand<PA, AMN>& a, const Operand<PB, BMN>& b,
-                                    bool accumulate = false) {
+__device__ __forceinline__ void mma_weight(uint32_t d, const Operand<PA, AMN>& a, const Operand<PB, BMN>& b, int w,
+                                           uint32_t& acc) {  // the products of parts i + j = w
   constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)AMN << 15) | ((uint32_t)BMN << 16) |
                              ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
   // descriptor: address, distance of 64-column blocks (MN-major), of eight rows, version 1, 128-byte swizzle
   constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-  constexpr int most = PA > PB ? PA : PB;
   const uint32_t la = ((a.addr & 0x3ffff) >> 4) | ((uint32_t)(AMN ? a.block >> 4 : 1) << 16);
   const uint32_t lb = ((b.addr & 0x3ffff) >> 4) | ((uint32_t)(BMN ? b.block >> 4 : 1) << 16);
+#pragma unroll
+  for (int i = 0; i < PA; ++i) {
+    const int j = w - i;
+    if (j < 0 || j >= PB) continue;
+#pragma unroll
+    for (int k = 0; k < K / 16; ++k) {
+      const uint32_t oa = i * a.part + (AMN ? k * 2048 : (k >> 2) * a.block + (k & 3) * 32);
+      const uint32_t ob = j * b.part + (BMN ? k * 2048 : (k >> 2) * b.block + (k & 3) * 32);
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+          "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+          "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(la + (oa >> 4)),
+          "r"(lb + (ob >> 4)), "r"(hi), "r"(idesc), "r"(acc)
+          : "memory");
+      acc = 1u;
+    }
+  }
+}
+template <int M, int N, int K, int PA, bool AMN, int PB, bool BMN>
+__device__ __forceinline__ void mma(uint32_t d, const Operand<PA, AMN>& a, const Operand<PB, BMN>& b,
+                                    bool accumulate = false) {
   uint32_t acc = accumulate ? 1u : 0u;
 #pragma unroll
-  for (int w = most - 1; w >= 0; --w)
+  for (int w = (PA > PB ? PA : PB) - 1; w >= 0; --w) mma_weight<M, N, K>(d, a, b, w, acc);
+}
+// D = A·B + C·E, the small products of both first.
+template <int M, int N, int K, int PA, bool AMN, int PB, bool BMN>
+__device__ __forceinline__ void mma_sum(uint32_t d, const Operand<PA, AMN>& a, const Operand<PB, BMN>& b,
+                                        const Operand<PA, AMN>& c, const Operand<PB, BMN>& e) {
+  uint32_t acc = 0;
 #pragma unroll
-    for (int i = 0; i < PA; ++i) {
-      const int j = w - i;
-      if (j < 0 || j >= PB) continue;
-#pragma unroll
-      for (int k = 0; k < K / 16; ++k) {
-        const uint32_t oa = i * a.part + (AMN ? k * 2048 : (k >> 2) * a.block + (k & 3) * 32);
-        const uint32_t ob = j * b.part + (BMN ? k * 2048 : (k >> 2) * b.block + (k & 3) * 32);
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-            "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(la + (oa >> 4)),
-            "r"(lb + (ob >> 4)), "r"(hi), "r"(idesc), "r"(acc)
-            : "memory");
-        acc = 1u;
-      }
-    }
+  for (int w = (PA > PB ? PA : PB) - 1; w >= 0; --w) {
+    mma_weight<M, N, K>(d, a, b, w, acc);
+    mma_weight<M, N, K>(d, c, e, w, acc);
+  }
 }
 // `bar` gets one arrival when every product issued so far is done.
 __device__ __forceinline__ void commit(uint64_t* bar) {

@@ -92,3 +92,22 @@ def test_gradients_in_the_2_norm(shape, io):
     want = O.backward(*(n[x] for x in names), f64(go), f64(gs))
     far = {x: rel(got[x], want[x]) for x in got if io == "f32" or x == "gstate0"}
     assert max(far.values()) <= 2.0 ** -19, far
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 8, 700, 64, 128), (2, 8, 8, 500, 16, 128), (2, 4, 8, 300, 64, 64),
+                                   (2, 4, 4, 300, 128, 64)])
+def test_gradients_of_wide_values_in_the_2_norm(shape):
+    """fp32 gradients that add products over two slices of V's columns, and gk,
+    which adds two products. Sums are cut to 24 bits with every instruction, by
+    2^-24 at most and always downwards: as long as small products never meet
+    large sums that is a few times, less than 2^-21 (24 times and more otherwise:
+    9e-7 and 1.2e-6). The decay's gradient sums these again: twice that."""
+    p = problem(*shape, "f32", seed=6, decay=0.1)
+    d, n = to_dev(p), {x: f64(y) for x, y in p.items()}
+    names = ("q", "k", "v", "g", "beta", "state0")
+    r = torch.Generator().manual_seed(1)
+    go, gs = torch.randn(p["v"].shape, generator=r), torch.randn(p["state0"].shape, generator=r)
+    got = kla.delta_backward(*(d[x] for x in names), go=go.to(DEV), gstateT=gs.to(DEV), scale=1.0)
+    want = O.backward(*(n[x] for x in names), f64(go), f64(gs))
+    far = {x: rel(got[x], want[x]) for x in got}
+    assert all(far[x] <= (2.0 ** -20 if x in ("gg", "gbeta") else 2.0 ** -21) for x in far), far
