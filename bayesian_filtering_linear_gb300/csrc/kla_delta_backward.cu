@@ -18,8 +18,8 @@
 // the chain runs forward for S and U, and beside it from the end for Z and dR;
 // then a block per chunk and head makes everything else here. Gradients of q and
 // k that several value heads share are summed from per-head fp32 parts in a
-// fixed order. At 8 × 16 heads of 64 × 64 and 4096 tokens in bf16: prepare 357 us,
-// the chains 232 (1.4 GB, 6 TB/s), gradients 405: two blocks an SM, bound by
+// fixed order. At 8 × 16 heads of 64 × 64 and 4096 tokens in bf16: prepare 350 us,
+// the chains 234 (1.45 GB, 6.2 TB/s), gradients 401: two blocks an SM, bound by
 // their steps' latencies, so that a block's loads start together at its start, and
 // the inputs of the block that follows on the SM are sent into L2 (425 -> 358 with
 // operands of two parts). Sixteen warps instead of eight leave 64 registers a

@@ -14,8 +14,8 @@
 // SMs, DRAM bounds it. `output` (a block per chunk, head and 64 columns) makes
 // O. The backward pass runs the same chain from the end with Mᵀ, beside the
 // other (see kla_delta_backward.cu). At 8 × 16 heads of 64 × 64 and 4096 tokens in
-// bf16: prepare 180 us (shared memory, and the latency of a dozen steps with four
-// blocks an SM), chain 109 (655 MB, 6.0 TB/s), output 106 (460 MB, 4.3 TB/s).
+// bf16: prepare 179 us (shared memory's data pipe, 82% busy with four blocks an
+// SM), chain 110 (640 MB, 5.8 TB/s), output 107 (460 MB, 4.3 TB/s).
 //
 // Operands are bf16 parts (kla_umma.cuh): bf16 inputs are exact in one, states
 // and everything else that is made of them are kept in three, so that states and
@@ -861,16 +861,18 @@ cudaError_t launch_chain(const DeltaArgs& a, const DeltaGradArgs* d, const Works
 }  // namespace delta
 
 // Chunks, or token by token (kla_delta.cu)? The estimated times of both, in
-// microseconds, fitted to bf16 calls on a GB300. Token by token: 0.19 us a token
-// (d_k 64; 0.16 and 0.23 for 16 and 128), or 3.3e6 elements a microsecond where
-// heads are many (heads of few rows count as 40 rows). Chunks: 20 us of launches
-// and first waits and, by latency, 1.7 us a chunk (23 and 2.1 for d_k 128), or by
-// work, 0.052 us a chunk and head (0.116). Measured, one by one / chunks: 8 heads
-// of 64 × 64, 64 tokens 17 / 23 us, 128 tokens 29 / 24; 128 heads of 64 × 64, 64
-// tokens 20 / 24, 128 tokens 35 / 30; 1024 heads of 64 × 64, 32 tokens 49 / 77, 64
-// tokens 88 / 79; 1024 heads of 16 × 16, 512 tokens 130 / 397; 128 heads of
-// 128 × 128, 64 tokens 55 / 32. Past 512 tokens always chunks: one by one, a
-// rounding per token adds up (1e-6 of the state after a thousand).
+// microseconds, fitted to bf16 calls, launches included, on a GB300. Token by
+// token: 0.19 us a token (d_k 64; 0.16 and 0.23 for 16 and 128), or 3.3e6 elements
+// a microsecond where heads are many (heads of few rows count as 40 rows). Chunks:
+// 20 us of launches and first waits and, by latency, 1.7 us a chunk (23 and 2.1 for
+// d_k 128), or by work, 0.052 us a chunk and head (0.116). Measured in a captured
+// graph, one by one / chunks, in bf16 and in fp32, whose chunks take longer: 8
+// heads of 64 × 64, 64 tokens 14 / 15 and 13 / 18 us, 128 tokens 26 / 17 and
+// 24 / 19; 128 such heads, 64 tokens 18 / 17 and 17 / 19, 128 tokens 33 / 23 and
+// 31 / 27; 1024, 32 tokens 49 / 74 and 49 / 90, 64 tokens 91 / 77 and 92 / 100 (where
+// chunks are taken); 1024 heads of 16 × 16, 512 tokens 136 / 387 and 137 / 480; 128
+// heads of 128 × 128, 64 tokens 54 / 28 and 54 / 40. Past 512 tokens always chunks:
+// one by one, a rounding per token adds up (1e-6 of the state after a thousand).
 bool delta_chunked(int B, int H, int T, int dk, int dv) {
   if (T > 512) return true;
   const double heads = (double)B * H, chunks = (T + delta::C - 1) / delta::C;

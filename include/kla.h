@@ -389,6 +389,10 @@ kla_status kla_conv_backward(const void* x, const float* weight, const float* bi
  *   workspace / ws_bytes: device scratch of at least
  *     kla_delta_forward_workspace_size() bytes (else WORKSPACE; may be NULL
  *     when that is 0): longer sequences run in chunks of 64 tokens.
+ *   States and everything that is not an input are held in fp32 (on the tensor
+ *   cores as three bf16 parts, 24 bits); a bf16 output is rounded once.
+ *   The workspace grows with T; a long sequence can be given in pieces, the
+ *   state of one being state0 of the next.
  *   A value that is not finite reaches every output of its 64-token chunk that
  *   it is coupled to (for v: its column), and what follows. */
 size_t kla_delta_forward_workspace_size(int B, int Hk, int H, int T, int dk, int dv);
