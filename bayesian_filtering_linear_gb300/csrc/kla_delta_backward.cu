@@ -19,11 +19,11 @@
 // then a block per chunk and head makes everything else here. Gradients of q and
 // k that several value heads share are summed from per-head fp32 parts in a
 // fixed order. At 8 × 16 heads of 64 × 64 and 4096 tokens in bf16: prepare 350 us,
-// the chains 234 (1.45 GB, 6.2 TB/s), gradients 401: two blocks an SM, bound by
+// the chains 234 (1.45 GB, 6.2 TB/s), gradients 378: two blocks an SM, bound by
 // their steps' latencies, so that a block's loads start together at its start, and
 // the inputs of the block that follows on the SM are sent into L2 (425 -> 358 with
-// operands of two parts). Sixteen warps instead of eight leave 64 registers a
-// thread: 473 us.
+// operands of two parts, 402 with three, 378 with the number of slices a constant).
+// Sixteen warps instead of eight leave 64 registers a thread: 473 us.
 #include "kla_delta_chunk.cuh"
 
 namespace kla {
@@ -44,6 +44,9 @@ struct GradSmem {
   // Two slices of 64 columns of V add to the same sums. Where TMEM has room each has accumulators of its own, added in
   // registers: what a slice's small products add to the other's whole sums is cut off too often (24 times).
   static constexpr int kSet = kBlocks == 1 && DK == 64 ? 256 : 0;
+  // fp32 with d_k 128 has no room: the first slice's sums wait in registers (440 -> 533 us at 2 × 16 heads of 128 × 128
+  // and 4096 tokens, for errors of 2e-7 to 3e-7 instead of 7e-7). bf16 outputs are rounded by far more.
+  static constexpr bool kKeep = sizeof(IO) == 4 && DK == 128;
   static_assert(W + 64 * 65 * 4 <= kBytes && kBytes <= kMaxBytes, "");
 };
 
@@ -67,11 +70,13 @@ __device__ __forceinline__ float2 tile_two(const char* tile, int part, int r, in
   return x;
 }
 
-template <typename IO, int DK>
+// SLICES: of 64 columns of V (padded).
+template <typename IO, int DK, int SLICES>
 __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs d,
                                                                  const Workspace w, unsigned ahead) {
   using L = GradSmem<IO, DK>;
   constexpr int PARTS = kParts<IO>, PN = L::PN, NB = DK / 64;  // NB: 32-column blocks of a thread in DK columns
+  constexpr bool KEEP = L::kKeep && SLICES == 2;
   constexpr int SET = L::kSet, COLS = DK == 64 && !SET ? 256 : 512, SH = 3 * DK;  // TMEM: dQ, X, Y of DK columns, then 64 shared
   extern __shared__ __align__(1024) char sm[];  // the swizzle counts rows from 1024-byte boundaries
   __shared__ __align__(16) float2 logs[C];
@@ -79,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-  const int DV = pad64(a.dv), slices = DV / 64;
+  constexpr int DV = 64 * SLICES, slices = SLICES;
   const Where at = where(a, blockIdx.x);
   const size_t krow = (size_t)at.key * a.T + at.t0, vrow = (size_t)at.bh * a.T + at.t0;
   const IO* k = reinterpret_cast<const IO*>(a.k) + krow * a.dk;
@@ -171,8 +176,18 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   tmem_load(tm + rows + 32 * half, kk);
   tmem_load(tm + 64 + rows + 32 * half, qk);
   // products with U, S: dP, dA before masks, dQ = O' Sᵀ, X = dR Sᵀ (dP and dA wait in the shared columns and in Y's)
+  float kept[KEEP ? 2 + 2 * NB : 1][16] = {};
   for (int sl = 0; sl < slices; ++sl) {
     if (sl) finish();
+    if (KEEP && sl) {
+      tmem_load(tm + SH + rows + 32 * half, kept[0]);
+      tmem_load(tm + 2 * DK + rows + 32 * half, kept[KEEP ? 1 : 0]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          tmem_load(tm + m * DK + rows + NB * 32 * half + 32 * nb, kept[KEEP ? 2 + 2 * nb + m : 0]);
+    }
     ol.put(sm + L::O, tid);
     ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
     rl.put<PN>(sm + L::R, kTileBytes, l.r, l.c);
@@ -181,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     publish();
     if (warp == 0 && elect()) {
       const uint32_t to = tm + sl * SET;
-      const bool more = !SET && sl > 0;
+      const bool more = !SET && !KEEP && sl > 0;
       mma<64, 64, 64>(to + SH, Or, Ur, more);
       mma<64, 64, 64>(to + 2 * DK, Rr, Ur, more);
       mma<64, DK, 64>(to, Or, Sr, more);
@@ -212,12 +227,18 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   finish();
   load_sum(tm + SH + rows + 32 * half, gp);
   load_sum(tm + 2 * DK + rows + 32 * half, ga);
+  if (KEEP)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) gp[e] += kept[0][e], ga[e] += kept[KEEP ? 1 : 0][e];
   fence_before();
   // Y = U Zᵀ, and <Z, S>, from the last slice on, whose U and S are at hand
-  float z = 0.f;
+  float z = 0.f, kept_y[KEEP ? NB : 1][16] = {};
   for (int sl = slices - 1; sl >= 0; --sl) {
     if (sl + 1 < slices) {
       finish();
+      if (KEEP)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) tmem_load(tm + 2 * DK + rows + NB * 32 * half + 32 * nb, kept_y[KEEP ? nb : 0]);
       ul.put<PN>(sm + L::U, kTileBytes, l.r, l.c);
     }
 #pragma unroll
@@ -228,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
     }
     publish();
     if (warp == 0 && elect()) {
-      mma<64, DK, 64>(tm + sl * SET + 2 * DK, Ur, Sr, !SET && sl + 1 < slices);
+      mma<64, DK, 64>(tm + sl * SET + 2 * DK, Ur, Sr, !SET && !KEEP && sl + 1 < slices);
       commit(&bar);
     }
     if (sl) {
@@ -258,7 +279,12 @@ __global__ void __launch_bounds__(kThreads, GradSmem<IO, DK>::kBlocks) kla_delta
   for (int nb = 0; nb < NB; ++nb) {
     const int cb = NB * 32 * half + 32 * nb;
 #pragma unroll
-    for (int m = 0; m < 3; ++m) load_sum(tm + m * DK + rows + cb, acc[m][nb]);
+    for (int m = 0; m < 3; ++m) {
+      load_sum(tm + m * DK + rows + cb, acc[m][nb]);
+      if (KEEP)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[m][nb][e] += m < 2 ? kept[KEEP ? 2 + 2 * nb + m : 0][e] : kept_y[KEEP ? nb : 0][e];
+    }
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
       const int t = row_of(e), o = (e & 2) >> 1, c = cb + 2 * (lane & 3) + (e >> 2) * 8;
@@ -427,7 +453,9 @@ template <typename IO, int DK>
 cudaError_t grad_dk(const DeltaArgs& a, const DeltaGradArgs& g, const Workspace& w, int num_sms, cudaStream_t s) {
   const unsigned blocks = (unsigned)((long long)a.B * a.H * ((a.T + C - 1) / C));
   using L = GradSmem<IO, DK>;
-  return run(kla_delta_grad_kernel<IO, DK>, L::kBytes, blocks, kThreads, s, a, g, w, (unsigned)(num_sms * L::kBlocks));
+  const unsigned ahead = num_sms * L::kBlocks;
+  if (pad64(a.dv) == 64) return run(kla_delta_grad_kernel<IO, DK, 1>, L::kBytes, blocks, kThreads, s, a, g, w, ahead);
+  return run(kla_delta_grad_kernel<IO, DK, 2>, L::kBytes, blocks, kThreads, s, a, g, w, ahead);
 }
 
 }  // namespace

@@ -95,7 +95,7 @@ def test_gradients_in_the_2_norm(shape, io):
 
 
 @pytest.mark.parametrize("shape", [(2, 4, 8, 700, 64, 128), (2, 8, 8, 500, 16, 128), (2, 4, 8, 300, 64, 64),
-                                   (2, 4, 4, 300, 128, 64)])
+                                   (2, 4, 4, 300, 128, 64), (2, 4, 4, 300, 128, 128)])
 def test_gradients_of_wide_values_in_the_2_norm(shape):
     """fp32 gradients that add products over two slices of V's columns, and gk,
     which adds two products. Sums are cut to 24 bits with every instruction, by
