@@ -337,6 +337,67 @@ kla::NormRopeArgs norm_rope_args(const float* inv_freq, const long long* positio
   return a;
 }
 
+// Shapes and options of the gated linear recurrence.
+kla_status check_recurrence(int B, int H, int T, int D, kla_dtype io, const kla_recurrence_options* opt) {
+  if (B < 0 || H < 0 || T < 0 || !opt) return KLA_ERR_INVALID_ARG;
+  if (D < 8 || D % 8 != 0) return KLA_ERR_UNSUPPORTED_SHAPE;
+  if (io != KLA_F32 && io != KLA_BF16) return KLA_ERR_INVALID_ARG;
+  if (opt->decay < KLA_DECAY_LOG || opt->decay > KLA_DECAY_RATE || opt->scale < KLA_SCALE_NONE ||
+      opt->scale > KLA_SCALE_COMPLEMENT)
+    return KLA_ERR_INVALID_ARG;
+  const long long bh = (long long)B * H;
+  if (bh > INT_MAX || bh * D > INT_MAX - 1024) return KLA_ERR_UNSUPPORTED_SHAPE;
+  if (bh > 0 && (long long)T > (1LL << 46) / (bh * D)) return KLA_ERR_UNSUPPORTED_SHAPE;
+  return KLA_OK;
+}
+
+// The strides of one [B,H,T,D] tensor (null: contiguous), and the elements that they reach. Rows of an output
+// (`apart`) must lie apart.
+kla_status check_strides(int B, int H, int T, int D, int io, const long long* strides, bool apart, long long st[3],
+                         size_t* span) {
+  const long long dense[3] = {(long long)H * T * D, (long long)T * D, D}, most[3] = {B, H, T};
+  const long long unit = 16 / (long long)io_size(io);
+  size_t last = D;
+  *span = 0;
+  for (int j = 0; j < 3; ++j) st[j] = strides ? strides[j] : dense[j];
+  if (most[0] == 0 || most[1] == 0 || most[2] == 0) return KLA_OK;
+  for (int j = 0; j < 3; ++j) {
+    if (most[j] <= 1) {
+      st[j] = 0;  // never taken
+      continue;
+    }
+    if (st[j] < (apart ? D : 0) || st[j] > (1LL << 46) / (most[j] - 1)) return KLA_ERR_INVALID_ARG;
+    if (st[j] % unit != 0) return KLA_ERR_MISALIGNED;
+    last += (size_t)(most[j] - 1) * (size_t)st[j];
+  }
+  *span = last;
+  return KLA_OK;
+}
+
+size_t recurrence_checkpoint_bytes(int B, int H, int T, int D) {
+  return (size_t)((T + (long long)kla::kRecTile - 1) / kla::kRecTile) * (size_t)B * H * D * sizeof(float);
+}
+size_t recurrence_backward_bytes(int B, int H, int T, int D, bool with_checkpoints) {
+  const size_t along = (T + (long long)kla::kRecTile - 1) / kla::kRecTile;
+  const size_t sums = std::min(along, (size_t)kla::kRecMaxCluster) * (size_t)B * H * D * sizeof(float);
+  return sums + (with_checkpoints ? 0 : recurrence_checkpoint_bytes(B, H, T, D));
+}
+
+// Rows of a layer norm's input: the elements that they reach.
+kla_status check_rows(long long rows, int D, long long stride, size_t* span) {
+  *span = 0;
+  if (rows == 0) return KLA_OK;
+  if (rows > 1 && (stride < 0 || stride > (1LL << 46) / (rows - 1))) return KLA_ERR_INVALID_ARG;
+  *span = (size_t)D + (rows > 1 ? (size_t)(rows - 1) * (size_t)stride : 0);
+  return KLA_OK;
+}
+kla_status check_layer_norm(long long rows, int D, kla_dtype io, float eps) {
+  if (rows < 0 || !(eps >= 0.f) || (io != KLA_F32 && io != KLA_BF16)) return KLA_ERR_INVALID_ARG;
+  if (D < 1 || D > kla::kLayerNormMaxD || rows > INT_MAX) return KLA_ERR_UNSUPPORTED_SHAPE;
+  return KLA_OK;
+}
+bool element_aligned(int io, const void* p) { return (reinterpret_cast<uintptr_t>(p) & (io_size(io) - 1)) == 0; }
+
 void fill_info(const Plan& p, kla_plan_info* out) {
   out->strategy = p.strategy;
   out->chunk_len = p.chunk_len;
@@ -952,6 +1013,252 @@ kla_status kla_norm_rope_backward(const void* q, const void* k, const float* q_w
   a.part = sums ? reinterpret_cast<float*>(workspace) : nullptr;
   a.gwq = gq_weight; a.gwk = gk_weight;
   return kla::launch_norm_rope_backward(a, sms, s) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+size_t kla_recurrence_checkpoints_size(int B, int H, int T, int D) {
+  const kla_recurrence_options opt{KLA_DECAY_LOG, KLA_SCALE_NONE};
+  if (check_recurrence(B, H, T, D, KLA_F32, &opt) != KLA_OK) return (size_t)-1;
+  return recurrence_checkpoint_bytes(B, H, T, D);
+}
+
+kla_status kla_recurrence_forward(const void* x, const void* g, const void* i, const float* rate, const float* h0,
+                                  void* y, float* hT, void* checkpoints, int B, int H, int T, int D,
+                                  const long long* x_strides, const long long* g_strides,
+                                  const long long* i_strides, const long long* y_strides, kla_dtype io,
+                                  const kla_recurrence_options* opt, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  kla_status st = check_recurrence(B, H, T, D, io, opt);
+  if (st != KLA_OK) return st;
+  const long long* strides[4] = {x_strides, g_strides, i_strides, y_strides};
+  long long s[4][3];
+  size_t span[4];
+  for (int n = 0; n < 4; ++n)
+    if ((n != 2 || i) && (st = check_strides(B, H, T, D, io, strides[n], n == 3, s[n], &span[n])) != KLA_OK) return st;
+  const long long bh = (long long)B * H;
+  const bool by_rate = opt->decay == KLA_DECAY_RATE;
+  if (bh * T > 0 && (!x || !g || !y || (by_rate && !rate))) return KLA_ERR_INVALID_ARG;
+  if (!by_rate) rate = nullptr;
+  const void* ptrs[] = {x, g, i, rate, h0, y, hT, checkpoints};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), states = (size_t)bh * D * sizeof(float);
+  const Range ins[] = {{x, span[0] * z}, {g, span[1] * z}, {i, i ? span[2] * z : 0},
+                       {rate, (size_t)H * D * sizeof(float)}, {h0, states}};
+  const Range outs[] = {{y, span[3] * z}, {hT, states}, {checkpoints, recurrence_checkpoint_bytes(B, H, T, D)}};
+  if (ranges_clash(outs, 3, ins, 5, 1, 4)) return KLA_ERR_INVALID_ARG;
+  if (bh == 0) return KLA_OK;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (!hT || hT == h0) return KLA_OK;
+    const cudaError_t e = h0 ? cudaMemcpyAsync(hT, h0, states, cudaMemcpyDeviceToDevice, cs)
+                             : cudaMemsetAsync(hT, 0, states, cs);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  }
+  int sms = 0;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
+  kla::RecArgs a{};
+  a.x = {x, s[0][0], s[0][1], s[0][2]};
+  a.g = {g, s[1][0], s[1][1], s[1][2]};
+  if (i) a.i = {i, s[2][0], s[2][1], s[2][2]};
+  a.y = {y, s[3][0], s[3][1], s[3][2]};
+  a.rate = rate; a.h0 = h0; a.hT = hT; a.ckpt = reinterpret_cast<float*>(checkpoints);
+  a.B = B; a.H = H; a.T = T; a.D = D; a.C = (int)(bh * D); a.decay = opt->decay; a.scale = opt->scale; a.io = (int)io;
+  return kla::launch_recurrence(a, sms, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+kla_status kla_recurrence_step(const void* x, const void* g, const void* i, const float* rate, float* state, void* y,
+                               int B, int H, int D, kla_dtype io, const kla_recurrence_options* opt, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  const kla_status st = check_recurrence(B, H, 1, D, io, opt);
+  if (st != KLA_OK) return st;
+  const long long bh = (long long)B * H;
+  const bool by_rate = opt->decay == KLA_DECAY_RATE;
+  if (bh > 0 && (!x || !g || !state || !y || (by_rate && !rate))) return KLA_ERR_INVALID_ARG;
+  if (!by_rate) rate = nullptr;
+  const void* ptrs[] = {x, g, i, rate, state, y};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  const size_t n = (size_t)bh * D, z = io_size(io);
+  const Range ins[] = {{x, n * z}, {g, n * z}, {i, n * z}, {rate, (size_t)H * D * sizeof(float)}};
+  const Range outs[] = {{y, n * z}, {state, n * sizeof(float)}};
+  if (ranges_clash(outs, 2, ins, 4)) return KLA_ERR_INVALID_ARG;
+  if (bh == 0) return KLA_OK;
+  kla::RecArgs a{};
+  const long long sb = (long long)H * D, sh = D;
+  a.x = {x, sb, sh, 0};
+  a.g = {g, sb, sh, 0};
+  if (i) a.i = {i, sb, sh, 0};
+  a.y = {y, sb, sh, 0};
+  a.rate = rate; a.h0 = state; a.hT = state;
+  a.B = B; a.H = H; a.T = 1; a.D = D; a.C = (int)(bh * D); a.decay = opt->decay; a.scale = opt->scale; a.io = (int)io;
+  return kla::launch_recurrence_step(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+size_t kla_recurrence_backward_workspace_size(int B, int H, int T, int D, int with_checkpoints) {
+  const kla_recurrence_options opt{KLA_DECAY_LOG, KLA_SCALE_NONE};
+  if (check_recurrence(B, H, T, D, KLA_F32, &opt) != KLA_OK) return (size_t)-1;
+  return recurrence_backward_bytes(B, H, T, D, with_checkpoints != 0);
+}
+
+kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, const float* rate, const float* h0,
+                                   const void* checkpoints, const void* gy, const float* ghT, void* gx, void* gg,
+                                   void* gi, float* grate, float* gh0, int B, int H, int T, int D,
+                                   const long long* x_strides, const long long* g_strides,
+                                   const long long* i_strides, const long long* gy_strides,
+                                   const long long* gx_strides, const long long* gg_strides,
+                                   const long long* gi_strides, kla_dtype io, const kla_recurrence_options* opt,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  kla_status st = check_recurrence(B, H, T, D, io, opt);
+  if (st != KLA_OK) return st;
+  if (!i) gi = nullptr;
+  const long long* strides[7] = {x_strides, g_strides, i_strides, gy_strides, gx_strides, gg_strides, gi_strides};
+  const void* tensors[7] = {x, g, i, gy, gx, gg, gi};
+  long long s[7][3] = {};
+  size_t span[7] = {};
+  for (int n = 0; n < 7; ++n)
+    if (tensors[n] && (st = check_strides(B, H, T, D, io, strides[n], n >= 4, s[n], &span[n])) != KLA_OK) return st;
+  const long long bh = (long long)B * H;
+  const bool by_rate = opt->decay == KLA_DECAY_RATE;
+  if (bh * T > 0 && (!x || !g || !gx || !gg || (i && !gi) || (by_rate && !rate))) return KLA_ERR_INVALID_ARG;
+  if (!by_rate) rate = nullptr, grate = nullptr;
+  const void* ptrs[] = {x, g, i, rate, h0, checkpoints, gy, ghT, gx, gg, gi, grate, gh0, workspace};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  const size_t need = recurrence_backward_bytes(B, H, T, D, checkpoints != nullptr);
+  const size_t z = io_size(io), states = (size_t)bh * D * sizeof(float), rates = (size_t)H * D * sizeof(float);
+  const Range ins[] = {{x, span[0] * z}, {g, span[1] * z}, {i, span[2] * z}, {rate, rates}, {h0, states},
+                       {checkpoints, recurrence_checkpoint_bytes(B, H, T, D)}, {gy, span[3] * z}, {ghT, states}};
+  const Range outs[] = {{gx, span[4] * z}, {gg, span[5] * z}, {gi, span[6] * z}, {grate, rates}, {gh0, states},
+                        {workspace, need}};
+  for (int o = 0; o < 6; ++o) {
+    if (ranges_clash(outs + o, 1, ins, 8)) return KLA_ERR_INVALID_ARG;
+    // gx, gg and gi may lie between each other's rows, as parts of one projection's gradient
+    for (int p = std::max(o + 1, 3); p < 6; ++p)
+      if (ranges_overlap(outs[o].p, outs[o].n, outs[p].p, outs[p].n)) return KLA_ERR_INVALID_ARG;
+  }
+  if (bh * T > 0 && (gx == gg || gx == gi || gg == gi)) return KLA_ERR_INVALID_ARG;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (bh == 0 || T == 0) {  // the state's gradient passes through, the rates' is zero
+    if (grate && rates && cudaMemsetAsync(grate, 0, rates, cs) != cudaSuccess) return KLA_ERR_CUDA;
+    if (!gh0 || bh == 0) return KLA_OK;
+    const cudaError_t e = ghT ? cudaMemcpyAsync(gh0, ghT, states, cudaMemcpyDeviceToDevice, cs)
+                              : cudaMemsetAsync(gh0, 0, states, cs);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  }
+  if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
+  kla::RecGradArgs a{};
+  a.f.x = {x, s[0][0], s[0][1], s[0][2]};
+  a.f.g = {g, s[1][0], s[1][1], s[1][2]};
+  if (i) a.f.i = {i, s[2][0], s[2][1], s[2][2]};
+  a.f.rate = rate; a.f.h0 = h0;
+  a.f.B = B; a.f.H = H; a.f.T = T; a.f.D = D; a.f.C = (int)(bh * D);
+  a.f.decay = opt->decay; a.f.scale = opt->scale; a.f.io = (int)io;
+  const size_t sums = recurrence_backward_bytes(B, H, T, D, true);
+  if (checkpoints) {
+    a.f.ckpt = reinterpret_cast<float*>(const_cast<void*>(checkpoints));
+  } else {
+    a.f.ckpt = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(workspace) + sums);
+    if (kla::launch_recurrence(a.f, sms, cs) != cudaSuccess) return KLA_ERR_CUDA;
+  }
+  if (gy) a.gy = {gy, s[3][0], s[3][1], s[3][2]};
+  a.gx = {gx, s[4][0], s[4][1], s[4][2]};
+  a.gg = {gg, s[5][0], s[5][1], s[5][2]};
+  if (gi) a.gi = {gi, s[6][0], s[6][1], s[6][2]};
+  a.ghT = ghT; a.gh0 = gh0; a.grate = grate;
+  a.part = grate ? reinterpret_cast<float*>(workspace) : nullptr;
+  return kla::launch_recurrence_backward(a, sms, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+kla_status kla_layer_norm(const void* x, const float* weight, const float* bias, const void* residual, void* y,
+                          void* total, long long rows, int D, long long x_stride, long long residual_stride,
+                          kla_dtype io, float eps, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  kla_status st = check_layer_norm(rows, D, io, eps);
+  if (st != KLA_OK) return st;
+  size_t span[2] = {0, 0};
+  if ((st = check_rows(rows, D, x_stride, &span[0])) != KLA_OK) return st;
+  if (residual && (st = check_rows(rows, D, residual_stride, &span[1])) != KLA_OK) return st;
+  if (rows > 0 && (!x || !y || (residual && !total))) return KLA_ERR_INVALID_ARG;
+  if (!residual) total = nullptr;
+  if (!aligned16(weight) || !aligned16(bias)) return KLA_ERR_MISALIGNED;
+  const void* ptrs[] = {x, residual, y, total};
+  for (const void* ptr : ptrs)
+    if (!element_aligned(io, ptr)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), n = (size_t)rows * D * z, wb = (size_t)D * sizeof(float);
+  const Range ins[] = {{x, span[0] * z}, {residual, span[1] * z}, {weight, wb}, {bias, wb}};
+  const Range outs[] = {{y, n}, {total, n}};
+  if (ranges_overlap(y, n, total, n)) return KLA_ERR_INVALID_ARG;
+  for (const Range& o : outs)
+    for (const Range& in : ins) {
+      const bool in_place = o.p == in.p && in.n == o.n && (in.p == x ? x_stride : residual_stride) == D;
+      if ((in.p == weight || in.p == bias || !(in_place || (rows == 1 && o.p == in.p))) &&
+          ranges_overlap(o.p, o.n, in.p, in.n))
+        return KLA_ERR_INVALID_ARG;
+    }
+  if (rows == 0) return KLA_OK;
+  const kla::LayerNormArgs a{x, residual, x_stride, residual_stride, weight, bias, y, total, rows, D, (int)io, eps,
+                             1.f / (float)D};
+  return kla::launch_layer_norm(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+size_t kla_layer_norm_backward_workspace_size(long long rows, int D) {
+  if (check_layer_norm(rows, D, KLA_F32, 0.f) != KLA_OK) return (size_t)-1;
+  int sms = 0;
+  if (device_sms(&sms) != KLA_OK) return (size_t)-1;
+  return kla::layer_norm_partial_bytes(rows, D, sms);
+}
+
+kla_status kla_layer_norm_backward(const void* x, const float* weight, const void* gy, const void* gtotal, void* gx,
+                                   float* gweight, float* gbias, long long rows, int D, long long x_stride,
+                                   long long gy_stride, long long gtotal_stride, kla_dtype io, float eps,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  // ---- validation: no CUDA call before it passes ---------------------------
+  kla_status st = check_layer_norm(rows, D, io, eps);
+  if (st != KLA_OK) return st;
+  size_t span[3] = {0, 0, 0};
+  if ((st = check_rows(rows, D, x_stride, &span[0])) != KLA_OK) return st;
+  if (gy && (st = check_rows(rows, D, gy_stride, &span[1])) != KLA_OK) return st;
+  if (gtotal && (st = check_rows(rows, D, gtotal_stride, &span[2])) != KLA_OK) return st;
+  if (rows > 0 && (!x || !gx)) return KLA_ERR_INVALID_ARG;
+  const void* wide[] = {weight, gweight, gbias, workspace};
+  for (const void* ptr : wide)
+    if (!aligned16(ptr)) return KLA_ERR_MISALIGNED;
+  const void* ptrs[] = {x, gy, gtotal, gx};
+  for (const void* ptr : ptrs)
+    if (!element_aligned(io, ptr)) return KLA_ERR_MISALIGNED;
+  const size_t z = io_size(io), n = (size_t)rows * D * z, wb = (size_t)D * sizeof(float);
+  const Range ins[] = {{x, span[0] * z}, {weight, wb}, {gy, span[1] * z}, {gtotal, span[2] * z}};
+  const Range outs[] = {{gx, n}, {gweight, wb}, {gbias, wb}};
+  for (int i = 0; i < 4; ++i) {
+    const bool same = gx == ins[i].p && ((i == 2 && (gy_stride == D || rows == 1)) ||
+                                         (i == 3 && (gtotal_stride == D || rows == 1)));
+    if (!same && ranges_overlap(gx, n, ins[i].p, ins[i].n)) return KLA_ERR_INVALID_ARG;
+  }
+  if (ranges_clash(outs + 1, 2, ins, 4) || ranges_overlap(gx, n, gweight, wb) || ranges_overlap(gx, n, gbias, wb))
+    return KLA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (gweight && cudaMemsetAsync(gweight, 0, wb, s) != cudaSuccess) return KLA_ERR_CUDA;
+    if (gbias && cudaMemsetAsync(gbias, 0, wb, s) != cudaSuccess) return KLA_ERR_CUDA;
+    return KLA_OK;
+  }
+  const bool sums = gweight || gbias;
+  if (sums && !workspace) return KLA_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_sms(&sms)) != KLA_OK) return st;
+  if (sums) {
+    const size_t need = kla::layer_norm_partial_bytes(rows, D, sms);
+    if (ws_bytes < need) return KLA_ERR_WORKSPACE;
+    const Range ws[] = {{workspace, need}};
+    if (ranges_clash(ws, 1, ins, 4) || ranges_clash(ws, 1, outs, 3)) return KLA_ERR_INVALID_ARG;
+  }
+  const kla::LayerNormGradArgs a{x, gy, gtotal, x_stride, gy_stride, gtotal_stride, weight, gx,
+                                 sums ? reinterpret_cast<float*>(workspace) : nullptr, gweight, gbias, rows, D, (int)io,
+                                 eps, 1.f / (float)D};
+  return kla::launch_layer_norm_backward(a, sms, s) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -183,4 +183,69 @@ size_t norm_rope_partial_bytes(int B, int Hq, int Hk, int T, int D, int num_sms)
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_rope_backward(const NormRopeArgs& a, int num_sms, cudaStream_t s);
 
+// Gated linear recurrence (kla_recurrence*.cu). Tensors [B,H,T,D] by strides in
+// elements, last dimension contiguous; states [B,H,D] fp32, flat channels
+// C = B·H·D.
+constexpr int kRecTile = 64;         // tokens of a tile, and between two checkpoints
+constexpr int kRecMaxCluster = 8;    // blocks that share a sequence
+constexpr int kRecLog = 0, kRecSigmoid = 1, kRecRate = 2;
+constexpr int kRecPlain = 0, kRecSqrt = 1, kRecComplement = 2;
+struct RecTensor {
+  const void* p;
+  long long sb, sh, st;
+};
+struct RecOut {
+  void* p;
+  long long sb, sh, st;
+};
+struct RecArgs {
+  RecTensor x, g, i;   // i.p null: no input gate
+  RecOut y;            // y.p null: states alone
+  const float* rate;   // [H,D], for kRecRate
+  const float* h0;     // null: zeros
+  float* hT;           // null: not wanted
+  float* ckpt;         // [ceil(T / kRecTile)][C]: the state before every tile, or null
+  int B, H, T, D, C, decay, scale, io;
+};
+// Blocks that go along a sequence together.
+int rec_cluster(int tiles, int T, int resident);
+cudaError_t launch_recurrence(const RecArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_recurrence_step(const RecArgs& a, cudaStream_t s);
+struct RecGradArgs {
+  RecArgs f;           // the forward's inputs; f.ckpt: its checkpoints (required)
+  RecTensor gy;        // gy.p null: zero
+  RecOut gx, gg, gi;   // gi.p null with f.i.p null
+  const float* ghT;    // null: zero
+  float* gh0;          // null: not wanted
+  float* part;         // [blocks along a sequence][C] for the sums of grate, or null
+  float* grate;        // [H,D], with part
+};
+cudaError_t launch_recurrence_backward(const RecGradArgs& a, int num_sms, cudaStream_t s);
+
+// Layer norm with the residual sum before it (kla_layer_norm.cu). Rows [rows,D],
+// inputs by row strides in elements, outputs contiguous.
+constexpr int kLayerNormMaxD = 8192;
+struct LayerNormArgs {
+  const void *x, *residual;  // residual null: total is x, not stored
+  long long x_stride, residual_stride;
+  const float *weight, *bias;  // [D] or null
+  void *y, *total;
+  long long rows;
+  int D, io;
+  float eps, inv_d;
+};
+struct LayerNormGradArgs {
+  const void *x, *gy, *gtotal;  // x: the rows that were normalised; gy, gtotal null: zero
+  long long x_stride, gy_stride, gtotal_stride;
+  const float* weight;
+  void* gx;
+  float *part, *gweight, *gbias;  // part: layer_norm_partial_bytes(), or null (no sums)
+  long long rows;
+  int D, io;
+  float eps, inv_d;
+};
+size_t layer_norm_partial_bytes(long long rows, int D, int num_sms);
+cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s);
+cudaError_t launch_layer_norm_backward(const LayerNormGradArgs& a, int num_sms, cudaStream_t s);
+
 }  // namespace kla

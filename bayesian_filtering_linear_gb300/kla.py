@@ -31,7 +31,9 @@ EXPORTS = ("kla_plan", "kla_plan_for_sms", "kla_forward_workspace_size", "kla_fo
            "kla_shard_map", "kla_shard_start", "kla_conv", "kla_conv_backward_workspace_size",
            "kla_conv_backward", "kla_delta_forward_workspace_size", "kla_delta_forward", "kla_delta_step", "kla_delta_backward_workspace_size",
            "kla_delta_backward", "kla_norm_rope", "kla_norm_rope_backward_workspace_size",
-           "kla_norm_rope_backward")
+           "kla_norm_rope_backward", "kla_recurrence_checkpoints_size", "kla_recurrence_forward", "kla_recurrence_step",
+           "kla_recurrence_backward_workspace_size", "kla_recurrence_backward", "kla_layer_norm",
+           "kla_layer_norm_backward_workspace_size", "kla_layer_norm_backward")
 
 
 class Options(ctypes.Structure):
@@ -47,6 +49,10 @@ class BackwardPlanInfo(ctypes.Structure):
 class NormRopeOptions(ctypes.Structure):
     _fields_ = [("norm", ctypes.c_int), ("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("eps", ctypes.c_float),
                 ("rot_scale", ctypes.c_float), ("offset", ctypes.c_longlong)]
+
+
+class RecurrenceOptions(ctypes.Structure):
+    _fields_ = [("decay", ctypes.c_int), ("scale", ctypes.c_int)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -115,6 +121,23 @@ def load_library(path: str = LIB_PATH):
     lib.kla_norm_rope_backward_workspace_size.argtypes = [i] * 5
     lib.kla_norm_rope_backward.restype = i
     lib.kla_norm_rope_backward.argtypes = [vp] * 12 + [i] * 5 + [strides] * 4 + [i, nr, vp, sz, vp]
+    rec, ll = ctypes.POINTER(RecurrenceOptions), ctypes.c_longlong
+    lib.kla_recurrence_checkpoints_size.restype = sz
+    lib.kla_recurrence_checkpoints_size.argtypes = [i] * 4
+    lib.kla_recurrence_forward.restype = i
+    lib.kla_recurrence_forward.argtypes = [vp] * 8 + [i] * 4 + [strides] * 4 + [i, rec, vp]
+    lib.kla_recurrence_step.restype = i
+    lib.kla_recurrence_step.argtypes = [vp] * 6 + [i] * 4 + [rec, vp]
+    lib.kla_recurrence_backward_workspace_size.restype = sz
+    lib.kla_recurrence_backward_workspace_size.argtypes = [i] * 5
+    lib.kla_recurrence_backward.restype = i
+    lib.kla_recurrence_backward.argtypes = [vp] * 13 + [i] * 4 + [strides] * 7 + [i, rec, vp, sz, vp]
+    lib.kla_layer_norm.restype = i
+    lib.kla_layer_norm.argtypes = [vp] * 6 + [ll, i, ll, ll, i, f, vp]
+    lib.kla_layer_norm_backward_workspace_size.restype = sz
+    lib.kla_layer_norm_backward_workspace_size.argtypes = [ll, i]
+    lib.kla_layer_norm_backward.restype = i
+    lib.kla_layer_norm_backward.argtypes = [vp] * 7 + [ll, i, ll, ll, ll, i, f, vp, sz, vp]
     return lib
 
 
@@ -223,7 +246,7 @@ def _on_stream(fn):
     return call
 
 
-def _need(t, name, dtype, shape, device):
+def _need(t, name, dtype, shape, device, strided=False):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -232,7 +255,10 @@ def _need(t, name, dtype, shape, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
+    if strided:
+        if t.stride(-1) != 1 and t.numel():
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+    elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -738,6 +764,16 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
     return freq.float().to(device or "cpu"), rot_scale
 
 
+def _own_order(x):
+    """An empty tensor of x's shape in the memory order of its first three dimensions, without gaps."""
+    g = torch.empty_like(x)  # a dense view's own strides; of a view with gaps, contiguous
+    if g.stride() != x.stride() and x.numel():
+        order = sorted(range(3), key=x.stride().__getitem__, reverse=True)
+        back = [order.index(d) for d in range(3)]
+        g = torch.empty([x.shape[d] for d in order] + [x.shape[3]], dtype=x.dtype, device=x.device).permute(*back, 3)
+    return g
+
+
 def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions, offset, norm, layout, eps, rot_scale):
     B, Hq, T, D = q.shape
     dt, index = q.dtype, q.get_device()
@@ -821,12 +857,8 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
     for n, (name, x) in enumerate((("gq", q), ("gk", k))):
         if x is None:
             continue
-        g = torch.empty_like(x)  # a dense view's own strides; of a view with gaps, contiguous
-        if g.stride() != x.stride() and x.numel():
-            order = sorted(range(3), key=x.stride().__getitem__, reverse=True)
-            back = [order.index(d) for d in range(3)]
-            g = torch.empty([x.shape[d] for d in order] + [D], dtype=dt, device=q.device).permute(*back, 3)
-        out[name], gstrides[n] = g, _Strides(*g.stride()[:3])
+        out[name] = g = _own_order(x)
+        gstrides[n] = _Strides(*g.stride()[:3])
     for name, w in (("gq_weight", q_weight), ("gk_weight", k_weight)):
         if w is not None:
             out[name] = torch.empty_like(w)
@@ -847,6 +879,243 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
                _addr(out.get("gk_weight")), B, Hq, Hk, T, D, q_strides, k_strides, *gstrides, _IO[dt],
                ctypes.byref(opt), _addr(workspace), ws_bytes))
     _check(st, "kla_norm_rope_backward")
+    return out
+
+
+# ---- the gated linear recurrence -------------------------------------------------
+
+_DECAYS = {"log": 0, "sigmoid": 1, "rate": 2}
+_SCALES = {"none": 0, "sqrt": 1, "complement": 2}
+_RECURRENCES = {(d, s): RecurrenceOptions(n, m) for d, n in _DECAYS.items() for s, m in _SCALES.items()}
+
+
+def _recurrence_args(x, g, i, rate, state, decay, scale, tokens=True):
+    """Checks of what the recurrence's calls share; ``state``: (name, tensor or None)."""
+    opt = _RECURRENCES.get((decay, scale))
+    if opt is None:
+        raise ValueError(f"unknown decay {decay!r} or scale {scale!r}")
+    B, H, T, D = x.shape if tokens else (*x.shape[:2], 1, x.shape[2])
+    dt, index = x.dtype, x.get_device()
+    if index < 0:
+        raise ValueError("inputs must be CUDA tensors")
+    io = _IO.get(dt)
+    if io is None:
+        raise TypeError(f"unsupported I/O dtype {dt}")
+    shape, strided = x.shape, _strided if tokens else _fits
+    if not (strided(x, dt, shape, index) and strided(g, dt, shape, index) and (i is None or strided(i, dt, shape, index))):
+        for name, t in (("x", x), ("g", g), ("i", i)):
+            if t is not None and not strided(t, dt, shape, index):
+                _need(t, name, dt, shape, x.device, strided=tokens)
+    if decay == "rate":
+        if not _fits(rate, torch.float32, (H, D), index):
+            _need(rate, "rate", torch.float32, (H, D), x.device)
+    elif rate is not None:
+        raise ValueError(f"decay {decay!r} takes no rate")
+    for name, t in state:
+        if t is not None and not _fits(t, torch.float32, (B, H, D), index):
+            _need(t, name, torch.float32, (B, H, D), x.device)
+    return B, H, T, D, index, dt, io, opt
+
+
+def _strided(x, dtype, shape, index):
+    """A tensor of this dtype and shape on CUDA device ``index`` whose last dimension is contiguous."""
+    try:
+        return x.dtype is dtype and x.shape == shape and x.get_device() == index and (x.stride(-1) == 1 or not x.numel())
+    except AttributeError:
+        return False
+
+
+def _st(t):
+    return None if t is None else _Strides(*t.stride()[:3])
+
+
+@_on_stream
+def recurrence_forward(x, g, i=None, rate=None, h0=None, *, decay: str = "log", scale: str = "none", y=None, hT=None,
+                       final_state: bool = True, checkpoints=False, stream=None):
+    """The gated linear recurrence over whole sequences (kla_recurrence_forward):
+    ``h_t = a_t h_{t-1} + s(a_t) σ(i_t) x_t``, ``y_t = h_t``, one number a
+    channel. ``decay``: a = e^g ("log"), σ(g) ("sigmoid") or exp(−rate σ(g))
+    ("rate", with ``rate`` fp32 ``[H,D]``); ``scale``: s = 1 ("none"),
+    sqrt(1 − a²) ("sqrt") or 1 − a ("complement"); ``i`` None: no input gate.
+    x, g, i ``[B,H,T,D]`` may be strided views, e.g. a projection's
+    ``[B,T,H,D]`` transposed; y comes in the memory order of x. ``h0`` fp32
+    ``[B,H,D]`` (None: zeros). Returns ``(y, hT)`` (hT None when ``final_state``
+    is False and none was given); with ``checkpoints`` (True, or a buffer of an
+    earlier call) also the states before every 64th token, which
+    :func:`recurrence_backward` takes instead of making them again."""
+    B, H, T, D, index, dt, io, opt = _recurrence_args(x, g, i, rate, (("h0", h0), ("hT", hT)), decay, scale)
+    if y is None:
+        y = _own_order(x)
+    elif not _strided(y, dt, x.shape, index):
+        _need(y, "y", dt, x.shape, x.device, strided=True)
+    if final_state and hT is None:
+        hT = torch.empty((B, H, D), dtype=torch.float32, device=x.device)
+    kept = None
+    if checkpoints is not False and checkpoints is not None:
+        shape = ((T + 63) // 64, B, H, D)
+        kept = torch.empty(shape, dtype=torch.float32, device=x.device) if checkpoints is True else checkpoints
+        if not _fits(kept, torch.float32, shape, index):
+            _need(kept, "checkpoints", torch.float32, shape, x.device)
+    st = _run(index, stream, LIB.kla_recurrence_forward,
+              (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), y.data_ptr(), _addr(hT), _addr(kept),
+               B, H, T, D, _st(x), _st(g), _st(i), _st(y), io, ctypes.byref(opt)))
+    _check(st, "kla_recurrence_forward", y, hT, kept)
+    return (y, hT) if kept is None else (y, hT, kept)
+
+
+@_on_stream
+def recurrence_step(x, g, i, rate, state, *, decay: str = "log", scale: str = "none", y=None, stream=None):
+    """One decode token of the gated linear recurrence (kla_recurrence_step): x,
+    g, i ``[B,H,D]`` (i None: no input gate; rate None unless ``decay`` is
+    "rate"); the fp32 state ``[B,H,D]`` is updated in place; returns y."""
+    B, H, _, D, index, dt, io, opt = _recurrence_args(x, g, i, rate, (), decay, scale, tokens=False)
+    if not _fits(state, torch.float32, x.shape, index):
+        _need(state, "state", torch.float32, x.shape, x.device)
+    if y is None:
+        y = torch.empty_like(x)
+    elif not _fits(y, dt, x.shape, index):
+        _need(y, "y", dt, x.shape, x.device)
+    st = _run(index, stream, LIB.kla_recurrence_step,
+              (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), state.data_ptr(), y.data_ptr(), B, H, D, io,
+               ctypes.byref(opt)))
+    _check(st, "kla_recurrence_step", y, state)
+    return y
+
+
+@_on_stream
+def recurrence_backward(x, g, i=None, rate=None, h0=None, *, gy=None, ghT=None, decay: str = "log",
+                        scale: str = "none", checkpoints=None, state_grad: bool = True, workspace=None, stream=None):
+    """Gradients of a scalar loss through :func:`recurrence_forward` given ``gy``
+    = dL/dy (may be strided; None: zero) and optionally ``ghT`` = dL/dh_T
+    (kla_recurrence_backward). ``checkpoints``: what the forward call returned
+    (None: made again). Returns a dict with ``gx, gg`` and, with an input gate,
+    ``gi`` (in the memory order of x, g and i), ``grate`` with decay "rate" and,
+    with ``state_grad``, ``gh0`` (fp32)."""
+    B, H, T, D, index, dt, io, opt = _recurrence_args(x, g, i, rate, (("h0", h0), ("ghT", ghT)), decay, scale)
+    if gy is not None and not _strided(gy, dt, x.shape, index):
+        _need(gy, "gy", dt, x.shape, x.device, strided=True)
+    if checkpoints is not None and not _fits(checkpoints, torch.float32, ((T + 63) // 64, B, H, D), index):
+        _need(checkpoints, "checkpoints", torch.float32, ((T + 63) // 64, B, H, D), x.device)
+    out = {"gx": _own_order(x), "gg": _own_order(g)}
+    if i is not None:
+        out["gi"] = _own_order(i)
+    if rate is not None:
+        out["grate"] = torch.empty_like(rate)
+    if state_grad:
+        out["gh0"] = torch.empty((B, H, D), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        nbytes = LIB.kla_recurrence_backward_workspace_size(B, H, T, D, checkpoints is not None)
+        if nbytes == _NO_SIZE:
+            raise KlaError(ERR_UNSUPPORTED_SHAPE, "kla_recurrence_backward_workspace_size")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    ws_bytes = _space(workspace, index)
+    gx, gg, gi = out["gx"], out["gg"], out.get("gi")
+    st = _run(index, stream, LIB.kla_recurrence_backward,
+              (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), _addr(checkpoints), _addr(gy), _addr(ghT),
+               gx.data_ptr(), gg.data_ptr(), _addr(gi), _addr(out.get("grate")), _addr(out.get("gh0")), B, H, T, D,
+               _st(x), _st(g), _st(i), _st(gy), _st(gx), _st(gg), _st(gi), io, ctypes.byref(opt), _addr(workspace),
+               ws_bytes))
+    _check(st, "kla_recurrence_backward")
+    return out
+
+
+# ---- layer norm with the residual sum before it -----------------------------------
+
+def _rows(t, name, dtype, shape, index):
+    """The row stride of a tensor ``[..., D]`` that is seen as rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    D = shape[-1]
+    if t.is_contiguous():
+        return D
+    if t.stride(-1) == 1 or D == 1:
+        if t.dim() == 2:
+            return t.stride(0)
+        try:
+            return t.view(-1, D).stride(0)
+        except RuntimeError:
+            pass
+    raise ValueError(f"{name} must be rows of contiguous elements at one distance from each other")
+
+
+def _layer_norm_args(x, weight, bias):
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have rows of at least one element")
+    dt, index, D = x.dtype, x.get_device(), x.shape[-1]
+    if index < 0:
+        raise ValueError("inputs must be CUDA tensors")
+    if dt not in _IO:
+        raise TypeError(f"unsupported I/O dtype {dt}")
+    for name, w in (("weight", weight), ("bias", bias)):
+        if w is not None and not _fits(w, torch.float32, (D,), index):
+            _need(w, name, torch.float32, (D,), x.device)
+    return x.numel() // D, D, index, dt
+
+
+@_on_stream
+def layer_norm(x, weight=None, bias=None, residual=None, *, eps: float = 1e-5, y=None, total=None, stream=None):
+    """Layer norm of the rows of ``x + residual`` (kla_layer_norm): ``total = x +
+    residual`` in the I/O dtype, ``y = (total − mean) / sqrt(var + eps) · weight +
+    bias``. x and residual ``[...,D]`` are rows at one distance (a slice of
+    tokens is read in place); weight, bias ``[D]`` fp32 (None: ones, zeros).
+    Returns ``(y, total)``, contiguous; total is None without a residual. ``y``
+    and ``total`` may be x and residual themselves where those are contiguous."""
+    rows, D, index, dt = _layer_norm_args(x, weight, bias)
+    xs, rs = _rows(x, "x", dt, x.shape, index), 0
+    if residual is not None:
+        rs = _rows(residual, "residual", dt, x.shape, index)
+        if total is None:
+            total = torch.empty(x.shape, dtype=dt, device=x.device)
+        elif not _fits(total, dt, x.shape, index):
+            _need(total, "total", dt, x.shape, x.device)
+    elif total is not None:
+        raise ValueError("total is written with a residual only")
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=x.device)
+    elif not _fits(y, dt, x.shape, index):
+        _need(y, "y", dt, x.shape, x.device)
+    st = _run(index, stream, LIB.kla_layer_norm,
+              (x.data_ptr(), _addr(weight), _addr(bias), _addr(residual), y.data_ptr(), _addr(total), rows, D, xs, rs,
+               _IO[dt], eps))
+    _check(st, "kla_layer_norm", y, total)
+    return y, total
+
+
+@_on_stream
+def layer_norm_backward(x, weight=None, *, gy=None, gtotal=None, eps: float = 1e-5, param_grads: bool | None = None,
+                        workspace=None, stream=None):
+    """Gradients through :func:`layer_norm` (kla_layer_norm_backward): ``x`` holds
+    the rows that were normalised (total, or x without a residual), ``gy`` =
+    dL/dy, ``gtotal`` = dL/dtotal from what else it went into (None: zero).
+    Returns a dict with ``gx`` (of x and of residual alike) and, with
+    ``param_grads`` (None: where there is a weight), ``gweight`` and ``gbias``."""
+    rows, D, index, dt = _layer_norm_args(x, weight, None)
+    xs = _rows(x, "x", dt, x.shape, index)
+    ys = 0 if gy is None else _rows(gy, "gy", dt, x.shape, index)
+    ts = 0 if gtotal is None else _rows(gtotal, "gtotal", dt, x.shape, index)
+    out = {"gx": torch.empty(x.shape, dtype=dt, device=x.device)}
+    if param_grads or (param_grads is None and weight is not None):
+        out["gweight"], out["gbias"] = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
+        if workspace is None:
+            if index == torch.cuda.current_device():  # the size goes by the device's SMs
+                nbytes = LIB.kla_layer_norm_backward_workspace_size(rows, D)
+            else:
+                with torch.cuda.device(index):
+                    nbytes = LIB.kla_layer_norm_backward_workspace_size(rows, D)
+            if nbytes == _NO_SIZE:
+                raise KlaError(ERR_UNSUPPORTED_SHAPE, "kla_layer_norm_backward_workspace_size")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    ws_bytes = _space(workspace, index)
+    st = _run(index, stream, LIB.kla_layer_norm_backward,
+              (x.data_ptr(), _addr(weight), _addr(gy), _addr(gtotal), out["gx"].data_ptr(), _addr(out.get("gweight")),
+               _addr(out.get("gbias")), rows, D, xs, ys, ts, _IO[dt], eps, _addr(workspace), ws_bytes))
+    _check(st, "kla_layer_norm_backward")
     return out
 
 
@@ -986,3 +1255,69 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positio
     kla_norm_rope_backward."""
     how = {"norm": norm, "layout": layout, "eps": eps, "rot_scale": rot_scale, "offset": offset}
     return _NormRopeFunction.apply(q, k, q_weight, k_weight, inv_freq, positions, how)
+
+
+class _RecurrenceFunction(torch.autograd.Function):
+    """kla_recurrence_forward with kla_recurrence_backward as its derivative."""
+
+    @staticmethod
+    def forward(ctx, x, g, i, rate, h0, how):
+        y, hT, kept = recurrence_forward(x, g, i, rate, h0, checkpoints=True, **how)
+        ctx.save_for_backward(x, g, i, rate, h0, kept)
+        ctx.how = how
+        ctx.set_materialize_grads(False)
+        return y, hT
+
+    @staticmethod
+    @_once
+    def backward(ctx, gy, ghT):
+        x, g, i, rate, h0, kept = ctx.saved_tensors
+        if gy is not None:
+            gy = gy.to(x.dtype)
+            if not _takes(gy):
+                gy = gy.contiguous()
+        d = recurrence_backward(x, g, i, rate, h0, gy=gy, ghT=None if ghT is None else ghT.contiguous(),
+                                checkpoints=kept, state_grad=h0 is not None, **ctx.how)
+        return d["gx"], d["gg"], d.get("gi"), d.get("grate"), d.get("gh0"), None
+
+
+def _takes(t):
+    """A view whose rows begin on 16 bytes, as the calls with strides read it in place."""
+    unit = 16 // t.element_size()
+    return (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
+            and all(s % unit == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1))
+
+
+def gated_recurrence(x, g, i=None, rate=None, h0=None, *, decay: str = "log", scale: str = "none"):
+    """Differentiable gated linear recurrence (autograd): returns ``(y, hT)`` like
+    :func:`recurrence_forward`; gradients come from kla_recurrence_backward."""
+    return _RecurrenceFunction.apply(x, g, i, rate, h0, {"decay": decay, "scale": scale})
+
+
+class _LayerNormFunction(torch.autograd.Function):
+    """kla_layer_norm with kla_layer_norm_backward as its derivative."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        y, total = layer_norm(x, weight, bias, residual, eps=eps)
+        ctx.save_for_backward(x if total is None else total, weight, bias)
+        ctx.eps, ctx.sums = eps, residual is not None
+        ctx.set_materialize_grads(False)
+        return y, total
+
+    @staticmethod
+    @_once
+    def backward(ctx, gy, gtotal):
+        x, weight, bias = ctx.saved_tensors
+        gy, gtotal = (None if t is None else t.to(x.dtype).contiguous() for t in (gy, gtotal))
+        d = layer_norm_backward(x, weight, gy=gy, gtotal=gtotal, eps=ctx.eps,
+                                param_grads=weight is not None or bias is not None)
+        return (d["gx"], None if weight is None else d["gweight"], None if bias is None else d["gbias"],
+                d["gx"] if ctx.sums else None, None)
+
+
+def add_layer_norm(x, weight=None, bias=None, residual=None, *, eps: float = 1e-5):
+    """Differentiable layer norm of ``x + residual`` (autograd): returns ``(y,
+    total)`` like :func:`layer_norm`; gradients come from
+    kla_layer_norm_backward."""
+    return _LayerNormFunction.apply(x, weight, bias, residual, eps)

@@ -472,6 +472,112 @@ kla_status kla_norm_rope_backward(const void* q, const void* k, const float* q_w
                                   const long long* gk_strides, kla_dtype io, const kla_norm_rope_options* opt,
                                   void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- the gated linear recurrence ------------------------------------------
+ * A sequence mixer with one number a channel, beside the Kalman scan and the
+ * delta rule:
+ *     h_t = a_t h_{t-1} + s(a_t) σ(i_t) x_t,   y_t = h_t
+ * with the decay a from the input g and the scale s of what is written: */
+typedef enum kla_recurrence_decay {
+  KLA_DECAY_LOG = 0,     /* a = e^g, g ≤ 0 (−∞ resets the state)              */
+  KLA_DECAY_SIGMOID = 1, /* a = σ(g)                                          */
+  KLA_DECAY_RATE = 2     /* a = exp(−rate σ(g)), one rate ≥ 0 a channel       */
+} kla_recurrence_decay;
+typedef enum kla_recurrence_scale {
+  KLA_SCALE_NONE = 0,      /* s = 1                                           */
+  KLA_SCALE_SQRT = 1,      /* s = sqrt(1 − a²): keeps the state's variance (0 where a > 1) */
+  KLA_SCALE_COMPLEMENT = 2 /* s = 1 − a: an average                           */
+} kla_recurrence_scale;
+typedef struct kla_recurrence_options {
+  int decay; /* kla_recurrence_decay */
+  int scale; /* kla_recurrence_scale */
+} kla_recurrence_options;
+
+/* Whole sequences.
+ *   x, g, i, y [B,H,T,D] in `io`, by strides in elements {batch, head, token}
+ *     (NULL: contiguous); the last dimension is contiguous and every stride a
+ *     multiple of 16 bytes (else MISALIGNED), so a projection's [B,T,H·D] is
+ *     read and written in place. i NULL: no input gate (σ(i) = 1). y must not
+ *     overlap any input; its rows must not share memory.
+ *   rate [H,D] fp32 (required for DECAY_RATE, else ignored).
+ *   h0 [B,H,D] fp32: the state before the first token, or NULL for zeros.
+ *   hT [B,H,D] fp32 or NULL: the state after the last token. It may be h0
+ *     itself but must not overlap it otherwise. T = 0 copies the state.
+ *   checkpoints or NULL: kla_recurrence_checkpoints_size() bytes, the state
+ *     before every 64th token, for kla_recurrence_backward.
+ *   D a multiple of 8 (else UNSUPPORTED_SHAPE); B, H, T ≥ 0; pointers 16-byte
+ *   aligned. States are fp32, and decays near 1 are held in more than fp32, so
+ *   that thousands of them multiply without drift. A value that is not finite
+ *   stays in its channel. Repeated calls give identical bits. */
+size_t kla_recurrence_checkpoints_size(int B, int H, int T, int D);
+kla_status kla_recurrence_forward(const void* x, const void* g, const void* i, const float* rate, const float* h0,
+                                  void* y, float* hT, void* checkpoints, int B, int H, int T, int D,
+                                  const long long* x_strides, const long long* g_strides,
+                                  const long long* i_strides, const long long* y_strides, kla_dtype io,
+                                  const kla_recurrence_options* opt, void* stream);
+
+/* One decode token: x, g, i, y contiguous [B,H,D]; the state [B,H,D] is read
+ * and overwritten. */
+kla_status kla_recurrence_step(const void* x, const void* g, const void* i, const float* rate, float* state, void* y,
+                               int B, int H, int D, kla_dtype io, const kla_recurrence_options* opt, void* stream);
+
+/* Gradients of a loss L through kla_recurrence_forward.
+ *   checkpoints: what the forward call stored, or NULL: made again in the
+ *     workspace (one more pass over x, g and i).
+ *   gy = dL/dy [B,H,T,D] in `io` by strides (NULL: zero); ghT = dL/dh_T
+ *     [B,H,D] fp32 (NULL: zero).
+ *   Outputs, written and not accumulated: gx, gg, gi [B,H,T,D] in `io`, by
+ *     strides of their own (NULL: contiguous; gi with i only; required unless
+ *     empty; their rows must not share memory, within or between them); grate
+ *     [H,D] fp32 or NULL, summed over B and T in a fixed order; gh0 [B,H,D]
+ *     fp32 or NULL.
+ *   Where a = 1 exactly the derivative of sqrt(1 − a²) has no value, and its
+ *   term is left out of gg.
+ *   workspace / ws_bytes: kla_recurrence_backward_workspace_size() bytes (else
+ *     WORKSPACE; may be NULL when that is 0); `with_checkpoints` says whether
+ *     the call gives them. */
+size_t kla_recurrence_backward_workspace_size(int B, int H, int T, int D, int with_checkpoints);
+kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, const float* rate, const float* h0,
+                                   const void* checkpoints, const void* gy, const float* ghT, void* gx, void* gg,
+                                   void* gi, float* grate, float* gh0, int B, int H, int T, int D,
+                                   const long long* x_strides, const long long* g_strides,
+                                   const long long* i_strides, const long long* gy_strides,
+                                   const long long* gx_strides, const long long* gg_strides,
+                                   const long long* gi_strides, kla_dtype io, const kla_recurrence_options* opt,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- layer norm with the residual sum before it ---------------------------
+ * What stands before a mixer: for every row of D entries
+ *     total = x + residual (rounded to `io`, as it is stored; x itself without)
+ *     y = (total − mean) / sqrt(var + eps) · weight + bias
+ * with the row's mean and (biased) variance, both in fp32.
+ *   x, residual: rows in `io`, x_stride and residual_stride elements apart
+ *     (0 repeats one row); residual NULL: no sum, and total is not written.
+ *   weight, bias [D] fp32, or NULL for ones and zeros.
+ *   y, total: contiguous [rows,D] in `io` (total required with residual). Each
+ *     may be x or residual itself where that is contiguous (in place), but
+ *     must not overlap an input otherwise, nor the other.
+ *   D in [1, 8192] (else UNSUPPORTED_SHAPE), rows ≥ 0. Rows need the alignment
+ *     of their elements only, weight and bias 16 bytes; rows that all begin on
+ *     16 bytes are read in wider pieces. eps ≥ 0 (else INVALID_ARG). */
+kla_status kla_layer_norm(const void* x, const float* weight, const float* bias, const void* residual, void* y,
+                          void* total, long long rows, int D, long long x_stride, long long residual_stride,
+                          kla_dtype io, float eps, void* stream);
+
+/* Gradients through kla_layer_norm: x holds the rows that were normalised (the
+ * forward call's total, or its x without a residual), gy = dL/dy and gtotal =
+ * dL/dtotal from what else the total went into (each NULL: zero), by row
+ * strides. gx, contiguous [rows,D] in `io` (required unless empty), is the
+ * gradient of x and of residual alike; it may be gy or gtotal itself where that
+ * is contiguous, but must not overlap an input otherwise. gweight, gbias [D]
+ * fp32 or NULL, summed over the rows in a fixed order.
+ *   workspace / ws_bytes: kla_layer_norm_backward_workspace_size() bytes when
+ *   gweight or gbias is wanted (else WORKSPACE); may be NULL otherwise. */
+size_t kla_layer_norm_backward_workspace_size(long long rows, int D);
+kla_status kla_layer_norm_backward(const void* x, const float* weight, const void* gy, const void* gtotal, void* gx,
+                                   float* gweight, float* gbias, long long rows, int D, long long x_stride,
+                                   long long gy_stride, long long gtotal_stride, kla_dtype io, float eps,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* kla_status_string(kla_status s);
 
