@@ -3,14 +3,14 @@
 // between the blocks of a cluster.
 //
 // Every channel (b, h, d) is a recurrence of its own, h <- a h + b x, so a
-// tile is 64 channels (in the flat order b, h, d) by 64 tokens: a warp takes
-// eight of the tokens and a lane two of the channels, in packed arithmetic.
-// A segment of tokens acts on the state before it as h -> A h + S.
+// tile is 64 channels (in the flat order b, h, d) by 64 tokens: the block's
+// warps share the tokens and a lane takes two of the channels, in packed
+// arithmetic. A segment of tokens acts on the state before it as h -> A h + S.
 //
 // Decays near 1 multiply by the thousand, and one float of a decay is off by
 // up to 2^-25, always the same way where a is the same. So a decay is a float
 // and the rest that it leaves (1 - a is known to a few 2^-24 of itself), and
-// so are the products of decays.
+// so are the products of decays that the state is carried by.
 #pragma once
 
 #include "kla_device.cuh"
@@ -19,61 +19,83 @@
 namespace kla {
 namespace rec {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kTok = 8;  // tokens a warp
-constexpr int kTile = kRecTile, kChans = 64;                 // tokens and channels a tile
-static_assert(kTile == kWarps * kTok, "a tile is the warps' tokens");
+constexpr int kTile = kRecTile, kChans = 64;  // tokens and channels a tile
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ f2 f2_both(float x) { return f2_make(x, x); }
-__device__ __forceinline__ f2 f2_neg(f2 x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ f2 f2_ex2(f2 x) { return f2_make(ex2(f2_lo(x)), ex2(f2_hi(x))); }
+// e^-x
+__device__ __forceinline__ f2 f2_exp_neg(f2 x) { return f2_ex2(f2_mul(x, f2_both(-1.4426950408889634f))); }
+// The same, held at 2^126 or below, whose reciprocal is still a normal number.
+__device__ __forceinline__ f2 f2_exp_neg_held(f2 x) {
+  const f2 e = f2_exp_neg(x);
+  return f2_make(fminf(f2_lo(e), 0x1p126f), fminf(f2_hi(e), 0x1p126f));
+}
 
-// e^-x, held at 2^126 or below, whose reciprocal is still a normal number
-__device__ __forceinline__ float exp_neg(float x) { return fminf(ex2(x * -1.4426950408889634f), 0x1p126f); }
-
-// A decay as the float nearest to it and the rest.
+// A decay: the float nearest to it, the rest, and a - 1.
 struct Decay {
-  f2 hi, lo;
+  f2 hi, lo, less;
 };
 
-// a - 1 and a of one decay given its logarithm: a polynomial near 1 (Taylor's,
-// the first term left out is 3e-8 of the value), else the exponential.
-__device__ __forceinline__ void decay_of_log(f2 la, Decay& a, f2& less) {
-  constexpr float kNear = 0.375f;
-  f2 p = f2_both(1.f / 5040.f);
-  p = f2_fma(p, la, f2_both(1.f / 720.f));
+// hi and lo of 1 + less.
+__device__ __forceinline__ void split(Decay& a) {
+  const f2 one = f2_both(1.f);
+  a.hi = f2_add(one, a.less);
+  a.lo = f2_add(f2_fma(a.hi, f2_both(-1.f), one), a.less);
+}
+
+// Of a decay's logarithm: near 1 a polynomial for a - 1 (Taylor's, the first
+// term left out is 3e-8 of the value), elsewhere the exponential. NEAR: all are.
+constexpr float kNear = 0.375f;
+template <bool NEAR>
+__device__ __forceinline__ Decay decay_of_log(f2 la) {
+  Decay a;
+  f2 p = f2_fma(la, f2_both(1.f / 5040.f), f2_both(1.f / 720.f));
   p = f2_fma(p, la, f2_both(1.f / 120.f));
   p = f2_fma(p, la, f2_both(1.f / 24.f));
   p = f2_fma(p, la, f2_both(1.f / 6.f));
   p = f2_fma(p, la, f2_both(0.5f));
-  p = f2_fma(f2_mul(p, la), la, la);
-  const f2 one = f2_both(1.f), hi = f2_add(one, p);
-  const f2 lo = f2_add(p, f2_neg(f2_add(hi, f2_neg(one))));
-  float h[2] = {f2_lo(hi), f2_hi(hi)}, l[2] = {f2_lo(lo), f2_hi(lo)}, m[2] = {f2_lo(p), f2_hi(p)};
-  const float x[2] = {f2_lo(la), f2_hi(la)};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float e = ex2(x[i] * 1.4426950408889634f);
-    const bool near = fabsf(x[i]) < kNear;
-    h[i] = near ? h[i] : e;
-    l[i] = near ? l[i] : 0.f;
-    m[i] = near ? m[i] : e - 1.f;
+  a.less = f2_fma(f2_mul(p, la), la, la);
+  split(a);
+  if (!NEAR) {
+    const f2 e = f2_ex2(f2_mul(la, f2_both(1.4426950408889634f))), m = f2_add(e, f2_both(-1.f));
+    const bool n0 = fabsf(f2_lo(la)) < kNear, n1 = fabsf(f2_hi(la)) < kNear;
+    a.hi = f2_make(n0 ? f2_lo(a.hi) : f2_lo(e), n1 ? f2_hi(a.hi) : f2_hi(e));
+    a.lo = f2_make(n0 ? f2_lo(a.lo) : 0.f, n1 ? f2_hi(a.lo) : 0.f);
+    a.less = f2_make(n0 ? f2_lo(a.less) : f2_lo(m), n1 ? f2_hi(a.less) : f2_hi(m));
   }
-  a.hi = f2_make(h[0], h[1]);
-  a.lo = f2_make(l[0], l[1]);
-  less = f2_make(m[0], m[1]);
+  return a;
 }
 
-// The same of a sigmoid: e = e^-g, a = 1 / (1 + e).
-__device__ __forceinline__ void decay_of_sigmoid(float e, float& hi, float& lo, float& less) {
-  const float s = rcp_approx(1.f + e);
-  less = -e * s;
-  hi = 1.f + less;
-  lo = less - (hi - 1.f);
-  if (e > 1.f) hi = s, lo = 0.f, less = s - 1.f;
+// Of a sigmoid: e = e^-g (held), a = 1 / (1 + e).
+__device__ __forceinline__ Decay decay_of_sigmoid(f2 e) {
+  Decay a;
+  const f2 s = f2_rcp(f2_add(e, f2_both(1.f))), m = f2_add(s, f2_both(-1.f));
+  a.less = f2_mul(f2_mul(e, f2_both(-1.f)), s);
+  split(a);
+  const bool n0 = f2_lo(e) <= 1.f, n1 = f2_hi(e) <= 1.f;
+  a.hi = f2_make(n0 ? f2_lo(a.hi) : f2_lo(s), n1 ? f2_hi(a.hi) : f2_hi(s));
+  a.lo = f2_make(n0 ? f2_lo(a.lo) : 0.f, n1 ? f2_hi(a.lo) : 0.f);
+  a.less = f2_make(n0 ? f2_lo(a.less) : f2_lo(m), n1 ? f2_hi(a.less) : f2_hi(m));
+  return a;
+}
+
+// 1 - a², zero below the normal numbers (and where a > 1), and 1/sqrt of it (there zero too).
+__device__ __forceinline__ f2 spread(f2 less) {
+  return f2_mul(f2_mul(less, f2_both(-1.f)), f2_add(less, f2_both(2.f)));
+}
+__device__ __forceinline__ f2 spread_rsqrt(f2 v) {
+  const float a = f2_lo(v), b = f2_hi(v);
+  return f2_make(a >= 0x1p-126f ? rsqrt_fast(a) : 0.f, b >= 0x1p-126f ? rsqrt_fast(b) : 0.f);
 }
 
 // The map of a segment, h -> A h + S: A in two floats.
@@ -83,12 +105,13 @@ struct Map {
 __device__ __forceinline__ f2 apply(f2 A, f2 Al, f2 S, f2 h) { return f2_fma(A, h, f2_fma(Al, h, S)); }
 // A <- a A
 __device__ __forceinline__ void lengthen(f2& A, f2& Al, f2 hi, f2 lo) {
-  const f2 p = f2_mul(hi, A), rest = f2_fma(hi, A, f2_neg(p));
+  const f2 p = f2_mul(hi, A);
+  const f2 rest = f2_fma(hi, A, f2_mul(p, f2_both(-1.f)));
   Al = f2_fma(hi, Al, f2_fma(lo, A, rest));
   A = p;
 }
 
-// ---- a token's pair of channels from a tile in shared memory ------------------
+// ---- a token's pair of channels -------------------------------------------------
 template <typename IO>
 __device__ __forceinline__ f2 pair_at(const IO* p);
 template <>
@@ -120,19 +143,36 @@ struct Place {
 
 // One stream's share of a tile's copies, 16 bytes a copy: a thread keeps its
 // channels and goes through the tokens.
-template <typename IO>
+template <typename IO, int THREADS>
 struct Copier {
-  static constexpr int VE = 16 / sizeof(IO), GROUPS = kChans / VE, ROWS = kThreads / GROUPS;
+  static constexpr int VE = 16 / sizeof(IO), GROUPS = kChans / VE, ROWS = THREADS / GROUPS;
   __device__ __forceinline__ static int group() { return threadIdx.x % GROUPS * VE; }
-  // tokens [t0, min(t0 + kTile, T)) of the stream at `src` (its thread's channels) into `dst`
-  __device__ __forceinline__ static void tile(IO* dst, const IO* src, long long st, int t0, int T) {
+  __device__ __forceinline__ static int row() { return threadIdx.x / GROUPS; }
+  // tokens [t0, t0 + kTile) of the stream, `src` its thread's channels of token 0, into `dst`; behind T, `fill`s
+  __device__ __forceinline__ static void tile(IO* dst, const IO* src, long long st, int t0, int T, uint32_t fill) {
+    dst += row() * kChans + group();
+    src += (long long)(t0 + row()) * st;
+    const long long down = ROWS * st;
+    if (t0 + kTile <= T) {
 #pragma unroll
-    for (int r = 0; r < kTile; r += ROWS) {
-      const int row = r + threadIdx.x / GROUPS;
-      if (t0 + row < T) cp_async16(dst + row * kChans + group(), src + (long long)(t0 + row) * st);
+      for (int r = 0; r < kTile; r += ROWS, src += down) cp_async16(dst + r * kChans, src);
+    } else {
+#pragma unroll
+      for (int r = 0; r < kTile; r += ROWS, src += down) {
+        if (t0 + row() + r < T) cp_async16(dst + r * kChans, src);
+        else *reinterpret_cast<uint4*>(dst + r * kChans) = make_uint4(fill, fill, fill, fill);
+      }
     }
   }
 };
+
+// What stands for g behind the last token: a decay of one.
+template <typename IO, int DECAY>
+__device__ __forceinline__ uint32_t still() {
+  if (DECAY == kRecLog) return 0;
+  if (sizeof(IO) == 2) return DECAY == kRecSigmoid ? 0x7f807f80u : 0xff80ff80u;  // ±∞
+  return DECAY == kRecSigmoid ? 0x7f800000u : 0xff800000u;
+}
 
 // ---- clusters ------------------------------------------------------------------
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -144,17 +184,16 @@ __device__ __forceinline__ void put_remote(const void* p, int rank, f2 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-// The segments' maps of a block's warps, and of a cluster's blocks (in two
-// halves, used in turn, so that one barrier a step is enough).
-struct Shared {
-  f2 warp[kWarps][4][32];
-  f2 block[2][kRecMaxCluster][3][32];
+// The maps of a cluster's blocks, [2][k], in two halves, used in turn, so that one barrier a step is enough.
+struct BlockMap {
+  f2 A[32], Al[32], S[32];
 };
+__host__ __device__ constexpr size_t block_maps_bytes(int k) { return k > 1 ? 2 * (size_t)k * sizeof(BlockMap) : 0; }
 
 // Launches `tiles` clusters of k blocks.
 template <typename Args>
-inline cudaError_t launch_rec_cluster(void (*kernel)(Args, int), const Args& a, int tiles, int k, size_t smem,
-                                      cudaStream_t s) {
+inline cudaError_t launch_rec_cluster(void (*kernel)(Args, int), const Args& a, int tiles, int k, int threads,
+                                      size_t smem, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -163,7 +202,7 @@ inline cudaError_t launch_rec_cluster(void (*kernel)(Args, int), const Args& a, 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)tiles * (unsigned)k);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;

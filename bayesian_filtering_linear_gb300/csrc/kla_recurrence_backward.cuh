@@ -1,0 +1,268 @@
+// Gradients of the gated linear recurrence (sm_103a), instantiated by type in
+// kla_recurrence_backward_f32.cu and kla_recurrence_backward_bf16.cu. With
+// G_t = dL/dh_t in all:
+//
+//   G_t = gy_t + a_{t+1} G_{t+1}
+//   gx = G s σ(i),  gi = G s σ(i) σ(-i) x
+//   dL/dlog a = G u,  u = a h_{t-1} + s' σ(i) x,  s' = ds/dlog a = 0, -a²/s or -a
+//   gg = dL/dlog a · (1, σ(-g) or -rate σ(g) σ(-g));  grate = -Σ dL/dlog a · σ(g)
+//
+// (where s = 0, at a = 1, s' has no value and its term is left out). Inputs and
+// gy are read once and the gradients written once, and HBM bounds it, the issue
+// of instructions close behind (about 55 an element with both gates). The kernel
+// goes from the last tile to the first as the forward's goes from the first to
+// the last: the state before a tile comes from the checkpoints that the forward
+// pass stored (in fp32: outputs in bf16 would put their rounding into every
+// gradient), and a warp's eight tokens need the maps of the warps before them
+// for h and of those behind them for G, which are exchanged together. Forward
+// through its tokens a warp makes P and V, u = P h + V with h the state before
+// the warp; back through them Q and R, G = Q z + R with z what reaches the last
+// one from behind. What the last loop needs and registers have no room for
+// stays in shared memory at the thread's own place: e^-g where g was (and i),
+// the gate's term beside.
+#pragma once
+
+#include "kla_recurrence_kernels.cuh"
+
+namespace kla {
+namespace rec {
+
+constexpr int kBackWarps = 8, kBackThreads = 32 * kBackWarps, kBackTok = kTile / kBackWarps;
+// Stages of the ring of tiles: two, or for fp32, whose tiles are twice as large, one that two blocks take turns by.
+template <typename IO>
+constexpr int kStages = sizeof(IO) == 2 ? 2 : 1;
+
+// A pair of floats at the thread's own place of a tile: where a pair of one (fp32) or of two streams was (bf16).
+__device__ __forceinline__ void keep(float* a, float*, f2 v) { *reinterpret_cast<f2*>(a) = v; }
+__device__ __forceinline__ f2 kept(const float* a, const float*) { return *reinterpret_cast<const f2*>(a); }
+__device__ __forceinline__ void keep(__nv_bfloat16* a, __nv_bfloat16* b, f2 v) {
+  *reinterpret_cast<float*>(a) = f2_lo(v);
+  *reinterpret_cast<float*>(b) = f2_hi(v);
+}
+__device__ __forceinline__ f2 kept(const __nv_bfloat16* a, const __nv_bfloat16* b) {
+  return f2_make(*reinterpret_cast<const float*>(a), *reinterpret_cast<const float*>(b));
+}
+// The gate's terms: where i was (fp32), or in an array of their own.
+template <typename IO>
+__device__ __forceinline__ f2* gate_place(IO* i, f2* own, int j) {
+  return sizeof(IO) == 4 ? reinterpret_cast<f2*>(i) : own + j * kBackThreads;
+}
+
+// Forward through a warp's tokens: its map, and for each the decay (hi, lo), P, V and b = s σ(i).
+template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
+__device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackTok], f2 (&lo)[kBackTok],
+                                     f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2 (&b)[kBackTok]) {
+  constexpr int S = kTile * kChans;
+  const f2 one = f2_both(1.f), minus = f2_both(-1.f);
+  Map m{one, 0, 0};
+#pragma unroll
+  for (int j = 0; j < kBackTok; ++j) {
+    IO* const at = tile + j * kChans;
+    const f2 x = pair_at<IO>(at);
+    f2 g = pair_at<IO>(at + S), open = one, shut = 0;
+    if (GATE) {
+      const f2 e = f2_exp_neg_held(pair_at<IO>(at + 2 * S));
+      open = f2_rcp(f2_add(one, e));
+      shut = f2_mul(e, open);
+    }
+    Decay a;
+    if (DECAY != kRecLog) {
+      const f2 e = f2_exp_neg_held(g);
+      keep(at + S, at + 2 * S, e);
+      if (DECAY == kRecSigmoid) a = decay_of_sigmoid(e);
+      else g = f2_mul(rate, f2_rcp(f2_add(one, e)));
+    }
+    if (DECAY != kRecSigmoid) a = decay_of_log<NEAR>(g);
+    hi[j] = a.hi, lo[j] = a.lo;
+    const f2 xo = GATE ? f2_mul(x, open) : x;
+    f2 w = 0;  // s' σ(i) x
+    b[j] = open;
+    if (SCALE == kRecSqrt) {
+      const f2 v = spread(a.less), rs = spread_rsqrt(v);
+      b[j] = f2_mul(f2_mul(v, rs), open);
+      w = f2_mul(f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus)), xo);
+    } else if (SCALE == kRecComplement) {
+      b[j] = f2_mul(f2_mul(a.less, minus), open);
+      w = f2_mul(f2_mul(a.hi, minus), xo);
+    }
+    const f2 bx = f2_mul(b[j], x);
+    if (GATE) *gate_place(at + 2 * S, own, j) = f2_mul(bx, shut);
+    const f2 ah = f2_fma(a.hi, m.S, f2_mul(a.lo, m.S));
+    V[j] = SCALE == kRecPlain ? ah : f2_add(ah, w);
+    m.S = f2_add(ah, bx);
+    lengthen(m.A, m.Al, a.hi, a.lo);
+    P[j] = m.A;
+  }
+  return m;
+}
+
+template <typename IO, int DECAY, int SCALE, bool GATE>
+__global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(const RecGradArgs q, int k) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ f2 maps[kBackWarps][4][32];
+  constexpr int S = kTile * kChans, STAGE = 4 * S;
+  BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
+  IO* const ring = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
+  f2* const own = reinterpret_cast<f2*>(ring + kStages<IO> * STAGE) + threadIdx.x;  // [kBackTok][kBackThreads], bf16 with a gate
+  const RecArgs& p = q.f;
+  const int rank = blockIdx.x % k, c0 = blockIdx.x / k * kChans, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (k > 1) cluster_arrive();  // every block of the cluster has started before another stores to it
+
+  // this thread's copies
+  using Copy = Copier<IO, kBackThreads>;
+  const int cc = c0 + Copy::group();
+  const bool copies = cc < p.C;
+  const Place at(copies ? cc : 0, p.H, p.D);
+  const IO* const sx = reinterpret_cast<const IO*>(p.x.p) + at.of(p.x);
+  const IO* const sg = reinterpret_cast<const IO*>(p.g.p) + at.of(p.g);
+  const IO* const si = reinterpret_cast<const IO*>(p.i.p) + (GATE ? at.of(p.i) : 0);
+  const IO* const sy = reinterpret_cast<const IO*>(q.gy.p) + (q.gy.p ? at.of(q.gy) : 0);
+  auto fetch = [&](long long step) {
+    if (copies && step >= 0) {
+      const long long first = (step * k + rank) * kTile;
+      const int t0 = (int)(first < p.T ? first : p.T);
+      IO* const d = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0);
+      Copy::tile(d, sx, p.x.st, t0, p.T, 0);
+      Copy::tile(d + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
+      if (GATE) Copy::tile(d + 2 * S, si, p.i.st, t0, p.T, 0);
+      if (q.gy.p) Copy::tile(d + 3 * S, sy, q.gy.st, t0, p.T, 0);
+    }
+    cp_async_commit();
+  };
+
+  // this lane's channels
+  const int c = c0 + 2 * lane;
+  const bool live = c < p.C;
+  const Place my(live ? c : 0, p.H, p.D);
+  IO* const gx = reinterpret_cast<IO*>(q.gx.p) + my.of(q.gx);
+  IO* const gg = reinterpret_cast<IO*>(q.gg.p) + my.of(q.gg);
+  IO* const gi = reinterpret_cast<IO*>(q.gi.p) + (GATE ? my.of(q.gi) : 0);
+  f2 rate = 0, z = 0, sum = 0;  // z: what reaches the step's last token from behind it
+  if (DECAY == kRecRate && live)
+    rate = f2_mul(*reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d), f2_both(-1.f));
+  if (q.ghT && live) z = *reinterpret_cast<const f2*>(q.ghT + c);
+  // rates too small for a decay far from 1 (the same lanes in every warp, so all the block's warps agree)
+  const bool near = DECAY == kRecRate && __all_sync(~0u, fabsf(f2_lo(rate)) < kNear && fabsf(f2_hi(rate)) < kNear);
+
+  const f2 one = f2_both(1.f);
+  const long long steps = ((long long)p.T + kTile * k - 1) / (kTile * k);
+  fetch(steps - 1);
+  for (long long step = steps - 1; step >= 0; --step) {
+    const long long first = (step * k + rank) * kTile, t0 = first + w * kBackTok;
+    f2 h = 0;
+    if (live && first < p.T) h = *reinterpret_cast<const f2*>(p.ckpt + first / kTile * p.C + c);
+    cp_async_wait<0>();
+    __syncthreads();
+    if (kStages<IO> == 2) fetch(step - 1);  // (the last loop of the step before has read that stage)
+    IO* const tile = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0) + w * kBackTok * kChans + 2 * lane;
+    f2 Q[kBackTok], R[kBackTok], P[kBackTok], V[kBackTok], b[kBackTok];  // Q, R: the decays first
+    Map m;
+    if (near) m = forth<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(tile, own, rate, Q, R, P, V, b);
+    else m = forth<IO, DECAY, SCALE, GATE, false>(tile, own, rate, Q, R, P, V, b);
+    f2 r = 0, prod = one;
+#pragma unroll
+    for (int j = kBackTok - 1; j >= 0; --j) {
+      const f2 hi = Q[j], lo = R[j];
+      R[j] = q.gy.p ? f2_add(r, pair_at<IO>(tile + 3 * S + j * kChans)) : r;
+      r = f2_fma(hi, R[j], f2_mul(lo, R[j]));
+      Q[j] = prod;
+      prod = f2_mul(prod, hi);
+    }
+    maps[w][0][lane] = m.A, maps[w][1][lane] = m.Al, maps[w][2][lane] = m.S, maps[w][3][lane] = r;
+    __syncthreads();
+    f2 next = z;
+    if (k > 1) {  // the block's map of G to every block of the cluster
+      BlockMap* const half = blocks + (step & 1) * k;
+      if (step == steps - 1) cluster_wait();
+      if (w == kBackWarps - 1) {
+        Map t{m.A, m.Al, r};
+#pragma unroll
+        for (int v = kBackWarps - 2; v >= 0; --v) {
+          const f2 A = maps[v][0][lane], Al = maps[v][1][lane];
+          t.S = apply(A, Al, maps[v][3][lane], t.S);
+          lengthen(t.A, t.Al, A, Al);
+        }
+        for (int o = 0; o < k; ++o) {
+          put_remote(&half[rank].A[lane], o, t.A);
+          put_remote(&half[rank].Al[lane], o, t.Al);
+          put_remote(&half[rank].S[lane], o, t.S);
+        }
+      }
+      cluster_arrive();
+      cluster_wait();
+      for (int o = k - 1; o >= 0; --o) {
+        if (o == rank) z = next;
+        next = apply(half[o].A[lane], half[o].Al[lane], half[o].S[lane], next);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kBackWarps - 1; ++v)
+      if (v < w) h = apply(maps[v][0][lane], maps[v][1][lane], maps[v][2][lane], h);
+    f2 behind = z;
+#pragma unroll
+    for (int v = kBackWarps - 1; v >= 0; --v) {
+      if (v == w) behind = z;
+      if (k == 1 || v > w) z = apply(maps[v][0][lane], maps[v][1][lane], maps[v][3][lane], z);
+    }
+    if (k > 1) z = next;
+    if (t0 < p.T) {
+      const int n = (int)min((long long)kBackTok, p.T - t0);
+      IO *ox = gx + t0 * q.gx.st, *og = gg + t0 * q.gg.st, *oi = gi + t0 * q.gi.st;
+#pragma unroll
+      for (int j = 0; j < kBackTok; ++j) {
+        const f2 G = f2_fma(Q[j], behind, R[j]);
+        f2 by_log = f2_mul(G, f2_fma(P[j], h, V[j]));
+        if (DECAY != kRecLog) {
+          const f2 e = kept(tile + S + j * kChans, tile + 2 * S + j * kChans);
+          const f2 open = f2_rcp(f2_add(one, e)), shut = f2_mul(e, open);
+          if (DECAY == kRecRate) {
+            by_log = f2_mul(by_log, open);
+            if (j < n) sum = f2_add(sum, by_log);
+            by_log = f2_mul(by_log, f2_mul(rate, shut));
+          } else {
+            by_log = f2_mul(by_log, shut);
+          }
+        }
+        if (live && j < n) {
+          put_pair(ox, f2_mul(G, b[j]));
+          put_pair(og, by_log);
+          if (GATE) put_pair(oi, f2_mul(G, *gate_place(tile + 2 * S + j * kChans, own, j)));
+        }
+        ox += q.gx.st, og += q.gg.st, oi += q.gi.st;
+      }
+    }
+    if (kStages<IO> == 1) {
+      __syncthreads();
+      fetch(step - 1);
+    }
+  }
+  if (q.gh0 && live && rank == 0 && w == 0) *reinterpret_cast<f2*>(q.gh0 + c) = z;
+  if (DECAY == kRecRate && q.part) {  // the block's sums of the rates' gradients, in a fixed order
+    __syncthreads();
+    maps[w][0][lane] = sum;
+    __syncthreads();
+    if (w == 0 && live) {
+#pragma unroll
+      for (int v = 1; v < kBackWarps; ++v) sum = f2_add(sum, maps[v][0][lane]);
+      *reinterpret_cast<f2*>(q.part + (long long)rank * p.C + c) = sum;
+    }
+  }
+}
+
+}  // namespace rec
+
+template <typename IO>
+cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int num_sms, int* parts, cudaStream_t s) {
+  const int tiles = (a.f.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, a.f.T, num_sms * 2);
+  const size_t tile = 4 * (size_t)rec::kTile * rec::kChans * sizeof(IO);
+  const size_t smem = rec::block_maps_bytes(k) + rec::kStages<IO> * tile +
+                      (sizeof(IO) == 2 && a.f.i.p ? (size_t)rec::kBackTok * rec::kBackThreads * sizeof(f2) : 0);
+  *parts = k;
+  return rec::by_kind(a.f, [&](auto d, auto sc, auto gate) {
+    return rec::launch_rec_cluster(
+        rec::kla_recurrence_grad_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>, a, tiles, k,
+        rec::kBackThreads, smem, s);
+  });
+}
+
+}  // namespace kla

@@ -1,0 +1,216 @@
+// The forward kernels of the gated linear recurrence (sm_103a), instantiated by
+// type in kla_recurrence_f32.cu and kla_recurrence_bf16.cu:
+//
+//   h_t = a_t h_{t-1} + s(a_t) σ(i_t) x_t,  y_t = h_t
+//   a = e^g, σ(g) or exp(-rate σ(g));  s = 1, sqrt(1 - a²) or 1 - a
+//
+// Every input is read once and every output written once, so HBM bounds it;
+// next comes the issue of instructions (about 30 an element with both gates). A
+// cluster of blocks goes along the sequence, a tile of 64 tokens a block at a
+// time. A warp runs through its sixteen tokens from a state of zero, keeping for
+// each the outcome Y and the product P of the decays so far, and leaves its map
+// (A, S); from then on the tile's inputs are no longer needed, and the next tile's
+// are sent for into the same place. The maps of the block's warps meet in shared
+// memory, those of the cluster's blocks are stored in each other's, and from
+// them every warp knows the state h that it starts from: y_t = P_t h + Y_t.
+// Nothing waits but barriers and nothing goes through memory.
+#pragma once
+
+#include "kla_recurrence.cuh"
+
+namespace kla {
+namespace rec {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kTok = kTile / kWarps;  // tokens a warp
+
+// A decay and the factor s σ(i) x of a pair, from what is read.
+template <int DECAY, int SCALE, bool NEAR>
+__device__ __forceinline__ Decay decay_of(f2 g, f2 rate) {
+  if (DECAY == kRecSigmoid) return decay_of_sigmoid(f2_exp_neg_held(g));
+  if (DECAY == kRecRate) g = f2_mul(rate, f2_rcp(f2_add(f2_exp_neg(g), f2_both(1.f))));
+  return decay_of_log<NEAR>(g);
+}
+template <int SCALE>
+__device__ __forceinline__ f2 scaled(f2 x, f2 less) {
+  if (SCALE == kRecSqrt) {
+    const f2 v = spread(less);
+    return f2_mul(x, f2_mul(v, spread_rsqrt(v)));
+  }
+  if (SCALE == kRecComplement) return f2_mul(x, f2_mul(less, f2_both(-1.f)));
+  return x;
+}
+
+template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
+__device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f2 (&Y)[kTok]) {
+  constexpr int S = kTile * kChans;  // elements a stream
+  Map m{f2_both(1.f), 0, 0};
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    f2 x = pair_at<IO>(tile + j * kChans);
+    const Decay a = decay_of<DECAY, SCALE, NEAR>(pair_at<IO>(tile + S + j * kChans), rate);
+    x = scaled<SCALE>(x, a.less);
+    if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(tile + 2 * S + j * kChans)), f2_both(1.f))));
+    m.S = apply(a.hi, a.lo, x, m.S);
+    lengthen(m.A, m.Al, a.hi, a.lo);
+    P[j] = m.A;
+    Y[j] = m.S;
+  }
+  return m;
+}
+
+template <typename IO, int DECAY, int SCALE, bool GATE>
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurrence_kernel(const RecArgs p, int k) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ f2 maps[kWarps][3][32];
+  BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
+  IO* const tile = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
+  constexpr int S = kTile * kChans;
+  const int rank = blockIdx.x % k, c0 = blockIdx.x / k * kChans, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (k > 1) cluster_arrive();  // every block of the cluster has started before another stores to it
+
+  // this thread's copies
+  using Copy = Copier<IO, kThreads>;
+  const int cc = c0 + Copy::group();
+  const bool copies = cc < p.C;
+  const Place at(copies ? cc : 0, p.H, p.D);
+  const IO* const sx = reinterpret_cast<const IO*>(p.x.p) + at.of(p.x);
+  const IO* const sg = reinterpret_cast<const IO*>(p.g.p) + at.of(p.g);
+  const IO* const si = reinterpret_cast<const IO*>(p.i.p) + (GATE ? at.of(p.i) : 0);
+  auto fetch = [&](long long step) {
+    const long long first = (step * k + rank) * kTile;
+    const int t0 = (int)(first < p.T ? first : p.T);
+    if (copies) {
+      Copy::tile(tile, sx, p.x.st, t0, p.T, 0);
+      Copy::tile(tile + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
+      if (GATE) Copy::tile(tile + 2 * S, si, p.i.st, t0, p.T, 0);
+    }
+    cp_async_commit();
+  };
+
+  // this lane's channels
+  const int c = c0 + 2 * lane;
+  const bool live = c < p.C;
+  const Place my(live ? c : 0, p.H, p.D);
+  IO* const y = p.y.p ? reinterpret_cast<IO*>(p.y.p) + my.of(p.y) : nullptr;
+  f2 rate = 0, h = 0;  // h: the state before the step's tokens
+  if (DECAY == kRecRate && live)
+    rate = f2_mul(*reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d), f2_both(-1.f));
+  if (p.h0 && live) h = *reinterpret_cast<const f2*>(p.h0 + c);
+  // rates too small for a decay far from 1 (the same lanes in every warp, so all the block's warps agree)
+  const bool near = DECAY == kRecRate && __all_sync(~0u, fabsf(f2_lo(rate)) < kNear && fabsf(f2_hi(rate)) < kNear);
+
+  const long long steps = ((long long)p.T + kTile * k - 1) / (kTile * k);
+  fetch(0);
+  for (long long step = 0; step < steps; ++step) {
+    cp_async_wait<0>();
+    __syncthreads();
+    f2 P[kTok], Y[kTok];
+    const IO* const mine = tile + w * kTok * kChans + 2 * lane;
+    Map m;
+    if (near) m = segment<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(mine, rate, P, Y);
+    else m = segment<IO, DECAY, SCALE, GATE, false>(mine, rate, P, Y);
+    maps[w][0][lane] = m.A, maps[w][1][lane] = m.Al, maps[w][2][lane] = m.S;
+    __syncthreads();
+    if (step + 1 < steps) fetch(step + 1);
+    f2 next = h;
+    if (k > 1) {  // the block's map to every block of the cluster
+      BlockMap* const half = blocks + (step & 1) * k;
+      if (step == 0) cluster_wait();
+      if (w == 0) {
+#pragma unroll
+        for (int v = 1; v < kWarps; ++v) {
+          const f2 A = maps[v][0][lane], Al = maps[v][1][lane];
+          m.S = apply(A, Al, maps[v][2][lane], m.S);
+          lengthen(m.A, m.Al, A, Al);
+        }
+        for (int r = 0; r < k; ++r) {
+          put_remote(&half[rank].A[lane], r, m.A);
+          put_remote(&half[rank].Al[lane], r, m.Al);
+          put_remote(&half[rank].S[lane], r, m.S);
+        }
+      }
+      cluster_arrive();
+      cluster_wait();
+      for (int r = 0; r < k; ++r) {
+        if (r == rank) h = next;
+        next = apply(half[r].A[lane], half[r].Al[lane], half[r].S[lane], next);
+      }
+    }
+    const long long first = (step * k + rank) * kTile;
+    if (p.ckpt && w == 0 && live && first < p.T) *reinterpret_cast<f2*>(p.ckpt + first / kTile * p.C + c) = h;
+    f2 mystart = h;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) {
+      if (v == w) mystart = h;
+      if (k == 1 || v < w) h = apply(maps[v][0][lane], maps[v][1][lane], maps[v][2][lane], h);
+    }
+    if (k > 1) h = next;
+    if (live && y) {
+      const long long t0 = first + w * kTok;
+      IO* out = y + t0 * p.y.st;
+      if (t0 + kTok <= p.T) {
+#pragma unroll
+        for (int j = 0; j < kTok; ++j, out += p.y.st) put_pair(out, f2_fma(P[j], mystart, Y[j]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kTok; ++j, out += p.y.st)
+          if (t0 + j < p.T) put_pair(out, f2_fma(P[j], mystart, Y[j]));
+      }
+    }
+  }
+  if (p.hT && live && rank == 0 && w == 0) *reinterpret_cast<f2*>(p.hT + c) = h;
+}
+
+// One token: a thread takes two channels.
+template <typename IO, int DECAY, int SCALE, bool GATE>
+__global__ void __launch_bounds__(128) kla_recurrence_step_kernel(const RecArgs p) {
+  const int c = 2 * (blockIdx.x * 128 + threadIdx.x);
+  if (c >= p.C) return;
+  const f2 h = *reinterpret_cast<const f2*>(p.h0 + c);
+  f2 x = pair_at<IO>(reinterpret_cast<const IO*>(p.x.p) + c), rate = 0;
+  if (DECAY == kRecRate) rate = f2_mul(*reinterpret_cast<const f2*>(p.rate + c % (p.H * p.D)), f2_both(-1.f));
+  const Decay a = decay_of<DECAY, SCALE, false>(pair_at<IO>(reinterpret_cast<const IO*>(p.g.p) + c), rate);
+  x = scaled<SCALE>(x, a.less);
+  if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(reinterpret_cast<const IO*>(p.i.p) + c)), f2_both(1.f))));
+  const f2 next = apply(a.hi, a.lo, x, h);
+  *reinterpret_cast<f2*>(p.hT + c) = next;
+  put_pair(reinterpret_cast<IO*>(p.y.p) + c, next);
+}
+
+// Calls f with the compile-time kinds of a call.
+template <typename F>
+inline cudaError_t by_kind(const RecArgs& a, F f) {
+  using std::integral_constant;
+  auto gate = [&](auto d, auto s) { return a.i.p ? f(d, s, std::true_type()) : f(d, s, std::false_type()); };
+  auto scale = [&](auto d) {
+    if (a.scale == kRecSqrt) return gate(d, integral_constant<int, kRecSqrt>());
+    if (a.scale == kRecComplement) return gate(d, integral_constant<int, kRecComplement>());
+    return gate(d, integral_constant<int, kRecPlain>());
+  };
+  if (a.decay == kRecSigmoid) return scale(integral_constant<int, kRecSigmoid>());
+  if (a.decay == kRecRate) return scale(integral_constant<int, kRecRate>());
+  return scale(integral_constant<int, kRecLog>());
+}
+
+}  // namespace rec
+
+template <typename IO>
+cudaError_t launch_recurrence_io(const RecArgs& a, int num_sms, cudaStream_t s) {
+  const int tiles = (a.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, a.T, num_sms * (sizeof(IO) == 2 ? 5 : 3));
+  const size_t smem = rec::block_maps_bytes(k) + (a.i.p ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
+  return rec::by_kind(a, [&](auto d, auto sc, auto gate) {
+    return rec::launch_rec_cluster(rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
+                                   a, tiles, k, rec::kThreads, smem, s);
+  });
+}
+
+template <typename IO>
+cudaError_t launch_recurrence_step_io(const RecArgs& a, cudaStream_t s) {
+  const unsigned blocks = (unsigned)((a.C + 255) / 256);
+  return rec::by_kind(a, [&](auto d, auto sc, auto gate) {
+    rec::kla_recurrence_step_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value><<<blocks, 128, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace kla
