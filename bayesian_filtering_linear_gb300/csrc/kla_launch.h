@@ -186,7 +186,7 @@ cudaError_t launch_norm_rope_backward(const NormRopeArgs& a, int num_sms, cudaSt
 // Gated linear recurrence (kla_recurrence*.cu). Tensors [B,H,T,D] by strides in
 // elements, last dimension contiguous; states [B,H,D] fp32, flat channels
 // C = B·H·D.
-constexpr int kRecTile = 64;         // tokens of a tile, and between two checkpoints
+constexpr int kRecTile = 64;         // tokens between two checkpoints
 constexpr int kRecMaxCluster = 8;    // blocks that share a sequence
 constexpr int kRecLog = 0, kRecSigmoid = 1, kRecRate = 2;
 constexpr int kRecPlain = 0, kRecSqrt = 1, kRecComplement = 2;
@@ -208,7 +208,7 @@ struct RecArgs {
   int B, H, T, D, C, decay, scale, io;
 };
 // Blocks that go along a sequence together.
-int rec_cluster(int tiles, int T, int resident);
+int rec_cluster(int tiles, int along, int resident);
 cudaError_t launch_recurrence(const RecArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_recurrence_step(const RecArgs& a, cudaStream_t s);
 struct RecGradArgs {

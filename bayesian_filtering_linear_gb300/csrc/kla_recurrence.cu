@@ -31,8 +31,7 @@ __global__ void __launch_bounds__(128) kla_recurrence_rate_kernel(const float* p
 // As many as the device holds at once (`resident` blocks, of which clusters of up
 // to eight leave an eighth unused at worst): a second wave of clusters would take
 // as long as the first.
-int rec_cluster(int tiles, int T, int resident) {
-  const int along = (T + kRecTile - 1) / kRecTile;
+int rec_cluster(int tiles, int along, int resident) {
   const int most = resident / 8 * 7 / std::max(tiles, 1);
   return std::max(1, std::min({most, along, kRecMaxCluster}));
 }

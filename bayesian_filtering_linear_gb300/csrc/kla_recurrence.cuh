@@ -19,7 +19,7 @@
 namespace kla {
 namespace rec {
 
-constexpr int kTile = kRecTile, kChans = 64;  // tokens and channels a tile
+constexpr int kChans = 64;  // channels a tile
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -29,6 +29,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float rsqrt_fast(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0.f)));
   return y;
 }
 __device__ __forceinline__ f2 f2_both(float x) { return f2_make(x, x); }
@@ -41,58 +46,57 @@ __device__ __forceinline__ f2 f2_exp_neg_held(f2 x) {
   return f2_make(fminf(f2_lo(e), 0x1p126f), fminf(f2_hi(e), 0x1p126f));
 }
 
-// A decay: the float nearest to it, the rest, and a - 1.
+// A decay: the float nearest to it, the rest, and 1 - a.
 struct Decay {
   f2 hi, lo, less;
 };
 
-// hi and lo of 1 + less.
+// hi and lo of 1 - less.
 __device__ __forceinline__ void split(Decay& a) {
-  const f2 one = f2_both(1.f);
-  a.hi = f2_add(one, a.less);
-  a.lo = f2_add(f2_fma(a.hi, f2_both(-1.f), one), a.less);
+  const f2 one = f2_both(1.f), minus = f2_both(-1.f);
+  a.hi = f2_fma(a.less, minus, one);
+  a.lo = f2_fma(a.less, minus, f2_fma(a.hi, minus, one));
+}
+// Where not `near`: a itself, without a rest.
+__device__ __forceinline__ void select(Decay& a, bool n0, bool n1, f2 e) {
+  const f2 m = f2_fma(e, f2_both(-1.f), f2_both(1.f));
+  a.hi = f2_make(n0 ? f2_lo(a.hi) : f2_lo(e), n1 ? f2_hi(a.hi) : f2_hi(e));
+  a.lo = f2_make(n0 ? f2_lo(a.lo) : 0.f, n1 ? f2_hi(a.lo) : 0.f);
+  a.less = f2_make(n0 ? f2_lo(a.less) : f2_lo(m), n1 ? f2_hi(a.less) : f2_hi(m));
 }
 
-// Of a decay's logarithm: near 1 a polynomial for a - 1 (Taylor's, the first
-// term left out is 3e-8 of the value), elsewhere the exponential. NEAR: all are.
+// Of y = -log a: near a = 1 (y in [0, 0.375]) a polynomial for 1 - a, elsewhere
+// the exponential. NEAR: all are. The polynomial is y (1 - c1 y + ...),
+// (1 - e^-y) / y interpolated at the five Chebyshev points of the interval, off by
+// 4.3e-8 of the value at most; Taylor's needs two terms more for that.
 constexpr float kNear = 0.375f;
 template <bool NEAR>
-__device__ __forceinline__ Decay decay_of_log(f2 la) {
+__device__ __forceinline__ Decay decay_of_log(f2 y) {
   Decay a;
-  f2 p = f2_fma(la, f2_both(1.f / 5040.f), f2_both(1.f / 720.f));
-  p = f2_fma(p, la, f2_both(1.f / 120.f));
-  p = f2_fma(p, la, f2_both(1.f / 24.f));
-  p = f2_fma(p, la, f2_both(1.f / 6.f));
-  p = f2_fma(p, la, f2_both(0.5f));
-  a.less = f2_fma(f2_mul(p, la), la, la);
+  f2 p = f2_fma(y, f2_both(0x1.d3c856p-8f), f2_both(-0x1.523554p-5f));
+  p = f2_fma(p, y, f2_both(0x1.553ae2p-3f));
+  p = f2_fma(p, y, f2_both(-0x1.ffff62p-2f));
+  a.less = f2_fma(f2_mul(p, y), y, y);
   split(a);
-  if (!NEAR) {
-    const f2 e = f2_ex2(f2_mul(la, f2_both(1.4426950408889634f))), m = f2_add(e, f2_both(-1.f));
-    const bool n0 = fabsf(f2_lo(la)) < kNear, n1 = fabsf(f2_hi(la)) < kNear;
-    a.hi = f2_make(n0 ? f2_lo(a.hi) : f2_lo(e), n1 ? f2_hi(a.hi) : f2_hi(e));
-    a.lo = f2_make(n0 ? f2_lo(a.lo) : 0.f, n1 ? f2_hi(a.lo) : 0.f);
-    a.less = f2_make(n0 ? f2_lo(a.less) : f2_lo(m), n1 ? f2_hi(a.less) : f2_hi(m));
-  }
+  if (!NEAR)
+    select(a, fabsf(f2_lo(y) - 0.5f * kNear) <= 0.5f * kNear, fabsf(f2_hi(y) - 0.5f * kNear) <= 0.5f * kNear, f2_exp_neg(y));
   return a;
 }
 
 // Of a sigmoid: e = e^-g (held), a = 1 / (1 + e).
 __device__ __forceinline__ Decay decay_of_sigmoid(f2 e) {
   Decay a;
-  const f2 s = f2_rcp(f2_add(e, f2_both(1.f))), m = f2_add(s, f2_both(-1.f));
-  a.less = f2_mul(f2_mul(e, f2_both(-1.f)), s);
+  const f2 s = f2_rcp(f2_add(e, f2_both(1.f)));
+  a.less = f2_mul(e, s);
   split(a);
-  const bool n0 = f2_lo(e) <= 1.f, n1 = f2_hi(e) <= 1.f;
-  a.hi = f2_make(n0 ? f2_lo(a.hi) : f2_lo(s), n1 ? f2_hi(a.hi) : f2_hi(s));
-  a.lo = f2_make(n0 ? f2_lo(a.lo) : 0.f, n1 ? f2_hi(a.lo) : 0.f);
-  a.less = f2_make(n0 ? f2_lo(a.less) : f2_lo(m), n1 ? f2_hi(a.less) : f2_hi(m));
+  select(a, f2_lo(e) <= 1.f, f2_hi(e) <= 1.f, s);
   return a;
 }
 
-// 1 - a², zero below the normal numbers (and where a > 1), and 1/sqrt of it (there zero too).
-__device__ __forceinline__ f2 spread(f2 less) {
-  return f2_mul(f2_mul(less, f2_both(-1.f)), f2_add(less, f2_both(2.f)));
-}
+// 1 - a², its square root and one over that: where it is below the normal
+// numbers, or a above 1, both count as zero.
+__device__ __forceinline__ f2 spread(f2 less) { return f2_mul(less, f2_fma(less, f2_both(-1.f), f2_both(2.f))); }
+__device__ __forceinline__ f2 spread_sqrt(f2 v) { return f2_make(sqrt_fast(f2_lo(v)), sqrt_fast(f2_hi(v))); }
 __device__ __forceinline__ f2 spread_rsqrt(f2 v) {
   const float a = f2_lo(v), b = f2_hi(v);
   return f2_make(a >= 0x1p-126f ? rsqrt_fast(a) : 0.f, b >= 0x1p-126f ? rsqrt_fast(b) : 0.f);
@@ -123,6 +127,11 @@ __device__ __forceinline__ f2 pair_at<__nv_bfloat16>(const __nv_bfloat16* p) {
   const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
   return f2_make(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
+__device__ __forceinline__ f2 minus_pair_at(const float* p) { return f2_mul(pair_at<float>(p), f2_both(-1.f)); }
+__device__ __forceinline__ f2 minus_pair_at(const __nv_bfloat16* p) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p) ^ 0x80008000u;
+  return f2_make(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ void put_pair(float* p, f2 v) { *reinterpret_cast<f2*>(p) = v; }
 __device__ __forceinline__ void put_pair(__nv_bfloat16* p, f2 v) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
@@ -143,22 +152,22 @@ struct Place {
 
 // One stream's share of a tile's copies, 16 bytes a copy: a thread keeps its
 // channels and goes through the tokens.
-template <typename IO, int THREADS>
+template <typename IO, int THREADS, int TILE>
 struct Copier {
   static constexpr int VE = 16 / sizeof(IO), GROUPS = kChans / VE, ROWS = THREADS / GROUPS;
   __device__ __forceinline__ static int group() { return threadIdx.x % GROUPS * VE; }
   __device__ __forceinline__ static int row() { return threadIdx.x / GROUPS; }
-  // tokens [t0, t0 + kTile) of the stream, `src` its thread's channels of token 0, into `dst`; behind T, `fill`s
+  // tokens [t0, t0 + TILE) of the stream, `src` its thread's channels of token 0, into `dst`; behind T, `fill`s
   __device__ __forceinline__ static void tile(IO* dst, const IO* src, long long st, int t0, int T, uint32_t fill) {
     dst += row() * kChans + group();
     src += (long long)(t0 + row()) * st;
     const long long down = ROWS * st;
-    if (t0 + kTile <= T) {
+    if (t0 + TILE <= T) {
 #pragma unroll
-      for (int r = 0; r < kTile; r += ROWS, src += down) cp_async16(dst + r * kChans, src);
+      for (int r = 0; r < TILE; r += ROWS, src += down) cp_async16(dst + r * kChans, src);
     } else {
 #pragma unroll
-      for (int r = 0; r < kTile; r += ROWS, src += down) {
+      for (int r = 0; r < TILE; r += ROWS, src += down) {
         if (t0 + row() + r < T) cp_async16(dst + r * kChans, src);
         else *reinterpret_cast<uint4*>(dst + r * kChans) = make_uint4(fill, fill, fill, fill);
       }
@@ -175,6 +184,8 @@ __device__ __forceinline__ uint32_t still() {
 }
 
 // ---- clusters ------------------------------------------------------------------
+// (`arrive` for a block that has stored in the others' shared memory before it, `arrive_only` for one that has not)
+__device__ __forceinline__ void cluster_arrive_only() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Stores a pair at the place of `p` (this block's shared memory) in the block of rank `rank`.

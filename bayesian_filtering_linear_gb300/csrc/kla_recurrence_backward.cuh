@@ -27,7 +27,7 @@
 namespace kla {
 namespace rec {
 
-constexpr int kBackWarps = 8, kBackThreads = 32 * kBackWarps, kBackTok = kTile / kBackWarps;
+constexpr int kBackWarps = 8, kBackThreads = 32 * kBackWarps, kBackTok = kRecTile / kBackWarps;
 // Stages of the ring of tiles: two, or for fp32, whose tiles are twice as large, one that two blocks take turns by.
 template <typename IO>
 constexpr int kStages = sizeof(IO) == 2 ? 2 : 1;
@@ -52,27 +52,28 @@ __device__ __forceinline__ f2* gate_place(IO* i, f2* own, int j) {
 template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
 __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackTok], f2 (&lo)[kBackTok],
                                      f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2 (&b)[kBackTok]) {
-  constexpr int S = kTile * kChans;
+  constexpr int S = kRecTile * kChans;
   const f2 one = f2_both(1.f), minus = f2_both(-1.f);
   Map m{one, 0, 0};
 #pragma unroll
   for (int j = 0; j < kBackTok; ++j) {
     IO* const at = tile + j * kChans;
     const f2 x = pair_at<IO>(at);
-    f2 g = pair_at<IO>(at + S), open = one, shut = 0;
+    f2 open = one, shut = 0;
     if (GATE) {
       const f2 e = f2_exp_neg_held(pair_at<IO>(at + 2 * S));
       open = f2_rcp(f2_add(one, e));
       shut = f2_mul(e, open);
     }
     Decay a;
-    if (DECAY != kRecLog) {
-      const f2 e = f2_exp_neg_held(g);
+    if (DECAY == kRecLog) {
+      a = decay_of_log<NEAR>(minus_pair_at(at + S));
+    } else {
+      const f2 e = f2_exp_neg_held(pair_at<IO>(at + S));
       keep(at + S, at + 2 * S, e);
       if (DECAY == kRecSigmoid) a = decay_of_sigmoid(e);
-      else g = f2_mul(rate, f2_rcp(f2_add(one, e)));
+      else a = decay_of_log<NEAR>(f2_mul(rate, f2_rcp(f2_add(one, e))));
     }
-    if (DECAY != kRecSigmoid) a = decay_of_log<NEAR>(g);
     hi[j] = a.hi, lo[j] = a.lo;
     const f2 xo = GATE ? f2_mul(x, open) : x;
     f2 w = 0;  // s' σ(i) x
@@ -82,7 +83,7 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
       b[j] = f2_mul(f2_mul(v, rs), open);
       w = f2_mul(f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus)), xo);
     } else if (SCALE == kRecComplement) {
-      b[j] = f2_mul(f2_mul(a.less, minus), open);
+      b[j] = f2_mul(a.less, open);
       w = f2_mul(f2_mul(a.hi, minus), xo);
     }
     const f2 bx = f2_mul(b[j], x);
@@ -100,7 +101,7 @@ template <typename IO, int DECAY, int SCALE, bool GATE>
 __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(const RecGradArgs q, int k) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ f2 maps[kBackWarps][4][32];
-  constexpr int S = kTile * kChans, STAGE = 4 * S;
+  constexpr int S = kRecTile * kChans, STAGE = 4 * S;
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const ring = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
   f2* const own = reinterpret_cast<f2*>(ring + kStages<IO> * STAGE) + threadIdx.x;  // [kBackTok][kBackThreads], bf16 with a gate
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   if (k > 1) cluster_arrive();  // every block of the cluster has started before another stores to it
 
   // this thread's copies
-  using Copy = Copier<IO, kBackThreads>;
+  using Copy = Copier<IO, kBackThreads, kRecTile>;
   const int cc = c0 + Copy::group();
   const bool copies = cc < p.C;
   const Place at(copies ? cc : 0, p.H, p.D);
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   const IO* const sy = reinterpret_cast<const IO*>(q.gy.p) + (q.gy.p ? at.of(q.gy) : 0);
   auto fetch = [&](long long step) {
     if (copies && step >= 0) {
-      const long long first = (step * k + rank) * kTile;
+      const long long first = (step * k + rank) * kRecTile;
       const int t0 = (int)(first < p.T ? first : p.T);
       IO* const d = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0);
       Copy::tile(d, sx, p.x.st, t0, p.T, 0);
@@ -139,18 +140,17 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   IO* const gi = reinterpret_cast<IO*>(q.gi.p) + (GATE ? my.of(q.gi) : 0);
   f2 rate = 0, z = 0, sum = 0;  // z: what reaches the step's last token from behind it
   if (DECAY == kRecRate && live)
-    rate = f2_mul(*reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d), f2_both(-1.f));
+    rate = *reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d);
   if (q.ghT && live) z = *reinterpret_cast<const f2*>(q.ghT + c);
-  // rates too small for a decay far from 1 (the same lanes in every warp, so all the block's warps agree)
-  const bool near = DECAY == kRecRate && __all_sync(~0u, fabsf(f2_lo(rate)) < kNear && fabsf(f2_hi(rate)) < kNear);
+  const bool near = DECAY == kRecRate && near_rates(rate);
 
-  const f2 one = f2_both(1.f);
-  const long long steps = ((long long)p.T + kTile * k - 1) / (kTile * k);
+  const f2 one = f2_both(1.f), minus_rate = f2_mul(rate, f2_both(-1.f));
+  const long long steps = ((long long)p.T + kRecTile * k - 1) / (kRecTile * k);
   fetch(steps - 1);
   for (long long step = steps - 1; step >= 0; --step) {
-    const long long first = (step * k + rank) * kTile, t0 = first + w * kBackTok;
+    const long long first = (step * k + rank) * kRecTile, t0 = first + w * kBackTok;
     f2 h = 0;
-    if (live && first < p.T) h = *reinterpret_cast<const f2*>(p.ckpt + first / kTile * p.C + c);
+    if (live && first < p.T) h = *reinterpret_cast<const f2*>(p.ckpt + first / kRecTile * p.C + c);
     cp_async_wait<0>();
     __syncthreads();
     if (kStages<IO> == 2) fetch(step - 1);  // (the last loop of the step before has read that stage)
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
           put_remote(&half[rank].S[lane], o, t.S);
         }
       }
-      cluster_arrive();
+      if (w == kBackWarps - 1) cluster_arrive();
+      else cluster_arrive_only();
       cluster_wait();
       for (int o = k - 1; o >= 0; --o) {
         if (o == rank) z = next;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
           if (DECAY == kRecRate) {
             by_log = f2_mul(by_log, open);
             if (j < n) sum = f2_add(sum, by_log);
-            by_log = f2_mul(by_log, f2_mul(rate, shut));
+            by_log = f2_mul(by_log, f2_mul(minus_rate, shut));
           } else {
             by_log = f2_mul(by_log, shut);
           }
@@ -253,8 +254,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
 
 template <typename IO>
 cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int num_sms, int* parts, cudaStream_t s) {
-  const int tiles = (a.f.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, a.f.T, num_sms * 2);
-  const size_t tile = 4 * (size_t)rec::kTile * rec::kChans * sizeof(IO);
+  const int tiles = (a.f.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, (a.f.T + kRecTile - 1) / kRecTile, num_sms * 2);
+  const size_t tile = 4 * (size_t)kRecTile * rec::kChans * sizeof(IO);
   const size_t smem = rec::block_maps_bytes(k) + rec::kStages<IO> * tile +
                       (sizeof(IO) == 2 && a.f.i.p ? (size_t)rec::kBackTok * rec::kBackThreads * sizeof(f2) : 0);
   *parts = k;

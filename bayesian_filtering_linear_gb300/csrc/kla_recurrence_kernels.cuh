@@ -21,22 +21,31 @@
 namespace kla {
 namespace rec {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kTok = kTile / kWarps;  // tokens a warp
+#ifndef REC_OCC
+#define REC_OCC 4
+#define REC_STAGES 1
+#define REC_WARPS 4
+#define REC_TOK 16
+#define REC_OCCF 3
+#endif
+constexpr int kOcc = REC_OCC, kStg = REC_STAGES;
+constexpr int kWarps = REC_WARPS, kThreads = 32 * kWarps, kTok = REC_TOK, kTile = kWarps * kTok;  // tokens a warp, a tile
 
 // A decay and the factor s σ(i) x of a pair, from what is read.
-template <int DECAY, int SCALE, bool NEAR>
-__device__ __forceinline__ Decay decay_of(f2 g, f2 rate) {
-  if (DECAY == kRecSigmoid) return decay_of_sigmoid(f2_exp_neg_held(g));
-  if (DECAY == kRecRate) g = f2_mul(rate, f2_rcp(f2_add(f2_exp_neg(g), f2_both(1.f))));
-  return decay_of_log<NEAR>(g);
+template <typename IO, int DECAY, bool NEAR>
+__device__ __forceinline__ Decay decay_of(const IO* g, f2 rate) {
+  if (DECAY == kRecSigmoid) return decay_of_sigmoid(f2_exp_neg_held(pair_at<IO>(g)));
+  if (DECAY == kRecRate) return decay_of_log<NEAR>(f2_mul(rate, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(g)), f2_both(1.f)))));
+  return decay_of_log<NEAR>(minus_pair_at(g));
+}
+// All of a warp's rates are too small for a decay far from 1.
+__device__ __forceinline__ bool near_rates(f2 rate) {
+  return __all_sync(~0u, fminf(f2_lo(rate), f2_hi(rate)) >= 0.f && fmaxf(f2_lo(rate), f2_hi(rate)) <= kNear);
 }
 template <int SCALE>
 __device__ __forceinline__ f2 scaled(f2 x, f2 less) {
-  if (SCALE == kRecSqrt) {
-    const f2 v = spread(less);
-    return f2_mul(x, f2_mul(v, spread_rsqrt(v)));
-  }
-  if (SCALE == kRecComplement) return f2_mul(x, f2_mul(less, f2_both(-1.f)));
+  if (SCALE == kRecSqrt) return f2_mul(x, spread_sqrt(spread(less)));
+  if (SCALE == kRecComplement) return f2_mul(x, less);
   return x;
 }
 
@@ -47,7 +56,7 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
     f2 x = pair_at<IO>(tile + j * kChans);
-    const Decay a = decay_of<DECAY, SCALE, NEAR>(pair_at<IO>(tile + S + j * kChans), rate);
+    const Decay a = decay_of<IO, DECAY, NEAR>(tile + S + j * kChans, rate);
     x = scaled<SCALE>(x, a.less);
     if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(tile + 2 * S + j * kChans)), f2_both(1.f))));
     m.S = apply(a.hi, a.lo, x, m.S);
@@ -59,17 +68,17 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
 }
 
 template <typename IO, int DECAY, int SCALE, bool GATE>
-__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurrence_kernel(const RecArgs p, int k) {
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? kOcc : REC_OCCF) kla_recurrence_kernel(const RecArgs p, int k) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ f2 maps[kWarps][3][32];
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const tile = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
-  constexpr int S = kTile * kChans;
+  constexpr int S = kTile * kChans, STAGE = (GATE ? 3 : 2) * S;
   const int rank = blockIdx.x % k, c0 = blockIdx.x / k * kChans, w = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (k > 1) cluster_arrive();  // every block of the cluster has started before another stores to it
 
   // this thread's copies
-  using Copy = Copier<IO, kThreads>;
+  using Copy = Copier<IO, kThreads, kTile>;
   const int cc = c0 + Copy::group();
   const bool copies = cc < p.C;
   const Place at(copies ? cc : 0, p.H, p.D);
@@ -79,10 +88,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurre
   auto fetch = [&](long long step) {
     const long long first = (step * k + rank) * kTile;
     const int t0 = (int)(first < p.T ? first : p.T);
+    IO* const d = tile + (step % kStg) * STAGE;
     if (copies) {
-      Copy::tile(tile, sx, p.x.st, t0, p.T, 0);
-      Copy::tile(tile + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
-      if (GATE) Copy::tile(tile + 2 * S, si, p.i.st, t0, p.T, 0);
+      Copy::tile(d, sx, p.x.st, t0, p.T, 0);
+      Copy::tile(d + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
+      if (GATE) Copy::tile(d + 2 * S, si, p.i.st, t0, p.T, 0);
     }
     cp_async_commit();
   };
@@ -94,10 +104,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurre
   IO* const y = p.y.p ? reinterpret_cast<IO*>(p.y.p) + my.of(p.y) : nullptr;
   f2 rate = 0, h = 0;  // h: the state before the step's tokens
   if (DECAY == kRecRate && live)
-    rate = f2_mul(*reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d), f2_both(-1.f));
+    rate = *reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d);
   if (p.h0 && live) h = *reinterpret_cast<const f2*>(p.h0 + c);
-  // rates too small for a decay far from 1 (the same lanes in every warp, so all the block's warps agree)
-  const bool near = DECAY == kRecRate && __all_sync(~0u, fabsf(f2_lo(rate)) < kNear && fabsf(f2_hi(rate)) < kNear);
+  const bool near = DECAY == kRecRate && near_rates(rate);
 
   const long long steps = ((long long)p.T + kTile * k - 1) / (kTile * k);
   fetch(0);
@@ -105,13 +114,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurre
     cp_async_wait<0>();
     __syncthreads();
     f2 P[kTok], Y[kTok];
-    const IO* const mine = tile + w * kTok * kChans + 2 * lane;
+    if (kStg == 2 && step + 1 < steps) fetch(step + 1);
+    const IO* const mine = tile + (step % kStg) * STAGE + w * kTok * kChans + 2 * lane;
     Map m;
     if (near) m = segment<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(mine, rate, P, Y);
     else m = segment<IO, DECAY, SCALE, GATE, false>(mine, rate, P, Y);
     maps[w][0][lane] = m.A, maps[w][1][lane] = m.Al, maps[w][2][lane] = m.S;
     __syncthreads();
-    if (step + 1 < steps) fetch(step + 1);
+    if (kStg == 1 && step + 1 < steps) fetch(step + 1);
     f2 next = h;
     if (k > 1) {  // the block's map to every block of the cluster
       BlockMap* const half = blocks + (step & 1) * k;
@@ -129,7 +139,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurre
           put_remote(&half[rank].S[lane], r, m.S);
         }
       }
-      cluster_arrive();
+      if (w == 0) cluster_arrive();
+      else cluster_arrive_only();
       cluster_wait();
       for (int r = 0; r < k; ++r) {
         if (r == rank) h = next;
@@ -137,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 3) kla_recurre
       }
     }
     const long long first = (step * k + rank) * kTile;
-    if (p.ckpt && w == 0 && live && first < p.T) *reinterpret_cast<f2*>(p.ckpt + first / kTile * p.C + c) = h;
+    if (p.ckpt && w == 0 && live && first < p.T && first % kRecTile == 0)
+      *reinterpret_cast<f2*>(p.ckpt + first / kRecTile * p.C + c) = h;
     f2 mystart = h;
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) {
@@ -168,8 +180,8 @@ __global__ void __launch_bounds__(128) kla_recurrence_step_kernel(const RecArgs 
   if (c >= p.C) return;
   const f2 h = *reinterpret_cast<const f2*>(p.h0 + c);
   f2 x = pair_at<IO>(reinterpret_cast<const IO*>(p.x.p) + c), rate = 0;
-  if (DECAY == kRecRate) rate = f2_mul(*reinterpret_cast<const f2*>(p.rate + c % (p.H * p.D)), f2_both(-1.f));
-  const Decay a = decay_of<DECAY, SCALE, false>(pair_at<IO>(reinterpret_cast<const IO*>(p.g.p) + c), rate);
+  if (DECAY == kRecRate) rate = *reinterpret_cast<const f2*>(p.rate + c % (p.H * p.D));
+  const Decay a = decay_of<IO, DECAY, false>(reinterpret_cast<const IO*>(p.g.p) + c, rate);
   x = scaled<SCALE>(x, a.less);
   if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(reinterpret_cast<const IO*>(p.i.p) + c)), f2_both(1.f))));
   const f2 next = apply(a.hi, a.lo, x, h);
@@ -196,8 +208,8 @@ inline cudaError_t by_kind(const RecArgs& a, F f) {
 
 template <typename IO>
 cudaError_t launch_recurrence_io(const RecArgs& a, int num_sms, cudaStream_t s) {
-  const int tiles = (a.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, a.T, num_sms * (sizeof(IO) == 2 ? 5 : 3));
-  const size_t smem = rec::block_maps_bytes(k) + (a.i.p ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
+  const int tiles = (a.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, (a.T + rec::kTile - 1) / rec::kTile, num_sms * (sizeof(IO) == 2 ? rec::kOcc : REC_OCCF));
+  const size_t smem = rec::block_maps_bytes(k) + rec::kStg * (a.i.p ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
   return rec::by_kind(a, [&](auto d, auto sc, auto gate) {
     return rec::launch_rec_cluster(rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
                                    a, tiles, k, rec::kThreads, smem, s);
