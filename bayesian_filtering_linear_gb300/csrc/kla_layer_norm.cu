@@ -20,8 +20,6 @@ namespace kla {
 
 namespace {
 
-constexpr int kThreads = 256;
-
 // VEC elements of a row as they lie in memory.
 template <typename IO, int VEC>
 struct Raw;
@@ -56,20 +54,57 @@ struct Raw<IO, 1> {
   __device__ __forceinline__ void from(const float (&x)[1]) { v = from_f32<IO>(x[0]); }
 };
 
-// A row over LANES lanes: lane l holds the NV pieces of VEC elements that begin
-// at (l + LANES j) VEC. LANES is 8 or 32 (lanes of a warp) or 256 (the block).
-template <int LANES>
-__device__ __forceinline__ float row_sum(float x, float* space) {
+// VEC floats of the weight or the bias.
+template <int VEC>
+__device__ __forceinline__ void params(const float* p, float (&w)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
 #pragma unroll
-  for (int m = 1; m < (LANES < 32 ? LANES : 32); m <<= 1) x += __shfl_xor_sync(~0u, x, m);
-  if (LANES > 32) {
-    if (threadIdx.x % 32 == 0) space[threadIdx.x / 32] = x;
-    __syncthreads();
-    x = 0.f;
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else {
 #pragma unroll
-    for (int i = 0; i < LANES / 32; ++i) x += space[i];
+    for (int i = 0; i < VEC; ++i) w[i] = p[i];
   }
-  return x;
+}
+
+// A row over LANES lanes: lane l holds the NV pieces of VEC elements that begin
+// at (l + LANES j) VEC. LANES is 8 or 32 (lanes of a warp), or some warps of the
+// block, its part `grp`. Sums N values over a row; `space`: N floats for
+// each of the row's warps, others at the next call.
+template <int LANES, int THREADS, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float* space, int grp) {
+  static_assert(N == 1 || N == 2, "one sum or two");
+  constexpr int W = LANES < 32 ? LANES : 32;
+  if constexpr (N == 2) {  // even lanes go on with one sum, odd lanes with the other
+    const bool odd = threadIdx.x & 1;
+    const float other = __shfl_xor_sync(~0u, odd ? x[0] : x[1], 1);
+    float s = (odd ? x[1] : x[0]) + other;
+#pragma unroll
+    for (int m = 2; m < W; m <<= 1) s += __shfl_xor_sync(~0u, s, m);
+    if constexpr (LANES > 32) {
+      if (threadIdx.x % 32 < 2) space[threadIdx.x % LANES / 32 * 2 + threadIdx.x % 32] = s;
+    } else {
+      const float t = __shfl_xor_sync(~0u, s, 1);
+      x[0] = odd ? t : s, x[1] = odd ? s : t;
+    }
+  } else {
+#pragma unroll
+    for (int m = 1; m < W; m <<= 1) x[0] += __shfl_xor_sync(~0u, x[0], m);
+    if constexpr (LANES > 32)
+      if (threadIdx.x % 32 == 0) space[threadIdx.x % LANES / 32] = x[0];
+  }
+  if constexpr (LANES > 32) {
+    if (LANES == THREADS) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "n"(LANES) : "memory");
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      x[n] = space[n];
+#pragma unroll
+      for (int i = 1; i < LANES / 32; ++i) x[n] += space[i * N + n];
+    }
+  }
 }
 
 template <typename IO, int VEC, int NV>
@@ -81,41 +116,15 @@ __device__ __forceinline__ void fetch(Raw<IO, VEC> (&r)[NV], const IO* row, int 
   }
 }
 
-// x becomes the normalised row (zero behind its end); returns r. `space`: 16 floats a call.
-template <int VEC, int NV, int LANES>
-__device__ __forceinline__ float standardise(float (&x)[NV][VEC], int l, int D, float inv_d, float eps, float* space) {
-  float s = 0.f, v = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) s += x[j][i];
-  const float mean = row_sum<LANES>(s, space) * inv_d;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const bool in = (l + LANES * j) * VEC < D;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      x[j][i] = in ? x[j][i] - mean : 0.f;
-      v = fmaf(x[j][i], x[j][i], v);
-    }
-  }
-  const float r = 1.f / sqrtf(fmaf(row_sum<LANES>(v, space + 8), inv_d, eps));
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[j][i] *= r;
-  return r;
-}
-
-template <typename IO, int VEC, int NV, int LANES>
-__global__ void __launch_bounds__(kThreads) kla_layer_norm_kernel(const LayerNormArgs p) {
+template <typename IO, int VEC, int NV, int LANES, int THREADS>
+__global__ void __launch_bounds__(THREADS) kla_layer_norm_kernel(const LayerNormArgs p) {
   using R = Raw<IO, VEC>;
-  __shared__ float space[16];
+  __shared__ float space[2][THREADS / 32];
   const int l = threadIdx.x % LANES;
-  const long long row = (long long)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const long long row = (long long)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
   const bool on = row < p.rows;
   R a[NV], b[NV];
-  float x[NV][VEC];
+  float x[NV][VEC], s[1] = {0.f}, v[1] = {0.f};
   if (on) fetch<IO, VEC, NV>(a, reinterpret_cast<const IO*>(p.x) + row * p.x_stride, l, LANES, p.D);
   if (on && p.residual)
     fetch<IO, VEC, NV>(b, reinterpret_cast<const IO*>(p.residual) + row * p.residual_stride, l, LANES, p.D);
@@ -124,11 +133,11 @@ __global__ void __launch_bounds__(kThreads) kla_layer_norm_kernel(const LayerNor
     const int e = (l + LANES * j) * VEC;
     const bool in = on && e < p.D;
     if (in && p.residual) {
-      float u[VEC], v[VEC];
+      float u[VEC], w[VEC];
       a[j].to(u);
-      b[j].to(v);
+      b[j].to(w);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) u[i] += v[i];
+      for (int i = 0; i < VEC; ++i) u[i] += w[i];
       a[j].from(u);
       *reinterpret_cast<R*>(reinterpret_cast<IO*>(p.total) + row * p.D + e) = a[j];
     }
@@ -136,16 +145,38 @@ __global__ void __launch_bounds__(kThreads) kla_layer_norm_kernel(const LayerNor
     else
 #pragma unroll
       for (int i = 0; i < VEC; ++i) x[j][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[0] += x[j][i];
   }
-  standardise<VEC, NV, LANES>(x, l, p.D, p.inv_d, p.eps, space);
+  row_sums<LANES, THREADS>(s, space[0], 0);
+  const float mean = s[0] * p.inv_d;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const bool in = (l + LANES * j) * VEC < p.D;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      x[j][i] -= mean;
+      if (in) v[0] = fmaf(x[j][i], x[j][i], v[0]);
+    }
+  }
+  row_sums<LANES, THREADS>(v, space[1], 0);
+  const float r = 1.f / sqrtf(fmaf(v[0], p.inv_d, p.eps));
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = (l + LANES * j) * VEC;
     if (!on || e >= p.D) continue;
+    float w[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float w = p.weight ? p.weight[e + i] : 1.f;
-      x[j][i] = p.bias ? fmaf(x[j][i], w, p.bias[e + i]) : x[j][i] * w;
+    for (int i = 0; i < VEC; ++i) x[j][i] *= r;
+    if (p.weight) {
+      params<VEC>(p.weight + e, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[j][i] *= w[i];
+    }
+    if (p.bias) {
+      params<VEC>(p.bias + e, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[j][i] += w[i];
     }
     R y;
     y.from(x[j]);
@@ -153,141 +184,289 @@ __global__ void __launch_bounds__(kThreads) kla_layer_norm_kernel(const LayerNor
   }
 }
 
-template <typename IO, int VEC, int NV, int LANES, int THREADS>
-__global__ void __launch_bounds__(THREADS) kla_layer_norm_grad_kernel(const LayerNormGradArgs p) {
+// A thread's pieces of the rows ahead, S - 1 of them on their way by asynchronous
+// copies into places that no other thread reads (so nothing waits but the
+// copies); elements of two bytes, which have no such copies, come through
+// registers, one row ahead. What no copy reaches (behind a row's end, a gradient
+// that is not there) stays zero.
+template <typename IO, int VEC, int NV, int LANES, int THREADS, int S>
+struct Ahead {
   using R = Raw<IO, VEC>;
-  constexpr int GROUPS = THREADS / LANES;
-  __shared__ float space[32];
+  static constexpr bool ASYNC = sizeof(R) >= 4;
+  static constexpr int P = (NV * VEC + 1) / 2;  // pairs of elements a thread
+  static constexpr size_t BYTES = ASYNC ? (size_t)S * 3 * NV * THREADS * sizeof(R) : 0;
+  R* ring;  // [S][3][NV][THREADS]
+  R next[ASYNC ? 1 : 3][ASYNC ? 1 : NV];
+  const IO* at[3];
+  long long down[3], left;
+  int step;
+  bool in[NV];  // pieces that the row has
+  __device__ __forceinline__ Ahead(unsigned char* smem, const LayerNormGradArgs& p, long long row, int rows_a_step, int l)
+      : ring(reinterpret_cast<R*>(smem)), left(p.rows - row), step(rows_a_step) {
+    const void* const from[3] = {p.x, p.gy, p.gtotal};
+    const long long stride[3] = {p.x_stride, p.gy_stride, p.gtotal_stride};
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      at[s] = from[s] ? reinterpret_cast<const IO*>(from[s]) + row * stride[s] + l * VEC : nullptr;
+      down[s] = step * stride[s];
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) in[j] = (l + LANES * j) * VEC < p.D;
+    float zero[VEC] = {};
+    R r;
+    r.from(zero);
+    if constexpr (ASYNC) {
+      for (int i = threadIdx.x; i < S * 3 * NV * THREADS; i += THREADS) ring[i] = r;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) next[0][j] = next[1][j] = next[2][j] = r;
+    }
+  }
+  __device__ __forceinline__ R* place(int stage, int stream, int j) const {
+    return ring + ((stage * 3 + stream) * NV + j) * THREADS + threadIdx.x;
+  }
+  // the next row of the thread's group, `step` rows after the one before
+  __device__ __forceinline__ void fetch(int stage) {
+    if (left > 0) {
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        if (!at[s]) continue;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (!in[j]) continue;
+          const IO* const from = at[s] + LANES * j * VEC;
+          if constexpr (sizeof(R) == 16) cp_async16(place(stage, s, j), from);
+          else if constexpr (ASYNC)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(place(stage, s, j))), "l"(from) : "memory");
+          else next[s][j] = *reinterpret_cast<const R*>(from);
+        }
+        at[s] += down[s];
+      }
+    }
+    left -= step;
+    if (ASYNC) cp_async_commit();
+  }
+  __device__ __forceinline__ void pairs(int stage, int stream, f2 (&x)[P]) const {
+    float v[2 * P];
+    if constexpr (NV * VEC % 2) v[2 * P - 1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float u[VEC];
+      if constexpr (ASYNC) place(stage, stream, j)->to(u);
+      else next[stream][j].to(u);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = f2_make(v[2 * i], v[2 * i + 1]);
+  }
+};
+
+// Two rounds of sums a row: Σx and Σ g w, then with d = x - mean Σ d² and Σ g w d.
+template <typename IO, int VEC, int NV, int LANES, int THREADS, int S, int MIN>
+__global__ void __launch_bounds__(THREADS, MIN) kla_layer_norm_grad_kernel(const LayerNormGradArgs p) {
+  using R = Raw<IO, VEC>;
+  using Rows = Ahead<IO, VEC, NV, LANES, THREADS, S>;
+  constexpr int GROUPS = THREADS / LANES, P = Rows::P, E = NV * VEC;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float space[2][THREADS / 32 * 2];
   const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const long long step = (long long)gridDim.x * GROUPS;
-  float gw[NV][VEC] = {}, gb[NV][VEC] = {};
-  R nx[NV], ng[NV], nt[NV];
-  auto ahead = [&](long long row) {
-    if (row >= p.rows) return;
-    fetch<IO, VEC, NV>(nx, reinterpret_cast<const IO*>(p.x) + row * p.x_stride, l, LANES, p.D);
-    if (p.gy) fetch<IO, VEC, NV>(ng, reinterpret_cast<const IO*>(p.gy) + row * p.gy_stride, l, LANES, p.D);
-    if (p.gtotal) fetch<IO, VEC, NV>(nt, reinterpret_cast<const IO*>(p.gtotal) + row * p.gtotal_stride, l, LANES, p.D);
-  };
-  ahead((long long)blockIdx.x * GROUPS + grp);
-  for (long long first = (long long)blockIdx.x * GROUPS; first < p.rows; first += step) {
-    const long long row = first + grp;
-    const bool on = row < p.rows;
-    float x[NV][VEC], g[NV][VEC];
-    R t[NV];
+  float* const room = space[0] + grp * (LANES / 32 * 2);
+  const int step = gridDim.x * GROUPS;
+  const long long first = (long long)blockIdx.x * GROUPS;
+  f2 gw[P] = {}, gb[P] = {}, w[P];
+  {
+    float v[2 * P];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool in = on && (l + LANES * j) * VEC < p.D;
-      if (in) nx[j].to(x[j]);
-      else
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[j][i] = 0.f;
-      if (in && p.gy) ng[j].to(g[j]);
-      else
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
-      t[j] = nt[j];
+    for (int i = 0; i < 2 * P; ++i) {
+      const int e = (l + LANES * (i / VEC)) * VEC + i % VEC;
+      v[i] = !p.weight || e >= p.D || i >= E ? 1.f : p.weight[e];
     }
-    ahead(row + step);
-    const float r = standardise<VEC, NV, LANES>(x, l, p.D, p.inv_d, p.eps, space);
-    float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = (l + LANES * j) * VEC;
+    for (int i = 0; i < P; ++i) w[i] = f2_make(v[2 * i], v[2 * i + 1]);
+  }
+  Rows rows(smem, p, first + grp, step, l);
+  if (Rows::ASYNC) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        gw[j][i] = fmaf(g[j][i], on ? x[j][i] : 0.f, gw[j][i]);
-        gb[j][i] += g[j][i];
-        if (p.weight && e < p.D) g[j][i] *= p.weight[e + i];
-        s1 += g[j][i];
-        s2 = fmaf(g[j][i], x[j][i], s2);
+  for (int i = 0; i < (Rows::ASYNC ? S - 1 : 1); ++i) rows.fetch(i);
+  int stage = 0;
+  for (long long at = first; at < p.rows; at += step) {
+    const long long row = at + grp;
+    f2 x[P], g[P], t[P], s2 = 0, v2 = 0;
+    if (Rows::ASYNC) {
+      rows.fetch(stage == 0 ? S - 1 : stage - 1);
+      cp_async_wait<S - 1>();
+    }
+    rows.pairs(stage, 0, x);
+    rows.pairs(stage, 1, g);
+    if (!Rows::ASYNC) {
+      rows.pairs(stage, 2, t);
+      rows.fetch(0);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      s2 = f2_add(s2, x[i]);
+      v2 = f2_fma(g[i], w[i], v2);
+    }
+    float s[2] = {f2_lo(s2) + f2_hi(s2), f2_lo(v2) + f2_hi(v2)};
+    row_sums<LANES, THREADS>(s, room, grp);
+    const float mean = s[0] * p.inv_d;
+    s2 = v2 = 0;
+    float away[NV];  // zeros behind the row's end stay
+#pragma unroll
+    for (int j = 0; j < NV; ++j) away[j] = rows.in[j] ? -mean : 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      x[i] = f2_add(x[i], f2_make(away[2 * i / VEC], 2 * i + 1 < E ? away[(2 * i + 1) / VEC < NV ? (2 * i + 1) / VEC : 0] : 0.f));
+      s2 = f2_fma(x[i], x[i], s2);
+      v2 = f2_fma(f2_mul(g[i], w[i]), x[i], v2);
+    }
+    float v[2] = {f2_lo(s2) + f2_hi(s2), f2_lo(v2) + f2_hi(v2)};
+    row_sums<LANES, THREADS>(v, room + THREADS / 32 * 2, grp);
+    if (row < p.rows) {
+      IO* const out = reinterpret_cast<IO*>(p.gx) + row * p.D + l * VEC;
+      const float r = 1.f / sqrtf(fmaf(v[0], p.inv_d, p.eps));
+      const float rest = -r * (s[1] * p.inv_d), by_n = -r * (v[1] * p.inv_d * r);
+      if (Rows::ASYNC && p.gtotal) rows.pairs(stage, 2, t);
+      float o[2 * P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const f2 n = f2_mul(x[i], f2_make(r, r));
+        gw[i] = f2_fma(g[i], n, gw[i]);
+        gb[i] = f2_add(gb[i], g[i]);
+        f2 y = f2_fma(f2_mul(g[i], w[i]), f2_make(r, r), f2_fma(n, f2_make(by_n, by_n), f2_make(rest, rest)));
+        if (p.gtotal) y = f2_add(y, t[i]);
+        o[2 * i] = f2_lo(y), o[2 * i + 1] = f2_hi(y);
       }
-    }
-    s1 = row_sum<LANES>(s1, space + 16) * p.inv_d;
-    s2 = row_sum<LANES>(s2, space + 24) * p.inv_d;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = (l + LANES * j) * VEC;
-      if (!on || e >= p.D) continue;
-      float o[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) o[i] = r * (g[j][i] - fmaf(x[j][i], s2, s1));
-      if (p.gtotal) {
+      for (int j = 0; j < NV; ++j) {
+        if (!rows.in[j]) continue;
         float u[VEC];
-        t[j].to(u);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] += u[i];
+        for (int i = 0; i < VEC; ++i) u[i] = o[j * VEC + i];
+        R y;
+        y.from(u);
+        *reinterpret_cast<R*>(out + LANES * j * VEC) = y;
       }
-      R y;
-      y.from(o);
-      *reinterpret_cast<R*>(reinterpret_cast<IO*>(p.gx) + row * p.D + e) = y;
     }
+    if (Rows::ASYNC) stage = stage + 1 == S ? 0 : stage + 1;
   }
   if (!p.part) return;
   // the block's sums of its groups, a group after the other
-  extern __shared__ float sums[];  // [2][D]
+  float* const part = p.part + (long long)blockIdx.x * 2 * p.D;
+  float* const sums = reinterpret_cast<float*>(smem + Rows::BYTES);  // [2][D], where there are groups
   for (int n = 0; n < GROUPS; ++n) {
     if (n == grp) {
+      float* const out = n == GROUPS - 1 ? part : sums;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int e = (l + LANES * j) * VEC + i;
-          if (e < p.D) {
-            sums[e] = n ? sums[e] + gw[j][i] : gw[j][i];
-            sums[p.D + e] = n ? sums[p.D + e] + gb[j][i] : gb[j][i];
-          }
+      for (int i = 0; i < E; ++i) {
+        const int e = (l + LANES * (i / VEC)) * VEC + i % VEC;
+        const float a = i % 2 ? f2_hi(gw[i / 2]) : f2_lo(gw[i / 2]), b = i % 2 ? f2_hi(gb[i / 2]) : f2_lo(gb[i / 2]);
+        if (e < p.D) {
+          out[e] = n ? sums[e] + a : a;
+          out[p.D + e] = n ? sums[p.D + e] + b : b;
         }
+      }
     }
-    __syncthreads();
+    if (GROUPS > 1) __syncthreads();
   }
-  for (int e = threadIdx.x; e < 2 * p.D; e += THREADS) p.part[(long long)blockIdx.x * 2 * p.D + e] = sums[e];
 }
 
-// Sums the blocks' partials: 32 columns a block, its warps over the blocks.
-__global__ void __launch_bounds__(kThreads) kla_layer_norm_sum_kernel(const LayerNormGradArgs p, int blocks) {
-  __shared__ float sums[kThreads / 32][33];
-  const int w = threadIdx.x / 32, c = blockIdx.x * 32 + threadIdx.x % 32;
+// Sums the blocks' partials: eight columns a block (32 bytes of a partial), its
+// 128 rows of threads over the blocks, four loads of a thread on their way at a time.
+__global__ void __launch_bounds__(1024) kla_layer_norm_sum_kernel(const LayerNormGradArgs p, int blocks) {
+  __shared__ float sums[128][9];
+  const int row = threadIdx.x / 8, col = threadIdx.x % 8, c = blockIdx.x * 8 + col, n = 2 * p.D;
   float x = 0.f;
-  if (c < 2 * p.D)
-    for (int b = w; b < blocks; b += kThreads / 32) x += p.part[(long long)b * 2 * p.D + c];
-  sums[w][threadIdx.x % 32] = x;
+  if (c < n) {
+    const float* const part = p.part + c;
+    for (int b = row; b < blocks; b += 4 * 128) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = b + 128 * i < blocks ? part[(long long)(b + 128 * i) * n] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x += v[i];
+    }
+  }
+  sums[row][col] = x;
   __syncthreads();
-  if (w == 0 && c < 2 * p.D) {
-    for (int i = 1; i < kThreads / 32; ++i) x += sums[i][threadIdx.x];
-    float* out = c < p.D ? p.gweight : p.gbias;
-    if (out) out[c < p.D ? c : c - p.D] = x;
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32, mine = blockIdx.x * 8 + w;  // a warp adds up one column
+  if (w >= 8) return;
+  x = (sums[lane][w] + sums[lane + 32][w]) + (sums[lane + 64][w] + sums[lane + 96][w]);
+#pragma unroll
+  for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(~0u, x, m);
+  if (lane == 0 && mine < n) {
+    float* const out = mine < p.D ? p.gweight : p.gbias;
+    if (out) out[mine < p.D ? mine : mine - p.D] = x;
   }
 }
 
-// Lanes a row and pieces a lane, by the row's width in pieces of VEC.
-template <typename F>
-void by_width(int pieces, bool vec, F f) {
-  using std::integral_constant;
-#define KLA_LN(NV, LANES) return f(integral_constant<int, NV>(), integral_constant<int, LANES>())
-  if (vec) {
-    if (pieces <= 8) KLA_LN(1, 8);
-    if (pieces <= 32) KLA_LN(1, 32);
-    if (pieces <= 64) KLA_LN(2, 32);
-    if (pieces <= 128) KLA_LN(4, 32);
-    if (pieces <= 256) KLA_LN(1, 256);
-    if (pieces <= 512) KLA_LN(2, 256);
-    if (pieces <= 1024) KLA_LN(4, 256);
-    KLA_LN(8, 256);
+// Lanes a row, pieces a lane, threads a block, and backward stages and blocks an SM
+template <int NV_, int LANES_, int THREADS_, int S_ = 2, int MIN_ = 1>
+struct Shape {
+  static constexpr int NV = NV_, LANES = LANES_, THREADS = THREADS_, S = S_, MIN = MIN_;
+};
+
+// Forward, by the row's width in pieces (of 16 bytes, or single elements).
+template <bool VEC, typename F>
+void by_width(int pieces, F f) {
+  if constexpr (VEC) {
+    if (pieces <= 8) return f(Shape<1, 8, 256>());
+    if (pieces <= 32) return f(Shape<1, 32, 256>());
+    if (pieces <= 64) return f(Shape<2, 32, 256>());
+    if (pieces <= 128) return f(Shape<4, 32, 256>());
+    if (pieces <= 256) return f(Shape<2, 128, 128>());
+    if (pieces <= 512) return f(Shape<4, 128, 128>());
+    if (pieces <= 1024) return f(Shape<4, 256, 256>());
+    return f(Shape<4, 512, 512>());
+  } else {
+    if (pieces <= 128) return f(Shape<4, 32, 256>());
+    if (pieces <= 512) return f(Shape<16, 32, 256>());
+    if (pieces <= 1024) return f(Shape<8, 128, 128>());
+    if (pieces <= 2048) return f(Shape<16, 128, 128>());
+    return f(Shape<16, 512, 512>());
   }
-  if (pieces <= 128) KLA_LN(4, 32);
-  if (pieces <= 1024) KLA_LN(32, 32);
-  KLA_LN(32, 256);
-#undef KLA_LN
 }
 
-constexpr int kGradThreads = 128;
-template <int LANES>
-constexpr int grad_threads() { return LANES > 32 ? LANES : kGradThreads; }
+// Backward, where a lane also keeps the sums of its columns: more lanes with fewer pieces.
+template <int VEC, typename F>
+void by_width_back(int pieces, F f) {
+  if constexpr (VEC == 8) {
+    if (pieces <= 8) return f(Shape<1, 8, 128, 3, 4>());
+    if (pieces <= 32) return f(Shape<1, 32, 128, 3, 4>());
+    if (pieces <= 64) return f(Shape<2, 32, 128, 3, 3>());
+    if (pieces <= 128) return f(Shape<2, 64, 128, 3, 3>());
+    if (pieces <= 256) return f(Shape<2, 128, 128, 3, 3>());
+    if (pieces <= 512) return f(Shape<2, 256, 256, 3, 2>());
+    return f(Shape<2, 512, 512, 2, 1>());
+  } else if constexpr (VEC == 4) {
+    if (pieces <= 8) return f(Shape<1, 8, 128, 3, 4>());
+    if (pieces <= 32) return f(Shape<1, 32, 128, 3, 4>());
+    if (pieces <= 64) return f(Shape<2, 32, 128, 3, 5>());
+    if (pieces <= 128) return f(Shape<4, 32, 128, 3, 3>());
+    if (pieces <= 256) return f(Shape<4, 64, 128, 3, 3>());
+    if (pieces <= 512) return f(Shape<4, 128, 128, 3, 3>());
+    if (pieces <= 1024) return f(Shape<4, 256, 256, 3, 2>());
+    return f(Shape<4, 512, 512, 2, 1>());
+  } else {
+    if (pieces <= 128) return f(Shape<4, 32, 128, 4, 5>());
+    if (pieces <= 256) return f(Shape<8, 32, 128, 3, 4>());
+    if (pieces <= 384) return f(Shape<6, 64, 128, 3, 5>());
+    if (pieces <= 512) return f(Shape<8, 64, 128, 3, 4>());
+    if (pieces <= 640) return f(Shape<5, 128, 128, 4, 4>());
+    if (pieces <= 768) return f(Shape<6, 128, 128, 4, 4>());
+    if (pieces <= 1024) return f(Shape<8, 128, 128, 3, 4>());
+    if (pieces <= 2048) return f(Shape<8, 256, 256, 3, 2>());
+    if (pieces <= 4096) return f(Shape<8, 512, 512, 3, 1>());
+    return f(Shape<16, 512, 512, 2, 1>());
+  }
+}
 
-// Blocks of the gradients' kernel: as many as the device holds at once, for each leaves partial sums.
-int grad_blocks(long long rows, int lanes, int num_sms) {
-  const int groups = (lanes > 32 ? lanes : kGradThreads) / lanes;
-  return (int)std::max(1LL, std::min((rows + groups - 1) / groups, (long long)num_sms * (lanes > 32 ? 2 : 4)));
+// Blocks of the gradients' kernel: as many as the device holds at once (every shape's MIN an SM), for each leaves partial sums.
+template <typename Sh>
+int grad_blocks(long long rows, int num_sms) {
+  constexpr int groups = Sh::THREADS / Sh::LANES;
+  return (int)std::max(1LL, std::min((rows + groups - 1) / groups, (long long)num_sms * Sh::MIN));
 }
 
 // Rows that all begin on 16 bytes.
@@ -309,14 +488,14 @@ cudaError_t launch_io(const LayerNormArgs& a, cudaStream_t s) {
   constexpr int VE = 16 / sizeof(IO);
   const bool vec = vector_rows<IO>(a.D, {{a.x, a.x_stride}, {a.residual, a.residual_stride}, {a.y, a.D},
                                          {a.total, a.D}});
-  by_width(vec ? a.D / VE : a.D, vec, [&](auto nv, auto lanes) {
-    constexpr int NV = decltype(nv)::value, LANES = decltype(lanes)::value, G = kThreads / LANES;
+  auto go = [&](auto ve, auto shape) {
+    using Sh = decltype(shape);
+    constexpr int G = Sh::THREADS / Sh::LANES;
     const unsigned blocks = (unsigned)((a.rows + G - 1) / G);
-    if constexpr (NV <= 8)
-      if (vec) return (void)(kla_layer_norm_kernel<IO, VE, NV, LANES><<<blocks, kThreads, 0, s>>>(a));
-    if constexpr (NV == 32 || (NV == 4 && LANES == 32))
-      kla_layer_norm_kernel<IO, 1, NV, LANES><<<blocks, kThreads, 0, s>>>(a);
-  });
+    kla_layer_norm_kernel<IO, decltype(ve)::value, Sh::NV, Sh::LANES, Sh::THREADS><<<blocks, Sh::THREADS, 0, s>>>(a);
+  };
+  if (vec) by_width<true>(a.D / VE, [&](auto shape) { go(std::integral_constant<int, VE>(), shape); });
+  else by_width<false>(a.D, [&](auto shape) { go(std::integral_constant<int, 1>(), shape); });
   return cudaGetLastError();
 }
 
@@ -327,29 +506,33 @@ cudaError_t launch_io(const LayerNormGradArgs& a, int num_sms, cudaStream_t s) {
                                          {a.gx, a.D}});
   int blocks = 0;
   cudaError_t e = cudaSuccess;
-  by_width(vec ? a.D / VE : a.D, vec, [&](auto nv, auto lanes) {
-    constexpr int NV = decltype(nv)::value, LANES = decltype(lanes)::value, THREADS = grad_threads<LANES>();
-    blocks = grad_blocks(a.rows, LANES, num_sms);
-    const size_t smem = a.part ? 2 * (size_t)a.D * sizeof(float) : 0;
-    auto go = [&](auto kernel) {
-      if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e == cudaSuccess) kernel<<<blocks, THREADS, smem, s>>>(a);
-    };
-    if constexpr (NV <= 8)
-      if (vec) return go(kla_layer_norm_grad_kernel<IO, VE, NV, LANES, THREADS>);
-    if constexpr (NV == 32 || (NV == 4 && LANES == 32)) go(kla_layer_norm_grad_kernel<IO, 1, NV, LANES, THREADS>);
-  });
+  auto go = [&](auto ve, auto shape) {
+    using Sh = decltype(shape);
+    constexpr int V = decltype(ve)::value;
+    const auto kernel = kla_layer_norm_grad_kernel<IO, V, Sh::NV, Sh::LANES, Sh::THREADS, Sh::S, Sh::MIN>;
+    size_t smem = Ahead<IO, V, Sh::NV, Sh::LANES, Sh::THREADS, Sh::S>::BYTES;
+    if (a.part && Sh::LANES < Sh::THREADS) smem += 2 * (size_t)a.D * sizeof(float);
+    blocks = grad_blocks<Sh>(a.rows, num_sms);
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) kernel<<<blocks, Sh::THREADS, smem, s>>>(a);
+  };
+  if (vec) by_width_back<VE>(a.D / VE, [&](auto shape) { go(std::integral_constant<int, VE>(), shape); });
+  else by_width_back<1>(a.D, [&](auto shape) { go(std::integral_constant<int, 1>(), shape); });
   if (e != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
-  kla_layer_norm_sum_kernel<<<(2 * a.D + 31) / 32, kThreads, 0, s>>>(a, blocks);
+  kla_layer_norm_sum_kernel<<<(2 * a.D + 7) / 8, 1024, 0, s>>>(a, blocks);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t layer_norm_partial_bytes(long long rows, int D, int num_sms) {
-  // the most that any choice of lanes asks for: groups of eight lanes do not for wide rows, but share a block's bound
-  return (size_t)std::max(grad_blocks(rows, 256, num_sms), grad_blocks(rows, 32, num_sms)) * 2 * (size_t)D * sizeof(float);
+  int most = 0;  // of rows in pieces of any kind
+  auto count = [&](auto shape) { most = std::max(most, grad_blocks<decltype(shape)>(rows, num_sms)); };
+  by_width_back<1>(D, count);
+  if (D % 4 == 0) by_width_back<4>(D / 4, count);
+  if (D % 8 == 0) by_width_back<8>(D / 8, count);
+  return (size_t)most * 2 * (size_t)D * sizeof(float);
 }
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {
