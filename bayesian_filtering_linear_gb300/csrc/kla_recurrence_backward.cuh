@@ -79,9 +79,11 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
     f2 w = 0;  // s' σ(i) x
     b[j] = open;
     if (SCALE == kRecSqrt) {
-      const f2 v = spread(a.less), rs = spread_rsqrt(v);
-      b[j] = f2_mul(f2_mul(v, rs), open);
-      w = f2_mul(f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus)), xo);
+      const f2 v = spread(a.less), rs = spread_rsqrt(v), s = f2_mul(v, rs);
+      b[j] = f2_mul(s, open);
+      // -a²/s, near 1 as s - 1/s (no digits are lost while a² is not small)
+      if (NEAR) w = f2_mul(f2_fma(rs, minus, s), xo);
+      else w = f2_mul(f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus)), xo);
     } else if (SCALE == kRecComplement) {
       b[j] = f2_mul(a.less, open);
       w = f2_mul(f2_mul(a.hi, minus), xo);
@@ -135,15 +137,18 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   const int c = c0 + 2 * lane;
   const bool live = c < p.C;
   const Place my(live ? c : 0, p.H, p.D);
-  IO* const gx = reinterpret_cast<IO*>(q.gx.p) + my.of(q.gx);
-  IO* const gg = reinterpret_cast<IO*>(q.gg.p) + my.of(q.gg);
-  IO* const gi = reinterpret_cast<IO*>(q.gi.p) + (GATE ? my.of(q.gi) : 0);
+  IO* const gx = reinterpret_cast<IO*>(q.gx.p) + at.of(q.gx);  // as this thread's copies
+  IO* const gg = reinterpret_cast<IO*>(q.gg.p) + at.of(q.gg);
+  IO* const gi = reinterpret_cast<IO*>(q.gi.p) + (GATE ? at.of(q.gi) : 0);
   f2 rate = 0, z = 0, sum = 0;  // z: what reaches the step's last token from behind it
   if (DECAY == kRecRate && live)
     rate = *reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d);
   if (q.ghT && live) z = *reinterpret_cast<const f2*>(q.ghT + c);
   const bool near = DECAY == kRecRate && near_rates(rate);
 
+  if (!q.gy.p)  // no copies: zeros
+    for (int i = threadIdx.x; i < kStages<IO> * S * (int)sizeof(IO) / 16; i += kBackThreads)
+      reinterpret_cast<uint4*>(ring + (i / (S * (int)sizeof(IO) / 16)) * STAGE + 3 * S)[i % (S * (int)sizeof(IO) / 16)] = make_uint4(0, 0, 0, 0);
   const f2 one = f2_both(1.f), minus_rate = f2_mul(rate, f2_both(-1.f));
   const long long steps = ((long long)p.T + kRecTile * k - 1) / (kRecTile * k);
   fetch(steps - 1);
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
 #pragma unroll
     for (int j = kBackTok - 1; j >= 0; --j) {
       const f2 hi = Q[j], lo = R[j];
-      R[j] = q.gy.p ? f2_add(r, pair_at<IO>(tile + 3 * S + j * kChans)) : r;
+      R[j] = f2_add(r, pair_at<IO>(tile + 3 * S + j * kChans));
       r = f2_fma(hi, R[j], f2_mul(lo, R[j]));
       Q[j] = prod;
       prod = f2_mul(prod, hi);
@@ -188,8 +193,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
           put_remote(&half[rank].S[lane], o, t.S);
         }
       }
-      if (w == kBackWarps - 1) cluster_arrive();
-      else cluster_arrive_only();
+      cluster_arrive();  // (by all: with the others' arrivals not held up by their stores, the headline took 213 us for 163)
       cluster_wait();
       for (int o = k - 1; o >= 0; --o) {
         if (o == rank) z = next;
@@ -208,28 +212,43 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     if (k > 1) z = next;
     if (t0 < p.T) {
       const int n = (int)min((long long)kBackTok, p.T - t0);
-      IO *ox = gx + t0 * q.gx.st, *og = gg + t0 * q.gg.st, *oi = gi + t0 * q.gi.st;
 #pragma unroll
       for (int j = 0; j < kBackTok; ++j) {
+        IO* const o = tile + j * kChans;
         const f2 G = f2_fma(Q[j], behind, R[j]);
         f2 by_log = f2_mul(G, f2_fma(P[j], h, V[j]));
         if (DECAY != kRecLog) {
-          const f2 e = kept(tile + S + j * kChans, tile + 2 * S + j * kChans);
-          const f2 open = f2_rcp(f2_add(one, e)), shut = f2_mul(e, open);
+          const f2 e = kept(o + S, o + 2 * S), open = f2_rcp(f2_add(one, e)), shut = f2_mul(e, open);
           if (DECAY == kRecRate) {
             by_log = f2_mul(by_log, open);
-            if (j < n) sum = f2_add(sum, by_log);
+            sum = f2_add(sum, by_log);  // (behind the last token σ(g) is 2^-126)
             by_log = f2_mul(by_log, f2_mul(minus_rate, shut));
           } else {
             by_log = f2_mul(by_log, shut);
           }
         }
-        if (live && j < n) {
-          put_pair(ox, f2_mul(G, b[j]));
-          put_pair(og, by_log);
-          if (GATE) put_pair(oi, f2_mul(G, *gate_place(tile + 2 * S + j * kChans, own, j)));
+        f2 by_gate = 0;
+        if (GATE) by_gate = f2_mul(G, *gate_place(o + 2 * S, own, j));
+        put_pair(o, f2_mul(G, b[j]));
+        put_pair(o + S, by_log);
+        if (GATE) put_pair(o + 2 * S, by_gate);
+      }
+      __syncwarp();
+      // the warp's rows leave in pieces of 16 bytes
+      if (copies) {
+        constexpr int ROWS = 32 / Copy::GROUPS;
+        const int row = lane / Copy::GROUPS;
+        const IO* const from = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0) + (w * kBackTok + row) * kChans + Copy::group();
+        IO *ox = gx + (t0 + row) * q.gx.st, *og = gg + (t0 + row) * q.gg.st, *oi = gi + (t0 + row) * q.gi.st;
+#pragma unroll
+        for (int r = 0; r < kBackTok; r += ROWS) {
+          if (row + r < n) {
+            *reinterpret_cast<uint4*>(ox) = *reinterpret_cast<const uint4*>(from + r * kChans);
+            *reinterpret_cast<uint4*>(og) = *reinterpret_cast<const uint4*>(from + r * kChans + S);
+            if (GATE) *reinterpret_cast<uint4*>(oi) = *reinterpret_cast<const uint4*>(from + r * kChans + 2 * S);
+          }
+          ox += ROWS * q.gx.st, og += ROWS * q.gg.st, oi += ROWS * q.gi.st;
         }
-        ox += q.gx.st, og += q.gg.st, oi += q.gi.st;
       }
     }
     if (kStages<IO> == 1) {
