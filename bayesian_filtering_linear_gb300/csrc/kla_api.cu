@@ -1054,8 +1054,6 @@ kla_status kla_recurrence_forward(const void* x, const void* g, const void* i, c
                              : cudaMemsetAsync(hT, 0, states, cs);
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
   }
-  int sms = 0;
-  if ((st = device_sms(&sms)) != KLA_OK) return st;
   kla::RecArgs a{};
   a.x = {x, s[0][0], s[0][1], s[0][2]};
   a.g = {g, s[1][0], s[1][1], s[1][2]};
@@ -1063,7 +1061,7 @@ kla_status kla_recurrence_forward(const void* x, const void* g, const void* i, c
   a.y = {y, s[3][0], s[3][1], s[3][2]};
   a.rate = rate; a.h0 = h0; a.hT = hT; a.ckpt = reinterpret_cast<float*>(checkpoints);
   a.B = B; a.H = H; a.T = T; a.D = D; a.C = (int)(bh * D); a.decay = opt->decay; a.scale = opt->scale; a.io = (int)io;
-  return kla::launch_recurrence(a, sms, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  return kla::launch_recurrence(a, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 kla_status kla_recurrence_step(const void* x, const void* g, const void* i, const float* rate, float* state, void* y,
@@ -1147,8 +1145,6 @@ kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, 
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
   }
   if (need > 0 && (!workspace || ws_bytes < need)) return KLA_ERR_WORKSPACE;
-  int sms = 0;
-  if ((st = device_sms(&sms)) != KLA_OK) return st;
   kla::RecGradArgs a{};
   a.f.x = {x, s[0][0], s[0][1], s[0][2]};
   a.f.g = {g, s[1][0], s[1][1], s[1][2]};
@@ -1161,7 +1157,7 @@ kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, 
     a.f.ckpt = reinterpret_cast<float*>(const_cast<void*>(checkpoints));
   } else {
     a.f.ckpt = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(workspace) + sums);
-    if (kla::launch_recurrence(a.f, sms, cs) != cudaSuccess) return KLA_ERR_CUDA;
+    if (kla::launch_recurrence(a.f, cs) != cudaSuccess) return KLA_ERR_CUDA;
   }
   if (gy) a.gy = {gy, s[3][0], s[3][1], s[3][2]};
   a.gx = {gx, s[4][0], s[4][1], s[4][2]};
@@ -1169,7 +1165,7 @@ kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, 
   if (gi) a.gi = {gi, s[6][0], s[6][1], s[6][2]};
   a.ghT = ghT; a.gh0 = gh0; a.grate = grate;
   a.part = grate ? reinterpret_cast<float*>(workspace) : nullptr;
-  return kla::launch_recurrence_backward(a, sms, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  return kla::launch_recurrence_backward(a, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 kla_status kla_layer_norm(const void* x, const float* weight, const float* bias, const void* residual, void* y,

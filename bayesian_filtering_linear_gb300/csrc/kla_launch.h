@@ -187,7 +187,7 @@ cudaError_t launch_norm_rope_backward(const NormRopeArgs& a, int num_sms, cudaSt
 // elements, last dimension contiguous; states [B,H,D] fp32, flat channels
 // C = B·H·D.
 constexpr int kRecTile = 64;         // tokens between two checkpoints
-constexpr int kRecMaxCluster = 8;    // blocks that share a sequence
+constexpr int kRecMaxCluster = 16;   // blocks that share a sequence
 constexpr int kRecLog = 0, kRecSigmoid = 1, kRecRate = 2;
 constexpr int kRecPlain = 0, kRecSqrt = 1, kRecComplement = 2;
 struct RecTensor {
@@ -207,9 +207,7 @@ struct RecArgs {
   float* ckpt;         // [ceil(T / kRecTile)][C]: the state before every tile, or null
   int B, H, T, D, C, decay, scale, io;
 };
-// Blocks that go along a sequence together.
-int rec_cluster(int tiles, int along, int resident);
-cudaError_t launch_recurrence(const RecArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_recurrence(const RecArgs& a, cudaStream_t s);
 cudaError_t launch_recurrence_step(const RecArgs& a, cudaStream_t s);
 struct RecGradArgs {
   RecArgs f;           // the forward's inputs; f.ckpt: its checkpoints (required)
@@ -220,7 +218,7 @@ struct RecGradArgs {
   float* part;         // [blocks along a sequence][C] for the sums of grate, or null
   float* grate;        // [H,D], with part
 };
-cudaError_t launch_recurrence_backward(const RecGradArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_recurrence_backward(const RecGradArgs& a, cudaStream_t s);
 
 // Layer norm with the residual sum before it (kla_layer_norm.cu). Rows [rows,D],
 // inputs by row strides in elements, outputs contiguous.

@@ -1,7 +1,4 @@
-// Host side of the gated linear recurrence: the blocks that share a sequence,
-// and the kernels by type.
-#include <algorithm>
-
+// Host side of the gated linear recurrence: the kernels by type.
 #include <cuda_bf16.h>
 
 #include "kla_launch.h"
@@ -9,11 +6,11 @@
 namespace kla {
 
 template <typename IO>
-cudaError_t launch_recurrence_io(const RecArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_recurrence_io(const RecArgs& a, cudaStream_t s);
 template <typename IO>
 cudaError_t launch_recurrence_step_io(const RecArgs& a, cudaStream_t s);
 template <typename IO>
-cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int num_sms, int* parts, cudaStream_t s);
+cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int* parts, cudaStream_t s);
 
 namespace {
 
@@ -28,26 +25,18 @@ __global__ void __launch_bounds__(128) kla_recurrence_rate_kernel(const float* p
 
 }  // namespace
 
-// As many as the device holds at once (`resident` blocks, of which clusters of up
-// to eight leave an eighth unused at worst): a second wave of clusters would take
-// as long as the first.
-int rec_cluster(int tiles, int along, int resident) {
-  const int most = resident / 8 * 7 / std::max(tiles, 1);
-  return std::max(1, std::min({most, along, kRecMaxCluster}));
-}
-
-cudaError_t launch_recurrence(const RecArgs& a, int num_sms, cudaStream_t s) {
-  return a.io == IO_BF16 ? launch_recurrence_io<__nv_bfloat16>(a, num_sms, s) : launch_recurrence_io<float>(a, num_sms, s);
+cudaError_t launch_recurrence(const RecArgs& a, cudaStream_t s) {
+  return a.io == IO_BF16 ? launch_recurrence_io<__nv_bfloat16>(a, s) : launch_recurrence_io<float>(a, s);
 }
 
 cudaError_t launch_recurrence_step(const RecArgs& a, cudaStream_t s) {
   return a.io == IO_BF16 ? launch_recurrence_step_io<__nv_bfloat16>(a, s) : launch_recurrence_step_io<float>(a, s);
 }
 
-cudaError_t launch_recurrence_backward(const RecGradArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_recurrence_backward(const RecGradArgs& a, cudaStream_t s) {
   int parts = 0;
-  const cudaError_t e = a.f.io == IO_BF16 ? launch_recurrence_backward_io<__nv_bfloat16>(a, num_sms, &parts, s)
-                                          : launch_recurrence_backward_io<float>(a, num_sms, &parts, s);
+  const cudaError_t e = a.f.io == IO_BF16 ? launch_recurrence_backward_io<__nv_bfloat16>(a, &parts, s)
+                                          : launch_recurrence_backward_io<float>(a, &parts, s);
   if (e != cudaSuccess || !a.part) return e;
   const int HD = a.f.H * a.f.D;
   kla_recurrence_rate_kernel<<<(HD + 127) / 128, 128, 0, s>>>(a.part, a.grate, parts, a.f.B, HD);

@@ -13,6 +13,8 @@
 // so are the products of decays that the state is carried by.
 #pragma once
 
+#include <atomic>
+
 #include "kla_device.cuh"
 #include "kla_launch.h"
 
@@ -201,24 +203,63 @@ struct BlockMap {
 };
 __host__ __device__ constexpr size_t block_maps_bytes(int k) { return k > 1 ? 2 * (size_t)k * sizeof(BlockMap) : 0; }
 
-// Launches `tiles` clusters of k blocks.
-template <typename Args>
-inline cudaError_t launch_rec_cluster(void (*kernel)(Args, int), const Args& a, int tiles, int k, int threads,
-                                      size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)k;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+inline cudaLaunchConfig_t cluster_config(unsigned blocks, int k, int threads, size_t smem, cudaLaunchAttribute* attr,
+                                         cudaStream_t s) {
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)k;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)tiles * (unsigned)k);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = smem + block_maps_bytes(k);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = k > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, k);
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of k blocks that the current device holds at once, asked for once a kernel, size and device.
+template <auto KERNEL, int THREADS, size_t SMEM>
+int clusters_at_once(int device, int k) {
+  static std::atomic<int> known[64][kRecMaxCluster + 1];  // count + 1
+  const bool keep = device >= 0 && device < 64;
+  int n = keep ? known[device][k].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n - 1;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(SMEM + block_maps_bytes(kRecMaxCluster))) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return -1;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = cluster_config(k, k, THREADS, SMEM, attr, nullptr);
+  if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) return -1;
+  if (keep) known[device][k].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Launches `tiles` clusters of as many blocks as there are tiles `along` the
+// sequence, as far as the device holds all clusters at once: a second wave
+// would take as long as the first. `used`: the blocks of a cluster.
+template <auto KERNEL, int THREADS, size_t SMEM, typename Args>
+cudaError_t launch_clusters(const Args& a, int tiles, int along, int* used, cudaStream_t s) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  constexpr int sizes[] = {16, 12, 8, 7, 6, 5, 4, 3, 2, 1};  // above eight, those that the device's groups of SMs hold well
+  static_assert(sizes[0] == kRecMaxCluster, "the largest");
+  int k = 1;
+  for (int n : sizes) {
+    if (n > along && n > 1) continue;
+    const int most = clusters_at_once<KERNEL, THREADS, SMEM>(device, n);
+    if (most < 0) return cudaErrorUnknown;
+    if (tiles <= most) {
+      k = n;
+      break;
+    }
+  }
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = cluster_config((unsigned)tiles * (unsigned)k, k, THREADS, SMEM, attr, s);
+  if (used) *used = k;
+  e = cudaLaunchKernelEx(&cfg, KERNEL, a, k);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -30,7 +30,7 @@ namespace rec {
 constexpr int kBackWarps = 8, kBackThreads = 32 * kBackWarps, kBackTok = kRecTile / kBackWarps;
 // Stages of the ring of tiles: two, or for fp32, whose tiles are twice as large, one that two blocks take turns by.
 template <typename IO>
-constexpr int kStages = sizeof(IO) == 2 ? 2 : 1;
+constexpr int kBackStages = sizeof(IO) == 2 ? 2 : 1;
 
 // A pair of floats at the thread's own place of a tile: where a pair of one (fp32) or of two streams was (bf16).
 __device__ __forceinline__ void keep(float* a, float*, f2 v) { *reinterpret_cast<f2*>(a) = v; }
@@ -45,16 +45,16 @@ __device__ __forceinline__ f2 kept(const __nv_bfloat16* a, const __nv_bfloat16* 
 // The gate's terms: where i was (fp32), or in an array of their own.
 template <typename IO>
 __device__ __forceinline__ f2* gate_place(IO* i, f2* own, int j) {
-  return sizeof(IO) == 4 ? reinterpret_cast<f2*>(i) : own + j * kBackThreads;
+  return sizeof(IO) == 4 ? reinterpret_cast<f2*>(i) : own + (kBackTok + j) * kBackThreads;
 }
 
-// Forward through a warp's tokens: its map, and for each the decay (hi, lo), P, V and b = s σ(i).
+// Forward through a warp's tokens: its maps of h and (in r) of G, and for each token the decay, P and V.
 template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
-__device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackTok], f2 (&lo)[kBackTok],
-                                     f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2 (&b)[kBackTok]) {
+__device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackTok], f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2& r) {
   constexpr int S = kRecTile * kChans;
   const f2 one = f2_both(1.f), minus = f2_both(-1.f);
   Map m{one, 0, 0};
+  r = 0;
 #pragma unroll
   for (int j = 0; j < kBackTok; ++j) {
     IO* const at = tile + j * kChans;
@@ -74,27 +74,30 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
       if (DECAY == kRecSigmoid) a = decay_of_sigmoid(e);
       else a = decay_of_log<NEAR>(f2_mul(rate, f2_rcp(f2_add(one, e))));
     }
-    hi[j] = a.hi, lo[j] = a.lo;
     const f2 xo = GATE ? f2_mul(x, open) : x;
-    f2 w = 0;  // s' σ(i) x
-    b[j] = open;
-    if (SCALE == kRecSqrt) {
+    f2 w = 0, bx = xo;  // s' σ(i) x and s σ(i) x
+    if (SCALE == kRecPlain) {
+      if (GATE) own[j * kBackThreads] = open;
+    } else if (SCALE == kRecSqrt) {
       const f2 v = spread(a.less), rs = spread_rsqrt(v), s = f2_mul(v, rs);
-      b[j] = f2_mul(s, open);
+      own[j * kBackThreads] = GATE ? f2_mul(s, open) : s;
+      bx = f2_mul(s, xo);
       // -a²/s, near 1 as s - 1/s (no digits are lost while a² is not small)
       if (NEAR) w = f2_mul(f2_fma(rs, minus, s), xo);
       else w = f2_mul(f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus)), xo);
-    } else if (SCALE == kRecComplement) {
-      b[j] = f2_mul(a.less, open);
+    } else {
+      own[j * kBackThreads] = GATE ? f2_mul(a.less, open) : a.less;
+      bx = f2_mul(a.less, xo);
       w = f2_mul(f2_mul(a.hi, minus), xo);
     }
-    const f2 bx = f2_mul(b[j], x);
     if (GATE) *gate_place(at + 2 * S, own, j) = f2_mul(bx, shut);
+    hi[j] = a.hi;
     const f2 ah = f2_fma(a.hi, m.S, f2_mul(a.lo, m.S));
     V[j] = SCALE == kRecPlain ? ah : f2_add(ah, w);
     m.S = f2_add(ah, bx);
     lengthen(m.A, m.Al, a.hi, a.lo);
     P[j] = m.A;
+    r = f2_fma(m.A, pair_at<IO>(at + 3 * S), r);
   }
   return m;
 }
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   constexpr int S = kRecTile * kChans, STAGE = 4 * S;
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const ring = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
-  f2* const own = reinterpret_cast<f2*>(ring + kStages<IO> * STAGE) + threadIdx.x;  // [kBackTok][kBackThreads], bf16 with a gate
+  f2* const own = reinterpret_cast<f2*>(ring + kBackStages<IO> * STAGE) + threadIdx.x;  // [kBackTok][kBackThreads], bf16 with a gate
   const RecArgs& p = q.f;
   const int rank = blockIdx.x % k, c0 = blockIdx.x / k * kChans, w = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (k > 1) cluster_arrive();  // every block of the cluster has started before another stores to it
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     if (copies && step >= 0) {
       const long long first = (step * k + rank) * kRecTile;
       const int t0 = (int)(first < p.T ? first : p.T);
-      IO* const d = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0);
+      IO* const d = ring + (kBackStages<IO> == 2 ? (step & 1) * STAGE : 0);
       Copy::tile(d, sx, p.x.st, t0, p.T, 0);
       Copy::tile(d + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
       if (GATE) Copy::tile(d + 2 * S, si, p.i.st, t0, p.T, 0);
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   const bool near = DECAY == kRecRate && near_rates(rate);
 
   if (!q.gy.p)  // no copies: zeros
-    for (int i = threadIdx.x; i < kStages<IO> * S * (int)sizeof(IO) / 16; i += kBackThreads)
+    for (int i = threadIdx.x; i < kBackStages<IO> * S * (int)sizeof(IO) / 16; i += kBackThreads)
       reinterpret_cast<uint4*>(ring + (i / (S * (int)sizeof(IO) / 16)) * STAGE + 3 * S)[i % (S * (int)sizeof(IO) / 16)] = make_uint4(0, 0, 0, 0);
   const f2 one = f2_both(1.f), minus_rate = f2_mul(rate, f2_both(-1.f));
   const long long steps = ((long long)p.T + kRecTile * k - 1) / (kRecTile * k);
@@ -158,21 +161,12 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     if (live && first < p.T) h = *reinterpret_cast<const f2*>(p.ckpt + first / kRecTile * p.C + c);
     cp_async_wait<0>();
     __syncthreads();
-    if (kStages<IO> == 2) fetch(step - 1);  // (the last loop of the step before has read that stage)
-    IO* const tile = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0) + w * kBackTok * kChans + 2 * lane;
-    f2 Q[kBackTok], R[kBackTok], P[kBackTok], V[kBackTok], b[kBackTok];  // Q, R: the decays first
+    if (kBackStages<IO> == 2) fetch(step - 1);  // (the last loop of the step before has read that stage)
+    IO* const tile = ring + (kBackStages<IO> == 2 ? (step & 1) * STAGE : 0) + w * kBackTok * kChans + 2 * lane;
+    f2 hi[kBackTok], P[kBackTok], V[kBackTok], r;
     Map m;
-    if (near) m = forth<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(tile, own, rate, Q, R, P, V, b);
-    else m = forth<IO, DECAY, SCALE, GATE, false>(tile, own, rate, Q, R, P, V, b);
-    f2 r = 0, prod = one;
-#pragma unroll
-    for (int j = kBackTok - 1; j >= 0; --j) {
-      const f2 hi = Q[j], lo = R[j];
-      R[j] = f2_add(r, pair_at<IO>(tile + 3 * S + j * kChans));
-      r = f2_fma(hi, R[j], f2_mul(lo, R[j]));
-      Q[j] = prod;
-      prod = f2_mul(prod, hi);
-    }
+    if (near) m = forth<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(tile, own, rate, hi, P, V, r);
+    else m = forth<IO, DECAY, SCALE, GATE, false>(tile, own, rate, hi, P, V, r);
     maps[w][0][lane] = m.A, maps[w][1][lane] = m.Al, maps[w][2][lane] = m.S, maps[w][3][lane] = r;
     __syncthreads();
     f2 next = z;
@@ -213,9 +207,10 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     if (t0 < p.T) {
       const int n = (int)min((long long)kBackTok, p.T - t0);
 #pragma unroll
-      for (int j = 0; j < kBackTok; ++j) {
+      for (int j = kBackTok - 1; j >= 0; --j) {
         IO* const o = tile + j * kChans;
-        const f2 G = f2_fma(Q[j], behind, R[j]);
+        const f2 G = f2_add(behind, pair_at<IO>(o + 3 * S));
+        behind = f2_mul(hi[j], G);
         f2 by_log = f2_mul(G, f2_fma(P[j], h, V[j]));
         if (DECAY != kRecLog) {
           const f2 e = kept(o + S, o + 2 * S), open = f2_rcp(f2_add(one, e)), shut = f2_mul(e, open);
@@ -229,7 +224,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
         }
         f2 by_gate = 0;
         if (GATE) by_gate = f2_mul(G, *gate_place(o + 2 * S, own, j));
-        put_pair(o, f2_mul(G, b[j]));
+        put_pair(o, SCALE == kRecPlain && !GATE ? G : f2_mul(G, own[j * kBackThreads]));
         put_pair(o + S, by_log);
         if (GATE) put_pair(o + 2 * S, by_gate);
       }
@@ -238,7 +233,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
       if (copies) {
         constexpr int ROWS = 32 / Copy::GROUPS;
         const int row = lane / Copy::GROUPS;
-        const IO* const from = ring + (kStages<IO> == 2 ? (step & 1) * STAGE : 0) + (w * kBackTok + row) * kChans + Copy::group();
+        const IO* const from = ring + (kBackStages<IO> == 2 ? (step & 1) * STAGE : 0) + (w * kBackTok + row) * kChans + Copy::group();
         IO *ox = gx + (t0 + row) * q.gx.st, *og = gg + (t0 + row) * q.gg.st, *oi = gi + (t0 + row) * q.gi.st;
 #pragma unroll
         for (int r = 0; r < kBackTok; r += ROWS) {
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
         }
       }
     }
-    if (kStages<IO> == 1) {
+    if (kBackStages<IO> == 1) {
       __syncthreads();
       fetch(step - 1);
     }
@@ -272,16 +267,13 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
 }  // namespace rec
 
 template <typename IO>
-cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int num_sms, int* parts, cudaStream_t s) {
-  const int tiles = (a.f.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, (a.f.T + kRecTile - 1) / kRecTile, num_sms * 2);
-  const size_t tile = 4 * (size_t)kRecTile * rec::kChans * sizeof(IO);
-  const size_t smem = rec::block_maps_bytes(k) + rec::kStages<IO> * tile +
-                      (sizeof(IO) == 2 && a.f.i.p ? (size_t)rec::kBackTok * rec::kBackThreads * sizeof(f2) : 0);
-  *parts = k;
+cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int* parts, cudaStream_t s) {
   return rec::by_kind(a.f, [&](auto d, auto sc, auto gate) {
-    return rec::launch_rec_cluster(
-        rec::kla_recurrence_grad_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>, a, tiles, k,
-        rec::kBackThreads, smem, s);
+    constexpr size_t ring = rec::kBackStages<IO> * 4 * (size_t)kRecTile * rec::kChans * sizeof(IO);
+    constexpr size_t own = (sizeof(IO) == 2 && decltype(gate)::value ? 2 : 1) * (size_t)rec::kBackTok * rec::kBackThreads * sizeof(f2);
+    return rec::launch_clusters<rec::kla_recurrence_grad_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
+                                rec::kBackThreads, ring + own>(a, (a.f.C + rec::kChans - 1) / rec::kChans,
+                                                               (a.f.T + kRecTile - 1) / kRecTile, parts, s);
   });
 }
 

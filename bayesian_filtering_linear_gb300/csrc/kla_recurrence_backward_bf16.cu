@@ -2,5 +2,5 @@
 #include "kla_recurrence_backward.cuh"
 
 namespace kla {
-template cudaError_t launch_recurrence_backward_io<__nv_bfloat16>(const RecGradArgs&, int, int*, cudaStream_t);
+template cudaError_t launch_recurrence_backward_io<__nv_bfloat16>(const RecGradArgs&, int*, cudaStream_t);
 }  // namespace kla

@@ -9,8 +9,7 @@
 // cluster of blocks goes along the sequence, a tile of 64 tokens a block at a
 // time. A warp runs through its sixteen tokens from a state of zero, keeping for
 // each the outcome Y and the product P of the decays so far, and leaves its map
-// (A, S); from then on the tile's inputs are no longer needed, and the next tile's
-// are sent for into the same place. The maps of the block's warps meet in shared
+// (A, S), while the next tile is on its way. The maps of the block's warps meet in shared
 // memory, those of the cluster's blocks are stored in each other's, and from
 // them every warp knows the state h that it starts from: y_t = P_t h + Y_t.
 // Nothing waits but barriers and nothing goes through memory.
@@ -21,15 +20,13 @@
 namespace kla {
 namespace rec {
 
-#ifndef REC_OCC
-#define REC_OCC 4
-#define REC_STAGES 1
-#define REC_WARPS 4
-#define REC_TOK 16
-#define REC_OCCF 3
-#endif
-constexpr int kOcc = REC_OCC, kStg = REC_STAGES;
-constexpr int kWarps = REC_WARPS, kThreads = 32 * kWarps, kTok = REC_TOK, kTile = kWarps * kTok;  // tokens a warp, a tile
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kTok = 16, kTile = kWarps * kTok;  // tokens a warp, a tile
+// Stages of the ring of tiles and blocks an SM. In bf16 a second stage and a fourth block are better than a fifth block
+// (headline 70 us with one stage; five blocks of 96 registers 90) or three blocks (76); fp32 tiles are twice as large.
+template <typename IO>
+constexpr int kStages = sizeof(IO) == 2 ? 2 : 1;
+template <typename IO>
+constexpr int kBlocks = sizeof(IO) == 2 ? 4 : 3;
 
 // A decay and the factor s σ(i) x of a pair, from what is read.
 template <typename IO, int DECAY, bool NEAR>
@@ -68,9 +65,8 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
 }
 
 template <typename IO, int DECAY, int SCALE, bool GATE>
-__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? kOcc : REC_OCCF) kla_recurrence_kernel(const RecArgs p, int k) {
+__global__ void __launch_bounds__(kThreads, kBlocks<IO>) kla_recurrence_kernel(const RecArgs p, int k) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ f2 maps[kWarps][3][32];
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const tile = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
   constexpr int S = kTile * kChans, STAGE = (GATE ? 3 : 2) * S;
@@ -88,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? kOcc : REC_OCCF) k
   auto fetch = [&](long long step) {
     const long long first = (step * k + rank) * kTile;
     const int t0 = (int)(first < p.T ? first : p.T);
-    IO* const d = tile + (step % kStg) * STAGE;
+    IO* const d = tile + (kStages<IO> == 2 ? (step & 1) * STAGE : 0);
     if (copies) {
       Copy::tile(d, sx, p.x.st, t0, p.T, 0);
       Copy::tile(d + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
@@ -114,14 +110,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? kOcc : REC_OCCF) k
     cp_async_wait<0>();
     __syncthreads();
     f2 P[kTok], Y[kTok];
-    if (kStg == 2 && step + 1 < steps) fetch(step + 1);
-    const IO* const mine = tile + (step % kStg) * STAGE + w * kTok * kChans + 2 * lane;
+    if (kStages<IO> == 2 && step + 1 < steps) fetch(step + 1);
+    IO* const now = tile + (kStages<IO> == 2 ? (step & 1) * STAGE : 0);
+    const IO* const mine = now + w * kTok * kChans + 2 * lane;
+    // the warps' maps: over their own rows of x, which no one needs any more, or, where the next tile comes there, behind the ring
+    const auto map_of = [&](int v) {
+      return reinterpret_cast<f2*>(kStages<IO> == 2 ? now + v * kTok * kChans : tile + STAGE) + (kStages<IO> == 2 ? 0 : 96 * v) + lane;
+    };
     Map m;
     if (near) m = segment<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(mine, rate, P, Y);
     else m = segment<IO, DECAY, SCALE, GATE, false>(mine, rate, P, Y);
-    maps[w][0][lane] = m.A, maps[w][1][lane] = m.Al, maps[w][2][lane] = m.S;
+    __syncwarp();
+    map_of(w)[0] = m.A, map_of(w)[32] = m.Al, map_of(w)[64] = m.S;
     __syncthreads();
-    if (kStg == 1 && step + 1 < steps) fetch(step + 1);
+    if (kStages<IO> == 1 && step + 1 < steps) fetch(step + 1);
     f2 next = h;
     if (k > 1) {  // the block's map to every block of the cluster
       BlockMap* const half = blocks + (step & 1) * k;
@@ -129,8 +131,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? kOcc : REC_OCCF) k
       if (w == 0) {
 #pragma unroll
         for (int v = 1; v < kWarps; ++v) {
-          const f2 A = maps[v][0][lane], Al = maps[v][1][lane];
-          m.S = apply(A, Al, maps[v][2][lane], m.S);
+          const f2 A = map_of(v)[0], Al = map_of(v)[32];
+          m.S = apply(A, Al, map_of(v)[64], m.S);
           lengthen(m.A, m.Al, A, Al);
         }
         for (int r = 0; r < k; ++r) {
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? kOcc : REC_OCCF) k
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) {
       if (v == w) mystart = h;
-      if (k == 1 || v < w) h = apply(maps[v][0][lane], maps[v][1][lane], maps[v][2][lane], h);
+      if (k == 1 || v < w) h = apply(map_of(v)[0], map_of(v)[32], map_of(v)[64], h);
     }
     if (k > 1) h = next;
     if (live && y) {
@@ -207,12 +209,13 @@ inline cudaError_t by_kind(const RecArgs& a, F f) {
 }  // namespace rec
 
 template <typename IO>
-cudaError_t launch_recurrence_io(const RecArgs& a, int num_sms, cudaStream_t s) {
-  const int tiles = (a.C + rec::kChans - 1) / rec::kChans, k = rec_cluster(tiles, (a.T + rec::kTile - 1) / rec::kTile, num_sms * (sizeof(IO) == 2 ? rec::kOcc : REC_OCCF));
-  const size_t smem = rec::block_maps_bytes(k) + rec::kStg * (a.i.p ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
+cudaError_t launch_recurrence_io(const RecArgs& a, cudaStream_t s) {
   return rec::by_kind(a, [&](auto d, auto sc, auto gate) {
-    return rec::launch_rec_cluster(rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
-                                   a, tiles, k, rec::kThreads, smem, s);
+    constexpr size_t ring = rec::kStages<IO> * (decltype(gate)::value ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
+    constexpr size_t maps = rec::kStages<IO> == 2 ? 0 : rec::kWarps * 96 * sizeof(f2);
+    return rec::launch_clusters<rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
+                                rec::kThreads, ring + maps>(a, (a.C + rec::kChans - 1) / rec::kChans, (a.T + rec::kTile - 1) / rec::kTile,
+                                                            nullptr, s);
   });
 }
 
