@@ -117,6 +117,30 @@ __device__ __forceinline__ void lengthen(f2& A, f2& Al, f2 hi, f2 lo) {
   A = p;
 }
 
+// The product of a segment's decays so far: by logarithms, where those are known,
+// its value for the tokens' outcomes and the sum, of which the segment's own
+// A comes in the end; else in two floats all along.
+template <int DECAY>
+struct Product {
+  f2 A = f2_both(1.f), rest = 0;  // rest: the sum of -log a, or what A leaves
+  __device__ __forceinline__ void times(const Decay& a, f2 y) {
+    if (DECAY == kRecSigmoid) {
+      lengthen(A, rest, a.hi, a.lo);
+    } else {
+      A = f2_mul(a.hi, A);
+      rest = f2_add(rest, y);
+    }
+  }
+  __device__ __forceinline__ void end(Map& m) const {
+    if (DECAY == kRecSigmoid) {
+      m.A = A, m.Al = rest;
+    } else {
+      const Decay a = decay_of_log<false>(rest);
+      m.A = a.hi, m.Al = a.lo;
+    }
+  }
+};
+
 // ---- a token's pair of channels -------------------------------------------------
 template <typename IO>
 __device__ __forceinline__ f2 pair_at(const IO* p);

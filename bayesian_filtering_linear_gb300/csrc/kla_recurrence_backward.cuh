@@ -53,7 +53,8 @@ template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
 __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackTok], f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2& r) {
   constexpr int S = kRecTile * kChans;
   const f2 one = f2_both(1.f), minus = f2_both(-1.f);
-  Map m{one, 0, 0};
+  Map m{0, 0, 0};
+  Product<DECAY> prod;
   r = 0;
 #pragma unroll
   for (int j = 0; j < kBackTok; ++j) {
@@ -66,13 +67,14 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
       shut = f2_mul(e, open);
     }
     Decay a;
+    f2 y = 0;  // -log a, but for a sigmoid
     if (DECAY == kRecLog) {
-      a = decay_of_log<NEAR>(minus_pair_at(at + S));
+      a = decay_of_log<NEAR>(y = minus_pair_at(at + S));
     } else {
       const f2 e = f2_exp_neg_held(pair_at<IO>(at + S));
       keep(at + S, at + 2 * S, e);
       if (DECAY == kRecSigmoid) a = decay_of_sigmoid(e);
-      else a = decay_of_log<NEAR>(f2_mul(rate, f2_rcp(f2_add(one, e))));
+      else a = decay_of_log<NEAR>(y = f2_mul(rate, f2_rcp(f2_add(one, e))));
     }
     const f2 xo = GATE ? f2_mul(x, open) : x;
     f2 w = 0, bx = xo;  // s' σ(i) x and s σ(i) x
@@ -95,10 +97,11 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
     const f2 ah = f2_fma(a.hi, m.S, f2_mul(a.lo, m.S));
     V[j] = SCALE == kRecPlain ? ah : f2_add(ah, w);
     m.S = f2_add(ah, bx);
-    lengthen(m.A, m.Al, a.hi, a.lo);
-    P[j] = m.A;
-    r = f2_fma(m.A, pair_at<IO>(at + 3 * S), r);
+    prod.times(a, y);
+    P[j] = prod.A;
+    r = f2_fma(prod.A, pair_at<IO>(at + 3 * S), r);
   }
+  prod.end(m);
   return m;
 }
 
@@ -106,6 +109,7 @@ template <typename IO, int DECAY, int SCALE, bool GATE>
 __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(const RecGradArgs q, int k) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ f2 maps[kBackWarps][4][32];
+  __shared__ const IO* places[Copier<IO, kBackThreads, kRecTile>::GROUPS][7];
   constexpr int S = kRecTile * kChans, STAGE = 4 * S;
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const ring = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
@@ -119,19 +123,27 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   const int cc = c0 + Copy::group();
   const bool copies = cc < p.C;
   const Place at(copies ? cc : 0, p.H, p.D);
-  const IO* const sx = reinterpret_cast<const IO*>(p.x.p) + at.of(p.x);
-  const IO* const sg = reinterpret_cast<const IO*>(p.g.p) + at.of(p.g);
-  const IO* const si = reinterpret_cast<const IO*>(p.i.p) + (GATE ? at.of(p.i) : 0);
-  const IO* const sy = reinterpret_cast<const IO*>(q.gy.p) + (q.gy.p ? at.of(q.gy) : 0);
-  auto fetch = [&](long long step) {
+  // (kept in shared memory: the registers are needed)
+  const IO** const from = places[threadIdx.x % Copy::GROUPS];
+  if (threadIdx.x < Copy::GROUPS) {
+    from[0] = reinterpret_cast<const IO*>(p.x.p) + at.of(p.x);
+    from[1] = reinterpret_cast<const IO*>(p.g.p) + at.of(p.g);
+    if (GATE) from[2] = reinterpret_cast<const IO*>(p.i.p) + at.of(p.i);
+    if (q.gy.p) from[3] = reinterpret_cast<const IO*>(q.gy.p) + at.of(q.gy);
+    from[4] = reinterpret_cast<const IO*>(q.gx.p) + at.of(q.gx);
+    from[5] = reinterpret_cast<const IO*>(q.gg.p) + at.of(q.gg);
+    if (GATE) from[6] = reinterpret_cast<const IO*>(q.gi.p) + at.of(q.gi);
+  }
+  __syncthreads();
+  auto fetch = [&](int step) {
     if (copies && step >= 0) {
-      const long long first = (step * k + rank) * kRecTile;
+      const long long first = ((long long)step * k + rank) * kRecTile;
       const int t0 = (int)(first < p.T ? first : p.T);
       IO* const d = ring + (kBackStages<IO> == 2 ? (step & 1) * STAGE : 0);
-      Copy::tile(d, sx, p.x.st, t0, p.T, 0);
-      Copy::tile(d + S, sg, p.g.st, t0, p.T, still<IO, DECAY>());
-      if (GATE) Copy::tile(d + 2 * S, si, p.i.st, t0, p.T, 0);
-      if (q.gy.p) Copy::tile(d + 3 * S, sy, q.gy.st, t0, p.T, 0);
+      Copy::tile(d, from[0], p.x.st, t0, p.T, 0);
+      Copy::tile(d + S, from[1], p.g.st, t0, p.T, still<IO, DECAY>());
+      if (GATE) Copy::tile(d + 2 * S, from[2], p.i.st, t0, p.T, 0);
+      if (q.gy.p) Copy::tile(d + 3 * S, from[3], q.gy.st, t0, p.T, 0);
     }
     cp_async_commit();
   };
@@ -140,9 +152,6 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   const int c = c0 + 2 * lane;
   const bool live = c < p.C;
   const Place my(live ? c : 0, p.H, p.D);
-  IO* const gx = reinterpret_cast<IO*>(q.gx.p) + at.of(q.gx);  // as this thread's copies
-  IO* const gg = reinterpret_cast<IO*>(q.gg.p) + at.of(q.gg);
-  IO* const gi = reinterpret_cast<IO*>(q.gi.p) + (GATE ? at.of(q.gi) : 0);
   f2 rate = 0, z = 0, sum = 0;  // z: what reaches the step's last token from behind it
   if (DECAY == kRecRate && live)
     rate = *reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d);
@@ -153,10 +162,10 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     for (int i = threadIdx.x; i < kBackStages<IO> * S * (int)sizeof(IO) / 16; i += kBackThreads)
       reinterpret_cast<uint4*>(ring + (i / (S * (int)sizeof(IO) / 16)) * STAGE + 3 * S)[i % (S * (int)sizeof(IO) / 16)] = make_uint4(0, 0, 0, 0);
   const f2 one = f2_both(1.f), minus_rate = f2_mul(rate, f2_both(-1.f));
-  const long long steps = ((long long)p.T + kRecTile * k - 1) / (kRecTile * k);
+  const int steps = (int)(((long long)p.T + kRecTile * k - 1) / (kRecTile * k));
   fetch(steps - 1);
-  for (long long step = steps - 1; step >= 0; --step) {
-    const long long first = (step * k + rank) * kRecTile, t0 = first + w * kBackTok;
+  for (int step = steps - 1; step >= 0; --step) {
+    const long long first = ((long long)step * k + rank) * kRecTile, t0 = first + w * kBackTok;
     f2 h = 0;
     if (live && first < p.T) h = *reinterpret_cast<const f2*>(p.ckpt + first / kRecTile * p.C + c);
     cp_async_wait<0>();
@@ -233,17 +242,16 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
       if (copies) {
         constexpr int ROWS = 32 / Copy::GROUPS;
         const int row = lane / Copy::GROUPS;
-        const IO* const from = ring + (kBackStages<IO> == 2 ? (step & 1) * STAGE : 0) + (w * kBackTok + row) * kChans + Copy::group();
-        IO *ox = gx + (t0 + row) * q.gx.st, *og = gg + (t0 + row) * q.gg.st, *oi = gi + (t0 + row) * q.gi.st;
+        const IO* const rows = ring + (kBackStages<IO> == 2 ? (step & 1) * STAGE : 0) + (w * kBackTok + row) * kChans + Copy::group();
+        const auto leave = [&](int stream, long long st) {
+          IO* out = const_cast<IO*>(from[4 + stream]) + (t0 + row) * st;
 #pragma unroll
-        for (int r = 0; r < kBackTok; r += ROWS) {
-          if (row + r < n) {
-            *reinterpret_cast<uint4*>(ox) = *reinterpret_cast<const uint4*>(from + r * kChans);
-            *reinterpret_cast<uint4*>(og) = *reinterpret_cast<const uint4*>(from + r * kChans + S);
-            if (GATE) *reinterpret_cast<uint4*>(oi) = *reinterpret_cast<const uint4*>(from + r * kChans + 2 * S);
-          }
-          ox += ROWS * q.gx.st, og += ROWS * q.gg.st, oi += ROWS * q.gi.st;
-        }
+          for (int r = 0; r < kBackTok; r += ROWS, out += ROWS * st)
+            if (row + r < n) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(rows + r * kChans + stream * S);
+        };
+        leave(0, q.gx.st);
+        leave(1, q.gg.st);
+        if (GATE) leave(2, q.gi.st);
       }
     }
     if (kBackStages<IO> == 1) {

@@ -28,12 +28,14 @@ constexpr int kStages = sizeof(IO) == 2 ? 2 : 1;
 template <typename IO>
 constexpr int kBlocks = sizeof(IO) == 2 ? 4 : 3;
 
-// A decay and the factor s σ(i) x of a pair, from what is read.
+// A decay (y: -log a, but for a sigmoid) and the factor s σ(i) x of a pair, from what is read.
 template <typename IO, int DECAY, bool NEAR>
-__device__ __forceinline__ Decay decay_of(const IO* g, f2 rate) {
+__device__ __forceinline__ Decay decay_of(const IO* g, f2 rate, f2& y) {
+  y = 0;
   if (DECAY == kRecSigmoid) return decay_of_sigmoid(f2_exp_neg_held(pair_at<IO>(g)));
-  if (DECAY == kRecRate) return decay_of_log<NEAR>(f2_mul(rate, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(g)), f2_both(1.f)))));
-  return decay_of_log<NEAR>(minus_pair_at(g));
+  if (DECAY == kRecRate) y = f2_mul(rate, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(g)), f2_both(1.f))));
+  else y = minus_pair_at(g);
+  return decay_of_log<NEAR>(y);
 }
 // All of a warp's rates are too small for a decay far from 1.
 __device__ __forceinline__ bool near_rates(f2 rate) {
@@ -49,18 +51,20 @@ __device__ __forceinline__ f2 scaled(f2 x, f2 less) {
 template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
 __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f2 (&Y)[kTok]) {
   constexpr int S = kTile * kChans;  // elements a stream
-  Map m{f2_both(1.f), 0, 0};
+  Map m{0, 0, 0};
+  Product<DECAY> prod;
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    f2 x = pair_at<IO>(tile + j * kChans);
-    const Decay a = decay_of<IO, DECAY, NEAR>(tile + S + j * kChans, rate);
+    f2 x = pair_at<IO>(tile + j * kChans), y;
+    const Decay a = decay_of<IO, DECAY, NEAR>(tile + S + j * kChans, rate, y);
     x = scaled<SCALE>(x, a.less);
     if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(tile + 2 * S + j * kChans)), f2_both(1.f))));
     m.S = apply(a.hi, a.lo, x, m.S);
-    lengthen(m.A, m.Al, a.hi, a.lo);
-    P[j] = m.A;
+    prod.times(a, y);
+    P[j] = prod.A;
     Y[j] = m.S;
   }
+  prod.end(m);
   return m;
 }
 
@@ -183,7 +187,8 @@ __global__ void __launch_bounds__(128) kla_recurrence_step_kernel(const RecArgs 
   const f2 h = *reinterpret_cast<const f2*>(p.h0 + c);
   f2 x = pair_at<IO>(reinterpret_cast<const IO*>(p.x.p) + c), rate = 0;
   if (DECAY == kRecRate) rate = *reinterpret_cast<const f2*>(p.rate + c % (p.H * p.D));
-  const Decay a = decay_of<IO, DECAY, false>(reinterpret_cast<const IO*>(p.g.p) + c, rate);
+  f2 y;
+  const Decay a = decay_of<IO, DECAY, false>(reinterpret_cast<const IO*>(p.g.p) + c, rate, y);
   x = scaled<SCALE>(x, a.less);
   if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(reinterpret_cast<const IO*>(p.i.p) + c)), f2_both(1.f))));
   const f2 next = apply(a.hi, a.lo, x, h);
