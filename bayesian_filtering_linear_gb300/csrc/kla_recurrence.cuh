@@ -221,9 +221,28 @@ __device__ __forceinline__ void put_remote(const void* p, int rank, f2 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ void put_remote(const void* p, int rank, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // The maps of a cluster's blocks, [2][k], in two halves, used in turn, so that one barrier a step is enough.
+// Al, which is 2^-24 of A at most, in bf16: eight bits of it are enough, and more blocks fit an SM.
 struct BlockMap {
-  f2 A[32], Al[32], S[32];
+  f2 A[32], S[32];
+  uint32_t Al[32];
+  __device__ __forceinline__ f2 of(int lane, f2 h) const {
+    const uint32_t l = Al[lane];
+    return apply(A[lane], f2_make(__uint_as_float(l << 16), __uint_as_float(l & 0xffff0000u)), S[lane], h);
+  }
+  // into the same place of the block of rank `rank`
+  __device__ __forceinline__ void put(int lane, int rank, const Map& m) {
+    const __nv_bfloat162 l = __floats2bfloat162_rn(f2_lo(m.Al), f2_hi(m.Al));
+    put_remote(&A[lane], rank, m.A);
+    put_remote(&S[lane], rank, m.S);
+    put_remote(&Al[lane], rank, *reinterpret_cast<const uint32_t*>(&l));
+  }
 };
 __host__ __device__ constexpr size_t block_maps_bytes(int k) { return k > 1 ? 2 * (size_t)k * sizeof(BlockMap) : 0; }
 
@@ -238,7 +257,7 @@ inline cudaLaunchConfig_t cluster_config(unsigned blocks, int k, int threads, si
   cfg.dynamicSmemBytes = smem + block_maps_bytes(k);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = k > 1 ? 1 : 0;
   return cfg;
 }
 
@@ -254,7 +273,8 @@ int clusters_at_once(int device, int k) {
       cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return -1;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = cluster_config(k, k, THREADS, SMEM, attr, nullptr);
+  cudaLaunchConfig_t cfg = cluster_config(k, k, THREADS, SMEM, attr, nullptr);
+  cfg.numAttrs = 1;
   if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) return -1;
   if (keep) known[device][k].store(n + 1, std::memory_order_relaxed);
   return n;

@@ -190,17 +190,13 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
           t.S = apply(A, Al, maps[v][3][lane], t.S);
           lengthen(t.A, t.Al, A, Al);
         }
-        for (int o = 0; o < k; ++o) {
-          put_remote(&half[rank].A[lane], o, t.A);
-          put_remote(&half[rank].Al[lane], o, t.Al);
-          put_remote(&half[rank].S[lane], o, t.S);
-        }
+        for (int o = 0; o < k; ++o) half[rank].put(lane, o, t);
       }
       cluster_arrive();  // (by all: with the others' arrivals not held up by their stores, the headline took 213 us for 163)
       cluster_wait();
       for (int o = k - 1; o >= 0; --o) {
         if (o == rank) z = next;
-        next = apply(half[o].A[lane], half[o].Al[lane], half[o].S[lane], next);
+        next = half[o].of(lane, next);
       }
     }
 #pragma unroll

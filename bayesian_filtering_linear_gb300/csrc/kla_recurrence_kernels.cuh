@@ -139,18 +139,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks<IO>) kla_recurrence_kernel(c
           m.S = apply(A, Al, map_of(v)[64], m.S);
           lengthen(m.A, m.Al, A, Al);
         }
-        for (int r = 0; r < k; ++r) {
-          put_remote(&half[rank].A[lane], r, m.A);
-          put_remote(&half[rank].Al[lane], r, m.Al);
-          put_remote(&half[rank].S[lane], r, m.S);
-        }
+        for (int r = 0; r < k; ++r) half[rank].put(lane, r, m);
       }
       if (w == 0) cluster_arrive();
       else cluster_arrive_only();
       cluster_wait();
       for (int r = 0; r < k; ++r) {
         if (r == rank) h = next;
-        next = apply(half[r].A[lane], half[r].Al[lane], half[r].S[lane], next);
+        next = half[r].of(lane, next);
       }
     }
     const long long first = (step * k + rank) * kTile;

@@ -218,7 +218,8 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-# the current stream's handle without making a Stream object, where torch has it
+# the current device, and the current stream's handle without making a Stream object, where torch has them
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -608,7 +609,7 @@ def _addr(t):
 def _run(index, stream, fn, args):
     """``fn(*args, stream)`` on device ``index``, with the given or its current stream."""
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         return fn(*args, handle)
     with torch.cuda.device(index):
         return fn(*args, handle)
@@ -766,6 +767,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
 
 def _own_order(x):
     """An empty tensor of x's shape in the memory order of its first three dimensions, without gaps."""
+    B, H, T, D = x.shape
+    if x.stride() == (T * H * D, D, H * D, 1):  # [B,T,H,D] seen as [B,H,T,D]: one plain allocation
+        return torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device)
     g = torch.empty_like(x)  # a dense view's own strides; of a view with gaps, contiguous
     if g.stride() != x.stride() and x.numel():
         order = sorted(range(3), key=x.stride().__getitem__, reverse=True)
@@ -864,7 +868,7 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
             out[name] = torch.empty_like(w)
     sums = q_weight is not None or k_weight is not None
     if workspace is None and sums:
-        if index == torch.cuda.current_device():  # the size goes by the device's SMs
+        if index == _current_device():  # the size goes by the device's SMs
             nbytes = LIB.kla_norm_rope_backward_workspace_size(B, Hq, Hk, T, D)
         else:
             with torch.cuda.device(index):
@@ -886,7 +890,7 @@ def norm_rope_backward(q, k=None, q_weight=None, k_weight=None, inv_freq=None, p
 
 _DECAYS = {"log": 0, "sigmoid": 1, "rate": 2}
 _SCALES = {"none": 0, "sqrt": 1, "complement": 2}
-_RECURRENCES = {(d, s): RecurrenceOptions(n, m) for d, n in _DECAYS.items() for s, m in _SCALES.items()}
+_RECURRENCES = {(d, s): ctypes.byref(RecurrenceOptions(n, m)) for d, n in _DECAYS.items() for s, m in _SCALES.items()}
 
 
 def _recurrence_args(x, g, i, rate, state, decay, scale, tokens=True):
@@ -894,17 +898,17 @@ def _recurrence_args(x, g, i, rate, state, decay, scale, tokens=True):
     opt = _RECURRENCES.get((decay, scale))
     if opt is None:
         raise ValueError(f"unknown decay {decay!r} or scale {scale!r}")
-    B, H, T, D = x.shape if tokens else (*x.shape[:2], 1, x.shape[2])
-    dt, index = x.dtype, x.get_device()
+    shape, dt, index = x.shape, x.dtype, x.get_device()
+    B, H, T, D = shape if tokens else (*shape[:2], 1, shape[2])
     if index < 0:
         raise ValueError("inputs must be CUDA tensors")
     io = _IO.get(dt)
     if io is None:
         raise TypeError(f"unsupported I/O dtype {dt}")
-    shape, strided = x.shape, _strided if tokens else _fits
-    if not (strided(x, dt, shape, index) and strided(g, dt, shape, index) and (i is None or strided(i, dt, shape, index))):
+    fits = _strided if tokens else _fits
+    if not (fits(x, dt, shape, index) and fits(g, dt, shape, index) and (i is None or fits(i, dt, shape, index))):
         for name, t in (("x", x), ("g", g), ("i", i)):
-            if t is not None and not strided(t, dt, shape, index):
+            if t is not None and not fits(t, dt, shape, index):
                 _need(t, name, dt, shape, x.device, strided=tokens)
     if decay == "rate":
         if not _fits(rate, torch.float32, (H, D), index):
@@ -925,8 +929,15 @@ def _strided(x, dtype, shape, index):
         return False
 
 
-def _st(t):
-    return None if t is None else _Strides(*t.stride()[:3])
+def _strides_of(*tensors):
+    """The strides {batch, head, token} for the library, one array for tensors that have the same."""
+    made, out = {}, []
+    for t in tensors:
+        s = None if t is None else t.stride()
+        if s is not None and s not in made:
+            made[s] = _Strides(*s[:3])
+        out.append(None if s is None else made[s])
+    return out
 
 
 @_on_stream
@@ -958,7 +969,7 @@ def recurrence_forward(x, g, i=None, rate=None, h0=None, *, decay: str = "log", 
             _need(kept, "checkpoints", torch.float32, shape, x.device)
     st = _run(index, stream, LIB.kla_recurrence_forward,
               (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), y.data_ptr(), _addr(hT), _addr(kept),
-               B, H, T, D, _st(x), _st(g), _st(i), _st(y), io, ctypes.byref(opt)))
+               B, H, T, D, *_strides_of(x, g, i, y), io, opt))
     _check(st, "kla_recurrence_forward", y, hT, kept)
     return (y, hT) if kept is None else (y, hT, kept)
 
@@ -972,12 +983,11 @@ def recurrence_step(x, g, i, rate, state, *, decay: str = "log", scale: str = "n
     if not _fits(state, torch.float32, x.shape, index):
         _need(state, "state", torch.float32, x.shape, x.device)
     if y is None:
-        y = torch.empty_like(x)
+        y = torch.empty(x.shape, dtype=dt, device=x.device)
     elif not _fits(y, dt, x.shape, index):
         _need(y, "y", dt, x.shape, x.device)
     st = _run(index, stream, LIB.kla_recurrence_step,
-              (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), state.data_ptr(), y.data_ptr(), B, H, D, io,
-               ctypes.byref(opt)))
+              (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), state.data_ptr(), y.data_ptr(), B, H, D, io, opt))
     _check(st, "kla_recurrence_step", y, state)
     return y
 
@@ -1000,7 +1010,7 @@ def recurrence_backward(x, g, i=None, rate=None, h0=None, *, gy=None, ghT=None, 
     if i is not None:
         out["gi"] = _own_order(i)
     if rate is not None:
-        out["grate"] = torch.empty_like(rate)
+        out["grate"] = torch.empty((H, D), dtype=torch.float32, device=x.device)
     if state_grad:
         out["gh0"] = torch.empty((B, H, D), dtype=torch.float32, device=x.device)
     if workspace is None:
@@ -1013,8 +1023,7 @@ def recurrence_backward(x, g, i=None, rate=None, h0=None, *, gy=None, ghT=None, 
     st = _run(index, stream, LIB.kla_recurrence_backward,
               (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), _addr(checkpoints), _addr(gy), _addr(ghT),
                gx.data_ptr(), gg.data_ptr(), _addr(gi), _addr(out.get("grate")), _addr(out.get("gh0")), B, H, T, D,
-               _st(x), _st(g), _st(i), _st(gy), _st(gx), _st(gg), _st(gi), io, ctypes.byref(opt), _addr(workspace),
-               ws_bytes))
+               *_strides_of(x, g, i, gy, gx, gg, gi), io, opt, _addr(workspace), ws_bytes))
     _check(st, "kla_recurrence_backward")
     return out
 
@@ -1103,7 +1112,7 @@ def layer_norm_backward(x, weight=None, *, gy=None, gtotal=None, eps: float = 1e
     if param_grads or (param_grads is None and weight is not None):
         out["gweight"], out["gbias"] = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
         if workspace is None:
-            if index == torch.cuda.current_device():  # the size goes by the device's SMs
+            if index == _current_device():  # the size goes by the device's SMs
                 nbytes = LIB.kla_layer_norm_backward_workspace_size(rows, D)
             else:
                 with torch.cuda.device(index):
