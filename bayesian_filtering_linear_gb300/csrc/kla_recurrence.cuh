@@ -48,50 +48,51 @@ __device__ __forceinline__ f2 f2_exp_neg_held(f2 x) {
   return f2_make(fminf(f2_lo(e), 0x1p126f), fminf(f2_hi(e), 0x1p126f));
 }
 
-// A decay: the float nearest to it, the rest, and 1 - a.
+// A decay: a float, the rest that it leaves, and 1 - a.
 struct Decay {
   f2 hi, lo, less;
+  __device__ __forceinline__ f2 nearest() const { return f2_add(hi, lo); }
 };
-
-// hi and lo of 1 - less.
-__device__ __forceinline__ void split(Decay& a) {
-  const f2 one = f2_both(1.f), minus = f2_both(-1.f);
-  a.hi = f2_fma(a.less, minus, one);
-  a.lo = f2_fma(a.less, minus, f2_fma(a.hi, minus, one));
-}
-// Where not `near`: a itself, without a rest.
-__device__ __forceinline__ void select(Decay& a, bool n0, bool n1, f2 e) {
-  const f2 m = f2_fma(e, f2_both(-1.f), f2_both(1.f));
-  a.hi = f2_make(n0 ? f2_lo(a.hi) : f2_lo(e), n1 ? f2_hi(a.hi) : f2_hi(e));
-  a.lo = f2_make(n0 ? f2_lo(a.lo) : 0.f, n1 ? f2_hi(a.lo) : 0.f);
-  a.less = f2_make(n0 ? f2_lo(a.less) : f2_lo(m), n1 ? f2_hi(a.less) : f2_hi(m));
+__device__ __forceinline__ f2 one_minus(f2 x) { return f2_fma(x, f2_both(-1.f), f2_both(1.f)); }
+// What `hi`, at least a half, leaves of 1 - less (1 - hi is exact), where wanted.
+__device__ __forceinline__ f2 rest_of(f2 hi, f2 less, bool n0, bool n1) {
+  const f2 r = f2_fma(less, f2_both(-1.f), one_minus(hi));
+  return f2_make(n0 ? f2_lo(r) : 0.f, n1 ? f2_hi(r) : 0.f);
 }
 
-// Of y = -log a: near a = 1 (y in [0, 0.375]) a polynomial for 1 - a, elsewhere
-// the exponential. NEAR: all are. The polynomial is y (1 - c1 y + ...),
-// (1 - e^-y) / y interpolated at the five Chebyshev points of the interval, off by
-// 4.3e-8 of the value at most; Taylor's needs two terms more for that.
+// Of y = -log a: near a = 1 (y in [0, 0.375]) a polynomial for 1 - a, which
+// corrects the exponential, elsewhere that alone. NEAR: all are, and hi is the
+// float nearest to a. The polynomial is y (1 - c1 y + ...), (1 - e^-y) / y
+// interpolated at the five Chebyshev points of the interval, off by 4.3e-8 of the
+// value at most; Taylor's needs two terms more for that.
 constexpr float kNear = 0.375f;
 template <bool NEAR>
 __device__ __forceinline__ Decay decay_of_log(f2 y) {
-  Decay a;
   f2 p = f2_fma(y, f2_both(0x1.d3c856p-8f), f2_both(-0x1.523554p-5f));
   p = f2_fma(p, y, f2_both(0x1.553ae2p-3f));
   p = f2_fma(p, y, f2_both(-0x1.ffff62p-2f));
-  a.less = f2_fma(f2_mul(p, y), y, y);
-  split(a);
-  if (!NEAR)
-    select(a, fabsf(f2_lo(y) - 0.5f * kNear) <= 0.5f * kNear, fabsf(f2_hi(y) - 0.5f * kNear) <= 0.5f * kNear, f2_exp_neg(y));
+  p = f2_fma(f2_mul(p, y), y, y);
+  Decay a;
+  if (NEAR) {
+    a.less = p;
+    a.hi = one_minus(p);
+    a.lo = f2_fma(p, f2_both(-1.f), one_minus(a.hi));
+  } else {
+    const bool n0 = fabsf(f2_lo(y) - 0.5f * kNear) <= 0.5f * kNear, n1 = fabsf(f2_hi(y) - 0.5f * kNear) <= 0.5f * kNear;
+    a.hi = f2_exp_neg(y);
+    a.lo = rest_of(a.hi, p, n0, n1);
+    const f2 far = one_minus(a.hi);
+    a.less = f2_make(n0 ? f2_lo(p) : f2_lo(far), n1 ? f2_hi(p) : f2_hi(far));
+  }
   return a;
 }
 
 // Of a sigmoid: e = e^-g (held), a = 1 / (1 + e).
 __device__ __forceinline__ Decay decay_of_sigmoid(f2 e) {
   Decay a;
-  const f2 s = f2_rcp(f2_add(e, f2_both(1.f)));
-  a.less = f2_mul(e, s);
-  split(a);
-  select(a, f2_lo(e) <= 1.f, f2_hi(e) <= 1.f, s);
+  a.hi = f2_rcp(f2_add(e, f2_both(1.f)));
+  a.less = f2_mul(e, a.hi);
+  a.lo = rest_of(a.hi, a.less, f2_lo(e) <= 1.f, f2_hi(e) <= 1.f);
   return a;
 }
 
@@ -120,17 +121,18 @@ __device__ __forceinline__ void lengthen(f2& A, f2& Al, f2 hi, f2 lo) {
 // The product of a segment's decays so far: by logarithms, where those are known,
 // its value for the tokens' outcomes and the sum, of which the segment's own
 // A comes in the end; else in two floats all along.
-template <int DECAY>
+template <int DECAY, bool NEAR>
 struct Product {
   f2 A = f2_both(1.f), rest = 0;  // rest: the sum of -log a, or what A leaves
   __device__ __forceinline__ void times(const Decay& a, f2 y) {
     if (DECAY == kRecSigmoid) {
       lengthen(A, rest, a.hi, a.lo);
     } else {
-      A = f2_mul(a.hi, A);
+      A = NEAR ? f2_mul(a.hi, A) : f2_fma(a.hi, A, f2_mul(a.lo, A));
       rest = f2_add(rest, y);
     }
   }
+  __device__ __forceinline__ f2 value() const { return DECAY == kRecSigmoid ? f2_add(A, rest) : A; }
   __device__ __forceinline__ void end(Map& m) const {
     if (DECAY == kRecSigmoid) {
       m.A = A, m.Al = rest;

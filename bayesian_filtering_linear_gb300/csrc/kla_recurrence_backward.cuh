@@ -54,7 +54,7 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
   constexpr int S = kRecTile * kChans;
   const f2 one = f2_both(1.f), minus = f2_both(-1.f);
   Map m{0, 0, 0};
-  Product<DECAY> prod;
+  Product<DECAY, NEAR> prod;
   r = 0;
 #pragma unroll
   for (int j = 0; j < kBackTok; ++j) {
@@ -93,13 +93,13 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
       w = f2_mul(f2_mul(a.hi, minus), xo);
     }
     if (GATE) *gate_place(at + 2 * S, own, j) = f2_mul(bx, shut);
-    hi[j] = a.hi;
+    hi[j] = NEAR ? a.hi : a.nearest();
     const f2 ah = f2_fma(a.hi, m.S, f2_mul(a.lo, m.S));
     V[j] = SCALE == kRecPlain ? ah : f2_add(ah, w);
     m.S = f2_add(ah, bx);
     prod.times(a, y);
-    P[j] = prod.A;
-    r = f2_fma(prod.A, pair_at<IO>(at + 3 * S), r);
+    P[j] = prod.value();
+    r = f2_fma(P[j], pair_at<IO>(at + 3 * S), r);
   }
   prod.end(m);
   return m;

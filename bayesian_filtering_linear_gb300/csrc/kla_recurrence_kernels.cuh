@@ -52,7 +52,7 @@ template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
 __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f2 (&Y)[kTok]) {
   constexpr int S = kTile * kChans;  // elements a stream
   Map m{0, 0, 0};
-  Product<DECAY> prod;
+  Product<DECAY, NEAR> prod;
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
     f2 x = pair_at<IO>(tile + j * kChans), y;
@@ -61,7 +61,7 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
     if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(tile + 2 * S + j * kChans)), f2_both(1.f))));
     m.S = apply(a.hi, a.lo, x, m.S);
     prod.times(a, y);
-    P[j] = prod.A;
+    P[j] = prod.value();
     Y[j] = m.S;
   }
   prod.end(m);
