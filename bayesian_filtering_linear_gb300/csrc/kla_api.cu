@@ -1123,7 +1123,8 @@ kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, 
   const void* ptrs[] = {x, g, i, rate, h0, checkpoints, gy, ghT, gx, gg, gi, grate, gh0, workspace};
   for (const void* ptr : ptrs)
     if (ptr && !aligned16(ptr)) return KLA_ERR_MISALIGNED;
-  const size_t need = recurrence_backward_bytes(B, H, T, D, checkpoints != nullptr);
+  // (the sums alone are wanted where the checkpoints are given)
+  const size_t need = !checkpoints || grate ? recurrence_backward_bytes(B, H, T, D, checkpoints != nullptr) : 0;
   const size_t z = io_size(io), states = (size_t)bh * D * sizeof(float), rates = (size_t)H * D * sizeof(float);
   const Range ins[] = {{x, span[0] * z}, {g, span[1] * z}, {i, span[2] * z}, {rate, rates}, {h0, states},
                        {checkpoints, recurrence_checkpoint_bytes(B, H, T, D)}, {gy, span[3] * z}, {ghT, states}};

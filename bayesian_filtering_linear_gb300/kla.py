@@ -157,7 +157,9 @@ def _check(status: int, where: str, *written):
     if status != OK:
         raise KlaError(status, where)
     if written:
-        torch.autograd.graph.increment_version([t for t in written if t is not None])
+        written = [t for t in written if t is not None]
+        if written:
+            torch.autograd.graph.increment_version(written)
 
 
 def status_string(status: int) -> str:
@@ -893,51 +895,57 @@ _SCALES = {"none": 0, "sqrt": 1, "complement": 2}
 _RECURRENCES = {(d, s): ctypes.byref(RecurrenceOptions(n, m)) for d, n in _DECAYS.items() for s, m in _SCALES.items()}
 
 
-def _recurrence_args(x, g, i, rate, state, decay, scale, tokens=True):
-    """Checks of what the recurrence's calls share; ``state``: (name, tensor or None)."""
+def _strided(x, dtype, shape, index):
+    """The strides of a tensor of this dtype and shape on CUDA device ``index`` whose last dimension is contiguous, or None."""
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == index:
+            strides = x.stride()
+            if strides[-1] == 1 or not x.numel():
+                return strides
+    except AttributeError:
+        pass
+    return None
+
+
+@functools.lru_cache(maxsize=256)
+def _triple(strides):
+    """{batch, head, token} of a tensor's strides, for the library."""
+    return _Strides(*strides[:3])
+
+
+def _recurrence_args(x, g, i, rate, decay, scale, tokens=True):
+    """Checks of what the recurrence's calls share."""
     opt = _RECURRENCES.get((decay, scale))
     if opt is None:
         raise ValueError(f"unknown decay {decay!r} or scale {scale!r}")
     shape, dt, index = x.shape, x.dtype, x.get_device()
-    B, H, T, D = shape if tokens else (*shape[:2], 1, shape[2])
     if index < 0:
         raise ValueError("inputs must be CUDA tensors")
     io = _IO.get(dt)
     if io is None:
         raise TypeError(f"unsupported I/O dtype {dt}")
+    if len(shape) != (4 if tokens else 3):
+        raise ValueError(f"x has shape {tuple(shape)}, expected {'[B,H,T,D]' if tokens else '[B,H,D]'}")
     fits = _strided if tokens else _fits
-    if not (fits(x, dt, shape, index) and fits(g, dt, shape, index) and (i is None or fits(i, dt, shape, index))):
+    sx, sg, si = fits(x, dt, shape, index), fits(g, dt, shape, index), i is None or fits(i, dt, shape, index)
+    if not (sx and sg and si):
         for name, t in (("x", x), ("g", g), ("i", i)):
             if t is not None and not fits(t, dt, shape, index):
                 _need(t, name, dt, shape, x.device, strided=tokens)
     if decay == "rate":
-        if not _fits(rate, torch.float32, (H, D), index):
-            _need(rate, "rate", torch.float32, (H, D), x.device)
+        rates = (shape[1], shape[-1])
+        if not _fits(rate, torch.float32, rates, index):
+            _need(rate, "rate", torch.float32, rates, x.device)
     elif rate is not None:
         raise ValueError(f"decay {decay!r} takes no rate")
-    for name, t in state:
-        if t is not None and not _fits(t, torch.float32, (B, H, D), index):
-            _need(t, name, torch.float32, (B, H, D), x.device)
-    return B, H, T, D, index, dt, io, opt
+    if not tokens:
+        return shape, index, dt, io, opt
+    return shape, index, dt, io, opt, _triple(sx), _triple(sg), None if i is None else _triple(si)
 
 
-def _strided(x, dtype, shape, index):
-    """A tensor of this dtype and shape on CUDA device ``index`` whose last dimension is contiguous."""
-    try:
-        return x.dtype is dtype and x.shape == shape and x.get_device() == index and (x.stride(-1) == 1 or not x.numel())
-    except AttributeError:
-        return False
-
-
-def _strides_of(*tensors):
-    """The strides {batch, head, token} for the library, one array for tensors that have the same."""
-    made, out = {}, []
-    for t in tensors:
-        s = None if t is None else t.stride()
-        if s is not None and s not in made:
-            made[s] = _Strides(*s[:3])
-        out.append(None if s is None else made[s])
-    return out
+def _need_state(t, name, shape, index, device):
+    if t is not None and not _fits(t, torch.float32, shape, index):
+        _need(t, name, torch.float32, shape, device)
 
 
 @_on_stream
@@ -954,23 +962,28 @@ def recurrence_forward(x, g, i=None, rate=None, h0=None, *, decay: str = "log", 
     is False and none was given); with ``checkpoints`` (True, or a buffer of an
     earlier call) also the states before every 64th token, which
     :func:`recurrence_backward` takes instead of making them again."""
-    B, H, T, D, index, dt, io, opt = _recurrence_args(x, g, i, rate, (("h0", h0), ("hT", hT)), decay, scale)
+    shape, index, dt, io, opt, sx, sg, si = _recurrence_args(x, g, i, rate, decay, scale)
+    B, H, T, D = shape
+    state, device, given = (B, H, D), x.device, (y, hT, checkpoints)
+    _need_state(h0, "h0", state, index, device)
+    _need_state(hT, "hT", state, index, device)
     if y is None:
         y = _own_order(x)
-    elif not _strided(y, dt, x.shape, index):
-        _need(y, "y", dt, x.shape, x.device, strided=True)
-    if final_state and hT is None:
-        hT = torch.empty((B, H, D), dtype=torch.float32, device=x.device)
+    sy = _strided(y, dt, shape, index)
+    if sy is None:
+        _need(y, "y", dt, shape, device, strided=True)
+    if hT is None and final_state:
+        hT = torch.empty(state, dtype=torch.float32, device=device)
     kept = None
     if checkpoints is not False and checkpoints is not None:
-        shape = ((T + 63) // 64, B, H, D)
-        kept = torch.empty(shape, dtype=torch.float32, device=x.device) if checkpoints is True else checkpoints
-        if not _fits(kept, torch.float32, shape, index):
-            _need(kept, "checkpoints", torch.float32, shape, x.device)
+        kept, shape = checkpoints, ((T + 63) // 64, B, H, D)
+        if kept is True:
+            kept = torch.empty(shape, dtype=torch.float32, device=device)
+        _need_state(kept, "checkpoints", shape, index, device)
     st = _run(index, stream, LIB.kla_recurrence_forward,
               (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), y.data_ptr(), _addr(hT), _addr(kept),
-               B, H, T, D, *_strides_of(x, g, i, y), io, opt))
-    _check(st, "kla_recurrence_forward", y, hT, kept)
+               B, H, T, D, sx, sg, si, _triple(sy), io, opt))
+    _check(st, "kla_recurrence_forward", *(t for t in given if t is not None and t is not True and t is not False))
     return (y, hT) if kept is None else (y, hT, kept)
 
 
@@ -979,16 +992,18 @@ def recurrence_step(x, g, i, rate, state, *, decay: str = "log", scale: str = "n
     """One decode token of the gated linear recurrence (kla_recurrence_step): x,
     g, i ``[B,H,D]`` (i None: no input gate; rate None unless ``decay`` is
     "rate"); the fp32 state ``[B,H,D]`` is updated in place; returns y."""
-    B, H, _, D, index, dt, io, opt = _recurrence_args(x, g, i, rate, (), decay, scale, tokens=False)
-    if not _fits(state, torch.float32, x.shape, index):
-        _need(state, "state", torch.float32, x.shape, x.device)
+    shape, index, dt, io, opt = _recurrence_args(x, g, i, rate, decay, scale, tokens=False)
+    B, H, D = shape
+    if not _fits(state, torch.float32, shape, index):
+        _need(state, "state", torch.float32, shape, x.device)
+    given = y
     if y is None:
-        y = torch.empty(x.shape, dtype=dt, device=x.device)
-    elif not _fits(y, dt, x.shape, index):
-        _need(y, "y", dt, x.shape, x.device)
+        y = torch.empty(shape, dtype=dt, device=x.device)
+    elif not _fits(y, dt, shape, index):
+        _need(y, "y", dt, shape, x.device)
     st = _run(index, stream, LIB.kla_recurrence_step,
               (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), state.data_ptr(), y.data_ptr(), B, H, D, io, opt))
-    _check(st, "kla_recurrence_step", y, state)
+    _check(st, "kla_recurrence_step", state, given)
     return y
 
 
@@ -1001,29 +1016,36 @@ def recurrence_backward(x, g, i=None, rate=None, h0=None, *, gy=None, ghT=None, 
     (None: made again). Returns a dict with ``gx, gg`` and, with an input gate,
     ``gi`` (in the memory order of x, g and i), ``grate`` with decay "rate" and,
     with ``state_grad``, ``gh0`` (fp32)."""
-    B, H, T, D, index, dt, io, opt = _recurrence_args(x, g, i, rate, (("h0", h0), ("ghT", ghT)), decay, scale)
-    if gy is not None and not _strided(gy, dt, x.shape, index):
-        _need(gy, "gy", dt, x.shape, x.device, strided=True)
-    if checkpoints is not None and not _fits(checkpoints, torch.float32, ((T + 63) // 64, B, H, D), index):
-        _need(checkpoints, "checkpoints", torch.float32, ((T + 63) // 64, B, H, D), x.device)
-    out = {"gx": _own_order(x), "gg": _own_order(g)}
+    shape, index, dt, io, opt, sx, sg, si = _recurrence_args(x, g, i, rate, decay, scale)
+    B, H, T, D = shape
+    state, device, sy = (B, H, D), x.device, None
+    _need_state(h0, "h0", state, index, device)
+    _need_state(ghT, "ghT", state, index, device)
+    _need_state(checkpoints, "checkpoints", ((T + 63) // 64, B, H, D), index, device)
+    if gy is not None:
+        sy = _strided(gy, dt, shape, index)
+        if sy is None:
+            _need(gy, "gy", dt, shape, device, strided=True)
+        sy = _triple(sy)
+    gx, gg = _own_order(x), _own_order(g)
+    out, gi, sgi, grate, gh0 = {"gx": gx, "gg": gg}, None, None, None, None
     if i is not None:
-        out["gi"] = _own_order(i)
+        out["gi"] = gi = _own_order(i)
+        sgi = _triple(gi.stride())
     if rate is not None:
-        out["grate"] = torch.empty((H, D), dtype=torch.float32, device=x.device)
+        out["grate"] = grate = torch.empty((H, D), dtype=torch.float32, device=device)
     if state_grad:
-        out["gh0"] = torch.empty((B, H, D), dtype=torch.float32, device=x.device)
-    if workspace is None:
+        out["gh0"] = gh0 = torch.empty(state, dtype=torch.float32, device=device)
+    if workspace is None and (checkpoints is None or rate is not None):
         nbytes = LIB.kla_recurrence_backward_workspace_size(B, H, T, D, checkpoints is not None)
         if nbytes == _NO_SIZE:
             raise KlaError(ERR_UNSUPPORTED_SHAPE, "kla_recurrence_backward_workspace_size")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     ws_bytes = _space(workspace, index)
-    gx, gg, gi = out["gx"], out["gg"], out.get("gi")
     st = _run(index, stream, LIB.kla_recurrence_backward,
               (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), _addr(checkpoints), _addr(gy), _addr(ghT),
-               gx.data_ptr(), gg.data_ptr(), _addr(gi), _addr(out.get("grate")), _addr(out.get("gh0")), B, H, T, D,
-               *_strides_of(x, g, i, gy, gx, gg, gi), io, opt, _addr(workspace), ws_bytes))
+               gx.data_ptr(), gg.data_ptr(), _addr(gi), _addr(grate), _addr(gh0), B, H, T, D, sx, sg, si, sy,
+               _triple(gx.stride()), _triple(gg.stride()), sgi, io, opt, _addr(workspace), ws_bytes))
     _check(st, "kla_recurrence_backward")
     return out
 
@@ -1032,6 +1054,8 @@ def recurrence_backward(x, g, i=None, rate=None, h0=None, *, gy=None, ghT=None, 
 
 def _rows(t, name, dtype, shape, index):
     """The row stride of a tensor ``[..., D]`` that is seen as rows."""
+    if _fits(t, dtype, shape, index):
+        return shape[-1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != index:
@@ -1041,8 +1065,6 @@ def _rows(t, name, dtype, shape, index):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     D = shape[-1]
-    if t.is_contiguous():
-        return D
     if t.stride(-1) == 1 or D == 1:
         if t.dim() == 2:
             return t.stride(0)
@@ -1079,20 +1101,21 @@ def layer_norm(x, weight=None, bias=None, residual=None, *, eps: float = 1e-5, y
     xs, rs = _rows(x, "x", dt, x.shape, index), 0
     if residual is not None:
         rs = _rows(residual, "residual", dt, x.shape, index)
-        if total is None:
-            total = torch.empty(x.shape, dtype=dt, device=x.device)
-        elif not _fits(total, dt, x.shape, index):
+        if total is not None and not _fits(total, dt, x.shape, index):
             _need(total, "total", dt, x.shape, x.device)
     elif total is not None:
         raise ValueError("total is written with a residual only")
+    if y is not None and not _fits(y, dt, x.shape, index):
+        _need(y, "y", dt, x.shape, x.device)
+    given = y, total
+    if residual is not None and total is None:
+        total = torch.empty(x.shape, dtype=dt, device=x.device)
     if y is None:
         y = torch.empty(x.shape, dtype=dt, device=x.device)
-    elif not _fits(y, dt, x.shape, index):
-        _need(y, "y", dt, x.shape, x.device)
     st = _run(index, stream, LIB.kla_layer_norm,
               (x.data_ptr(), _addr(weight), _addr(bias), _addr(residual), y.data_ptr(), _addr(total), rows, D, xs, rs,
                _IO[dt], eps))
-    _check(st, "kla_layer_norm", y, total)
+    _check(st, "kla_layer_norm", *given)
     return y, total
 
 

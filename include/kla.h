@@ -533,8 +533,8 @@ kla_status kla_recurrence_step(const void* x, const void* g, const void* i, cons
  *   Where a = 1 exactly the derivative of sqrt(1 − a²) has no value, and its
  *   term is left out of gg.
  *   workspace / ws_bytes: kla_recurrence_backward_workspace_size() bytes (else
- *     WORKSPACE; may be NULL when that is 0); `with_checkpoints` says whether
- *     the call gives them. */
+ *     WORKSPACE), `with_checkpoints` saying whether the call gives them; may be
+ *     NULL for a call that gives them and wants no grate. */
 size_t kla_recurrence_backward_workspace_size(int B, int H, int T, int D, int with_checkpoints);
 kla_status kla_recurrence_backward(const void* x, const void* g, const void* i, const float* rate, const float* h0,
                                    const void* checkpoints, const void* gy, const float* ghT, void* gx, void* gg,
