@@ -401,10 +401,14 @@ __global__ void __launch_bounds__(1024) kla_layer_norm_sum_kernel(const LayerNor
   }
 }
 
-// Lanes a row, pieces a lane, threads a block, and backward stages and blocks an SM
-template <int NV_, int LANES_, int THREADS_, int S_ = 2, int MIN_ = 1>
+// Pieces a lane, lanes a row and threads a block, and backward stages and blocks an SM.
+template <int NV_, int LANES_, int THREADS_>
 struct Shape {
-  static constexpr int NV = NV_, LANES = LANES_, THREADS = THREADS_, S = S_, MIN = MIN_;
+  static constexpr int NV = NV_, LANES = LANES_, THREADS = THREADS_;
+};
+template <int NV, int LANES, int THREADS, int S_, int MIN_>
+struct BackShape : Shape<NV, LANES, THREADS> {
+  static constexpr int S = S_, MIN = MIN_;
 };
 
 // Forward, by the row's width in pieces (of 16 bytes, or single elements).
@@ -432,33 +436,33 @@ void by_width(int pieces, F f) {
 template <int VEC, typename F>
 void by_width_back(int pieces, F f) {
   if constexpr (VEC == 8) {
-    if (pieces <= 8) return f(Shape<1, 8, 128, 3, 4>());
-    if (pieces <= 32) return f(Shape<1, 32, 128, 3, 4>());
-    if (pieces <= 64) return f(Shape<2, 32, 128, 3, 3>());
-    if (pieces <= 128) return f(Shape<2, 64, 128, 3, 3>());
-    if (pieces <= 256) return f(Shape<2, 128, 128, 3, 3>());
-    if (pieces <= 512) return f(Shape<2, 256, 256, 3, 2>());
-    return f(Shape<2, 512, 512, 2, 1>());
+    if (pieces <= 8) return f(BackShape<1, 8, 128, 3, 4>());
+    if (pieces <= 32) return f(BackShape<1, 32, 128, 3, 4>());
+    if (pieces <= 64) return f(BackShape<2, 32, 128, 3, 3>());
+    if (pieces <= 128) return f(BackShape<2, 64, 128, 3, 3>());
+    if (pieces <= 256) return f(BackShape<2, 128, 128, 3, 3>());
+    if (pieces <= 512) return f(BackShape<2, 256, 256, 3, 2>());
+    return f(BackShape<2, 512, 512, 2, 1>());
   } else if constexpr (VEC == 4) {
-    if (pieces <= 8) return f(Shape<1, 8, 128, 3, 4>());
-    if (pieces <= 32) return f(Shape<1, 32, 128, 3, 4>());
-    if (pieces <= 64) return f(Shape<2, 32, 128, 3, 5>());
-    if (pieces <= 128) return f(Shape<4, 32, 128, 3, 3>());
-    if (pieces <= 256) return f(Shape<4, 64, 128, 3, 3>());
-    if (pieces <= 512) return f(Shape<4, 128, 128, 3, 3>());
-    if (pieces <= 1024) return f(Shape<4, 256, 256, 3, 2>());
-    return f(Shape<4, 512, 512, 2, 1>());
+    if (pieces <= 8) return f(BackShape<1, 8, 128, 3, 4>());
+    if (pieces <= 32) return f(BackShape<1, 32, 128, 3, 4>());
+    if (pieces <= 64) return f(BackShape<2, 32, 128, 3, 5>());
+    if (pieces <= 128) return f(BackShape<4, 32, 128, 3, 3>());
+    if (pieces <= 256) return f(BackShape<4, 64, 128, 3, 3>());
+    if (pieces <= 512) return f(BackShape<4, 128, 128, 3, 3>());
+    if (pieces <= 1024) return f(BackShape<4, 256, 256, 3, 2>());
+    return f(BackShape<4, 512, 512, 2, 1>());
   } else {
-    if (pieces <= 128) return f(Shape<4, 32, 128, 4, 5>());
-    if (pieces <= 256) return f(Shape<8, 32, 128, 3, 4>());
-    if (pieces <= 384) return f(Shape<6, 64, 128, 3, 5>());
-    if (pieces <= 512) return f(Shape<8, 64, 128, 3, 4>());
-    if (pieces <= 640) return f(Shape<5, 128, 128, 4, 4>());
-    if (pieces <= 768) return f(Shape<6, 128, 128, 4, 4>());
-    if (pieces <= 1024) return f(Shape<8, 128, 128, 3, 4>());
-    if (pieces <= 2048) return f(Shape<8, 256, 256, 3, 2>());
-    if (pieces <= 4096) return f(Shape<8, 512, 512, 3, 1>());
-    return f(Shape<16, 512, 512, 2, 1>());
+    if (pieces <= 128) return f(BackShape<4, 32, 128, 4, 5>());
+    if (pieces <= 256) return f(BackShape<8, 32, 128, 3, 4>());
+    if (pieces <= 384) return f(BackShape<6, 64, 128, 3, 5>());
+    if (pieces <= 512) return f(BackShape<8, 64, 128, 3, 4>());
+    if (pieces <= 640) return f(BackShape<5, 128, 128, 4, 4>());
+    if (pieces <= 768) return f(BackShape<6, 128, 128, 4, 4>());
+    if (pieces <= 1024) return f(BackShape<8, 128, 128, 3, 4>());
+    if (pieces <= 2048) return f(BackShape<8, 256, 256, 3, 2>());
+    if (pieces <= 4096) return f(BackShape<8, 512, 512, 3, 1>());
+    return f(BackShape<16, 512, 512, 2, 1>());
   }
 }
 

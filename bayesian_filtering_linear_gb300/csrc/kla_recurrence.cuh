@@ -190,13 +190,13 @@ struct Copier {
     dst += row() * kChans + group();
     src += (long long)(t0 + row()) * st;
     const long long down = ROWS * st;
-    if (t0 + TILE <= T) {
+    if (T - t0 >= TILE) {
 #pragma unroll
       for (int r = 0; r < TILE; r += ROWS, src += down) cp_async16(dst + r * kChans, src);
     } else {
 #pragma unroll
       for (int r = 0; r < TILE; r += ROWS, src += down) {
-        if (t0 + row() + r < T) cp_async16(dst + r * kChans, src);
+        if (row() + r < T - t0) cp_async16(dst + r * kChans, src);
         else *reinterpret_cast<uint4*>(dst + r * kChans) = make_uint4(fill, fill, fill, fill);
       }
     }

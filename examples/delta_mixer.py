@@ -1,5 +1,5 @@
-"""A small model of gated delta rule layers: causal convolution, norm of queries
-and keys with the position rotation, the delta rule, and an output projection.
+"""A small model of gated delta rule layers: layer norm with the residual sum,
+causal convolution, norm of queries and keys with the position rotation, the delta rule, and an output projection.
 It learns to recall which value followed a key earlier in the sequence, then
 answers one token at a time from the carried state, and both ways agree.
 
@@ -62,13 +62,18 @@ class Recall(torch.nn.Module):
         self.mixers = torch.nn.ModuleList(DeltaMixer(width) for _ in range(layers))
         self.head = torch.nn.Linear(width, symbols)
 
+    def norm(self, i, x, y):
+        """The norm of x + y (y: what the last layer adds, None before the first), and that sum."""
+        n, total = kla.add_layer_norm(x, self.norms[i].weight, self.norms[i].bias, y, eps=self.norms[i].eps)
+        return n, x if total is None else total
+
     def forward(self, tokens, carried=None):
-        x, left = self.embed(tokens), []
+        x, y, left = self.embed(tokens), None, []
         for i, mixer in enumerate(self.mixers):
-            y, c = mixer(self.norms[i](x), None if carried is None else carried[i])
-            x = x + y
+            n, x = self.norm(i, x, y)
+            y, c = mixer(n, None if carried is None else carried[i])
             left.append(c)
-        return self.head(self.norms[-1](x)), left
+        return self.head(self.norm(-1, x, y)[0]), left
 
 
 def batch(B, pairs, symbols, generator, device):

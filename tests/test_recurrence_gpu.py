@@ -92,6 +92,12 @@ def test_clusters_of_every_size(channels):
     check(channels // 64, 2, 700, 32, "bf16", "rate", "sqrt", heads_last=True, seed=channels)
 
 
+@pytest.mark.parametrize("channels,T", [(64, 1100), (64 * 12, 1025), (64 * 18, 1400), (64 * 30, 800)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_clusters_above_eight(channels, T, io):
+    check(1, channels // 64, T, 64, io, "log", "sqrt", gate=False)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_many_channels(io):
     check(40, 16, 131, 64, io, "log", "sqrt", gate=False)
