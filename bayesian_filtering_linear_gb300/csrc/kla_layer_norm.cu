@@ -441,8 +441,8 @@ void by_width_back(int pieces, F f) {
     if (pieces <= 64) return f(BackShape<2, 32, 128, 3, 3>());
     if (pieces <= 128) return f(BackShape<2, 64, 128, 3, 3>());
     if (pieces <= 256) return f(BackShape<2, 128, 128, 3, 3>());
-    if (pieces <= 512) return f(BackShape<2, 256, 256, 3, 2>());
-    return f(BackShape<2, 512, 512, 2, 1>());
+    if (pieces <= 512) return f(BackShape<4, 128, 128, 2, 2>());
+    return f(BackShape<4, 256, 256, 3, 1>());
   } else if constexpr (VEC == 4) {
     if (pieces <= 8) return f(BackShape<1, 8, 128, 3, 4>());
     if (pieces <= 32) return f(BackShape<1, 32, 128, 3, 4>());

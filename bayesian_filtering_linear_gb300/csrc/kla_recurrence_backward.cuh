@@ -42,15 +42,39 @@ __device__ __forceinline__ void keep(__nv_bfloat16* a, __nv_bfloat16* b, f2 v) {
 __device__ __forceinline__ f2 kept(const __nv_bfloat16* a, const __nv_bfloat16* b) {
   return f2_make(*reinterpret_cast<const float*>(a), *reinterpret_cast<const float*>(b));
 }
-// The gate's terms: where i was (fp32), or in an array of their own.
-template <typename IO>
-__device__ __forceinline__ f2* gate_place(IO* i, f2* own, int j) {
-  return sizeof(IO) == 4 ? reinterpret_cast<f2*>(i) : own + (kBackTok + j) * kBackThreads;
-}
+// s σ(i) of a token's pair and, with a gate, the gate's term: in an array of the
+// thread's own, the gate's term in fp32 where i was.
+template <typename IO, bool GATE>
+struct Own {
+  static constexpr bool BOTH = GATE && sizeof(IO) == 2;
+  static constexpr size_t BYTES = (BOTH ? 2 : 1) * (size_t)kBackTok * kBackThreads * sizeof(f2);
+  f2* at;
+  __device__ __forceinline__ explicit Own(void* p) : at(reinterpret_cast<f2*>(p) + (BOTH ? 2 : 1) * threadIdx.x) {}
+  __device__ __forceinline__ void put(int j, IO* i, f2 b, f2 term) const {
+    if (BOTH) {
+      *reinterpret_cast<ulonglong2*>(at + 2 * j * kBackThreads) = make_ulonglong2(b, term);
+    } else {
+      at[j * kBackThreads] = b;
+      if (GATE) *reinterpret_cast<f2*>(i) = term;
+    }
+  }
+  __device__ __forceinline__ ulonglong2 get(int j, const IO* i) const {
+    if (BOTH) return *reinterpret_cast<const ulonglong2*>(at + 2 * j * kBackThreads);
+    return make_ulonglong2(at[j * kBackThreads], GATE ? *reinterpret_cast<const f2*>(i) : 0);
+  }
+};
+
+// What a warp's tokens do to h and to G.
+struct WarpMaps {
+  ulonglong2 A[32];  // and Al
+  f2 S[32], R[32];
+  __device__ __forceinline__ f2 h(int lane, f2 v) const { return apply(A[lane].x, A[lane].y, S[lane], v); }
+  __device__ __forceinline__ f2 g(int lane, f2 v) const { return apply(A[lane].x, A[lane].y, R[lane], v); }
+};
 
 // Forward through a warp's tokens: its maps of h and (in r) of G, and for each token the decay, P and V.
 template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
-__device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackTok], f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2& r) {
+__device__ __forceinline__ Map forth(IO* tile, const Own<IO, GATE>& own, f2 rate, f2 (&hi)[kBackTok], f2 (&P)[kBackTok], f2 (&V)[kBackTok], f2& r) {
   constexpr int S = kRecTile * kChans;
   const f2 one = f2_both(1.f), minus = f2_both(-1.f);
   Map m{0, 0, 0};
@@ -77,22 +101,20 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
       else a = decay_of_log<NEAR>(y = f2_mul(rate, f2_rcp(f2_add(one, e))));
     }
     const f2 xo = GATE ? f2_mul(x, open) : x;
-    f2 w = 0, bx = xo;  // s' σ(i) x and s σ(i) x
-    if (SCALE == kRecPlain) {
-      if (GATE) own[j * kBackThreads] = open;
-    } else if (SCALE == kRecSqrt) {
+    f2 w = 0, bx = xo, b = open;  // s' σ(i) x, s σ(i) x and s σ(i)
+    if (SCALE == kRecSqrt) {
       const f2 v = spread(a.less), rs = spread_rsqrt(v), s = f2_mul(v, rs);
-      own[j * kBackThreads] = GATE ? f2_mul(s, open) : s;
+      b = GATE ? f2_mul(s, open) : s;
       bx = f2_mul(s, xo);
       // -a²/s, near 1 as s - 1/s (no digits are lost while a² is not small)
       if (NEAR) w = f2_mul(f2_fma(rs, minus, s), xo);
       else w = f2_mul(f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus)), xo);
-    } else {
-      own[j * kBackThreads] = GATE ? f2_mul(a.less, open) : a.less;
+    } else if (SCALE == kRecComplement) {
+      b = GATE ? f2_mul(a.less, open) : a.less;
       bx = f2_mul(a.less, xo);
       w = f2_mul(f2_mul(a.hi, minus), xo);
     }
-    if (GATE) *gate_place(at + 2 * S, own, j) = f2_mul(bx, shut);
+    if (SCALE != kRecPlain || GATE) own.put(j, at + 2 * S, b, GATE ? f2_mul(bx, shut) : 0);
     hi[j] = NEAR ? a.hi : a.nearest();
     const f2 ah = f2_fma(a.hi, m.S, f2_mul(a.lo, m.S));
     V[j] = SCALE == kRecPlain ? ah : f2_add(ah, w);
@@ -108,12 +130,12 @@ __device__ __forceinline__ Map forth(IO* tile, f2* own, f2 rate, f2 (&hi)[kBackT
 template <typename IO, int DECAY, int SCALE, bool GATE>
 __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(const RecGradArgs q, int k) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ f2 maps[kBackWarps][4][32];
+  __shared__ WarpMaps maps[kBackWarps];
   __shared__ const IO* places[Copier<IO, kBackThreads, kRecTile>::GROUPS][7];
   constexpr int S = kRecTile * kChans, STAGE = 4 * S;
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const ring = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
-  f2* const own = reinterpret_cast<f2*>(ring + kBackStages<IO> * STAGE) + threadIdx.x;  // [kBackTok][kBackThreads], bf16 with a gate
+  const Own<IO, GATE> own(ring + kBackStages<IO> * STAGE);
   const RecArgs& p = q.f;
   const int rank = blockIdx.x % k, c0 = blockIdx.x / k * kChans, w = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (k > 1) cluster_arrive();  // every block of the cluster has started before another stores to it
@@ -176,7 +198,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     Map m;
     if (near) m = forth<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(tile, own, rate, hi, P, V, r);
     else m = forth<IO, DECAY, SCALE, GATE, false>(tile, own, rate, hi, P, V, r);
-    maps[w][0][lane] = m.A, maps[w][1][lane] = m.Al, maps[w][2][lane] = m.S, maps[w][3][lane] = r;
+    maps[w].A[lane] = make_ulonglong2(m.A, m.Al), maps[w].S[lane] = m.S, maps[w].R[lane] = r;
     __syncthreads();
     f2 next = z;
     if (k > 1) {  // the block's map of G to every block of the cluster
@@ -186,9 +208,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
         Map t{m.A, m.Al, r};
 #pragma unroll
         for (int v = kBackWarps - 2; v >= 0; --v) {
-          const f2 A = maps[v][0][lane], Al = maps[v][1][lane];
-          t.S = apply(A, Al, maps[v][3][lane], t.S);
-          lengthen(t.A, t.Al, A, Al);
+          t.S = maps[v].g(lane, t.S);
+          lengthen(t.A, t.Al, maps[v].A[lane].x, maps[v].A[lane].y);
         }
         for (int o = 0; o < k; ++o) half[rank].put(lane, o, t);
       }
@@ -201,12 +222,12 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     }
 #pragma unroll
     for (int v = 0; v < kBackWarps - 1; ++v)
-      if (v < w) h = apply(maps[v][0][lane], maps[v][1][lane], maps[v][2][lane], h);
+      if (v < w) h = maps[v].h(lane, h);
     f2 behind = z;
 #pragma unroll
     for (int v = kBackWarps - 1; v >= 0; --v) {
       if (v == w) behind = z;
-      if (k == 1 || v > w) z = apply(maps[v][0][lane], maps[v][1][lane], maps[v][3][lane], z);
+      if (k == 1 || v > w) z = maps[v].g(lane, z);
     }
     if (k > 1) z = next;
     if (t0 < p.T) {
@@ -227,11 +248,14 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
             by_log = f2_mul(by_log, shut);
           }
         }
-        f2 by_gate = 0;
-        if (GATE) by_gate = f2_mul(G, *gate_place(o + 2 * S, own, j));
-        put_pair(o, SCALE == kRecPlain && !GATE ? G : f2_mul(G, own[j * kBackThreads]));
+        if (SCALE == kRecPlain && !GATE) {
+          put_pair(o, G);
+        } else {
+          const ulonglong2 b = own.get(j, o + 2 * S);
+          put_pair(o, f2_mul(G, b.x));
+          if (GATE) put_pair(o + 2 * S, f2_mul(G, b.y));
+        }
         put_pair(o + S, by_log);
-        if (GATE) put_pair(o + 2 * S, by_gate);
       }
       __syncwarp();
       // the warp's rows leave in pieces of 16 bytes
@@ -258,11 +282,11 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   if (q.gh0 && live && rank == 0 && w == 0) *reinterpret_cast<f2*>(q.gh0 + c) = z;
   if (DECAY == kRecRate && q.part) {  // the block's sums of the rates' gradients, in a fixed order
     __syncthreads();
-    maps[w][0][lane] = sum;
+    maps[w].S[lane] = sum;
     __syncthreads();
     if (w == 0 && live) {
 #pragma unroll
-      for (int v = 1; v < kBackWarps; ++v) sum = f2_add(sum, maps[v][0][lane]);
+      for (int v = 1; v < kBackWarps; ++v) sum = f2_add(sum, maps[v].S[lane]);
       *reinterpret_cast<f2*>(q.part + (long long)rank * p.C + c) = sum;
     }
   }
@@ -274,7 +298,7 @@ template <typename IO>
 cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int* parts, cudaStream_t s) {
   return rec::by_kind(a.f, [&](auto d, auto sc, auto gate) {
     constexpr size_t ring = rec::kBackStages<IO> * 4 * (size_t)kRecTile * rec::kChans * sizeof(IO);
-    constexpr size_t own = (sizeof(IO) == 2 && decltype(gate)::value ? 2 : 1) * (size_t)rec::kBackTok * rec::kBackThreads * sizeof(f2);
+    constexpr size_t own = rec::Own<IO, decltype(gate)::value>::BYTES;
     return rec::launch_clusters<rec::kla_recurrence_grad_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
                                 rec::kBackThreads, ring + own>(a, (a.f.C + rec::kChans - 1) / rec::kChans,
                                                                (a.f.T + kRecTile - 1) / kRecTile, parts, s);
