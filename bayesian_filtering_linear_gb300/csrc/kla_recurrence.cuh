@@ -259,7 +259,7 @@ inline cudaLaunchConfig_t cluster_config(unsigned blocks, int k, int threads, si
   cfg.dynamicSmemBytes = smem + block_maps_bytes(k);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = k > 1 ? 1 : 0;
+  cfg.numAttrs = 1;
   return cfg;
 }
 
@@ -275,8 +275,7 @@ int clusters_at_once(int device, int k) {
       cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return -1;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = cluster_config(k, k, THREADS, SMEM, attr, nullptr);
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = cluster_config(k, k, THREADS, SMEM, attr, nullptr);
   if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) return -1;
   if (keep) known[device][k].store(n + 1, std::memory_order_relaxed);
   return n;
@@ -302,9 +301,13 @@ cudaError_t launch_clusters(const Args& a, int tiles, int along, int* used, cuda
       break;
     }
   }
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = cluster_config((unsigned)tiles * (unsigned)k, k, THREADS, SMEM, attr, s);
   if (used) *used = k;
+  if (k == 1) {
+    KERNEL<<<(unsigned)tiles, THREADS, SMEM, s>>>(a, 1);
+    return cudaGetLastError();
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = cluster_config((unsigned)tiles * (unsigned)k, k, THREADS, SMEM, attr, s);
   e = cudaLaunchKernelEx(&cfg, KERNEL, a, k);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -964,7 +964,7 @@ def recurrence_forward(x, g, i=None, rate=None, h0=None, *, decay: str = "log", 
     :func:`recurrence_backward` takes instead of making them again."""
     shape, index, dt, io, opt, sx, sg, si = _recurrence_args(x, g, i, rate, decay, scale)
     B, H, T, D = shape
-    state, device, given = (B, H, D), x.device, (y, hT, checkpoints)
+    state, device, y_given, hT_given = (B, H, D), x.device, y, hT
     _need_state(h0, "h0", state, index, device)
     _need_state(hT, "hT", state, index, device)
     if y is None:
@@ -983,7 +983,7 @@ def recurrence_forward(x, g, i=None, rate=None, h0=None, *, decay: str = "log", 
     st = _run(index, stream, LIB.kla_recurrence_forward,
               (x.data_ptr(), g.data_ptr(), _addr(i), _addr(rate), _addr(h0), y.data_ptr(), _addr(hT), _addr(kept),
                B, H, T, D, sx, sg, si, _triple(sy), io, opt))
-    _check(st, "kla_recurrence_forward", *(t for t in given if t is not None and t is not True and t is not False))
+    _check(st, "kla_recurrence_forward", y_given, hT_given, None if checkpoints is True else kept)
     return (y, hT) if kept is None else (y, hT, kept)
 
 
