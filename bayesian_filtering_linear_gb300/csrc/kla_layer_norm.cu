@@ -4,13 +4,20 @@
 //   gx = gtotal + r (g w - mean(g w) - n mean(g w n)),   gw = Σ g n,  gb = Σ g
 //
 // Every element is read once and written once, so HBM bounds it. A row stays in
-// the registers of its lanes (eight, a warp or a block, by its width), so the
+// the registers of its lanes (eight to all of a block's, by its width), so the
 // variance is the mean square of differences from the mean, as exact as the
 // mean, at no further reads; the gradients make both again from the row rather
-// than read them. Backward a group of lanes goes through rows, the next one on
-// its way while one is worked on, and adds up the weight's and the bias's
-// gradients of its columns in registers; blocks leave partial sums, and a
+// than read them. Backward a group of lanes goes through rows, the next ones on
+// their way by asynchronous copies meanwhile, and adds up the weight's and the
+// bias's gradients of its columns in registers; blocks leave partial sums, and a
 // second kernel adds those, both in a fixed order.
+//
+// Measured, 32768 rows of 1024 in bf16: with the residual 45.6 us (5.9 TB/s), the
+// gradients 47 us and 5 for the sums (before: 86 with the next row in registers and
+// a warp a row, where 254 registers left eight warps an SM; 56 with sums of one
+// thread a block; three blocks of two rows at a time, 164 registers, are faster
+// than four of 128, which spill). Rows of an odd width are read an element at a
+// time: 8188 of 517 in fp32, gradients 14 us and 5.
 #include <algorithm>
 
 #include "kla_device.cuh"

@@ -5,14 +5,22 @@
 //   a = e^g, σ(g) or exp(-rate σ(g));  s = 1, sqrt(1 - a²) or 1 - a
 //
 // Every input is read once and every output written once, so HBM bounds it;
-// next comes the issue of instructions (about 30 an element with both gates). A
-// cluster of blocks goes along the sequence, a tile of 64 tokens a block at a
-// time. A warp runs through its sixteen tokens from a state of zero, keeping for
-// each the outcome Y and the product P of the decays so far, and leaves its map
-// (A, S), while the next tile is on its way. The maps of the block's warps meet in shared
-// memory, those of the cluster's blocks are stored in each other's, and from
-// them every warp knows the state h that it starts from: y_t = P_t h + Y_t.
-// Nothing waits but barriers and nothing goes through memory.
+// next comes the issue of instructions (37 an element with both gates, five of
+// them special functions). A cluster of blocks goes along the sequence, a tile of
+// 64 tokens a block at a time. A warp runs through its sixteen tokens from a state
+// of zero, keeping for each the outcome Y and the product P of the decays so far,
+// and leaves its map (A, S), while the next tile is on its way. The maps of the
+// block's warps meet in shared memory, those of the cluster's blocks are stored in
+// each other's, and from them every warp knows the state h that it starts from:
+// y_t = P_t h + Y_t. Nothing waits but barriers and nothing goes through memory.
+// (No block may end before the others' stores into its shared memory have come:
+// the last step's barrier is behind the last of them.)
+//
+// Measured: 608 tiles of 64 channels, one block each, 4096 tokens in bf16, 6.15
+// TB/s (91% of a copy); B8 H16 T4096 D64 bf16, 128 tiles in clusters of four, 67 us
+// (4.0 TB/s): 512 blocks leave a sixth of the 608 places empty, and the cluster's
+// exchange takes the rest. Eight tokens a warp took 90 us: the composition of the
+// maps costs as much for half the tokens.
 #pragma once
 
 #include "kla_recurrence.cuh"

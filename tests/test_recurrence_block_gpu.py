@@ -3,6 +3,9 @@ recurrence — trained through autograd and decoded one token at a time.
 
 In fp32 against the same block in 64 bits on the CPU, written with torch: gradients pass through about 20 operations
 and two projections of 48 inputs, so 2^-24 · (20 + 2 · 48) · 16 of the largest gradient bounds their error."""
+import os
+import re
+
 import pytest
 import torch
 import torch.nn.functional as F
@@ -129,3 +132,13 @@ def test_captured_backward_while_an_eager_graph_of_the_leaves_lives():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_readme_example_runs():
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    block = [b for b in re.findall(r"```python\n(.*?)```", text, flags=re.S) if "recurrence_forward" in b]
+    scope = {}
+    exec(compile(block[0], "README.md", "exec"), scope)
+    torch.cuda.synchronize()
+    assert scope["y"].shape == (2, 8, 1000, 64) and bool(scope["y"].isfinite().all()) and bool(scope["y_t"].isfinite().all())
+    assert scope["y"].transpose(1, 2).is_contiguous() and bool(scope["state"].isfinite().all())
