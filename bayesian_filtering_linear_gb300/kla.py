@@ -121,17 +121,17 @@ def load_library(path: str = LIB_PATH):
     lib.kla_norm_rope_backward_workspace_size.argtypes = [i] * 5
     lib.kla_norm_rope_backward.restype = i
     lib.kla_norm_rope_backward.argtypes = [vp] * 12 + [i] * 5 + [strides] * 4 + [i, nr, vp, sz, vp]
-    rec, ll = ctypes.POINTER(RecurrenceOptions), ctypes.c_longlong
+    ll = ctypes.c_longlong  # (strides and options go as plain pointers, which cost the least to hand over)
     lib.kla_recurrence_checkpoints_size.restype = sz
     lib.kla_recurrence_checkpoints_size.argtypes = [i] * 4
     lib.kla_recurrence_forward.restype = i
-    lib.kla_recurrence_forward.argtypes = [vp] * 8 + [i] * 4 + [strides] * 4 + [i, rec, vp]
+    lib.kla_recurrence_forward.argtypes = [vp] * 8 + [i] * 4 + [vp] * 4 + [i, vp, vp]
     lib.kla_recurrence_step.restype = i
-    lib.kla_recurrence_step.argtypes = [vp] * 6 + [i] * 4 + [rec, vp]
+    lib.kla_recurrence_step.argtypes = [vp] * 6 + [i] * 4 + [vp, vp]
     lib.kla_recurrence_backward_workspace_size.restype = sz
     lib.kla_recurrence_backward_workspace_size.argtypes = [i] * 5
     lib.kla_recurrence_backward.restype = i
-    lib.kla_recurrence_backward.argtypes = [vp] * 13 + [i] * 4 + [strides] * 7 + [i, rec, vp, sz, vp]
+    lib.kla_recurrence_backward.argtypes = [vp] * 13 + [i] * 4 + [vp] * 7 + [i, vp, vp, sz, vp]
     lib.kla_layer_norm.restype = i
     lib.kla_layer_norm.argtypes = [vp] * 6 + [ll, i, ll, ll, i, f, vp]
     lib.kla_layer_norm_backward_workspace_size.restype = sz
@@ -943,6 +943,16 @@ def _recurrence_args(x, g, i, rate, decay, scale, tokens=True):
     return shape, index, dt, io, opt, _triple(sx), _triple(sg), None if i is None else _triple(si)
 
 
+@functools.lru_cache(maxsize=256)
+def _size(name, index, *shape):
+    """A workspace's bytes, which go by the shape and by the device's SMs."""
+    with torch.cuda.device(index):
+        nbytes = getattr(LIB, name)(*shape)
+    if nbytes == _NO_SIZE:
+        raise KlaError(ERR_UNSUPPORTED_SHAPE, name)
+    return nbytes
+
+
 def _need_state(t, name, shape, index, device):
     if t is not None and not _fits(t, torch.float32, shape, index):
         _need(t, name, torch.float32, shape, device)
@@ -1037,9 +1047,7 @@ def recurrence_backward(x, g, i=None, rate=None, h0=None, *, gy=None, ghT=None, 
     if state_grad:
         out["gh0"] = gh0 = torch.empty(state, dtype=torch.float32, device=device)
     if workspace is None and (checkpoints is None or rate is not None):
-        nbytes = LIB.kla_recurrence_backward_workspace_size(B, H, T, D, checkpoints is not None)
-        if nbytes == _NO_SIZE:
-            raise KlaError(ERR_UNSUPPORTED_SHAPE, "kla_recurrence_backward_workspace_size")
+        nbytes = _size("kla_recurrence_backward_workspace_size", index, B, H, T, D, checkpoints is not None)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     ws_bytes = _space(workspace, index)
     st = _run(index, stream, LIB.kla_recurrence_backward,
@@ -1135,13 +1143,7 @@ def layer_norm_backward(x, weight=None, *, gy=None, gtotal=None, eps: float = 1e
     if param_grads or (param_grads is None and weight is not None):
         out["gweight"], out["gbias"] = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
         if workspace is None:
-            if index == _current_device():  # the size goes by the device's SMs
-                nbytes = LIB.kla_layer_norm_backward_workspace_size(rows, D)
-            else:
-                with torch.cuda.device(index):
-                    nbytes = LIB.kla_layer_norm_backward_workspace_size(rows, D)
-            if nbytes == _NO_SIZE:
-                raise KlaError(ERR_UNSUPPORTED_SHAPE, "kla_layer_norm_backward_workspace_size")
+            nbytes = _size("kla_layer_norm_backward_workspace_size", index, rows, D)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     ws_bytes = _space(workspace, index)
     st = _run(index, stream, LIB.kla_layer_norm_backward,
