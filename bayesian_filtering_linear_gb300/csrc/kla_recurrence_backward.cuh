@@ -308,7 +308,7 @@ cudaError_t launch_recurrence_backward_io(const RecGradArgs& a, int* parts, cuda
     constexpr size_t own = rec::Own<IO, decltype(gate)::value>::BYTES;
     return rec::launch_clusters<rec::kla_recurrence_grad_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
                                 rec::kBackThreads, ring + own>(a, (a.f.C + rec::kChans - 1) / rec::kChans,
-                                                               (a.f.T + kRecTile - 1) / kRecTile, parts, s);
+                                                               (int)(((long long)a.f.T + kRecTile - 1) / kRecTile), parts, s);
   });
 }
 

@@ -223,7 +223,7 @@ cudaError_t launch_recurrence_io(const RecArgs& a, cudaStream_t s) {
     constexpr size_t ring = rec::kStages<IO> * (decltype(gate)::value ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
     constexpr size_t maps = rec::kStages<IO> == 2 ? 0 : rec::kWarps * 96 * sizeof(f2);
     return rec::launch_clusters<rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
-                                rec::kThreads, ring + maps>(a, (a.C + rec::kChans - 1) / rec::kChans, (a.T + rec::kTile - 1) / rec::kTile,
+                                rec::kThreads, ring + maps>(a, (a.C + rec::kChans - 1) / rec::kChans, (int)(((long long)a.T + rec::kTile - 1) / rec::kTile),
                                                             nullptr, s);
   });
 }
