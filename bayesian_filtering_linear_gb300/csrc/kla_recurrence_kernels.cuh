@@ -7,7 +7,7 @@
 // Every input is read once and every output written once, so HBM bounds it;
 // next comes the issue of instructions (37 an element with both gates, five of
 // them special functions). A cluster of blocks goes along the sequence, a tile of
-// 64 tokens a block at a time. A warp runs through its sixteen tokens from a state
+// 64 or 128 tokens a block at a time. A warp runs through its sixteen tokens from a state
 // of zero, keeping for each the outcome Y and the product P of the decays so far,
 // and leaves its map (A, S), while the next tile is on its way. The maps of the
 // block's warps meet in shared memory, those of the cluster's blocks are stored in
@@ -28,13 +28,19 @@
 namespace kla {
 namespace rec {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kTok = 16, kTile = kWarps * kTok;  // tokens a warp, a tile
+constexpr int kTok = 16;  // tokens a warp
+// Warps of a block: four, or where channels are few (so few that clusters of
+// sixteen fit) and sequences longer than those reach in a step, eight, which halve
+// the exchanges. Measured, bf16, four and eight: 65536 tokens of 16 heads of 128 258
+// and 243 us, of one head of 64 158 and 114, 16384 of four heads of 64 45 and 33;
+// the headline, whose channels are many, 67 and 73.
+constexpr int kNarrow = 4, kWide = 8;
 // Stages of the ring of tiles and blocks an SM. In bf16 a second stage and a fourth block are better than a fifth block
 // (headline 70 us with one stage; five blocks of 96 registers 90) or three blocks (76); fp32 tiles are twice as large.
 template <typename IO>
 constexpr int kStages = sizeof(IO) == 2 ? 2 : 1;
-template <typename IO>
-constexpr int kBlocks = sizeof(IO) == 2 ? 4 : 3;
+template <typename IO, int WARPS>
+constexpr int kBlocks = (sizeof(IO) == 2 ? 16 : WARPS == kNarrow ? 12 : 8) / WARPS;
 
 // A decay (y: -log a, but for a sigmoid) and the factor s σ(i) x of a pair, from what is read.
 template <typename IO, int DECAY, bool NEAR>
@@ -56,9 +62,8 @@ __device__ __forceinline__ f2 scaled(f2 x, f2 less) {
   return x;
 }
 
-template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR>
+template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR, int S>  // S: elements a stream
 __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f2 (&Y)[kTok]) {
-  constexpr int S = kTile * kChans;  // elements a stream
   Map m{0, 0, 0};
   Product<DECAY, NEAR> prod;
 #pragma unroll
@@ -76,8 +81,9 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
   return m;
 }
 
-template <typename IO, int DECAY, int SCALE, bool GATE>
-__global__ void __launch_bounds__(kThreads, kBlocks<IO>) kla_recurrence_kernel(const RecArgs p, int k) {
+template <typename IO, int DECAY, int SCALE, bool GATE, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurrence_kernel(const RecArgs p, int k) {
+  constexpr int kThreads = 32 * kWarps, kTile = kWarps * kTok;
   extern __shared__ __align__(16) unsigned char smem[];
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const tile = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
@@ -130,8 +136,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<IO>) kla_recurrence_kernel(c
       return reinterpret_cast<f2*>(kStages<IO> == 2 ? now + v * kTok * kChans : tile + STAGE) + (kStages<IO> == 2 ? 0 : 96 * v) + lane;
     };
     Map m;
-    if (near) m = segment<IO, DECAY, SCALE, GATE, DECAY == kRecRate>(mine, rate, P, Y);
-    else m = segment<IO, DECAY, SCALE, GATE, false>(mine, rate, P, Y);
+    if (near) m = segment<IO, DECAY, SCALE, GATE, DECAY == kRecRate, S>(mine, rate, P, Y);
+    else m = segment<IO, DECAY, SCALE, GATE, false, S>(mine, rate, P, Y);
     __syncwarp();
     map_of(w)[0] = m.A, map_of(w)[32] = m.Al, map_of(w)[64] = m.S;
     __syncthreads();
@@ -158,8 +164,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks<IO>) kla_recurrence_kernel(c
       }
     }
     const long long first = (step * k + rank) * kTile;
-    if (p.ckpt && w == 0 && live && first < p.T && first % kRecTile == 0)
-      *reinterpret_cast<f2*>(p.ckpt + first / kRecTile * p.C + c) = h;
     f2 mystart = h;
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) {
@@ -167,8 +171,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<IO>) kla_recurrence_kernel(c
       if (k == 1 || v < w) h = apply(map_of(v)[0], map_of(v)[32], map_of(v)[64], h);
     }
     if (k > 1) h = next;
+    const long long t0 = first + w * kTok;
+    if (p.ckpt && live && t0 < p.T && t0 % kRecTile == 0) *reinterpret_cast<f2*>(p.ckpt + t0 / kRecTile * p.C + c) = mystart;
     if (live && y) {
-      const long long t0 = first + w * kTok;
       IO* out = y + t0 * p.y.st;
       if (t0 + kTok <= p.T) {
 #pragma unroll
@@ -215,16 +220,37 @@ inline cudaError_t by_kind(const RecArgs& a, F f) {
   return scale(integral_constant<int, kRecLog>());
 }
 
+// Shared memory of a block, but for the cluster's maps: the ring of tiles and, where the warps' maps have no place in it, those.
+template <typename IO>
+constexpr size_t forward_bytes(int warps, bool gate) {
+  return kStages<IO> * (gate ? 3 : 2) * (size_t)warps * kTok * kChans * sizeof(IO) +
+         (kStages<IO> == 2 ? 0 : warps * 96 * sizeof(f2));
+}
+
 }  // namespace rec
 
 template <typename IO>
 cudaError_t launch_recurrence_io(const RecArgs& a, cudaStream_t s) {
+  const int tiles = (a.C + rec::kChans - 1) / rec::kChans;
   return rec::by_kind(a, [&](auto d, auto sc, auto gate) {
-    constexpr size_t ring = rec::kStages<IO> * (decltype(gate)::value ? 3 : 2) * (size_t)rec::kTile * rec::kChans * sizeof(IO);
-    constexpr size_t maps = rec::kStages<IO> == 2 ? 0 : rec::kWarps * 96 * sizeof(f2);
-    return rec::launch_clusters<rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value>,
-                                rec::kThreads, ring + maps>(a, (a.C + rec::kChans - 1) / rec::kChans, (int)(((long long)a.T + rec::kTile - 1) / rec::kTile),
-                                                            nullptr, s);
+    const auto along = [&](int warps) { return (int)(((long long)a.T + warps * rec::kTok - 1) / (warps * rec::kTok)); };
+    const auto go = [&](auto warps) {
+      constexpr int W = decltype(warps)::value;
+      return rec::launch_clusters<
+          rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value, W>, 32 * W,
+          rec::forward_bytes<IO>(W, decltype(gate)::value)>(a, tiles, along(W), nullptr, s);
+    };
+    if (along(rec::kNarrow) > kRecMaxCluster) {
+      int device = 0;
+      const cudaError_t e = cudaGetDevice(&device);
+      if (e != cudaSuccess) return e;
+      constexpr auto narrow =
+          rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value, rec::kNarrow>;
+      const int most = rec::clusters_at_once<narrow, 32 * rec::kNarrow, rec::forward_bytes<IO>(rec::kNarrow, decltype(gate)::value)>(
+          device, kRecMaxCluster);
+      if (tiles <= most) return go(std::integral_constant<int, rec::kWide>());
+    }
+    return go(std::integral_constant<int, rec::kNarrow>());
   });
 }
 
