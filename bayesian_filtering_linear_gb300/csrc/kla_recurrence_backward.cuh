@@ -240,11 +240,17 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     if (t0 < p.T) {
       const int n = (int)min((long long)kBackTok, p.T - t0);
 #pragma unroll
-      for (int j = kBackTok - 1; j >= 0; --j) {
-        IO* const o = tile + j * kChans;
-        const f2 G = f2_add(behind, pair_at<IO>(o + 3 * S));
+      for (int j = kBackTok - 1; j >= 0; --j) {  // G in the decays' place, dL/dlog a in V's
+        const f2 G = f2_add(behind, pair_at<IO>(tile + 3 * S + j * kChans));
         behind = f2_mul(hi[j], G);
-        f2 by_log = f2_mul(G, f2_fma(P[j], h, V[j]));
+        hi[j] = G;
+        V[j] = f2_mul(G, f2_fma(P[j], h, V[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < kBackTok; ++j) {
+        IO* const o = tile + j * kChans;
+        const f2 G = hi[j];
+        f2 by_log = V[j];
         if (DECAY != kRecLog) {
           const f2 e = kept(o + S, o + 2 * S), open = f2_rcp(f2_add(one, e)), shut = f2_mul(e, open);
           if (DECAY == kRecRate) {
