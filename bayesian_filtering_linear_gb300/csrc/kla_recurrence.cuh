@@ -295,7 +295,7 @@ cudaError_t launch_clusters(const Args& a, int tiles, int along, int* used, cuda
   for (int n : sizes) {
     if (n > along && n > 1) continue;
     const int most = clusters_at_once<KERNEL, THREADS, SMEM>(device, n);
-    if (most < 0) return cudaErrorUnknown;
+    if (most < 0) return cudaGetLastError();
     if (tiles <= most) {
       k = n;
       break;

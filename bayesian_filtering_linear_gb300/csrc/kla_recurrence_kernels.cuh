@@ -248,6 +248,7 @@ cudaError_t launch_recurrence_io(const RecArgs& a, cudaStream_t s) {
           rec::kla_recurrence_kernel<IO, decltype(d)::value, decltype(sc)::value, decltype(gate)::value, rec::kNarrow>;
       const int most = rec::clusters_at_once<narrow, 32 * rec::kNarrow, rec::forward_bytes<IO>(rec::kNarrow, decltype(gate)::value)>(
           device, kRecMaxCluster);
+      if (most < 0) return cudaGetLastError();
       if (tiles <= most) return go(std::integral_constant<int, rec::kWide>());
     }
     return go(std::integral_constant<int, rec::kNarrow>());
