@@ -33,9 +33,20 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The smaller and the larger of two; NaN where one is (fminf and fmaxf give the other).
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 __device__ __forceinline__ float sqrt_fast(float x) {
   float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0.f)));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(max_nan(x, 0.f)));
   return y;
 }
 __device__ __forceinline__ f2 f2_both(float x) { return f2_make(x, x); }
@@ -45,7 +56,13 @@ __device__ __forceinline__ f2 f2_exp_neg(f2 x) { return f2_ex2(f2_mul(x, f2_both
 // The same, held at 2^126 or below, whose reciprocal is still a normal number.
 __device__ __forceinline__ f2 f2_exp_neg_held(f2 x) {
   const f2 e = f2_exp_neg(x);
-  return f2_make(fminf(f2_lo(e), 0x1p126f), fminf(f2_hi(e), 0x1p126f));
+  return f2_make(min_nan(f2_lo(e), 0x1p126f), min_nan(f2_hi(e), 0x1p126f));
+}
+// Two channels' rates, held at 2^80 or below (infinite ones: a = 0): times the σ(g) behind the last token, 0 or, of
+// the held exponential, 2^-126, that is no decay.
+__device__ __forceinline__ f2 rates_at(const float* p) {
+  const float2 r = *reinterpret_cast<const float2*>(p);
+  return f2_make(min_nan(r.x, 0x1p80f), min_nan(r.y, 0x1p80f));
 }
 
 // A decay: a float, the rest that it leaves, and 1 - a.

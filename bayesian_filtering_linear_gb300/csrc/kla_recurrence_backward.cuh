@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
   const Place my(live ? c : 0, p.H, p.D);
   f2 rate = 0, z = 0, sum = 0;  // z: what reaches the step's last token from behind it
   if (DECAY == kRecRate && live)
-    rate = *reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d);
+    rate = rates_at(p.rate + (long long)my.h * p.D + my.d);
   if (q.ghT && live) z = *reinterpret_cast<const f2*>(q.ghT + c);
   const bool near = DECAY == kRecRate && near_rates(rate);
 

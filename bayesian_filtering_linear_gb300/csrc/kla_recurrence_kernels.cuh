@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurren
   IO* const y = p.y.p ? reinterpret_cast<IO*>(p.y.p) + my.of(p.y) : nullptr;
   f2 rate = 0, h = 0;  // h: the state before the step's tokens
   if (DECAY == kRecRate && live)
-    rate = *reinterpret_cast<const f2*>(p.rate + (long long)my.h * p.D + my.d);
+    rate = rates_at(p.rate + (long long)my.h * p.D + my.d);
   if (p.h0 && live) h = *reinterpret_cast<const f2*>(p.h0 + c);
   const bool near = DECAY == kRecRate && near_rates(rate);
 
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(128) kla_recurrence_step_kernel(const RecArgs 
   if (c >= p.C) return;
   const f2 h = *reinterpret_cast<const f2*>(p.h0 + c);
   f2 x = pair_at<IO>(reinterpret_cast<const IO*>(p.x.p) + c), rate = 0;
-  if (DECAY == kRecRate) rate = *reinterpret_cast<const f2*>(p.rate + c % (p.H * p.D));
+  if (DECAY == kRecRate) rate = rates_at(p.rate + c % (p.H * p.D));
   f2 y;
   const Decay a = decay_of<IO, DECAY, false>(reinterpret_cast<const IO*>(p.g.p) + c, rate, y);
   x = scaled<SCALE>(x, a.less);

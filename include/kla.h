@@ -499,7 +499,8 @@ typedef struct kla_recurrence_options {
  *     multiple of 16 bytes (else MISALIGNED), so a projection's [B,T,H·D] is
  *     read and written in place. i NULL: no input gate (σ(i) = 1). y must not
  *     overlap any input; its rows must not share memory.
- *   rate [H,D] fp32 (required for DECAY_RATE, else ignored).
+ *   rate [H,D] fp32 (required for DECAY_RATE, else ignored; above 2^80 it
+ *     counts as 2^80).
  *   h0 [B,H,D] fp32: the state before the first token, or NULL for zeros.
  *   hT [B,H,D] fp32 or NULL: the state after the last token. It may be h0
  *     itself but must not overlap it otherwise. T = 0 copies the state.
