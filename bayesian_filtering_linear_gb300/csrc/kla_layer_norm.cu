@@ -17,7 +17,9 @@
 // a warp a row, where 254 registers left eight warps an SM; 56 with sums of one
 // thread a block; three blocks of two rows at a time, 164 registers, are faster
 // than four of 128, which spill). Rows of an odd width are read an element at a
-// time: 8188 of 517 in fp32, gradients 14 us and 5.
+// time: 8188 of 517 in fp32, gradients 14 us and 5; in bf16, pairs where rows begin
+// on four bytes (38972 of 446 with the residual: 26 us, by elements 34; gradients of
+// 20000: 20, by elements 24, by copies of four bytes 21).
 #include <algorithm>
 
 #include "kla_device.cuh"
@@ -54,6 +56,15 @@ struct Raw<__nv_bfloat16, 8> {
     v = make_uint4(u[0], u[1], u[2], u[3]);
   }
 };
+template <>
+struct Raw<__nv_bfloat16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void to(float (&x)[2]) const { x[0] = __uint_as_float(v << 16), x[1] = __uint_as_float(v & 0xffff0000u); }
+  __device__ __forceinline__ void from(const float (&x)[2]) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(x[0], x[1]);
+    v = *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
 template <typename IO>
 struct Raw<IO, 1> {
   IO v;
@@ -70,9 +81,11 @@ __device__ __forceinline__ void params(const float* p, float (&w)[VEC]) {
       const float4 v = *reinterpret_cast<const float4*>(p + i);
       w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
     }
+  } else if constexpr (VEC == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    w[0] = v.x, w[1] = v.y;
   } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = p[i];
+    w[0] = *p;
   }
 }
 
@@ -193,13 +206,13 @@ __global__ void __launch_bounds__(THREADS) kla_layer_norm_kernel(const LayerNorm
 
 // A thread's pieces of the rows ahead, S - 1 of them on their way by asynchronous
 // copies into places that no other thread reads (so nothing waits but the
-// copies); elements of two bytes, which have no such copies, come through
-// registers, one row ahead. What no copy reaches (behind a row's end, a gradient
+// copies); two-byte elements and their pairs come through registers, one row
+// ahead. What no copy reaches (behind a row's end, a gradient
 // that is not there) stays zero.
 template <typename IO, int VEC, int NV, int LANES, int THREADS, int S>
 struct Ahead {
   using R = Raw<IO, VEC>;
-  static constexpr bool ASYNC = sizeof(R) >= 4;
+  static constexpr bool ASYNC = sizeof(R) == 16 || sizeof(IO) == 4;
   static constexpr int P = (NV * VEC + 1) / 2;  // pairs of elements a thread
   static constexpr size_t BYTES = ASYNC ? (size_t)S * 3 * NV * THREADS * sizeof(R) : 0;
   R* ring;  // [S][3][NV][THREADS]
@@ -418,10 +431,12 @@ struct BackShape : Shape<NV, LANES, THREADS> {
   static constexpr int S = S_, MIN = MIN_;
 };
 
-// Forward, by the row's width in pieces (of 16 bytes, or single elements).
-template <bool VEC, typename F>
+// Forward, by the row's width in pieces (of 16 bytes; else pairs or single elements: 5000 fp32 rows of 3001 take 43 us
+// with eight elements a lane of 512, 67 with sixteen; 200000 bf16 rows of 50 take 21 with eight lanes a row, 43 with
+// 32; up to 512, fp32 rows of 501 take 22 us with 128 lanes and 25 with 64, bf16 rows of 411 take 22 and 18).
+template <typename IO, int VEC, typename F>
 void by_width(int pieces, F f) {
-  if constexpr (VEC) {
+  if constexpr (VEC >= 4) {
     if (pieces <= 8) return f(Shape<1, 8, 256>());
     if (pieces <= 32) return f(Shape<1, 32, 256>());
     if (pieces <= 64) return f(Shape<2, 32, 256>());
@@ -431,10 +446,14 @@ void by_width(int pieces, F f) {
     if (pieces <= 1024) return f(Shape<4, 256, 256>());
     return f(Shape<4, 512, 512>());
   } else {
+    if (pieces <= 64) return f(Shape<8, 8, 256>());
     if (pieces <= 128) return f(Shape<4, 32, 256>());
-    if (pieces <= 512) return f(Shape<16, 32, 256>());
+    if (pieces <= 256) return f(Shape<8, 32, 256>());
+    if (pieces <= 512 && sizeof(IO) == 4) return f(Shape<4, 128, 128>());
+    if (pieces <= 512) return f(Shape<8, 64, 64>());
     if (pieces <= 1024) return f(Shape<8, 128, 128>());
-    if (pieces <= 2048) return f(Shape<16, 128, 128>());
+    if (pieces <= 2048) return f(Shape<8, 256, 256>());
+    if (pieces <= 4096) return f(Shape<8, 512, 512>());
     return f(Shape<16, 512, 512>());
   }
 }
@@ -459,6 +478,13 @@ void by_width_back(int pieces, F f) {
     if (pieces <= 512) return f(BackShape<4, 128, 128, 3, 3>());
     if (pieces <= 1024) return f(BackShape<4, 256, 256, 3, 2>());
     return f(BackShape<4, 512, 512, 2, 1>());
+  } else if constexpr (VEC == 2) {
+    if (pieces <= 128) return f(BackShape<4, 32, 128, 3, 5>());
+    if (pieces <= 256) return f(BackShape<4, 64, 128, 3, 4>());
+    if (pieces <= 512) return f(BackShape<4, 128, 128, 3, 4>());
+    if (pieces <= 1024) return f(BackShape<4, 256, 256, 3, 2>());
+    if (pieces <= 2048) return f(BackShape<4, 512, 512, 3, 1>());
+    return f(BackShape<8, 512, 512, 2, 1>());
   } else {
     if (pieces <= 128) return f(BackShape<4, 32, 128, 4, 5>());
     if (pieces <= 256) return f(BackShape<8, 32, 128, 3, 4>());
@@ -480,41 +506,43 @@ int grad_blocks(long long rows, int num_sms) {
   return (int)std::max(1LL, std::min((rows + groups - 1) / groups, (long long)num_sms * Sh::MIN));
 }
 
-// Rows that all begin on 16 bytes.
+// Calls f with the elements of a piece: 16 bytes where all rows begin on them, else of two-byte elements pairs where
+// all rows begin on four bytes, else one.
 struct Rows {
   const void* p;
   long long stride;
 };
-template <typename IO>
-bool vector_rows(int D, std::initializer_list<Rows> all) {
+template <typename IO, typename F>
+void by_piece(int D, std::initializer_list<Rows> all, F f) {
+  auto fits = [&](int elements) {
+    if (D % elements) return false;
+    for (const Rows& r : all)
+      if (r.p && (r.stride % elements || reinterpret_cast<uintptr_t>(r.p) % (elements * sizeof(IO)))) return false;
+    return true;
+  };
   constexpr int VE = 16 / sizeof(IO);
-  if (D % VE) return false;
-  for (const Rows& r : all)
-    if (r.p && (r.stride % VE || reinterpret_cast<uintptr_t>(r.p) % 16)) return false;
-  return true;
+  if (fits(VE)) return f(std::integral_constant<int, VE>());
+  if constexpr (sizeof(IO) == 2)
+    if (fits(2)) return f(std::integral_constant<int, 2>());
+  f(std::integral_constant<int, 1>());
 }
 
 template <typename IO>
 cudaError_t launch_io(const LayerNormArgs& a, cudaStream_t s) {
-  constexpr int VE = 16 / sizeof(IO);
-  const bool vec = vector_rows<IO>(a.D, {{a.x, a.x_stride}, {a.residual, a.residual_stride}, {a.y, a.D},
-                                         {a.total, a.D}});
   auto go = [&](auto ve, auto shape) {
     using Sh = decltype(shape);
     constexpr int G = Sh::THREADS / Sh::LANES;
     const unsigned blocks = (unsigned)((a.rows + G - 1) / G);
     kla_layer_norm_kernel<IO, decltype(ve)::value, Sh::NV, Sh::LANES, Sh::THREADS><<<blocks, Sh::THREADS, 0, s>>>(a);
   };
-  if (vec) by_width<true>(a.D / VE, [&](auto shape) { go(std::integral_constant<int, VE>(), shape); });
-  else by_width<false>(a.D, [&](auto shape) { go(std::integral_constant<int, 1>(), shape); });
+  by_piece<IO>(a.D, {{a.x, a.x_stride}, {a.residual, a.residual_stride}, {a.y, a.D}, {a.total, a.D}}, [&](auto ve) {
+    by_width<IO, decltype(ve)::value>(a.D / ve, [&](auto shape) { go(ve, shape); });
+  });
   return cudaGetLastError();
 }
 
 template <typename IO>
 cudaError_t launch_io(const LayerNormGradArgs& a, int num_sms, cudaStream_t s) {
-  constexpr int VE = 16 / sizeof(IO);
-  const bool vec = vector_rows<IO>(a.D, {{a.x, a.x_stride}, {a.gy, a.gy_stride}, {a.gtotal, a.gtotal_stride},
-                                         {a.gx, a.D}});
   int blocks = 0;
   cudaError_t e = cudaSuccess;
   auto go = [&](auto ve, auto shape) {
@@ -527,8 +555,9 @@ cudaError_t launch_io(const LayerNormGradArgs& a, int num_sms, cudaStream_t s) {
     if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) kernel<<<blocks, Sh::THREADS, smem, s>>>(a);
   };
-  if (vec) by_width_back<VE>(a.D / VE, [&](auto shape) { go(std::integral_constant<int, VE>(), shape); });
-  else by_width_back<1>(a.D, [&](auto shape) { go(std::integral_constant<int, 1>(), shape); });
+  by_piece<IO>(a.D, {{a.x, a.x_stride}, {a.gy, a.gy_stride}, {a.gtotal, a.gtotal_stride}, {a.gx, a.D}}, [&](auto ve) {
+    by_width_back<decltype(ve)::value>(a.D / ve, [&](auto shape) { go(ve, shape); });
+  });
   if (e != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
   kla_layer_norm_sum_kernel<<<(2 * a.D + 7) / 8, 1024, 0, s>>>(a, blocks);
@@ -541,6 +570,7 @@ size_t layer_norm_partial_bytes(long long rows, int D, int num_sms) {
   int most = 0;  // of rows in pieces of any kind
   auto count = [&](auto shape) { most = std::max(most, grad_blocks<decltype(shape)>(rows, num_sms)); };
   by_width_back<1>(D, count);
+  if (D % 2 == 0) by_width_back<2>(D / 2, count);
   if (D % 4 == 0) by_width_back<4>(D / 4, count);
   if (D % 8 == 0) by_width_back<8>(D / 8, count);
   return (size_t)most * 2 * (size_t)D * sizeof(float);
