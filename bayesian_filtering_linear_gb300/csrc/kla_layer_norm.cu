@@ -458,7 +458,9 @@ void by_width(int pieces, F f) {
   }
 }
 
-// Backward, where a lane also keeps the sums of its columns: more lanes with fewer pieces.
+// Backward, where a lane also keeps the sums of its columns: more lanes with fewer pieces, but few warps a row, which
+// wait for each other twice (5000 rows of 3001 with 16 and 8 warps: 99 and 70 us in fp32, 115 and 46 in bf16; 4000 of
+// 4090 in bf16: 59 and 39).
 template <int VEC, typename F>
 void by_width_back(int pieces, F f) {
   if constexpr (VEC == 8) {
@@ -482,8 +484,8 @@ void by_width_back(int pieces, F f) {
     if (pieces <= 128) return f(BackShape<4, 32, 128, 3, 5>());
     if (pieces <= 256) return f(BackShape<4, 64, 128, 3, 4>());
     if (pieces <= 512) return f(BackShape<4, 128, 128, 3, 4>());
-    if (pieces <= 1024) return f(BackShape<4, 256, 256, 3, 2>());
-    if (pieces <= 2048) return f(BackShape<4, 512, 512, 3, 1>());
+    if (pieces <= 1024) return f(BackShape<8, 128, 128, 3, 3>());
+    if (pieces <= 2048) return f(BackShape<8, 256, 256, 3, 1>());
     return f(BackShape<8, 512, 512, 2, 1>());
   } else {
     if (pieces <= 128) return f(BackShape<4, 32, 128, 4, 5>());
@@ -493,8 +495,8 @@ void by_width_back(int pieces, F f) {
     if (pieces <= 640) return f(BackShape<5, 128, 128, 4, 4>());
     if (pieces <= 768) return f(BackShape<6, 128, 128, 4, 4>());
     if (pieces <= 1024) return f(BackShape<8, 128, 128, 3, 4>());
-    if (pieces <= 2048) return f(BackShape<8, 256, 256, 3, 2>());
-    if (pieces <= 4096) return f(BackShape<8, 512, 512, 3, 1>());
+    if (pieces <= 2048) return f(BackShape<16, 128, 128, 3, 2>());
+    if (pieces <= 4096) return f(BackShape<16, 256, 256, 2, 1>());
     return f(BackShape<16, 512, 512, 2, 1>());
   }
 }
