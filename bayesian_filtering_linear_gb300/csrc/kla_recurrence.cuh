@@ -126,7 +126,19 @@ __device__ __forceinline__ f2 spread_rsqrt(f2 v) {
 struct Map {
   f2 A, Al, S;
 };
-__device__ __forceinline__ f2 apply(f2 A, f2 Al, f2 S, f2 h) { return f2_fma(A, h, f2_fma(Al, h, S)); }
+// Infinite values held at the largest float (and NaN, which the product with the upper part keeps).
+__device__ __forceinline__ f2 held(f2 x) {
+  float a, b;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(a) : "f"(f2_lo(x)), "f"(0x1.fffffep127f));
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(b) : "f"(f2_hi(x)), "f"(0x1.fffffep127f));
+  return f2_make(a, b);
+}
+__device__ __forceinline__ bool finite(f2 x) { return isfinite(f2_lo(x)) && isfinite(f2_hi(x)); }
+// A h + S. The rest of A is zero or below zero as often as above, and its product with an infinite h would make NaN of
+// what stays infinite: it meets the h that is held. Along the sequence the maps go without (the two instructions more
+// took the headline from 67 to 70 us) and leave NaN, by which the kernels' ends find the channels to go through again.
+template <bool HELD>
+__device__ __forceinline__ f2 apply(f2 A, f2 Al, f2 S, f2 h) { return f2_fma(A, h, f2_fma(Al, HELD ? held(h) : h, S)); }
 // A <- a A
 __device__ __forceinline__ void lengthen(f2& A, f2& Al, f2 hi, f2 lo) {
   const f2 p = f2_mul(hi, A);
@@ -180,6 +192,12 @@ __device__ __forceinline__ f2 minus_pair_at(const __nv_bfloat16* p) {
 __device__ __forceinline__ void put_pair(float* p, f2 v) { *reinterpret_cast<f2*>(p) = v; }
 __device__ __forceinline__ void put_pair(__nv_bfloat16* p, f2 v) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
+}
+// Stores those of a pair that are not finite.
+template <typename T>
+__device__ __forceinline__ void put_odd(T* p, f2 v) {
+  if (!isfinite(f2_lo(v))) p[0] = from_f32<T>(f2_lo(v));
+  if (!isfinite(f2_hi(v))) p[1] = from_f32<T>(f2_hi(v));
 }
 
 // Where a flat channel lies.
@@ -253,7 +271,7 @@ struct BlockMap {
   uint32_t Al[32];
   __device__ __forceinline__ f2 of(int lane, f2 h) const {
     const uint32_t l = Al[lane];
-    return apply(A[lane], f2_make(__uint_as_float(l << 16), __uint_as_float(l & 0xffff0000u)), S[lane], h);
+    return apply<false>(A[lane], f2_make(__uint_as_float(l << 16), __uint_as_float(l & 0xffff0000u)), S[lane], h);
   }
   // into the same place of the block of rank `rank`
   __device__ __forceinline__ void put(int lane, int rank, const Map& m) {

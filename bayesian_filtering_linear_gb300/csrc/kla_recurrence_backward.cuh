@@ -75,8 +75,8 @@ struct Own {
 struct WarpMaps {
   ulonglong2 A[32];  // and Al
   f2 S[32], R[32];
-  __device__ __forceinline__ f2 h(int lane, f2 v) const { return apply(A[lane].x, A[lane].y, S[lane], v); }
-  __device__ __forceinline__ f2 g(int lane, f2 v) const { return apply(A[lane].x, A[lane].y, R[lane], v); }
+  __device__ __forceinline__ f2 h(int lane, f2 v) const { return apply<false>(A[lane].x, A[lane].y, S[lane], v); }
+  __device__ __forceinline__ f2 g(int lane, f2 v) const { return apply<false>(A[lane].x, A[lane].y, R[lane], v); }
 };
 
 // Forward through a warp's tokens: its maps of h and (in r) of G, and for each token the decay, P and V.
@@ -132,6 +132,105 @@ __device__ __forceinline__ Map forth(IO* tile, const Own<IO, GATE>& own, f2 rate
   }
   prod.end(m);
   return m;
+}
+
+// For two channels in which a state that the thread's tokens meet (`odd`) or a G is not finite: as one_by_one of the
+// forward pass, from the last token back, storing what is not finite among the gradients of the thread's tokens. `sum`,
+// `z`: the rates' sum and what reaches the state before the first token, put right where they are not finite. (The
+// headline with an infinite state takes 1.4 ms, with NaN alone 0.2.)
+template <typename IO, int DECAY, int SCALE, bool GATE>
+__device__ __forceinline__ void one_by_one_back(const RecGradArgs& q, int c, int rank, int k, int w, f2 rate, bool odd, const Own<IO, GATE>& own,
+                                                f2& sum, f2& z) {
+  const RecArgs& p = q.f;
+  const Place at(c, p.H, p.D);
+  const int tiles = (int)(((long long)p.T + kRecTile - 1) / kRecTile);
+  const auto before = [&](int tile) { return *reinterpret_cast<const f2*>(p.ckpt + (long long)tile * p.C + c); };
+  const auto inf = [](f2 s) { return isinf(f2_lo(s)) || isinf(f2_hi(s)); };
+  if (odd) {  // is one infinite, or are all others NaN? (a tile between two finite states has none, one behind NaN only those)
+    odd = false;
+#pragma unroll 1
+    for (int tile = rank; tile < tiles && !odd; tile += k) {
+      f2 h = before(tile);
+      const f2 next = tile + 1 < tiles ? before(tile + 1) : f2_both(__int_as_float(0x7fc00000));
+      if ((isnan(f2_lo(h)) || isfinite(f2_lo(next))) && (isnan(f2_hi(h)) || isfinite(f2_hi(next)))) continue;
+      odd = inf(h);
+#pragma unroll 1
+      for (long long t = (long long)tile * kRecTile; t < p.T && t < (tile + 1LL) * kRecTile && !odd; t += kFew)
+        h = few_states<IO, DECAY, SCALE, GATE>(p, at, (int)t, rate, h, [&](int, f2 s) { return !(odd |= inf(s)); });
+    }
+  }
+  const bool lo = !odd && isfinite(f2_lo(z)), hi = !odd && isfinite(f2_hi(z));
+  const f2 one = f2_both(1.f), minus = f2_both(-1.f);
+  f2 behind = q.ghT ? *reinterpret_cast<const f2*>(q.ghT + c) : 0, rates = 0;
+  const auto done = [&](f2 s) { return (lo || isnan(f2_lo(s))) && (hi || isnan(f2_hi(s))); };
+  if (lo && hi) return;
+  static_assert(kFew == kBackTok, "a warp's tokens");
+  int few_at = (p.T - 1) / kFew;
+#pragma unroll 1
+  for (; few_at >= 0 && !done(behind); --few_at) {
+    const int t0 = few_at * kFew;
+    Two<IO> g[kFew], gy[kFew];
+    few<IO>(g, p.g, at.of(p.g), t0, p.T);
+    if (q.gy.p) few<IO>(gy, q.gy, at.of(q.gy), t0, p.T);
+    bool here = odd;
+#pragma unroll
+    for (int j = kFew - 1; j >= 0; --j) {
+      if (j >= p.T - t0) continue;
+      f2 y;
+      const Decay a = decay_of<IO, DECAY, false>(g[j].v, rate, y);
+      const f2 G = q.gy.p ? f2_add(behind, pair_at<IO>(gy[j].v)) : behind;
+      here |= !finite(G);
+      behind = apply<true>(a.hi, a.lo, 0, G);
+      own.at[j * kBackThreads * (own.BOTH ? 2 : 1)] = G;
+    }
+    if (!here || t0 / kRecTile % k != rank || t0 / kBackTok % kBackWarps != w) continue;
+    f2 h = before(t0 / kRecTile);
+#pragma unroll 1
+    for (int t = t0 / kRecTile * kRecTile; t < t0; t += kFew)
+      h = few_states<IO, DECAY, SCALE, GATE>(p, at, t, rate, h, [](int, f2) { return true; });
+    const auto of = [&](const auto& t, int j) {
+      return reinterpret_cast<IO*>(const_cast<void*>(t.p)) + at.of(t) + (long long)(t0 + j) * t.st;
+    };
+#pragma unroll 1
+    for (int j = 0; j < min(kFew, p.T - t0); ++j) {
+      const IO *const x = of(p.x, j), *const g = of(p.g, j), *const i = GATE ? of(p.i, j) : nullptr;
+      const f2 G = own.at[j * kBackThreads * (own.BOTH ? 2 : 1)];
+      f2 open = one, shut = 0, b = one, slope = 0, y;  // b: s; slope: s'
+      const Decay a = decay_of<IO, DECAY, false>(g, rate, y);
+      if (GATE) {
+        const f2 e = f2_exp_neg_held(pair_at<IO>(i));
+        open = f2_rcp(f2_add(one, e));
+        shut = f2_mul(e, open);
+      }
+      const f2 xo = f2_mul(pair_at<IO>(x), open);
+      if (SCALE == kRecSqrt) {
+        const f2 v = spread(a.less), rs = spread_rsqrt(v);
+        b = f2_mul(v, rs);
+        slope = f2_mul(f2_mul(a.hi, a.hi), f2_mul(rs, minus));
+      } else if (SCALE == kRecComplement) {
+        b = a.less;
+        slope = f2_mul(a.hi, minus);
+      }
+      put_odd(of(q.gx, j), f2_mul(G, f2_mul(b, open)));
+      if (GATE) put_odd(of(q.gi, j), f2_mul(G, f2_mul(f2_mul(b, xo), shut)));
+      f2 by_log = f2_mul(G, apply<true>(a.hi, a.lo, SCALE == kRecPlain ? 0 : f2_mul(slope, xo), h));
+      if (DECAY != kRecLog) {
+        const f2 e = f2_exp_neg_held(pair_at<IO>(g)), sg = f2_rcp(f2_add(one, e));
+        if (DECAY == kRecRate) {
+          by_log = f2_mul(by_log, sg);
+          rates = f2_add(rates, by_log);
+          by_log = f2_mul(by_log, f2_mul(rate, minus));
+        }
+        by_log = f2_mul(by_log, f2_mul(e, sg));
+      }
+      put_odd(of(q.gg, j), by_log);
+      h = token<IO, DECAY, SCALE, GATE>(x, g, i, rate, h);
+    }
+  }
+  if (few_at >= 0) rates = f2_add(rates, f2_make(isnan(f2_lo(behind)) ? f2_lo(behind) : 0.f, isnan(f2_hi(behind)) ? f2_hi(behind) : 0.f));
+  // (tokens that were passed over add finite values)
+  sum = finite_or(sum, f2_make(isfinite(f2_lo(rates)) ? f2_lo(sum) : f2_lo(rates), isfinite(f2_hi(rates)) ? f2_hi(sum) : f2_hi(rates)));
+  z = finite_or(z, behind);
 }
 
 template <typename IO, int DECAY, int SCALE, bool GATE>
@@ -192,6 +291,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
       reinterpret_cast<uint4*>(ring + (i / (S * (int)sizeof(IO) / 16)) * STAGE + 3 * S)[i % (S * (int)sizeof(IO) / 16)] = make_uint4(0, 0, 0, 0);
   const f2 one = f2_both(1.f), minus_rate = f2_mul(rate, f2_both(-1.f));
   const int steps = (int)(((long long)p.T + kRecTile * k - 1) / (kRecTile * k));
+  bool odd = false;  // a state that the thread's tokens meet is not finite
   fetch(steps - 1);
   for (int step = steps - 1; step >= 0; --step) {
     const long long first = ((long long)step * k + rank) * kRecTile, t0 = first + w * kBackTok;
@@ -238,6 +338,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
     }
     if (k > 1) z = next;
     if (t0 < p.T) {
+      odd |= !finite(f2_add(h, m.S));
       const int n = (int)min((long long)kBackTok, p.T - t0);
 #pragma unroll
       for (int j = kBackTok - 1; j >= 0; --j) {  // G in the decays' place, dL/dlog a in V's
@@ -292,6 +393,9 @@ __global__ void __launch_bounds__(kBackThreads, 2) kla_recurrence_grad_kernel(co
       fetch(step - 1);
     }
   }
+  __syncwarp();  // (other lanes have stored gradients of this one's channels)
+  if (live && (odd || !finite(z)))
+    one_by_one_back<IO, DECAY, SCALE, GATE>(q, c, rank, k, w, rate, odd, own, sum, z);
   if (q.gh0 && live && rank == 0 && w == 0) *reinterpret_cast<f2*>(q.gh0 + c) = z;
   if (DECAY == kRecRate && q.part) {  // the block's sums of the rates' gradients, in a fixed order
     __syncthreads();

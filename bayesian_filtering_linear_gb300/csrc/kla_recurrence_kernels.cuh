@@ -62,6 +62,71 @@ __device__ __forceinline__ f2 scaled(f2 x, f2 less) {
   return x;
 }
 
+// The state behind one token, from the state before it.
+template <typename IO, int DECAY, int SCALE, bool GATE>
+__device__ __forceinline__ f2 token(const IO* x_at, const IO* g_at, const IO* i_at, f2 rate, f2 h) {
+  f2 x = pair_at<IO>(x_at), y;
+  const Decay a = decay_of<IO, DECAY, false>(g_at, rate, y);
+  x = scaled<SCALE>(x, a.less);
+  if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(i_at)), f2_both(1.f))));
+  return apply<true>(a.hi, a.lo, x, h);
+}
+// x, or `other` where it is not finite
+__device__ __forceinline__ f2 finite_or(f2 x, f2 other) {
+  return f2_make(isfinite(f2_lo(x)) ? f2_lo(x) : f2_lo(other), isfinite(f2_hi(x)) ? f2_hi(x) : f2_hi(other));
+}
+// Eight tokens of two channels, all on their way at the same time; behind the last token, the last one again.
+constexpr int kFew = 8;
+template <typename IO>
+struct alignas(2 * sizeof(IO)) Two {
+  IO v[2];
+};
+template <typename IO, typename Tensor>
+__device__ __forceinline__ void few(Two<IO> (&r)[kFew], const Tensor& x, long long at, int t, int T) {
+#pragma unroll
+  for (int j = 0; j < kFew; ++j)
+    r[j] = *reinterpret_cast<const Two<IO>*>(reinterpret_cast<const IO*>(x.p) + at + min((long long)t + j, (long long)T - 1) * x.st);
+}
+// The states behind tokens t to t + 7 (as many as there are), given to `f` with their number one after the other until
+// it says no; returns the last one.
+template <typename IO, int DECAY, int SCALE, bool GATE, typename F>
+__device__ __forceinline__ f2 few_states(const RecArgs& p, const Place& at, int t, f2 rate, f2 h, F f) {
+  Two<IO> x[kFew], g[kFew], i[kFew];
+  few<IO>(x, p.x, at.of(p.x), t, p.T);
+  few<IO>(g, p.g, at.of(p.g), t, p.T);
+  if (GATE) few<IO>(i, p.i, at.of(p.i), t, p.T);
+#pragma unroll
+  for (int j = 0; j < kFew; ++j) {
+    if (j >= p.T - t) return h;
+    h = token<IO, DECAY, SCALE, GATE>(x[j].v, g[j].v, i[j].v, rate, h);
+    if (!f(j, h)) return h;
+  }
+  return h;
+}
+// For two channels whose last state is not finite, as none is behind the first such one. From that one on the kernel's
+// own values are NaN, where they should be infinite until a token makes NaN of them: this goes from the first state `h`
+// through the tokens one by one, until what is left is NaN or, by `last`, finite, and a thread stores what is not finite
+// where it has stored before. (Every thread of a channel goes through all of its tokens: the headline with an infinite
+// state takes 0.9 ms, and 0.07 with NaN alone.)
+template <typename IO, int DECAY, int SCALE, bool GATE, int kWarps>
+__device__ __forceinline__ void one_by_one(const RecArgs& p, int c, int rank, int k, int w, f2 rate, f2 h, f2 last) {
+  const Place at(c, p.H, p.D);
+  const long long y_at = at.of(p.y);
+  const bool lo = isfinite(f2_lo(last)), hi = isfinite(f2_hi(last));
+  const auto done = [&](f2 s) { return (lo || isnan(f2_lo(s))) && (hi || isnan(f2_hi(s))); };
+#pragma unroll 1
+  for (long long t = 0; t < p.T; t += kFew) {
+    const bool mine = t / (kWarps * kTok) % k == rank && t / kTok % kWarps == w;
+    if (mine && p.ckpt && t % kRecTile == 0) put_odd(p.ckpt + t / kRecTile * p.C + c, h);
+    h = few_states<IO, DECAY, SCALE, GATE>(p, at, (int)t, rate, h, [&](int j, f2 s) {
+      if (mine && p.y.p) put_odd(reinterpret_cast<IO*>(p.y.p) + y_at + (t + j) * p.y.st, s);
+      return true;
+    });
+    if (done(h)) return;
+  }
+  if (p.hT && rank == 0 && w == 0) put_odd(p.hT + c, h);
+}
+
 template <typename IO, int DECAY, int SCALE, bool GATE, bool NEAR, int S>  // S: elements a stream
 __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f2 (&Y)[kTok]) {
   Map m{0, 0, 0};
@@ -72,7 +137,7 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
     const Decay a = decay_of<IO, DECAY, NEAR>(tile + S + j * kChans, rate, y);
     x = scaled<SCALE>(x, a.less);
     if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(tile + 2 * S + j * kChans)), f2_both(1.f))));
-    m.S = apply(a.hi, a.lo, x, m.S);
+    m.S = apply<false>(a.hi, a.lo, x, m.S);
     prod.times(a, y);
     P[j] = prod.value();
     Y[j] = m.S;
@@ -84,6 +149,7 @@ __device__ __forceinline__ Map segment(const IO* tile, f2 rate, f2 (&P)[kTok], f
 template <typename IO, int DECAY, int SCALE, bool GATE, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurrence_kernel(const RecArgs p, int k) {
   constexpr int kThreads = 32 * kWarps, kTile = kWarps * kTok;
+  __shared__ f2 start[32];  // the first states (hT may lie where h0 does)
   extern __shared__ __align__(16) unsigned char smem[];
   BlockMap* const blocks = reinterpret_cast<BlockMap*>(smem);  // [2][k]
   IO* const tile = reinterpret_cast<IO*>(smem + block_maps_bytes(k));
@@ -120,6 +186,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurren
   if (DECAY == kRecRate && live)
     rate = rates_at(p.rate + (long long)my.h * p.D + my.d);
   if (p.h0 && live) h = *reinterpret_cast<const f2*>(p.h0 + c);
+  if (w == 0) start[lane] = h;
   const bool near = DECAY == kRecRate && near_rates(rate);
 
   const long long steps = ((long long)p.T + kTile * k - 1) / (kTile * k);
@@ -150,7 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurren
 #pragma unroll
         for (int v = 1; v < kWarps; ++v) {
           const f2 A = map_of(v)[0], Al = map_of(v)[32];
-          m.S = apply(A, Al, map_of(v)[64], m.S);
+          m.S = apply<false>(A, Al, map_of(v)[64], m.S);
           lengthen(m.A, m.Al, A, Al);
         }
         for (int r = 0; r < k; ++r) half[rank].put(lane, r, m);
@@ -168,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurren
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) {
       if (v == w) mystart = h;
-      if (k == 1 || v < w) h = apply(map_of(v)[0], map_of(v)[32], map_of(v)[64], h);
+      if (k == 1 || v < w) h = apply<false>(map_of(v)[0], map_of(v)[32], map_of(v)[64], h);
     }
     if (k > 1) h = next;
     const long long t0 = first + w * kTok;
@@ -185,7 +252,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<IO, kWarps>) kla_recurren
       }
     }
   }
-  if (p.hT && live && rank == 0 && w == 0) *reinterpret_cast<f2*>(p.hT + c) = h;
+  if (!live) return;
+  if (p.hT && rank == 0 && w == 0) *reinterpret_cast<f2*>(p.hT + c) = h;
+  if (!finite(h)) one_by_one<IO, DECAY, SCALE, GATE, kWarps>(p, c, rank, k, w, rate, start[lane], h);
 }
 
 // One token: a thread takes two channels.
@@ -194,13 +263,10 @@ __global__ void __launch_bounds__(128) kla_recurrence_step_kernel(const RecArgs 
   const int c = 2 * (blockIdx.x * 128 + threadIdx.x);
   if (c >= p.C) return;
   const f2 h = *reinterpret_cast<const f2*>(p.h0 + c);
-  f2 x = pair_at<IO>(reinterpret_cast<const IO*>(p.x.p) + c), rate = 0;
+  f2 rate = 0;
   if (DECAY == kRecRate) rate = rates_at(p.rate + c % (p.H * p.D));
-  f2 y;
-  const Decay a = decay_of<IO, DECAY, false>(reinterpret_cast<const IO*>(p.g.p) + c, rate, y);
-  x = scaled<SCALE>(x, a.less);
-  if (GATE) x = f2_mul(x, f2_rcp(f2_add(f2_exp_neg(pair_at<IO>(reinterpret_cast<const IO*>(p.i.p) + c)), f2_both(1.f))));
-  const f2 next = apply(a.hi, a.lo, x, h);
+  const f2 next = token<IO, DECAY, SCALE, GATE>(reinterpret_cast<const IO*>(p.x.p) + c, reinterpret_cast<const IO*>(p.g.p) + c,
+                                                reinterpret_cast<const IO*>(p.i.p) + (GATE ? c : 0), rate, h);
   *reinterpret_cast<f2*>(p.hT + c) = next;
   put_pair(reinterpret_cast<IO*>(p.y.p) + c, next);
 }

@@ -509,7 +509,10 @@ typedef struct kla_recurrence_options {
  *   D a multiple of 8 (else UNSUPPORTED_SHAPE); B, H, T ≥ 0; pointers 16-byte
  *   aligned. States are fp32, and decays near 1 are held in more than fp32, so
  *   that thousands of them multiply without drift. A value that is not finite
- *   stays in its channel. Repeated calls give identical bits. */
+ *   stays in its channel: an infinite state stays infinite until a token makes
+ *   NaN of it (NaN, an infinity of the other sign, or a decay below 2^-126,
+ *   which counts as 0). Channels with an infinite state go through their tokens
+ *   a second time, one by one. Repeated calls give identical bits. */
 size_t kla_recurrence_checkpoints_size(int B, int H, int T, int D);
 kla_status kla_recurrence_forward(const void* x, const void* g, const void* i, const float* rate, const float* h0,
                                   void* y, float* hT, void* checkpoints, int B, int H, int T, int D,
