@@ -1181,6 +1181,15 @@ def _once(backward):
     return call
 
 
+def _given(g, dtype=None):
+    """A gradient from autograd as the kernels read it: contiguous, from 16 bytes on (a slice of torch.cat's gradient may
+    begin anywhere), and of this dtype."""
+    if g is None:
+        return None
+    g = (g if dtype is None else g.to(dtype)).contiguous()
+    return g.clone() if g.data_ptr() % 16 else g
+
+
 class _ScanFunction(torch.autograd.Function):
     """kla_forward with kla_backward as its derivative."""
 
@@ -1196,9 +1205,7 @@ class _ScanFunction(torch.autograd.Function):
     def backward(ctx, gy, glamT, getaT):
         q, k, v, lam_v, a, pbar, lam0, eta0 = ctx.saved_tensors
         g = backward(q, k, v, lam_v, a, pbar, lam0, eta0,
-                     gy=None if gy is None else gy.to(q.dtype).contiguous(),
-                     glamT=None if glamT is None else glamT.contiguous(),
-                     getaT=None if getaT is None else getaT.contiguous(),
+                     gy=_given(gy, q.dtype), glamT=_given(glamT), getaT=_given(getaT),
                      state_grads=lam0 is not None, gates=ctx.gates)
         return (g["gq"], g["gk"], g["gv"], g["glam_v"], g["ga"], g["gpbar"], g.get("glam0"), g.get("geta0"), None)
 
@@ -1223,9 +1230,7 @@ class _ConvFunction(torch.autograd.Function):
     @_once
     def backward(ctx, gy, gwindow_out):
         x, weight, bias, window = ctx.saved_tensors
-        g = conv_backward(x, weight, bias, window,
-                          gy=None if gy is None else gy.to(x.dtype).contiguous(),
-                          gwindow_out=None if gwindow_out is None else gwindow_out.to(x.dtype).contiguous(),
+        g = conv_backward(x, weight, bias, window, gy=_given(gy, x.dtype), gwindow_out=_given(gwindow_out, x.dtype),
                           activation=ctx.activation, window_grad=window is not None)
         return (g["gx"], g["gweight"], None if bias is None else g["gbias"], g.get("gwindow"), None)
 
@@ -1251,8 +1256,7 @@ class _DeltaFunction(torch.autograd.Function):
     @_once
     def backward(ctx, go, gstateT):
         q, k, v, g, beta, state0 = ctx.saved_tensors
-        d = delta_backward(q, k, v, g, beta, state0, go=None if go is None else go.to(q.dtype).contiguous(),
-                           gstateT=None if gstateT is None else gstateT.contiguous(), scale=ctx.scale,
+        d = delta_backward(q, k, v, g, beta, state0, go=_given(go, q.dtype), gstateT=_given(gstateT), scale=ctx.scale,
                            state_grad=state0 is not None)
         return d["gq"], d["gk"], d["gv"], d["gg"], d["gbeta"], d.get("gstate0"), None
 
@@ -1276,9 +1280,8 @@ class _NormRopeFunction(torch.autograd.Function):
     @_once
     def backward(ctx, gyq, gyk):
         q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
-        d = norm_rope_backward(q, k, q_weight, k_weight, inv_freq, positions,
-                               gyq=None if gyq is None else gyq.to(q.dtype).contiguous(),
-                               gyk=None if gyk is None else gyk.to(q.dtype).contiguous(), **ctx.how)
+        d = norm_rope_backward(q, k, q_weight, k_weight, inv_freq, positions, gyq=_given(gyq, q.dtype),
+                               gyk=_given(gyk, q.dtype), **ctx.how)
         return d["gq"], d.get("gk"), d.get("gq_weight"), d.get("gk_weight"), None, None, None
 
 
@@ -1309,8 +1312,8 @@ class _RecurrenceFunction(torch.autograd.Function):
         if gy is not None:
             gy = gy.to(x.dtype)
             if not _takes(gy):
-                gy = gy.contiguous()
-        d = recurrence_backward(x, g, i, rate, h0, gy=gy, ghT=None if ghT is None else ghT.contiguous(),
+                gy = _given(gy)
+        d = recurrence_backward(x, g, i, rate, h0, gy=gy, ghT=_given(ghT),
                                 checkpoints=kept, state_grad=h0 is not None, **ctx.how)
         return d["gx"], d["gg"], d.get("gi"), d.get("grate"), d.get("gh0"), None
 
