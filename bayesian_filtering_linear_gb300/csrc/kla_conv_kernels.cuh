@@ -29,12 +29,12 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 
 #include <cuda_bf16.h>
 
 #include "kla_device.cuh"
 #include "kla_launch.h"
+#include "kla_prepare.cuh"
 
 namespace kla {
 
@@ -43,7 +43,6 @@ namespace kla {
 namespace {
 
 constexpr int kConvThreads = 256;
-constexpr int kMaxDevices = 256;
 // Consecutive tokens per thread and stage. With D ≤ 512 a stage holds at
 // least two threads' rows, eight tokens, so it always covers the W − 1 ≤ 7
 // rows that the next stage reads before its start.
@@ -505,23 +504,7 @@ __global__ void __launch_bounds__(256) kla_conv_bwd_finish_kernel(const ConvArgs
   }
 }
 
-// Raise kernel `Kernel`'s dynamic shared-memory limit to `smem_max` — the
-// most any launch of that instantiation asks for (a stage holds at most 256
-// threads' rows: TT·D ≤ 1024·kConvRows) — once per device.
-template <auto Kernel>
-cudaError_t prepare_kernel(size_t smem_max) {
-  static std::atomic<int> done[kMaxDevices];  // one set per kernel instantiation
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-  if ((e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max)) != cudaSuccess)
-    return e;
-  done[dev].store(1, std::memory_order_relaxed);
-  return cudaSuccess;
-}
-
+// (Dynamic shared memory: a stage holds at most 256 threads' rows, TT·D ≤ 1024·kConvRows.)
 template <typename IO, int W, bool ACT, int DC>
 cudaError_t launch_fwd(ConvArgs a, int num_sms, cudaStream_t s) {
   const long long bh = (long long)a.B * a.H;

@@ -24,6 +24,7 @@
 
 #include "kla_device.cuh"
 #include "kla_launch.h"
+#include "kla_prepare.cuh"
 
 namespace kla {
 
@@ -550,11 +551,13 @@ cudaError_t launch_io(const LayerNormGradArgs& a, int num_sms, cudaStream_t s) {
   auto go = [&](auto ve, auto shape) {
     using Sh = decltype(shape);
     constexpr int V = decltype(ve)::value;
-    const auto kernel = kla_layer_norm_grad_kernel<IO, V, Sh::NV, Sh::LANES, Sh::THREADS, Sh::S, Sh::MIN>;
-    size_t smem = Ahead<IO, V, Sh::NV, Sh::LANES, Sh::THREADS, Sh::S>::BYTES;
-    if (a.part && Sh::LANES < Sh::THREADS) smem += 2 * (size_t)a.D * sizeof(float);
+    constexpr auto kernel = kla_layer_norm_grad_kernel<IO, V, Sh::NV, Sh::LANES, Sh::THREADS, Sh::S, Sh::MIN>;
+    constexpr size_t ring = Ahead<IO, V, Sh::NV, Sh::LANES, Sh::THREADS, Sh::S>::BYTES;
+    constexpr bool groups = Sh::LANES < Sh::THREADS;  // which add up their sums in shared memory
+    constexpr size_t most = ring + (groups ? 2 * Sh::LANES * Sh::NV * V * sizeof(float) : 0);
+    const size_t smem = ring + (a.part && groups ? 2 * (size_t)a.D * sizeof(float) : 0);
     blocks = grad_blocks<Sh>(a.rows, num_sms);
-    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if constexpr (most > 40 * 1024) e = prepare_kernel<kernel>(most);
     if (e == cudaSuccess) kernel<<<blocks, Sh::THREADS, smem, s>>>(a);
   };
   by_piece<IO>(a.D, {{a.x, a.x_stride}, {a.gy, a.gy_stride}, {a.gtotal, a.gtotal_stride}, {a.gx, a.D}}, [&](auto ve) {
