@@ -15,12 +15,13 @@
 
 #include "kla.h"
 #include "kla_launch.h"
+#include "kla_prepare.cuh"
 
 namespace {
 
+using kla::kMaxSmem;
 using kla::Plan;
 
-constexpr size_t kMaxSmem = 227 * 1024;
 constexpr int kChunkAlign = 32;  // chunk lengths are multiples of the largest tile
 
 bool valid_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }

@@ -45,6 +45,7 @@
 
 #include "kla_device.cuh"
 #include "kla_launch.h"
+#include "kla_prepare.cuh"
 
 namespace kla {
 namespace {
@@ -492,7 +493,7 @@ template <typename IO, int DK, int CPL>
 cudaError_t launch_bwd_typed(const BwdParams& bp, dim3 grid, int threads, size_t smem, cudaStream_t s) {
   auto bw = kla_bwd_kernel<IO, DK, CPL>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(bw, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = prepare_kernel<kla_bwd_kernel<IO, DK, CPL>>(kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   const size_t BHTdk = (size_t)grid.x * bp.T * DK;
@@ -531,7 +532,7 @@ cudaError_t launch_bwd_io(int dk, int cpl, const BwdParams& bp, dim3 grid, int t
 
 BwdPlan backward_plan(long long bh, int T, int dk, int dv, int num_sms) {
   constexpr int kMaxWarps = 16;  // 512 threads at the reverse kernel's register budget
-  constexpr size_t kMaxSmem = 220 * 1024;
+  constexpr size_t kBwdMaxSmem = 220 * 1024;
   const int rw = dk < 32 ? dk : 32, nwr = dk / rw;
   // Column block and threads for `cpl` columns per lane.
   auto geometry = [&](int cpl) {
@@ -540,7 +541,7 @@ BwdPlan backward_plan(long long bh, int T, int dk, int dv, int num_sms) {
     const int wcols = (32 / rw) * cpl;
     int cc = dv;
     while (cc > wcols &&
-           (nwr * (cc / wcols) > kMaxWarps || BwdSmem::bytes(dk, cc, 32 * nwr * (cc / wcols), cpl) > kMaxSmem))
+           (nwr * (cc / wcols) > kMaxWarps || BwdSmem::bytes(dk, cc, 32 * nwr * (cc / wcols), cpl) > kBwdMaxSmem))
       cc /= 2;
     // Few heads: narrower column blocks, so that at least half the SMs get a
     // block (a block of up to 16 warps keeps an SM busy on its own).

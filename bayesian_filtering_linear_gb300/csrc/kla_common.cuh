@@ -4,6 +4,7 @@
 
 #include "kla_device.cuh"
 #include "kla_launch.h"
+#include "kla_prepare.cuh"
 
 namespace kla {
 
@@ -177,14 +178,13 @@ inline KernelParams make_params(const ForwardArgs& f, const Plan& p) {
 }
 
 // Launch with the dynamic shared memory a kernel needs (opting in above 48 KB).
-template <typename Kern>
-inline cudaError_t launch_kernel(Kern fn, dim3 grid, int threads, size_t smem, cudaStream_t s,
-                                 const KernelParams& kp) {
+template <auto Kernel>
+inline cudaError_t launch_kernel(dim3 grid, int threads, size_t smem, cudaStream_t s, const KernelParams& kp) {
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = prepare_kernel<Kernel>(kMaxSmem);
     if (e != cudaSuccess) return e;
   }
-  fn<<<grid, threads, smem, s>>>(kp);
+  Kernel<<<grid, threads, smem, s>>>(kp);
   return cudaGetLastError();
 }
 

@@ -278,13 +278,13 @@ template <typename IO>
 cudaError_t compose_dispatch(int dk, dim3 grid, int threads, size_t smem, cudaStream_t s, const KernelParams& kp) {
   switch (dk) {
     case 16:
-      return launch_kernel(kla_compose_kernel<IO, 16, RowsPerLane<16>::value, kComposeTile>, grid, threads, smem, s, kp);
+      return launch_kernel<kla_compose_kernel<IO, 16, RowsPerLane<16>::value, kComposeTile>>(grid, threads, smem, s, kp);
     case 32:
-      return launch_kernel(kla_compose_kernel<IO, 32, RowsPerLane<32>::value, kComposeTile>, grid, threads, smem, s, kp);
+      return launch_kernel<kla_compose_kernel<IO, 32, RowsPerLane<32>::value, kComposeTile>>(grid, threads, smem, s, kp);
     case 64:
-      return launch_kernel(kla_compose_kernel<IO, 64, RowsPerLane<64>::value, kComposeTile>, grid, threads, smem, s, kp);
+      return launch_kernel<kla_compose_kernel<IO, 64, RowsPerLane<64>::value, kComposeTile>>(grid, threads, smem, s, kp);
     case 128:
-      return launch_kernel(kla_compose_kernel<IO, 128, RowsPerLane<128>::value, kComposeTile>, grid, threads, smem, s, kp);
+      return launch_kernel<kla_compose_kernel<IO, 128, RowsPerLane<128>::value, kComposeTile>>(grid, threads, smem, s, kp);
     default:
       return cudaErrorInvalidValue;
   }

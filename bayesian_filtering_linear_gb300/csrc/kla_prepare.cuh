@@ -8,6 +8,7 @@
 namespace kla {
 
 constexpr int kMaxDevices = 256;
+constexpr size_t kMaxSmem = 227 * 1024;  // a block's shared memory at most
 
 // Raise kernel `Kernel`'s dynamic shared-memory limit to `smem_max` — the
 // most any launch of that instantiation asks for — once per device. The limit

@@ -627,12 +627,12 @@ template <typename IO, int MODE>
 cudaError_t scan_launch_mode(int dk, int rl, dim3 grid, int threads, size_t smem, cudaStream_t s,
                              const KernelParams& kp) {
   switch (dk * 16 + rl) {
-    case 16 * 16 + 4: return launch_kernel(kla_scan_kernel<IO, 16, 4, kTile, MODE>, grid, threads, smem, s, kp);
-    case 32 * 16 + 4: return launch_kernel(kla_scan_kernel<IO, 32, 4, kTile, MODE>, grid, threads, smem, s, kp);
-    case 64 * 16 + 4: return launch_kernel(kla_scan_kernel<IO, 64, 4, kTile, MODE>, grid, threads, smem, s, kp);
-    case 64 * 16 + 8: return launch_kernel(kla_scan_kernel<IO, 64, 8, kTile, MODE>, grid, threads, smem, s, kp);
-    case 128 * 16 + 4: return launch_kernel(kla_scan_kernel<IO, 128, 4, kTile, MODE>, grid, threads, smem, s, kp);
-    case 128 * 16 + 8: return launch_kernel(kla_scan_kernel<IO, 128, 8, kTile, MODE>, grid, threads, smem, s, kp);
+    case 16 * 16 + 4: return launch_kernel<kla_scan_kernel<IO, 16, 4, kTile, MODE>>(grid, threads, smem, s, kp);
+    case 32 * 16 + 4: return launch_kernel<kla_scan_kernel<IO, 32, 4, kTile, MODE>>(grid, threads, smem, s, kp);
+    case 64 * 16 + 4: return launch_kernel<kla_scan_kernel<IO, 64, 4, kTile, MODE>>(grid, threads, smem, s, kp);
+    case 64 * 16 + 8: return launch_kernel<kla_scan_kernel<IO, 64, 8, kTile, MODE>>(grid, threads, smem, s, kp);
+    case 128 * 16 + 4: return launch_kernel<kla_scan_kernel<IO, 128, 4, kTile, MODE>>(grid, threads, smem, s, kp);
+    case 128 * 16 + 8: return launch_kernel<kla_scan_kernel<IO, 128, 8, kTile, MODE>>(grid, threads, smem, s, kp);
     default: return cudaErrorInvalidValue;
   }
 }
