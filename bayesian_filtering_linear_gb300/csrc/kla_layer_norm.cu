@@ -491,7 +491,6 @@ void by_width_back(int pieces, F f) {
   } else {
     if (pieces <= 128) return f(BackShape<4, 32, 128, 4, 5>());
     if (pieces <= 256) return f(BackShape<8, 32, 128, 3, 4>());
-    if (pieces <= 384) return f(BackShape<6, 64, 128, 3, 5>());
     if (pieces <= 512) return f(BackShape<8, 64, 128, 3, 4>());
     if (pieces <= 640) return f(BackShape<5, 128, 128, 4, 4>());
     if (pieces <= 768) return f(BackShape<6, 128, 128, 4, 4>());
