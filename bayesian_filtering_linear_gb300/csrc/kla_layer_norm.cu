@@ -16,10 +16,10 @@
 // gradients 47 us and 5 for the sums (before: 86 with the next row in registers and
 // a warp a row, where 254 registers left eight warps an SM; 56 with sums of one
 // thread a block; three blocks of two rows at a time, 164 registers, are faster
-// than four of 128, which spill). Rows of an odd width are read an element at a
-// time: 8188 of 517 in fp32, gradients 14 us and 5; in bf16, pairs where rows begin
-// on four bytes (38972 of 446 with the residual: 26 us, by elements 34; gradients of
-// 20000: 20, by elements 24, by copies of four bytes 21).
+// than four of 128, which spill). Rows that do not all begin on 16 bytes are read in
+// pairs where they are bf16 and all begin on four (38972 of 446 with the residual: 26
+// us, by elements 34; gradients of 20000: 20, by elements 24, by copies of four bytes
+// 21), else an element at a time (8188 of 517 in fp32, gradients 14 us and 5).
 #include <algorithm>
 
 #include "kla_device.cuh"
@@ -432,9 +432,10 @@ struct BackShape : Shape<NV, LANES, THREADS> {
   static constexpr int S = S_, MIN = MIN_;
 };
 
-// Forward, by the row's width in pieces (of 16 bytes; else pairs or single elements: 5000 fp32 rows of 3001 take 43 us
-// with eight elements a lane of 512, 67 with sixteen; 200000 bf16 rows of 50 take 21 with eight lanes a row, 43 with
-// 32; up to 512, fp32 rows of 501 take 22 us with 128 lanes and 25 with 64, bf16 rows of 411 take 22 and 18).
+// Forward, by the row's width in pieces (of 16 bytes; else pairs or single elements): the smallest shape that holds the
+// row, as the next one costs more at every step (210 MB of rows of 1024 in pieces of 16 bytes: bf16 37 us with 32 lanes, 39
+// with 128; of 2048 with 128 lanes and four pieces 39, with two 35; fp32 rows of 50 elements 40 with eight lanes, 57 with
+// 32). Up to 512 pieces, fp32 rows of 501 take 36 us with 128 lanes and 38 with 64, bf16 rows of 411 take 63 and 47.
 template <typename IO, int VEC, typename F>
 void by_width(int pieces, F f) {
   if constexpr (VEC >= 4) {
@@ -461,7 +462,9 @@ void by_width(int pieces, F f) {
 
 // Backward, where a lane also keeps the sums of its columns: more lanes with fewer pieces, but few warps a row, which
 // wait for each other twice (5000 rows of 3001 with 16 and 8 warps: 99 and 70 us in fp32, 115 and 46 in bf16; 4000 of
-// 4090 in bf16: 59 and 39).
+// 4090 in bf16: 59 and 39). The smallest shape that holds the row again (210 MB of bf16 rows of 1024: 41 us, with the next
+// shape 65; of 4096: 46 and 69; fp32 rows of 255 elements: 45 and 51, of 1023: 45 and 53; fp32 rows of 1024
+// in pieces of 16 bytes would take 38 with the next one, and take 43).
 template <int VEC, typename F>
 void by_width_back(int pieces, F f) {
   if constexpr (VEC == 8) {
@@ -501,7 +504,8 @@ void by_width_back(int pieces, F f) {
   }
 }
 
-// Blocks of the gradients' kernel: as many as the device holds at once (every shape's MIN an SM), for each leaves partial sums.
+// Blocks of the gradients' kernel: MIN an SM, for each leaves partial sums. That is about as many as the device holds at
+// once; with sums, the rings of fp32 rows of 372 to 1024 let an SM hold two for MIN = 3, and of 2052 to 4096 one for two.
 template <typename Sh>
 int grad_blocks(long long rows, int num_sms) {
   constexpr int groups = Sh::THREADS / Sh::LANES;

@@ -324,7 +324,8 @@ cudaError_t launch_clusters(const Args& a, int tiles, int along, int* used, cuda
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  constexpr int sizes[] = {16, 12, 8, 7, 6, 5, 4, 3, 2, 1};  // above eight, those that the device's groups of SMs hold well
+  constexpr int sizes[] = {16, 12, 8, 7, 6, 5, 4, 3, 2, 1};  // above eight, 12 and 16: of 12 the device holds 432 bf16 blocks of the
+                                                            // forward kernel in all, of 9 to 15 else 364 to 430; 16 goes the furthest
   static_assert(sizes[0] == kRecMaxCluster, "the largest");
   int k = 1;
   for (int n : sizes) {

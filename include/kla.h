@@ -481,7 +481,8 @@ kla_status kla_norm_rope_backward(const void* q, const void* k, const float* q_w
 typedef enum kla_recurrence_decay {
   KLA_DECAY_LOG = 0,     /* a = e^g, g ≤ 0 (−∞ resets the state)              */
   KLA_DECAY_SIGMOID = 1, /* a = σ(g)                                          */
-  KLA_DECAY_RATE = 2     /* a = exp(−rate σ(g)), one rate ≥ 0 a channel       */
+  KLA_DECAY_RATE = 2     /* a = exp(−rate σ(g)), one rate ≥ 0 a channel (no g
+                            makes a = 0: only the others pack sequences)     */
 } kla_recurrence_decay;
 typedef enum kla_recurrence_scale {
   KLA_SCALE_NONE = 0,      /* s = 1                                           */

@@ -90,7 +90,7 @@ def backward(x, g, i=None, rate=None, h0=None, gy=None, ghT=None, decay="log", s
     if i is not None:
         p = size * open_ * x * sigmoid(-i)
         out["gi"], out["gi_err"] = G * p, np.abs(p) * (G_err + (2 * c + 8) * U * np.abs(G))
-    if rate is not None:  # a sum over B and T: T / 64 + B + 16 roundings in a row at most
+    if rate is not None:  # a sum over B and T: a thread adds up an eighth of a sequence, then come the blocks and the batch
         out["grate"] = -(log_ * sg).sum((0, 2))
         depth = x.shape[2] / 8 + 8 * x.shape[0] + 32
         out["grate_err"] = (sg * (log_err + (c + depth) * U * np.abs(log_))).sum((0, 2))
