@@ -26,7 +26,8 @@
  *  - All array pointers are DEVICE pointers owned by the caller; the library
  *    allocates no device memory and keeps no state beyond a per-device cache
  *    of the SM count, of how many clusters of the recurrence's blocks the
- *    device holds and of the kernels whose limit of shared memory is raised. The one exception is kla_forward_chunked_noalloc: its
+ *    device holds and of the kernels whose limit of shared memory is raised.
+ *    The one exception is kla_forward_chunked_noalloc: its
  *    fixed 32 MiB scratch array lives in device memory on every GPU that
  *    loads the library, its address is cached per CUDA context, and calls of
  *    it that overlap on the GPU race (see its comment below). Work is queued
